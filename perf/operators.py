@@ -214,8 +214,8 @@ def _route_plain(s):
     if s["sigmoid"]:
         score = 1 / (1 + torch.exp(-l))
     else:
-        e = torch.exp(l - l.amax(dim=1, keepdim=True))
-        score = e / e.sum(dim=1, keepdim=True)
+        e = torch.exp(l - l.amax(dim=1, keepdim=True)).masked_fill(away, 0)
+        score = e / e.sum(dim=1, keepdim=True).clamp(min=1e-37)  # zeros for a row with every expert masked
     # without a bias the order of the scores is that of the logits
     key = l if s["bias_values"] is None else (score + s["bias_values"]).masked_fill(away, -math.inf)
     if s["groups"] > 1:
@@ -229,7 +229,7 @@ def _route_plain(s):
         ids = _best(key, s["k"])
     w = score.gather(1, ids)
     if s["renormalize"]:
-        w = w / w.sum(dim=1, keepdim=True)
+        w = w / w.sum(dim=1, keepdim=True).clamp(min=1e-37)
     return w * s["scale"], ids.to(torch.int32)
 
 
@@ -339,7 +339,7 @@ def _route_exact(s):
     w = torch.gather(score, 1, ids)
     if s["renormalize"]:
         w = w / w.sum(1, keepdim=True)
-    return w * s["scale"], None
+    return torch.nan_to_num(w * s["scale"]), None  # a row with every expert masked: zeros
 
 
 def _lora_exact(s):
