@@ -384,6 +384,148 @@ W4_API int w4_last_device_error(void *workspace_dev, void *stream);
 W4_API int w4a16_gemm_noalloc(const void *x_dev, const void *packed_dev, int64_t M, int64_t N, int64_t K,
                        int32_t g, void *y_dev, void *stream);
 
+/* ------------------------------------------------------------------------
+ * Weights chosen row by row, on the device: the router of a mixture of
+ * experts, the experts' W4A16 products, and the low-rank adapters of many
+ * requests beside a projection that they share. The pages have no
+ * counterpart; the experts' weights are w4_pack / w4_repack's. No rows
+ * (T = 0) is no error: nothing is enqueued. Workspaces need not be zeroed,
+ * hold nothing between calls, and calls that share one must not overlap on
+ * the device. Results are deterministic run to run on one device.
+ * ------------------------------------------------------------------------ */
+
+#define W4_DTYPE_F32 2 /* router logits only */
+
+/*
+ * w4_route -- the experts of each token and their weights.
+ *
+ *   s_i = softmax(l)_i, or 1 / (1 + e^-l_i) (sigmoid)
+ *   c_i = s_i + bias_i; without a bias c orders the experts as the logits do
+ *   the row keeps its top_groups best groups of experts / groups consecutive
+ *   experts; a group is worth the largest c in it (group_top 1) or the sum of
+ *   its two largest (2; of s, without a bias)
+ *   ids: the k largest c in the kept groups, largest first; of equal ones the
+ *   lowest index first
+ *   weights_j = s at ids_j (/ their sum over j, renormalize) * scale
+ *
+ * Computed in fp32. A logit of -inf (or NaN) masks its expert: it is chosen
+ * after all others, with a weight of 0; a row with every expert masked has
+ * weights of 0. The ids of a row are always distinct and in range.
+ *
+ * logits_dev  [T, experts] of opts->dtype (fp16, bf16 or fp32), rows `ld`
+ *             values apart, aligned to the type.
+ * bias_dev    fp32 [experts], or NULL.
+ * weights_dev out: fp32 [T, k]. ids_dev out: int32 [T, k].
+ * Limits: experts <= 1024, k <= 32, groups <= 32 (W4_ERR_UNSUPPORTED_SHAPE
+ * beyond); k <= top_groups * experts / groups.
+ */
+typedef struct {
+    int32_t k;
+    int32_t sigmoid;     /* 0: softmax, 1: sigmoid */
+    int32_t groups;      /* 0: 1 */
+    int32_t top_groups;  /* 0: all */
+    int32_t group_top;   /* 1 or 2; 0: 1 */
+    int32_t renormalize; /* 0 or 1 */
+    float scale;
+    int32_t dtype;       /* of the logits */
+} w4_route_options;
+W4_API int w4_route(const void *logits_dev, int64_t T, int32_t experts, int64_t ld, const float *bias_dev,
+                    const w4_route_options *opts, float *weights_dev, int32_t *ids_dev, void *stream);
+
+/*
+ * w4a16_experts -- a token's chosen experts, each a gated pair of 4-bit
+ * linear layers, added with the router's weights:
+ *
+ *   y[t] = sum_j weights[t, j] * down_e . (silu(gate_e . x[t]) * up_e . x[t]),
+ *   e = ids[t, j], silu(v) = v / (1 + e^-v)
+ *
+ * x_dev, y_dev  [T, K] of dtype (fp16 or bf16), row-major, 16-byte aligned.
+ * gate_up_dev   `experts` w4_repack outputs for (2 I, K, g), one after
+ *               another; row 2j of each is gate row j, row 2j + 1 up row j.
+ * down_dev      `experts` w4_repack outputs for (K, I, g).
+ * ids_dev       int32 [T, k]; an id outside [0, experts) is a dropped choice
+ *               and adds nothing (a token without a choice has y = 0).
+ * weights_dev   fp32 [T, k].
+ * K, I multiples of 8; g a positive multiple of 8 (g a multiple of 64 runs
+ * fastest); experts <= 1024, k <= min(experts, 32).
+ *
+ * Numerics: q - z enters the products exactly and a group's sum is scaled in
+ * fp32; silu(gate) * up is rounded once to the type (the second product's
+ * operand); sums are fp32, added in a fixed order, and y is rounded once.
+ * The workspace is at least w4a16_experts_workspace_bytes(...) bytes,
+ * 256-byte aligned.
+ */
+typedef struct {
+    const void *x_dev;
+    const void *gate_up_dev;
+    const void *down_dev;
+    const int32_t *ids_dev;
+    const float *weights_dev;
+    void *y_dev;
+    int64_t T;
+    int64_t K;
+    int64_t I;
+    int32_t experts;
+    int32_t k;
+    int32_t g;
+    int32_t dtype;
+} w4a16_experts_args;
+W4_API int w4a16_experts(const w4a16_experts_args *args, void *workspace_dev, size_t workspace_bytes, void *stream);
+/* 0 for sizes that w4a16_experts refuses. */
+W4_API size_t w4a16_experts_workspace_bytes(int64_t T, int64_t K, int64_t I, int32_t experts, int32_t k, int32_t g);
+
+/*
+ * w4_lora_add -- each row's own low-rank adapter, beside a projection that
+ * all rows share:
+ *
+ *   y[t] = base[t] + scaling[a] * B[a] . (A[a] . x[t]),  a = adapter[t]
+ *
+ * and y[t] = base[t] for a row without an adapter (an index outside
+ * [0, adapters)).
+ *
+ * x_dev        [T, K] of dtype (fp16 or bf16), rows ldx values apart (a
+ *              multiple of 8), 16-byte aligned.
+ * base_dev     [T, N] of dtype, rows ldbase apart, or NULL for zeros. May be
+ *              y_dev itself (with ldbase = ldy); else y must not overlap it.
+ * y_dev        out: [T, N], rows ldy apart. base and y are 2-byte aligned;
+ *              16-byte aligned rows are fastest.
+ * A_dev, B_dev [adapters, rank, K] and [adapters, N, rank], 16-byte aligned.
+ * adapter_dev  int32 [T].
+ * scaling_dev  fp32 [adapters], or NULL for 1.
+ * ranks_dev    int32 [adapters], or NULL: the adapter's own rank, up to
+ *              `rank`; what A and B hold past it is not used.
+ * K and rank multiples of 8; rank <= 128; adapters <= 1024.
+ *
+ * Numerics: A . x in fp32; it enters the second product as two 16-bit values
+ * that hold about twice the type's bits (fp16: after division of the row by a
+ * power of two, so that it cannot overflow); sums in fp32, y rounded once.
+ * The workspace is at least w4_lora_workspace_bytes(...) bytes, 256-byte
+ * aligned.
+ */
+typedef struct {
+    const void *x_dev;
+    const void *A_dev;
+    const void *B_dev;
+    const int32_t *adapter_dev;
+    const float *scaling_dev;
+    const int32_t *ranks_dev;
+    const void *base_dev;
+    void *y_dev;
+    int64_t T;
+    int64_t K;
+    int64_t N;
+    int64_t ldx;
+    int64_t ldbase;
+    int64_t ldy;
+    int32_t adapters;
+    int32_t rank;
+    int32_t dtype;
+    int32_t reserved; /* 0 */
+} w4_lora_args;
+W4_API int w4_lora_add(const w4_lora_args *args, void *workspace_dev, size_t workspace_bytes, void *stream);
+/* 0 for sizes that w4_lora_add refuses. */
+W4_API size_t w4_lora_workspace_bytes(int64_t T, int64_t K, int64_t N, int32_t adapters, int32_t rank);
+
 #ifdef __cplusplus
 }
 #endif

@@ -28,7 +28,8 @@ __all__ = [
     "Options", "STATUS", "KERNEL_DECODE", "KERNEL_TMEM", "FLAG_WEIGHTS_STATIC", "FLAG_TEST_TIMEOUT",
     "Epilogue", "Problem", "EPI_NONE", "EPI_SILU_MUL", "EPI_QKV_SPLIT", "w4a16_gemm_grouped",
     "w4a16_grouped_workspace_bytes", "w4a16_gemm_silu_mul", "w4a16_gemm_qkv", "interleave_gate_up",
-    "qkv_head_group_rows",
+    "qkv_head_group_rows", "w4_route", "w4a16_experts", "w4a16_experts_workspace_bytes", "w4_lora_add",
+    "w4_lora_workspace_bytes",
 ]
 
 KERNEL_DECODE = 1
@@ -52,6 +53,34 @@ class Epilogue(ctypes.Structure):
 
     _fields_ = [("kind", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("q_per_group", ctypes.c_int32),
                 ("reserved", ctypes.c_int32), ("k_dev", ctypes.c_void_p), ("v_dev", ctypes.c_void_p)]
+
+
+class RouteOptions(ctypes.Structure):
+    """w4_route_options of the C ABI."""
+
+    _fields_ = [("k", ctypes.c_int32), ("sigmoid", ctypes.c_int32), ("groups", ctypes.c_int32),
+                ("top_groups", ctypes.c_int32), ("group_top", ctypes.c_int32), ("renormalize", ctypes.c_int32),
+                ("scale", ctypes.c_float), ("dtype", ctypes.c_int32)]
+
+
+class ExpertsArgs(ctypes.Structure):
+    """w4a16_experts_args of the C ABI."""
+
+    _fields_ = [("x_dev", ctypes.c_void_p), ("gate_up_dev", ctypes.c_void_p), ("down_dev", ctypes.c_void_p),
+                ("ids_dev", ctypes.c_void_p), ("weights_dev", ctypes.c_void_p), ("y_dev", ctypes.c_void_p),
+                ("T", ctypes.c_int64), ("K", ctypes.c_int64), ("I", ctypes.c_int64), ("experts", ctypes.c_int32),
+                ("k", ctypes.c_int32), ("g", ctypes.c_int32), ("dtype", ctypes.c_int32)]
+
+
+class LoraArgs(ctypes.Structure):
+    """w4_lora_args of the C ABI."""
+
+    _fields_ = [("x_dev", ctypes.c_void_p), ("A_dev", ctypes.c_void_p), ("B_dev", ctypes.c_void_p),
+                ("adapter_dev", ctypes.c_void_p), ("scaling_dev", ctypes.c_void_p), ("ranks_dev", ctypes.c_void_p),
+                ("base_dev", ctypes.c_void_p), ("y_dev", ctypes.c_void_p), ("T", ctypes.c_int64),
+                ("K", ctypes.c_int64), ("N", ctypes.c_int64), ("ldx", ctypes.c_int64), ("ldbase", ctypes.c_int64),
+                ("ldy", ctypes.c_int64), ("adapters", ctypes.c_int32), ("rank", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
 class Problem(ctypes.Structure):
@@ -107,6 +136,11 @@ def load() -> ctypes.CDLL:
             "w4a16_gemm_grouped": ([ctypes.POINTER(Problem), I32, I64, I32, P, SZ, ctypes.POINTER(Options), P],
                                    ctypes.c_int),
             "w4a16_grouped_workspace_bytes": ([ctypes.POINTER(Problem), I32, I64, I32, ctypes.POINTER(Options)], SZ),
+            "w4_route": ([P, I64, I32, I64, P, ctypes.POINTER(RouteOptions), P, P, P], ctypes.c_int),
+            "w4a16_experts": ([ctypes.POINTER(ExpertsArgs), P, SZ, P], ctypes.c_int),
+            "w4a16_experts_workspace_bytes": ([I64, I64, I64, I32, I32, I32], SZ),
+            "w4_lora_add": ([ctypes.POINTER(LoraArgs), P, SZ, P], ctypes.c_int),
+            "w4_lora_workspace_bytes": ([I64, I64, I64, I32, I32], SZ),
         }
         for name, (args, res) in sigs.items():
             fn = getattr(lib, name)
@@ -409,3 +443,162 @@ def qkv_head_group_rows(wq: torch.Tensor, wk: torch.Tensor, wv: torch.Tensor, he
     k = wk.reshape(groups, head_dim, K)
     v = wv.reshape(groups, head_dim, K)
     return torch.cat([q, k, v], dim=1).reshape(-1, K)
+
+
+# ----------------------------------------------------------------------------- weights chosen row by row
+
+_LOGIT_DTYPES = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}
+
+
+def _rows(t: torch.Tensor, name: str) -> int:
+    """The address of a 2-D CUDA tensor whose rows are contiguous (they may lie further apart than they are long)."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"the rows of {name} must be contiguous")
+    return t.data_ptr()
+
+
+def _ld(t: torch.Tensor) -> int:
+    """Values between a 2-D tensor's rows, which must not overlap (a single row's stride says nothing)."""
+    if t.shape[0] <= 1:
+        return -(-t.shape[1] // 8) * 8
+    if t.stride(0) < t.shape[1]:
+        raise ValueError("rows must not overlap")
+    return t.stride(0)
+
+
+def _like(t, name: str, dtype, shape, device) -> int:
+    """The address of a contiguous tensor of this type, shape and device."""
+    if t.dtype != dtype or tuple(t.shape) != shape or t.device != device:
+        raise ValueError(f"{name} must be {dtype} {list(shape)} on {device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _on_stream(stream, *made):
+    """The stream's handle; what a call made for itself is kept until a stream other than the current one is done."""
+    if stream is not None:
+        for t in made:
+            if t is not None:
+                t.record_stream(stream)
+    return _stream(stream)
+
+
+def _scratch(workspace, need: int, device, stream) -> torch.Tensor:
+    if workspace is None:
+        ws = torch.empty(need, dtype=torch.uint8, device=device)
+        if stream is not None:
+            ws.record_stream(stream)
+        return ws
+    return workspace.get(need) if isinstance(workspace, Workspace) else workspace
+
+
+def w4_route(logits: torch.Tensor, k: int, *, sigmoid: bool = False, bias: torch.Tensor | None = None, groups: int = 1,
+             top_groups: int | None = None, group_top: int = 1, renormalize: bool = True, scale: float = 1.0,
+             weights: torch.Tensor | None = None, ids: torch.Tensor | None = None, stream=None):
+    """The k experts of each row of logits [T, E] (fp16, bf16 or fp32) and their weights: (weights fp32 [T, k], ids
+    int32 [T, k]), largest first, the lowest index first among equals. Scores are the softmax of the logits, or
+    their sigmoid; ``bias`` (fp32 [E]) is added for the choice alone; with ``groups`` > 1 only the ``top_groups``
+    groups with the largest sum of their ``group_top`` best scores are chosen from. Weights are the chosen scores,
+    divided by their sum (``renormalize``), times ``scale``. -inf masks an expert."""
+    dt = _LOGIT_DTYPES.get(logits.dtype)
+    if dt is None or logits.dim() != 2:
+        raise ValueError("logits must be a 2-D fp16, bf16 or fp32 tensor")
+    T, E = logits.shape
+    device = logits.device
+    at = _rows(logits, "logits")
+    b = None if bias is None else _like(bias, "bias", torch.float32, (E,), device)
+    made = (weights is None, ids is None)
+    if weights is None:
+        weights = torch.empty((T, k), dtype=torch.float32, device=device)
+    if ids is None:
+        ids = torch.empty((T, k), dtype=torch.int32, device=device)
+    o = RouteOptions(k, sigmoid, groups, groups if top_groups is None else top_groups, group_top, renormalize, scale, dt)
+    rc = load().w4_route(at, T, E, _ld(logits), b, ctypes.byref(o),
+                         _like(weights, "weights", torch.float32, (T, k), device),
+                         _like(ids, "ids", torch.int32, (T, k), device),
+                         _on_stream(stream, weights if made[0] else None, ids if made[1] else None))
+    _check(rc, "w4_route")
+    return weights, ids
+
+
+def w4a16_experts_workspace_bytes(T: int, K: int, I: int, experts: int, k: int, g: int) -> int:
+    return int(load().w4a16_experts_workspace_bytes(T, K, I, experts, k, g))
+
+
+def w4a16_experts(x: torch.Tensor, gate_up: torch.Tensor, down: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor,
+                  inter: int, g: int, *, y: torch.Tensor | None = None, workspace=None, stream=None) -> torch.Tensor:
+    """y [T, K] with y[t] = sum_j weights[t, j] * down_e (silu(gate_e x[t]) * up_e x[t]), e = ids[t, j].
+
+    x [T, K] fp16 or bf16; gate_up uint8 [E, w4_repacked_bytes(2 * inter, K, g)], each expert's packed rows
+    alternating gate, up (see interleave_gate_up); down uint8 [E, w4_repacked_bytes(K, inter, g)]; ids int32 and
+    weights fp32 [T, k] as w4_route gives them (an id outside [0, E) is a dropped choice)."""
+    dt = _DTYPES.get(x.dtype)
+    if dt is None or x.dim() != 2 or gate_up.dim() != 2 or ids.dim() != 2:
+        raise ValueError("x must be fp16 or bf16 [T, K], gate_up [E, bytes] and ids [T, k]")
+    T, K = x.shape
+    E, k = gate_up.shape[0], ids.shape[1]
+    device = x.device
+    need = w4a16_experts_workspace_bytes(T, K, inter, E, k, g)
+    if need == 0:
+        raise W4Error(1 if min(K, inter, E, k, g) < 1 or k > E or g % 8 else 2, "w4a16_experts")
+    x_at = _dev(x, "x")
+    made = None
+    if y is None:
+        y = made = torch.empty((T, K), dtype=x.dtype, device=device)
+    ws = _scratch(workspace, need, device, stream)
+    a = ExpertsArgs(x_at,
+                    _like(gate_up, "gate_up", torch.uint8, (E, w4_repacked_bytes(2 * inter, K, g)), device),
+                    _like(down, "down", torch.uint8, (E, w4_repacked_bytes(K, inter, g)), device),
+                    _like(ids, "ids", torch.int32, (T, k), device),
+                    _like(weights, "weights", torch.float32, (T, k), device),
+                    _like(y, "y", x.dtype, (T, K), device), T, K, inter, E, k, g, dt)
+    rc = load().w4a16_experts(ctypes.byref(a), _dev(ws, "workspace"), ws.numel() * ws.element_size(),
+                              _on_stream(stream, made))
+    _check(rc, "w4a16_experts")
+    return y
+
+
+def w4_lora_workspace_bytes(T: int, K: int, N: int, adapters: int, rank: int) -> int:
+    return int(load().w4_lora_workspace_bytes(T, K, N, adapters, rank))
+
+
+def w4_lora_add(base: torch.Tensor | None, x: torch.Tensor, A: torch.Tensor, B: torch.Tensor, adapter: torch.Tensor, *,
+                scaling: torch.Tensor | None = None, ranks: torch.Tensor | None = None, y: torch.Tensor | None = None,
+                workspace=None, stream=None) -> torch.Tensor:
+    """y [T, N] = base + scaling[a] * B[a] . (A[a] . x) with each row's own adapter a (base alone for a row whose index
+    is outside [0, R)).
+
+    x [T, K], base [T, N] (or None for zeros) and y fp16 or bf16, rows contiguous, A [R, rank, K], B [R, N, rank] of
+    the same type, adapter int32 [T], scaling fp32 [R] (None: 1), ranks int32 [R] (None: rank): an adapter's own
+    rank, past which A and B are not used. ``y`` may be ``base`` (in place)."""
+    dt = _DTYPES.get(x.dtype)
+    if dt is None or x.dim() != 2 or A.dim() != 3 or B.dim() != 3:
+        raise ValueError("x must be fp16 or bf16 [T, K], A [R, rank, K] and B [R, N, rank]")
+    T, K = x.shape
+    R, rank, _ = A.shape
+    N = B.shape[1]
+    device = x.device
+    x_at = _rows(x, "x")
+    made = None
+    if y is None:
+        y = made = torch.empty((T, N), dtype=x.dtype, device=device)
+    for t, name in ((y, "y"), (base, "base")):
+        if t is not None and (t.dtype != x.dtype or tuple(t.shape) != (T, N) or t.device != device):
+            raise ValueError(f"{name} must be {x.dtype} [{T}, {N}] on {device}")
+    need = w4_lora_workspace_bytes(T, K, N, R, rank)
+    if need == 0:
+        raise W4Error(1 if min(K, N, R, rank) < 1 else 2, "w4_lora_add")
+    ws = _scratch(workspace, need, device, stream)
+    a = LoraArgs(x_at, _like(A, "A", x.dtype, (R, rank, K), device), _like(B, "B", x.dtype, (R, N, rank), device),
+                 _like(adapter, "adapter", torch.int32, (T,), device),
+                 None if scaling is None else _like(scaling, "scaling", torch.float32, (R,), device),
+                 None if ranks is None else _like(ranks, "ranks", torch.int32, (R,), device),
+                 None if base is None else _rows(base, "base"), _rows(y, "y"), T, K, N, _ld(x),
+                 0 if base is None else _ld(base), _ld(y), R, rank, dt, 0)
+    rc = load().w4_lora_add(ctypes.byref(a), _dev(ws, "workspace"), ws.numel() * ws.element_size(),
+                            _on_stream(stream, made))
+    _check(rc, "w4_lora_add")
+    return y

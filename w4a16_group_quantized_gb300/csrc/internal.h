@@ -18,6 +18,7 @@ inline int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // 16-bit value types of weights, scales, activations and outputs.
 constexpr int kDtypeF16 = 0;
 constexpr int kDtypeBf16 = 1;
+constexpr int kDtypeF32 = 2;  // router logits only
 
 // Output epilogues (W4_EPI_* of the C ABI).
 constexpr int kEpiNone = 0;
@@ -131,5 +132,71 @@ bool make_group_plan(const GemmProblem *probs, int count, int64_t M, int32_t g, 
 cudaError_t launch_gemm_grouped(const GemmProblem *probs, int count, int64_t M, int32_t g, void *workspace,
                                 const GroupPlan &plan, const GemmOptions &opt, int num_sms, cudaStream_t stream,
                                 bool *encode_failed);
+
+// ------------------------------------------------------------------ weights chosen row by row
+
+// w4_route's options (w4_route_options of the C ABI), checked.
+struct RouteParams {
+  int k, groups, top_groups, group_top;
+  uint32_t group_mul;  // ceil(2^22 / group size): e * group_mul >> 22 is e's group for e < 1024
+  bool sigmoid, renormalize;
+  float scale;
+};
+constexpr int kRouteMaxExperts = 1024;
+constexpr int kRouteMaxK = 32;
+
+cudaError_t launch_route(const void *logits, int dtype, int64_t T, int E, int64_t ld, const float *bias,
+                         const RouteParams &o, float *weights, int32_t *ids, cudaStream_t stream);
+
+// Rows sorted by a key chosen on the device (rows.cu): the rows of key 0, then of key 1, ... and last those of
+// any key outside [0, nkeys).
+struct RowTile {
+  int32_t key;   // nkeys: rows without a key
+  int32_t row0;  // first sorted position
+  int32_t rows;
+  int32_t pad;
+};
+struct RowPlan {
+  int32_t *perm;     // [count] the row at each sorted position
+  int32_t *inverse;  // [count] the sorted position of each row, -1 without a key (or null: not written)
+  RowTile *tiles;    // each key's positions cut into tiles of `tile` rows, key after key
+  int32_t *ntiles;
+};
+constexpr int kRowsMaxKeys = 1024;
+// The most tiles that `count` rows of `nkeys` keys (and the rows without one) can make.
+inline int64_t max_row_tiles(int64_t count, int nkeys, int tile) {
+  const int64_t most = count / tile + nkeys + 1;
+  return most < count ? most : count;
+}
+// keyless: also cut the rows without a key into tiles.
+cudaError_t launch_row_plan(const int32_t *keys, int64_t count, int nkeys, int tile, bool keyless, const RowPlan &plan,
+                            cudaStream_t stream);
+
+// w4_lora_add.
+struct LoraArgs {
+  const void *base;  // null: zeros
+  const void *x, *A, *B;
+  const int32_t *adapter;
+  const float *scaling;  // null: 1
+  const int32_t *ranks;  // null: rank
+  void *y;
+  int64_t T, N, K, ldx, ldbase, ldy;
+  int adapters, rank, dtype;
+};
+constexpr int kLoraMaxRank = 128;
+size_t lora_workspace_bytes(int64_t T, int64_t N, int64_t K, int adapters, int rank, int num_sms);
+cudaError_t launch_lora(const LoraArgs &a, void *workspace, int num_sms, cudaStream_t stream);
+
+// w4a16_experts.
+struct ExpertsArgs {
+  const void *x, *gate_up, *down;
+  const int32_t *ids;
+  const float *weights;
+  void *y;
+  int64_t T, K, I;
+  int experts, k, g, dtype;
+};
+size_t experts_workspace_bytes(int64_t T, int64_t K, int64_t I, int experts, int k, int g, int num_sms);
+cudaError_t launch_experts(const ExpertsArgs &a, void *workspace, int num_sms, cudaStream_t stream);
 
 }  // namespace w4
