@@ -14,6 +14,7 @@
 // Codes become operands without arithmetic: a code's four bits under the exponent of 16 are 16 + q in either type.
 // A product with ones gives X = sum x over the same k, and (q - z) x sums to sum (16 + q) x - (16 + z) X, exactly in
 // the operands and in 32 bits in the sums; a group's sum is multiplied by its 32-bit s. So no weight is rounded.
+#include "experts.cuh"
 #include "gemm_common.cuh"
 #include "internal.h"
 #include "mma.cuh"
@@ -26,19 +27,7 @@ using namespace detail;
 
 constexpr int kWarps = 8;      // they split K
 constexpr int kSlabRows = 32;  // weight rows of a block
-
-struct Products {
-  const uint16_t *in;    // gate/up: x [T, K]; down: h [pairs, K]
-  const uint8_t *codes;  // expert 0's packed weights
-  int64_t expert_bytes;
-  int64_t meta;          // offset of the group records in them
-  void *out;             // gate/up: h [pairs, N / 2], 16 bits; down: [pairs, N], 32 bits
-  RowPlan plan;
-  int K, N, G, KB, g;
-  int slabs;
-  int choices;           // k: pair / k is the token
-  FastDiv gdiv;
-};
+constexpr int kTmemRows = 12;  // rows an expert has on average from which the tensor-memory kernel runs
 
 // Eight codes -> four pairs (k, k + 1) of 16 + q: each code's bits moved to the top of the fraction that 16 leaves
 // (fp16: a step of 2^-6 at 16, bits 6 to 9; bf16: 2^-3, bits 3 to 6).
@@ -236,31 +225,34 @@ __global__ void __launch_bounds__(256)
                                                          out_bits2<DT>(s[4], s[5]), out_bits2<DT>(s[6], s[7]));
 }
 
-// The workspace: [outputs in 32 bits][h][perm][inverse][tiles][ntiles].
+// The workspace: [error word][ntiles][outputs in 32 bits][h][perm][inverse][tiles].
 struct ExpertsPlan {
+  bool tmem;
   int tile, max_tiles;
-  size_t h, perm, inverse, tiles, ntiles, bytes;
+  size_t part, h, perm, inverse, tiles, bytes;
 };
 
-ExpertsPlan experts_plan(int64_t T, int64_t K, int64_t I, int experts, int k) {
+ExpertsPlan experts_plan(int64_t T, int64_t K, int64_t I, int experts, int k, int g) {
   ExpertsPlan p;
   const int64_t pairs = T * k;
-  // rows per tile: as many as an expert has on average, from the widths that the kernel has
+  // rows per tile: as many as an expert has on average, from the widths that the kernels have
   const int64_t mean = pairs / experts;
-  p.tile = mean <= 8 ? 8 : mean <= 16 ? 16 : 32;
+  p.tmem = mean >= kTmemRows && experts_tmem_takes(g);
+  p.tile = p.tmem ? (mean <= 48 || g % 64 != 0 ? 64 : 128) : mean <= 8 ? 8 : mean <= 16 ? 16 : 32;
   p.max_tiles = static_cast<int>(max_row_tiles(pairs, experts, p.tile));
   auto up = [](size_t v) { return (v + 255) / 256 * 256; };
-  p.h = up(static_cast<size_t>(pairs) * K * 4);
+  p.part = 256;
+  p.h = p.part + up(static_cast<size_t>(pairs) * K * 4);
   p.perm = p.h + up(static_cast<size_t>(pairs) * I * 2);
   p.inverse = p.perm + up(static_cast<size_t>(pairs) * 4);
   p.tiles = p.inverse + up(static_cast<size_t>(pairs) * 4);
-  p.ntiles = p.tiles + up(static_cast<size_t>(p.max_tiles) * sizeof(RowTile));
-  p.bytes = p.ntiles + 256;
+  p.bytes = p.tiles + up(static_cast<size_t>(p.max_tiles) * sizeof(RowTile));
   return p;
 }
 
 template <int DT, bool GATED>
-cudaError_t launch_products(const Products &p, const ExpertsPlan &plan, cudaStream_t stream) {
+cudaError_t launch_products(const Products &p, const ExpertsPlan &plan, int num_sms, cudaStream_t stream) {
+  if (plan.tmem) return launch_experts_tmem(p, DT, GATED, plan.tile, num_sms, stream);
   const bool whole = p.g % kTK == 0;
   auto kern = plan.tile == 8    ? (whole ? experts_kernel<DT, 1, GATED, true> : experts_kernel<DT, 1, GATED, false>)
               : plan.tile == 16 ? (whole ? experts_kernel<DT, 2, GATED, true> : experts_kernel<DT, 2, GATED, false>)
@@ -269,12 +261,13 @@ cudaError_t launch_products(const Products &p, const ExpertsPlan &plan, cudaStre
 }
 
 template <int DT>
-cudaError_t launch_dt(const ExpertsArgs &a, uint8_t *ws, const ExpertsPlan &plan, cudaStream_t stream) {
+cudaError_t launch_dt(const ExpertsArgs &a, uint8_t *ws, const ExpertsPlan &plan, int num_sms, cudaStream_t stream) {
   RowPlan rows;
   rows.perm = reinterpret_cast<int32_t *>(ws + plan.perm);
   rows.inverse = reinterpret_cast<int32_t *>(ws + plan.inverse);
   rows.tiles = reinterpret_cast<RowTile *>(ws + plan.tiles);
-  rows.ntiles = reinterpret_cast<int32_t *>(ws + plan.ntiles);
+  rows.ntiles = reinterpret_cast<int32_t *>(ws + 4);
+  rows.err = reinterpret_cast<uint32_t *>(ws);
   cudaError_t e = launch_row_plan(a.ids, a.T * a.k, a.experts, plan.tile, false, rows, stream);
   if (e != cudaSuccess) return e;
   auto products = [&](const void *in, const void *packed, int64_t N, int64_t K, void *out) {
@@ -290,33 +283,33 @@ cudaError_t launch_dt(const ExpertsArgs &a, uint8_t *ws, const ExpertsPlan &plan
     p.expert_bytes = p.meta + cdiv(N, kTN) * p.G * kRecBytes;
     p.out = out;
     p.plan = rows;
-    p.slabs = static_cast<int>(cdiv(N, kSlabRows));
+    p.err = rows.err;
+    p.slabs = static_cast<int>(cdiv(N, plan.tmem ? kTN : kSlabRows));
     p.choices = a.k;
     p.gdiv = make_fastdiv(static_cast<uint32_t>(a.g));
     return p;
   };
-  e = launch_products<DT, true>(products(a.x, a.gate_up, 2 * a.I, a.K, ws + plan.h), plan, stream);
+  e = launch_products<DT, true>(products(a.x, a.gate_up, 2 * a.I, a.K, ws + plan.h), plan, num_sms, stream);
   if (e != cudaSuccess) return e;
-  e = launch_products<DT, false>(products(ws + plan.h, a.down, a.K, a.I, ws), plan, stream);
+  e = launch_products<DT, false>(products(ws + plan.h, a.down, a.K, a.I, ws + plan.part), plan, num_sms, stream);
   if (e != cudaSuccess) return e;
   return launch_programmatic(combine_kernel<DT>, static_cast<int>(cdiv(a.T * (a.K / 8), 256)), 256, 0, stream,
-                             reinterpret_cast<const float *>(ws), static_cast<const int32_t *>(rows.inverse), a.weights,
+                             reinterpret_cast<const float *>(ws + plan.part), static_cast<const int32_t *>(rows.inverse), a.weights,
                              a.T, static_cast<int>(a.K), a.k, static_cast<uint16_t *>(a.y));
 }
 
 }  // namespace
 
 size_t experts_workspace_bytes(int64_t T, int64_t K, int64_t I, int experts, int k, int g, int num_sms) {
-  (void)g;
   (void)num_sms;
-  return experts_plan(T, K, I, experts, k).bytes;
+  return experts_plan(T, K, I, experts, k, g).bytes;
 }
 
 cudaError_t launch_experts(const ExpertsArgs &a, void *workspace, int num_sms, cudaStream_t stream) {
-  (void)num_sms;
-  const ExpertsPlan plan = experts_plan(a.T, a.K, a.I, a.experts, a.k);
+  const ExpertsPlan plan = experts_plan(a.T, a.K, a.I, a.experts, a.k, a.g);
   uint8_t *ws = static_cast<uint8_t *>(workspace);
-  return a.dtype == kDtypeBf16 ? launch_dt<kDtypeBf16>(a, ws, plan, stream) : launch_dt<kDtypeF16>(a, ws, plan, stream);
+  return a.dtype == kDtypeBf16 ? launch_dt<kDtypeBf16>(a, ws, plan, num_sms, stream)
+                               : launch_dt<kDtypeF16>(a, ws, plan, num_sms, stream);
 }
 
 }  // namespace w4

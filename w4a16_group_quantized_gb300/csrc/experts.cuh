@@ -1,0 +1,31 @@
+// What the two kernels of the experts' products share (experts.cu: few rows an expert; experts_tmem.cu: many).
+#pragma once
+
+#include "gemm_common.cuh"
+#include "internal.h"
+
+namespace w4 {
+namespace detail {
+
+struct Products {
+  const uint16_t *in;    // gate/up: x [T, K]; down: h [pairs, K]
+  const uint8_t *codes;  // expert 0's packed weights
+  int64_t expert_bytes;
+  int64_t meta;          // offset of the group records in them
+  void *out;             // gate/up: h [pairs, N / 2], 16 bits; down: [pairs, N], 32 bits
+  RowPlan plan;
+  uint32_t *err;
+  int K, N, G, KB, g;
+  int slabs;             // blocks (experts.cu) or weight tiles (experts_tmem.cu) of N
+  int choices;           // k: pair / k is the token
+  FastDiv gdiv;
+};
+
+// Whether the tensor-memory kernel takes groups of g: a block of 64 k then holds at most two, 32 k each.
+inline bool experts_tmem_takes(int g) { return g % 32 == 0; }
+
+// Rows of `in` per tile of the tensor-memory kernel, tile 64 or 128.
+cudaError_t launch_experts_tmem(const Products &p, int dtype, bool gated, int tile, int num_sms, cudaStream_t stream);
+
+}  // namespace detail
+}  // namespace w4

@@ -1,0 +1,454 @@
+// The experts' products for many rows an expert, on tcgen05 (the formulas and the few-row form: experts.cu).
+//
+// As in gemm.cu the weights are the MMA's M = 128 side and the rows of `in` its N side; A comes from tensor memory,
+// where dequant warps store it, and B from shared memory. Unlike there, A is the integers q - z, exactly, and a
+// group's sum is multiplied by its 32-bit scale outside of the tensor cores: no weight is rounded, so that the one
+// 16-bit rounding between x and y is that of h. The price is that every group's sums leave tensor memory once
+// (128 x 128 values per 128 k, a packed 32-bit multiply-add for two of them).
+//
+// A unit is one 128-row weight tile x one tile of up to BN rows of one expert; the CTAs take units in turn and walk K in
+// chunks of CB blocks of 64, with no stop between units. Roles (24 warps, one CTA a SM):
+//   4 producer warps   gather the rows of x (16-byte asynchronous copies, 128-byte swizzle); one lane copies the
+//                      chunk's codes and group records in bulk
+//   2 MMA warps        take the chunks in turn, each into an accumulator of its own that the chunk starts from zero
+//   8 dequant warps    two warpgroups take the chunks in turn: thread r stores row r's q - z in tensor memory and its
+//                      scale in a ring in shared memory
+//   8 sum warps        two warpgroups, each one half of the rows of `in`: add scale * (chunk's sums) to their 32-bit
+//                      registers, and write h or the output at a unit's end
+// SUB = 2: a chunk of one block whose halves of 32 k lie in different groups, each with an accumulator of its own.
+//
+// Barriers, each waited for in every phase and in order (chunk c; S stages):
+//   full[c % S]      the chunk's rows, codes and records have landed
+//   ready[c % 2][c / 2 % 2]  its A operand is stored
+//   free[c % 2][c / 2 % 2]   its MMAs are complete, for the dequant warps: the A slot is free
+//   done[c % S]      its MMAs are complete, for the others: the stage is free, its sums can be read
+//   empty[c % 2]     its sums have been read
+// The sum warps of chunk c are done before chunk c + 2's MMAs start, hence before done of c + 2: the scale ring's
+// eight places (a dequant warp writes c + 8's after free of c + 4) and done's parity are never overtaken. The
+// dequant warps do not wait for done: the other warpgroup may be a whole turn of the stages ahead of one.
+// Every wait is bounded (ptx.cuh).
+#include <atomic>
+
+#include "experts.cuh"
+#include "internal.h"
+#include "ptx.cuh"
+
+namespace w4 {
+namespace {
+
+using namespace detail;
+
+constexpr int kRegsLaunch = 80;  // 65,536 / 768 threads, a multiple of 8
+constexpr int kRegsLow = 56;     // producers, MMA warps
+constexpr int kRegsDequant = 72;
+constexpr int kRegsSum = 112;
+static_assert(2 * kRegsLow + 2 * kRegsDequant + 2 * kRegsSum <= 6 * kRegsLaunch, "registers the block was launched with");
+
+template <int BN, int CB, int SUB>
+struct TCfg {
+  static constexpr int kXSub = BN * 128;  // one block of 64 k of BN rows
+  static constexpr int kXBytes = CB * kXSub;
+  static constexpr int kCodeBytes = CB * kTileBytes;
+  static constexpr int kStageBytes = (kXBytes + kCodeBytes + SUB * kRecBytes + 1023) / 1024 * 1024;
+  static constexpr int kStagesRaw = 216 * 1024 / kStageBytes;
+  static constexpr int kStages = kStagesRaw > 8 ? 8 : kStagesRaw;
+  static constexpr int kScaleSlots = 8;
+  static constexpr int kSmemBytes = kStages * kStageBytes + 1024;
+  static constexpr int kASlotCols = CB * 32;   // 128 rows x 64 16-bit values: 32 columns a block
+  static constexpr int kACol0 = 2 * SUB * BN;  // accumulators first
+  static constexpr int kLag = 2;               // chunks a producer keeps in flight before it waits for one
+  static_assert(kACol0 + 4 * kASlotCols <= 512, "tensor memory");
+  static_assert(kStages > kLag + 1, "a producer signals a chunk kLag chunks late");
+};
+
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t pack2(uint32_t lo, uint32_t hi) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(lo), "r"(hi));
+  return d;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float *lo, float *hi) {
+  uint32_t a, b;
+  asm("mov.b64 {%0, %1}, %2;" : "=r"(a), "=r"(b) : "l"(v));
+  *lo = __uint_as_float(a);
+  *hi = __uint_as_float(b);
+}
+
+template <int R>
+__device__ __forceinline__ void regs_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
+}
+template <int R>
+__device__ __forceinline__ void regs_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R));
+}
+
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// The units of a CTA in order, the next one's tile read ahead.
+struct UnitWalk {
+  const Products &p;
+  int64_t u, units;
+  int step;
+  RowTile next;
+  __device__ __forceinline__ UnitWalk(const Products &p_, int64_t units_) : p(p_), u(blockIdx.x), units(units_), step(gridDim.x) {
+    if (u < units) next = p.plan.tiles[u / p.slabs];
+  }
+  __device__ __forceinline__ bool take(RowTile *tile, int *wt) {
+    if (u >= units) return false;
+    *tile = next;
+    *wt = static_cast<int>(u % p.slabs);
+    u += step;
+    if (u < units) next = p.plan.tiles[u / p.slabs];
+    return true;
+  }
+};
+
+template <int DT, int BN, int CB, int SUB, bool GATED>
+__global__ void __launch_bounds__(768, 1) experts_tmem_kernel(const __grid_constant__ Products p) {
+  using C = TCfg<BN, CB, SUB>;
+  constexpr int S = C::kStages;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t full_bar[S], done_bar[S], ready_bar[2][2], free_bar[2][2], empty_bar[2], drain_bar[2];
+  __shared__ float scales[C::kScaleSlots][SUB][kTN];
+  __shared__ uint32_t tmem_sh, abort_sh;
+
+  const uint32_t smem_base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  volatile uint32_t *abort_flag = &abort_sh;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(smem_u32(&full_bar[s]), 128 + 1);  // the producers' threads and the bulk copies' bytes
+      mbar_init(smem_u32(&done_bar[s]), 1);
+    }
+    for (int e = 0; e < 2; ++e) {
+      for (int a = 0; a < 2; ++a) {
+        mbar_init(smem_u32(&ready_bar[e][a]), 4);
+        mbar_init(smem_u32(&free_bar[e][a]), 1);
+      }
+      mbar_init(smem_u32(&empty_bar[e]), 8);
+      mbar_init(smem_u32(&drain_bar[e]), 1);
+    }
+    abort_sh = 0;
+    fence_mbar_init();
+  }
+  if (warp == 8) {
+    tmem_alloc(smem_u32(&tmem_sh), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncwarp();
+  cta_sync_all();
+  tc_fence_after();
+  const uint32_t tmem = tmem_sh;
+  if (threadIdx.x == 0) griddep_launch_dependents();
+  griddep_wait();  // the plan and `in` come from the grids before this one
+  const int64_t units = static_cast<int64_t>(*p.plan.ntiles) * p.slabs;
+  const int chunks = (p.KB + CB - 1) / CB;  // of a unit
+  constexpr uint64_t kLimit = kWaitLimitCycles;
+
+  if (warp < 4) {
+    // ------------------------------------------------------------ producers
+    regs_down<kRegsLow>();
+    const int tid = threadIdx.x;
+    constexpr int kRows = BN / 16;  // rows of a thread: tid / 8, + 16, ...; its 16 bytes of each 128: tid % 8
+    const int sub = tid / 8, part = tid % 8;
+    const uint32_t spot = sub * 128 + ((part ^ (sub & 7)) * 16);
+    uint32_t c = 0;
+    bool ok = true;
+    RowTile rt;
+    int wt;
+    for (UnitWalk w(p, units); ok && w.take(&rt, &wt);) {
+      const uint16_t *row[kRows];
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) {
+        const int m = sub + 16 * i;
+        row[i] = nullptr;
+        if (m < rt.rows) {
+          const int64_t at = GATED ? p.plan.perm[rt.row0 + m] / p.choices : rt.row0 + m;
+          row[i] = p.in + at * p.K + part * 8;
+        }
+      }
+      const uint8_t *expert = p.codes + rt.key * p.expert_bytes;
+      const uint8_t *codes = expert + static_cast<int64_t>(wt) * p.KB * kTileBytes;
+      const uint8_t *meta = expert + p.meta + static_cast<int64_t>(wt) * p.G * kRecBytes;
+      const uint64_t policy = policy_evict_normal();  // an expert's other row tiles read the weights again
+      for (int q = 0; q < chunks; ++q, ++c) {
+        const int s = c % S;
+        if (c >= static_cast<uint32_t>(S)) ok = warp_wait(smem_u32(&done_bar[s]), (c / S - 1) & 1, abort_flag, p.err, kLimit);
+        if (!ok) break;
+        const uint32_t stage = smem_base + s * C::kStageBytes;
+        const int k0 = q * CB * kTK;
+        const int nb = min(CB, p.KB - q * CB);
+        if (tid == 0) {
+          const int j0 = p.gdiv.div(k0);
+          const int nrec = SUB == 1 ? 1 : p.gdiv.div(min(k0 + kTK, p.K) - 1) - j0 + 1;
+          const uint32_t bar = smem_u32(&full_bar[s]);
+          mbar_arrive_expect_tx(bar, nb * kTileBytes + nrec * kRecBytes);
+          bulk_g2s(stage + C::kXBytes, codes + static_cast<int64_t>(q) * CB * kTileBytes, nb * kTileBytes, bar, policy);
+          bulk_g2s(stage + C::kXBytes + C::kCodeBytes, meta + static_cast<int64_t>(j0) * kRecBytes, nrec * kRecBytes, bar,
+                   policy);
+        }
+#pragma unroll
+        for (int b = 0; b < CB; ++b) {
+          const int k = k0 + b * kTK;
+          if (b >= nb) break;
+          const uint32_t bytes = k + part * 8 < p.K ? 16u : 0u;  // K is a multiple of 8
+#pragma unroll
+          for (int i = 0; i < kRows; ++i)
+            if (row[i])
+              cp_async16_zfill(stage + b * C::kXSub + i * 2048 + spot, bytes ? row[i] + k : p.in, bytes);
+        }
+        cp_async_commit();
+        if (c >= static_cast<uint32_t>(C::kLag)) {
+          cp_async_wait<C::kLag>();
+          fence_proxy_async_shared();  // the copies' bytes before the MMAs' reads of them
+          mbar_arrive(smem_u32(&full_bar[(c - C::kLag) % S]));
+        }
+      }
+    }
+    cp_async_wait<0>();
+    fence_proxy_async_shared();
+    for (uint32_t i = c >= static_cast<uint32_t>(C::kLag) ? c - C::kLag : 0u; i < c; ++i) mbar_arrive(smem_u32(&full_bar[i % S]));
+    if (!ok && tid == 0)  // no copy in flight when the CTA leaves
+      for (uint32_t i = c >= static_cast<uint32_t>(S) ? c - S : 0u; i < c; ++i) drain_wait(smem_u32(&full_bar[i % S]), (i / S) & 1);
+  } else if (warp < 8) {
+    regs_down<kRegsLow>();
+    if (warp < 6) {
+      // ---------------------------------------------------------- MMA issue
+      const int e = warp - 4;
+      uint32_t c = 0;
+      bool ok = true;
+      RowTile rt;
+      int wt;
+      for (UnitWalk w(p, units); ok && w.take(&rt, &wt);) {
+        const uint32_t idesc = idesc_f16_f32(128, (rt.rows + 15) / 16 * 16, DT == kDtypeBf16);
+        for (int q = 0; q < chunks; ++q, ++c) {
+          if (static_cast<int>(c & 1) != e) continue;
+          const int s = c % S;
+          const uint32_t n = c / 2;  // this warp's chunks so far
+          if (n > 0) ok = warp_wait(smem_u32(&empty_bar[e]), (n - 1) & 1, abort_flag, p.err, kLimit);
+          if (ok) ok = warp_wait(smem_u32(&ready_bar[e][n & 1]), (n / 2) & 1, abort_flag, p.err, kLimit);
+          if (!ok) break;
+          tc_fence_after();
+          if (lane == 0) {
+            const int nb = min(CB, p.KB - q * CB);
+            const uint32_t xs = smem_base + s * C::kStageBytes;
+            const uint32_t a = tmem + C::kACol0 + (2 * e + (n & 1)) * C::kASlotCols;
+#pragma unroll
+            for (int b = 0; b < CB; ++b) {
+              if (b >= nb) break;
+              const uint64_t bdesc = sw128_kmajor_desc(xs + b * C::kXSub);
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk) {
+                const int half = SUB == 2 ? kk / 2 : 0;
+                const bool fresh = SUB == 2 ? kk % 2 == 0 : b == 0 && kk == 0;
+                mma_f16_ts(tmem + (e * SUB + half) * BN, a + b * 32 + kk * 8, bdesc + static_cast<uint64_t>(kk * 2), idesc,
+                           fresh ? 0u : 1u);
+              }
+            }
+            mma_commit(smem_u32(&free_bar[e][n & 1]));
+            mma_commit(smem_u32(&done_bar[s]));
+          }
+          __syncwarp();
+        }
+      }
+      if (lane == 0 && *abort_flag) {
+        mma_commit(smem_u32(&drain_bar[e]));
+        drain_wait(smem_u32(&drain_bar[e]), 0);
+      }
+    }
+  } else if (warp < 16) {
+    // ------------------------------------------------------------ dequant
+    regs_down<kRegsDequant>();
+    const int e = (warp - 8) / 4;
+    const int lq = warp % 4;
+    const int r = lq * 32 + lane;
+    const uint32_t lane_addr = static_cast<uint32_t>(lq * 32) << 16;
+    int64_t mine = 0;  // chunks of the CTA
+    if (blockIdx.x < units) mine = (units - blockIdx.x + gridDim.x - 1) / gridDim.x * chunks;
+    int q = e;         // chunk of its unit
+    while (q >= chunks) q -= chunks;
+    for (int64_t c = e; c < mine; c += 2) {
+      const int s = static_cast<int>(c % S);
+      if (!warp_wait(smem_u32(&full_bar[s]), static_cast<uint32_t>(c / S) & 1, abort_flag, p.err, kLimit)) break;
+      const uint32_t n = static_cast<uint32_t>(c / 2);  // this warpgroup's chunks so far
+      if (n >= 2 && !warp_wait(smem_u32(&free_bar[e][n & 1]), (n / 2 - 1) & 1, abort_flag, p.err, kLimit)) break;
+      const uint32_t stage = smem_base + s * C::kStageBytes;
+      const uint32_t codes = stage + C::kXBytes + r * 16;
+      const uint32_t rec = stage + C::kXBytes + C::kCodeBytes;
+      const int nb = min(CB, p.KB - q * CB);
+      GroupConsts gc[SUB];
+#pragma unroll
+      for (int h = 0; h < SUB; ++h) {
+        // the second half's record is the first's when both lie in one group (or the half lies past K)
+        const int k0 = q * kTK;
+        const uint32_t off = h == 0 ? 0u : (p.gdiv.div(min(k0 + 32, p.K - 1)) - p.gdiv.div(k0)) * kRecBytes;
+        const uint32_t bits = lds16(rec + off + 2 * r);
+        gc[h] = group_consts<DT>(bits, (lds8(rec + off + 256 + r / 2) >> (4 * (r & 1))) & 0xFu);
+        scales[c % C::kScaleSlots][h][r] = scale_f32<DT>(bits);
+      }
+      const uint32_t a = tmem + lane_addr + C::kACol0 + (2 * e + (n & 1)) * C::kASlotCols;
+      tc_fence_after();
+#pragma unroll
+      for (int b = 0; b < CB; ++b) {
+        if (b >= nb) break;
+        const uint4 w0 = lds128(codes + b * kTileBytes);
+        const uint4 w1 = lds128(codes + b * kTileBytes + 2048);
+        uint32_t out[16];
+        dequant_word_int<DT>(w0.x, gc[0], out);
+        dequant_word_int<DT>(w0.y, gc[0], out + 4);
+        dequant_word_int<DT>(w0.z, gc[0], out + 8);
+        dequant_word_int<DT>(w0.w, gc[0], out + 12);
+        tmem_st_32x32b_x16(a + b * 32, out);
+        dequant_word_int<DT>(w1.x, gc[SUB - 1], out);
+        dequant_word_int<DT>(w1.y, gc[SUB - 1], out + 4);
+        dequant_word_int<DT>(w1.z, gc[SUB - 1], out + 8);
+        dequant_word_int<DT>(w1.w, gc[SUB - 1], out + 12);
+        tmem_st_32x32b_x16(a + b * 32 + 16, out);
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&ready_bar[e][n & 1]));
+      q += 2;
+      while (q >= chunks) q -= chunks;
+    }
+  } else {
+    // ------------------------------------------------------------ sums
+    regs_up<kRegsSum>();
+    constexpr int kCols = BN / 2;  // of a warpgroup
+    static_assert(kCols % 32 == 0, "two loads of 16 columns at a time");
+    const int half = (warp - 16) / 4;
+    const int lq = warp % 4;
+    const int r = lq * 32 + lane;
+    const uint32_t lane_addr = static_cast<uint32_t>(lq * 32) << 16;
+    uint32_t c = 0;
+    bool ok = true;
+    RowTile rt;
+    int wt;
+    for (UnitWalk w(p, units); ok && w.take(&rt, &wt);) {
+      const int cols = min(max(rt.rows - half * kCols, 0), kCols);  // this warpgroup's columns with a row
+      uint64_t acc[kCols / 2];
+#pragma unroll
+      for (int i = 0; i < kCols / 2; ++i) acc[i] = 0ull;
+      for (int q = 0; q < chunks; ++q, ++c) {
+        const int s = c % S;
+        ok = warp_wait(smem_u32(&done_bar[s]), (c / S) & 1, abort_flag, p.err, kLimit);
+        if (!ok) break;
+        tc_fence_after();
+#pragma unroll
+        for (int h = 0; h < SUB; ++h) {
+          if (h == 1 && q * kTK + 32 >= p.K) break;  // its products were not of this unit's K
+          const uint32_t sb = __float_as_uint(scales[c % C::kScaleSlots][h][r]);
+          const uint64_t s2 = pack2(sb, sb);
+          const uint32_t d = tmem + lane_addr + ((c & 1) * SUB + h) * BN + half * kCols;
+#pragma unroll
+          for (int j = 0; j < kCols; j += 32) {
+            if (j >= cols) break;
+            uint32_t v0[16], v1[16];
+            tmem_ld_32x32b_x16(d + j, v0);
+            tmem_ld_32x32b_x16(d + j + 16, v1);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 8; ++i) acc[j / 2 + i] = fma2(s2, pack2(v0[2 * i], v0[2 * i + 1]), acc[j / 2 + i]);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) acc[j / 2 + 8 + i] = fma2(s2, pack2(v1[2 * i], v1[2 * i + 1]), acc[j / 2 + 8 + i]);
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&empty_bar[c & 1]));
+      }
+      if (!ok) break;
+      const int n = wt * kTN + r;
+      const int64_t pos0 = rt.row0 + half * kCols;
+      if (GATED) {
+        // rows n & ~1 (even lane: gate) and n | 1 (odd lane: up): the pair swaps values, the even lane makes the
+        // first half of the columns, the odd lane the second
+        const int odd = lane & 1;
+        uint16_t *out = static_cast<uint16_t *>(p.out) + n / 2;
+        const int ld = p.N / 2;
+#pragma unroll
+        for (int i = 0; i < kCols / 4; ++i) {
+          float f[2], b[2];  // columns 2 i, 2 i + 1 of the first and the second half
+          unpack2(acc[i], &f[0], &f[1]);
+          unpack2(acc[i + kCols / 4], &b[0], &b[1]);
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const float got = __shfl_xor_sync(0xffffffffu, odd ? f[j] : b[j], 1);
+            const float gate = odd ? got : f[j], up = odd ? b[j] : got;
+            const int col = 2 * i + j + odd * (kCols / 2);
+            if (n < p.N && col < cols) out[(pos0 + col) * ld] = out_bits<DT>(silu_mul(gate, up));
+          }
+        }
+      } else if (n < p.N) {
+        float *out = static_cast<float *>(p.out) + n;
+#pragma unroll
+        for (int i = 0; i < kCols / 2; ++i) {
+          float f0, f1;
+          unpack2(acc[i], &f0, &f1);
+          if (2 * i < cols) out[(pos0 + 2 * i) * p.N] = f0;
+          if (2 * i + 1 < cols) out[(pos0 + 2 * i + 1) * p.N] = f1;
+        }
+      }
+      __syncwarp();
+    }
+  }
+
+  tc_fence_before();
+  __syncwarp();
+  cta_sync_all();
+  if (warp == 8) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int DT, int BN, int CB, int SUB, bool GATED>
+cudaError_t launch_one(const Products &p, int num_sms, cudaStream_t stream) {
+  auto kern = experts_tmem_kernel<DT, BN, CB, SUB, GATED>;
+  constexpr int bytes = TCfg<BN, CB, SUB>::kSmemBytes;
+  // the opt-in to this much shared memory is an attribute of the function on each device
+  static std::atomic<uint64_t> set{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? uint64_t{1} << dev : 0;
+  if (!(set.load() & bit)) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess) return e;
+    set.fetch_or(bit);
+  }
+  return launch_programmatic(kern, num_sms, 768, bytes, stream, p);
+}
+
+template <int DT, bool GATED>
+cudaError_t launch_groups(const Products &p, int tile, int num_sms, cudaStream_t stream) {
+  if (p.g % 128 == 0)
+    return tile == 128 ? launch_one<DT, 128, 2, 1, GATED>(p, num_sms, stream) : launch_one<DT, 64, 2, 1, GATED>(p, num_sms, stream);
+  if (p.g % 64 == 0)
+    return tile == 128 ? launch_one<DT, 128, 1, 1, GATED>(p, num_sms, stream) : launch_one<DT, 64, 1, 1, GATED>(p, num_sms, stream);
+  return launch_one<DT, 64, 1, 2, GATED>(p, num_sms, stream);
+}
+
+}  // namespace
+
+namespace detail {
+
+cudaError_t launch_experts_tmem(const Products &p, int dtype, bool gated, int tile, int num_sms, cudaStream_t stream) {
+  if (dtype == kDtypeBf16)
+    return gated ? launch_groups<kDtypeBf16, true>(p, tile, num_sms, stream) : launch_groups<kDtypeBf16, false>(p, tile, num_sms, stream);
+  return gated ? launch_groups<kDtypeF16, true>(p, tile, num_sms, stream) : launch_groups<kDtypeF16, false>(p, tile, num_sms, stream);
+}
+
+}  // namespace detail
+}  // namespace w4

@@ -161,6 +161,7 @@ struct RowPlan {
   int32_t *inverse;  // [count] the sorted position of each row, -1 without a key (or null: not written)
   RowTile *tiles;    // each key's positions cut into tiles of `tile` rows, key after key
   int32_t *ntiles;
+  uint32_t *err;     // a device error word to clear (or null)
 };
 constexpr int kRowsMaxKeys = 1024;
 // The most tiles that `count` rows of `nkeys` keys (and the rows without one) can make.

@@ -82,6 +82,7 @@ __global__ void __launch_bounds__(kThreads)
     all += (counts[nkeys] + tile - 1) / tile;
   }
   if (tid == 0) *plan.ntiles = all;
+  if (tid == 0 && plan.err) *plan.err = 0u;
   __syncthreads();
   const int buckets = nkeys + (keyless ? 1 : 0);
   for (int i = tid; i < all; i += kThreads) {
