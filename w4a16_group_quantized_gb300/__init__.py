@@ -16,6 +16,7 @@ uint32 words are carried in torch.int32 tensors (same bits).
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -448,51 +449,63 @@ def qkv_head_group_rows(wq: torch.Tensor, wk: torch.Tensor, wv: torch.Tensor, he
 # ----------------------------------------------------------------------------- weights chosen row by row
 
 _LOGIT_DTYPES = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}
+_repacked = functools.lru_cache(maxsize=1024)(w4_repacked_bytes)
+
+# A decode step makes these calls with a few microseconds of device work each, so the argument checks below read each
+# property once and the workspace is sized only when the library finds it too small.
 
 
 def _rows(t: torch.Tensor, name: str) -> int:
-    """The address of a 2-D CUDA tensor whose rows are contiguous (they may lie further apart than they are long)."""
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.shape[1] > 1 and t.stride(1) != 1:
+    """Values between the rows of a 2-D CUDA tensor, which are contiguous and do not overlap, but may lie further apart
+    than they are long (a single row's stride says nothing)."""
+    n, m = t.shape
+    if t.is_contiguous():
+        return m if n > 1 else -(-m // 8) * 8
+    if m > 1 and t.stride(1) != 1:
         raise ValueError(f"the rows of {name} must be contiguous")
-    return t.data_ptr()
-
-
-def _ld(t: torch.Tensor) -> int:
-    """Values between a 2-D tensor's rows, which must not overlap (a single row's stride says nothing)."""
-    if t.shape[0] <= 1:
-        return -(-t.shape[1] // 8) * 8
-    if t.stride(0) < t.shape[1]:
-        raise ValueError("rows must not overlap")
+    if n <= 1:
+        return -(-m // 8) * 8
+    if t.stride(0) < m:
+        raise ValueError(f"the rows of {name} must not overlap")
     return t.stride(0)
 
 
-def _like(t, name: str, dtype, shape, device) -> int:
+def _like(t: torch.Tensor, name: str, dtype, shape, device) -> int:
     """The address of a contiguous tensor of this type, shape and device."""
-    if t.dtype != dtype or tuple(t.shape) != shape or t.device != device:
+    if t.dtype != dtype or t.shape != shape or t.device != device:
         raise ValueError(f"{name} must be {dtype} {list(shape)} on {device}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     return t.data_ptr()
 
 
-def _on_stream(stream, *made):
-    """The stream's handle; what a call made for itself is kept until a stream other than the current one is done."""
-    if stream is not None:
-        for t in made:
-            if t is not None:
-                t.record_stream(stream)
-    return _stream(stream)
+def _handle(stream, device, *made) -> int:
+    """The stream's handle. What a call made for itself (``made``) is kept until a stream given by the caller is done
+    with it."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device.index)
+    for t in made:
+        if t is not None:
+            t.record_stream(stream)
+    return stream.cuda_stream
 
 
-def _scratch(workspace, need: int, device, stream) -> torch.Tensor:
+def _run_with(call, args, workspace, sized, device, stream, made, what: str):
+    """call(args, workspace, its bytes, stream). A Workspace grows, and without one a buffer is made, by sized()."""
+    own = None
     if workspace is None:
-        ws = torch.empty(need, dtype=torch.uint8, device=device)
-        if stream is not None:
-            ws.record_stream(stream)
-        return ws
-    return workspace.get(need) if isinstance(workspace, Workspace) else workspace
+        ws = own = torch.empty(max(sized(), 1), dtype=torch.uint8, device=device)
+    else:
+        ws = workspace.buf if isinstance(workspace, Workspace) else workspace
+        if ws.device != device or not ws.is_contiguous():
+            raise ValueError(f"workspace must be contiguous on {device}")
+    handle = _handle(stream, device, made, own)
+    rc = call(args, ws.data_ptr(), ws.numel() * ws.element_size(), handle)
+    if rc == 4 and isinstance(workspace, Workspace):
+        ws = workspace.get(sized())
+        rc = call(args, ws.data_ptr(), ws.numel() * ws.element_size(), handle)
+    if rc != 0:
+        raise W4Error(rc, what)
 
 
 def w4_route(logits: torch.Tensor, k: int, *, sigmoid: bool = False, bias: torch.Tensor | None = None, groups: int = 1,
@@ -504,23 +517,29 @@ def w4_route(logits: torch.Tensor, k: int, *, sigmoid: bool = False, bias: torch
     groups with the largest sum of their ``group_top`` best scores are chosen from. Weights are the chosen scores,
     divided by their sum (``renormalize``), times ``scale``. -inf masks an expert."""
     dt = _LOGIT_DTYPES.get(logits.dtype)
-    if dt is None or logits.dim() != 2:
-        raise ValueError("logits must be a 2-D fp16, bf16 or fp32 tensor")
+    if dt is None or logits.dim() != 2 or not logits.is_cuda:
+        raise ValueError("logits must be a 2-D fp16, bf16 or fp32 CUDA tensor")
     T, E = logits.shape
     device = logits.device
-    at = _rows(logits, "logits")
+    ld = _rows(logits, "logits")
     b = None if bias is None else _like(bias, "bias", torch.float32, (E,), device)
-    made = (weights is None, ids is None)
+    shape = (T, max(k, 0))
+    made_w = made_i = None
     if weights is None:
-        weights = torch.empty((T, k), dtype=torch.float32, device=device)
+        weights = made_w = torch.empty(shape, dtype=torch.float32, device=device)
+        w_at = weights.data_ptr()
+    else:
+        w_at = _like(weights, "weights", torch.float32, shape, device)
     if ids is None:
-        ids = torch.empty((T, k), dtype=torch.int32, device=device)
+        ids = made_i = torch.empty(shape, dtype=torch.int32, device=device)
+        i_at = ids.data_ptr()
+    else:
+        i_at = _like(ids, "ids", torch.int32, shape, device)
     o = RouteOptions(k, sigmoid, groups, groups if top_groups is None else top_groups, group_top, renormalize, scale, dt)
-    rc = load().w4_route(at, T, E, _ld(logits), b, ctypes.byref(o),
-                         _like(weights, "weights", torch.float32, (T, k), device),
-                         _like(ids, "ids", torch.int32, (T, k), device),
-                         _on_stream(stream, weights if made[0] else None, ids if made[1] else None))
-    _check(rc, "w4_route")
+    rc = (_lib or load()).w4_route(logits.data_ptr(), T, E, ld, b, o, w_at, i_at,
+                                   _handle(stream, device, made_w, made_i))
+    if rc != 0:
+        raise W4Error(rc, "w4_route")
     return weights, ids
 
 
@@ -536,28 +555,29 @@ def w4a16_experts(x: torch.Tensor, gate_up: torch.Tensor, down: torch.Tensor, id
     alternating gate, up (see interleave_gate_up); down uint8 [E, w4_repacked_bytes(K, inter, g)]; ids int32 and
     weights fp32 [T, k] as w4_route gives them (an id outside [0, E) is a dropped choice)."""
     dt = _DTYPES.get(x.dtype)
-    if dt is None or x.dim() != 2 or gate_up.dim() != 2 or ids.dim() != 2:
-        raise ValueError("x must be fp16 or bf16 [T, K], gate_up [E, bytes] and ids [T, k]")
+    if dt is None or x.dim() != 2 or not x.is_cuda or not x.is_contiguous():
+        raise ValueError("x must be a contiguous fp16 or bf16 CUDA tensor [T, K]")
+    if gate_up.dim() != 2 or ids.dim() != 2:
+        raise ValueError("gate_up must be [E, bytes] and ids [T, k]")
     T, K = x.shape
     E, k = gate_up.shape[0], ids.shape[1]
     device = x.device
-    need = w4a16_experts_workspace_bytes(T, K, inter, E, k, g)
-    if need == 0:
-        raise W4Error(1 if min(K, inter, E, k, g) < 1 or k > E or g % 8 else 2, "w4a16_experts")
-    x_at = _dev(x, "x")
+    lib = _lib or load()
+    gu_bytes, dn_bytes = _repacked(2 * inter, K, g), _repacked(K, inter, g)
+    if not gu_bytes or not dn_bytes:
+        raise W4Error(1, "w4a16_experts")
+    if K % 8 or inter % 8:
+        raise W4Error(2, "w4a16_experts")
     made = None
     if y is None:
-        y = made = torch.empty((T, K), dtype=x.dtype, device=device)
-    ws = _scratch(workspace, need, device, stream)
-    a = ExpertsArgs(x_at,
-                    _like(gate_up, "gate_up", torch.uint8, (E, w4_repacked_bytes(2 * inter, K, g)), device),
-                    _like(down, "down", torch.uint8, (E, w4_repacked_bytes(K, inter, g)), device),
+        y = made = torch.empty_like(x)
+    a = ExpertsArgs(x.data_ptr(), _like(gate_up, "gate_up", torch.uint8, (E, gu_bytes), device),
+                    _like(down, "down", torch.uint8, (E, dn_bytes), device),
                     _like(ids, "ids", torch.int32, (T, k), device),
                     _like(weights, "weights", torch.float32, (T, k), device),
-                    _like(y, "y", x.dtype, (T, K), device), T, K, inter, E, k, g, dt)
-    rc = load().w4a16_experts(ctypes.byref(a), _dev(ws, "workspace"), ws.numel() * ws.element_size(),
-                              _on_stream(stream, made))
-    _check(rc, "w4a16_experts")
+                    y.data_ptr() if made is not None else _like(y, "y", x.dtype, (T, K), device), T, K, inter, E, k, g, dt)
+    _run_with(lib.w4a16_experts, a, workspace, lambda: w4a16_experts_workspace_bytes(T, K, inter, E, k, g), device, stream,
+              made, "w4a16_experts")
     return y
 
 
@@ -574,31 +594,28 @@ def w4_lora_add(base: torch.Tensor | None, x: torch.Tensor, A: torch.Tensor, B: 
     x [T, K], base [T, N] (or None for zeros) and y fp16 or bf16, rows contiguous, A [R, rank, K], B [R, N, rank] of
     the same type, adapter int32 [T], scaling fp32 [R] (None: 1), ranks int32 [R] (None: rank): an adapter's own
     rank, past which A and B are not used. ``y`` may be ``base`` (in place)."""
-    dt = _DTYPES.get(x.dtype)
-    if dt is None or x.dim() != 2 or A.dim() != 3 or B.dim() != 3:
-        raise ValueError("x must be fp16 or bf16 [T, K], A [R, rank, K] and B [R, N, rank]")
+    dtype = x.dtype
+    dt = _DTYPES.get(dtype)
+    if dt is None or x.dim() != 2 or not x.is_cuda or A.dim() != 3 or B.dim() != 3:
+        raise ValueError("x must be a fp16 or bf16 CUDA tensor [T, K], A [R, rank, K] and B [R, N, rank]")
     T, K = x.shape
     R, rank, _ = A.shape
     N = B.shape[1]
     device = x.device
-    x_at = _rows(x, "x")
+    shape = (T, N)
     made = None
     if y is None:
-        y = made = torch.empty((T, N), dtype=x.dtype, device=device)
-    for t, name in ((y, "y"), (base, "base")):
-        if t is not None and (t.dtype != x.dtype or tuple(t.shape) != (T, N) or t.device != device):
-            raise ValueError(f"{name} must be {x.dtype} [{T}, {N}] on {device}")
-    need = w4_lora_workspace_bytes(T, K, N, R, rank)
-    if need == 0:
-        raise W4Error(1 if min(K, N, R, rank) < 1 else 2, "w4_lora_add")
-    ws = _scratch(workspace, need, device, stream)
-    a = LoraArgs(x_at, _like(A, "A", x.dtype, (R, rank, K), device), _like(B, "B", x.dtype, (R, N, rank), device),
+        y = made = torch.empty(shape, dtype=dtype, device=device)
+    elif y.dtype != dtype or y.shape != shape or y.device != device:
+        raise ValueError(f"y must be {dtype} [{T}, {N}] on {device}")
+    if base is not None and (base.dtype != dtype or base.shape != shape or base.device != device):
+        raise ValueError(f"base must be {dtype} [{T}, {N}] on {device}")
+    a = LoraArgs(x.data_ptr(), _like(A, "A", dtype, (R, rank, K), device), _like(B, "B", dtype, (R, N, rank), device),
                  _like(adapter, "adapter", torch.int32, (T,), device),
                  None if scaling is None else _like(scaling, "scaling", torch.float32, (R,), device),
                  None if ranks is None else _like(ranks, "ranks", torch.int32, (R,), device),
-                 None if base is None else _rows(base, "base"), _rows(y, "y"), T, K, N, _ld(x),
-                 0 if base is None else _ld(base), _ld(y), R, rank, dt, 0)
-    rc = load().w4_lora_add(ctypes.byref(a), _dev(ws, "workspace"), ws.numel() * ws.element_size(),
-                            _on_stream(stream, made))
-    _check(rc, "w4_lora_add")
+                 None if base is None else base.data_ptr(), y.data_ptr(), T, K, N, _rows(x, "x"),
+                 0 if base is None else _rows(base, "base"), _rows(y, "y"), R, rank, dt, 0)
+    _run_with((_lib or load()).w4_lora_add, a, workspace, lambda: w4_lora_workspace_bytes(T, K, N, R, rank), device, stream,
+              made, "w4_lora_add")
     return y

@@ -56,9 +56,7 @@ struct TCfg {
   static constexpr int kSmemBytes = kStages * kStageBytes + 1024;
   static constexpr int kASlotCols = CB * 32;   // 128 rows x 64 16-bit values: 32 columns a block
   static constexpr int kACol0 = 2 * SUB * BN;  // accumulators first
-  static constexpr int kLag = 2;               // chunks a producer keeps in flight before it waits for one
   static_assert(kACol0 + 4 * kASlotCols <= 512, "tensor memory");
-  static_assert(kStages > kLag + 1, "a producer signals a chunk kLag chunks late");
 };
 
 __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
@@ -87,11 +85,7 @@ __device__ __forceinline__ void regs_up() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R));
 }
 
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 // The units of a CTA in order, the next one's tile read ahead.
 struct UnitWalk {
@@ -207,17 +201,10 @@ __global__ void __launch_bounds__(768, 1) experts_tmem_kernel(const __grid_const
             if (row[i])
               cp_async16_zfill(stage + b * C::kXSub + i * 2048 + spot, bytes ? row[i] + k : p.in, bytes);
         }
-        cp_async_commit();
-        if (c >= static_cast<uint32_t>(C::kLag)) {
-          cp_async_wait<C::kLag>();
-          fence_proxy_async_shared();  // the copies' bytes before the MMAs' reads of them
-          mbar_arrive(smem_u32(&full_bar[(c - C::kLag) % S]));
-        }
+        cp_async_mbar_arrive(smem_u32(&full_bar[s]));  // when this thread's copies have landed
       }
     }
-    cp_async_wait<0>();
-    fence_proxy_async_shared();
-    for (uint32_t i = c >= static_cast<uint32_t>(C::kLag) ? c - C::kLag : 0u; i < c; ++i) mbar_arrive(smem_u32(&full_bar[i % S]));
+    cp_async_wait_all();
     if (!ok && tid == 0)  // no copy in flight when the CTA leaves
       for (uint32_t i = c >= static_cast<uint32_t>(S) ? c - S : 0u; i < c; ++i) drain_wait(smem_u32(&full_bar[i % S]), (i / S) & 1);
   } else if (warp < 8) {
@@ -236,10 +223,12 @@ __global__ void __launch_bounds__(768, 1) experts_tmem_kernel(const __grid_const
           const int s = c % S;
           const uint32_t n = c / 2;  // this warp's chunks so far
           if (n > 0) ok = warp_wait(smem_u32(&empty_bar[e]), (n - 1) & 1, abort_flag, p.err, kLimit);
+          if (ok) ok = warp_wait(smem_u32(&full_bar[s]), (c / S) & 1, abort_flag, p.err, kLimit);
           if (ok) ok = warp_wait(smem_u32(&ready_bar[e][n & 1]), (n / 2) & 1, abort_flag, p.err, kLimit);
           if (!ok) break;
           tc_fence_after();
           if (lane == 0) {
+            fence_proxy_async_shared();  // the rows were copied by ordinary writes; the MMAs read them as async ones
             const int nb = min(CB, p.KB - q * CB);
             const uint32_t xs = smem_base + s * C::kStageBytes;
             const uint32_t a = tmem + C::kACol0 + (2 * e + (n & 1)) * C::kASlotCols;

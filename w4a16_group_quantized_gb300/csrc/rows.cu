@@ -2,9 +2,10 @@
 // share weights stand together: counts per key, their running sum, each row's place, and the list of tiles of one
 // key that the kernels after it walk.
 //
-// One block: the keys are a few kilobytes (a decode batch) to a few hundred, so the launch itself and the latency of
-// its passes over them bound it. The rows of one key come in no fixed order: a place decides where a row's sums are
-// held, never what is added to what, so no result depends on it.
+// The keys are a few kilobytes (a decode batch) to a few hundred, so latency bounds it: one block up to 4096 rows, above
+// that a cluster of eight, each of which counts and places its part of the rows and reads the others' counts in their
+// shared memory (32,768 rows of 64 keys: 60 us in one block). The rows of one key come in no fixed order within
+// their part: a place decides where a row's sums are held, never what is added to what, so no result depends on it.
 #include "gemm_common.cuh"
 #include "internal.h"
 #include "ptx.cuh"
@@ -14,98 +15,144 @@ namespace {
 
 constexpr int kThreads = 1024;
 constexpr int kBuckets = kRowsMaxKeys + 1;  // the last: no key
+constexpr int kPlanCluster = 8;
 
-// Adds the warp's rows to their buckets' counters, one addition per bucket and warp, and returns each row's old
-// count (its rank among the bucket's rows so far). Every lane of the warp calls it; bucket < 0 takes no part.
+// Adds the warp's rows to their buckets' counters and returns each row's old count (its rank among the bucket's rows so
+// far): one addition for a warp whose rows are all of one key (the rows of a long request), else one a row. Every lane
+// of the warp calls it; bucket < 0 takes no part.
 __device__ __forceinline__ int count_in(int32_t *counter, int bucket) {
-  const int lane = threadIdx.x & 31;
-  const uint32_t same = __match_any_sync(0xffffffffu, bucket);
-  const int leader = __ffs(same) - 1;
-  int at = 0;
-  if (lane == leader && bucket >= 0) at = atomicAdd(&counter[bucket], __popc(same));
-  return __shfl_sync(0xffffffffu, at, leader) + __popc(same & ((1u << lane) - 1u));
+  int same;
+  __match_all_sync(0xffffffffu, bucket, &same);
+  if (same) {
+    const int lane = threadIdx.x & 31;
+    int at = 0;
+    if (lane == 0 && bucket >= 0) at = atomicAdd(&counter[bucket], 32);
+    return __shfl_sync(0xffffffffu, at, 0) + lane;
+  }
+  return bucket >= 0 ? atomicAdd(&counter[bucket], 1) : 0;
 }
 
-// Running sum over the block of one value per thread: the sum of the values of the threads before this one.
-__device__ __forceinline__ int sum_before(int v, int32_t *warp_sums, int *total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int s = v;
+__device__ __forceinline__ int warp_sum_to(int v) {
+  const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
-    const int o = __shfl_up_sync(0xffffffffu, s, d);
-    if (lane >= d) s += o;
+    const int o = __shfl_up_sync(0xffffffffu, v, d);
+    if (lane >= d) v += o;
   }
-  __syncthreads();  // the last use of warp_sums is over
-  if (lane == 31) warp_sums[warp] = s;
-  __syncthreads();
-  int before = 0, all = 0;
-  for (int w = 0; w < kThreads / 32; ++w) {
-    const int x = warp_sums[w];
-    before += w < warp ? x : 0;
-    all += x;
-  }
-  *total = all;
-  return before + s - v;
+  return v;
 }
 
+// Running sums over the block of two values per thread: the sums of the threads before this one, and of all.
+__device__ __forceinline__ int2 sums_before(int2 v, int2 *warp_sums, int2 *total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int2 s = make_int2(warp_sum_to(v.x), warp_sum_to(v.y));
+  if (lane == 31) warp_sums[warp] = s;
+  __syncthreads();
+  if (warp == 0) {
+    const int2 w = warp_sums[lane];
+    warp_sums[lane] = make_int2(warp_sum_to(w.x), warp_sum_to(w.y));
+  }
+  __syncthreads();
+  const int2 before = warp > 0 ? warp_sums[warp - 1] : make_int2(0, 0);
+  *total = warp_sums[kThreads / 32 - 1];
+  return make_int2(before.x + s.x - v.x, before.y + s.y - v.y);
+}
+
+__device__ __forceinline__ int32_t ld_cluster_s32(uint32_t addr) {
+  int32_t v;
+  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+template <int C>
 __global__ void __launch_bounds__(kThreads)
     row_plan_kernel(const int32_t *__restrict__ keys, int64_t count, int nkeys, int tile, int keyless, RowPlan plan) {
-  __shared__ int32_t counts[kBuckets], begin[kBuckets], tile_begin[kBuckets], warp_sums[kThreads / 32];
+  // counts: of this block's rows; all: of every block's; begin: the next free place of a bucket for this block
+  __shared__ int32_t counts[kBuckets], all[kBuckets], begin[kBuckets], tile_begin[kBuckets];
+  __shared__ int2 warp_sums[kThreads / 32];
   const int tid = threadIdx.x;
+  const int rank = C > 1 ? static_cast<int>(cluster_ctarank()) : 0;
   griddep_launch_dependents();
-  for (int b = tid; b < kBuckets; b += kThreads) counts[b] = 0;
+  for (int b = tid; b <= nkeys; b += kThreads) counts[b] = 0;
   griddep_wait();
   __syncthreads();
-  for (int64_t i0 = 0; i0 < count; i0 += kThreads) {
+  const int64_t part = (count + C * kThreads - 1) / (C * kThreads) * kThreads;
+  const int64_t i_end = min(count, (rank + 1) * part);
+  for (int64_t i0 = rank * part; i0 < i_end; i0 += kThreads) {
     const int64_t i = i0 + tid;
     int bucket = -1;
-    if (i < count) {
+    if (i < i_end) {
       const int32_t key = keys[i];
       bucket = key >= 0 && key < nkeys ? key : nkeys;
     }
     count_in(counts, bucket);
   }
+  if (C > 1) cluster_sync_all(); else __syncthreads();
+  // per bucket: rows in the blocks before this one, and in all
+  for (int b = tid; b <= nkeys; b += kThreads) {
+    int before = 0, sum = 0;
+    if (C == 1) {
+      sum = counts[b];
+    } else {
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        const int n = ld_cluster_s32(mapa_shared(smem_u32(&counts[b]), c));
+        before += c < rank ? n : 0;
+        sum += n;
+      }
+    }
+    all[b] = sum;
+    begin[b] = before;
+  }
   __syncthreads();
-  int rows = 0, tiles = 0, all;
-  const bool own = tid <= nkeys && tid < kThreads;  // bucket nkeys = 1024 comes after every thread's
-  if (own) {
-    rows = counts[tid];
-    tiles = tid < nkeys || keyless ? (rows + tile - 1) / tile : 0;
+  // bucket nkeys = 1024 comes after every thread's
+  const int rows = tid <= nkeys ? all[tid] : 0;
+  const int tiles = tid < nkeys || (tid == nkeys && keyless) ? (rows + tile - 1) / tile : 0;
+  int2 total;
+  const int2 at = sums_before(make_int2(rows, tiles), warp_sums, &total);
+  if (tid <= nkeys) {
+    begin[tid] += at.x;
+    tile_begin[tid] = at.y;
   }
-  const int b0 = sum_before(rows, warp_sums, &all);
-  if (own) begin[tid] = b0;
-  if (nkeys == kThreads && tid == 0) begin[nkeys] = all;
-  const int t0 = sum_before(tiles, warp_sums, &all);
-  if (own) tile_begin[tid] = t0;
-  if (nkeys == kThreads && keyless) {
-    if (tid == 0) tile_begin[nkeys] = all;
-    all += (counts[nkeys] + tile - 1) / tile;
+  int ntiles = total.y;
+  if (nkeys == kThreads) {
+    if (tid == 0) {
+      begin[nkeys] += total.x;
+      tile_begin[nkeys] = total.y;
+    }
+    if (keyless) ntiles += (all[nkeys] + tile - 1) / tile;
   }
-  if (tid == 0) *plan.ntiles = all;
-  if (tid == 0 && plan.err) *plan.err = 0u;
+  if (rank == 0 && tid == 0) {
+    *plan.ntiles = ntiles;
+    if (plan.err) *plan.err = 0u;
+  }
   __syncthreads();
   const int buckets = nkeys + (keyless ? 1 : 0);
-  for (int i = tid; i < all; i += kThreads) {
+  for (int i = rank * kThreads + tid; i < ntiles; i += C * kThreads) {
     int lo = 0, hi = buckets;  // the last bucket with tile_begin <= i
     while (hi - lo > 1) {
       const int mid = (lo + hi) / 2;
       if (tile_begin[mid] <= i) lo = mid; else hi = mid;
     }
-    const int first = (i - tile_begin[lo]) * tile;
-    plan.tiles[i] = RowTile{lo, begin[lo] + first, min(tile, counts[lo] - first), 0};
+    // the bucket's first place: this block's next one less the rows of the blocks before it
+    int first = begin[lo];
+    if (C > 1)
+      for (int c = 0; c < rank; ++c) first -= ld_cluster_s32(mapa_shared(smem_u32(&counts[lo]), c));
+    const int in = (i - tile_begin[lo]) * tile;
+    plan.tiles[i] = RowTile{lo, first + in, min(tile, all[lo] - in), 0};
   }
-  __syncthreads();
-  for (int64_t i0 = 0; i0 < count; i0 += kThreads) {
+  if (C > 1) cluster_sync_all_relaxed(); else __syncthreads();  // counts of every block have been read
+  for (int64_t i0 = rank * part; i0 < i_end; i0 += kThreads) {
     const int64_t i = i0 + tid;
     int bucket = -1;
-    if (i < count) {
+    if (i < i_end) {
       const int32_t key = keys[i];
       bucket = key >= 0 && key < nkeys ? key : nkeys;
     }
-    const int at = count_in(begin, bucket);
-    if (i < count) {
-      plan.perm[at] = static_cast<int32_t>(i);
-      if (plan.inverse) plan.inverse[i] = bucket < nkeys ? at : -1;
+    const int place = count_in(begin, bucket);
+    if (i < i_end) {
+      plan.perm[place] = static_cast<int32_t>(i);
+      if (plan.inverse) plan.inverse[i] = bucket < nkeys ? place : -1;
     }
   }
 }
@@ -114,8 +161,23 @@ __global__ void __launch_bounds__(kThreads)
 
 cudaError_t launch_row_plan(const int32_t *keys, int64_t count, int nkeys, int tile, bool keyless, const RowPlan &plan,
                             cudaStream_t stream) {
-  return detail::launch_programmatic(row_plan_kernel, 1, kThreads, 0, stream, keys, count, nkeys, tile,
-                                     static_cast<int>(keyless), plan);
+  if (count <= 4096)
+    return detail::launch_programmatic(row_plan_kernel<1>, 1, kThreads, 0, stream, keys, count, nkeys, tile,
+                                       static_cast<int>(keyless), plan);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(kPlanCluster);
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim = {kPlanCluster, 1, 1};
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, row_plan_kernel<kPlanCluster>, keys, count, nkeys, tile,
+                                           static_cast<int>(keyless), plan);
+  return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 }  // namespace w4
