@@ -7,14 +7,14 @@
 // (128 x 128 values per 128 k, a packed 32-bit multiply-add for two of them).
 //
 // A unit is one 128-row weight tile x one tile of up to BN rows of one expert; the CTAs take units in turn and walk K in
-// chunks of CB blocks of 64, with no stop between units. Roles (24 warps, one CTA a SM):
-//   4 producer warps   gather the rows of x (16-byte asynchronous copies, 128-byte swizzle); one lane copies the
-//                      chunk's codes and group records in bulk
+// chunks of CB blocks of 64, with no stop between units. Roles (24 or 32 warps, one CTA a SM):
+//   4 row warps        gather the rows of x (16-byte asynchronous copies, 128-byte swizzle)
+//   2 weight warps     copy the chunks' codes, and their group records, in bulk
 //   2 MMA warps        take the chunks in turn, each into an accumulator of its own that the chunk starts from zero
 //   8 dequant warps    two warpgroups take the chunks in turn: thread r stores row r's q - z in tensor memory and its
 //                      scale in a ring in shared memory
-//   8 sum warps        two warpgroups, each one half of the rows of `in`: add scale * (chunk's sums) to their 32-bit
-//                      registers, and write h or the output at a unit's end
+//   8 or 16 sum warps  a warpgroup for each 32 rows of `in`: add scale * (chunk's sums) to their 32-bit registers, and
+//                      write h or the output at a unit's end
 // SUB = 2: a chunk of one block whose halves of 32 k lie in different groups, each with an accumulator of its own.
 //
 // Barriers, each waited for in every phase and in order (chunk c; S stages):
@@ -38,14 +38,15 @@ namespace {
 
 using namespace detail;
 
-constexpr int kRegsLaunch = 80;  // 65,536 / 768 threads, a multiple of 8
-constexpr int kRegsLow = 56;     // producers, MMA warps
-constexpr int kRegsDequant = 72;
-constexpr int kRegsSum = 112;
-static_assert(2 * kRegsLow + 2 * kRegsDequant + 2 * kRegsSum <= 6 * kRegsLaunch, "registers the block was launched with");
-
 template <int BN, int CB, int SUB>
 struct TCfg {
+  static constexpr int kSumGroups = BN / 32;                     // warpgroups that add, 32 rows of `in` each
+  static constexpr int kThreads = 4 * 128 + kSumGroups * 128;    // 768 (BN = 64) or 1024
+  // BN = 128: 64 registers a thread at launch, dealt out anew by warpgroup
+  static constexpr bool kDeal = BN == 128;
+  static constexpr int kRegsRows = 48, kRegsIssue = 40, kRegsDequant = 64, kRegsSum = 72;
+  static_assert(!kDeal || kRegsRows + kRegsIssue + 2 * kRegsDequant + kSumGroups * kRegsSum <= 64 * kThreads / 128,
+                "the registers that the block was launched with");
   static constexpr int kXSub = BN * 128;  // one block of 64 k of BN rows
   static constexpr int kXBytes = CB * kXSub;
   static constexpr int kCodeBytes = CB * kTileBytes;
@@ -76,13 +77,13 @@ __device__ __forceinline__ void unpack2(uint64_t v, float *lo, float *hi) {
   *hi = __uint_as_float(b);
 }
 
-template <int R>
+template <bool ON, int R>
 __device__ __forceinline__ void regs_down() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
+  if constexpr (ON) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
 }
-template <int R>
+template <bool ON, int R>
 __device__ __forceinline__ void regs_up() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R));
+  if constexpr (ON) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R));
 }
 
 __device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
@@ -107,7 +108,8 @@ struct UnitWalk {
 };
 
 template <int DT, int BN, int CB, int SUB, bool GATED>
-__global__ void __launch_bounds__(768, 1) experts_tmem_kernel(const __grid_constant__ Products p) {
+__global__ void __launch_bounds__(TCfg<BN, CB, SUB>::kThreads, 1)
+    experts_tmem_kernel(const __grid_constant__ Products p) {
   using C = TCfg<BN, CB, SUB>;
   constexpr int S = C::kStages;
   extern __shared__ uint8_t smem_raw[];
@@ -116,11 +118,11 @@ __global__ void __launch_bounds__(768, 1) experts_tmem_kernel(const __grid_const
   __shared__ uint32_t tmem_sh, abort_sh;
 
   const uint32_t smem_base = (smem_u32(smem_raw) + 1023u) & ~1023u;
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
   volatile uint32_t *abort_flag = &abort_sh;
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
-      mbar_init(smem_u32(&full_bar[s]), 128 + 1);  // the producers' threads and the bulk copies' bytes
+      mbar_init(smem_u32(&full_bar[s]), 128 + 2);  // the row warps' threads and the weight warps
       mbar_init(smem_u32(&done_bar[s]), 1);
     }
     for (int e = 0; e < 2; ++e) {
@@ -128,7 +130,7 @@ __global__ void __launch_bounds__(768, 1) experts_tmem_kernel(const __grid_const
         mbar_init(smem_u32(&ready_bar[e][a]), 4);
         mbar_init(smem_u32(&free_bar[e][a]), 1);
       }
-      mbar_init(smem_u32(&empty_bar[e]), 8);
+      mbar_init(smem_u32(&empty_bar[e]), 4 * C::kSumGroups);
       mbar_init(smem_u32(&drain_bar[e]), 1);
     }
     abort_sh = 0;
@@ -142,7 +144,7 @@ __global__ void __launch_bounds__(768, 1) experts_tmem_kernel(const __grid_const
   __syncwarp();
   cta_sync_all();
   tc_fence_after();
-  const uint32_t tmem = tmem_sh;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_sh, 0);
   if (threadIdx.x == 0) griddep_launch_dependents();
   griddep_wait();  // the plan and `in` come from the grids before this one
   const int64_t units = static_cast<int64_t>(*p.plan.ntiles) * p.slabs;
@@ -150,8 +152,8 @@ __global__ void __launch_bounds__(768, 1) experts_tmem_kernel(const __grid_const
   constexpr uint64_t kLimit = kWaitLimitCycles;
 
   if (warp < 4) {
-    // ------------------------------------------------------------ producers
-    regs_down<kRegsLow>();
+    // ----------------------------------------------------------------- rows
+    regs_down<C::kDeal, C::kRegsRows>();
     const int tid = threadIdx.x;
     constexpr int kRows = BN / 16;  // rows of a thread: tid / 8, + 16, ...; its 16 bytes of each 128: tid % 8
     const int sub = tid / 8, part = tid % 8;
@@ -171,10 +173,6 @@ __global__ void __launch_bounds__(768, 1) experts_tmem_kernel(const __grid_const
           row[i] = p.in + at * p.K + part * 8;
         }
       }
-      const uint8_t *expert = p.codes + rt.key * p.expert_bytes;
-      const uint8_t *codes = expert + static_cast<int64_t>(wt) * p.KB * kTileBytes;
-      const uint8_t *meta = expert + p.meta + static_cast<int64_t>(wt) * p.G * kRecBytes;
-      const uint64_t policy = policy_evict_normal();  // an expert's other row tiles read the weights again
       for (int q = 0; q < chunks; ++q, ++c) {
         const int s = c % S;
         if (c >= static_cast<uint32_t>(S)) ok = warp_wait(smem_u32(&done_bar[s]), (c / S - 1) & 1, abort_flag, p.err, kLimit);
@@ -182,15 +180,6 @@ __global__ void __launch_bounds__(768, 1) experts_tmem_kernel(const __grid_const
         const uint32_t stage = smem_base + s * C::kStageBytes;
         const int k0 = q * CB * kTK;
         const int nb = min(CB, p.KB - q * CB);
-        if (tid == 0) {
-          const int j0 = p.gdiv.div(k0);
-          const int nrec = SUB == 1 ? 1 : p.gdiv.div(min(k0 + kTK, p.K) - 1) - j0 + 1;
-          const uint32_t bar = smem_u32(&full_bar[s]);
-          mbar_arrive_expect_tx(bar, nb * kTileBytes + nrec * kRecBytes);
-          bulk_g2s(stage + C::kXBytes, codes + static_cast<int64_t>(q) * CB * kTileBytes, nb * kTileBytes, bar, policy);
-          bulk_g2s(stage + C::kXBytes + C::kCodeBytes, meta + static_cast<int64_t>(j0) * kRecBytes, nrec * kRecBytes, bar,
-                   policy);
-        }
 #pragma unroll
         for (int b = 0; b < CB; ++b) {
           const int k = k0 + b * kTK;
@@ -205,10 +194,8 @@ __global__ void __launch_bounds__(768, 1) experts_tmem_kernel(const __grid_const
       }
     }
     cp_async_wait_all();
-    if (!ok && tid == 0)  // no copy in flight when the CTA leaves
-      for (uint32_t i = c >= static_cast<uint32_t>(S) ? c - S : 0u; i < c; ++i) drain_wait(smem_u32(&full_bar[i % S]), (i / S) & 1);
   } else if (warp < 8) {
-    regs_down<kRegsLow>();
+    regs_down<C::kDeal, C::kRegsIssue>();
     if (warp < 6) {
       // ---------------------------------------------------------- MMA issue
       const int e = warp - 4;
@@ -227,7 +214,7 @@ __global__ void __launch_bounds__(768, 1) experts_tmem_kernel(const __grid_const
           if (ok) ok = warp_wait(smem_u32(&ready_bar[e][n & 1]), (n / 2) & 1, abort_flag, p.err, kLimit);
           if (!ok) break;
           tc_fence_after();
-          if (lane == 0) {
+          if (elect_one()) {
             fence_proxy_async_shared();  // the rows were copied by ordinary writes; the MMAs read them as async ones
             const int nb = min(CB, p.KB - q * CB);
             const uint32_t xs = smem_base + s * C::kStageBytes;
@@ -254,10 +241,45 @@ __global__ void __launch_bounds__(768, 1) experts_tmem_kernel(const __grid_const
         mma_commit(smem_u32(&drain_bar[e]));
         drain_wait(smem_u32(&drain_bar[e]), 0);
       }
+    } else {
+      // ------------------------------------------------- codes and records
+      const bool records = warp == 7;
+      const uint64_t policy = policy_evict_normal();  // an expert's other row tiles read the weights again
+      uint32_t c = 0;
+      bool ok = true;
+      RowTile rt;
+      int wt;
+      for (UnitWalk w(p, units); ok && w.take(&rt, &wt);) {
+        const uint8_t *expert = p.codes + rt.key * p.expert_bytes;
+        const uint8_t *codes = expert + static_cast<int64_t>(wt) * p.KB * kTileBytes;
+        const uint8_t *meta = expert + p.meta + static_cast<int64_t>(wt) * p.G * kRecBytes;
+        for (int q = 0; q < chunks; ++q, ++c) {
+          const int s = c % S;
+          if (c >= static_cast<uint32_t>(S)) ok = warp_wait(smem_u32(&done_bar[s]), (c / S - 1) & 1, abort_flag, p.err, kLimit);
+          if (!ok) break;
+          if (lane == 0) {
+            const uint32_t to = smem_base + s * C::kStageBytes + C::kXBytes;
+            const uint32_t bar = smem_u32(&full_bar[s]);
+            if (records) {
+              const int k0 = q * CB * kTK;
+              const int j0 = p.gdiv.div(k0);
+              const int nrec = SUB == 1 ? 1 : p.gdiv.div(min(k0 + kTK, p.K) - 1) - j0 + 1;
+              mbar_arrive_expect_tx(bar, nrec * kRecBytes);
+              bulk_g2s(to + C::kCodeBytes, meta + static_cast<int64_t>(j0) * kRecBytes, nrec * kRecBytes, bar, policy);
+            } else {
+              const int nb = min(CB, p.KB - q * CB);
+              mbar_arrive_expect_tx(bar, nb * kTileBytes);
+              bulk_g2s(to, codes + static_cast<int64_t>(q) * CB * kTileBytes, nb * kTileBytes, bar, policy);
+            }
+          }
+          __syncwarp();
+        }
+      }
+      if (lane == 0 && !ok)  // no copy in flight when the CTA leaves
+        for (uint32_t i = c >= static_cast<uint32_t>(S) ? c - S : 0u; i < c; ++i) drain_wait(smem_u32(&full_bar[i % S]), (i / S) & 1);
     }
   } else if (warp < 16) {
     // ------------------------------------------------------------ dequant
-    regs_down<kRegsDequant>();
     const int e = (warp - 8) / 4;
     const int lq = warp % 4;
     const int r = lq * 32 + lane;
@@ -313,10 +335,9 @@ __global__ void __launch_bounds__(768, 1) experts_tmem_kernel(const __grid_const
     }
   } else {
     // ------------------------------------------------------------ sums
-    regs_up<kRegsSum>();
-    constexpr int kCols = BN / 2;  // of a warpgroup
-    static_assert(kCols % 32 == 0, "two loads of 16 columns at a time");
-    const int half = (warp - 16) / 4;
+    regs_up<C::kDeal, C::kRegsSum>();
+    constexpr int kCols = 32;  // of a warpgroup
+    const int part = (warp - 16) / 4;
     const int lq = warp % 4;
     const int r = lq * 32 + lane;
     const uint32_t lane_addr = static_cast<uint32_t>(lq * 32) << 16;
@@ -325,7 +346,7 @@ __global__ void __launch_bounds__(768, 1) experts_tmem_kernel(const __grid_const
     RowTile rt;
     int wt;
     for (UnitWalk w(p, units); ok && w.take(&rt, &wt);) {
-      const int cols = min(max(rt.rows - half * kCols, 0), kCols);  // this warpgroup's columns with a row
+      const int cols = min(max(rt.rows - part * kCols, 0), kCols);  // this warpgroup's columns with a row
       uint64_t acc[kCols / 2];
 #pragma unroll
       for (int i = 0; i < kCols / 2; ++i) acc[i] = 0ull;
@@ -339,27 +360,31 @@ __global__ void __launch_bounds__(768, 1) experts_tmem_kernel(const __grid_const
           if (h == 1 && q * kTK + 32 >= p.K) break;  // its products were not of this unit's K
           const uint32_t sb = __float_as_uint(scales[c % C::kScaleSlots][h][r]);
           const uint64_t s2 = pack2(sb, sb);
-          const uint32_t d = tmem + lane_addr + ((c & 1) * SUB + h) * BN + half * kCols;
-#pragma unroll
-          for (int j = 0; j < kCols; j += 32) {
-            if (j >= cols) break;
+          const uint32_t d = tmem + lane_addr + ((c & 1) * SUB + h) * BN + part * kCols;
+          if (cols > 0) {
             uint32_t v0[16], v1[16];
-            tmem_ld_32x32b_x16(d + j, v0);
-            tmem_ld_32x32b_x16(d + j + 16, v1);
+            tmem_ld_32x32b_x16(d, v0);
+            tmem_ld_32x32b_x16(d + 16, v1);
             tmem_wait_ld();
+            if (h == SUB - 1 || q * kTK + 32 >= p.K) {  // the last read of the chunk's sums
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(smem_u32(&empty_bar[c & 1]));
+            }
 #pragma unroll
-            for (int i = 0; i < 8; ++i) acc[j / 2 + i] = fma2(s2, pack2(v0[2 * i], v0[2 * i + 1]), acc[j / 2 + i]);
+            for (int i = 0; i < 8; ++i) acc[i] = fma2(s2, pack2(v0[2 * i], v0[2 * i + 1]), acc[i]);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) acc[j / 2 + 8 + i] = fma2(s2, pack2(v1[2 * i], v1[2 * i + 1]), acc[j / 2 + 8 + i]);
+            for (int i = 0; i < 8; ++i) acc[8 + i] = fma2(s2, pack2(v1[2 * i], v1[2 * i + 1]), acc[8 + i]);
           }
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&empty_bar[c & 1]));
+        if (cols == 0) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&empty_bar[c & 1]));
+        }
       }
       if (!ok) break;
       const int n = wt * kTN + r;
-      const int64_t pos0 = rt.row0 + half * kCols;
+      const int64_t pos0 = rt.row0 + part * kCols;
       if (GATED) {
         // rows n & ~1 (even lane: gate) and n | 1 (odd lane: up): the pair swaps values, the even lane makes the
         // first half of the columns, the odd lane the second
@@ -417,7 +442,7 @@ cudaError_t launch_one(const Products &p, int num_sms, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     set.fetch_or(bit);
   }
-  return launch_programmatic(kern, num_sms, 768, bytes, stream, p);
+  return launch_programmatic(kern, num_sms, TCfg<BN, CB, SUB>::kThreads, bytes, stream, p);
 }
 
 template <int DT, bool GATED>
