@@ -270,8 +270,9 @@ cudaError_t launch_dt(const ExpertsArgs &a, uint8_t *ws, const ExpertsPlan &plan
   rows.err = reinterpret_cast<uint32_t *>(ws);
   cudaError_t e = launch_row_plan(a.ids, a.T * a.k, a.experts, plan.tile, false, rows, stream);
   if (e != cudaSuccess) return e;
-  auto products = [&](const void *in, const void *packed, int64_t N, int64_t K, void *out) {
+  auto products = [&](const void *in, int64_t in_rows, const void *packed, int64_t N, int64_t K, void *out) {
     Products p;
+    p.in_rows = in_rows;
     p.in = static_cast<const uint16_t *>(in);
     p.codes = static_cast<const uint8_t *>(packed);
     p.K = static_cast<int>(K);
@@ -289,9 +290,9 @@ cudaError_t launch_dt(const ExpertsArgs &a, uint8_t *ws, const ExpertsPlan &plan
     p.gdiv = make_fastdiv(static_cast<uint32_t>(a.g));
     return p;
   };
-  e = launch_products<DT, true>(products(a.x, a.gate_up, 2 * a.I, a.K, ws + plan.h), plan, num_sms, stream);
+  e = launch_products<DT, true>(products(a.x, a.T, a.gate_up, 2 * a.I, a.K, ws + plan.h), plan, num_sms, stream);
   if (e != cudaSuccess) return e;
-  e = launch_products<DT, false>(products(ws + plan.h, a.down, a.K, a.I, ws + plan.part), plan, num_sms, stream);
+  e = launch_products<DT, false>(products(ws + plan.h, a.T * a.k, a.down, a.K, a.I, ws + plan.part), plan, num_sms, stream);
   if (e != cudaSuccess) return e;
   return launch_programmatic(combine_kernel<DT>, static_cast<int>(cdiv(a.T * (a.K / 8), 256)), 256, 0, stream,
                              reinterpret_cast<const float *>(ws + plan.part), static_cast<const int32_t *>(rows.inverse), a.weights,

@@ -15,6 +15,7 @@ struct Products {
   void *out;             // gate/up: h [pairs, N / 2], 16 bits; down: [pairs, N], 32 bits
   RowPlan plan;
   uint32_t *err;
+  int64_t in_rows;
   int K, N, G, KB, g;
   int slabs;             // blocks (experts.cu) or weight tiles (experts_tmem.cu) of N
   int choices;           // k: pair / k is the token

@@ -8,7 +8,8 @@
 //
 // A unit is one 128-row weight tile x one tile of up to BN rows of one expert; the CTAs take units in turn and walk K in
 // chunks of CB blocks of 64, with no stop between units. Roles (24 or 32 warps, one CTA a SM):
-//   4 row warps        gather the rows of x (16-byte asynchronous copies, 128-byte swizzle)
+//   4 row warps        copy the rows of `in` with the 128-byte swizzle, a quarter of them each: gate/up gathers the
+//                      tokens' rows four to a copy, down's rows are already in order (one copy a block)
 //   2 weight warps     copy the chunks' codes, and their group records, in bulk
 //   2 MMA warps        take the chunks in turn, each into an accumulator of its own that the chunk starts from zero
 //   8 dequant warps    two warpgroups take the chunks in turn: thread r stores row r's q - z in tensor memory and its
@@ -44,7 +45,7 @@ struct TCfg {
   static constexpr int kThreads = 4 * 128 + kSumGroups * 128;    // 768 (BN = 64) or 1024
   // BN = 128: 64 registers a thread at launch, dealt out anew by warpgroup
   static constexpr bool kDeal = BN == 128;
-  static constexpr int kRegsRows = 48, kRegsIssue = 40, kRegsDequant = 64, kRegsSum = 72;
+  static constexpr int kRegsRows = 56, kRegsIssue = 40, kRegsDequant = 64, kRegsSum = 72;
   static_assert(!kDeal || kRegsRows + kRegsIssue + 2 * kRegsDequant + kSumGroups * kRegsSum <= 64 * kThreads / 128,
                 "the registers that the block was launched with");
   static constexpr int kXSub = BN * 128;  // one block of 64 k of BN rows
@@ -86,8 +87,6 @@ __device__ __forceinline__ void regs_up() {
   if constexpr (ON) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R));
 }
 
-__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
-
 // The units of a CTA in order, the next one's tile read ahead.
 struct UnitWalk {
   const Products &p;
@@ -109,7 +108,7 @@ struct UnitWalk {
 
 template <int DT, int BN, int CB, int SUB, bool GATED>
 __global__ void __launch_bounds__(TCfg<BN, CB, SUB>::kThreads, 1)
-    experts_tmem_kernel(const __grid_constant__ Products p) {
+    experts_tmem_kernel(const __grid_constant__ CUtensorMap in_map, const __grid_constant__ Products p) {
   using C = TCfg<BN, CB, SUB>;
   constexpr int S = C::kStages;
   extern __shared__ uint8_t smem_raw[];
@@ -122,7 +121,7 @@ __global__ void __launch_bounds__(TCfg<BN, CB, SUB>::kThreads, 1)
   volatile uint32_t *abort_flag = &abort_sh;
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
-      mbar_init(smem_u32(&full_bar[s]), 128 + 2);  // the row warps' threads and the weight warps
+      mbar_init(smem_u32(&full_bar[s]), 4 + 2);  // the row warps and the weight warps
       mbar_init(smem_u32(&done_bar[s]), 1);
     }
     for (int e = 0; e < 2; ++e) {
@@ -136,6 +135,7 @@ __global__ void __launch_bounds__(TCfg<BN, CB, SUB>::kThreads, 1)
     abort_sh = 0;
     fence_mbar_init();
   }
+  if (warp == 0 && elect_one()) prefetch_tensormap(&in_map);
   if (warp == 8) {
     tmem_alloc(smem_u32(&tmem_sh), 512);
     tmem_relinquish();
@@ -154,46 +154,51 @@ __global__ void __launch_bounds__(TCfg<BN, CB, SUB>::kThreads, 1)
   if (warp < 4) {
     // ----------------------------------------------------------------- rows
     regs_down<C::kDeal, C::kRegsRows>();
-    const int tid = threadIdx.x;
-    constexpr int kRows = BN / 16;  // rows of a thread: tid / 8, + 16, ...; its 16 bytes of each 128: tid % 8
-    const int sub = tid / 8, part = tid % 8;
-    const uint32_t spot = sub * 128 + ((part ^ (sub & 7)) * 16);
+    constexpr int kRows = BN / 4;  // of a warp
     uint32_t c = 0;
     bool ok = true;
     RowTile rt;
     int wt;
     for (UnitWalk w(p, units); ok && w.take(&rt, &wt);) {
-      const uint16_t *row[kRows];
+      const int first = rt.row0 + warp * kRows;
+      const int rows = min(max(rt.rows - warp * kRows, 0), kRows);
+      // gate/up: the tokens of the warp's rows, four to a copy (a copy's rows past the tile's are any row of it)
+      int32_t tok[kRows];
+      if (GATED) {
+        const int32_t mine = rows > 0 ? p.plan.perm[first + min(lane, rows - 1)] / p.choices : 0;
 #pragma unroll
-      for (int i = 0; i < kRows; ++i) {
-        const int m = sub + 16 * i;
-        row[i] = nullptr;
-        if (m < rt.rows) {
-          const int64_t at = GATED ? p.plan.perm[rt.row0 + m] / p.choices : rt.row0 + m;
-          row[i] = p.in + at * p.K + part * 8;
-        }
+        for (int i = 0; i < kRows; ++i) tok[i] = __shfl_sync(0xffffffffu, mine, i);
       }
+      const uint32_t bytes = rows == 0 ? 0u : GATED ? (rows + 3) / 4 * 512u : kRows * 128u;
       for (int q = 0; q < chunks; ++q, ++c) {
         const int s = c % S;
         if (c >= static_cast<uint32_t>(S)) ok = warp_wait(smem_u32(&done_bar[s]), (c / S - 1) & 1, abort_flag, p.err, kLimit);
         if (!ok) break;
-        const uint32_t stage = smem_base + s * C::kStageBytes;
-        const int k0 = q * CB * kTK;
-        const int nb = min(CB, p.KB - q * CB);
+        if (elect_one()) {
+          const uint32_t to = smem_base + s * C::kStageBytes + warp * kRows * 128;
+          const uint32_t bar = smem_u32(&full_bar[s]);
+          const int nb = min(CB, p.KB - q * CB);
+          mbar_arrive_expect_tx(bar, bytes * nb);
 #pragma unroll
-        for (int b = 0; b < CB; ++b) {
-          const int k = k0 + b * kTK;
-          if (b >= nb) break;
-          const uint32_t bytes = k + part * 8 < p.K ? 16u : 0u;  // K is a multiple of 8
+          for (int b = 0; b < CB; ++b) {
+            if (b >= nb || rows == 0) break;
+            const int k = (q * CB + b) * kTK;
+            if (GATED) {
 #pragma unroll
-          for (int i = 0; i < kRows; ++i)
-            if (row[i])
-              cp_async16_zfill(stage + b * C::kXSub + i * 2048 + spot, bytes ? row[i] + k : p.in, bytes);
+              for (int i = 0; i < kRows / 4; ++i)
+                if (4 * i < rows)
+                  tma_gather4_2d(to + b * C::kXSub + i * 512, &in_map, k, tok[4 * i], tok[4 * i + 1], tok[4 * i + 2],
+                                 tok[4 * i + 3], bar);
+            } else {
+              tma_load_2d(to + b * C::kXSub, &in_map, k, first, bar);
+            }
+          }
         }
-        cp_async_mbar_arrive(smem_u32(&full_bar[s]));  // when this thread's copies have landed
+        __syncwarp();
       }
     }
-    cp_async_wait_all();
+    if (!ok && elect_one())  // no copy in flight when the CTA leaves
+      for (uint32_t i = c >= static_cast<uint32_t>(S) ? c - S : 0u; i < c; ++i) drain_wait(smem_u32(&full_bar[i % S]), (i / S) & 1);
   } else if (warp < 8) {
     regs_down<C::kDeal, C::kRegsIssue>();
     if (warp < 6) {
@@ -215,7 +220,6 @@ __global__ void __launch_bounds__(TCfg<BN, CB, SUB>::kThreads, 1)
           if (!ok) break;
           tc_fence_after();
           if (elect_one()) {
-            fence_proxy_async_shared();  // the rows were copied by ordinary writes; the MMAs read them as async ones
             const int nb = min(CB, p.KB - q * CB);
             const uint32_t xs = smem_base + s * C::kStageBytes;
             const uint32_t a = tmem + C::kACol0 + (2 * e + (n & 1)) * C::kASlotCols;
@@ -237,7 +241,8 @@ __global__ void __launch_bounds__(TCfg<BN, CB, SUB>::kThreads, 1)
           __syncwarp();
         }
       }
-      if (lane == 0 && *abort_flag) {
+      const bool aborted = __any_sync(0xffffffffu, *abort_flag != 0);
+      if (aborted && elect_one()) {
         mma_commit(smem_u32(&drain_bar[e]));
         drain_wait(smem_u32(&drain_bar[e]), 0);
       }
@@ -257,7 +262,7 @@ __global__ void __launch_bounds__(TCfg<BN, CB, SUB>::kThreads, 1)
           const int s = c % S;
           if (c >= static_cast<uint32_t>(S)) ok = warp_wait(smem_u32(&done_bar[s]), (c / S - 1) & 1, abort_flag, p.err, kLimit);
           if (!ok) break;
-          if (lane == 0) {
+          if (elect_one()) {
             const uint32_t to = smem_base + s * C::kStageBytes + C::kXBytes;
             const uint32_t bar = smem_u32(&full_bar[s]);
             if (records) {
@@ -275,7 +280,7 @@ __global__ void __launch_bounds__(TCfg<BN, CB, SUB>::kThreads, 1)
           __syncwarp();
         }
       }
-      if (lane == 0 && !ok)  // no copy in flight when the CTA leaves
+      if (!ok && elect_one())  // no copy in flight when the CTA leaves
         for (uint32_t i = c >= static_cast<uint32_t>(S) ? c - S : 0u; i < c; ++i) drain_wait(smem_u32(&full_bar[i % S]), (i / S) & 1);
     }
   } else if (warp < 16) {
@@ -442,7 +447,9 @@ cudaError_t launch_one(const Products &p, int num_sms, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     set.fetch_or(bit);
   }
-  return launch_programmatic(kern, num_sms, TCfg<BN, CB, SUB>::kThreads, bytes, stream, p);
+  CUtensorMap in_map;
+  if (!make_rows_map(&in_map, p.in, p.in_rows, p.K, GATED ? 1 : BN / 4, DT)) return cudaErrorInvalidValue;
+  return launch_programmatic(kern, num_sms, TCfg<BN, CB, SUB>::kThreads, bytes, stream, in_map, p);
 }
 
 template <int DT, bool GATED>

@@ -745,6 +745,16 @@ bool make_x_map(CUtensorMap *map, const void *x, int64_t M, int64_t K, int bn, i
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+}  // namespace
+
+// Rows of 16-bit values [nrows][cols] (cols a multiple of 8), 128-byte swizzle, zero fill outside: one box is 64 columns
+// of box_rows rows.
+bool detail::make_rows_map(CUtensorMap *map, const void *rows, int64_t nrows, int64_t cols, int box_rows, int dtype) {
+  return make_x_map(map, rows, nrows, cols, box_rows, 1, false, dtype);
+}
+
+namespace {
+
 // The packed weights as two 3-D tensors of 32-bit words for the two-tile units (no swizzle, zero fill
 // outside): the tile region [NT][KB * 16][64] (a 4 KB code block is 16 rows of 256 bytes), one box
 // {64, 16 sbk, 2} = sbk blocks of two consecutive tiles; the record region [NT][G][80], one box

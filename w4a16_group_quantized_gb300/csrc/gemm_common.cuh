@@ -437,6 +437,9 @@ __device__ __forceinline__ void produce_stages(const CUtensorMap *x_map, const P
   }
 }
 
+// A tensor map of rows of 16-bit values in boxes of 64 columns x box_rows rows (gemm.cu).
+bool make_rows_map(CUtensorMap *map, const void *rows, int64_t nrows, int64_t cols, int box_rows, int dtype);
+
 // Launch with programmatic stream serialization: the launch may overlap the previous kernel's tail;
 // the kernels wait for it (griddepcontrol.wait) before touching global memory it may have written.
 template <typename Kernel, typename... Args>
