@@ -78,6 +78,15 @@ __device__ __forceinline__ void unpack2(uint64_t v, float *lo, float *hi) {
   *hi = __uint_as_float(b);
 }
 
+__device__ __forceinline__ void sts_f32(uint32_t addr, float v) {
+  asm volatile("st.shared.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+
 template <bool ON, int R>
 __device__ __forceinline__ void regs_down() {
   if constexpr (ON) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
@@ -90,19 +99,30 @@ __device__ __forceinline__ void regs_up() {
 // The units of a CTA in order, the next one's tile read ahead.
 struct UnitWalk {
   const Products &p;
-  int64_t u, units;
-  int step;
+  int u, units, step;
   RowTile next;
-  __device__ __forceinline__ UnitWalk(const Products &p_, int64_t units_) : p(p_), u(blockIdx.x), units(units_), step(gridDim.x) {
+  __device__ __forceinline__ UnitWalk(const Products &p_, int units_) : p(p_), u(blockIdx.x), units(units_), step(gridDim.x) {
     if (u < units) next = p.plan.tiles[u / p.slabs];
   }
   __device__ __forceinline__ bool take(RowTile *tile, int *wt) {
     if (u >= units) return false;
     *tile = next;
-    *wt = static_cast<int>(u % p.slabs);
+    *wt = u % p.slabs;
     u += step;
     if (u < units) next = p.plan.tiles[u / p.slabs];
     return true;
+  }
+};
+
+// A place in the ring of S stages: chunk c's, with the parity of its phase.
+template <int S>
+struct Ring {
+  uint32_t s = 0, phase = 0;
+  __device__ __forceinline__ void step() {
+    if (++s == S) {
+      s = 0;
+      phase ^= 1;
+    }
   }
 };
 
@@ -147,14 +167,17 @@ __global__ void __launch_bounds__(TCfg<BN, CB, SUB>::kThreads, 1)
   const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_sh, 0);
   if (threadIdx.x == 0) griddep_launch_dependents();
   griddep_wait();  // the plan and `in` come from the grids before this one
-  const int64_t units = static_cast<int64_t>(*p.plan.ntiles) * p.slabs;
+  const int units = *p.plan.ntiles * p.slabs;  // (the host has checked that this fits)
   const int chunks = (p.KB + CB - 1) / CB;  // of a unit
   constexpr uint64_t kLimit = kWaitLimitCycles;
+  const uint32_t full0 = smem_u32(&full_bar[0]), done0 = smem_u32(&done_bar[0]), empty0 = smem_u32(&empty_bar[0]);
+  const uint32_t ready0 = smem_u32(&ready_bar[0][0]), free0 = smem_u32(&free_bar[0][0]);
 
   if (warp < 4) {
     // ----------------------------------------------------------------- rows
     regs_down<C::kDeal, C::kRegsRows>();
     constexpr int kRows = BN / 4;  // of a warp
+    Ring<S> at;
     uint32_t c = 0;
     bool ok = true;
     RowTile rt;
@@ -170,13 +193,12 @@ __global__ void __launch_bounds__(TCfg<BN, CB, SUB>::kThreads, 1)
         for (int i = 0; i < kRows; ++i) tok[i] = __shfl_sync(0xffffffffu, mine, i);
       }
       const uint32_t bytes = rows == 0 ? 0u : GATED ? (rows + 3) / 4 * 512u : kRows * 128u;
-      for (int q = 0; q < chunks; ++q, ++c) {
-        const int s = c % S;
-        if (c >= static_cast<uint32_t>(S)) ok = warp_wait(smem_u32(&done_bar[s]), (c / S - 1) & 1, abort_flag, p.err, kLimit);
+      for (int q = 0; q < chunks; ++q, ++c, at.step()) {
+        if (c >= static_cast<uint32_t>(S)) ok = warp_wait(done0 + 8 * at.s, at.phase ^ 1, abort_flag, p.err, kLimit);
         if (!ok) break;
         if (elect_one()) {
-          const uint32_t to = smem_base + s * C::kStageBytes + warp * kRows * 128;
-          const uint32_t bar = smem_u32(&full_bar[s]);
+          const uint32_t to = smem_base + at.s * C::kStageBytes + warp * kRows * 128;
+          const uint32_t bar = full0 + 8 * at.s;
           const int nb = min(CB, p.KB - q * CB);
           mbar_arrive_expect_tx(bar, bytes * nb);
 #pragma unroll
@@ -198,31 +220,32 @@ __global__ void __launch_bounds__(TCfg<BN, CB, SUB>::kThreads, 1)
       }
     }
     if (!ok && elect_one())  // no copy in flight when the CTA leaves
-      for (uint32_t i = c >= static_cast<uint32_t>(S) ? c - S : 0u; i < c; ++i) drain_wait(smem_u32(&full_bar[i % S]), (i / S) & 1);
+      for (uint32_t i = c >= static_cast<uint32_t>(S) ? c - S : 0u; i < c; ++i) drain_wait(full0 + 8 * (i % S), (i / S) & 1);
   } else if (warp < 8) {
     regs_down<C::kDeal, C::kRegsIssue>();
     if (warp < 6) {
       // ---------------------------------------------------------- MMA issue
       const int e = warp - 4;
+      Ring<S> at;
       uint32_t c = 0;
       bool ok = true;
       RowTile rt;
       int wt;
       for (UnitWalk w(p, units); ok && w.take(&rt, &wt);) {
         const uint32_t idesc = idesc_f16_f32(128, (rt.rows + 15) / 16 * 16, DT == kDtypeBf16);
-        for (int q = 0; q < chunks; ++q, ++c) {
+        for (int q = 0; q < chunks; ++q, ++c, at.step()) {
           if (static_cast<int>(c & 1) != e) continue;
-          const int s = c % S;
           const uint32_t n = c / 2;  // this warp's chunks so far
-          if (n > 0) ok = warp_wait(smem_u32(&empty_bar[e]), (n - 1) & 1, abort_flag, p.err, kLimit);
-          if (ok) ok = warp_wait(smem_u32(&full_bar[s]), (c / S) & 1, abort_flag, p.err, kLimit);
-          if (ok) ok = warp_wait(smem_u32(&ready_bar[e][n & 1]), (n / 2) & 1, abort_flag, p.err, kLimit);
+          const uint32_t slot = 2 * e + (n & 1);
+          if (n > 0) ok = warp_wait(empty0 + 8 * e, (n - 1) & 1, abort_flag, p.err, kLimit);
+          if (ok) ok = warp_wait(full0 + 8 * at.s, at.phase, abort_flag, p.err, kLimit);
+          if (ok) ok = warp_wait(ready0 + 8 * slot, (n / 2) & 1, abort_flag, p.err, kLimit);
           if (!ok) break;
           tc_fence_after();
           if (elect_one()) {
             const int nb = min(CB, p.KB - q * CB);
-            const uint32_t xs = smem_base + s * C::kStageBytes;
-            const uint32_t a = tmem + C::kACol0 + (2 * e + (n & 1)) * C::kASlotCols;
+            const uint32_t xs = smem_base + at.s * C::kStageBytes;
+            const uint32_t a = tmem + C::kACol0 + slot * C::kASlotCols;
 #pragma unroll
             for (int b = 0; b < CB; ++b) {
               if (b >= nb) break;
@@ -235,8 +258,8 @@ __global__ void __launch_bounds__(TCfg<BN, CB, SUB>::kThreads, 1)
                            fresh ? 0u : 1u);
               }
             }
-            mma_commit(smem_u32(&free_bar[e][n & 1]));
-            mma_commit(smem_u32(&done_bar[s]));
+            mma_commit(free0 + 8 * slot);
+            mma_commit(done0 + 8 * at.s);
           }
           __syncwarp();
         }
@@ -250,6 +273,7 @@ __global__ void __launch_bounds__(TCfg<BN, CB, SUB>::kThreads, 1)
       // ------------------------------------------------- codes and records
       const bool records = warp == 7;
       const uint64_t policy = policy_evict_normal();  // an expert's other row tiles read the weights again
+      Ring<S> at;
       uint32_t c = 0;
       bool ok = true;
       RowTile rt;
@@ -258,13 +282,12 @@ __global__ void __launch_bounds__(TCfg<BN, CB, SUB>::kThreads, 1)
         const uint8_t *expert = p.codes + rt.key * p.expert_bytes;
         const uint8_t *codes = expert + static_cast<int64_t>(wt) * p.KB * kTileBytes;
         const uint8_t *meta = expert + p.meta + static_cast<int64_t>(wt) * p.G * kRecBytes;
-        for (int q = 0; q < chunks; ++q, ++c) {
-          const int s = c % S;
-          if (c >= static_cast<uint32_t>(S)) ok = warp_wait(smem_u32(&done_bar[s]), (c / S - 1) & 1, abort_flag, p.err, kLimit);
+        for (int q = 0; q < chunks; ++q, ++c, at.step()) {
+          if (c >= static_cast<uint32_t>(S)) ok = warp_wait(done0 + 8 * at.s, at.phase ^ 1, abort_flag, p.err, kLimit);
           if (!ok) break;
           if (elect_one()) {
-            const uint32_t to = smem_base + s * C::kStageBytes + C::kXBytes;
-            const uint32_t bar = smem_u32(&full_bar[s]);
+            const uint32_t to = smem_base + at.s * C::kStageBytes + C::kXBytes;
+            const uint32_t bar = full0 + 8 * at.s;
             if (records) {
               const int k0 = q * CB * kTK;
               const int j0 = p.gdiv.div(k0);
@@ -281,7 +304,7 @@ __global__ void __launch_bounds__(TCfg<BN, CB, SUB>::kThreads, 1)
         }
       }
       if (!ok && elect_one())  // no copy in flight when the CTA leaves
-        for (uint32_t i = c >= static_cast<uint32_t>(S) ? c - S : 0u; i < c; ++i) drain_wait(smem_u32(&full_bar[i % S]), (i / S) & 1);
+        for (uint32_t i = c >= static_cast<uint32_t>(S) ? c - S : 0u; i < c; ++i) drain_wait(full0 + 8 * (i % S), (i / S) & 1);
     }
   } else if (warp < 16) {
     // ------------------------------------------------------------ dequant
@@ -289,16 +312,24 @@ __global__ void __launch_bounds__(TCfg<BN, CB, SUB>::kThreads, 1)
     const int lq = warp % 4;
     const int r = lq * 32 + lane;
     const uint32_t lane_addr = static_cast<uint32_t>(lq * 32) << 16;
-    int64_t mine = 0;  // chunks of the CTA
-    if (blockIdx.x < units) mine = (units - blockIdx.x + gridDim.x - 1) / gridDim.x * chunks;
-    int q = e;         // chunk of its unit
-    while (q >= chunks) q -= chunks;
-    for (int64_t c = e; c < mine; c += 2) {
-      const int s = static_cast<int>(c % S);
-      if (!warp_wait(smem_u32(&full_bar[s]), static_cast<uint32_t>(c / S) & 1, abort_flag, p.err, kLimit)) break;
-      const uint32_t n = static_cast<uint32_t>(c / 2);  // this warpgroup's chunks so far
-      if (n >= 2 && !warp_wait(smem_u32(&free_bar[e][n & 1]), (n / 2 - 1) & 1, abort_flag, p.err, kLimit)) break;
-      const uint32_t stage = smem_base + s * C::kStageBytes;
+    const int mine = static_cast<int>(blockIdx.x) < units ? (units - static_cast<int>(blockIdx.x) + static_cast<int>(gridDim.x) - 1) /
+                                                               static_cast<int>(gridDim.x)
+                                                         : 0;  // units of the CTA
+    // the warpgroup's chunks: chunk q of unit i, n of them so far
+    int i = 0, q = e;
+    Ring<S> at;
+    if (e) at.step();
+    const uint32_t scale0 = smem_u32(&scales[0][0][0]) + 4 * r;
+    for (uint32_t n = 0;; ++n) {
+      while (q >= chunks) {
+        q -= chunks;
+        ++i;
+      }
+      if (i >= mine) break;
+      if (!warp_wait(full0 + 8 * at.s, at.phase, abort_flag, p.err, kLimit)) break;
+      const uint32_t slot = 2 * e + (n & 1);
+      if (n >= 2 && !warp_wait(free0 + 8 * slot, (n / 2 - 1) & 1, abort_flag, p.err, kLimit)) break;
+      const uint32_t stage = smem_base + at.s * C::kStageBytes;
       const uint32_t codes = stage + C::kXBytes + r * 16;
       const uint32_t rec = stage + C::kXBytes + C::kCodeBytes;
       const int nb = min(CB, p.KB - q * CB);
@@ -310,9 +341,9 @@ __global__ void __launch_bounds__(TCfg<BN, CB, SUB>::kThreads, 1)
         const uint32_t off = h == 0 ? 0u : (p.gdiv.div(min(k0 + 32, p.K - 1)) - p.gdiv.div(k0)) * kRecBytes;
         const uint32_t bits = lds16(rec + off + 2 * r);
         gc[h] = group_consts<DT>(bits, (lds8(rec + off + 256 + r / 2) >> (4 * (r & 1))) & 0xFu);
-        scales[c % C::kScaleSlots][h][r] = scale_f32<DT>(bits);
+        sts_f32(scale0 + (((2 * n + e) % C::kScaleSlots) * SUB + h) * kTN * 4, scale_f32<DT>(bits));
       }
-      const uint32_t a = tmem + lane_addr + C::kACol0 + (2 * e + (n & 1)) * C::kASlotCols;
+      const uint32_t a = tmem + lane_addr + C::kACol0 + slot * C::kASlotCols;
       tc_fence_after();
 #pragma unroll
       for (int b = 0; b < CB; ++b) {
@@ -334,9 +365,10 @@ __global__ void __launch_bounds__(TCfg<BN, CB, SUB>::kThreads, 1)
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&ready_bar[e][n & 1]));
+      if (lane == 0) mbar_arrive(ready0 + 8 * slot);
       q += 2;
-      while (q >= chunks) q -= chunks;
+      at.step();
+      at.step();
     }
   } else {
     // ------------------------------------------------------------ sums
@@ -346,8 +378,10 @@ __global__ void __launch_bounds__(TCfg<BN, CB, SUB>::kThreads, 1)
     const int lq = warp % 4;
     const int r = lq * 32 + lane;
     const uint32_t lane_addr = static_cast<uint32_t>(lq * 32) << 16;
+    Ring<S> at;
     uint32_t c = 0;
     bool ok = true;
+    const uint32_t scale0 = smem_u32(&scales[0][0][0]) + 4 * r;
     RowTile rt;
     int wt;
     for (UnitWalk w(p, units); ok && w.take(&rt, &wt);) {
@@ -355,15 +389,14 @@ __global__ void __launch_bounds__(TCfg<BN, CB, SUB>::kThreads, 1)
       uint64_t acc[kCols / 2];
 #pragma unroll
       for (int i = 0; i < kCols / 2; ++i) acc[i] = 0ull;
-      for (int q = 0; q < chunks; ++q, ++c) {
-        const int s = c % S;
-        ok = warp_wait(smem_u32(&done_bar[s]), (c / S) & 1, abort_flag, p.err, kLimit);
+      for (int q = 0; q < chunks; ++q, ++c, at.step()) {
+        ok = warp_wait(done0 + 8 * at.s, at.phase, abort_flag, p.err, kLimit);
         if (!ok) break;
         tc_fence_after();
 #pragma unroll
         for (int h = 0; h < SUB; ++h) {
           if (h == 1 && q * kTK + 32 >= p.K) break;  // its products were not of this unit's K
-          const uint32_t sb = __float_as_uint(scales[c % C::kScaleSlots][h][r]);
+          const uint32_t sb = lds32(scale0 + ((c % C::kScaleSlots) * SUB + h) * kTN * 4);
           const uint64_t s2 = pack2(sb, sb);
           const uint32_t d = tmem + lane_addr + ((c & 1) * SUB + h) * BN + part * kCols;
           if (cols > 0) {
@@ -374,7 +407,7 @@ __global__ void __launch_bounds__(TCfg<BN, CB, SUB>::kThreads, 1)
             if (h == SUB - 1 || q * kTK + 32 >= p.K) {  // the last read of the chunk's sums
               tc_fence_before();
               __syncwarp();
-              if (lane == 0) mbar_arrive(smem_u32(&empty_bar[c & 1]));
+              if (lane == 0) mbar_arrive(empty0 + 8 * (c & 1));
             }
 #pragma unroll
             for (int i = 0; i < 8; ++i) acc[i] = fma2(s2, pack2(v0[2 * i], v0[2 * i + 1]), acc[i]);
@@ -384,7 +417,7 @@ __global__ void __launch_bounds__(TCfg<BN, CB, SUB>::kThreads, 1)
         }
         if (cols == 0) {
           __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&empty_bar[c & 1]));
+          if (lane == 0) mbar_arrive(empty0 + 8 * (c & 1));
         }
       }
       if (!ok) break;
