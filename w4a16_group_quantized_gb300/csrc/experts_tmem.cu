@@ -16,17 +16,17 @@
 //                      scale in a ring in shared memory
 //   8 or 16 sum warps  a warpgroup for each 32 rows of `in`: add scale * (chunk's sums) to their 32-bit registers, and
 //                      write h or the output at a unit's end
-// SUB = 2: a chunk of one block whose halves of 32 k lie in different groups, each with an accumulator of its own.
+// SUB = 2: a chunk's halves (64 k, or 32 for one block) lie in different groups, each with an accumulator of its own.
 //
-// Barriers, each waited for in every phase and in order (chunk c; S stages):
-//   full[c % S]      the chunk's rows, codes and records have landed
-//   ready[c % 2][c / 2 % 2]  its A operand is stored
+// Barriers, each waited for in every phase and in order (chunk c; S stages of rows, W of weights):
+//   go[c % S]        what the chunk's MMAs need: its rows have landed, its A operand is stored, and its accumulator has
+//                    been read (one barrier for the three: each wait costs an MMA warp some 200 cycles, even when over)
+//   wfull[c % W], wfree[c % W]   its codes and records have landed; a dequant warpgroup has read them
 //   free[c % 2][c / 2 % 2]   its MMAs are complete, for the dequant warps: the A slot is free
-//   done[c % S]      its MMAs are complete, for the others: the stage is free, its sums can be read
-//   empty[c % 2]     its sums have been read
-// The sum warps of chunk c are done before chunk c + 2's MMAs start, hence before done of c + 2: the scale ring's
-// eight places (a dequant warp writes c + 8's after free of c + 4) and done's parity are never overtaken. The
-// dequant warps do not wait for done: the other warpgroup may be a whole turn of the stages ahead of one.
+//   done[c % S]      its MMAs are complete, for the others: the rows' stage is free, its sums can be read
+// The sum warps have read chunk c's sums before the MMAs of c + 2 or, with two accumulators an MMA warp, c + 4 start, hence
+// before done of those: the scale ring's eight places (a dequant warp writes c + 8's after free of c + 4) and done's
+// parity (S is at least 4, or 6 with two) are never overtaken.
 // Every wait is bounded (ptx.cuh).
 #include <atomic>
 
@@ -51,13 +51,19 @@ struct TCfg {
   static constexpr int kXSub = BN * 128;  // one block of 64 k of BN rows
   static constexpr int kXBytes = CB * kXSub;
   static constexpr int kCodeBytes = CB * kTileBytes;
-  static constexpr int kStageBytes = (kXBytes + kCodeBytes + SUB * kRecBytes + 1023) / 1024 * 1024;
-  static constexpr int kStagesRaw = 216 * 1024 / kStageBytes;
-  static constexpr int kStages = kStagesRaw > 8 ? 8 : kStagesRaw;
+  static constexpr int kSubK = CB * kTK / SUB;            // k of an accumulator: a group's part of a chunk
+  static constexpr int kWBytes = kCodeBytes + SUB * 384;  // codes, group records (320 bytes each)
+  // two rings: rows wait for their turn in the tensor cores, codes only until a dequant warp has read them
+  static constexpr int kXStages = BN == 128 ? (CB == 2 ? 4 : 8) : (CB == 2 ? 6 : 8);
+  static constexpr int kWStagesRaw = (214 * 1024 - kXStages * kXBytes) / kWBytes;
+  static constexpr int kWStages = kWStagesRaw > 16 ? 16 : kWStagesRaw;
   static constexpr int kScaleSlots = 8;
-  static constexpr int kSmemBytes = kStages * kStageBytes + 1024;
+  static constexpr int kSmemBytes = kXStages * kXBytes + kWStages * kWBytes + 1024;
   static constexpr int kASlotCols = CB * 32;   // 128 rows x 64 16-bit values: 32 columns a block
-  static constexpr int kACol0 = 2 * SUB * BN;  // accumulators first
+  // accumulators of each MMA warp; a second one where tensor memory has room
+  static constexpr int kDBufs = SUB * BN <= 64 ? 2 : 1;
+  static constexpr int kACol0 = 2 * kDBufs * SUB * BN;  // accumulators first
+  static_assert(kXStages % 2 == 0 && kXStages >= 4 && kXStages >= 2 * kDBufs, "ring of rows");
   static_assert(kACol0 + 4 * kASlotCols <= 512, "tensor memory");
 };
 
@@ -96,6 +102,13 @@ __device__ __forceinline__ void regs_up() {
   if constexpr (ON) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R));
 }
 
+// After a wait that gave up, the barriers say no more when the copies in flight have landed, which takes some
+// microseconds: ten milliseconds pass before the CTA leaves its shared memory.
+__device__ __forceinline__ void let_copies_land() {
+  const uint64_t t0 = clock_cycles();
+  while (clock_cycles() - t0 < 20ull * 1000 * 1000) __nanosleep(1000);
+}
+
 // The units of a CTA in order, the next one's tile read ahead.
 struct UnitWalk {
   const Products &p;
@@ -130,9 +143,9 @@ template <int DT, int BN, int CB, int SUB, bool GATED>
 __global__ void __launch_bounds__(TCfg<BN, CB, SUB>::kThreads, 1)
     experts_tmem_kernel(const __grid_constant__ CUtensorMap in_map, const __grid_constant__ Products p) {
   using C = TCfg<BN, CB, SUB>;
-  constexpr int S = C::kStages;
+  constexpr int S = C::kXStages, W = C::kWStages;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t full_bar[S], done_bar[S], ready_bar[2][2], free_bar[2][2], empty_bar[2], drain_bar[2];
+  __shared__ __align__(8) uint64_t go_bar[S], done_bar[S], wfull_bar[W], wfree_bar[W], free_bar[2][2], drain_bar[2];
   __shared__ float scales[C::kScaleSlots][SUB][kTN];
   __shared__ uint32_t tmem_sh, abort_sh;
 
@@ -141,15 +154,16 @@ __global__ void __launch_bounds__(TCfg<BN, CB, SUB>::kThreads, 1)
   volatile uint32_t *abort_flag = &abort_sh;
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
-      mbar_init(smem_u32(&full_bar[s]), 4 + 2);  // the row warps and the weight warps
+      // the row warps, the chunk's dequant warps, and the sum warps of the accumulator's chunk before
+      mbar_init(smem_u32(&go_bar[s]), 4 + 4 + 4 * C::kSumGroups);
       mbar_init(smem_u32(&done_bar[s]), 1);
     }
+    for (int s = 0; s < W; ++s) {
+      mbar_init(smem_u32(&wfull_bar[s]), 2);  // the weight warps
+      mbar_init(smem_u32(&wfree_bar[s]), 4);
+    }
     for (int e = 0; e < 2; ++e) {
-      for (int a = 0; a < 2; ++a) {
-        mbar_init(smem_u32(&ready_bar[e][a]), 4);
-        mbar_init(smem_u32(&free_bar[e][a]), 1);
-      }
-      mbar_init(smem_u32(&empty_bar[e]), 4 * C::kSumGroups);
+      for (int a = 0; a < 2; ++a) mbar_init(smem_u32(&free_bar[e][a]), 1);
       mbar_init(smem_u32(&drain_bar[e]), 1);
     }
     abort_sh = 0;
@@ -170,8 +184,10 @@ __global__ void __launch_bounds__(TCfg<BN, CB, SUB>::kThreads, 1)
   const int units = *p.plan.ntiles * p.slabs;  // (the host has checked that this fits)
   const int chunks = (p.KB + CB - 1) / CB;  // of a unit
   constexpr uint64_t kLimit = kWaitLimitCycles;
-  const uint32_t full0 = smem_u32(&full_bar[0]), done0 = smem_u32(&done_bar[0]), empty0 = smem_u32(&empty_bar[0]);
-  const uint32_t ready0 = smem_u32(&ready_bar[0][0]), free0 = smem_u32(&free_bar[0][0]);
+  const uint32_t go0 = smem_u32(&go_bar[0]), done0 = smem_u32(&done_bar[0]);
+  const uint32_t wfull0 = smem_u32(&wfull_bar[0]), wfree0 = smem_u32(&wfree_bar[0]);
+  const uint32_t w_base = smem_base + S * C::kXBytes;
+  const uint32_t free0 = smem_u32(&free_bar[0][0]);
 
   if (warp < 4) {
     // ----------------------------------------------------------------- rows
@@ -197,8 +213,8 @@ __global__ void __launch_bounds__(TCfg<BN, CB, SUB>::kThreads, 1)
         if (c >= static_cast<uint32_t>(S)) ok = warp_wait(done0 + 8 * at.s, at.phase ^ 1, abort_flag, p.err, kLimit);
         if (!ok) break;
         if (elect_one()) {
-          const uint32_t to = smem_base + at.s * C::kStageBytes + warp * kRows * 128;
-          const uint32_t bar = full0 + 8 * at.s;
+          const uint32_t to = smem_base + at.s * C::kXBytes + warp * kRows * 128;
+          const uint32_t bar = go0 + 8 * at.s;
           const int nb = min(CB, p.KB - q * CB);
           mbar_arrive_expect_tx(bar, bytes * nb);
 #pragma unroll
@@ -219,32 +235,31 @@ __global__ void __launch_bounds__(TCfg<BN, CB, SUB>::kThreads, 1)
         __syncwarp();
       }
     }
-    if (!ok && elect_one())  // no copy in flight when the CTA leaves
-      for (uint32_t i = c >= static_cast<uint32_t>(S) ? c - S : 0u; i < c; ++i) drain_wait(full0 + 8 * (i % S), (i / S) & 1);
+    if (!ok) let_copies_land();
   } else if (warp < 8) {
     regs_down<C::kDeal, C::kRegsIssue>();
     if (warp < 6) {
       // ---------------------------------------------------------- MMA issue
       const int e = warp - 4;
-      Ring<S> at;
-      uint32_t c = 0;
+      Ring<S> at;  // S is even: a stage's chunks are all of one warp, which so waits for each of its phases
+      if (e) at.step();
+      uint32_t n = 0;  // this warp's chunks so far
+      int skip = e;    // chunks of the unit before its first
       bool ok = true;
       RowTile rt;
       int wt;
       for (UnitWalk w(p, units); ok && w.take(&rt, &wt);) {
         const uint32_t idesc = idesc_f16_f32(128, (rt.rows + 15) / 16 * 16, DT == kDtypeBf16);
-        for (int q = 0; q < chunks; ++q, ++c, at.step()) {
-          if (static_cast<int>(c & 1) != e) continue;
-          const uint32_t n = c / 2;  // this warp's chunks so far
+        int q = skip;
+        for (; q < chunks; q += 2, ++n) {
           const uint32_t slot = 2 * e + (n & 1);
-          if (n > 0) ok = warp_wait(empty0 + 8 * e, (n - 1) & 1, abort_flag, p.err, kLimit);
-          if (ok) ok = warp_wait(full0 + 8 * at.s, at.phase, abort_flag, p.err, kLimit);
-          if (ok) ok = warp_wait(ready0 + 8 * slot, (n / 2) & 1, abort_flag, p.err, kLimit);
+          const uint32_t d = C::kDBufs * e + n % C::kDBufs;
+          ok = warp_wait(go0 + 8 * at.s, at.phase, abort_flag, p.err, kLimit);
           if (!ok) break;
           tc_fence_after();
           if (elect_one()) {
             const int nb = min(CB, p.KB - q * CB);
-            const uint32_t xs = smem_base + at.s * C::kStageBytes;
+            const uint32_t xs = smem_base + at.s * C::kXBytes;
             const uint32_t a = tmem + C::kACol0 + slot * C::kASlotCols;
 #pragma unroll
             for (int b = 0; b < CB; ++b) {
@@ -252,9 +267,9 @@ __global__ void __launch_bounds__(TCfg<BN, CB, SUB>::kThreads, 1)
               const uint64_t bdesc = sw128_kmajor_desc(xs + b * C::kXSub);
 #pragma unroll
               for (int kk = 0; kk < 4; ++kk) {
-                const int half = SUB == 2 ? kk / 2 : 0;
-                const bool fresh = SUB == 2 ? kk % 2 == 0 : b == 0 && kk == 0;
-                mma_f16_ts(tmem + (e * SUB + half) * BN, a + b * 32 + kk * 8, bdesc + static_cast<uint64_t>(kk * 2), idesc,
+                const int half = (b * kTK + kk * 16) / C::kSubK;
+                const bool fresh = (b * kTK + kk * 16) % C::kSubK == 0;
+                mma_f16_ts(tmem + (d * SUB + half) * BN, a + b * 32 + kk * 8, bdesc + static_cast<uint64_t>(kk * 2), idesc,
                            fresh ? 0u : 1u);
               }
             }
@@ -262,7 +277,10 @@ __global__ void __launch_bounds__(TCfg<BN, CB, SUB>::kThreads, 1)
             mma_commit(done0 + 8 * at.s);
           }
           __syncwarp();
+          at.step();
+          at.step();
         }
+        skip = q - chunks;
       }
       const bool aborted = __any_sync(0xffffffffu, *abort_flag != 0);
       if (aborted && elect_one()) {
@@ -273,7 +291,7 @@ __global__ void __launch_bounds__(TCfg<BN, CB, SUB>::kThreads, 1)
       // ------------------------------------------------- codes and records
       const bool records = warp == 7;
       const uint64_t policy = policy_evict_normal();  // an expert's other row tiles read the weights again
-      Ring<S> at;
+      Ring<W> at;
       uint32_t c = 0;
       bool ok = true;
       RowTile rt;
@@ -283,15 +301,15 @@ __global__ void __launch_bounds__(TCfg<BN, CB, SUB>::kThreads, 1)
         const uint8_t *codes = expert + static_cast<int64_t>(wt) * p.KB * kTileBytes;
         const uint8_t *meta = expert + p.meta + static_cast<int64_t>(wt) * p.G * kRecBytes;
         for (int q = 0; q < chunks; ++q, ++c, at.step()) {
-          if (c >= static_cast<uint32_t>(S)) ok = warp_wait(done0 + 8 * at.s, at.phase ^ 1, abort_flag, p.err, kLimit);
+          if (c >= static_cast<uint32_t>(W)) ok = warp_wait(wfree0 + 8 * at.s, at.phase ^ 1, abort_flag, p.err, kLimit);
           if (!ok) break;
           if (elect_one()) {
-            const uint32_t to = smem_base + at.s * C::kStageBytes + C::kXBytes;
-            const uint32_t bar = full0 + 8 * at.s;
+            const uint32_t to = w_base + at.s * C::kWBytes;
+            const uint32_t bar = wfull0 + 8 * at.s;
             if (records) {
               const int k0 = q * CB * kTK;
               const int j0 = p.gdiv.div(k0);
-              const int nrec = SUB == 1 ? 1 : p.gdiv.div(min(k0 + kTK, p.K) - 1) - j0 + 1;
+              const int nrec = SUB == 1 ? 1 : p.gdiv.div(min(k0 + CB * kTK, p.K) - 1) - j0 + 1;
               mbar_arrive_expect_tx(bar, nrec * kRecBytes);
               bulk_g2s(to + C::kCodeBytes, meta + static_cast<int64_t>(j0) * kRecBytes, nrec * kRecBytes, bar, policy);
             } else {
@@ -303,8 +321,7 @@ __global__ void __launch_bounds__(TCfg<BN, CB, SUB>::kThreads, 1)
           __syncwarp();
         }
       }
-      if (!ok && elect_one())  // no copy in flight when the CTA leaves
-        for (uint32_t i = c >= static_cast<uint32_t>(S) ? c - S : 0u; i < c; ++i) drain_wait(full0 + 8 * (i % S), (i / S) & 1);
+      if (!ok) let_copies_land();
     }
   } else if (warp < 16) {
     // ------------------------------------------------------------ dequant
@@ -317,7 +334,8 @@ __global__ void __launch_bounds__(TCfg<BN, CB, SUB>::kThreads, 1)
                                                          : 0;  // units of the CTA
     // the warpgroup's chunks: chunk q of unit i, n of them so far
     int i = 0, q = e;
-    Ring<S> at;
+    uint32_t x_at = e;  // its place in the ring of rows
+    Ring<W> at;
     if (e) at.step();
     const uint32_t scale0 = smem_u32(&scales[0][0][0]) + 4 * r;
     for (uint32_t n = 0;; ++n) {
@@ -326,19 +344,18 @@ __global__ void __launch_bounds__(TCfg<BN, CB, SUB>::kThreads, 1)
         ++i;
       }
       if (i >= mine) break;
-      if (!warp_wait(full0 + 8 * at.s, at.phase, abort_flag, p.err, kLimit)) break;
+      if (!warp_wait(wfull0 + 8 * at.s, at.phase, abort_flag, p.err, kLimit)) break;
       const uint32_t slot = 2 * e + (n & 1);
       if (n >= 2 && !warp_wait(free0 + 8 * slot, (n / 2 - 1) & 1, abort_flag, p.err, kLimit)) break;
-      const uint32_t stage = smem_base + at.s * C::kStageBytes;
-      const uint32_t codes = stage + C::kXBytes + r * 16;
-      const uint32_t rec = stage + C::kXBytes + C::kCodeBytes;
+      const uint32_t codes = w_base + at.s * C::kWBytes + r * 16;
+      const uint32_t rec = w_base + at.s * C::kWBytes + C::kCodeBytes;
       const int nb = min(CB, p.KB - q * CB);
       GroupConsts gc[SUB];
 #pragma unroll
       for (int h = 0; h < SUB; ++h) {
         // the second half's record is the first's when both lie in one group (or the half lies past K)
-        const int k0 = q * kTK;
-        const uint32_t off = h == 0 ? 0u : (p.gdiv.div(min(k0 + 32, p.K - 1)) - p.gdiv.div(k0)) * kRecBytes;
+        const int k0 = q * CB * kTK;
+        const uint32_t off = h == 0 ? 0u : (p.gdiv.div(min(k0 + C::kSubK, p.K - 1)) - p.gdiv.div(k0)) * kRecBytes;
         const uint32_t bits = lds16(rec + off + 2 * r);
         gc[h] = group_consts<DT>(bits, (lds8(rec + off + 256 + r / 2) >> (4 * (r & 1))) & 0xFu);
         sts_f32(scale0 + (((2 * n + e) % C::kScaleSlots) * SUB + h) * kTN * 4, scale_f32<DT>(bits));
@@ -350,22 +367,27 @@ __global__ void __launch_bounds__(TCfg<BN, CB, SUB>::kThreads, 1)
         if (b >= nb) break;
         const uint4 w0 = lds128(codes + b * kTileBytes);
         const uint4 w1 = lds128(codes + b * kTileBytes + 2048);
+        if (b == nb - 1) {  // the stage has been read
+          __syncwarp();
+          if (lane == 0) mbar_arrive(wfree0 + 8 * at.s);
+        }
         uint32_t out[16];
-        dequant_word_int<DT>(w0.x, gc[0], out);
-        dequant_word_int<DT>(w0.y, gc[0], out + 4);
-        dequant_word_int<DT>(w0.z, gc[0], out + 8);
-        dequant_word_int<DT>(w0.w, gc[0], out + 12);
+        dequant_word_int<DT>(w0.x, gc[b * kTK / C::kSubK], out);
+        dequant_word_int<DT>(w0.y, gc[b * kTK / C::kSubK], out + 4);
+        dequant_word_int<DT>(w0.z, gc[b * kTK / C::kSubK], out + 8);
+        dequant_word_int<DT>(w0.w, gc[b * kTK / C::kSubK], out + 12);
         tmem_st_32x32b_x16(a + b * 32, out);
-        dequant_word_int<DT>(w1.x, gc[SUB - 1], out);
-        dequant_word_int<DT>(w1.y, gc[SUB - 1], out + 4);
-        dequant_word_int<DT>(w1.z, gc[SUB - 1], out + 8);
-        dequant_word_int<DT>(w1.w, gc[SUB - 1], out + 12);
+        dequant_word_int<DT>(w1.x, gc[(b * kTK + 32) / C::kSubK], out);
+        dequant_word_int<DT>(w1.y, gc[(b * kTK + 32) / C::kSubK], out + 4);
+        dequant_word_int<DT>(w1.z, gc[(b * kTK + 32) / C::kSubK], out + 8);
+        dequant_word_int<DT>(w1.w, gc[(b * kTK + 32) / C::kSubK], out + 12);
         tmem_st_32x32b_x16(a + b * 32 + 16, out);
       }
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(ready0 + 8 * slot);
+      if (lane == 0) mbar_arrive(go0 + 8 * x_at);
+      x_at = x_at + 2 >= S ? x_at + 2 - S : x_at + 2;
       q += 2;
       at.step();
       at.step();
@@ -379,6 +401,9 @@ __global__ void __launch_bounds__(TCfg<BN, CB, SUB>::kThreads, 1)
     const int r = lq * 32 + lane;
     const uint32_t lane_addr = static_cast<uint32_t>(lq * 32) << 16;
     Ring<S> at;
+    constexpr uint32_t kAhead = 2 * C::kDBufs;  // the accumulator's next chunk
+    if (lane == 0)
+      for (uint32_t i = 0; i < kAhead; ++i) mbar_arrive(go0 + 8 * i);  // the first chunks' accumulators are free
     uint32_t c = 0;
     bool ok = true;
     const uint32_t scale0 = smem_u32(&scales[0][0][0]) + 4 * r;
@@ -393,21 +418,23 @@ __global__ void __launch_bounds__(TCfg<BN, CB, SUB>::kThreads, 1)
         ok = warp_wait(done0 + 8 * at.s, at.phase, abort_flag, p.err, kLimit);
         if (!ok) break;
         tc_fence_after();
+        const uint32_t buf = C::kDBufs * (c & 1) + c / 2 % C::kDBufs;
+        const uint32_t next = go0 + 8 * (at.s + kAhead >= S ? at.s + kAhead - S : at.s + kAhead);
 #pragma unroll
         for (int h = 0; h < SUB; ++h) {
-          if (h == 1 && q * kTK + 32 >= p.K) break;  // its products were not of this unit's K
+          if (h == 1 && q * CB * kTK + C::kSubK >= p.K) break;  // its products were not of this unit's K
           const uint32_t sb = lds32(scale0 + ((c % C::kScaleSlots) * SUB + h) * kTN * 4);
           const uint64_t s2 = pack2(sb, sb);
-          const uint32_t d = tmem + lane_addr + ((c & 1) * SUB + h) * BN + part * kCols;
+          const uint32_t d = tmem + lane_addr + (buf * SUB + h) * BN + part * kCols;
           if (cols > 0) {
             uint32_t v0[16], v1[16];
             tmem_ld_32x32b_x16(d, v0);
             tmem_ld_32x32b_x16(d + 16, v1);
             tmem_wait_ld();
-            if (h == SUB - 1 || q * kTK + 32 >= p.K) {  // the last read of the chunk's sums
+            if (h == SUB - 1 || q * CB * kTK + C::kSubK >= p.K) {  // the last read of the chunk's sums
               tc_fence_before();
               __syncwarp();
-              if (lane == 0) mbar_arrive(empty0 + 8 * (c & 1));
+              if (lane == 0) mbar_arrive(next);
             }
 #pragma unroll
             for (int i = 0; i < 8; ++i) acc[i] = fma2(s2, pack2(v0[2 * i], v0[2 * i + 1]), acc[i]);
@@ -417,7 +444,7 @@ __global__ void __launch_bounds__(TCfg<BN, CB, SUB>::kThreads, 1)
         }
         if (cols == 0) {
           __syncwarp();
-          if (lane == 0) mbar_arrive(empty0 + 8 * (c & 1));
+          if (lane == 0) mbar_arrive(next);
         }
       }
       if (!ok) break;
@@ -490,7 +517,7 @@ cudaError_t launch_groups(const Products &p, int tile, int num_sms, cudaStream_t
   if (p.g % 128 == 0)
     return tile == 128 ? launch_one<DT, 128, 2, 1, GATED>(p, num_sms, stream) : launch_one<DT, 64, 2, 1, GATED>(p, num_sms, stream);
   if (p.g % 64 == 0)
-    return tile == 128 ? launch_one<DT, 128, 1, 1, GATED>(p, num_sms, stream) : launch_one<DT, 64, 1, 1, GATED>(p, num_sms, stream);
+    return tile == 128 ? launch_one<DT, 128, 1, 1, GATED>(p, num_sms, stream) : launch_one<DT, 64, 2, 2, GATED>(p, num_sms, stream);
   return launch_one<DT, 64, 1, 2, GATED>(p, num_sms, stream);
 }
 
