@@ -7,7 +7,7 @@
 // memory straight to the registers of the tensor-core products, 16 bytes a lane: a lane's k are consecutive (mma.cuh),
 // and for the outputs' sake so are the four pairs of columns n that a lane holds of four products.
 //
-// Rows stand by adapter (rows.cu), cut into tiles of up to 32; up to kDirectRows rows go without a sort, one row to a
+// Rows stand by adapter (rows.cu), cut into tiles of 16 to 64; up to kDirectRows rows go without a sort, one row to a
 // tile (rows of one adapter then read its weights again, from L2).
 //
 // v stands in the second product as the sum of two 16-bit values, its rounding and what that left, which keeps about
@@ -42,8 +42,8 @@ __device__ __forceinline__ bool get_tile(const Tiles &ts, int i, int adapters, i
     *rows = 1;
     return true;
   }
+  const RowTile t = ts.plan.tiles[i];  // (read beside the count: the list has room for every block)
   if (i >= *ts.plan.ntiles) return false;
-  const RowTile t = ts.plan.tiles[i];
   *key = t.key < adapters ? t.key : -1;
   *row0 = t.row0;
   *rows = t.rows;
@@ -54,19 +54,21 @@ __device__ __forceinline__ int64_t row_at(const Tiles &ts, int pos) { return ts.
 
 __device__ __forceinline__ uint4 ldg16(const uint16_t *p) { return __ldg(reinterpret_cast<const uint4 *>(p)); }
 
-// v[split][position][rank] = A[a] . x over the split's part of K. A block holds a tile of 16 MT rows and NB * 8 ranks;
-// its warps take 32 U of K in turn and add their sums in shared memory, in a fixed order.
-template <int DT, int MT, int NB, int U>
-__global__ void __launch_bounds__(32 * kWarps)
+// v[split][position][rank] = A[a] . x over the split's part of K. A block holds a tile of 16 MT RG rows and NB * 8 ranks;
+// the warps of a group of rows take 32 U of K in turn and add their sums in shared memory, in a fixed order.
+template <int DT, int MT, int RG, int NB, int U>
+__global__ void __launch_bounds__(32 * kWarps, 2)
     lora_shrink_kernel(const Tiles ts, const LoraArgs a, float *__restrict__ v) {
+  constexpr int KW = kWarps / RG;  // warps that share a group's K
   griddep_launch_dependents();
   griddep_wait();
   int key, row0, rows;
   if (!get_tile(ts, blockIdx.x, a.adapters, &key, &row0, &rows) || key < 0) return;
   const int rank = a.ranks ? min(max(a.ranks[key], 0), a.rank) : a.rank;
-  const int r0 = blockIdx.z * NB * 8;
-  if (r0 >= rank) return;  // (the second kernel reads no v at or past the adapter's rank)
+  const int n0 = blockIdx.z * NB * 8;
+  if (n0 >= rank) return;  // (the second kernel reads no v at or past the adapter's rank)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int kw = warp % KW, r0 = warp / KW * MT * 16;
   const int g = lane >> 2, t = lane & 3;
   const int K = static_cast<int>(a.K);
 
@@ -74,19 +76,20 @@ __global__ void __launch_bounds__(32 * kWarps)
   bool has[2 * MT];
 #pragma unroll
   for (int m = 0; m < 2 * MT; ++m) {
-    has[m] = m * 8 + g < rows;
-    xr[m] = static_cast<const uint16_t *>(a.x) + (has[m] ? row_at(ts, row0 + m * 8 + g) * a.ldx : 0);
+    const int r = r0 + m * 8 + g;
+    has[m] = r < rows;
+    xr[m] = static_cast<const uint16_t *>(a.x) + (has[m] ? row_at(ts, row0 + r) * a.ldx : 0);
   }
-  const uint16_t *ar = static_cast<const uint16_t *>(a.A) + (static_cast<int64_t>(key) * a.rank + r0 + g) * K;
+  const uint16_t *ar = static_cast<const uint16_t *>(a.A) + (static_cast<int64_t>(key) * a.rank + n0 + g) * K;
   bool live[NB];
 #pragma unroll
-  for (int n = 0; n < NB; ++n) live[n] = r0 + n * 8 + g < rank;
+  for (int n = 0; n < NB; ++n) live[n] = n0 + n * 8 + g < rank;
 
   float acc[MT][NB][4] = {};
   const int chunk = 32 * U;
-  const int step = chunk * kWarps * gridDim.y;
+  const int step = chunk * KW * gridDim.y;
   const uint4 zero = make_uint4(0, 0, 0, 0);
-  for (int k0 = (blockIdx.y * kWarps + warp) * chunk; k0 < K; k0 += step) {
+  for (int k0 = (blockIdx.y * KW + kw) * chunk; k0 < K; k0 += step) {
     uint4 xa[U][2 * MT], wb[U][NB];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -110,30 +113,31 @@ __global__ void __launch_bounds__(32 * kWarps)
         }
   }
 
-  // the upper half of the warps gives its sums to the lower half until one warp has them all
+  // the upper half of a group's warps gives its sums to the lower half until one warp has them all
   __shared__ float red[kWarps / 2][MT * NB * 4][32];
 #pragma unroll
-  for (int half = kWarps / 2; half > 0; half >>= 1) {
-    if (warp >= half && warp < 2 * half) {
+  for (int half = KW / 2; half > 0; half >>= 1) {
+    float(*slot)[32] = red[warp / KW * (KW / 2) + kw % half];
+    if (kw >= half && kw < 2 * half) {
 #pragma unroll
-      for (int i = 0; i < MT * NB * 4; ++i) red[warp - half][i][lane] = acc[i / (NB * 4)][i / 4 % NB][i % 4];
+      for (int i = 0; i < MT * NB * 4; ++i) slot[i][lane] = acc[i / (NB * 4)][i / 4 % NB][i % 4];
     }
     __syncthreads();
-    if (warp < half) {
+    if (kw < half) {
 #pragma unroll
-      for (int i = 0; i < MT * NB * 4; ++i) acc[i / (NB * 4)][i / 4 % NB][i % 4] += red[warp][i][lane];
+      for (int i = 0; i < MT * NB * 4; ++i) acc[i / (NB * 4)][i / 4 % NB][i % 4] += slot[i][lane];
     }
     __syncthreads();
   }
-  if (warp != 0) return;
+  if (kw != 0) return;
   float *vs = v + static_cast<int64_t>(blockIdx.y) * ts.T * a.rank;
 #pragma unroll
   for (int m = 0; m < 2 * MT; ++m) {
     if (!has[m]) continue;
-    float *row = vs + static_cast<int64_t>(row0 + m * 8 + g) * a.rank + r0 + 2 * t;
+    float *row = vs + static_cast<int64_t>(row0 + r0 + m * 8 + g) * a.rank + n0 + 2 * t;
 #pragma unroll
     for (int n = 0; n < NB; ++n)
-      if (r0 + n * 8 < a.rank)
+      if (n0 + n * 8 < a.rank)
         *reinterpret_cast<float2 *>(row + n * 8) = make_float2(acc[m / 2][n][2 * (m & 1)], acc[m / 2][n][2 * (m & 1) + 1]);
   }
 }
@@ -147,20 +151,37 @@ __device__ __forceinline__ void split_pair(float p, float q, uint32_t *hi, uint3
   *lo = out_bits2<DT>(isinf(ph) ? 0.0f : p - ph, isinf(qh) ? 0.0f : q - qh);
 }
 
-// Four values of B's row from rank place k on, as pairs; what lies at or past the adapter's rank is zero and not read.
-__device__ __forceinline__ uint2 load_b4(const uint16_t *row, int k, int rank) {
-  if (k + 4 <= rank) return __ldg(reinterpret_cast<const uint2 *>(row + k));
-  uint32_t e[4];
+// N consecutive values of B's row from rank place k on; what lies at or past the adapter's rank is zero and not read.
+template <int WORDS>
+__device__ __forceinline__ void load_b(const uint16_t *row, int k, int rank, uint32_t *w) {
+  if (k + 2 * WORDS <= rank) {
+    if (WORDS == 4) {
+      const uint4 v = ldg16(row + k);
+      w[0] = v.x, w[1] = v.y, w[2 % WORDS] = v.z, w[3 % WORDS] = v.w;
+    } else {
+      const uint2 v = __ldg(reinterpret_cast<const uint2 *>(row + k));
+      w[0] = v.x, w[1] = v.y;
+    }
+    return;
+  }
 #pragma unroll
-  for (int i = 0; i < 4; ++i) e[i] = k + i < rank ? row[k + i] : 0u;
-  return make_uint2(e[0] | e[1] << 16, e[2] | e[3] << 16);
+  for (int i = 0; i < WORDS; ++i)
+    w[i] = (k + 2 * i < rank ? row[k + 2 * i] : 0u) | (k + 2 * i + 1 < rank ? row[k + 2 * i + 1] : 0u) << 16;
 }
 
-// y = base + scaling * B[a] . v for a tile of 16 MT rows. A warp takes 32 columns of y at a time: four products whose
-// columns are dealt so that lane t holds the eight from 8 t on.
-template <int DT, int MT, int KB>
-__global__ void __launch_bounds__(32 * kWarps)
-    lora_expand_kernel(const Tiles ts, const LoraArgs a, const float *__restrict__ v, int splits, int vec) {
+// y = base + scaling * B[a] . v for a tile of 16 RW rows: warp (w % RW, w / RW) has 16 rows and every CW-th stretch of 32
+// columns, four products whose columns are dealt so that lane t holds the eight from 8 t on. WIDE: rows of y and base
+// are 16-byte aligned; else a stretch goes through shared memory, so that a warp writes consecutive columns of a row
+// (rows of odd length: 55 -> 16 us at 1501 x 4099 against two-byte accesses 16 bytes apart).
+template <int DT, int RW, int KB, bool WIDE>
+__global__ void __launch_bounds__(32 * kWarps, KB <= 2 ? 3 : KB <= 4 ? 2 : 1)
+    lora_expand_kernel(const Tiles ts, const LoraArgs a, const float *__restrict__ v, int splits) {
+  constexpr int CW = kWarps / RW;
+  constexpr int kLd = KB * 16 + 4;
+  constexpr int P = KB == 1 ? 1 : KB / 2;      // loads of B a product
+  constexpr int WORDS = KB == 1 ? 2 : 4;       // 32-bit words of each
+  __shared__ float vs[16 * RW][kLd];
+  __shared__ float stage[WIDE ? 1 : kWarps][WIDE ? 1 : 16][33];
   griddep_launch_dependents();
   griddep_wait();
   int key, row0, rows;
@@ -170,43 +191,54 @@ __global__ void __launch_bounds__(32 * kWarps)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
   const int N = static_cast<int>(a.N);
+
+  // the tile's v, added over the splits; zero past the rows and past the adapter's rank, whatever stands there
+  for (int i = threadIdx.x; i < 16 * RW * KB * 4; i += 32 * kWarps) {
+    const int row = i / (KB * 4), k = i % (KB * 4) * 4;
+    float4 p = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (row < rows && k < rank) {
+      const float *at = v + (static_cast<int64_t>(row0) + row) * a.rank + k;
+      for (int s0 = 0; s0 < splits; s0 += 4) {
+        float4 q[4];
+#pragma unroll
+        for (int s = 0; s < 4; ++s)
+          q[s] = s0 + s < splits ? __ldg(reinterpret_cast<const float4 *>(at + static_cast<int64_t>(s0 + s) * ts.T * a.rank))
+                                 : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+          p.x += q[s].x;
+          p.y += q[s].y;
+          p.z += q[s].z;
+          p.w += q[s].w;
+        }
+      }
+      if (k + 1 >= rank) p.y = 0.0f;
+      if (k + 2 >= rank) p.z = 0.0f;
+      if (k + 3 >= rank) p.w = 0.0f;
+    }
+    *reinterpret_cast<float4 *>(&vs[row][k]) = p;
+  }
+  __syncthreads();
+  const int r0 = warp % RW * 16;
+  if (r0 >= rows) return;
   const float scale = key >= 0 && a.scaling ? a.scaling[key] : 1.0f;
 
-  int64_t yr[2 * MT], br[2 * MT];  // the rows' first values in y and base
-  bool has[2 * MT];
-  float mul[2 * MT];
-  uint32_t hi[MT][KB][4], lo[MT][KB][4];
+  int64_t yr[2], br[2];  // the rows' first values in y and base
+  bool has[2];
+  float mul[2];
+  uint32_t hi[KB][4], lo[KB][4];
 #pragma unroll
-  for (int m = 0; m < 2 * MT; ++m) {
-    has[m] = m * 8 + g < rows;
-    const int64_t row = has[m] ? row_at(ts, row0 + m * 8 + g) : 0;
+  for (int m = 0; m < 2; ++m) {
+    const int r = r0 + m * 8 + g;
+    has[m] = r < rows;
+    const int64_t row = has[m] ? row_at(ts, row0 + r) : 0;
     yr[m] = row * a.ldy;
     br[m] = row * a.ldbase;
-    float4 p[KB];
-    float top = 0.0f;
-#pragma unroll
-    for (int b = 0; b < KB; ++b) {
-      p[b] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      const int k = b * 16 + t * 4;
-      if (has[m] && k < rank) {
-        for (int s = 0; s < splits; ++s) {
-          const float4 q = __ldg(reinterpret_cast<const float4 *>(
-              v + (static_cast<int64_t>(s) * ts.T + row0 + m * 8 + g) * a.rank + k));
-          p[b].x += q.x;
-          p[b].y += q.y;
-          p[b].z += q.z;
-          p[b].w += q.w;
-        }
-        // v past the adapter's rank is zero, whatever stands there
-        if (k + 1 >= rank) p[b].y = 0.0f;
-        if (k + 2 >= rank) p[b].z = 0.0f;
-        if (k + 3 >= rank) p[b].w = 0.0f;
-      }
-      top = fmaxf(top, fmaxf(fmaxf(fabsf(p[b].x), fabsf(p[b].y)), fmaxf(fabsf(p[b].z), fabsf(p[b].w))));
-    }
-    mul[m] = scale;
     float down = 1.0f;
+    mul[m] = scale;
     if (DT == kDtypeF16) {
+      float top = 0.0f;
+      for (int k = t; k < KB * 16; k += 4) top = fmaxf(top, fabsf(vs[r][k]));
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
       // 2^e <= top < 2^(e + 1), e kept where 2^e and 2^-e are normal: the row divided by 2^e has its largest in [1, 2)
@@ -218,67 +250,98 @@ __global__ void __launch_bounds__(32 * kWarps)
     }
 #pragma unroll
     for (int b = 0; b < KB; ++b) {
-      split_pair<DT>(p[b].x * down, p[b].y * down, &hi[m / 2][b][m & 1], &lo[m / 2][b][m & 1]);
-      split_pair<DT>(p[b].z * down, p[b].w * down, &hi[m / 2][b][2 + (m & 1)], &lo[m / 2][b][2 + (m & 1)]);
+      // the lane's four k of product b: the half of its load of B
+      const int k = KB == 1 ? 4 * t : 32 * (b / 2) + 8 * t + 4 * (b % 2);
+      const float4 p = *reinterpret_cast<const float4 *>(&vs[r][k]);
+      split_pair<DT>(p.x * down, p.y * down, &hi[b][m], &lo[b][m]);
+      split_pair<DT>(p.z * down, p.w * down, &hi[b][2 + m], &lo[b][2 + m]);
     }
   }
 
   const uint16_t *B = static_cast<const uint16_t *>(a.B) + static_cast<int64_t>(max(key, 0)) * N * a.rank;
   const uint16_t *base = static_cast<const uint16_t *>(a.base);
   uint16_t *y = static_cast<uint16_t *>(a.y);
-  for (int n0 = (blockIdx.y * kWarps + warp) * 32; n0 < N; n0 += gridDim.y * kWarps * 32) {
-    uint2 w[4][KB];
+  for (int n0 = (blockIdx.y * CW + warp / RW) * 32; n0 < N; n0 += gridDim.y * CW * 32) {
+    uint32_t w[4][P][WORDS];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int n = n0 + 8 * (g >> 1) + 2 * j + (g & 1);  // product j's column g
 #pragma unroll
-      for (int b = 0; b < KB; ++b) {
-        const int k = b * 16 + t * 4;
-        w[j][b] = n < N && k < rank ? load_b4(B + static_cast<int64_t>(n) * a.rank, k, rank) : make_uint2(0u, 0u);
+      for (int q = 0; q < P; ++q) {
+        const int k = q * 32 + t * 2 * WORDS;
+#pragma unroll
+        for (int i = 0; i < WORDS; ++i) w[j][q][i] = 0u;
+        if (n < N && k < rank) load_b<WORDS>(B + static_cast<int64_t>(n) * a.rank, k, rank, w[j][q]);
       }
     }
     const int n = n0 + 8 * t;
-    const bool wide = vec && n + 8 <= N;
-    uint4 old[2 * MT];
+    uint4 old[2];
+    uint16_t few[16];
+    if (WIDE) {
 #pragma unroll
-    for (int m = 0; m < 2 * MT; ++m) {
-      old[m] = make_uint4(0u, 0u, 0u, 0u);
-      if (!base || !has[m] || n >= N) continue;
-      if (wide) {
-        old[m] = *reinterpret_cast<const uint4 *>(base + br[m] + n);
-      } else {
-        uint32_t e[8];
+      for (int m = 0; m < 2; ++m) {
+        old[m] = make_uint4(0u, 0u, 0u, 0u);
+        if (!base || !has[m]) continue;
+        if (n + 8 <= N) {
+          old[m] = *reinterpret_cast<const uint4 *>(base + br[m] + n);
+        } else {
+          uint32_t e[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) e[i] = n + i < N ? base[br[m] + n + i] : 0u;
-        old[m] = make_uint4(e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16);
+          for (int i = 0; i < 8; ++i) e[i] = n + i < N ? base[br[m] + n + i] : 0u;
+          old[m] = make_uint4(e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const int64_t at = __shfl_sync(0xffffffffu, br[i / 8], i % 8 * 4);
+        few[i] = base && r0 + i < rows && n0 + lane < N ? base[at + n0 + lane] : 0;
       }
     }
-    float acc[MT][4][4] = {};
+    float acc[4][4] = {};
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
+    for (int j = 0; j < 4; ++j)
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-#pragma unroll
-        for (int b = 0; b < KB; ++b) {
-          mma_16816<DT>(acc[m][j], lo[m][b][0], lo[m][b][1], lo[m][b][2], lo[m][b][3], w[j][b].x, w[j][b].y);
-          mma_16816<DT>(acc[m][j], hi[m][b][0], hi[m][b][1], hi[m][b][2], hi[m][b][3], w[j][b].x, w[j][b].y);
-        }
-#pragma unroll
-    for (int m = 0; m < 2 * MT; ++m) {
-      if (!has[m] || n >= N) continue;
-      uint32_t out[4] = {old[m].x, old[m].y, old[m].z, old[m].w};
-      if (key >= 0) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          out[j] = out_bits2<DT>(value_f32<DT>(out[j] & 0xffffu) + mul[m] * acc[m / 2][j][2 * (m & 1)],
-                                 value_f32<DT>(out[j] >> 16) + mul[m] * acc[m / 2][j][2 * (m & 1) + 1]);
+      for (int b = 0; b < KB; ++b) {
+        const uint32_t b0 = w[j][KB == 1 ? 0 : b / 2][KB == 1 ? 0 : 2 * (b % 2)];
+        const uint32_t b1 = w[j][KB == 1 ? 0 : b / 2][KB == 1 ? 1 : 2 * (b % 2) + 1];
+        mma_16816<DT>(acc[j], lo[b][0], lo[b][1], lo[b][2], lo[b][3], b0, b1);
+        mma_16816<DT>(acc[j], hi[b][0], hi[b][1], hi[b][2], hi[b][3], b0, b1);
       }
-      if (wide) {
-        *reinterpret_cast<uint4 *>(y + yr[m] + n) = make_uint4(out[0], out[1], out[2], out[3]);
-      } else {
+    if (WIDE) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (n + i < N) y[yr[m] + n + i] = static_cast<uint16_t>(out[i / 2] >> (16 * (i & 1)));
+      for (int m = 0; m < 2; ++m) {
+        if (!has[m] || n >= N) continue;
+        uint32_t out[4] = {old[m].x, old[m].y, old[m].z, old[m].w};
+        if (key >= 0) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            out[j] = out_bits2<DT>(value_f32<DT>(out[j] & 0xffffu) + mul[m] * acc[j][2 * m],
+                                   value_f32<DT>(out[j] >> 16) + mul[m] * acc[j][2 * m + 1]);
+        }
+        if (n + 8 <= N) {
+          *reinterpret_cast<uint4 *>(y + yr[m] + n) = make_uint4(out[0], out[1], out[2], out[3]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (n + i < N) y[yr[m] + n + i] = static_cast<uint16_t>(out[i / 2] >> (16 * (i & 1)));
+        }
+      }
+    } else {
+      __syncwarp();
+#pragma unroll
+      for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          stage[warp][m * 8 + g][8 * t + 2 * j] = mul[m] * acc[j][2 * m];
+          stage[warp][m * 8 + g][8 * t + 2 * j + 1] = mul[m] * acc[j][2 * m + 1];
+        }
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const int64_t at = __shfl_sync(0xffffffffu, yr[i / 8], i % 8 * 4);
+        if (r0 + i < rows && n0 + lane < N)
+          y[at + n0 + lane] = key >= 0 ? out_bits<DT>(value_f32<DT>(few[i]) + stage[warp][i][lane]) : few[i];
       }
     }
   }
@@ -287,14 +350,16 @@ __global__ void __launch_bounds__(32 * kWarps)
 // The launch's shape, and the workspace's: [v][perm][tiles][ntiles].
 struct LoraPlan {
   bool direct;
-  int tile, max_tiles, splits;
+  int rw, tile, max_tiles, splits;
   size_t perm, tiles, ntiles, bytes;
 };
 
 LoraPlan lora_plan(int64_t T, int64_t N, int64_t K, int adapters, int rank, int num_sms) {
   LoraPlan p;
   p.direct = T <= kDirectRows;
-  p.tile = rank > 64 ? 16 : 32;
+  // rows a tile: 16 for a few rows an adapter, more where an adapter's rows fill them (its weights are then read less)
+  p.rw = p.direct || T < 32 * adapters ? 1 : T < 128 * adapters ? 2 : 4;
+  p.tile = 16 * p.rw;
   p.max_tiles = static_cast<int>(p.direct ? T : max_row_tiles(T, adapters, p.tile));
   // few tiles: the blocks of one tile split K, no finer than one turn of a block's warps (32 K values each)
   const int64_t turns = cdiv(K, 32 * kWarps);
@@ -308,36 +373,42 @@ LoraPlan lora_plan(int64_t T, int64_t N, int64_t K, int adapters, int rank, int 
   return p;
 }
 
-template <int DT, int MT>
-cudaError_t launch_mt(const Tiles &ts, const LoraArgs &a, const LoraPlan &p, float *v, int num_sms, cudaStream_t stream) {
-  auto shrink = a.rank <= 8    ? lora_shrink_kernel<DT, MT, 1, 4>
-                : a.rank <= 16 ? lora_shrink_kernel<DT, MT, 2, 4>
-                : a.rank <= 32 ? lora_shrink_kernel<DT, MT, 4, 2>
-                               : lora_shrink_kernel<DT, MT, 8, 1>;
-  const int vec = a.ldy % 8 == 0 && reinterpret_cast<uintptr_t>(a.y) % 16 == 0 &&
-                  (!a.base || (a.ldbase % 8 == 0 && reinterpret_cast<uintptr_t>(a.base) % 16 == 0));
+template <typename... Args>
+cudaError_t launch_grid(void (*kern)(Args...), dim3 grid, cudaStream_t stream, Args... args) {
   cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(32 * kWarps);
+  cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  cfg.stream = stream;
-  cfg.blockDim = dim3(32 * kWarps);
-  cfg.gridDim = dim3(p.max_tiles, p.splits, a.rank > 64 ? 2 : 1);
-  cudaError_t e = cudaLaunchKernelEx(&cfg, shrink, ts, a, v);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, args...);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+template <int DT, int RW>
+cudaError_t launch_rw(const Tiles &ts, const LoraArgs &a, const LoraPlan &p, float *v, int num_sms, cudaStream_t stream) {
+  constexpr int MT = RW == 1 ? 1 : 2;
+  constexpr int RG = RW == 4 ? 2 : 1;
+  auto shrink = a.rank <= 8    ? lora_shrink_kernel<DT, MT, RG, 1, 4>
+                : a.rank <= 16 ? lora_shrink_kernel<DT, MT, RG, 2, 4>
+                : a.rank <= 32 ? lora_shrink_kernel<DT, MT, RG, 4, 2>
+                               : lora_shrink_kernel<DT, MT, RG, 8, 1>;
+  cudaError_t e = launch_grid(shrink, dim3(p.max_tiles, p.splits, a.rank > 64 ? 2 : 1), stream, ts, a, v);
   if (e != cudaSuccess) return e;
-  // columns: enough blocks for the device, no more than one turn of a block's warps each
-  const int64_t turns = cdiv(a.N, 32 * kWarps);
-  const int64_t want = cdiv(4 * num_sms, p.max_tiles);
-  cfg.gridDim = dim3(p.max_tiles, static_cast<unsigned>(turns < want ? turns : want), 1);
-  auto expand = a.rank <= 16   ? lora_expand_kernel<DT, MT, 1>
-                : a.rank <= 32 ? lora_expand_kernel<DT, MT, 2>
-                : a.rank <= 64 ? lora_expand_kernel<DT, MT, 4>
-                               : lora_expand_kernel<DT, 1, 8>;
-  e = cudaLaunchKernelEx(&cfg, expand, ts, a, static_cast<const float *>(v), p.splits, vec);
-  if (e != cudaSuccess) return e;
-  return cudaGetLastError();
+  const bool wide = a.ldy % 8 == 0 && reinterpret_cast<uintptr_t>(a.y) % 16 == 0 &&
+                    (!a.base || (a.ldbase % 8 == 0 && reinterpret_cast<uintptr_t>(a.base) % 16 == 0));
+  auto expand = a.rank <= 16   ? (wide ? lora_expand_kernel<DT, RW, 1, true> : lora_expand_kernel<DT, RW, 1, false>)
+                : a.rank <= 32 ? (wide ? lora_expand_kernel<DT, RW, 2, true> : lora_expand_kernel<DT, RW, 2, false>)
+                : a.rank <= 64 ? (wide ? lora_expand_kernel<DT, RW, 4, true> : lora_expand_kernel<DT, RW, 4, false>)
+                               : (wide ? lora_expand_kernel<DT, RW, 8, true> : lora_expand_kernel<DT, RW, 8, false>);
+  // columns: enough blocks to fill the device a few times over, no more than one turn of a block's warps each
+  const int64_t turns = cdiv(a.N, 32 * kWarps / RW);
+  const int64_t want = cdiv(12 * num_sms, p.max_tiles);
+  return launch_grid(expand, dim3(p.max_tiles, static_cast<unsigned>(turns < want ? turns : want)), stream, ts, a,
+                     static_cast<const float *>(v), p.splits);
 }
 
 }  // namespace
@@ -361,12 +432,13 @@ cudaError_t launch_lora(const LoraArgs &a, void *workspace, int num_sms, cudaStr
     if (e != cudaSuccess) return e;
   }
   float *v = reinterpret_cast<float *>(ws);
-  const bool small = p.direct || p.tile == 16;
   if (a.dtype == kDtypeBf16)
-    return small ? launch_mt<kDtypeBf16, 1>(ts, a, p, v, num_sms, stream)
-                 : launch_mt<kDtypeBf16, 2>(ts, a, p, v, num_sms, stream);
-  return small ? launch_mt<kDtypeF16, 1>(ts, a, p, v, num_sms, stream)
-               : launch_mt<kDtypeF16, 2>(ts, a, p, v, num_sms, stream);
+    return p.rw == 1   ? launch_rw<kDtypeBf16, 1>(ts, a, p, v, num_sms, stream)
+           : p.rw == 2 ? launch_rw<kDtypeBf16, 2>(ts, a, p, v, num_sms, stream)
+                       : launch_rw<kDtypeBf16, 4>(ts, a, p, v, num_sms, stream);
+  return p.rw == 1   ? launch_rw<kDtypeF16, 1>(ts, a, p, v, num_sms, stream)
+         : p.rw == 2 ? launch_rw<kDtypeF16, 2>(ts, a, p, v, num_sms, stream)
+                     : launch_rw<kDtypeF16, 4>(ts, a, p, v, num_sms, stream);
 }
 
 }  // namespace w4
