@@ -52,10 +52,17 @@ __device__ __forceinline__ bool get_tile(const Tiles &ts, int i, int adapters, i
 
 __device__ __forceinline__ int64_t row_at(const Tiles &ts, int pos) { return ts.direct ? pos : ts.plan.perm[pos]; }
 
+__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+
 __device__ __forceinline__ uint4 ldg16(const uint16_t *p) { return __ldg(reinterpret_cast<const uint4 *>(p)); }
 
-// v[split][position][rank] = A[a] . x over the split's part of K. A block holds a tile of 16 MT RG rows and NB * 8 ranks;
-// the warps of a group of rows take 32 U of K in turn and add their sums in shared memory, in a fixed order.
+// v[position][rank] = A[a] . x. A block holds a tile of 16 MT RG rows and NB * 8 ranks; the warps of a group of rows take
+// 32 U of K in turn and add their sums in shared memory, in a fixed order. Where tiles are few the blocks of a cluster
+// split K and add theirs through distributed shared memory, each a part of the tile, in the order of their ranks.
 template <int DT, int MT, int RG, int NB, int U>
 __global__ void __launch_bounds__(32 * kWarps, 2)
     lora_shrink_kernel(const Tiles ts, const LoraArgs a, float *__restrict__ v) {
@@ -129,17 +136,39 @@ __global__ void __launch_bounds__(32 * kWarps, 2)
     }
     __syncthreads();
   }
-  if (kw != 0) return;
-  float *vs = v + static_cast<int64_t>(blockIdx.y) * ts.T * a.rank;
+  const int C = gridDim.y;  // blocks of the cluster
+  if (C == 1) {
+    if (kw != 0) return;
 #pragma unroll
-  for (int m = 0; m < 2 * MT; ++m) {
-    if (!has[m]) continue;
-    float *row = vs + static_cast<int64_t>(row0 + r0 + m * 8 + g) * a.rank + n0 + 2 * t;
+    for (int m = 0; m < 2 * MT; ++m) {
+      if (!has[m]) continue;
+      float *row = v + static_cast<int64_t>(row0 + r0 + m * 8 + g) * a.rank + n0 + 2 * t;
 #pragma unroll
-    for (int n = 0; n < NB; ++n)
-      if (n0 + n * 8 < a.rank)
-        *reinterpret_cast<float2 *>(row + n * 8) = make_float2(acc[m / 2][n][2 * (m & 1)], acc[m / 2][n][2 * (m & 1) + 1]);
+      for (int n = 0; n < NB; ++n)
+        if (n0 + n * 8 < a.rank)
+          *reinterpret_cast<float2 *>(row + n * 8) = make_float2(acc[m / 2][n][2 * (m & 1)], acc[m / 2][n][2 * (m & 1) + 1]);
+    }
+    return;
   }
+  float *part = &red[0][0][0];  // [row of the tile][NB * 8]
+  static_assert(16 * MT * RG * NB * 8 <= kWarps / 2 * MT * NB * 4 * 32, "the tile's sums fit");
+  if (kw == 0) {
+#pragma unroll
+    for (int m = 0; m < 2 * MT; ++m)
+#pragma unroll
+      for (int n = 0; n < NB; ++n)
+        *reinterpret_cast<float2 *>(part + (r0 + m * 8 + g) * NB * 8 + n * 8 + 2 * t) =
+            make_float2(acc[m / 2][n][2 * (m & 1)], acc[m / 2][n][2 * (m & 1) + 1]);
+  }
+  cluster_sync_all();
+  for (int i = threadIdx.x + 32 * kWarps * blockIdx.y; i < rows * NB * 8; i += 32 * kWarps * C) {
+    const int n = n0 + i % (NB * 8);
+    if (n >= a.rank) continue;
+    float sum = 0.0f;
+    for (int c = 0; c < C; ++c) sum += ld_cluster_f32(mapa_shared(smem_u32(part + i), c));
+    v[static_cast<int64_t>(row0 + i / (NB * 8)) * a.rank + n] = sum;
+  }
+  cluster_sync_all();  // no block leaves while another reads its sums
 }
 
 // Two values as the type's nearest (hi) and what that leaves (lo), each as a pair of 16-bit values. What an infinity
@@ -169,19 +198,38 @@ __device__ __forceinline__ void load_b(const uint16_t *row, int k, int rank, uin
     w[i] = (k + 2 * i < rank ? row[k + 2 * i] : 0u) | (k + 2 * i + 1 < rank ? row[k + 2 * i + 1] : 0u) << 16;
 }
 
+constexpr int kAhead = 4;  // stretches of base that a warp has in flight
+
+// Values n and n + 1 of a row at p, which is 4-byte aligned if `pair` (and both are below N).
+__device__ __forceinline__ uint32_t load_two(const uint16_t *p, int n, int N, bool pair) {
+  if (pair && n + 1 < N) return *reinterpret_cast<const uint32_t *>(p + n);
+  return (n >= 0 && n < N ? p[n] : 0u) | (n + 1 < N ? p[n + 1] : 0u) << 16;
+}
+__device__ __forceinline__ void store_two(uint16_t *p, int n, int N, bool pair, uint32_t v) {
+  if (pair && n + 1 < N) {
+    *reinterpret_cast<uint32_t *>(p + n) = v;
+    return;
+  }
+  if (n >= 0 && n < N) p[n] = static_cast<uint16_t>(v);
+  if (n + 1 < N) p[n + 1] = static_cast<uint16_t>(v >> 16);
+}
+
 // y = base + scaling * B[a] . v for a tile of 16 RW rows: warp (w % RW, w / RW) has 16 rows and every CW-th stretch of 32
 // columns, four products whose columns are dealt so that lane t holds the eight from 8 t on. WIDE: rows of y and base
-// are 16-byte aligned; else a stretch goes through shared memory, so that a warp writes consecutive columns of a row
-// (rows of odd length: 55 -> 16 us at 1501 x 4099 against two-byte accesses 16 bytes apart).
+// are 16-byte aligned, and base's next stretches are copied ahead to shared memory (one stretch at a time in registers
+// kept too few bytes in flight: 3.6 TB/s). Else (rows of odd length) the sums of two stretches go through shared memory,
+// so that a warp reads and writes 64 consecutive columns of a row, in pairs from the row's first 4-byte boundary.
 template <int DT, int RW, int KB, bool WIDE>
-__global__ void __launch_bounds__(32 * kWarps, KB <= 2 ? 3 : KB <= 4 ? 2 : 1)
-    lora_expand_kernel(const Tiles ts, const LoraArgs a, const float *__restrict__ v, int splits) {
+__global__ void __launch_bounds__(32 * kWarps, KB <= 2 ? 3 : (KB <= 4 && WIDE) ? 2 : 1)
+    lora_expand_kernel(const Tiles ts, const LoraArgs a, const float *__restrict__ v) {
   constexpr int CW = kWarps / RW;
   constexpr int kLd = KB * 16 + 4;
   constexpr int P = KB == 1 ? 1 : KB / 2;      // loads of B a product
   constexpr int WORDS = KB == 1 ? 2 : 4;       // 32-bit words of each
   __shared__ float vs[16 * RW][kLd];
-  __shared__ float stage[WIDE ? 1 : kWarps][WIDE ? 1 : 16][33];
+  // WIDE: base's stretches on their way, each lane's own 32 bytes of each; else a stretch of scaled sums
+  __shared__ __align__(16) uint4 ahead[WIDE ? kWarps : 1][WIDE ? kAhead : 1][WIDE ? 2 : 1][32];
+  __shared__ float stage[WIDE ? 1 : kWarps][WIDE ? 1 : 16][WIDE ? 1 : 66];
   griddep_launch_dependents();
   griddep_wait();
   int key, row0, rows;
@@ -192,26 +240,12 @@ __global__ void __launch_bounds__(32 * kWarps, KB <= 2 ? 3 : KB <= 4 ? 2 : 1)
   const int g = lane >> 2, t = lane & 3;
   const int N = static_cast<int>(a.N);
 
-  // the tile's v, added over the splits; zero past the rows and past the adapter's rank, whatever stands there
+  // the tile's v; zero past the rows and past the adapter's rank, whatever stands there
   for (int i = threadIdx.x; i < 16 * RW * KB * 4; i += 32 * kWarps) {
     const int row = i / (KB * 4), k = i % (KB * 4) * 4;
     float4 p = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     if (row < rows && k < rank) {
-      const float *at = v + (static_cast<int64_t>(row0) + row) * a.rank + k;
-      for (int s0 = 0; s0 < splits; s0 += 4) {
-        float4 q[4];
-#pragma unroll
-        for (int s = 0; s < 4; ++s)
-          q[s] = s0 + s < splits ? __ldg(reinterpret_cast<const float4 *>(at + static_cast<int64_t>(s0 + s) * ts.T * a.rank))
-                                 : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll
-        for (int s = 0; s < 4; ++s) {
-          p.x += q[s].x;
-          p.y += q[s].y;
-          p.z += q[s].z;
-          p.w += q[s].w;
-        }
-      }
+      p = __ldg(reinterpret_cast<const float4 *>(v + (static_cast<int64_t>(row0) + row) * a.rank + k));
       if (k + 1 >= rank) p.y = 0.0f;
       if (k + 2 >= rank) p.z = 0.0f;
       if (k + 3 >= rank) p.w = 0.0f;
@@ -261,7 +295,8 @@ __global__ void __launch_bounds__(32 * kWarps, KB <= 2 ? 3 : KB <= 4 ? 2 : 1)
   const uint16_t *B = static_cast<const uint16_t *>(a.B) + static_cast<int64_t>(max(key, 0)) * N * a.rank;
   const uint16_t *base = static_cast<const uint16_t *>(a.base);
   uint16_t *y = static_cast<uint16_t *>(a.y);
-  for (int n0 = (blockIdx.y * CW + warp / RW) * 32; n0 < N; n0 += gridDim.y * CW * 32) {
+  // four products of columns n0 .. n0 + 31
+  auto products = [&](int n0, float (&acc)[4][4]) {
     uint32_t w[4][P][WORDS];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -274,33 +309,10 @@ __global__ void __launch_bounds__(32 * kWarps, KB <= 2 ? 3 : KB <= 4 ? 2 : 1)
         if (n < N && k < rank) load_b<WORDS>(B + static_cast<int64_t>(n) * a.rank, k, rank, w[j][q]);
       }
     }
-    const int n = n0 + 8 * t;
-    uint4 old[2];
-    uint16_t few[16];
-    if (WIDE) {
 #pragma unroll
-      for (int m = 0; m < 2; ++m) {
-        old[m] = make_uint4(0u, 0u, 0u, 0u);
-        if (!base || !has[m]) continue;
-        if (n + 8 <= N) {
-          old[m] = *reinterpret_cast<const uint4 *>(base + br[m] + n);
-        } else {
-          uint32_t e[8];
+    for (int j = 0; j < 4; ++j) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) e[i] = n + i < N ? base[br[m] + n + i] : 0u;
-          old[m] = make_uint4(e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16);
-        }
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const int64_t at = __shfl_sync(0xffffffffu, br[i / 8], i % 8 * 4);
-        few[i] = base && r0 + i < rows && n0 + lane < N ? base[at + n0 + lane] : 0;
-      }
-    }
-    float acc[4][4] = {};
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
+      for (int i = 0; i < 4; ++i) acc[j][i] = 0.0f;
 #pragma unroll
       for (int b = 0; b < KB; ++b) {
         const uint32_t b0 = w[j][KB == 1 ? 0 : b / 2][KB == 1 ? 0 : 2 * (b % 2)];
@@ -308,11 +320,34 @@ __global__ void __launch_bounds__(32 * kWarps, KB <= 2 ? 3 : KB <= 4 ? 2 : 1)
         mma_16816<DT>(acc[j], lo[b][0], lo[b][1], lo[b][2], lo[b][3], b0, b1);
         mma_16816<DT>(acc[j], hi[b][0], hi[b][1], hi[b][2], hi[b][3], b0, b1);
       }
-    if (WIDE) {
+    }
+  };
+  constexpr int kCols = WIDE ? 32 : 64;
+  const int first = (blockIdx.y * CW + warp / RW) * kCols, step = gridDim.y * CW * kCols;
+  if (WIDE) {
+    auto fetch = [&](int n0, int slot) {
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        const int n = n0 + 8 * t;
+        const int bytes = base && has[m] && n < N ? min(2 * (N - n), 16) : 0;
+        cp_async16_zfill(smem_u32(&ahead[warp][slot][m][lane]), bytes ? base + br[m] + n : a.B, bytes);
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    int slot = 0;
+#pragma unroll
+    for (int i = 0; i < kAhead - 1; ++i) fetch(first + i * step, i);
+    for (int n0 = first; n0 < N; n0 += step) {
+      fetch(n0 + (kAhead - 1) * step, (slot + kAhead - 1) % kAhead);
+      float acc[4][4];
+      if (key >= 0) products(n0, acc);
+      asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
+      const int n = n0 + 8 * t;
 #pragma unroll
       for (int m = 0; m < 2; ++m) {
         if (!has[m] || n >= N) continue;
-        uint32_t out[4] = {old[m].x, old[m].y, old[m].z, old[m].w};
+        const uint4 old = ahead[warp][slot][m][lane];
+        uint32_t out[4] = {old.x, old.y, old.z, old.w};
         if (key >= 0) {
 #pragma unroll
           for (int j = 0; j < 4; ++j)
@@ -327,21 +362,65 @@ __global__ void __launch_bounds__(32 * kWarps, KB <= 2 ? 3 : KB <= 4 ? 2 : 1)
             if (n + i < N) y[yr[m] + n + i] = static_cast<uint16_t>(out[i / 2] >> (16 * (i & 1)));
         }
       }
-    } else {
+      slot = (slot + 1) % kAhead;
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+  } else {
+    for (int n0 = first; n0 < N; n0 += step) {
       __syncwarp();
 #pragma unroll
-      for (int m = 0; m < 2; ++m)
+      for (int h = 0; h < 2; ++h) {
+        float acc[4][4];
+        if (key >= 0) {
+          products(n0 + 32 * h, acc);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          stage[warp][m * 8 + g][8 * t + 2 * j] = mul[m] * acc[j][2 * m];
-          stage[warp][m * 8 + g][8 * t + 2 * j + 1] = mul[m] * acc[j][2 * m + 1];
+          for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              *reinterpret_cast<float2 *>(&stage[warp][m * 8 + g][32 * h + 8 * t + 2 * j]) =
+                  make_float2(mul[m] * acc[j][2 * m], mul[m] * acc[j][2 * m + 1]);
         }
+      }
       __syncwarp();
+      const int end = min(N, n0 + 64);
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const int64_t at = __shfl_sync(0xffffffffu, yr[i / 8], i % 8 * 4);
-        if (r0 + i < rows && n0 + lane < N)
-          y[at + n0 + lane] = key >= 0 ? out_bits<DT>(value_f32<DT>(few[i]) + stage[warp][i][lane]) : few[i];
+      for (int i0 = 0; i0 < 16; i0 += 8) {
+        uint32_t old[8];
+        const uint16_t *bp[8];
+        uint16_t *yp[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          bp[i] = base + __shfl_sync(0xffffffffu, br[i0 / 8], i * 4);
+          yp[i] = y + __shfl_sync(0xffffffffu, yr[i0 / 8], i * 4);
+          // pairs start at the row's 4-byte boundary; the value before it takes the place of the pair past the end
+          const int odd = (reinterpret_cast<uintptr_t>(yp[i] + n0) >> 1) & 1;
+          const int n = n0 + 2 * lane - odd;
+          const bool pair = ((reinterpret_cast<uintptr_t>(bp[i]) ^ reinterpret_cast<uintptr_t>(yp[i])) & 2) == 0;
+          old[i] = 0u;
+          if (base && r0 + i0 + i < rows) {
+            if (n >= n0)
+              old[i] = load_two(bp[i], n, end, pair);
+            else
+              old[i] = (n0 + 63 < end ? bp[i][n0 + 63] : 0u) | static_cast<uint32_t>(bp[i][n0]) << 16;
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          if (r0 + i0 + i >= rows) continue;
+          const int odd = (reinterpret_cast<uintptr_t>(yp[i] + n0) >> 1) & 1;
+          const int c = 2 * lane - odd;
+          uint32_t out = old[i];
+          if (key >= 0) {
+            const float *sums = stage[warp][i0 + i];
+            out = out_bits2<DT>(value_f32<DT>(out & 0xffffu) + sums[c < 0 ? 63 : c], value_f32<DT>(out >> 16) + sums[c + 1]);
+          }
+          if (c >= 0) {
+            store_two(yp[i], n0 + c, end, true, out);
+          } else {
+            if (n0 + 63 < end) yp[i][n0 + 63] = static_cast<uint16_t>(out);
+            yp[i][n0] = static_cast<uint16_t>(out >> 16);
+          }
+        }
       }
     }
   }
@@ -361,12 +440,14 @@ LoraPlan lora_plan(int64_t T, int64_t N, int64_t K, int adapters, int rank, int 
   p.rw = p.direct || T < 32 * adapters ? 1 : T < 128 * adapters ? 2 : 4;
   p.tile = 16 * p.rw;
   p.max_tiles = static_cast<int>(p.direct ? T : max_row_tiles(T, adapters, p.tile));
-  // few tiles: the blocks of one tile split K, no finer than one turn of a block's warps (32 K values each)
+  // few tiles: the blocks of a cluster split a tile's K, no finer than one turn of a block's warps (32 K values each)
   const int64_t turns = cdiv(K, 32 * kWarps);
-  const int64_t want = cdiv(2 * num_sms, p.max_tiles < 1 ? 1 : p.max_tiles);
-  p.splits = static_cast<int>(want < turns ? (want < 8 ? want : 8) : (turns < 8 ? turns : 8));
+  // (two blocks an SM run at a time: as many blocks as fit at once, since one more would wait for a whole turn)
+  const int64_t want = 2 * num_sms / p.max_tiles;
+  const int64_t splits = want < turns ? want : turns;
+  p.splits = static_cast<int>(splits < 1 ? 1 : splits < 8 ? splits : 8);
   auto up = [](size_t v) { return (v + 255) / 256 * 256; };
-  p.perm = up(static_cast<size_t>(p.splits) * T * rank * 4);
+  p.perm = up(static_cast<size_t>(T) * rank * 4);
   p.tiles = p.perm + (p.direct ? 0 : up(static_cast<size_t>(T) * 4));
   p.ntiles = p.tiles + (p.direct ? 0 : up(static_cast<size_t>(p.max_tiles) * sizeof(RowTile)));
   p.bytes = p.ntiles + 256;
@@ -374,16 +455,18 @@ LoraPlan lora_plan(int64_t T, int64_t N, int64_t K, int adapters, int rank, int 
 }
 
 template <typename... Args>
-cudaError_t launch_grid(void (*kern)(Args...), dim3 grid, cudaStream_t stream, Args... args) {
+cudaError_t launch_grid(void (*kern)(Args...), dim3 grid, int cluster, cudaStream_t stream, Args... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(32 * kWarps);
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim = {1, static_cast<unsigned>(cluster), 1};
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, args...);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
@@ -396,7 +479,7 @@ cudaError_t launch_rw(const Tiles &ts, const LoraArgs &a, const LoraPlan &p, flo
                 : a.rank <= 16 ? lora_shrink_kernel<DT, MT, RG, 2, 4>
                 : a.rank <= 32 ? lora_shrink_kernel<DT, MT, RG, 4, 2>
                                : lora_shrink_kernel<DT, MT, RG, 8, 1>;
-  cudaError_t e = launch_grid(shrink, dim3(p.max_tiles, p.splits, a.rank > 64 ? 2 : 1), stream, ts, a, v);
+  cudaError_t e = launch_grid(shrink, dim3(p.max_tiles, p.splits, a.rank > 64 ? 2 : 1), p.splits, stream, ts, a, v);
   if (e != cudaSuccess) return e;
   const bool wide = a.ldy % 8 == 0 && reinterpret_cast<uintptr_t>(a.y) % 16 == 0 &&
                     (!a.base || (a.ldbase % 8 == 0 && reinterpret_cast<uintptr_t>(a.base) % 16 == 0));
@@ -404,11 +487,11 @@ cudaError_t launch_rw(const Tiles &ts, const LoraArgs &a, const LoraPlan &p, flo
                 : a.rank <= 32 ? (wide ? lora_expand_kernel<DT, RW, 2, true> : lora_expand_kernel<DT, RW, 2, false>)
                 : a.rank <= 64 ? (wide ? lora_expand_kernel<DT, RW, 4, true> : lora_expand_kernel<DT, RW, 4, false>)
                                : (wide ? lora_expand_kernel<DT, RW, 8, true> : lora_expand_kernel<DT, RW, 8, false>);
-  // columns: enough blocks to fill the device a few times over, no more than one turn of a block's warps each
-  const int64_t turns = cdiv(a.N, 32 * kWarps / RW);
-  const int64_t want = cdiv(12 * num_sms, p.max_tiles);
-  return launch_grid(expand, dim3(p.max_tiles, static_cast<unsigned>(turns < want ? turns : want)), stream, ts, a,
-                     static_cast<const float *>(v), p.splits);
+  // columns: blocks for the device a few times over, no more than one turn of a block's warps each
+  const int64_t turns = cdiv(a.N, (wide ? 32 : 64) * kWarps / RW);
+  const int64_t want = 3 * num_sms / p.max_tiles;
+  return launch_grid(expand, dim3(p.max_tiles, static_cast<unsigned>(want < 1 ? 1 : want < turns ? want : turns)), 1, stream,
+                     ts, a, static_cast<const float *>(v));
 }
 
 }  // namespace
