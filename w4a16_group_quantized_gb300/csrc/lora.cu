@@ -13,6 +13,8 @@
 // v stands in the second product as the sum of two 16-bit values, its rounding and what that left, which keeps about
 // twice the type's bits for one more product each (they are not what bounds the kernel). For fp16 a row of v is first
 // divided by a power of two, so that no v overflows the type.
+#include <atomic>
+
 #include "gemm_common.cuh"
 #include "internal.h"
 #include "mma.cuh"
@@ -180,38 +182,44 @@ __device__ __forceinline__ void split_pair(float p, float q, uint32_t *hi, uint3
   *lo = out_bits2<DT>(isinf(ph) ? 0.0f : p - ph, isinf(qh) ? 0.0f : q - qh);
 }
 
-// N consecutive values of B's row from rank place k on; what lies at or past the adapter's rank is zero and not read.
-template <int WORDS>
-__device__ __forceinline__ void load_b(const uint16_t *row, int k, int rank, uint32_t *w) {
-  if (k + 2 * WORDS <= rank) {
-    if (WORDS == 4) {
-      const uint4 v = ldg16(row + k);
-      w[0] = v.x, w[1] = v.y, w[2 % WORDS] = v.z, w[3 % WORDS] = v.w;
-    } else {
-      const uint2 v = __ldg(reinterpret_cast<const uint2 *>(row + k));
-      w[0] = v.x, w[1] = v.y;
-    }
-    return;
-  }
-#pragma unroll
-  for (int i = 0; i < WORDS; ++i)
-    w[i] = (k + 2 * i < rank ? row[k + 2 * i] : 0u) | (k + 2 * i + 1 < rank ? row[k + 2 * i + 1] : 0u) << 16;
+constexpr int kAhead = 4;   // stretches of base that a warp has in flight
+constexpr int kAheadB = 2;  // stretches of B
+
+// Asynchronous copy of BYTES (8 or 16), of which the first `have` are read and the rest is zero.
+template <int BYTES>
+__device__ __forceinline__ void copy_ahead(uint32_t to, const void *from, uint32_t have) {
+  if (BYTES == 16)
+    cp_async16_zfill(to, from, have);
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(to), "l"(from), "r"(have) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-constexpr int kAhead = 4;  // stretches of base that a warp has in flight
+// Shared memory of an expand block: v, then B's stretches and base's (or the sums of rows of odd length) of each warp.
+template <int RW, int KB, bool WIDE>
+struct Expand {
+  static constexpr int kLd = KB * 16 + 4;
+  static constexpr int P = KB == 1 ? 1 : KB / 2;  // loads of B a product: 8 bytes a lane at ranks up to 16, else 16
+  static constexpr int kLoad = KB == 1 ? 8 : 16;
+  static constexpr int kV = (16 * RW * kLd * 4 + 15) / 16 * 16;
+  static constexpr int kB = kAheadB * 4 * P * 32 * kLoad;
+  static constexpr int kLdSums = 66;
+  static constexpr int kBase = WIDE ? kAhead * 2 * 32 * 16 : 16 * kLdSums * 4;
+  static constexpr int kBytes = kV + kWarps * (kB + kBase);
+};
 
-// Values n and n + 1 of a row at p, which is 4-byte aligned if `pair` (and both are below N).
-__device__ __forceinline__ uint32_t load_two(const uint16_t *p, int n, int N, bool pair) {
-  if (pair && n + 1 < N) return *reinterpret_cast<const uint32_t *>(p + n);
-  return (n >= 0 && n < N ? p[n] : 0u) | (n + 1 < N ? p[n + 1] : 0u) << 16;
-}
-__device__ __forceinline__ void store_two(uint16_t *p, int n, int N, bool pair, uint32_t v) {
-  if (pair && n + 1 < N) {
+
+// Stores values n and n + 1 of a row (those that lie in 0 .. N - 1), p + n 4-byte aligned.
+__device__ __forceinline__ void store_two(uint16_t *p, int n, int N, uint32_t v) {
+  if (n + 1 < N) {
     *reinterpret_cast<uint32_t *>(p + n) = v;
     return;
   }
-  if (n >= 0 && n < N) p[n] = static_cast<uint16_t>(v);
-  if (n + 1 < N) p[n + 1] = static_cast<uint16_t>(v >> 16);
+  if (n < N) p[n] = static_cast<uint16_t>(v);
 }
 
 // y = base + scaling * B[a] . v for a tile of 16 RW rows: warp (w % RW, w / RW) has 16 rows and every CW-th stretch of 32
@@ -220,16 +228,13 @@ __device__ __forceinline__ void store_two(uint16_t *p, int n, int N, bool pair, 
 // kept too few bytes in flight: 3.6 TB/s). Else (rows of odd length) the sums of two stretches go through shared memory,
 // so that a warp reads and writes 64 consecutive columns of a row, in pairs from the row's first 4-byte boundary.
 template <int DT, int RW, int KB, bool WIDE>
-__global__ void __launch_bounds__(32 * kWarps, KB <= 2 ? 3 : (KB <= 4 && WIDE) ? 2 : 1)
+__global__ void __launch_bounds__(32 * kWarps, KB <= 2 && WIDE ? 3 : KB <= 4 ? 2 : 1)
     lora_expand_kernel(const Tiles ts, const LoraArgs a, const float *__restrict__ v) {
+  using E = Expand<RW, KB, WIDE>;
   constexpr int CW = kWarps / RW;
-  constexpr int kLd = KB * 16 + 4;
-  constexpr int P = KB == 1 ? 1 : KB / 2;      // loads of B a product
-  constexpr int WORDS = KB == 1 ? 2 : 4;       // 32-bit words of each
-  __shared__ float vs[16 * RW][kLd];
-  // WIDE: base's stretches on their way, each lane's own 32 bytes of each; else a stretch of scaled sums
-  __shared__ __align__(16) uint4 ahead[WIDE ? kWarps : 1][WIDE ? kAhead : 1][WIDE ? 2 : 1][32];
-  __shared__ float stage[WIDE ? 1 : kWarps][WIDE ? 1 : 16][WIDE ? 1 : 66];
+  constexpr int P = E::P, kLoad = E::kLoad, WORDS = kLoad / 4;
+  extern __shared__ __align__(16) uint8_t smem[];
+  float(*vs)[E::kLd] = reinterpret_cast<float(*)[E::kLd]>(smem);
   griddep_launch_dependents();
   griddep_wait();
   int key, row0, rows;
@@ -240,20 +245,24 @@ __global__ void __launch_bounds__(32 * kWarps, KB <= 2 ? 3 : (KB <= 4 && WIDE) ?
   const int g = lane >> 2, t = lane & 3;
   const int N = static_cast<int>(a.N);
 
+  const int r0 = warp % RW * 16;
+  int64_t row[2];  // read beside v
+#pragma unroll
+  for (int m = 0; m < 2; ++m) row[m] = r0 + m * 8 + g < rows ? row_at(ts, row0 + r0 + m * 8 + g) : 0;
+
   // the tile's v; zero past the rows and past the adapter's rank, whatever stands there
   for (int i = threadIdx.x; i < 16 * RW * KB * 4; i += 32 * kWarps) {
-    const int row = i / (KB * 4), k = i % (KB * 4) * 4;
+    const int r = i / (KB * 4), k = i % (KB * 4) * 4;
     float4 p = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    if (row < rows && k < rank) {
-      p = __ldg(reinterpret_cast<const float4 *>(v + (static_cast<int64_t>(row0) + row) * a.rank + k));
+    if (r < rows && k < rank) {
+      p = __ldg(reinterpret_cast<const float4 *>(v + (static_cast<int64_t>(row0) + r) * a.rank + k));
       if (k + 1 >= rank) p.y = 0.0f;
       if (k + 2 >= rank) p.z = 0.0f;
       if (k + 3 >= rank) p.w = 0.0f;
     }
-    *reinterpret_cast<float4 *>(&vs[row][k]) = p;
+    *reinterpret_cast<float4 *>(&vs[r][k]) = p;
   }
   __syncthreads();
-  const int r0 = warp % RW * 16;
   if (r0 >= rows) return;
   const float scale = key >= 0 && a.scaling ? a.scaling[key] : 1.0f;
 
@@ -265,9 +274,8 @@ __global__ void __launch_bounds__(32 * kWarps, KB <= 2 ? 3 : (KB <= 4 && WIDE) ?
   for (int m = 0; m < 2; ++m) {
     const int r = r0 + m * 8 + g;
     has[m] = r < rows;
-    const int64_t row = has[m] ? row_at(ts, row0 + r) : 0;
-    yr[m] = row * a.ldy;
-    br[m] = row * a.ldbase;
+    yr[m] = row[m] * a.ldy;
+    br[m] = row[m] * a.ldbase;
     float down = 1.0f;
     mul[m] = scale;
     if (DT == kDtypeF16) {
@@ -292,31 +300,48 @@ __global__ void __launch_bounds__(32 * kWarps, KB <= 2 ? 3 : (KB <= 4 && WIDE) ?
     }
   }
 
+  // each lane's own part of B's stretches, and of base's: nobody else reads what a lane copies
+  uint8_t *mine = smem + E::kV + warp * (E::kB + E::kBase);
+  const uint32_t b_at = smem_u32(mine) + lane * kLoad;
+  uint4 *const ahead = reinterpret_cast<uint4 *>(mine + E::kB) + lane;                       // WIDE
+  float(*sums)[E::kLdSums] = reinterpret_cast<float(*)[E::kLdSums]>(mine + E::kB);  // else
   const uint16_t *B = static_cast<const uint16_t *>(a.B) + static_cast<int64_t>(max(key, 0)) * N * a.rank;
   const uint16_t *base = static_cast<const uint16_t *>(a.base);
   uint16_t *y = static_cast<uint16_t *>(a.y);
-  // four products of columns n0 .. n0 + 31
-  auto products = [&](int n0, float (&acc)[4][4]) {
-    uint32_t w[4][P][WORDS];
+  auto fetch_b = [&](int n0, int slot) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int n = n0 + 8 * (g >> 1) + 2 * j + (g & 1);  // product j's column g
 #pragma unroll
       for (int q = 0; q < P; ++q) {
-        const int k = q * 32 + t * 2 * WORDS;
-#pragma unroll
-        for (int i = 0; i < WORDS; ++i) w[j][q][i] = 0u;
-        if (n < N && k < rank) load_b<WORDS>(B + static_cast<int64_t>(n) * a.rank, k, rank, w[j][q]);
+        const int k = q * (kLoad * 2) + t * (kLoad / 2);
+        const int have = n < N ? min(max(2 * (rank - k), 0), kLoad) : 0;
+        copy_ahead<kLoad>(b_at + (slot * 4 * P + j * P + q) * 32 * kLoad,
+                          have ? B + static_cast<int64_t>(n) * a.rank + k : a.B, have);
       }
     }
+  };
+  // four products of a stretch of 32 columns
+  auto products = [&](int slot, float (&acc)[4][4]) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
+      uint32_t w[P][WORDS];
+#pragma unroll
+      for (int q = 0; q < P; ++q) {
+        const uint32_t at = b_at + (slot * 4 * P + j * P + q) * 32 * kLoad;
+        if (kLoad == 16) {
+          const uint4 v4 = lds128(at);
+          w[q][0] = v4.x, w[q][1] = v4.y, w[q][2 % WORDS] = v4.z, w[q][3 % WORDS] = v4.w;
+        } else {
+          asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w[q][0]), "=r"(w[q][1]) : "r"(at) : "memory");
+        }
+      }
 #pragma unroll
       for (int i = 0; i < 4; ++i) acc[j][i] = 0.0f;
 #pragma unroll
       for (int b = 0; b < KB; ++b) {
-        const uint32_t b0 = w[j][KB == 1 ? 0 : b / 2][KB == 1 ? 0 : 2 * (b % 2)];
-        const uint32_t b1 = w[j][KB == 1 ? 0 : b / 2][KB == 1 ? 1 : 2 * (b % 2) + 1];
+        const uint32_t b0 = w[KB == 1 ? 0 : b / 2][KB == 1 ? 0 : 2 * (b % 2)];
+        const uint32_t b1 = w[KB == 1 ? 0 : b / 2][KB == 1 ? 1 : 2 * (b % 2) + 1];
         mma_16816<DT>(acc[j], lo[b][0], lo[b][1], lo[b][2], lo[b][3], b0, b1);
         mma_16816<DT>(acc[j], hi[b][0], hi[b][1], hi[b][2], hi[b][3], b0, b1);
       }
@@ -330,23 +355,31 @@ __global__ void __launch_bounds__(32 * kWarps, KB <= 2 ? 3 : (KB <= 4 && WIDE) ?
       for (int m = 0; m < 2; ++m) {
         const int n = n0 + 8 * t;
         const int bytes = base && has[m] && n < N ? min(2 * (N - n), 16) : 0;
-        cp_async16_zfill(smem_u32(&ahead[warp][slot][m][lane]), bytes ? base + br[m] + n : a.B, bytes);
+        cp_async16_zfill(smem_u32(ahead + (slot * 2 + m) * 32), bytes ? base + br[m] + n : a.B, bytes);
       }
-      asm volatile("cp.async.commit_group;" ::: "memory");
     };
+    // the groups of copies in order: base's first stretches, then with each of B's the base kAhead - kAheadB after it
     int slot = 0;
 #pragma unroll
-    for (int i = 0; i < kAhead - 1; ++i) fetch(first + i * step, i);
+    for (int i = 0; i < kAhead - kAheadB; ++i) fetch(first + i * step, i);
+#pragma unroll
+    for (int i = 0; i < kAheadB - 1; ++i) {
+      fetch_b(first + i * step, i);
+      fetch(first + (i + kAhead - kAheadB) * step, i + kAhead - kAheadB);
+      copies_commit();
+    }
     for (int n0 = first; n0 < N; n0 += step) {
+      fetch_b(n0 + (kAheadB - 1) * step, (slot + kAheadB - 1) % kAheadB);
       fetch(n0 + (kAhead - 1) * step, (slot + kAhead - 1) % kAhead);
+      copies_commit();
+      copies_wait<kAheadB - 1>();
       float acc[4][4];
-      if (key >= 0) products(n0, acc);
-      asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
+      if (key >= 0) products(slot % kAheadB, acc);
       const int n = n0 + 8 * t;
 #pragma unroll
       for (int m = 0; m < 2; ++m) {
         if (!has[m] || n >= N) continue;
-        const uint4 old = ahead[warp][slot][m][lane];
+        const uint4 old = ahead[(slot * 2 + m) * 32];
         uint32_t out[4] = {old.x, old.y, old.z, old.w};
         if (key >= 0) {
 #pragma unroll
@@ -364,66 +397,65 @@ __global__ void __launch_bounds__(32 * kWarps, KB <= 2 ? 3 : (KB <= 4 && WIDE) ?
       }
       slot = (slot + 1) % kAhead;
     }
-    asm volatile("cp.async.wait_all;" ::: "memory");
   } else {
+    fetch_b(first, 0);
+    copies_commit();
     for (int n0 = first; n0 < N; n0 += step) {
-      __syncwarp();
+      // base's pairs start at y's 4-byte boundary in the row; the value before it takes the place of the pair past the
+      // end. The loads are predicated, not branched around, and joined only after the products
+      const int end = min(N, n0 + 64);
+      uint32_t both[16], low[16], high[16];
 #pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const uint16_t *bp = base + __shfl_sync(0xffffffffu, br[i / 8], i % 8 * 4);
+        const uint16_t *yp = y + __shfl_sync(0xffffffffu, yr[i / 8], i % 8 * 4);
+        const int odd = (reinterpret_cast<uintptr_t>(yp + n0) >> 1) & 1;
+        const int n = n0 + 2 * lane - odd;
+        const int lo = n < n0 ? n0 + 63 : n;
+        const bool in = base && r0 + i < rows;
+        const bool pair = in && n >= n0 && n + 1 < end && (reinterpret_cast<uintptr_t>(bp + n) & 3) == 0;
+        both[i] = pair ? *reinterpret_cast<const uint32_t *>(bp + n) : 0u;
+        low[i] = in && !pair && lo < end ? bp[lo] : 0u;
+        high[i] = in && !pair && n + 1 < end ? bp[n + 1] : 0u;
+      }
+      __syncwarp();  // the stretch before has been read
+#pragma unroll 1
       for (int h = 0; h < 2; ++h) {
+        fetch_b(h == 0 ? n0 + 32 : n0 + step, 1 - h);
+        copies_commit();
+        copies_wait<1>();
+        if (key < 0) continue;
         float acc[4][4];
-        if (key >= 0) {
-          products(n0 + 32 * h, acc);
+        products(h, acc);
 #pragma unroll
-          for (int m = 0; m < 2; ++m)
+        for (int m = 0; m < 2; ++m)
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-              *reinterpret_cast<float2 *>(&stage[warp][m * 8 + g][32 * h + 8 * t + 2 * j]) =
-                  make_float2(mul[m] * acc[j][2 * m], mul[m] * acc[j][2 * m + 1]);
-        }
+          for (int j = 0; j < 4; ++j)
+            *reinterpret_cast<float2 *>(&sums[m * 8 + g][32 * h + 8 * t + 2 * j]) =
+                make_float2(mul[m] * acc[j][2 * m], mul[m] * acc[j][2 * m + 1]);
       }
       __syncwarp();
-      const int end = min(N, n0 + 64);
 #pragma unroll
-      for (int i0 = 0; i0 < 16; i0 += 8) {
-        uint32_t old[8];
-        const uint16_t *bp[8];
-        uint16_t *yp[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          bp[i] = base + __shfl_sync(0xffffffffu, br[i0 / 8], i * 4);
-          yp[i] = y + __shfl_sync(0xffffffffu, yr[i0 / 8], i * 4);
-          // pairs start at the row's 4-byte boundary; the value before it takes the place of the pair past the end
-          const int odd = (reinterpret_cast<uintptr_t>(yp[i] + n0) >> 1) & 1;
-          const int n = n0 + 2 * lane - odd;
-          const bool pair = ((reinterpret_cast<uintptr_t>(bp[i]) ^ reinterpret_cast<uintptr_t>(yp[i])) & 2) == 0;
-          old[i] = 0u;
-          if (base && r0 + i0 + i < rows) {
-            if (n >= n0)
-              old[i] = load_two(bp[i], n, end, pair);
-            else
-              old[i] = (n0 + 63 < end ? bp[i][n0 + 63] : 0u) | static_cast<uint32_t>(bp[i][n0]) << 16;
-          }
+      for (int i = 0; i < 16; ++i) {
+        uint16_t *yp = y + __shfl_sync(0xffffffffu, yr[i / 8], i % 8 * 4);
+        if (r0 + i >= rows) continue;
+        const int odd = (reinterpret_cast<uintptr_t>(yp + n0) >> 1) & 1;
+        const int c = 2 * lane - odd;
+        uint32_t out = both[i] | low[i] | high[i] << 16;
+        if (key >= 0) {
+          const float *sum = sums[i];
+          out = out_bits2<DT>(value_f32<DT>(out & 0xffffu) + sum[c < 0 ? 63 : c], value_f32<DT>(out >> 16) + sum[c + 1]);
         }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          if (r0 + i0 + i >= rows) continue;
-          const int odd = (reinterpret_cast<uintptr_t>(yp[i] + n0) >> 1) & 1;
-          const int c = 2 * lane - odd;
-          uint32_t out = old[i];
-          if (key >= 0) {
-            const float *sums = stage[warp][i0 + i];
-            out = out_bits2<DT>(value_f32<DT>(out & 0xffffu) + sums[c < 0 ? 63 : c], value_f32<DT>(out >> 16) + sums[c + 1]);
-          }
-          if (c >= 0) {
-            store_two(yp[i], n0 + c, end, true, out);
-          } else {
-            if (n0 + 63 < end) yp[i][n0 + 63] = static_cast<uint16_t>(out);
-            yp[i][n0] = static_cast<uint16_t>(out >> 16);
-          }
+        if (c >= 0) {
+          store_two(yp, n0 + c, end, out);
+        } else {
+          if (n0 + 63 < end) yp[n0 + 63] = static_cast<uint16_t>(out);
+          yp[n0] = static_cast<uint16_t>(out >> 16);
         }
       }
     }
   }
+  copies_wait<0>();
 }
 
 // The launch's shape, and the workspace's: [v][perm][tiles][ntiles].
@@ -455,10 +487,11 @@ LoraPlan lora_plan(int64_t T, int64_t N, int64_t K, int adapters, int rank, int 
 }
 
 template <typename... Args>
-cudaError_t launch_grid(void (*kern)(Args...), dim3 grid, int cluster, cudaStream_t stream, Args... args) {
+cudaError_t launch_grid(void (*kern)(Args...), dim3 grid, int cluster, int smem, cudaStream_t stream, Args... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(32 * kWarps);
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -471,6 +504,29 @@ cudaError_t launch_grid(void (*kern)(Args...), dim3 grid, int cluster, cudaStrea
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
+template <int DT, int RW, int KB, bool WIDE>
+cudaError_t launch_expand(const Tiles &ts, const LoraArgs &a, const LoraPlan &p, const float *v, int num_sms,
+                          cudaStream_t stream) {
+  auto kern = lora_expand_kernel<DT, RW, KB, WIDE>;
+  constexpr int bytes = Expand<RW, KB, WIDE>::kBytes;
+  // the opt-in to this much shared memory is an attribute of the function on each device
+  static std::atomic<uint64_t> set{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? uint64_t{1} << dev : 0;
+  if (!(set.load() & bit)) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess) return e;
+    set.fetch_or(bit);
+  }
+  // columns: as many blocks as run at a time, no more than one turn of a block's warps each
+  const int64_t turns = cdiv(a.N, (WIDE ? 32 : 64) * kWarps / RW);
+  const int64_t want = (KB <= 2 && WIDE ? 3 : KB <= 4 ? 2 : 1) * num_sms / p.max_tiles;
+  return launch_grid(kern, dim3(p.max_tiles, static_cast<unsigned>(want < 1 ? 1 : want < turns ? want : turns)), 1, bytes,
+                     stream, ts, a, v);
+}
+
 template <int DT, int RW>
 cudaError_t launch_rw(const Tiles &ts, const LoraArgs &a, const LoraPlan &p, float *v, int num_sms, cudaStream_t stream) {
   constexpr int MT = RW == 1 ? 1 : 2;
@@ -479,21 +535,20 @@ cudaError_t launch_rw(const Tiles &ts, const LoraArgs &a, const LoraPlan &p, flo
                 : a.rank <= 16 ? lora_shrink_kernel<DT, MT, RG, 2, 4>
                 : a.rank <= 32 ? lora_shrink_kernel<DT, MT, RG, 4, 2>
                                : lora_shrink_kernel<DT, MT, RG, 8, 1>;
-  cudaError_t e = launch_grid(shrink, dim3(p.max_tiles, p.splits, a.rank > 64 ? 2 : 1), p.splits, stream, ts, a, v);
+  cudaError_t e = launch_grid(shrink, dim3(p.max_tiles, p.splits, a.rank > 64 ? 2 : 1), p.splits, 0, stream, ts, a, v);
   if (e != cudaSuccess) return e;
   const bool wide = a.ldy % 8 == 0 && reinterpret_cast<uintptr_t>(a.y) % 16 == 0 &&
                     (!a.base || (a.ldbase % 8 == 0 && reinterpret_cast<uintptr_t>(a.base) % 16 == 0));
-  auto expand = a.rank <= 16   ? (wide ? lora_expand_kernel<DT, RW, 1, true> : lora_expand_kernel<DT, RW, 1, false>)
-                : a.rank <= 32 ? (wide ? lora_expand_kernel<DT, RW, 2, true> : lora_expand_kernel<DT, RW, 2, false>)
-                : a.rank <= 64 ? (wide ? lora_expand_kernel<DT, RW, 4, true> : lora_expand_kernel<DT, RW, 4, false>)
-                               : (wide ? lora_expand_kernel<DT, RW, 8, true> : lora_expand_kernel<DT, RW, 8, false>);
-  // columns: blocks for the device a few times over, no more than one turn of a block's warps each
-  const int64_t turns = cdiv(a.N, (wide ? 32 : 64) * kWarps / RW);
-  const int64_t want = 3 * num_sms / p.max_tiles;
-  return launch_grid(expand, dim3(p.max_tiles, static_cast<unsigned>(want < 1 ? 1 : want < turns ? want : turns)), 1, stream,
-                     ts, a, static_cast<const float *>(v));
+  if (wide)
+    return a.rank <= 16   ? launch_expand<DT, RW, 1, true>(ts, a, p, v, num_sms, stream)
+           : a.rank <= 32 ? launch_expand<DT, RW, 2, true>(ts, a, p, v, num_sms, stream)
+           : a.rank <= 64 ? launch_expand<DT, RW, 4, true>(ts, a, p, v, num_sms, stream)
+                          : launch_expand<DT, RW, 8, true>(ts, a, p, v, num_sms, stream);
+  return a.rank <= 16   ? launch_expand<DT, RW, 1, false>(ts, a, p, v, num_sms, stream)
+         : a.rank <= 32 ? launch_expand<DT, RW, 2, false>(ts, a, p, v, num_sms, stream)
+         : a.rank <= 64 ? launch_expand<DT, RW, 4, false>(ts, a, p, v, num_sms, stream)
+                        : launch_expand<DT, RW, 8, false>(ts, a, p, v, num_sms, stream);
 }
-
 }  // namespace
 
 size_t lora_workspace_bytes(int64_t T, int64_t N, int64_t K, int adapters, int rank, int num_sms) {
