@@ -8,12 +8,14 @@
 // The products here run on register-operand tensor-core instructions, for few rows per expert: the weights of the
 // chosen experts are read once and that bounds them. Codes go from global memory straight to the registers that the
 // products read (8 bytes a lane: the tile layout deals a lane 16 consecutive codes of a row), with no barrier between
-// the loads; a block's warps split K, so that a slab of 32 weight rows starts all its loads at once, and add their
-// sums in shared memory in a fixed order.
+// the loads; where slabs of 32 weight rows are few, a block's warps split K and add their sums in shared memory in a
+// fixed order.
 //
 // Codes become operands without arithmetic: a code's four bits under the exponent of 16 are 16 + q in either type.
 // A product with ones gives X = sum x over the same k, and (q - z) x sums to sum (16 + q) x - (16 + z) X, exactly in
 // the operands and in 32 bits in the sums; a group's sum is multiplied by its 32-bit s. So no weight is rounded.
+#include <atomic>
+
 #include "experts.cuh"
 #include "gemm_common.cuh"
 #include "internal.h"
@@ -25,7 +27,6 @@ namespace {
 
 using namespace detail;
 
-constexpr int kWarps = 8;      // they split K
 constexpr int kSlabRows = 32;  // weight rows of a block
 constexpr int kTmemRows = 12;  // rows an expert has on average from which the tensor-memory kernel runs
 
@@ -46,121 +47,245 @@ __device__ __forceinline__ void operands(uint32_t w, uint32_t *o) {
   }
 }
 
-// A block: 32 weight rows of one expert x one tile of up to 8 NT rows of `in`. GATED: rows 2 j and 2 j + 1 are gate
-// and up j. WHOLE: g is a multiple of 64, so that a block of 64 k lies in one group; else a k block's groups take
-// turns, each with the other groups' x as zeros.
-template <int DT, int NT, bool GATED, bool WHOLE>
-__global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 2 : 1) experts_kernel(const Products p) {
+// How groups lie: kAny takes a 64-block's groups in turn, each with the other groups' x as zeros; kBlock: g a multiple of
+// 64, one group a block; kTwo: g a multiple of 128, one group two blocks.
+enum Groups { kAny, kBlock, kTwo };
+
+// A warp's ring of stages of two blocks of 64 k: [codes: block, half of its k, row, 16 bytes][x: block, 8 rows x 128 bytes,
+// 16-byte pieces swapped by row][group records: block, 32 scales and 32 zeros].
+template <int NT>
+struct Stage {
+  static constexpr int kX = 2048, kRec = kX + 2 * NT * 1024, kBytes = kRec + 256;
+  static constexpr int kCount = NT <= 2 ? 3 : 2;
+  static constexpr int kRing = kCount * kBytes;
+};
+
+// A block of warps: kw of them share a slab of 32 weight rows x one tile of up to 8 NT rows of `in`, and split its K in
+// steps of two blocks. GATED: rows 2 j and 2 j + 1 are gate and up j. DIRECT: no plan (see Products); down then runs over
+// all choices of a token, each group's scale multiplied by the choice's weight, and its sums are y.
+// Everything a warp reads it copies ahead into its own ring: as loads to registers, two blocks ahead, the same traffic ran
+// at 2.9 TB/s.
+template <int DT, int NT, bool GATED, Groups MODE, bool DIRECT, int NW>
+__global__ void __launch_bounds__(32 * NW, NT == 1 && NW == 8 ? 2 : 1) experts_kernel(const Products p) {
+  using St = Stage<NT>;
+  constexpr int D = St::kCount;
+  constexpr bool ALL = DIRECT && !GATED;
+  extern __shared__ __align__(128) uint8_t smem[];
   griddep_launch_dependents();
   griddep_wait();
-  const int tile = blockIdx.x / p.slabs;
-  const int n0 = (blockIdx.x - tile * p.slabs) * kSlabRows;
-  if (tile >= *p.plan.ntiles) return;
-  const RowTile rt = p.plan.tiles[tile];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
-
-  const uint16_t *xr[NT];
-  bool has[NT];
-#pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    has[n] = n * 8 + g < rt.rows;
-    const int pos = rt.row0 + n * 8 + g;
-    const int64_t row = !has[n] ? 0 : GATED ? p.plan.perm[pos] / p.choices : pos;
-    xr[n] = p.in + row * p.K + 16 * t;
+  const int kw = p.kw, part = warp % kw;
+  const int slabs_block = NW / kw;
+  const int per_tile = (p.slabs + slabs_block - 1) / slabs_block;
+  const int tile = blockIdx.x / per_tile;
+  const int n0 = ((blockIdx.x - tile * per_tile) * slabs_block + warp / kw) * kSlabRows;
+  RowTile rt;
+  int id = -1;        // ALL: lane j's are choice j's
+  float weight = 0.0f;
+  if (DIRECT) {
+    rt = RowTile{ALL ? 0 : p.ids[tile], tile, 1, 0};
+    if (!ALL && (rt.key < 0 || rt.key >= p.experts)) return;
+    if (ALL && lane < p.choices) {
+      id = p.ids[static_cast<int64_t>(tile) * p.choices + lane];
+      weight = p.weights[static_cast<int64_t>(tile) * p.choices + lane];
+      if (id >= p.experts) id = -1;
+    }
+  } else {
+    rt = p.plan.tiles[tile];  // (read beside the count: the list has room for every block)
+    if (tile >= *p.plan.ntiles) return;
   }
-  const uint8_t *expert = p.codes + rt.key * p.expert_bytes;
-  const int wt = n0 / kTN, r0 = n0 % kTN;
-  // lane t's 16 codes of row r in a 4 KB tile: k = 16 t ..: half t / 2, bytes 8 (t % 2) of the row's 16
-  const uint8_t *codes =
-      expert + static_cast<int64_t>(wt) * p.KB * kTileBytes + (t >> 1) * 2048 + (r0 + g) * 16 + 8 * (t & 1);
-  const uint8_t *meta = expert + p.meta + static_cast<int64_t>(wt) * p.G * kRecBytes;
 
-  const int kb0 = p.KB * warp / kWarps, kb1 = p.KB * (warp + 1) / kWarps;
-  constexpr uint32_t kOne = DT == kDtypeBf16 ? 0x3F803F80u : 0x3C003C00u;
-  float sum[2][NT][4] = {};  // rows g, g + 8 (and 16, 24): what is done
-  constexpr int U = NT == 1 ? 4 : 2;
-  for (int kb = kb0; kb < kb1; kb += U) {
-    uint2 c[U][4];
-    uint4 x[U][NT][2];
-    uint32_t rec[U];
+  // the rows that the lane copies: lane / 8 and lane / 8 + 4 of each eight, piece lane % 8 of their 128 bytes
+  const uint16_t *xr[2 * NT];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const bool in = kb + u < kb1;
-      const uint8_t *cb = codes + static_cast<int64_t>(kb + u) * kTileBytes;
+  for (int n = 0; n < 2 * NT; ++n) {
+    const int col = n * 4 + (lane >> 3), pos = rt.row0 + col;
+    xr[n] = nullptr;
+    if (col < rt.rows) {
+      const int64_t row = ALL ? static_cast<int64_t>(pos) * p.choices
+                          : DIRECT && GATED ? pos / p.choices
+                          : GATED ? p.plan.perm[pos] / p.choices : pos;
+      xr[n] = p.in + row * p.K + 8 * (lane & 7);
+    }
+  }
+  const int wt = n0 / kTN, r0 = n0 % kTN;
+  const int64_t codes0 = static_cast<int64_t>(wt) * p.KB * kTileBytes + (r0 + lane) * 16;
+  const int64_t meta0 = p.meta + static_cast<int64_t>(wt) * p.G * kRecBytes;
+  const bool live = n0 < p.N;
+  const uint32_t ring = smem_u32(smem) + warp * St::kRing;
+  // where the lane's pieces of x go
+  const uint32_t x_to = ring + St::kX + (lane >> 3) * 128 + ((lane & 7) ^ (lane >> 3)) * 16;
+  const uint32_t x_to4 = ring + St::kX + ((lane >> 3) + 4) * 128 + ((lane & 7) ^ ((lane >> 3) + 4)) * 16;
+  if (rt.rows < 8 * NT)  // rows that the tile has not are zeros
+    for (int i = lane; i < D * 2 * NT * 64; i += 32) {
+      const int at = i / 64, row = i % (64) / 8;
+      if (at % NT * 8 + row >= rt.rows)
+        asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(ring + at / (2 * NT) * St::kBytes + St::kX +
+                                                                      at % (2 * NT) * 1024 + i % 64 * 16),
+                     "r"(0)
+                     : "memory");
+    }
+
+  // the warp's steps: of the tile's expert, or of all choices one after another
+  const int steps = (p.KB + 1) / 2, all = ALL ? steps * p.choices : steps;
+  const int f0 = all * part / kw, f1 = live ? all * (part + 1) / kw : f0;
+  int jf = ALL ? f0 / steps : 0;  // choice and step of the next copies
+  int sf = f0 - jf * steps;
+  auto fill = [&](int f, int slot) {
+    if (f < f1) {
+      int key = rt.key;
+      const int choice = jf, kb = 2 * sf++;
+      if (ALL) {
+        key = __shfl_sync(0xffffffffu, id, choice);
+        if (sf == steps) sf = 0, ++jf;
+      }
+      if (key >= 0) {
+        const uint8_t *expert = p.codes + key * p.expert_bytes;
+        const uint32_t to = slot * St::kBytes;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) c[u][i] = in ? __ldg(reinterpret_cast<const uint2 *>(cb + i * 128)) : make_uint2(0u, 0u);
+        for (int u = 0; u < 2; ++u) {
+          if (kb + u >= p.KB) break;
+          const uint8_t *cb = expert + codes0 + static_cast<int64_t>(kb + u) * kTileBytes;
+          cp_async16_zfill(ring + to + u * 1024 + lane * 16, cb, 16);
+          cp_async16_zfill(ring + to + u * 1024 + 512 + lane * 16, cb + 2048, 16);
+          const int k = (kb + u) * kTK;
+          const uint32_t bytes = k + 8 * (lane & 7) < p.K ? 16u : 0u;  // K is a multiple of 8
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int k = (kb + u) * kTK + 8 * i;  // K is a multiple of 8
-          x[u][n][i] = in && has[n] && k + 16 * t < p.K ? __ldg(reinterpret_cast<const uint4 *>(xr[n] + k))
-                                                         : make_uint4(0u, 0u, 0u, 0u);
+          for (int n = 0; n < 2 * NT; ++n)
+            if (xr[n])
+              cp_async16_zfill((n & 1 ? x_to4 : x_to) + to + (u * NT + n / 2) * 1024,
+                               bytes ? xr[n] + (ALL ? static_cast<int64_t>(choice) * p.K : 0) + k : p.in, bytes);
+          if (MODE == kBlock || (MODE == kTwo && u == 0)) {
+            const uint8_t *m = expert + meta0 + static_cast<int64_t>(p.gdiv.div(k)) * kRecBytes;
+            if (lane < 20)  // 32 scales and 32 zeros, 4 bytes a lane
+              asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(ring + to + St::kRec + u * 128 + 4 * lane),
+                           "l"(lane < 16 ? m + 2 * r0 + 4 * lane : m + 256 + r0 / 2 + 4 * (lane - 16))
+                           : "memory");
+          }
         }
-      if (WHOLE) {  // lane l: row l's scale, and its zero in the upper half
-        const uint8_t *m = meta + static_cast<int64_t>(p.gdiv.div((kb + u) * kTK)) * kRecBytes;
-        rec[u] = in ? *reinterpret_cast<const uint16_t *>(m + 2 * (r0 + lane)) |
-                          static_cast<uint32_t>((m[256 + (r0 + lane) / 2] >> (4 * (lane & 1))) & 15) << 16
-                    : 0u;
       }
     }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  // row l's scale, and its zero in the upper half, for lane l
+  auto record = [&](const uint8_t *m) {
+    return *reinterpret_cast<const uint16_t *>(m + 2 * (r0 + lane)) |
+           static_cast<uint32_t>((m[256 + (r0 + lane) / 2] >> (4 * (lane & 1))) & 15) << 16;
+  };
+  auto record_at = [&](uint32_t at) { return lds16(at + 2 * lane) | ((lds8(at + 64 + lane / 2) >> (4 * (lane & 1))) & 15) << 16; };
+
+  constexpr uint32_t kOne = DT == kDtypeBf16 ? 0x3F803F80u : 0x3C003C00u;
+  float sum[2][NT][4] = {};  // rows g, g + 8 (and 16, 24): what is done
+  float d0[NT][4], d1[NT][4], ones[NT][4];
+  auto clear = [&] {
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (kb + u >= kb1) break;
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) d0[n][i] = d1[n][i] = ones[n][i] = 0.0f;
+  };
+  // adds a group's products to the sums: scale * (sum (16 + q) x - (16 + zero) sum x)
+  auto close = [&](uint32_t rec, float weight) {
+    float s[4], zb[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t v = __shfl_sync(0xffffffffu, rec, i * 8 + g);
+      s[i] = scale_f32<DT>(v & 0xffffu);
+      if (ALL) s[i] *= weight;
+      zb[i] = static_cast<float>(16 + static_cast<int>(v >> 16));
+    }
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {  // i / 2: row g or g + 8; i % 2: column 2 t + i % 2
+        sum[0][n][i] += s[i / 2] * (d0[n][i] - zb[i / 2] * ones[n][i]);
+        sum[1][n][i] += s[2 + i / 2] * (d1[n][i] - zb[2 + i / 2] * ones[n][i]);
+      }
+  };
+  // one block's products; first, second: whether the lane's two words of codes take part
+  auto block = [&](const uint32_t (&a)[4][8], uint32_t x_at, bool first, bool second) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const uint4 x0 = lds128(x_at + n * 1024 + g * 128 + ((2 * t) ^ g) * 16);
+      const uint4 x1 = lds128(x_at + n * 1024 + g * 128 + ((2 * t + 1) ^ g) * 16);
+      uint32_t b[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
+      if (MODE == kAny) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) b[i] = (i < 4 ? first : second) ? b[i] : 0u;
+      }
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        mma_16816<DT>(d0[n], a[0][2 * q], a[1][2 * q], a[0][2 * q + 1], a[1][2 * q + 1], b[2 * q], b[2 * q + 1]);
+        mma_16816<DT>(d1[n], a[2][2 * q], a[3][2 * q], a[2][2 * q + 1], a[3][2 * q + 1], b[2 * q], b[2 * q + 1]);
+        mma_16816<DT>(ones[n], kOne, kOne, kOne, kOne, b[2 * q], b[2 * q + 1]);
+      }
+    }
+  };
+  int jc = ALL ? f0 / steps : 0, sc = f0 - jc * steps;  // choice and step of the next products
+  auto compute = [&](int slot) {
+    const int kb = 2 * sc++;
+    int key = rt.key;
+    float w = 1.0f;
+    if (ALL) {
+      key = __shfl_sync(0xffffffffu, id, jc);
+      w = __shfl_sync(0xffffffffu, weight, jc);
+      if (sc == steps) sc = 0, ++jc;
+      if (key < 0) return;
+    }
+    const uint32_t at = ring + slot * St::kBytes;
+    if (MODE != kAny) clear();
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      if (kb + u >= p.KB) break;
       uint32_t a[4][8];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        operands<DT>(c[u][i].x, a[i]);
-        operands<DT>(c[u][i].y, a[i] + 4);
+        // lane t's 16 codes of a row: half t / 2 of the block's k, bytes 8 (t % 2) of the row's 16
+        uint32_t c0, c1;
+        asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];"
+                     : "=r"(c0), "=r"(c1)
+                     : "r"(at + u * 1024 + (t >> 1) * 512 + (8 * i + g) * 16 + 8 * (t & 1))
+                     : "memory");
+        operands<DT>(c0, a[i]);
+        operands<DT>(c1, a[i] + 4);
       }
-      const int k0 = (kb + u) * kTK;
-      const int j0 = WHOLE ? 0 : p.gdiv.div(k0), j1 = WHOLE ? 0 : p.gdiv.div(min(k0 + kTK, p.K) - 1);
-      for (int j = j0; j <= j1; ++j) {
-        uint32_t r = WHOLE ? rec[u] : 0u;
-        bool first = true, second = true;  // whether the lane's two words of codes lie in group j
-        if (!WHOLE) {
-          const uint8_t *m = meta + static_cast<int64_t>(j) * kRecBytes;
-          r = *reinterpret_cast<const uint16_t *>(m + 2 * (r0 + lane)) |
-              static_cast<uint32_t>((m[256 + (r0 + lane) / 2] >> (4 * (lane & 1))) & 15) << 16;
-          first = p.gdiv.div(k0 + 16 * t) == j;
-          second = p.gdiv.div(k0 + 16 * t + 8) == j;
+      const uint32_t x_at = at + St::kX + u * NT * 1024;
+      if (MODE == kAny) {
+        const uint8_t *meta = p.codes + key * p.expert_bytes + meta0;
+        const int k0 = (kb + u) * kTK;
+        const int j1 = p.gdiv.div(min(k0 + kTK, p.K) - 1);
+        for (int j = p.gdiv.div(k0); j <= j1; ++j) {
+          clear();
+          block(a, x_at, p.gdiv.div(k0 + 16 * t) == j, p.gdiv.div(k0 + 16 * t + 8) == j);
+          close(record(meta + static_cast<int64_t>(j) * kRecBytes), w);
         }
-        float s[4], zb[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t v = __shfl_sync(0xffffffffu, r, i * 8 + g);
-          s[i] = scale_f32<DT>(v & 0xffffu);
-          zb[i] = static_cast<float>(16 + static_cast<int>(v >> 16));
-        }
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          uint32_t b[8] = {x[u][n][0].x, x[u][n][0].y, x[u][n][0].z, x[u][n][0].w,
-                           x[u][n][1].x, x[u][n][1].y, x[u][n][1].z, x[u][n][1].w};
-          if (!WHOLE) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) b[i] = (i < 4 ? first : second) ? b[i] : 0u;
-          }
-          float d0[4] = {}, d1[4] = {}, ones[4] = {};
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            mma_16816<DT>(d0, a[0][2 * q], a[1][2 * q], a[0][2 * q + 1], a[1][2 * q + 1], b[2 * q], b[2 * q + 1]);
-            mma_16816<DT>(d1, a[2][2 * q], a[3][2 * q], a[2][2 * q + 1], a[3][2 * q + 1], b[2 * q], b[2 * q + 1]);
-            mma_16816<DT>(ones, kOne, kOne, kOne, kOne, b[2 * q], b[2 * q + 1]);
-          }
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {  // i / 2: row g or g + 8; i % 2: column 2 t + i % 2
-            sum[0][n][i] += s[i / 2] * (d0[i] - zb[i / 2] * ones[i]);
-            sum[1][n][i] += s[2 + i / 2] * (d1[i] - zb[2 + i / 2] * ones[i]);
-          }
+      } else {
+        block(a, x_at, true, true);
+        if (MODE == kBlock) {
+          close(record_at(at + St::kRec + u * 128), w);
+          clear();
         }
       }
     }
+    if (MODE == kTwo) close(record_at(at + St::kRec), w);
+  };
+#pragma unroll
+  for (int i = 0; i < D - 1; ++i) fill(f0 + i, i);
+  int slot = 0;
+  for (int f = f0; f < f1; ++f) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(D - 2) : "memory");
+    __syncwarp();  // every lane's copies of this stage are there, and every lane is done with the stage before
+    fill(f + D - 1, slot == 0 ? D - 1 : slot - 1);
+    compute(slot);
+    slot = slot == D - 1 ? 0 : slot + 1;
   }
+  asm volatile("cp.async.wait_all;" ::: "memory");
 
   // [warp][column][row], a column's rows one bank off the next column's
   constexpr int kLd = kSlabRows + 4;
-  __shared__ float red[kWarps][8 * NT][kLd];
+  __syncthreads();  // every warp is done with its ring, which the sums take over
+  float(*red)[8 * NT][kLd] = reinterpret_cast<float(*)[8 * NT][kLd]>(smem);
+  static_assert(sizeof(float) * 8 * NT * kLd <= St::kRing, "the sums fit");
 #pragma unroll
   for (int m = 0; m < 2; ++m)
 #pragma unroll
@@ -168,13 +293,14 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 2 : 1) experts_kernel(c
 #pragma unroll
       for (int i = 0; i < 4; ++i) red[warp][n * 8 + 2 * t + (i & 1)][m * 16 + (i >> 1) * 8 + g] = sum[m][n][i];
   __syncthreads();
+  // the slab's warps write its outputs: the sums of its parts of K in order
+  const int w0 = warp - part, tid = part * 32 + lane, threads = 32 * kw;
   if (GATED) {
-    for (int i = threadIdx.x; i < 8 * NT * 16; i += 32 * kWarps) {
+    for (int i = tid; i < rt.rows * 16; i += threads) {
       const int col = i / 16, j = i % 16;
-      if (col >= rt.rows || n0 + 2 * j >= p.N) continue;
+      if (n0 + 2 * j >= p.N) continue;
       float gate = 0.0f, up = 0.0f;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
+      for (int w = w0; w < w0 + kw; ++w) {
         gate += red[w][col][2 * j];
         up += red[w][col][2 * j + 1];
       }
@@ -182,13 +308,16 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 2 : 1) experts_kernel(c
           out_bits<DT>(silu_mul(gate, up));
     }
   } else {
-    for (int i = threadIdx.x; i < 8 * NT * 32; i += 32 * kWarps) {
+    for (int i = tid; i < rt.rows * 32; i += threads) {
       const int col = i / 32, r = i % 32;
-      if (col >= rt.rows || n0 + r >= p.N) continue;
+      if (n0 + r >= p.N) continue;
       float v = 0.0f;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) v += red[w][col][r];
-      static_cast<float *>(p.out)[static_cast<int64_t>(rt.row0 + col) * p.N + n0 + r] = v;
+      for (int w = w0; w < w0 + kw; ++w) v += red[w][col][r];
+      const int64_t at = static_cast<int64_t>(rt.row0 + col) * p.N + n0 + r;
+      if (ALL)
+        static_cast<uint16_t *>(p.out)[at] = out_bits<DT>(v);
+      else
+        static_cast<float *>(p.out)[at] = v;
     }
   }
 }
@@ -227,6 +356,7 @@ __global__ void __launch_bounds__(256)
 
 // The workspace: [error word][ntiles][outputs in 32 bits][h][perm][inverse][tiles].
 struct ExpertsPlan {
+  bool direct;  // no sort: each pair by itself, and a token's choices added in the second product
   bool tmem;
   int tile, max_tiles;
   size_t part, h, perm, inverse, tiles, bytes;
@@ -237,9 +367,11 @@ ExpertsPlan experts_plan(int64_t T, int64_t K, int64_t I, int experts, int k, in
   const int64_t pairs = T * k;
   // rows per tile: as many as an expert has on average, from the widths that the kernels have
   const int64_t mean = pairs / experts;
-  p.tmem = mean >= kTmemRows && experts_tmem_takes(g);
+  // (pairs that are few beside the experts seldom share one)
+  p.direct = T == 1 || pairs <= experts / 4;
+  p.tmem = !p.direct && mean >= kTmemRows && experts_tmem_takes(g);
   p.tile = p.tmem ? (mean <= 48 || g % 64 != 0 ? 64 : 128) : mean <= 8 ? 8 : mean <= 16 ? 16 : 32;
-  p.max_tiles = static_cast<int>(max_row_tiles(pairs, experts, p.tile));
+  p.max_tiles = static_cast<int>(p.direct ? pairs : max_row_tiles(pairs, experts, p.tile));
   auto up = [](size_t v) { return (v + 255) / 256 * 256; };
   p.part = 256;
   p.h = p.part + up(static_cast<size_t>(pairs) * K * 4);
@@ -250,14 +382,34 @@ ExpertsPlan experts_plan(int64_t T, int64_t K, int64_t I, int experts, int k, in
   return p;
 }
 
+template <int DT, int NT, bool GATED, bool DIRECT, int NW>
+cudaError_t launch_few(const Products &p, int tiles, cudaStream_t stream) {
+  const int mode = p.g % 128 == 0 ? kTwo : p.g % kTK == 0 ? kBlock : kAny;
+  auto kern = mode == kTwo     ? experts_kernel<DT, NT, GATED, kTwo, DIRECT, NW>
+              : mode == kBlock ? experts_kernel<DT, NT, GATED, kBlock, DIRECT, NW>
+                               : experts_kernel<DT, NT, GATED, kAny, DIRECT, NW>;
+  constexpr int bytes = NW * Stage<NT>::kRing;
+  static std::atomic<uint64_t> set[3];
+  const cudaError_t e = allow_smem(kern, bytes, &set[mode]);
+  if (e != cudaSuccess) return e;
+  return launch_programmatic(kern, static_cast<int>(cdiv(p.slabs, NW / p.kw)) * tiles, 32 * NW, bytes, stream, p);
+}
+
 template <int DT, bool GATED>
-cudaError_t launch_products(const Products &p, const ExpertsPlan &plan, int num_sms, cudaStream_t stream) {
+cudaError_t launch_products(Products p, const ExpertsPlan &plan, int64_t T, int num_sms, cudaStream_t stream) {
   if (plan.tmem) return launch_experts_tmem(p, DT, GATED, plan.tile, num_sms, stream);
-  const bool whole = p.g % kTK == 0;
-  auto kern = plan.tile == 8    ? (whole ? experts_kernel<DT, 1, GATED, true> : experts_kernel<DT, 1, GATED, false>)
-              : plan.tile == 16 ? (whole ? experts_kernel<DT, 2, GATED, true> : experts_kernel<DT, 2, GATED, false>)
-                                : (whole ? experts_kernel<DT, 4, GATED, true> : experts_kernel<DT, 4, GATED, false>);
-  return launch_programmatic(kern, p.slabs * plan.max_tiles, 32 * kWarps, 0, stream, p);
+  const int tiles = plan.direct && !GATED ? static_cast<int>(T) : plan.max_tiles;
+  // K is split over as many warps as fill the device a few times over, none with fewer than two steps
+  const int64_t slabs = static_cast<int64_t>(p.slabs) * tiles;
+  const int64_t steps = cdiv(p.KB, 2) * (plan.direct && !GATED ? p.choices : 1);
+  const int most = plan.direct ? 16 : 8;
+  p.kw = most;
+  while (p.kw > 1 && (slabs * p.kw / 2 >= 48 * num_sms || steps < 2 * p.kw)) p.kw /= 2;
+  if (plan.direct)
+    return launch_few<DT, 1, GATED, true, 16>(p, tiles, stream);
+  return plan.tile == 8    ? launch_few<DT, 1, GATED, false, 8>(p, tiles, stream)
+         : plan.tile == 16 ? launch_few<DT, 2, GATED, false, 8>(p, tiles, stream)
+                           : launch_few<DT, 4, GATED, false, 8>(p, tiles, stream);
 }
 
 template <int DT>
@@ -268,7 +420,8 @@ cudaError_t launch_dt(const ExpertsArgs &a, uint8_t *ws, const ExpertsPlan &plan
   rows.tiles = reinterpret_cast<RowTile *>(ws + plan.tiles);
   rows.ntiles = reinterpret_cast<int32_t *>(ws + 4);
   rows.err = reinterpret_cast<uint32_t *>(ws);
-  cudaError_t e = launch_row_plan(a.ids, a.T * a.k, a.experts, plan.tile, false, rows, stream);
+  cudaError_t e = cudaSuccess;
+  if (!plan.direct) e = launch_row_plan(a.ids, a.T * a.k, a.experts, plan.tile, false, rows, stream);
   if (e != cudaSuccess) return e;
   auto products = [&](const void *in, int64_t in_rows, const void *packed, int64_t N, int64_t K, void *out) {
     Products p;
@@ -287,12 +440,18 @@ cudaError_t launch_dt(const ExpertsArgs &a, uint8_t *ws, const ExpertsPlan &plan
     p.err = rows.err;
     p.slabs = static_cast<int>(cdiv(N, plan.tmem ? kTN : kSlabRows));
     p.choices = a.k;
+    p.ids = a.ids;
+    p.weights = a.weights;
+    p.experts = a.experts;
+    p.kw = 1;
     p.gdiv = make_fastdiv(static_cast<uint32_t>(a.g));
     return p;
   };
-  e = launch_products<DT, true>(products(a.x, a.T, a.gate_up, 2 * a.I, a.K, ws + plan.h), plan, num_sms, stream);
+  e = launch_products<DT, true>(products(a.x, a.T, a.gate_up, 2 * a.I, a.K, ws + plan.h), plan, a.T, num_sms, stream);
   if (e != cudaSuccess) return e;
-  e = launch_products<DT, false>(products(ws + plan.h, a.T * a.k, a.down, a.K, a.I, ws + plan.part), plan, num_sms, stream);
+  if (plan.direct)
+    return launch_products<DT, false>(products(ws + plan.h, a.T * a.k, a.down, a.K, a.I, a.y), plan, a.T, num_sms, stream);
+  e = launch_products<DT, false>(products(ws + plan.h, a.T * a.k, a.down, a.K, a.I, ws + plan.part), plan, a.T, num_sms, stream);
   if (e != cudaSuccess) return e;
   return launch_programmatic(combine_kernel<DT>, static_cast<int>(cdiv(a.T * (a.K / 8), 256)), 256, 0, stream,
                              reinterpret_cast<const float *>(ws + plan.part), static_cast<const int32_t *>(rows.inverse), a.weights,

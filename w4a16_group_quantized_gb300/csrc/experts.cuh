@@ -19,6 +19,11 @@ struct Products {
   int K, N, G, KB, g;
   int slabs;             // blocks (experts.cu) or weight tiles (experts_tmem.cu) of N
   int choices;           // k: pair / k is the token
+  // experts.cu without a plan: tile i is pair i (gate/up) or token i with all its choices (down, whose out is then y)
+  const int32_t *ids;
+  const float *weights;
+  int experts;
+  int kw;                // warps that share a slab's K
   FastDiv gdiv;
 };
 

@@ -496,17 +496,9 @@ template <int DT, int BN, int CB, int SUB, bool GATED>
 cudaError_t launch_one(const Products &p, int num_sms, cudaStream_t stream) {
   auto kern = experts_tmem_kernel<DT, BN, CB, SUB, GATED>;
   constexpr int bytes = TCfg<BN, CB, SUB>::kSmemBytes;
-  // the opt-in to this much shared memory is an attribute of the function on each device
   static std::atomic<uint64_t> set{0};
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
+  const cudaError_t e = allow_smem(kern, bytes, &set);
   if (e != cudaSuccess) return e;
-  const uint64_t bit = dev < 64 ? uint64_t{1} << dev : 0;
-  if (!(set.load() & bit)) {
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e != cudaSuccess) return e;
-    set.fetch_or(bit);
-  }
   CUtensorMap in_map;
   if (!make_rows_map(&in_map, p.in, p.in_rows, p.K, GATED ? 1 : BN / 4, DT)) return cudaErrorInvalidValue;
   return launch_programmatic(kern, num_sms, TCfg<BN, CB, SUB>::kThreads, bytes, stream, in_map, p);

@@ -3,6 +3,7 @@
 // dequant of 8 packed codes, bounded waits and the owner-reduces finish of tiles cut between CTAs.
 #pragma once
 
+#include <atomic>
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -435,6 +436,20 @@ __device__ __forceinline__ void produce_stages(const CUtensorMap *x_map, const P
     // let every copy this warp issued land before the CTA's shared memory goes away
     for (int j = i - 2; j >= 0 && j >= i - S; j -= 2) drain_wait(smem_u32(&full_bar[j % S]), (j / S) & 1);
   }
+}
+
+// Lets a kernel take `bytes` of dynamic shared memory: an attribute of the function on each device, set once (*set, a bit a
+// device).
+template <typename Kernel>
+cudaError_t allow_smem(Kernel kern, int bytes, std::atomic<uint64_t> *set) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? uint64_t{1} << dev : 0;
+  if (set->load() & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) set->fetch_or(bit);
+  return e;
 }
 
 // A tensor map of rows of 16-bit values in boxes of 64 columns x box_rows rows (gemm.cu).

@@ -509,17 +509,9 @@ cudaError_t launch_expand(const Tiles &ts, const LoraArgs &a, const LoraPlan &p,
                           cudaStream_t stream) {
   auto kern = lora_expand_kernel<DT, RW, KB, WIDE>;
   constexpr int bytes = Expand<RW, KB, WIDE>::kBytes;
-  // the opt-in to this much shared memory is an attribute of the function on each device
   static std::atomic<uint64_t> set{0};
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
+  const cudaError_t e = allow_smem(kern, bytes, &set);
   if (e != cudaSuccess) return e;
-  const uint64_t bit = dev < 64 ? uint64_t{1} << dev : 0;
-  if (!(set.load() & bit)) {
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e != cudaSuccess) return e;
-    set.fetch_or(bit);
-  }
   // columns: as many blocks as run at a time, no more than one turn of a block's warps each
   const int64_t turns = cdiv(a.N, (WIDE ? 32 : 64) * kWarps / RW);
   const int64_t want = (KB <= 2 && WIDE ? 3 : KB <= 4 ? 2 : 1) * num_sms / p.max_tiles;
