@@ -18,6 +18,7 @@ from __future__ import annotations
 import ctypes
 import functools
 import os
+import struct
 import threading
 
 import torch
@@ -54,34 +55,6 @@ class Epilogue(ctypes.Structure):
 
     _fields_ = [("kind", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("q_per_group", ctypes.c_int32),
                 ("reserved", ctypes.c_int32), ("k_dev", ctypes.c_void_p), ("v_dev", ctypes.c_void_p)]
-
-
-class RouteOptions(ctypes.Structure):
-    """w4_route_options of the C ABI."""
-
-    _fields_ = [("k", ctypes.c_int32), ("sigmoid", ctypes.c_int32), ("groups", ctypes.c_int32),
-                ("top_groups", ctypes.c_int32), ("group_top", ctypes.c_int32), ("renormalize", ctypes.c_int32),
-                ("scale", ctypes.c_float), ("dtype", ctypes.c_int32)]
-
-
-class ExpertsArgs(ctypes.Structure):
-    """w4a16_experts_args of the C ABI."""
-
-    _fields_ = [("x_dev", ctypes.c_void_p), ("gate_up_dev", ctypes.c_void_p), ("down_dev", ctypes.c_void_p),
-                ("ids_dev", ctypes.c_void_p), ("weights_dev", ctypes.c_void_p), ("y_dev", ctypes.c_void_p),
-                ("T", ctypes.c_int64), ("K", ctypes.c_int64), ("I", ctypes.c_int64), ("experts", ctypes.c_int32),
-                ("k", ctypes.c_int32), ("g", ctypes.c_int32), ("dtype", ctypes.c_int32)]
-
-
-class LoraArgs(ctypes.Structure):
-    """w4_lora_args of the C ABI."""
-
-    _fields_ = [("x_dev", ctypes.c_void_p), ("A_dev", ctypes.c_void_p), ("B_dev", ctypes.c_void_p),
-                ("adapter_dev", ctypes.c_void_p), ("scaling_dev", ctypes.c_void_p), ("ranks_dev", ctypes.c_void_p),
-                ("base_dev", ctypes.c_void_p), ("y_dev", ctypes.c_void_p), ("T", ctypes.c_int64),
-                ("K", ctypes.c_int64), ("N", ctypes.c_int64), ("ldx", ctypes.c_int64), ("ldbase", ctypes.c_int64),
-                ("ldy", ctypes.c_int64), ("adapters", ctypes.c_int32), ("rank", ctypes.c_int32),
-                ("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
 class Problem(ctypes.Structure):
@@ -137,10 +110,10 @@ def load() -> ctypes.CDLL:
             "w4a16_gemm_grouped": ([ctypes.POINTER(Problem), I32, I64, I32, P, SZ, ctypes.POINTER(Options), P],
                                    ctypes.c_int),
             "w4a16_grouped_workspace_bytes": ([ctypes.POINTER(Problem), I32, I64, I32, ctypes.POINTER(Options)], SZ),
-            "w4_route": ([P, I64, I32, I64, P, ctypes.POINTER(RouteOptions), P, P, P], ctypes.c_int),
-            "w4a16_experts": ([ctypes.POINTER(ExpertsArgs), P, SZ, P], ctypes.c_int),
+            "w4_route": ([P, I64, I32, I64, P, ctypes.c_char_p, P, P, P], ctypes.c_int),
+            "w4a16_experts": ([ctypes.c_char_p, P, SZ, P], ctypes.c_int),
             "w4a16_experts_workspace_bytes": ([I64, I64, I64, I32, I32, I32], SZ),
-            "w4_lora_add": ([ctypes.POINTER(LoraArgs), P, SZ, P], ctypes.c_int),
+            "w4_lora_add": ([ctypes.c_char_p, P, SZ, P], ctypes.c_int),
             "w4_lora_workspace_bytes": ([I64, I64, I64, I32, I32], SZ),
         }
         for name, (args, res) in sigs.items():
@@ -451,59 +424,65 @@ def qkv_head_group_rows(wq: torch.Tensor, wk: torch.Tensor, wv: torch.Tensor, he
 _LOGIT_DTYPES = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}
 _repacked = functools.lru_cache(maxsize=1024)(w4_repacked_bytes)
 
-# A decode step makes these calls with a few microseconds of device work each, so the argument checks below read each
-# property once and the workspace is sized only when the library finds it too small.
+# A decode step makes these calls with a few microseconds of device work each, so the argument checks read each property
+# once, the C ABI's argument structs are packed in one step, and the workspace is sized only when the library finds it
+# too small.
+_ROUTE_OPTIONS = struct.Struct("@6ifi")   # w4_route_options
+_EXPERTS_ARGS = struct.Struct("@6P3q4i")  # w4a16_experts_args
+_LORA_ARGS = struct.Struct("@8P6q4i")     # w4_lora_args
 
 
 def _rows(t: torch.Tensor, name: str) -> int:
     """Values between the rows of a 2-D CUDA tensor, which are contiguous and do not overlap, but may lie further apart
     than they are long (a single row's stride says nothing)."""
     n, m = t.shape
+    if n <= 1:
+        if m > 1 and t.stride(1) != 1:
+            raise ValueError(f"the rows of {name} must be contiguous")
+        return -(-m // 8) * 8
     if t.is_contiguous():
-        return m if n > 1 else -(-m // 8) * 8
+        return m
     if m > 1 and t.stride(1) != 1:
         raise ValueError(f"the rows of {name} must be contiguous")
-    if n <= 1:
-        return -(-m // 8) * 8
     if t.stride(0) < m:
         raise ValueError(f"the rows of {name} must not overlap")
     return t.stride(0)
 
 
-def _like(t: torch.Tensor, name: str, dtype, shape, device) -> int:
-    """The address of a contiguous tensor of this type, shape and device."""
-    if t.dtype != dtype or t.shape != shape or t.device != device:
-        raise ValueError(f"{name} must be {dtype} {list(shape)} on {device}")
+def _like(t: torch.Tensor, name: str, dtype, shape, device: int) -> int:
+    """The address of a contiguous CUDA tensor of this type, shape and device index."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != device:
+        raise ValueError(f"{name} must be {dtype} {list(shape)} on cuda:{device}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     return t.data_ptr()
 
 
-def _handle(stream, device, *made) -> int:
+def _handle(stream, device: int, *made) -> int:
     """The stream's handle. What a call made for itself (``made``) is kept until a stream given by the caller is done
     with it."""
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(device.index)
+        return torch._C._cuda_getCurrentRawStream(device)
     for t in made:
         if t is not None:
             t.record_stream(stream)
     return stream.cuda_stream
 
 
-def _run_with(call, args, workspace, sized, device, stream, made, what: str):
+def _run_with(call, args, workspace, sized, device: int, stream, made, what: str):
     """call(args, workspace, its bytes, stream). A Workspace grows, and without one a buffer is made, by sized()."""
     own = None
     if workspace is None:
-        ws = own = torch.empty(max(sized(), 1), dtype=torch.uint8, device=device)
+        ws = own = torch.empty(max(sized(), 1), dtype=torch.uint8, device=f"cuda:{device}")
     else:
         ws = workspace.buf if isinstance(workspace, Workspace) else workspace
-        if ws.device != device or not ws.is_contiguous():
-            raise ValueError(f"workspace must be contiguous on {device}")
+        if ws.get_device() != device or not ws.is_contiguous():
+            raise ValueError(f"workspace must be contiguous on cuda:{device}")
     handle = _handle(stream, device, made, own)
-    rc = call(args, ws.data_ptr(), ws.numel() * ws.element_size(), handle)
+    rc = call(args, ws.data_ptr(), ws.nbytes, handle)
     if rc == 4 and isinstance(workspace, Workspace):
         ws = workspace.get(sized())
-        rc = call(args, ws.data_ptr(), ws.numel() * ws.element_size(), handle)
+        rc = call(args, ws.data_ptr(), ws.nbytes, handle)
     if rc != 0:
         raise W4Error(rc, what)
 
@@ -520,22 +499,23 @@ def w4_route(logits: torch.Tensor, k: int, *, sigmoid: bool = False, bias: torch
     if dt is None or logits.dim() != 2 or not logits.is_cuda:
         raise ValueError("logits must be a 2-D fp16, bf16 or fp32 CUDA tensor")
     T, E = logits.shape
-    device = logits.device
+    device = logits.get_device()
     ld = _rows(logits, "logits")
     b = None if bias is None else _like(bias, "bias", torch.float32, (E,), device)
     shape = (T, max(k, 0))
     made_w = made_i = None
     if weights is None:
-        weights = made_w = torch.empty(shape, dtype=torch.float32, device=device)
+        weights = made_w = torch.empty(shape, dtype=torch.float32, device=logits.device)
         w_at = weights.data_ptr()
     else:
         w_at = _like(weights, "weights", torch.float32, shape, device)
     if ids is None:
-        ids = made_i = torch.empty(shape, dtype=torch.int32, device=device)
+        ids = made_i = torch.empty(shape, dtype=torch.int32, device=logits.device)
         i_at = ids.data_ptr()
     else:
         i_at = _like(ids, "ids", torch.int32, shape, device)
-    o = RouteOptions(k, sigmoid, groups, groups if top_groups is None else top_groups, group_top, renormalize, scale, dt)
+    o = _ROUTE_OPTIONS.pack(k, sigmoid, groups, groups if top_groups is None else top_groups, group_top, renormalize, scale,
+                            dt)
     rc = (_lib or load()).w4_route(logits.data_ptr(), T, E, ld, b, o, w_at, i_at,
                                    _handle(stream, device, made_w, made_i))
     if rc != 0:
@@ -561,7 +541,7 @@ def w4a16_experts(x: torch.Tensor, gate_up: torch.Tensor, down: torch.Tensor, id
         raise ValueError("gate_up must be [E, bytes] and ids [T, k]")
     T, K = x.shape
     E, k = gate_up.shape[0], ids.shape[1]
-    device = x.device
+    device = x.get_device()
     lib = _lib or load()
     gu_bytes, dn_bytes = _repacked(2 * inter, K, g), _repacked(K, inter, g)
     if not gu_bytes or not dn_bytes:
@@ -571,11 +551,11 @@ def w4a16_experts(x: torch.Tensor, gate_up: torch.Tensor, down: torch.Tensor, id
     made = None
     if y is None:
         y = made = torch.empty_like(x)
-    a = ExpertsArgs(x.data_ptr(), _like(gate_up, "gate_up", torch.uint8, (E, gu_bytes), device),
-                    _like(down, "down", torch.uint8, (E, dn_bytes), device),
-                    _like(ids, "ids", torch.int32, (T, k), device),
-                    _like(weights, "weights", torch.float32, (T, k), device),
-                    y.data_ptr() if made is not None else _like(y, "y", x.dtype, (T, K), device), T, K, inter, E, k, g, dt)
+    a = _EXPERTS_ARGS.pack(
+        x.data_ptr(), _like(gate_up, "gate_up", torch.uint8, (E, gu_bytes), device),
+        _like(down, "down", torch.uint8, (E, dn_bytes), device), _like(ids, "ids", torch.int32, (T, k), device),
+        _like(weights, "weights", torch.float32, (T, k), device),
+        y.data_ptr() if made is not None else _like(y, "y", x.dtype, (T, K), device), T, K, inter, E, k, g, dt)
     _run_with(lib.w4a16_experts, a, workspace, lambda: w4a16_experts_workspace_bytes(T, K, inter, E, k, g), device, stream,
               made, "w4a16_experts")
     return y
@@ -601,21 +581,25 @@ def w4_lora_add(base: torch.Tensor | None, x: torch.Tensor, A: torch.Tensor, B: 
     T, K = x.shape
     R, rank, _ = A.shape
     N = B.shape[1]
-    device = x.device
+    device = x.get_device()
     shape = (T, N)
     made = None
     if y is None:
-        y = made = torch.empty(shape, dtype=dtype, device=device)
-    elif y.dtype != dtype or y.shape != shape or y.device != device:
-        raise ValueError(f"y must be {dtype} [{T}, {N}] on {device}")
-    if base is not None and (base.dtype != dtype or base.shape != shape or base.device != device):
-        raise ValueError(f"base must be {dtype} [{T}, {N}] on {device}")
-    a = LoraArgs(x.data_ptr(), _like(A, "A", dtype, (R, rank, K), device), _like(B, "B", dtype, (R, N, rank), device),
-                 _like(adapter, "adapter", torch.int32, (T,), device),
-                 None if scaling is None else _like(scaling, "scaling", torch.float32, (R,), device),
-                 None if ranks is None else _like(ranks, "ranks", torch.int32, (R,), device),
-                 None if base is None else base.data_ptr(), y.data_ptr(), T, K, N, _rows(x, "x"),
-                 0 if base is None else _rows(base, "base"), _rows(y, "y"), R, rank, dt, 0)
+        y = made = torch.empty(shape, dtype=dtype, device=x.device)
+    elif y.dtype is not dtype or y.shape != shape or y.get_device() != device:
+        raise ValueError(f"y must be {dtype} [{T}, {N}] on cuda:{device}")
+    if base is None:
+        base_at = ldbase = 0
+    elif base.dtype is not dtype or base.shape != shape or base.get_device() != device:
+        raise ValueError(f"base must be {dtype} [{T}, {N}] on cuda:{device}")
+    else:
+        base_at, ldbase = base.data_ptr(), _rows(base, "base")
+    a = _LORA_ARGS.pack(
+        x.data_ptr(), _like(A, "A", dtype, (R, rank, K), device), _like(B, "B", dtype, (R, N, rank), device),
+        _like(adapter, "adapter", torch.int32, (T,), device),
+        0 if scaling is None else _like(scaling, "scaling", torch.float32, (R,), device),
+        0 if ranks is None else _like(ranks, "ranks", torch.int32, (R,), device),
+        base_at, y.data_ptr(), T, K, N, _rows(x, "x"), ldbase, _rows(y, "y"), R, rank, dt, 0)
     _run_with((_lib or load()).w4_lora_add, a, workspace, lambda: w4_lora_workspace_bytes(T, K, N, R, rank), device, stream,
               made, "w4_lora_add")
     return y

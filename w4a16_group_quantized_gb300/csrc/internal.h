@@ -138,8 +138,10 @@ cudaError_t launch_gemm_grouped(const GemmProblem *probs, int count, int64_t M, 
 // w4_route's options (w4_route_options of the C ABI), checked.
 struct RouteParams {
   int k, groups, top_groups, group_top;
+  int group_lanes;     // lanes of the kernel's warp that hold a group, where that is a power of two of whole lanes; else 0
   uint32_t group_mul;  // ceil(2^22 / group size): e * group_mul >> 22 is e's group for e < 1024
   bool sigmoid, renormalize;
+  bool wide;  // every lane's logits are there and 16-byte aligned
   float scale;
 };
 constexpr int kRouteMaxExperts = 1024;

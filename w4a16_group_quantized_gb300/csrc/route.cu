@@ -7,9 +7,10 @@
 // found by the logits themselves, which order the scores and do not round (32-bit scores of unlike logits may be
 // equal).
 //
-// One warp per row: lane i holds the experts i, i + 32, ... as 32-bit keys whose unsigned order is that of the
-// values, so that each choice is two warp-wide integer reductions (the largest key, then the lowest index that
-// has it). The rows are independent and short (512 bytes at E = 256): latency bounds a decode step, and the
+// One warp per row: lane i holds PER consecutive experts as 32-bit keys whose unsigned order is that of the values, so
+// that each choice is a warp-wide integer reduction (the largest key) and a vote (the lowest lane that has it). Groups
+// that are a power of two of whole lanes are all ranked at once, by exchanges between their lanes; others one
+// after another. The rows are independent and short (512 bytes at E = 256): latency bounds a decode step, and the
 // issue of the k choices a large prefill.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -29,6 +30,33 @@ __device__ __forceinline__ float load_logit(const void *p, int64_t i) {
   if (DT == kDtypeF32) return static_cast<const float *>(p)[i];
   if (DT == kDtypeBf16) return __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t *>(p)[i]) << 16);
   return __half2float(static_cast<const __half *>(p)[i]);
+}
+
+// A lane's PER consecutive logits, in as few loads as 16 bytes each allow.
+template <int DT, int PER>
+__device__ __forceinline__ void load_logits(const void *p, int64_t i, float (&l)[PER]) {
+  constexpr int kSize = DT == kDtypeF32 ? 4 : 2, kBytes = PER * kSize;
+  constexpr int kWords = (kBytes + 3) / 4;
+  uint32_t w[kWords];
+  const char *at = static_cast<const char *>(p) + i * kSize;
+  if constexpr (kBytes >= 16) {
+#pragma unroll
+    for (int j = 0; j < kBytes / 16; ++j) {
+      const uint4 v = __ldg(reinterpret_cast<const uint4 *>(at) + j);
+      w[4 * j] = v.x, w[4 * j + 1] = v.y, w[4 * j + 2] = v.z, w[4 * j + 3] = v.w;
+    }
+  } else if constexpr (kBytes == 8) {
+    const uint2 v = __ldg(reinterpret_cast<const uint2 *>(at));
+    w[0] = v.x, w[1] = v.y;
+  } else if constexpr (kBytes == 4) {
+    w[0] = __ldg(reinterpret_cast<const uint32_t *>(at));
+  } else {
+    w[0] = __ldg(reinterpret_cast<const uint16_t *>(at));
+  }
+#pragma unroll
+  for (int j = 0; j < PER; ++j)
+    l[j] = DT == kDtypeF32 ? __uint_as_float(w[j * kSize / 4])
+                           : detail::scale_f32<DT == kDtypeF32 ? kDtypeF16 : DT>(w[j * kSize / 4] >> (16 * (j & 1)) & 0xffffu);
 }
 
 // Unsigned key with the order of the value (-0 and 0 alike; every key of a value is above 0, which marks
@@ -65,10 +93,15 @@ __global__ void __launch_bounds__(32 * kRouteWarps)
 
   float l[PER];
   float top = -INFINITY;
+  if (o.wide) {
+    load_logits<DT, PER>(logits, at + lane * PER, l);
+  } else {
+#pragma unroll
+    for (int i = 0; i < PER; ++i) l[i] = lane * PER + i < E ? load_logit<DT>(logits, at + lane * PER + i) : -INFINITY;
+  }
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
-    const int e = i * 32 + lane;
-    l[i] = e < E ? masked(load_logit<DT>(logits, at + e)) : -INFINITY;
+    l[i] = masked(l[i]);
     top = fmaxf(top, l[i]);
   }
   float sum = 1.0f;
@@ -85,7 +118,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps)
   uint32_t key[PER];
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
-    const int e = i * 32 + lane;
+    const int e = lane * PER + i;
     float c = l[i];
     if (bias && e < E && c != -INFINITY) c = (o.sigmoid ? sigmoid(c) : exp_below(c, top) / sum) + __ldg(bias + e);
     key[i] = e < E ? key_of(isnan(c) ? -INFINITY : c) : 0u;
@@ -94,26 +127,47 @@ __global__ void __launch_bounds__(32 * kRouteWarps)
   if (o.groups > 1) {
     // lane j keeps what group j is worth; a place's group by a multiplication (e < 1024, exact)
     uint32_t worth = 0u;
-    for (int j = 0; j < o.groups; ++j) {
+    const int lanes = o.group_lanes;  // of a group, a power of two; 0: groups that end inside a lane
+    // the sum of two is one of scores, which the logits' own order cannot give
+    const bool by_score = o.group_top == 2 && !bias;
+    auto merged = [&](uint32_t first, uint32_t second) {
+      return o.group_top == 2 ? key_of(value_of(first) + value_of(second)) : first;
+    };
+    if (lanes > 0) {
       uint32_t first = 0u, second = 0u;
 #pragma unroll
       for (int i = 0; i < PER; ++i) {
-        const int e = i * 32 + lane;
-        if (e >= E || static_cast<int>((e * o.group_mul) >> 22) != j) continue;
-        uint32_t v = key[i];
-        // the sum of two is one of scores, which the logits' own order cannot give
-        if (o.group_top == 2 && !bias) v = key_of(o.sigmoid ? sigmoid(l[i]) : exp_below(l[i], top) / sum);
+        const uint32_t v = by_score && key[i] != 0u ? key_of(o.sigmoid ? sigmoid(l[i]) : exp_below(l[i], top) / sum) : key[i];
         second = max(second, min(first, v));
         first = max(first, v);
       }
-      const uint32_t best = __reduce_max_sync(kFull, first);
-      uint32_t w = best;
-      if (o.group_top == 2) {
-        const int has = __ffs(__ballot_sync(kFull, first == best)) - 1;  // one lane gives its best up
-        const uint32_t next = __reduce_max_sync(kFull, lane == has ? second : first);
-        w = key_of(value_of(best) + value_of(next));
+      for (int d = 1; d < lanes; d <<= 1) {
+        const uint32_t f = __shfl_xor_sync(kFull, first, d), s = __shfl_xor_sync(kFull, second, d);
+        second = max(max(second, s), min(first, f));
+        first = max(first, f);
       }
-      if (lane == j) worth = w;
+      worth = __shfl_sync(kFull, merged(first, second), (lane * lanes) & 31);
+      if (lane >= o.groups) worth = 0u;
+    } else {
+      for (int j = 0; j < o.groups; ++j) {
+        uint32_t first = 0u, second = 0u;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+          const int e = lane * PER + i;
+          if (e >= E || static_cast<int>((e * o.group_mul) >> 22) != j) continue;
+          const uint32_t v = by_score ? key_of(o.sigmoid ? sigmoid(l[i]) : exp_below(l[i], top) / sum) : key[i];
+          second = max(second, min(first, v));
+          first = max(first, v);
+        }
+        const uint32_t best = __reduce_max_sync(kFull, first);
+        uint32_t next = 0u;
+        if (o.group_top == 2) {
+          const int has = __ffs(__ballot_sync(kFull, first == best)) - 1;  // one lane gives its best up
+          next = __reduce_max_sync(kFull, lane == has ? second : first);
+        }
+        const uint32_t w = merged(best, next);
+        if (lane == j) worth = w;
+      }
     }
     uint32_t kept = 0u;
     for (int j = 0; j < o.top_groups; ++j) {
@@ -124,26 +178,30 @@ __global__ void __launch_bounds__(32 * kRouteWarps)
     }
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-      const int e = i * 32 + lane;
+      const int e = lane * PER + i;
       if (e < E && !((kept >> ((e * o.group_mul) >> 22)) & 1u)) key[i] = 0u;
     }
   }
 
   int mine = 0;  // lane j: the j-th choice
   for (int j = 0; j < o.k; ++j) {
-    uint32_t best = 0u;
+    uint32_t mine_best = 0u;
 #pragma unroll
-    for (int i = 0; i < PER; ++i) best = max(best, key[i]);
-    best = __reduce_max_sync(kFull, best);
-    uint32_t place = 0xffffffffu;
+    for (int i = 0; i < PER; ++i) mine_best = max(mine_best, key[i]);
+    const uint32_t best = __reduce_max_sync(kFull, mine_best);
+    // the lowest lane that has it holds the lowest such places; the first of its own is the choice
+    const int has = __ffs(__ballot_sync(kFull, mine_best == best)) - 1;
+    int place = 0;
 #pragma unroll
     for (int i = PER - 1; i >= 0; --i)
-      if (key[i] == best) place = i * 32 + lane;
-    place = __reduce_min_sync(kFull, place);
+      if (key[i] == best) place = i;
+    if (lane == has) {
 #pragma unroll
-    for (int i = 0; i < PER; ++i)
-      if (place == static_cast<uint32_t>(i * 32 + lane)) key[i] = 0u;
-    if (lane == j) mine = static_cast<int>(place);
+      for (int i = 0; i < PER; ++i)
+        if (i == place) key[i] = 0u;
+    }
+    place = __shfl_sync(kFull, place, has) + has * PER;
+    if (lane == j) mine = place;
   }
 
   float w = 0.0f;
@@ -164,9 +222,14 @@ __global__ void __launch_bounds__(32 * kRouteWarps)
 }
 
 template <int DT>
-cudaError_t launch_dt(const void *logits, int64_t T, int E, int64_t ld, const float *bias, const RouteParams &o,
+cudaError_t launch_dt(const void *logits, int64_t T, int E, int64_t ld, const float *bias, RouteParams o,
                       float *weights, int32_t *ids, cudaStream_t stream) {
-  const int per = (E + 31) / 32;
+  int per = 1;
+  while (per * 32 < E) per *= 2;
+  const int size = E / o.groups, lanes = size % per == 0 ? size / per : 0;
+  const int bytes = DT == kDtypeF32 ? 4 : 2;
+  o.wide = E == 32 * per && ld * bytes % 16 == 0 && reinterpret_cast<uintptr_t>(logits) % 16 == 0;
+  o.group_lanes = lanes > 0 && (lanes & (lanes - 1)) == 0 ? lanes : 0;
   auto kern = per <= 1   ? route_kernel<DT, 1>
               : per <= 2 ? route_kernel<DT, 2>
               : per <= 4 ? route_kernel<DT, 4>
