@@ -182,7 +182,7 @@ __device__ __forceinline__ void split_pair(float p, float q, uint32_t *hi, uint3
   *lo = out_bits2<DT>(isinf(ph) ? 0.0f : p - ph, isinf(qh) ? 0.0f : q - qh);
 }
 
-constexpr int kAhead = 4;   // stretches of base that a warp has in flight
+constexpr int kAhead = 2;   // stretches of base that a warp has in flight
 constexpr int kAheadB = 2;  // stretches of B
 
 // Asynchronous copy of BYTES (8 or 16), of which the first `have` are read and the rest is zero.
@@ -199,19 +199,234 @@ __device__ __forceinline__ void copies_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// Shared memory of an expand block: v, then B's stretches and base's (or the sums of rows of odd length) of each warp.
+// Shared memory of an expand block. Both kernels: v; each warp's ring of B's stretches, every lane its own part. Rows of 16-byte
+// pieces (wide): the rows' operands, factors and offsets, each warp's ring of base's stretches. Else: each warp's sums.
 template <int RW, int KB, bool WIDE>
 struct Expand {
   static constexpr int kLd = KB * 16 + 4;
   static constexpr int P = KB == 1 ? 1 : KB / 2;  // loads of B a product: 8 bytes a lane at ranks up to 16, else 16
   static constexpr int kLoad = KB == 1 ? 8 : 16;
-  static constexpr int kV = (16 * RW * kLd * 4 + 15) / 16 * 16;
-  static constexpr int kB = kAheadB * 4 * P * 32 * kLoad;
+  static constexpr int kWords = kLoad / 4;
+  static constexpr int kStageB = 4 * P * 32 * kLoad;
   static constexpr int kLdSums = 66;
-  static constexpr int kBase = WIDE ? kAhead * 2 * 32 * 16 : 16 * kLdSums * 4;
-  static constexpr int kBytes = kV + kWarps * (kB + kBase);
+  static constexpr int kV = (16 * RW * kLd * 4 + 15) / 16 * 16;
+  static constexpr int kStageBase = RW * 2 * 32 * 16;
+  static constexpr int kWarp = kAheadB * kStageB + (WIDE ? kAhead * kStageBase : 16 * kLdSums * 4);
+  static constexpr int kWarp0 = WIDE ? 0 : kV;  // wide: once the operands are made the rings take v's place
+  static constexpr int kRings = kWarp0 + kWarps * kWarp;
+  static constexpr int kFrags = kRings > kV ? kRings : kV;                      // [row group][KB][hi, lo][lane] 16 bytes
+  static constexpr int kOffsets = kFrags + (WIDE ? RW * KB * 2 * 32 * 16 : 0);  // [row] offset in y, in base
+  static constexpr int kFactors = kOffsets + (WIDE ? 16 * RW * 16 : 0);         // [row] factor of the sums, divisor's inverse
+  static constexpr int kBytes = kFactors + (WIDE ? 16 * RW * 8 : 0);
+  // that an SM's 228 KB hold, each with 1 KB of the system's
+  static constexpr int kBlocks = kBytes > 113 * 1024 ? 1 : kBytes > 75 * 1024 ? 2 : 3;
 };
 
+// The tile's v to shared memory; zero past the rows and past the adapter's rank, whatever stands there.
+template <int ROWS, int KB, int LD>
+__device__ __forceinline__ void load_v(float (*vs)[LD], const float *__restrict__ v, int row0, int rows, int rank, int rank_all) {
+  for (int i = threadIdx.x; i < ROWS * KB * 4; i += 32 * kWarps) {
+    const int r = i / (KB * 4), k = i % (KB * 4) * 4;
+    float4 p = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (r < rows && k < rank) {
+      p = __ldg(reinterpret_cast<const float4 *>(v + (static_cast<int64_t>(row0) + r) * rank_all + k));
+      if (k + 1 >= rank) p.y = 0.0f;
+      if (k + 2 >= rank) p.z = 0.0f;
+      if (k + 3 >= rank) p.w = 0.0f;
+    }
+    *reinterpret_cast<float4 *>(&vs[r][k]) = p;
+  }
+}
+
+// What a row of v is multiplied by (down) before its operands are made, and its sums after (mul).
+template <int DT>
+__device__ __forceinline__ void row_factors(float top, float scale, float *down, float *mul) {
+  *down = 1.0f;
+  *mul = scale;
+  if (DT == kDtypeF16 && top > 0.0f && top < INFINITY) {
+    // 2^e <= top < 2^(e + 1), e kept where 2^e and 2^-e are normal: the row divided by 2^e has its largest in [1, 2)
+    const int e = min(max(static_cast<int>(__float_as_uint(top) >> 23) - 127, -100), 100);
+    *down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+    *mul = scale * __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+  }
+}
+
+// A lane's four k of product b: a half of its load of B.
+template <int KB>
+__device__ __forceinline__ int k_of(int b, int t) {
+  return KB == 1 ? 4 * t : 32 * (b / 2) + 8 * t + 4 * (b % 2);
+}
+
+// Copies a stretch of 32 columns of B ahead: the lane's part of four products, whose columns are dealt so that lane t then
+// holds the eight columns of y from 8 t on.
+template <typename E>
+__device__ __forceinline__ void fetch_b(uint32_t to, const uint16_t *B, int n0, int N, int rank, int rank_all, const void *any) {
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int n = n0 + 8 * (g >> 1) + 2 * j + (g & 1);  // product j's column g
+#pragma unroll
+    for (int q = 0; q < E::P; ++q) {
+      const int k = q * (E::kLoad * 2) + t * (E::kLoad / 2);
+      const int have = n < N ? min(max(2 * (rank - k), 0), E::kLoad) : 0;
+      copy_ahead<E::kLoad>(to + ((j * E::P + q) * 32 + lane) * E::kLoad,
+                           have ? B + static_cast<int64_t>(n) * rank_all + k : any, have);
+    }
+  }
+}
+
+template <typename E>
+__device__ __forceinline__ void load_b(uint32_t (&w)[E::P][E::kWords], uint32_t stage, int j) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int q = 0; q < E::P; ++q) {
+    const uint32_t at = stage + ((j * E::P + q) * 32 + lane) * E::kLoad;
+    if (E::kLoad == 16) {
+      const uint4 v4 = lds128(at);
+      w[q][0] = v4.x, w[q][1] = v4.y, w[q][2 % E::kWords] = v4.z, w[q][3 % E::kWords] = v4.w;
+    } else {
+      asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w[q][0]), "=r"(w[q][1]) : "r"(at) : "memory");
+    }
+  }
+}
+
+// Product b of one column tile: lo before hi, so that the small terms are added first.
+template <int DT, int KB, typename E>
+__device__ __forceinline__ void product(float (&acc)[4], const uint32_t (&w)[E::P][E::kWords], int b, uint4 hi, uint4 lo) {
+  const uint32_t b0 = w[KB == 1 ? 0 : b / 2][KB == 1 ? 0 : 2 * (b % 2)];
+  const uint32_t b1 = w[KB == 1 ? 0 : b / 2][KB == 1 ? 1 : 2 * (b % 2) + 1];
+  mma_16816<DT>(acc, lo.x, lo.y, lo.z, lo.w, b0, b1);
+  mma_16816<DT>(acc, hi.x, hi.y, hi.z, hi.w, b0, b1);
+}
+
+// y = base + scaling * B[a] . v for a tile of 16 RW rows whose rows of y and base are 16-byte aligned. A warp takes every
+// eighth stretch of 32 columns for all the tile's rows: B's stretch is read once, base's are copied ahead (as loads to
+// registers, or with a warp to each 16 rows, too few bytes were in flight: 3.6 TB/s).
+template <int DT, int RW, int KB>
+__global__ void __launch_bounds__(32 * kWarps, Expand<RW, KB, true>::kBlocks)
+    lora_expand_wide_kernel(const Tiles ts, const LoraArgs a, const float *__restrict__ v) {
+  using E = Expand<RW, KB, true>;
+  extern __shared__ __align__(16) uint8_t smem[];
+  float(*vs)[E::kLd] = reinterpret_cast<float(*)[E::kLd]>(smem);
+  uint4 *frags = reinterpret_cast<uint4 *>(smem + E::kFrags);
+  int64_t(*offsets)[2] = reinterpret_cast<int64_t(*)[2]>(smem + E::kOffsets);
+  float(*factors)[2] = reinterpret_cast<float(*)[2]>(smem + E::kFactors);
+  griddep_launch_dependents();
+  griddep_wait();
+  int key, row0, rows;
+  if (!get_tile(ts, blockIdx.x, a.adapters, &key, &row0, &rows)) return;
+  if (key < 0 && a.base == a.y) return;  // rows without an adapter, in place
+  const int rank = key < 0 ? 0 : a.ranks ? min(max(a.ranks[key], 0), a.rank) : a.rank;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = lane >> 2, t = lane & 3;
+  const int N = static_cast<int>(a.N);
+  const float scale = key >= 0 && a.scaling ? a.scaling[key] : 1.0f;
+
+  if (threadIdx.x < 16 * RW) {
+    const int64_t row = static_cast<int>(threadIdx.x) < rows ? row_at(ts, row0 + threadIdx.x) : 0;
+    offsets[threadIdx.x][0] = row * a.ldy;
+    offsets[threadIdx.x][1] = row * a.ldbase;
+  }
+  load_v<16 * RW, KB>(vs, v, row0, rows, rank, a.rank);
+  __syncthreads();
+  if (threadIdx.x < 16 * RW) {
+    float top = 0.0f;
+    if (DT == kDtypeF16)
+      for (int k = 0; k < KB * 16; ++k) top = fmaxf(top, fabsf(vs[threadIdx.x][k]));
+    row_factors<DT>(top, scale, &factors[threadIdx.x][1], &factors[threadIdx.x][0]);
+  }
+  __syncthreads();
+  for (int i = warp; i < RW * KB; i += kWarps) {
+    const int rg = i / KB, b = i % KB;
+    uint32_t hi[4], lo[4];
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+      const int r = rg * 16 + m * 8 + g;
+      const float down = factors[r][1];
+      const float4 p = *reinterpret_cast<const float4 *>(&vs[r][k_of<KB>(b, t)]);
+      split_pair<DT>(p.x * down, p.y * down, &hi[m], &lo[m]);
+      split_pair<DT>(p.z * down, p.w * down, &hi[2 + m], &lo[2 + m]);
+    }
+    frags[(i * 2 + 0) * 32 + lane] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+    frags[(i * 2 + 1) * 32 + lane] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+  }
+  __syncthreads();
+
+  const uint16_t *B = static_cast<const uint16_t *>(a.B) + static_cast<int64_t>(max(key, 0)) * N * a.rank;
+  const uint16_t *base = static_cast<const uint16_t *>(a.base);
+  uint16_t *y = static_cast<uint16_t *>(a.y);
+  uint8_t *mine = smem + E::kWarp0 + warp * E::kWarp;
+  const uint32_t b_ring = smem_u32(mine);
+  uint4 *const ahead = reinterpret_cast<uint4 *>(mine + kAheadB * E::kStageB) + lane;
+  auto fetch = [&](int n0, int slot) {
+    const int n = n0 + 8 * t;
+#pragma unroll
+    for (int m = 0; m < 2 * RW; ++m) {
+      const int r = m * 8 + g;
+      const int bytes = base && r < rows && n < N ? min(2 * (N - n), 16) : 0;
+      cp_async16_zfill(smem_u32(ahead + (slot * 2 * RW + m) * 32), bytes ? base + offsets[r][1] + n : a.B, bytes);
+    }
+  };
+  const int first = (blockIdx.y * kWarps + warp) * 32, step = gridDim.y * kWarps * 32;
+  static_assert(kAhead >= kAheadB, "base's copies lead");
+  // the groups of copies in order: base's first stretches, then with each of B's the base kAhead - kAheadB after it
+#pragma unroll
+  for (int i = 0; i < kAhead - kAheadB; ++i) fetch(first + i * step, i);
+#pragma unroll
+  for (int i = 0; i < kAheadB - 1; ++i) {
+    fetch_b<E>(b_ring + i * E::kStageB, B, first + i * step, N, rank, a.rank, a.B);
+    fetch(first + (i + kAhead - kAheadB) * step, i + kAhead - kAheadB);
+    copies_commit();
+  }
+  int slot = 0, slot_b = 0;
+  for (int n0 = first; n0 < N; n0 += step) {
+    fetch_b<E>(b_ring + (slot_b + kAheadB - 1) % kAheadB * E::kStageB, B, n0 + (kAheadB - 1) * step, N, rank, a.rank, a.B);
+    fetch(n0 + (kAhead - 1) * step, (slot + kAhead - 1) % kAhead);
+    copies_commit();
+    copies_wait<kAheadB - 1>();
+    const int n = n0 + 8 * t;
+    uint32_t w[4][E::P][E::kWords];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) load_b<E>(w[j], b_ring + slot_b * E::kStageB, j);
+#pragma unroll 1
+    for (int rg = 0; rg < RW && rg * 16 < rows; ++rg) {
+      float acc[4][4] = {};
+      if (key >= 0) {
+#pragma unroll
+        for (int b = 0; b < KB; ++b) {
+          const uint4 hi = frags[((rg * KB + b) * 2 + 0) * 32 + lane], lo = frags[((rg * KB + b) * 2 + 1) * 32 + lane];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) product<DT, KB, E>(acc[j], w[j], b, hi, lo);
+        }
+      }
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        const int r = rg * 16 + m * 8 + g;
+        if (r >= rows || n >= N) continue;
+        const uint4 old = ahead[(slot * 2 * RW + rg * 2 + m) * 32];
+        uint32_t out[4] = {old.x, old.y, old.z, old.w};
+        if (key >= 0) {
+          const float mul = factors[r][0];
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            out[j] = out_bits2<DT>(value_f32<DT>(out[j] & 0xffffu) + mul * acc[j][2 * m],
+                                   value_f32<DT>(out[j] >> 16) + mul * acc[j][2 * m + 1]);
+        }
+        uint16_t *to = y + offsets[r][0] + n;
+        if (n + 8 <= N) {
+          *reinterpret_cast<uint4 *>(to) = make_uint4(out[0], out[1], out[2], out[3]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (n + i < N) to[i] = static_cast<uint16_t>(out[i / 2] >> (16 * (i & 1)));
+        }
+      }
+    }
+    slot = (slot + 1) % kAhead;
+    slot_b = (slot_b + 1) % kAheadB;
+  }
+  copies_wait<0>();
+}
 
 // Stores values n and n + 1 of a row (those that lie in 0 .. N - 1), p + n 4-byte aligned.
 __device__ __forceinline__ void store_two(uint16_t *p, int n, int N, uint32_t v) {
@@ -222,17 +437,14 @@ __device__ __forceinline__ void store_two(uint16_t *p, int n, int N, uint32_t v)
   if (n < N) p[n] = static_cast<uint16_t>(v);
 }
 
-// y = base + scaling * B[a] . v for a tile of 16 RW rows: warp (w % RW, w / RW) has 16 rows and every CW-th stretch of 32
-// columns, four products whose columns are dealt so that lane t holds the eight from 8 t on. WIDE: rows of y and base
-// are 16-byte aligned, and base's next stretches are copied ahead to shared memory (one stretch at a time in registers
-// kept too few bytes in flight: 3.6 TB/s). Else (rows of odd length) the sums of two stretches go through shared memory,
-// so that a warp reads and writes 64 consecutive columns of a row, in pairs from the row's first 4-byte boundary.
-template <int DT, int RW, int KB, bool WIDE>
-__global__ void __launch_bounds__(32 * kWarps, KB <= 2 && WIDE ? 3 : KB <= 4 ? 2 : 1)
+// The same for rows that are not 16-byte aligned (of odd length, say): warp (w % RW, w / RW) has 16 rows and every CW-th
+// stretch of 64 columns, whose sums go through shared memory, so that the warp reads and writes consecutive columns of a
+// row, in pairs from the row's first 4-byte boundary.
+template <int DT, int RW, int KB>
+__global__ void __launch_bounds__(32 * kWarps, KB <= 4 ? 2 : 1)
     lora_expand_kernel(const Tiles ts, const LoraArgs a, const float *__restrict__ v) {
-  using E = Expand<RW, KB, WIDE>;
+  using E = Expand<RW, KB, false>;
   constexpr int CW = kWarps / RW;
-  constexpr int P = E::P, kLoad = E::kLoad, WORDS = kLoad / 4;
   extern __shared__ __align__(16) uint8_t smem[];
   float(*vs)[E::kLd] = reinterpret_cast<float(*)[E::kLd]>(smem);
   griddep_launch_dependents();
@@ -244,214 +456,108 @@ __global__ void __launch_bounds__(32 * kWarps, KB <= 2 && WIDE ? 3 : KB <= 4 ? 2
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
   const int N = static_cast<int>(a.N);
+  const float scale = key >= 0 && a.scaling ? a.scaling[key] : 1.0f;
 
   const int r0 = warp % RW * 16;
   int64_t row[2];  // read beside v
 #pragma unroll
   for (int m = 0; m < 2; ++m) row[m] = r0 + m * 8 + g < rows ? row_at(ts, row0 + r0 + m * 8 + g) : 0;
-
-  // the tile's v; zero past the rows and past the adapter's rank, whatever stands there
-  for (int i = threadIdx.x; i < 16 * RW * KB * 4; i += 32 * kWarps) {
-    const int r = i / (KB * 4), k = i % (KB * 4) * 4;
-    float4 p = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    if (r < rows && k < rank) {
-      p = __ldg(reinterpret_cast<const float4 *>(v + (static_cast<int64_t>(row0) + r) * a.rank + k));
-      if (k + 1 >= rank) p.y = 0.0f;
-      if (k + 2 >= rank) p.z = 0.0f;
-      if (k + 3 >= rank) p.w = 0.0f;
-    }
-    *reinterpret_cast<float4 *>(&vs[r][k]) = p;
-  }
+  load_v<16 * RW, KB>(vs, v, row0, rows, rank, a.rank);
   __syncthreads();
   if (r0 >= rows) return;
-  const float scale = key >= 0 && a.scaling ? a.scaling[key] : 1.0f;
 
   int64_t yr[2], br[2];  // the rows' first values in y and base
-  bool has[2];
   float mul[2];
   uint32_t hi[KB][4], lo[KB][4];
 #pragma unroll
   for (int m = 0; m < 2; ++m) {
     const int r = r0 + m * 8 + g;
-    has[m] = r < rows;
     yr[m] = row[m] * a.ldy;
     br[m] = row[m] * a.ldbase;
-    float down = 1.0f;
-    mul[m] = scale;
+    float top = 0.0f, down;
     if (DT == kDtypeF16) {
-      float top = 0.0f;
       for (int k = t; k < KB * 16; k += 4) top = fmaxf(top, fabsf(vs[r][k]));
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-      // 2^e <= top < 2^(e + 1), e kept where 2^e and 2^-e are normal: the row divided by 2^e has its largest in [1, 2)
-      const int e = min(max(static_cast<int>(__float_as_uint(top) >> 23) - 127, -100), 100);
-      if (top > 0.0f && top < INFINITY) {
-        down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-        mul[m] = scale * __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
-      }
     }
+    row_factors<DT>(top, scale, &down, &mul[m]);
 #pragma unroll
     for (int b = 0; b < KB; ++b) {
-      // the lane's four k of product b: the half of its load of B
-      const int k = KB == 1 ? 4 * t : 32 * (b / 2) + 8 * t + 4 * (b % 2);
-      const float4 p = *reinterpret_cast<const float4 *>(&vs[r][k]);
+      const float4 p = *reinterpret_cast<const float4 *>(&vs[r][k_of<KB>(b, t)]);
       split_pair<DT>(p.x * down, p.y * down, &hi[b][m], &lo[b][m]);
       split_pair<DT>(p.z * down, p.w * down, &hi[b][2 + m], &lo[b][2 + m]);
     }
   }
 
-  // each lane's own part of B's stretches, and of base's: nobody else reads what a lane copies
-  uint8_t *mine = smem + E::kV + warp * (E::kB + E::kBase);
-  const uint32_t b_at = smem_u32(mine) + lane * kLoad;
-  uint4 *const ahead = reinterpret_cast<uint4 *>(mine + E::kB) + lane;                       // WIDE
-  float(*sums)[E::kLdSums] = reinterpret_cast<float(*)[E::kLdSums]>(mine + E::kB);  // else
   const uint16_t *B = static_cast<const uint16_t *>(a.B) + static_cast<int64_t>(max(key, 0)) * N * a.rank;
   const uint16_t *base = static_cast<const uint16_t *>(a.base);
   uint16_t *y = static_cast<uint16_t *>(a.y);
-  auto fetch_b = [&](int n0, int slot) {
+  uint8_t *mine = smem + E::kWarp0 + warp * E::kWarp;
+  const uint32_t b_ring = smem_u32(mine);
+  float(*sums)[E::kLdSums] = reinterpret_cast<float(*)[E::kLdSums]>(mine + kAheadB * E::kStageB);
+  const int first = (blockIdx.y * CW + warp / RW) * 64, step = gridDim.y * CW * 64;
+  static_assert(kAheadB == 2, "a stretch's halves take the ring's places in turn");
+  fetch_b<E>(b_ring, B, first, N, rank, a.rank, a.B);
+  copies_commit();
+  for (int n0 = first; n0 < N; n0 += step) {
+    // base's pairs start at y's 4-byte boundary in the row; the value before it takes the place of the pair past the
+    // end. The loads are predicated, not branched around, and joined only after the products
+    const int end = min(N, n0 + 64);
+    uint32_t both[16], low[16], high[16];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int n = n0 + 8 * (g >> 1) + 2 * j + (g & 1);  // product j's column g
-#pragma unroll
-      for (int q = 0; q < P; ++q) {
-        const int k = q * (kLoad * 2) + t * (kLoad / 2);
-        const int have = n < N ? min(max(2 * (rank - k), 0), kLoad) : 0;
-        copy_ahead<kLoad>(b_at + (slot * 4 * P + j * P + q) * 32 * kLoad,
-                          have ? B + static_cast<int64_t>(n) * a.rank + k : a.B, have);
-      }
+    for (int i = 0; i < 16; ++i) {
+      const uint16_t *bp = base + __shfl_sync(0xffffffffu, br[i / 8], i % 8 * 4);
+      const uint16_t *yp = y + __shfl_sync(0xffffffffu, yr[i / 8], i % 8 * 4);
+      const int odd = (reinterpret_cast<uintptr_t>(yp + n0) >> 1) & 1;
+      const int n = n0 + 2 * lane - odd;
+      const int lo = n < n0 ? n0 + 63 : n;
+      const bool in = base && r0 + i < rows;
+      const bool pair = in && n >= n0 && n + 1 < end && (reinterpret_cast<uintptr_t>(bp + n) & 3) == 0;
+      both[i] = pair ? *reinterpret_cast<const uint32_t *>(bp + n) : 0u;
+      low[i] = in && !pair && lo < end ? bp[lo] : 0u;
+      high[i] = in && !pair && n + 1 < end ? bp[n + 1] : 0u;
     }
-  };
-  // four products of a stretch of 32 columns
-  auto products = [&](int slot, float (&acc)[4][4]) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      uint32_t w[P][WORDS];
-#pragma unroll
-      for (int q = 0; q < P; ++q) {
-        const uint32_t at = b_at + (slot * 4 * P + j * P + q) * 32 * kLoad;
-        if (kLoad == 16) {
-          const uint4 v4 = lds128(at);
-          w[q][0] = v4.x, w[q][1] = v4.y, w[q][2 % WORDS] = v4.z, w[q][3 % WORDS] = v4.w;
-        } else {
-          asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w[q][0]), "=r"(w[q][1]) : "r"(at) : "memory");
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) acc[j][i] = 0.0f;
-#pragma unroll
-      for (int b = 0; b < KB; ++b) {
-        const uint32_t b0 = w[KB == 1 ? 0 : b / 2][KB == 1 ? 0 : 2 * (b % 2)];
-        const uint32_t b1 = w[KB == 1 ? 0 : b / 2][KB == 1 ? 1 : 2 * (b % 2) + 1];
-        mma_16816<DT>(acc[j], lo[b][0], lo[b][1], lo[b][2], lo[b][3], b0, b1);
-        mma_16816<DT>(acc[j], hi[b][0], hi[b][1], hi[b][2], hi[b][3], b0, b1);
-      }
-    }
-  };
-  constexpr int kCols = WIDE ? 32 : 64;
-  const int first = (blockIdx.y * CW + warp / RW) * kCols, step = gridDim.y * CW * kCols;
-  if (WIDE) {
-    auto fetch = [&](int n0, int slot) {
-#pragma unroll
-      for (int m = 0; m < 2; ++m) {
-        const int n = n0 + 8 * t;
-        const int bytes = base && has[m] && n < N ? min(2 * (N - n), 16) : 0;
-        cp_async16_zfill(smem_u32(ahead + (slot * 2 + m) * 32), bytes ? base + br[m] + n : a.B, bytes);
-      }
-    };
-    // the groups of copies in order: base's first stretches, then with each of B's the base kAhead - kAheadB after it
-    int slot = 0;
-#pragma unroll
-    for (int i = 0; i < kAhead - kAheadB; ++i) fetch(first + i * step, i);
-#pragma unroll
-    for (int i = 0; i < kAheadB - 1; ++i) {
-      fetch_b(first + i * step, i);
-      fetch(first + (i + kAhead - kAheadB) * step, i + kAhead - kAheadB);
-      copies_commit();
-    }
-    for (int n0 = first; n0 < N; n0 += step) {
-      fetch_b(n0 + (kAheadB - 1) * step, (slot + kAheadB - 1) % kAheadB);
-      fetch(n0 + (kAhead - 1) * step, (slot + kAhead - 1) % kAhead);
-      copies_commit();
-      copies_wait<kAheadB - 1>();
-      float acc[4][4];
-      if (key >= 0) products(slot % kAheadB, acc);
-      const int n = n0 + 8 * t;
-#pragma unroll
-      for (int m = 0; m < 2; ++m) {
-        if (!has[m] || n >= N) continue;
-        const uint4 old = ahead[(slot * 2 + m) * 32];
-        uint32_t out[4] = {old.x, old.y, old.z, old.w};
-        if (key >= 0) {
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            out[j] = out_bits2<DT>(value_f32<DT>(out[j] & 0xffffu) + mul[m] * acc[j][2 * m],
-                                   value_f32<DT>(out[j] >> 16) + mul[m] * acc[j][2 * m + 1]);
-        }
-        if (n + 8 <= N) {
-          *reinterpret_cast<uint4 *>(y + yr[m] + n) = make_uint4(out[0], out[1], out[2], out[3]);
-        } else {
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            if (n + i < N) y[yr[m] + n + i] = static_cast<uint16_t>(out[i / 2] >> (16 * (i & 1)));
-        }
-      }
-      slot = (slot + 1) % kAhead;
-    }
-  } else {
-    fetch_b(first, 0);
-    copies_commit();
-    for (int n0 = first; n0 < N; n0 += step) {
-      // base's pairs start at y's 4-byte boundary in the row; the value before it takes the place of the pair past the
-      // end. The loads are predicated, not branched around, and joined only after the products
-      const int end = min(N, n0 + 64);
-      uint32_t both[16], low[16], high[16];
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const uint16_t *bp = base + __shfl_sync(0xffffffffu, br[i / 8], i % 8 * 4);
-        const uint16_t *yp = y + __shfl_sync(0xffffffffu, yr[i / 8], i % 8 * 4);
-        const int odd = (reinterpret_cast<uintptr_t>(yp + n0) >> 1) & 1;
-        const int n = n0 + 2 * lane - odd;
-        const int lo = n < n0 ? n0 + 63 : n;
-        const bool in = base && r0 + i < rows;
-        const bool pair = in && n >= n0 && n + 1 < end && (reinterpret_cast<uintptr_t>(bp + n) & 3) == 0;
-        both[i] = pair ? *reinterpret_cast<const uint32_t *>(bp + n) : 0u;
-        low[i] = in && !pair && lo < end ? bp[lo] : 0u;
-        high[i] = in && !pair && n + 1 < end ? bp[n + 1] : 0u;
-      }
-      __syncwarp();  // the stretch before has been read
+    __syncwarp();  // the stretch before has been read
 #pragma unroll 1
-      for (int h = 0; h < 2; ++h) {
-        fetch_b(h == 0 ? n0 + 32 : n0 + step, 1 - h);
-        copies_commit();
-        copies_wait<1>();
-        if (key < 0) continue;
-        float acc[4][4];
-        products(h, acc);
+    for (int h = 0; h < 2; ++h) {
+      fetch_b<E>(b_ring + (1 - h) * E::kStageB, B, h == 0 ? n0 + 32 : n0 + step, N, rank, a.rank, a.B);
+      copies_commit();
+      copies_wait<1>();
+      if (key < 0) continue;
+      float acc[4][4] = {};
 #pragma unroll
-        for (int m = 0; m < 2; ++m)
+      for (int j = 0; j < 4; ++j) {
+        uint32_t w[E::P][E::kWords];
+        load_b<E>(w, b_ring + h * E::kStageB, j);
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            *reinterpret_cast<float2 *>(&sums[m * 8 + g][32 * h + 8 * t + 2 * j]) =
-                make_float2(mul[m] * acc[j][2 * m], mul[m] * acc[j][2 * m + 1]);
+        for (int b = 0; b < KB; ++b)
+          product<DT, KB, E>(acc[j], w, b, make_uint4(hi[b][0], hi[b][1], hi[b][2], hi[b][3]),
+                             make_uint4(lo[b][0], lo[b][1], lo[b][2], lo[b][3]));
       }
-      __syncwarp();
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        uint16_t *yp = y + __shfl_sync(0xffffffffu, yr[i / 8], i % 8 * 4);
-        if (r0 + i >= rows) continue;
-        const int odd = (reinterpret_cast<uintptr_t>(yp + n0) >> 1) & 1;
-        const int c = 2 * lane - odd;
-        uint32_t out = both[i] | low[i] | high[i] << 16;
-        if (key >= 0) {
-          const float *sum = sums[i];
-          out = out_bits2<DT>(value_f32<DT>(out & 0xffffu) + sum[c < 0 ? 63 : c], value_f32<DT>(out >> 16) + sum[c + 1]);
-        }
-        if (c >= 0) {
-          store_two(yp, n0 + c, end, out);
-        } else {
-          if (n0 + 63 < end) yp[n0 + 63] = static_cast<uint16_t>(out);
-          yp[n0] = static_cast<uint16_t>(out >> 16);
-        }
+      for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          *reinterpret_cast<float2 *>(&sums[m * 8 + g][32 * h + 8 * t + 2 * j]) =
+              make_float2(mul[m] * acc[j][2 * m], mul[m] * acc[j][2 * m + 1]);
+    }
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      uint16_t *yp = y + __shfl_sync(0xffffffffu, yr[i / 8], i % 8 * 4);
+      if (r0 + i >= rows) continue;
+      const int odd = (reinterpret_cast<uintptr_t>(yp + n0) >> 1) & 1;
+      const int c = 2 * lane - odd;
+      uint32_t out = both[i] | low[i] | high[i] << 16;
+      if (key >= 0) {
+        const float *sum = sums[i];
+        out = out_bits2<DT>(value_f32<DT>(out & 0xffffu) + sum[c < 0 ? 63 : c], value_f32<DT>(out >> 16) + sum[c + 1]);
+      }
+      if (c >= 0) {
+        store_two(yp, n0 + c, end, out);
+      } else {
+        if (n0 + 63 < end) yp[n0 + 63] = static_cast<uint16_t>(out);
+        yp[n0] = static_cast<uint16_t>(out >> 16);
       }
     }
   }
@@ -507,14 +613,18 @@ cudaError_t launch_grid(void (*kern)(Args...), dim3 grid, int cluster, int smem,
 template <int DT, int RW, int KB, bool WIDE>
 cudaError_t launch_expand(const Tiles &ts, const LoraArgs &a, const LoraPlan &p, const float *v, int num_sms,
                           cudaStream_t stream) {
-  auto kern = lora_expand_kernel<DT, RW, KB, WIDE>;
+  void (*kern)(const Tiles, const LoraArgs, const float *);
+  if constexpr (WIDE)
+    kern = lora_expand_wide_kernel<DT, RW, KB>;
+  else
+    kern = lora_expand_kernel<DT, RW, KB>;
   constexpr int bytes = Expand<RW, KB, WIDE>::kBytes;
   static std::atomic<uint64_t> set{0};
   const cudaError_t e = allow_smem(kern, bytes, &set);
   if (e != cudaSuccess) return e;
   // columns: as many blocks as run at a time, no more than one turn of a block's warps each
-  const int64_t turns = cdiv(a.N, (WIDE ? 32 : 64) * kWarps / RW);
-  const int64_t want = (KB <= 2 && WIDE ? 3 : KB <= 4 ? 2 : 1) * num_sms / p.max_tiles;
+  const int64_t turns = cdiv(a.N, WIDE ? 32 * kWarps : 64 * kWarps / RW);
+  const int64_t want = (WIDE ? Expand<RW, KB, true>::kBlocks : KB <= 4 ? 2 : 1) * num_sms / p.max_tiles;
   return launch_grid(kern, dim3(p.max_tiles, static_cast<unsigned>(want < 1 ? 1 : want < turns ? want : turns)), 1, bytes,
                      stream, ts, a, v);
 }
