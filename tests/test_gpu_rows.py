@@ -481,3 +481,50 @@ def test_experts_no_rows_and_refusals():
         kw = dict(x=x, gate_up=m.gate_up, down=m.down, ids=ids, weights=w, inter=64, g=64) | bad
         with pytest.raises(ValueError):
             w4.w4a16_experts(**kw)
+
+
+def test_one_workspace_for_gemms_and_rows():
+    """A Workspace may serve the GEMMs, whose counters have to stay zero, and the calls here, which leave anything."""
+    ws = w4.Workspace()
+    W = randn(21, 512, 1024)
+    qw, s, z = w4.w4_pack(W, 128)
+    packed = w4.w4_repack(qw, s, z, 512, 1024, 128)
+    x = randn(22, 64, 1024)
+    want = w4.w4a16_gemm(x, packed, 512, 1024, 128, workspace=ws)
+    m = Experts(1024, 256, 4, 128, "f16")
+    for T in (1, 64):
+        ids, w = choices(3, T, 4, 2)
+        first = m.run(x[:T].contiguous(), ids, w, workspace=ws)
+        assert w4.w4_last_device_error(ws.scratch) == 0
+        assert torch.equal(w4.w4a16_gemm(x, packed, 512, 1024, 128, workspace=ws), want)
+        w4.w4_lora_add(None, x, randn(23, 2, 8, 1024), randn(24, 2, 64, 8), torch.zeros(64, dtype=torch.int32, device="cuda"),
+                       workspace=ws)
+        assert torch.equal(w4.w4a16_gemm(x, packed, 512, 1024, 128, workspace=ws), want)
+        assert torch.equal(m.run(x[:T].contiguous(), ids, w, workspace=ws), first)
+
+
+def test_rows_in_a_captured_graph():
+    """The three calls capture into a CUDA graph (no allocation, no synchronisation) and replay on new inputs."""
+    m = Experts(256, 128, 8, 128, "bf16")
+    x, base = randn(1, 40, 256, dtype="bf16"), randn(2, 40, 320, dtype="bf16")
+    A, B = randn(3, 3, 16, 256, dtype="bf16"), randn(4, 3, 320, 16, dtype="bf16")
+    adapter = (torch.arange(40) % 4 - 1).to(torch.int32).cuda()
+    logits = randn(5, 40, 8, dtype="bf16")
+    ws = w4.Workspace()
+
+    def step():
+        y = w4.w4_lora_add(base, x, A, B, adapter, workspace=ws)
+        w, ids = w4.w4_route(logits, 2)
+        return y, w, ids, m.run(x, ids, w, workspace=ws)
+
+    step()  # the workspace grows here
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step()
+    x.copy_(randn(6, 40, 256, dtype="bf16"))
+    logits.copy_(randn(7, 40, 8, dtype="bf16"))
+    graph.replay()
+    torch.cuda.synchronize()
+    for a, b in zip(got, step()):
+        assert torch.equal(a, b)

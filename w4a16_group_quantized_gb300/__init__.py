@@ -208,16 +208,24 @@ def w4a16_gemm_plan(M: int, N: int, K: int, g: int):
 
 
 class Workspace:
-    """A zero-filled device workspace that grows on demand (reuse it across calls on one stream)."""
+    """A zero-filled device workspace that grows on demand (reuse it across calls on one stream). ``scratch`` is a second
+    buffer, for the calls that leave arbitrary bytes behind (w4a16_experts, w4_lora_add): the GEMMs' counters in the
+    first have to stay zero."""
 
     def __init__(self, device=None):
         self.device = torch.device(device or "cuda")
         self.buf = torch.zeros(256, dtype=torch.uint8, device=self.device)
+        self.scratch = torch.zeros(256, dtype=torch.uint8, device=self.device)
 
     def get(self, nbytes: int) -> torch.Tensor:
         if self.buf.numel() < nbytes:
             self.buf = torch.zeros(max(nbytes, 2 * self.buf.numel()), dtype=torch.uint8, device=self.device)
         return self.buf
+
+    def get_scratch(self, nbytes: int) -> torch.Tensor:
+        if self.scratch.numel() < nbytes:
+            self.scratch = torch.empty(max(nbytes, 2 * self.scratch.numel()), dtype=torch.uint8, device=self.device)
+        return self.scratch
 
 
 def _gemm_common(x, packed, N, K, g, y, workspace, block_n, ctas, schedule, stream):
@@ -475,13 +483,13 @@ def _run_with(call, args, workspace, sized, device: int, stream, made, what: str
     if workspace is None:
         ws = own = torch.empty(max(sized(), 1), dtype=torch.uint8, device=f"cuda:{device}")
     else:
-        ws = workspace.buf if isinstance(workspace, Workspace) else workspace
+        ws = workspace.scratch if isinstance(workspace, Workspace) else workspace
         if ws.get_device() != device or not ws.is_contiguous():
             raise ValueError(f"workspace must be contiguous on cuda:{device}")
     handle = _handle(stream, device, made, own)
     rc = call(args, ws.data_ptr(), ws.nbytes, handle)
     if rc == 4 and isinstance(workspace, Workspace):
-        ws = workspace.get(sized())
+        ws = workspace.get_scratch(sized())
         rc = call(args, ws.data_ptr(), ws.nbytes, handle)
     if rc != 0:
         raise W4Error(rc, what)

@@ -132,7 +132,7 @@ int w4_lora_add(const w4_lora_args *a, void *workspace_dev, size_t workspace_byt
 
 size_t w4a16_experts_workspace_bytes(int64_t T, int64_t K, int64_t I, int32_t experts, int32_t k, int32_t g) {
   if (check_experts_sizes(T, K, I, experts, k, g) != W4_OK) return 0;
-  return w4::experts_workspace_bytes(T > 0 ? T : 1, K, I, experts, k, g, num_sms_current_device());
+  return w4::experts_workspace_bytes(T > 0 ? T : 1, K, I, experts, k, g);
 }
 
 int w4a16_experts(const w4a16_experts_args *a, void *workspace_dev, size_t workspace_bytes, void *stream) {
@@ -147,7 +147,7 @@ int w4a16_experts(const w4a16_experts_args *a, void *workspace_dev, size_t works
       !aligned(a->weights_dev, 4) || !aligned(a->y_dev, 16) || !aligned(workspace_dev, 256))
     return W4_ERR_MISALIGNED;
   const int sms = num_sms_current_device();
-  if (workspace_bytes < w4::experts_workspace_bytes(a->T, a->K, a->I, a->experts, a->k, a->g, sms))
+  if (workspace_bytes < w4::experts_workspace_bytes(a->T, a->K, a->I, a->experts, a->k, a->g))
     return W4_ERR_WORKSPACE_TOO_SMALL;
   w4::ExpertsArgs e;
   e.x = a->x_dev;

@@ -28,7 +28,7 @@ namespace {
 using namespace detail;
 
 constexpr int kSlabRows = 32;  // weight rows of a block
-constexpr int kTmemRows = 12;  // rows an expert has on average from which the tensor-memory kernel runs
+constexpr int kTmemRows = 8;  // rows an expert has on average from which the tensor-memory kernel runs
 
 // Eight codes -> four pairs (k, k + 1) of 16 + q: each code's bits moved to the top of the fraction that 16 leaves
 // (fp16: a step of 2^-6 at 16, bits 6 to 9; bf16: 2^-3, bits 3 to 6).
@@ -73,6 +73,7 @@ __global__ void __launch_bounds__(32 * NW, NT == 1 && NW == 8 ? 2 : 1) experts_k
   extern __shared__ __align__(128) uint8_t smem[];
   griddep_launch_dependents();
   griddep_wait();
+  if (DIRECT && GATED && blockIdx.x == 0 && threadIdx.x == 0) *p.err = 0u;  // (else the sort clears it)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
   const int kw = p.kw, part = warp % kw;
@@ -370,7 +371,7 @@ ExpertsPlan experts_plan(int64_t T, int64_t K, int64_t I, int experts, int k, in
   // (pairs that are few beside the experts seldom share one)
   p.direct = T == 1 || pairs <= experts / 4;
   p.tmem = !p.direct && mean >= kTmemRows && experts_tmem_takes(g);
-  p.tile = p.tmem ? (mean <= 48 || g % 64 != 0 ? 64 : 128) : mean <= 8 ? 8 : mean <= 16 ? 16 : 32;
+  p.tile = p.tmem ? (mean <= 64 || g % 64 != 0 ? 64 : 128) : mean <= 8 ? 8 : mean <= 16 ? 16 : 32;
   p.max_tiles = static_cast<int>(p.direct ? pairs : max_row_tiles(pairs, experts, p.tile));
   auto up = [](size_t v) { return (v + 255) / 256 * 256; };
   p.part = 256;
@@ -460,8 +461,7 @@ cudaError_t launch_dt(const ExpertsArgs &a, uint8_t *ws, const ExpertsPlan &plan
 
 }  // namespace
 
-size_t experts_workspace_bytes(int64_t T, int64_t K, int64_t I, int experts, int k, int g, int num_sms) {
-  (void)num_sms;
+size_t experts_workspace_bytes(int64_t T, int64_t K, int64_t I, int experts, int k, int g) {
   return experts_plan(T, K, I, experts, k, g).bytes;
 }
 

@@ -199,7 +199,7 @@ struct ExpertsArgs {
   int64_t T, K, I;
   int experts, k, g, dtype;
 };
-size_t experts_workspace_bytes(int64_t T, int64_t K, int64_t I, int experts, int k, int g, int num_sms);
+size_t experts_workspace_bytes(int64_t T, int64_t K, int64_t I, int experts, int k, int g);
 cudaError_t launch_experts(const ExpertsArgs &a, void *workspace, int num_sms, cudaStream_t stream);
 
 }  // namespace w4

@@ -26,6 +26,7 @@ namespace {
 using namespace detail;
 
 constexpr int kWarps = 8;
+constexpr int kTileRows = 16;
 constexpr int kDirectRows = 32;
 
 struct Tiles {
@@ -62,13 +63,11 @@ __device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
 
 __device__ __forceinline__ uint4 ldg16(const uint16_t *p) { return __ldg(reinterpret_cast<const uint4 *>(p)); }
 
-// v[position][rank] = A[a] . x. A block holds a tile of 16 MT RG rows and NB * 8 ranks; the warps of a group of rows take
-// 32 U of K in turn and add their sums in shared memory, in a fixed order. Where tiles are few the blocks of a cluster
-// split K and add theirs through distributed shared memory, each a part of the tile, in the order of their ranks.
-template <int DT, int MT, int RG, int NB, int U>
-__global__ void __launch_bounds__(32 * kWarps, 2)
-    lora_shrink_kernel(const Tiles ts, const LoraArgs a, float *__restrict__ v) {
-  constexpr int KW = kWarps / RG;  // warps that share a group's K
+// v[position][rank] = A[a] . x. A block holds a tile of 16 rows and NB * 8 ranks; its warps take 32 U of K in turn and add
+// their sums in shared memory, in a fixed order. Where tiles are few the blocks of a cluster split K and add theirs through
+// distributed shared memory, each a part of the tile, in the order of their ranks.
+template <int DT, int NB, int U>
+__global__ void __launch_bounds__(32 * kWarps, 2) lora_shrink_kernel(const Tiles ts, const LoraArgs a, float *__restrict__ v) {
   griddep_launch_dependents();
   griddep_wait();
   int key, row0, rows;
@@ -77,90 +76,81 @@ __global__ void __launch_bounds__(32 * kWarps, 2)
   const int n0 = blockIdx.z * NB * 8;
   if (n0 >= rank) return;  // (the second kernel reads no v at or past the adapter's rank)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int kw = warp % KW, r0 = warp / KW * MT * 16;
   const int g = lane >> 2, t = lane & 3;
   const int K = static_cast<int>(a.K);
 
-  const uint16_t *xr[2 * MT];
-  bool has[2 * MT];
+  const uint16_t *xr[2];
+  bool has[2];
 #pragma unroll
-  for (int m = 0; m < 2 * MT; ++m) {
-    const int r = r0 + m * 8 + g;
-    has[m] = r < rows;
-    xr[m] = static_cast<const uint16_t *>(a.x) + (has[m] ? row_at(ts, row0 + r) * a.ldx : 0);
+  for (int m = 0; m < 2; ++m) {
+    has[m] = m * 8 + g < rows;
+    xr[m] = static_cast<const uint16_t *>(a.x) + (has[m] ? row_at(ts, row0 + m * 8 + g) * a.ldx : 0);
   }
   const uint16_t *ar = static_cast<const uint16_t *>(a.A) + (static_cast<int64_t>(key) * a.rank + n0 + g) * K;
   bool live[NB];
 #pragma unroll
   for (int n = 0; n < NB; ++n) live[n] = n0 + n * 8 + g < rank;
 
-  float acc[MT][NB][4] = {};
+  float acc[NB][4] = {};
   const int chunk = 32 * U;
-  const int step = chunk * KW * gridDim.y;
+  const int step = chunk * kWarps * gridDim.y;
   const uint4 zero = make_uint4(0, 0, 0, 0);
-  for (int k0 = (blockIdx.y * KW + kw) * chunk; k0 < K; k0 += step) {
-    uint4 xa[U][2 * MT], wb[U][NB];
+  for (int k0 = (blockIdx.y * kWarps + warp) * chunk; k0 < K; k0 += step) {
+    uint4 xa[U][2], wb[U][NB];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int k = k0 + u * 32 + t * 8;  // K is a multiple of 8: eight values lie inside or outside together
       const bool in = k < K;
 #pragma unroll
-      for (int m = 0; m < 2 * MT; ++m) xa[u][m] = in && has[m] ? ldg16(xr[m] + k) : zero;
+      for (int m = 0; m < 2; ++m) xa[u][m] = in && has[m] ? ldg16(xr[m] + k) : zero;
 #pragma unroll
       for (int n = 0; n < NB; ++n) wb[u][n] = in && live[n] ? ldg16(ar + static_cast<int64_t>(n) * 8 * K + k) : zero;
     }
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
-      for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int n = 0; n < NB; ++n) {
-          mma_16816<DT>(acc[m][n], xa[u][2 * m].x, xa[u][2 * m + 1].x, xa[u][2 * m].y, xa[u][2 * m + 1].y, wb[u][n].x,
-                        wb[u][n].y);
-          mma_16816<DT>(acc[m][n], xa[u][2 * m].z, xa[u][2 * m + 1].z, xa[u][2 * m].w, xa[u][2 * m + 1].w, wb[u][n].z,
-                        wb[u][n].w);
-        }
+      for (int n = 0; n < NB; ++n) {
+        mma_16816<DT>(acc[n], xa[u][0].x, xa[u][1].x, xa[u][0].y, xa[u][1].y, wb[u][n].x, wb[u][n].y);
+        mma_16816<DT>(acc[n], xa[u][0].z, xa[u][1].z, xa[u][0].w, xa[u][1].w, wb[u][n].z, wb[u][n].w);
+      }
   }
 
-  // the upper half of a group's warps gives its sums to the lower half until one warp has them all
-  __shared__ float red[kWarps / 2][MT * NB * 4][32];
+  // the upper half of the warps gives its sums to the lower half until one warp has them all
+  __shared__ float red[kWarps / 2][NB * 4][32];
 #pragma unroll
-  for (int half = KW / 2; half > 0; half >>= 1) {
-    float(*slot)[32] = red[warp / KW * (KW / 2) + kw % half];
-    if (kw >= half && kw < 2 * half) {
+  for (int half = kWarps / 2; half > 0; half >>= 1) {
+    if (warp >= half && warp < 2 * half) {
 #pragma unroll
-      for (int i = 0; i < MT * NB * 4; ++i) slot[i][lane] = acc[i / (NB * 4)][i / 4 % NB][i % 4];
+      for (int i = 0; i < NB * 4; ++i) red[warp - half][i][lane] = acc[i / 4][i % 4];
     }
     __syncthreads();
-    if (kw < half) {
+    if (warp < half) {
 #pragma unroll
-      for (int i = 0; i < MT * NB * 4; ++i) acc[i / (NB * 4)][i / 4 % NB][i % 4] += slot[i][lane];
+      for (int i = 0; i < NB * 4; ++i) acc[i / 4][i % 4] += red[warp][i][lane];
     }
     __syncthreads();
   }
   const int C = gridDim.y;  // blocks of the cluster
   if (C == 1) {
-    if (kw != 0) return;
+    if (warp != 0) return;
 #pragma unroll
-    for (int m = 0; m < 2 * MT; ++m) {
+    for (int m = 0; m < 2; ++m) {
       if (!has[m]) continue;
-      float *row = v + static_cast<int64_t>(row0 + r0 + m * 8 + g) * a.rank + n0 + 2 * t;
+      float *row = v + static_cast<int64_t>(row0 + m * 8 + g) * a.rank + n0 + 2 * t;
 #pragma unroll
       for (int n = 0; n < NB; ++n)
-        if (n0 + n * 8 < a.rank)
-          *reinterpret_cast<float2 *>(row + n * 8) = make_float2(acc[m / 2][n][2 * (m & 1)], acc[m / 2][n][2 * (m & 1) + 1]);
+        if (n0 + n * 8 < a.rank) *reinterpret_cast<float2 *>(row + n * 8) = make_float2(acc[n][2 * m], acc[n][2 * m + 1]);
     }
     return;
   }
   float *part = &red[0][0][0];  // [row of the tile][NB * 8]
-  static_assert(16 * MT * RG * NB * 8 <= kWarps / 2 * MT * NB * 4 * 32, "the tile's sums fit");
-  if (kw == 0) {
+  static_assert(16 * NB * 8 <= kWarps / 2 * NB * 4 * 32, "the tile's sums fit");
+  if (warp == 0) {
 #pragma unroll
-    for (int m = 0; m < 2 * MT; ++m)
+    for (int m = 0; m < 2; ++m)
 #pragma unroll
       for (int n = 0; n < NB; ++n)
-        *reinterpret_cast<float2 *>(part + (r0 + m * 8 + g) * NB * 8 + n * 8 + 2 * t) =
-            make_float2(acc[m / 2][n][2 * (m & 1)], acc[m / 2][n][2 * (m & 1) + 1]);
+        *reinterpret_cast<float2 *>(part + (m * 8 + g) * NB * 8 + n * 8 + 2 * t) = make_float2(acc[n][2 * m], acc[n][2 * m + 1]);
   }
   cluster_sync_all();
   for (int i = threadIdx.x + 32 * kWarps * blockIdx.y; i < rows * NB * 8; i += 32 * kWarps * C) {
@@ -201,7 +191,7 @@ __device__ __forceinline__ void copies_wait() {
 
 // Shared memory of an expand block. Both kernels: v; each warp's ring of B's stretches, every lane its own part. Rows of 16-byte
 // pieces (wide): the rows' operands, factors and offsets, each warp's ring of base's stretches. Else: each warp's sums.
-template <int RW, int KB, bool WIDE>
+template <int KB, bool WIDE>
 struct Expand {
   static constexpr int kLd = KB * 16 + 4;
   static constexpr int P = KB == 1 ? 1 : KB / 2;  // loads of B a product: 8 bytes a lane at ranks up to 16, else 16
@@ -209,23 +199,23 @@ struct Expand {
   static constexpr int kWords = kLoad / 4;
   static constexpr int kStageB = 4 * P * 32 * kLoad;
   static constexpr int kLdSums = 66;
-  static constexpr int kV = (16 * RW * kLd * 4 + 15) / 16 * 16;
-  static constexpr int kStageBase = RW * 2 * 32 * 16;
+  static constexpr int kV = 16 * kLd * 4;
+  static constexpr int kStageBase = 2 * 32 * 16;
   static constexpr int kWarp = kAheadB * kStageB + (WIDE ? kAhead * kStageBase : 16 * kLdSums * 4);
   static constexpr int kWarp0 = WIDE ? 0 : kV;  // wide: once the operands are made the rings take v's place
   static constexpr int kRings = kWarp0 + kWarps * kWarp;
-  static constexpr int kFrags = kRings > kV ? kRings : kV;                      // [row group][KB][hi, lo][lane] 16 bytes
-  static constexpr int kOffsets = kFrags + (WIDE ? RW * KB * 2 * 32 * 16 : 0);  // [row] offset in y, in base
-  static constexpr int kFactors = kOffsets + (WIDE ? 16 * RW * 16 : 0);         // [row] factor of the sums, divisor's inverse
-  static constexpr int kBytes = kFactors + (WIDE ? 16 * RW * 8 : 0);
+  static constexpr int kFrags = kRings > kV ? kRings : kV;                      // [KB][hi, lo][lane] 16 bytes
+  static constexpr int kOffsets = kFrags + (WIDE ? KB * 2 * 32 * 16 : 0);  // [row] offset in y, in base
+  static constexpr int kFactors = kOffsets + (WIDE ? 16 * 16 : 0);         // [row] factor of the sums, divisor's inverse
+  static constexpr int kBytes = kFactors + (WIDE ? 16 * 8 : 0);
   // that an SM's 228 KB hold, each with 1 KB of the system's
   static constexpr int kBlocks = kBytes > 113 * 1024 ? 1 : kBytes > 75 * 1024 ? 2 : 3;
 };
 
 // The tile's v to shared memory; zero past the rows and past the adapter's rank, whatever stands there.
-template <int ROWS, int KB, int LD>
+template <int KB, int LD>
 __device__ __forceinline__ void load_v(float (*vs)[LD], const float *__restrict__ v, int row0, int rows, int rank, int rank_all) {
-  for (int i = threadIdx.x; i < ROWS * KB * 4; i += 32 * kWarps) {
+  for (int i = threadIdx.x; i < 16 * KB * 4; i += 32 * kWarps) {
     const int r = i / (KB * 4), k = i % (KB * 4) * 4;
     float4 p = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     if (r < rows && k < rank) {
@@ -299,13 +289,13 @@ __device__ __forceinline__ void product(float (&acc)[4], const uint32_t (&w)[E::
   mma_16816<DT>(acc, hi.x, hi.y, hi.z, hi.w, b0, b1);
 }
 
-// y = base + scaling * B[a] . v for a tile of 16 RW rows whose rows of y and base are 16-byte aligned. A warp takes every
-// eighth stretch of 32 columns for all the tile's rows: B's stretch is read once, base's are copied ahead (as loads to
-// registers, or with a warp to each 16 rows, too few bytes were in flight: 3.6 TB/s).
-template <int DT, int RW, int KB>
-__global__ void __launch_bounds__(32 * kWarps, Expand<RW, KB, true>::kBlocks)
+// y = base + scaling * B[a] . v for a tile of 16 rows whose rows of y and base are 16-byte aligned. A warp takes every
+// eighth stretch of 32 columns; B's and base's next stretches are copied ahead to shared memory (as loads to registers
+// too few bytes were in flight: 95 us for 8192 x 10240 at rank 32, against 78).
+template <int DT, int KB>
+__global__ void __launch_bounds__(32 * kWarps, Expand<KB, true>::kBlocks)
     lora_expand_wide_kernel(const Tiles ts, const LoraArgs a, const float *__restrict__ v) {
-  using E = Expand<RW, KB, true>;
+  using E = Expand<KB, true>;
   extern __shared__ __align__(16) uint8_t smem[];
   float(*vs)[E::kLd] = reinterpret_cast<float(*)[E::kLd]>(smem);
   uint4 *frags = reinterpret_cast<uint4 *>(smem + E::kFrags);
@@ -322,33 +312,33 @@ __global__ void __launch_bounds__(32 * kWarps, Expand<RW, KB, true>::kBlocks)
   const int N = static_cast<int>(a.N);
   const float scale = key >= 0 && a.scaling ? a.scaling[key] : 1.0f;
 
-  if (threadIdx.x < 16 * RW) {
+  if (threadIdx.x < 16) {
     const int64_t row = static_cast<int>(threadIdx.x) < rows ? row_at(ts, row0 + threadIdx.x) : 0;
     offsets[threadIdx.x][0] = row * a.ldy;
     offsets[threadIdx.x][1] = row * a.ldbase;
   }
-  load_v<16 * RW, KB>(vs, v, row0, rows, rank, a.rank);
+  load_v<KB>(vs, v, row0, rows, rank, a.rank);
   __syncthreads();
-  if (threadIdx.x < 16 * RW) {
+  if (threadIdx.x < 16) {
     float top = 0.0f;
     if (DT == kDtypeF16)
       for (int k = 0; k < KB * 16; ++k) top = fmaxf(top, fabsf(vs[threadIdx.x][k]));
     row_factors<DT>(top, scale, &factors[threadIdx.x][1], &factors[threadIdx.x][0]);
   }
   __syncthreads();
-  for (int i = warp; i < RW * KB; i += kWarps) {
-    const int rg = i / KB, b = i % KB;
+  if (warp < KB) {
+    const int b = warp;
     uint32_t hi[4], lo[4];
 #pragma unroll
     for (int m = 0; m < 2; ++m) {
-      const int r = rg * 16 + m * 8 + g;
+      const int r = m * 8 + g;
       const float down = factors[r][1];
       const float4 p = *reinterpret_cast<const float4 *>(&vs[r][k_of<KB>(b, t)]);
       split_pair<DT>(p.x * down, p.y * down, &hi[m], &lo[m]);
       split_pair<DT>(p.z * down, p.w * down, &hi[2 + m], &lo[2 + m]);
     }
-    frags[(i * 2 + 0) * 32 + lane] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-    frags[(i * 2 + 1) * 32 + lane] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    frags[(b * 2 + 0) * 32 + lane] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+    frags[(b * 2 + 1) * 32 + lane] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
   }
   __syncthreads();
 
@@ -361,10 +351,10 @@ __global__ void __launch_bounds__(32 * kWarps, Expand<RW, KB, true>::kBlocks)
   auto fetch = [&](int n0, int slot) {
     const int n = n0 + 8 * t;
 #pragma unroll
-    for (int m = 0; m < 2 * RW; ++m) {
+    for (int m = 0; m < 2; ++m) {
       const int r = m * 8 + g;
       const int bytes = base && r < rows && n < N ? min(2 * (N - n), 16) : 0;
-      cp_async16_zfill(smem_u32(ahead + (slot * 2 * RW + m) * 32), bytes ? base + offsets[r][1] + n : a.B, bytes);
+      cp_async16_zfill(smem_u32(ahead + (slot * 2 + m) * 32), bytes ? base + offsets[r][1] + n : a.B, bytes);
     }
   };
   const int first = (blockIdx.y * kWarps + warp) * 32, step = gridDim.y * kWarps * 32;
@@ -385,41 +375,38 @@ __global__ void __launch_bounds__(32 * kWarps, Expand<RW, KB, true>::kBlocks)
     copies_commit();
     copies_wait<kAheadB - 1>();
     const int n = n0 + 8 * t;
-    uint32_t w[4][E::P][E::kWords];
+    float acc[4][4] = {};
+    if (key >= 0) {
+      uint32_t w[4][E::P][E::kWords];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) load_b<E>(w[j], b_ring + slot_b * E::kStageB, j);
-#pragma unroll 1
-    for (int rg = 0; rg < RW && rg * 16 < rows; ++rg) {
-      float acc[4][4] = {};
-      if (key >= 0) {
+      for (int j = 0; j < 4; ++j) load_b<E>(w[j], b_ring + slot_b * E::kStageB, j);
 #pragma unroll
-        for (int b = 0; b < KB; ++b) {
-          const uint4 hi = frags[((rg * KB + b) * 2 + 0) * 32 + lane], lo = frags[((rg * KB + b) * 2 + 1) * 32 + lane];
+      for (int b = 0; b < KB; ++b) {
+        const uint4 hi = frags[(b * 2 + 0) * 32 + lane], lo = frags[(b * 2 + 1) * 32 + lane];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) product<DT, KB, E>(acc[j], w[j], b, hi, lo);
-        }
+        for (int j = 0; j < 4; ++j) product<DT, KB, E>(acc[j], w[j], b, hi, lo);
       }
+    }
 #pragma unroll
-      for (int m = 0; m < 2; ++m) {
-        const int r = rg * 16 + m * 8 + g;
-        if (r >= rows || n >= N) continue;
-        const uint4 old = ahead[(slot * 2 * RW + rg * 2 + m) * 32];
-        uint32_t out[4] = {old.x, old.y, old.z, old.w};
-        if (key >= 0) {
-          const float mul = factors[r][0];
+    for (int m = 0; m < 2; ++m) {
+      const int r = m * 8 + g;
+      if (r >= rows || n >= N) continue;
+      const uint4 old = ahead[(slot * 2 + m) * 32];
+      uint32_t out[4] = {old.x, old.y, old.z, old.w};
+      if (key >= 0) {
+        const float mul = factors[r][0];
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            out[j] = out_bits2<DT>(value_f32<DT>(out[j] & 0xffffu) + mul * acc[j][2 * m],
-                                   value_f32<DT>(out[j] >> 16) + mul * acc[j][2 * m + 1]);
-        }
-        uint16_t *to = y + offsets[r][0] + n;
-        if (n + 8 <= N) {
-          *reinterpret_cast<uint4 *>(to) = make_uint4(out[0], out[1], out[2], out[3]);
-        } else {
+        for (int j = 0; j < 4; ++j)
+          out[j] = out_bits2<DT>(value_f32<DT>(out[j] & 0xffffu) + mul * acc[j][2 * m],
+                                 value_f32<DT>(out[j] >> 16) + mul * acc[j][2 * m + 1]);
+      }
+      uint16_t *to = y + offsets[r][0] + n;
+      if (n + 8 <= N) {
+        *reinterpret_cast<uint4 *>(to) = make_uint4(out[0], out[1], out[2], out[3]);
+      } else {
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            if (n + i < N) to[i] = static_cast<uint16_t>(out[i / 2] >> (16 * (i & 1)));
-        }
+        for (int i = 0; i < 8; ++i)
+          if (n + i < N) to[i] = static_cast<uint16_t>(out[i / 2] >> (16 * (i & 1)));
       }
     }
     slot = (slot + 1) % kAhead;
@@ -437,14 +424,13 @@ __device__ __forceinline__ void store_two(uint16_t *p, int n, int N, uint32_t v)
   if (n < N) p[n] = static_cast<uint16_t>(v);
 }
 
-// The same for rows that are not 16-byte aligned (of odd length, say): warp (w % RW, w / RW) has 16 rows and every CW-th
-// stretch of 64 columns, whose sums go through shared memory, so that the warp reads and writes consecutive columns of a
+// The same for rows that are not 16-byte aligned (of odd length, say): a warp takes every eighth stretch of 64 columns, whose
+// sums go through shared memory, so that the warp reads and writes consecutive columns of a
 // row, in pairs from the row's first 4-byte boundary.
-template <int DT, int RW, int KB>
+template <int DT, int KB>
 __global__ void __launch_bounds__(32 * kWarps, KB <= 4 ? 2 : 1)
     lora_expand_kernel(const Tiles ts, const LoraArgs a, const float *__restrict__ v) {
-  using E = Expand<RW, KB, false>;
-  constexpr int CW = kWarps / RW;
+  using E = Expand<KB, false>;
   extern __shared__ __align__(16) uint8_t smem[];
   float(*vs)[E::kLd] = reinterpret_cast<float(*)[E::kLd]>(smem);
   griddep_launch_dependents();
@@ -458,20 +444,18 @@ __global__ void __launch_bounds__(32 * kWarps, KB <= 4 ? 2 : 1)
   const int N = static_cast<int>(a.N);
   const float scale = key >= 0 && a.scaling ? a.scaling[key] : 1.0f;
 
-  const int r0 = warp % RW * 16;
   int64_t row[2];  // read beside v
 #pragma unroll
-  for (int m = 0; m < 2; ++m) row[m] = r0 + m * 8 + g < rows ? row_at(ts, row0 + r0 + m * 8 + g) : 0;
-  load_v<16 * RW, KB>(vs, v, row0, rows, rank, a.rank);
+  for (int m = 0; m < 2; ++m) row[m] = m * 8 + g < rows ? row_at(ts, row0 + m * 8 + g) : 0;
+  load_v<KB>(vs, v, row0, rows, rank, a.rank);
   __syncthreads();
-  if (r0 >= rows) return;
 
   int64_t yr[2], br[2];  // the rows' first values in y and base
   float mul[2];
   uint32_t hi[KB][4], lo[KB][4];
 #pragma unroll
   for (int m = 0; m < 2; ++m) {
-    const int r = r0 + m * 8 + g;
+    const int r = m * 8 + g;
     yr[m] = row[m] * a.ldy;
     br[m] = row[m] * a.ldbase;
     float top = 0.0f, down;
@@ -495,7 +479,7 @@ __global__ void __launch_bounds__(32 * kWarps, KB <= 4 ? 2 : 1)
   uint8_t *mine = smem + E::kWarp0 + warp * E::kWarp;
   const uint32_t b_ring = smem_u32(mine);
   float(*sums)[E::kLdSums] = reinterpret_cast<float(*)[E::kLdSums]>(mine + kAheadB * E::kStageB);
-  const int first = (blockIdx.y * CW + warp / RW) * 64, step = gridDim.y * CW * 64;
+  const int first = (blockIdx.y * kWarps + warp) * 64, step = gridDim.y * kWarps * 64;
   static_assert(kAheadB == 2, "a stretch's halves take the ring's places in turn");
   fetch_b<E>(b_ring, B, first, N, rank, a.rank, a.B);
   copies_commit();
@@ -511,7 +495,7 @@ __global__ void __launch_bounds__(32 * kWarps, KB <= 4 ? 2 : 1)
       const int odd = (reinterpret_cast<uintptr_t>(yp + n0) >> 1) & 1;
       const int n = n0 + 2 * lane - odd;
       const int lo = n < n0 ? n0 + 63 : n;
-      const bool in = base && r0 + i < rows;
+      const bool in = base && i < rows;
       const bool pair = in && n >= n0 && n + 1 < end && (reinterpret_cast<uintptr_t>(bp + n) & 3) == 0;
       both[i] = pair ? *reinterpret_cast<const uint32_t *>(bp + n) : 0u;
       low[i] = in && !pair && lo < end ? bp[lo] : 0u;
@@ -545,7 +529,7 @@ __global__ void __launch_bounds__(32 * kWarps, KB <= 4 ? 2 : 1)
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       uint16_t *yp = y + __shfl_sync(0xffffffffu, yr[i / 8], i % 8 * 4);
-      if (r0 + i >= rows) continue;
+      if (i >= rows) continue;
       const int odd = (reinterpret_cast<uintptr_t>(yp + n0) >> 1) & 1;
       const int c = 2 * lane - odd;
       uint32_t out = both[i] | low[i] | high[i] << 16;
@@ -567,17 +551,14 @@ __global__ void __launch_bounds__(32 * kWarps, KB <= 4 ? 2 : 1)
 // The launch's shape, and the workspace's: [v][perm][tiles][ntiles].
 struct LoraPlan {
   bool direct;
-  int rw, tile, max_tiles, splits;
+  int max_tiles, splits;
   size_t perm, tiles, ntiles, bytes;
 };
 
 LoraPlan lora_plan(int64_t T, int64_t N, int64_t K, int adapters, int rank, int num_sms) {
   LoraPlan p;
   p.direct = T <= kDirectRows;
-  // rows a tile: 16 for a few rows an adapter, more where an adapter's rows fill them (its weights are then read less)
-  p.rw = p.direct || T < 32 * adapters ? 1 : T < 128 * adapters ? 2 : 4;
-  p.tile = 16 * p.rw;
-  p.max_tiles = static_cast<int>(p.direct ? T : max_row_tiles(T, adapters, p.tile));
+  p.max_tiles = static_cast<int>(p.direct ? T : max_row_tiles(T, adapters, kTileRows));
   // few tiles: the blocks of a cluster split a tile's K, no finer than one turn of a block's warps (32 K values each)
   const int64_t turns = cdiv(K, 32 * kWarps);
   // (two blocks an SM run at a time: as many blocks as fit at once, since one more would wait for a whole turn)
@@ -610,47 +591,49 @@ cudaError_t launch_grid(void (*kern)(Args...), dim3 grid, int cluster, int smem,
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-template <int DT, int RW, int KB, bool WIDE>
+template <int DT, int KB, bool WIDE>
 cudaError_t launch_expand(const Tiles &ts, const LoraArgs &a, const LoraPlan &p, const float *v, int num_sms,
                           cudaStream_t stream) {
   void (*kern)(const Tiles, const LoraArgs, const float *);
   if constexpr (WIDE)
-    kern = lora_expand_wide_kernel<DT, RW, KB>;
+    kern = lora_expand_wide_kernel<DT, KB>;
   else
-    kern = lora_expand_kernel<DT, RW, KB>;
-  constexpr int bytes = Expand<RW, KB, WIDE>::kBytes;
+    kern = lora_expand_kernel<DT, KB>;
+  constexpr int bytes = Expand<KB, WIDE>::kBytes;
   static std::atomic<uint64_t> set{0};
   const cudaError_t e = allow_smem(kern, bytes, &set);
   if (e != cudaSuccess) return e;
-  // columns: as many blocks as run at a time, no more than one turn of a block's warps each
-  const int64_t turns = cdiv(a.N, WIDE ? 32 * kWarps : 64 * kWarps / RW);
-  const int64_t want = (WIDE ? Expand<RW, KB, true>::kBlocks : KB <= 4 ? 2 : 1) * num_sms / p.max_tiles;
-  return launch_grid(kern, dim3(p.max_tiles, static_cast<unsigned>(want < 1 ? 1 : want < turns ? want : turns)), 1, bytes,
-                     stream, ts, a, v);
+  // columns: as many blocks as run at a time, but three parts at least (8192 rows in one part 132 us, in three 123: the
+  // parts of a tile run apart from one another) and no more than one turn of a block's warps each
+  const int64_t turns = cdiv(a.N, (WIDE ? 32 : 64) * kWarps);
+  int64_t parts = (WIDE ? Expand<KB, true>::kBlocks : KB <= 4 ? 2 : 1) * num_sms / p.max_tiles;
+  parts = parts < 3 ? 3 : parts;
+  return launch_grid(kern, dim3(p.max_tiles, static_cast<unsigned>(parts < turns ? parts : turns)), 1, bytes, stream, ts, a,
+                     v);
 }
 
-template <int DT, int RW>
-cudaError_t launch_rw(const Tiles &ts, const LoraArgs &a, const LoraPlan &p, float *v, int num_sms, cudaStream_t stream) {
-  constexpr int MT = RW == 1 ? 1 : 2;
-  constexpr int RG = RW == 4 ? 2 : 1;
-  auto shrink = a.rank <= 8    ? lora_shrink_kernel<DT, MT, RG, 1, 4>
-                : a.rank <= 16 ? lora_shrink_kernel<DT, MT, RG, 2, 4>
-                : a.rank <= 32 ? lora_shrink_kernel<DT, MT, RG, 4, 2>
-                               : lora_shrink_kernel<DT, MT, RG, 8, 1>;
-  cudaError_t e = launch_grid(shrink, dim3(p.max_tiles, p.splits, a.rank > 64 ? 2 : 1), p.splits, 0, stream, ts, a, v);
+template <int DT>
+cudaError_t launch_dt(const Tiles &ts, const LoraArgs &a, const LoraPlan &p, float *v, int num_sms, cudaStream_t stream) {
+  auto shrink = a.rank <= 8    ? lora_shrink_kernel<DT, 1, 4>
+                : a.rank <= 16 ? lora_shrink_kernel<DT, 2, 4>
+                : a.rank <= 32 ? lora_shrink_kernel<DT, 4, 2>
+                               : lora_shrink_kernel<DT, 8, 1>;
+  const cudaError_t e =
+      launch_grid(shrink, dim3(p.max_tiles, p.splits, a.rank > 64 ? 2 : 1), p.splits, 0, stream, ts, a, v);
   if (e != cudaSuccess) return e;
   const bool wide = a.ldy % 8 == 0 && reinterpret_cast<uintptr_t>(a.y) % 16 == 0 &&
                     (!a.base || (a.ldbase % 8 == 0 && reinterpret_cast<uintptr_t>(a.base) % 16 == 0));
   if (wide)
-    return a.rank <= 16   ? launch_expand<DT, RW, 1, true>(ts, a, p, v, num_sms, stream)
-           : a.rank <= 32 ? launch_expand<DT, RW, 2, true>(ts, a, p, v, num_sms, stream)
-           : a.rank <= 64 ? launch_expand<DT, RW, 4, true>(ts, a, p, v, num_sms, stream)
-                          : launch_expand<DT, RW, 8, true>(ts, a, p, v, num_sms, stream);
-  return a.rank <= 16   ? launch_expand<DT, RW, 1, false>(ts, a, p, v, num_sms, stream)
-         : a.rank <= 32 ? launch_expand<DT, RW, 2, false>(ts, a, p, v, num_sms, stream)
-         : a.rank <= 64 ? launch_expand<DT, RW, 4, false>(ts, a, p, v, num_sms, stream)
-                        : launch_expand<DT, RW, 8, false>(ts, a, p, v, num_sms, stream);
+    return a.rank <= 16   ? launch_expand<DT, 1, true>(ts, a, p, v, num_sms, stream)
+           : a.rank <= 32 ? launch_expand<DT, 2, true>(ts, a, p, v, num_sms, stream)
+           : a.rank <= 64 ? launch_expand<DT, 4, true>(ts, a, p, v, num_sms, stream)
+                          : launch_expand<DT, 8, true>(ts, a, p, v, num_sms, stream);
+  return a.rank <= 16   ? launch_expand<DT, 1, false>(ts, a, p, v, num_sms, stream)
+         : a.rank <= 32 ? launch_expand<DT, 2, false>(ts, a, p, v, num_sms, stream)
+         : a.rank <= 64 ? launch_expand<DT, 4, false>(ts, a, p, v, num_sms, stream)
+                        : launch_expand<DT, 8, false>(ts, a, p, v, num_sms, stream);
 }
+
 }  // namespace
 
 size_t lora_workspace_bytes(int64_t T, int64_t N, int64_t K, int adapters, int rank, int num_sms) {
@@ -668,17 +651,12 @@ cudaError_t launch_lora(const LoraArgs &a, void *workspace, int num_sms, cudaStr
     ts.plan.perm = reinterpret_cast<int32_t *>(ws + p.perm);
     ts.plan.tiles = reinterpret_cast<RowTile *>(ws + p.tiles);
     ts.plan.ntiles = reinterpret_cast<int32_t *>(ws + p.ntiles);
-    const cudaError_t e = launch_row_plan(a.adapter, a.T, a.adapters, p.tile, true, ts.plan, stream);
+    const cudaError_t e = launch_row_plan(a.adapter, a.T, a.adapters, kTileRows, true, ts.plan, stream);
     if (e != cudaSuccess) return e;
   }
   float *v = reinterpret_cast<float *>(ws);
-  if (a.dtype == kDtypeBf16)
-    return p.rw == 1   ? launch_rw<kDtypeBf16, 1>(ts, a, p, v, num_sms, stream)
-           : p.rw == 2 ? launch_rw<kDtypeBf16, 2>(ts, a, p, v, num_sms, stream)
-                       : launch_rw<kDtypeBf16, 4>(ts, a, p, v, num_sms, stream);
-  return p.rw == 1   ? launch_rw<kDtypeF16, 1>(ts, a, p, v, num_sms, stream)
-         : p.rw == 2 ? launch_rw<kDtypeF16, 2>(ts, a, p, v, num_sms, stream)
-                     : launch_rw<kDtypeF16, 4>(ts, a, p, v, num_sms, stream);
+  return a.dtype == kDtypeBf16 ? launch_dt<kDtypeBf16>(ts, a, p, v, num_sms, stream)
+                               : launch_dt<kDtypeF16>(ts, a, p, v, num_sms, stream);
 }
 
 }  // namespace w4
