@@ -389,9 +389,13 @@ W4_API int w4a16_gemm_noalloc(const void *x_dev, const void *packed_dev, int64_t
  * experts, the experts' W4A16 products, and the low-rank adapters of many
  * requests beside a projection that they share. The pages have no
  * counterpart; the experts' weights are w4_pack / w4_repack's. No rows
- * (T = 0) is no error: nothing is enqueued. Workspaces need not be zeroed,
- * hold nothing between calls, and calls that share one must not overlap on
- * the device. Results are deterministic run to run on one device.
+ * (T = 0) is no error: nothing is enqueued. The workspaces of these calls need
+ * not be zeroed and hold nothing between calls; calls that share one must not
+ * overlap on the device, and it must not be one that w4a16_gemm uses, whose
+ * counters have to stay zero. Results are deterministic run to run on one
+ * device. None of the calls allocates or synchronises: all of them capture
+ * into a CUDA graph. Outputs must not overlap inputs, but for w4_lora_add's
+ * base.
  * ------------------------------------------------------------------------ */
 
 #define W4_DTYPE_F32 2 /* router logits only */
@@ -453,7 +457,9 @@ W4_API int w4_route(const void *logits_dev, int64_t T, int32_t experts, int64_t 
  * fp32; silu(gate) * up is rounded once to the type (the second product's
  * operand); sums are fp32, added in a fixed order, and y is rounded once.
  * The workspace is at least w4a16_experts_workspace_bytes(...) bytes,
- * 256-byte aligned.
+ * 256-byte aligned. Its first word is a device error word: after a wait inside
+ * a kernel gave up (about a second) w4_last_device_error(workspace) reports
+ * W4_ERR_TIMEOUT, and y is undefined. Each call clears it first.
  */
 typedef struct {
     const void *x_dev;

@@ -36,6 +36,7 @@ int check_experts_sizes(int64_t T, int64_t K, int64_t I, int32_t experts, int32_
   if (T < 0 || K < 1 || I < 1 || experts < 1 || k < 1 || k > experts || g < 1 || g % 8 != 0) return W4_ERR_INVALID_ARG;
   if (K % 8 != 0 || I % 8 != 0 || experts > w4::kRowsMaxKeys || k > w4::kRouteMaxK) return W4_ERR_UNSUPPORTED_SHAPE;
   if (T > kMaxDim || K > kMaxDim / 2 || I > kMaxDim / 4 || T * k > kMaxDim) return W4_ERR_UNSUPPORTED_SHAPE;
+  if (T * K > (int64_t{1} << 40) || T * I > (int64_t{1} << 40)) return W4_ERR_UNSUPPORTED_SHAPE;
   // a launch's blocks: 32 weight rows of one tile of rows each
   const int64_t rows = K > 2 * I ? K : 2 * I;
   if (w4::max_row_tiles(T * k, experts, 8) * w4::cdiv(rows, 32) > kMaxDim) return W4_ERR_UNSUPPORTED_SHAPE;
@@ -46,8 +47,8 @@ int check_lora_sizes(int64_t T, int64_t K, int64_t N, int32_t adapters, int32_t 
   if (T < 0 || K < 1 || N < 1 || adapters < 1 || rank < 1) return W4_ERR_INVALID_ARG;
   if (K % 8 != 0 || rank % 8 != 0 || rank > w4::kLoraMaxRank || adapters > w4::kRowsMaxKeys)
     return W4_ERR_UNSUPPORTED_SHAPE;
-  // 2^30: the last turn of a loop over K or N still fits 32 bits
-  if (T > kMaxDim || K > (1 << 30) || N > (1 << 30)) return W4_ERR_UNSUPPORTED_SHAPE;
+  // 2^28: a turn past the end of a loop over K or N still fits 32 bits
+  if (T > kMaxDim || K > (1 << 28) || N > (1 << 28)) return W4_ERR_UNSUPPORTED_SHAPE;
   return W4_OK;
 }
 
@@ -95,7 +96,8 @@ int w4_lora_add(const w4_lora_args *a, void *workspace_dev, size_t workspace_byt
   if (!a) return W4_ERR_INVALID_ARG;
   const int rc = check_lora_sizes(a->T, a->K, a->N, a->adapters, a->rank);
   if (rc != W4_OK) return rc;
-  if (!type16(a->dtype) || a->ldx < a->K || a->ldy < a->N || (a->base_dev && a->ldbase < a->N)) return W4_ERR_INVALID_ARG;
+  if (!type16(a->dtype) || a->reserved != 0 || a->ldx < a->K || a->ldy < a->N || (a->base_dev && a->ldbase < a->N))
+    return W4_ERR_INVALID_ARG;
   if (a->ldx % 8 != 0) return W4_ERR_UNSUPPORTED_SHAPE;  // rows of x start on 16-byte boundaries
   // in place means the same rows
   if (a->base_dev == a->y_dev && a->base_dev && a->ldbase != a->ldy) return W4_ERR_INVALID_ARG;

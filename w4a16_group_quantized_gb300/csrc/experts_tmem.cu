@@ -10,7 +10,7 @@
 // chunks of CB blocks of 64, with no stop between units. Roles (24 or 32 warps, one CTA a SM):
 //   4 row warps        copy the rows of `in` with the 128-byte swizzle, a quarter of them each: gate/up gathers the
 //                      tokens' rows four to a copy, down's rows are already in order (one copy a block)
-//   2 weight warps     copy the chunks' codes, and their group records, in bulk
+//   2 weight warps     copy the chunks' codes, and their group records, in bulk, through a ring of their own
 //   2 MMA warps        take the chunks in turn, each into an accumulator of its own that the chunk starts from zero
 //   8 dequant warps    two warpgroups take the chunks in turn: thread r stores row r's q - z in tensor memory and its
 //                      scale in a ring in shared memory
@@ -28,6 +28,14 @@
 // before done of those: the scale ring's eight places (a dequant warp writes c + 8's after free of c + 4) and done's
 // parity (S is at least 4, or 6 with two) are never overtaken.
 // Every wait is bounded (ptx.cuh).
+//
+// Measured (bf16, 64 experts of 2048 x 1024, 4096 rows of 8 choices): 354 us for gate/up and 162 for down, 0.78 and 0.85
+// PFLOP/s; the tensor pipe is 35% busy and the issue slots 73%: some 950 warp instructions an SM quarter and chunk of
+// 128 x 128 x 128 (dequant 270, gathering copies 280, sums 270, the rest waits) where the products take 512 cycles.
+// tcgen05 instructions are issued under elect.sync, which keeps their operands in uniform registers: by "lane 0" an
+// MMA took 125 cycles to issue, so 40. Rows by 16-byte asynchronous copies of 128 threads bound a chunk at 1200 cycles.
+// Measured no faster: one MMA warp, or two with three barriers each, one ring for rows and weights, sum warps of 64
+// columns, waits that poll or sleep longer.
 #include <atomic>
 
 #include "experts.cuh"
