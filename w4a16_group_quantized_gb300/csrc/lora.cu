@@ -211,9 +211,9 @@ struct Expand {
   static constexpr int kWarp0 = WIDE ? 0 : kV;  // wide: once the operands are made the rings take v's place
   static constexpr int kRings = kWarp0 + kWarps * kWarp;
   static constexpr int kFrags = kRings > kV ? kRings : kV;                      // [KB][hi, lo][lane] 16 bytes
-  static constexpr int kOffsets = kFrags + (WIDE ? KB * 2 * 32 * 16 : 0);  // [row] offset in y, in base
-  static constexpr int kFactors = kOffsets + (WIDE ? 16 * 16 : 0);         // [row] factor of the sums, divisor's inverse
-  static constexpr int kBytes = kFactors + (WIDE ? 16 * 8 : 0);
+  static constexpr int kOffsets = kFrags + (WIDE ? KB * 2 * 32 * 16 : 0);  // [row] offset in y, in base; else addresses
+  static constexpr int kFactors = kOffsets + 16 * 16;                      // [row] factor of the sums, divisor's inverse; else flags
+  static constexpr int kBytes = kFactors + 16 * 8;
   // that an SM's 228 KB hold, each with 1 KB of the system's (rows that are not wide: by their registers)
   static constexpr int kBlocks = !WIDE ? (KB <= 4 ? 2 : 1) : kBytes > 113 * 1024 ? 1 : kBytes > 75 * 1024 ? 2 : 3;
 };
@@ -421,18 +421,10 @@ __global__ void __launch_bounds__(32 * kWarps, Expand<KB, true>::kBlocks)
   copies_wait<0>();
 }
 
-// Stores values n and n + 1 of a row (those that lie in 0 .. N - 1), p + n 4-byte aligned.
-__device__ __forceinline__ void store_two(uint16_t *p, int n, int N, uint32_t v) {
-  if (n + 1 < N) {
-    *reinterpret_cast<uint32_t *>(p + n) = v;
-    return;
-  }
-  if (n < N) p[n] = static_cast<uint16_t>(v);
-}
-
 // The same for rows that are not 16-byte aligned (of odd length, say): a warp takes every eighth stretch of 64 columns, whose
-// sums go through shared memory, so that the warp reads and writes consecutive columns of a
-// row, in pairs from the row's first 4-byte boundary.
+// sums go through shared memory, so that the warp reads and writes consecutive columns of a row, in pairs from the row's
+// first 4-byte boundary. In a row that starts off that boundary lane 0 has the stretch's last column and its first instead
+// of a pair.
 template <int DT, int KB>
 __global__ void __launch_bounds__(32 * kWarps, Expand<KB, false>::kBlocks)
     lora_expand_kernel(const Tiles ts, const LoraArgs a, const float *__restrict__ v) {
@@ -450,20 +442,33 @@ __global__ void __launch_bounds__(32 * kWarps, Expand<KB, false>::kBlocks)
   const int N = static_cast<int>(a.N);
   const float scale = key >= 0 && a.scaling ? a.scaling[key] : 1.0f;
 
-  int64_t row[2];  // read beside v
-#pragma unroll
-  for (int m = 0; m < 2; ++m) row[m] = m * 8 + g < rows ? row_at(ts, row0 + m * 8 + g) : 0;
+  const uint16_t *base = static_cast<const uint16_t *>(a.base);
+  // the rows' first pairs in y and in base (the value before the row for one off the boundary), and how they lie
+  struct Row {
+    uint16_t *y;
+    const uint16_t *base;
+  };
+  Row *const row_of = reinterpret_cast<Row *>(smem + E::kOffsets);
+  int *const lies = reinterpret_cast<int *>(smem + E::kFactors);
+  constexpr int kOff = 1, kPairs = 2, kLive = 4, kBase = 8;
+  if (threadIdx.x < 16) {
+    const bool live = static_cast<int>(threadIdx.x) < rows;
+    const int64_t row = live ? row_at(ts, row0 + threadIdx.x) : 0;
+    uint16_t *yp = static_cast<uint16_t *>(a.y) + row * a.ldy;
+    const int off = (reinterpret_cast<uintptr_t>(yp) >> 1) & 1;
+    const uint16_t *bp = base ? base + row * a.ldbase - off : nullptr;
+    row_of[threadIdx.x] = Row{yp - off, bp};
+    lies[threadIdx.x] = (off ? kOff : 0) | ((reinterpret_cast<uintptr_t>(bp) & 3) == 0 ? kPairs : 0) | (live ? kLive : 0) |
+                        (base && live ? kBase : 0);
+  }
   load_v<KB>(vs, v, row0, rows, rank, a.rank);
   __syncthreads();
 
-  int64_t yr[2], br[2];  // the rows' first values in y and base
   float mul[2];
   uint32_t hi[KB][4], lo[KB][4];
 #pragma unroll
   for (int m = 0; m < 2; ++m) {
     const int r = m * 8 + g;
-    yr[m] = row[m] * a.ldy;
-    br[m] = row[m] * a.ldbase;
     float top = 0.0f, down;
     if (DT == kDtypeF16) {
       for (int k = t; k < KB * 16; k += 4) top = fmaxf(top, fabsf(vs[r][k]));
@@ -480,8 +485,6 @@ __global__ void __launch_bounds__(32 * kWarps, Expand<KB, false>::kBlocks)
   }
 
   const uint16_t *B = static_cast<const uint16_t *>(a.B) + static_cast<int64_t>(max(key, 0)) * N * a.rank;
-  const uint16_t *base = static_cast<const uint16_t *>(a.base);
-  uint16_t *y = static_cast<uint16_t *>(a.y);
   uint8_t *mine = smem + E::kWarp0 + warp * E::kWarp;
   const uint32_t b_ring = smem_u32(mine);
   float(*sums)[E::kLdSums] = reinterpret_cast<float(*)[E::kLdSums]>(mine + kAheadB * E::kStageB);
@@ -490,22 +493,25 @@ __global__ void __launch_bounds__(32 * kWarps, Expand<KB, false>::kBlocks)
   fetch_b<E>(b_ring, B, first, N, rank, a.rank, a.B);
   copies_commit();
   for (int n0 = first; n0 < N; n0 += step) {
-    // base's pairs start at y's 4-byte boundary in the row; the value before it takes the place of the pair past the
-    // end. The loads are predicated, not branched around, and joined only after the products
-    const int end = min(N, n0 + 64);
+    // base's pairs: the loads are predicated, not branched around, and joined only after the products
+    const bool whole = n0 + 64 <= N;
     uint32_t both[16], low[16], high[16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-      const uint16_t *bp = base + __shfl_sync(0xffffffffu, br[i / 8], i % 8 * 4);
-      const uint16_t *yp = y + __shfl_sync(0xffffffffu, yr[i / 8], i % 8 * 4);
-      const int odd = (reinterpret_cast<uintptr_t>(yp + n0) >> 1) & 1;
-      const int n = n0 + 2 * lane - odd;
-      const int lo = n < n0 ? n0 + 63 : n;
-      const bool in = base && i < rows;
-      const bool pair = in && n >= n0 && n + 1 < end && (reinterpret_cast<uintptr_t>(bp + n) & 3) == 0;
-      both[i] = pair ? *reinterpret_cast<const uint32_t *>(bp + n) : 0u;
-      low[i] = in && !pair && lo < end ? bp[lo] : 0u;
-      high[i] = in && !pair && n + 1 < end ? bp[n + 1] : 0u;
+      const int how = lies[i];
+      const uint16_t *bp = row_of[i].base + n0 + 2 * lane;
+      const bool split = (how & kOff) && lane == 0;
+      const int lo = split ? 64 : 0;  // where the lane's first value is, and its column:
+      const int col = 2 * lane - (how & kOff) + lo;
+      if (whole && (how & kPairs)) {
+        both[i] = (how & kBase) && !split ? *reinterpret_cast<const uint32_t *>(bp) : 0u;
+        low[i] = (how & kBase) && split ? bp[64] : 0u;
+        high[i] = (how & kBase) && split ? bp[1] : 0u;
+      } else {
+        both[i] = 0u;
+        low[i] = (how & kBase) && n0 + col < N ? bp[lo] : 0u;
+        high[i] = (how & kBase) && n0 + 2 * lane - (how & kOff) + 1 < N ? bp[1] : 0u;
+      }
     }
     __syncwarp();  // the stretch before has been read
 #pragma unroll 1
@@ -534,20 +540,20 @@ __global__ void __launch_bounds__(32 * kWarps, Expand<KB, false>::kBlocks)
     __syncwarp();
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-      uint16_t *yp = y + __shfl_sync(0xffffffffu, yr[i / 8], i % 8 * 4);
-      if (i >= rows) continue;
-      const int odd = (reinterpret_cast<uintptr_t>(yp + n0) >> 1) & 1;
-      const int c = 2 * lane - odd;
+      const int how = lies[i];
+      if (!(how & kLive)) continue;
+      uint16_t *yp = row_of[i].y + n0 + 2 * lane;
+      const bool split = (how & kOff) && lane == 0;
+      const int lo = split ? 64 : 0;
+      const int col = 2 * lane - (how & kOff);  // the second value's column less one
       uint32_t out = both[i] | low[i] | high[i] << 16;
-      if (key >= 0) {
-        const float *sum = sums[i];
-        out = out_bits2<DT>(value_f32<DT>(out & 0xffffu) + sum[c < 0 ? 63 : c], value_f32<DT>(out >> 16) + sum[c + 1]);
-      }
-      if (c >= 0) {
-        store_two(yp, n0 + c, end, out);
+      if (key >= 0)
+        out = out_bits2<DT>(value_f32<DT>(out & 0xffffu) + sums[i][col + lo], value_f32<DT>(out >> 16) + sums[i][col + 1]);
+      if (whole && !split) {
+        *reinterpret_cast<uint32_t *>(yp) = out;
       } else {
-        if (n0 + 63 < end) yp[n0 + 63] = static_cast<uint16_t>(out);
-        yp[n0] = static_cast<uint16_t>(out >> 16);
+        if (n0 + col + lo < N) yp[lo] = static_cast<uint16_t>(out);
+        if (n0 + col + 1 < N) yp[1] = static_cast<uint16_t>(out >> 16);
       }
     }
   }
