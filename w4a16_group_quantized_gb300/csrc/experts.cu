@@ -379,8 +379,9 @@ ExpertsPlan experts_plan(int64_t T, int64_t K, int64_t I, int experts, int k, in
   // the sort, 4 tokens 44 against 42)
   p.direct = T == 1 || pairs <= experts / 4;
   p.tmem = !p.direct && mean >= kTmemRows && experts_tmem_takes(g);
-  // (tensor memory, 64 / 128 rows a tile, 64 experts: 48 rows an expert 121 / 135 us, 64 rows 139 / 145, 96 rows 179 / 167)
-  p.tile = p.tmem ? (mean <= 64 || g % 64 != 0 ? 64 : 128) : mean <= 8 ? 8 : mean <= 16 ? 16 : 32;
+  // (tensor memory, 64 / 128 rows a tile, 64 experts of 2048 x 1024, g = 128: 48 rows an expert 121 / 135 us, 64 rows 139 /
+  // 145, 96 rows 179 / 167; g = 64, whose tiles of 128 rows take 64 k a chunk: 64 rows 164 / 190, 256 rows 461 / 420)
+  p.tile = p.tmem ? (mean <= (g % 128 == 0 ? 64 : 128) || g % 64 != 0 ? 64 : 128) : mean <= 8 ? 8 : mean <= 16 ? 16 : 32;
   p.max_tiles = static_cast<int>(p.direct ? pairs : max_row_tiles(pairs, experts, p.tile));
   auto up = [](size_t v) { return (v + 255) / 256 * 256; };
   p.part = 256;
