@@ -73,6 +73,9 @@ struct TCfg {
   static constexpr int kACol0 = 2 * kDBufs * SUB * BN;  // accumulators first
   static_assert(kXStages % 2 == 0 && kXStages >= 4 && kXStages >= 2 * kDBufs, "ring of rows");
   static_assert(kACol0 + 4 * kASlotCols <= 512, "tensor memory");
+  // a dequant warpgroup may meet a stage of weights that the other one had last: that chunk, c - W, is then long done (a
+  // warpgroup at c has seen c - 4 done, whose MMAs waited for the sums of c - 8 at the latest, read in order)
+  static_assert(kWStages >= 9, "ring of weights");
 };
 
 __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
