@@ -330,6 +330,21 @@ __global__ void __launch_bounds__(32 * NW, NT == 1 && NW == 8 ? 2 : 1) experts_k
   }
 }
 
+// in[pos] = x[token of the pair at pos]: the rows of gate/up in the sort's order, a warp a row. The tensor-memory kernel
+// reads each of them once per 128 weight rows; for its large tiles one copy of a box of rows then takes the place of eight
+// gathering ones a warp, whose instructions it has no room for.
+__global__ void __launch_bounds__(256) order_kernel(const uint4 *__restrict__ x, const int32_t *__restrict__ perm, int64_t pairs,
+                                                    int pieces, int choices, uint4 *__restrict__ in) {
+  griddep_launch_dependents();
+  griddep_wait();
+  const int64_t pos = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  if (pos >= pairs) return;
+  const uint4 *from = x + static_cast<int64_t>(perm[pos] / choices) * pieces;
+  uint4 *to = in + pos * pieces;
+#pragma unroll 4
+  for (int i = threadIdx.x & 31; i < pieces; i += 32) to[i] = __ldg(from + i);
+}
+
 // y[t] = sum over the token's choices of weight * output, in their order; a dropped choice adds nothing.
 template <int DT>
 __global__ void __launch_bounds__(256)
@@ -459,7 +474,17 @@ cudaError_t launch_dt(const ExpertsArgs &a, uint8_t *ws, const ExpertsPlan &plan
     p.gdiv = make_fastdiv(static_cast<uint32_t>(a.g));
     return p;
   };
-  e = launch_products<DT, true>(products(a.x, a.T, a.gate_up, 2 * a.I, a.K, ws + plan.h), plan, a.T, num_sms, stream);
+  const void *in = a.x;
+  int64_t in_rows = a.T;
+  if (plan.tmem && plan.tile >= kTileInOrder) {  // the outputs' place holds the rows until the second product
+    in = ws + plan.part;
+    in_rows = a.T * a.k;
+    e = launch_programmatic(order_kernel, static_cast<int>(cdiv(in_rows, 8)), 256, 0, stream,
+                            static_cast<const uint4 *>(a.x), static_cast<const int32_t *>(rows.perm), in_rows,
+                            static_cast<int>(a.K / 8), a.k, reinterpret_cast<uint4 *>(ws + plan.part));
+    if (e != cudaSuccess) return e;
+  }
+  e = launch_products<DT, true>(products(in, in_rows, a.gate_up, 2 * a.I, a.K, ws + plan.h), plan, a.T, num_sms, stream);
   if (e != cudaSuccess) return e;
   if (plan.direct)
     return launch_products<DT, false>(products(ws + plan.h, a.T * a.k, a.down, a.K, a.I, a.y), plan, a.T, num_sms, stream);

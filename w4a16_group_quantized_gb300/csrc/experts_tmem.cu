@@ -56,6 +56,7 @@ struct TCfg {
   static constexpr int kRegsRows = 56, kRegsIssue = 40, kRegsDequant = 64, kRegsSum = 72;
   static_assert(!kDeal || kRegsRows + kRegsIssue + 2 * kRegsDequant + kSumGroups * kRegsSum <= 64 * kThreads / 128,
                 "the registers that the block was launched with");
+  static constexpr bool kGather = BN < kTileInOrder;  // gate/up: rows by their tokens, else already in order
   static constexpr int kXSub = BN * 128;  // one block of 64 k of BN rows
   static constexpr int kXBytes = CB * kXSub;
   static constexpr int kCodeBytes = CB * kTileBytes;
@@ -154,6 +155,7 @@ template <int DT, int BN, int CB, int SUB, bool GATED>
 __global__ void __launch_bounds__(TCfg<BN, CB, SUB>::kThreads, 1)
     experts_tmem_kernel(const __grid_constant__ CUtensorMap in_map, const __grid_constant__ Products p) {
   using C = TCfg<BN, CB, SUB>;
+  constexpr bool GATHER = GATED && C::kGather;
   constexpr int S = C::kXStages, W = C::kWStages;
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t go_bar[S], done_bar[S], wfull_bar[W], wfree_bar[W], free_bar[2][2], drain_bar[2];
@@ -212,14 +214,14 @@ __global__ void __launch_bounds__(TCfg<BN, CB, SUB>::kThreads, 1)
     for (UnitWalk w(p, units); ok && w.take(&rt, &wt);) {
       const int first = rt.row0 + warp * kRows;
       const int rows = min(max(rt.rows - warp * kRows, 0), kRows);
-      // gate/up: the tokens of the warp's rows, four to a copy (a copy's rows past the tile's are any row of it)
+      // the tokens of the warp's rows, four to a copy (a copy's rows past the tile's are any row of it)
       int32_t tok[kRows];
-      if (GATED) {
+      if (GATHER) {
         const int32_t mine = rows > 0 ? p.plan.perm[first + min(lane, rows - 1)] / p.choices : 0;
 #pragma unroll
         for (int i = 0; i < kRows; ++i) tok[i] = __shfl_sync(0xffffffffu, mine, i);
       }
-      const uint32_t bytes = rows == 0 ? 0u : GATED ? (rows + 3) / 4 * 512u : kRows * 128u;
+      const uint32_t bytes = rows == 0 ? 0u : GATHER ? (rows + 3) / 4 * 512u : kRows * 128u;
       for (int q = 0; q < chunks; ++q, ++c, at.step()) {
         if (c >= static_cast<uint32_t>(S)) ok = warp_wait(done0 + 8 * at.s, at.phase ^ 1, abort_flag, p.err, kLimit);
         if (!ok) break;
@@ -232,7 +234,7 @@ __global__ void __launch_bounds__(TCfg<BN, CB, SUB>::kThreads, 1)
           for (int b = 0; b < CB; ++b) {
             if (b >= nb || rows == 0) break;
             const int k = (q * CB + b) * kTK;
-            if (GATED) {
+            if (GATHER) {
 #pragma unroll
               for (int i = 0; i < kRows / 4; ++i)
                 if (4 * i < rows)
@@ -511,7 +513,7 @@ cudaError_t launch_one(const Products &p, int num_sms, cudaStream_t stream) {
   const cudaError_t e = allow_smem(kern, bytes, &set);
   if (e != cudaSuccess) return e;
   CUtensorMap in_map;
-  if (!make_rows_map(&in_map, p.in, p.in_rows, p.K, GATED ? 1 : BN / 4, DT)) return cudaErrorInvalidValue;
+  if (!make_rows_map(&in_map, p.in, p.in_rows, p.K, GATED && TCfg<BN, CB, SUB>::kGather ? 1 : BN / 4, DT)) return cudaErrorInvalidValue;
   return launch_programmatic(kern, num_sms, TCfg<BN, CB, SUB>::kThreads, bytes, stream, in_map, p);
 }
 
