@@ -331,8 +331,7 @@ __global__ void __launch_bounds__(32 * NW, NT == 1 && NW == 8 ? 2 : 1) experts_k
 }
 
 // in[pos] = x[token of the pair at pos]: the rows of gate/up in the sort's order, a warp a row. The tensor-memory kernel
-// reads each of them once per 128 weight rows; for its large tiles one copy of a box of rows then takes the place of eight
-// gathering ones a warp, whose instructions it has no room for.
+// reads each of them once per 128 weight rows, a box of rows a copy.
 __global__ void __launch_bounds__(256) order_kernel(const uint4 *__restrict__ x, const int32_t *__restrict__ perm, int64_t pairs,
                                                     int pieces, int choices, uint4 *__restrict__ in) {
   griddep_launch_dependents();
@@ -394,9 +393,9 @@ ExpertsPlan experts_plan(int64_t T, int64_t K, int64_t I, int experts, int k, in
   // the sort, 4 tokens 44 against 42)
   p.direct = T == 1 || pairs <= experts / 4;
   p.tmem = !p.direct && mean >= kTmemRows && experts_tmem_takes(g);
-  // (tensor memory, 64 / 128 rows a tile, 64 experts of 2048 x 1024, g = 128: 48 rows an expert 121 / 135 us, 64 rows 139 /
-  // 145, 96 rows 179 / 167; g = 64, whose tiles of 128 rows take 64 k a chunk: 64 rows 164 / 190, 256 rows 461 / 420)
-  p.tile = p.tmem ? (mean <= (g % 128 == 0 ? 64 : 128) || g % 64 != 0 ? 64 : 128) : mean <= 8 ? 8 : mean <= 16 ? 16 : 32;
+  // (tensor memory, 64 / 128 rows a tile, 64 experts of 2048 x 1024, g = 128: 32 rows an expert 108 / 114 us, 48 rows 123 /
+  // 121, 96 rows 181 / 152; g = 64, whose tiles of 128 rows take 64 k a chunk: 64 rows 164 / 182, 128 rows 256 / 251)
+  p.tile = p.tmem ? (mean < (g % 128 == 0 ? 48 : 128) || g % 64 != 0 ? 64 : 128) : mean <= 8 ? 8 : mean <= 16 ? 16 : 32;
   p.max_tiles = static_cast<int>(p.direct ? pairs : max_row_tiles(pairs, experts, p.tile));
   auto up = [](size_t v) { return (v + 255) / 256 * 256; };
   p.part = 256;
@@ -476,7 +475,7 @@ cudaError_t launch_dt(const ExpertsArgs &a, uint8_t *ws, const ExpertsPlan &plan
   };
   const void *in = a.x;
   int64_t in_rows = a.T;
-  if (plan.tmem && plan.tile >= kTileInOrder) {  // the outputs' place holds the rows until the second product
+  if (plan.tmem) {  // the outputs' place holds the rows until the second product
     in = ws + plan.part;
     in_rows = a.T * a.k;
     e = launch_programmatic(order_kernel, static_cast<int>(cdiv(in_rows, 8)), 256, 0, stream,

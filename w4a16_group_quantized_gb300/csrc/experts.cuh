@@ -30,9 +30,7 @@ struct Products {
 // Whether the tensor-memory kernel takes groups of g: a block of 64 k then holds at most two, 32 k each.
 inline bool experts_tmem_takes(int g) { return g % 32 == 0; }
 
-// Rows of `in` per tile of the tensor-memory kernel, tile 64 or 128. From kTileInOrder rows gate/up's rows are copied into
-// order first (launch_experts_order), and `in` are those.
-constexpr int kTileInOrder = 128;
+// The products with `tile` (64 or 128) rows of `in` a tile; `in` stands in the sort's order for gate/up too.
 cudaError_t launch_experts_tmem(const Products &p, int dtype, bool gated, int tile, int num_sms, cudaStream_t stream);
 
 }  // namespace detail

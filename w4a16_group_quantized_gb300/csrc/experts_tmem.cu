@@ -8,8 +8,8 @@
 //
 // A unit is one 128-row weight tile x one tile of up to BN rows of one expert; the CTAs take units in turn and walk K in
 // chunks of CB blocks of 64, with no stop between units. Roles (24 or 32 warps, one CTA a SM):
-//   4 row warps        copy the rows of `in` with the 128-byte swizzle, a quarter of them each: gate/up gathers the
-//                      tokens' rows four to a copy, down's rows are already in order (one copy a block)
+//   1 row warp         copies the rows of `in`, which stand in the sort's order, with the 128-byte swizzle, one box a
+//                      block (three idle warps fill up its warpgroup)
 //   2 weight warps     copy the chunks' codes, and their group records, in bulk, through a ring of their own
 //   2 MMA warps        take the chunks in turn, each into an accumulator of its own that the chunk starts from zero
 //   8 dequant warps    two warpgroups take the chunks in turn: thread r stores row r's q - z in tensor memory and its
@@ -29,13 +29,14 @@
 // parity (S is at least 4, or 6 with two) are never overtaken.
 // Every wait is bounded (ptx.cuh).
 //
-// Measured (bf16, 64 experts of 2048 x 1024, 4096 rows of 8 choices): 354 us for gate/up and 162 for down, 0.78 and 0.85
-// PFLOP/s; the tensor pipe is 35% busy and the issue slots 73%: some 950 warp instructions an SM quarter and chunk of
-// 128 x 128 x 128 (dequant 270, gathering copies 280, sums 270, the rest waits) where the products take 512 cycles.
+// Measured (bf16, 64 experts of 2048 x 1024, 4096 rows of 8 choices): 281 us for gate/up and 161 for down, 0.98 and 0.85
+// PFLOP/s; issue slots bound it: some 700 warp instructions an SM quarter and chunk of 128 x 128 x 128 (dequant 270, sums
+// 270) where the products take 512 cycles.
 // tcgen05 instructions are issued under elect.sync, which keeps their operands in uniform registers: by "lane 0" an
-// MMA took 125 cycles to issue, so 40. Rows by 16-byte asynchronous copies of 128 threads bound a chunk at 1200 cycles.
-// Measured no faster: one MMA warp, or two with three barriers each, one ring for rows and weights, sum warps of 64
-// columns, waits that poll or sleep longer.
+// MMA took 125 cycles to issue, so 40. Gathering x's rows here, by 16-byte asynchronous copies of 128 threads, took 1200
+// cycles a chunk, and by four-row tensor copies 280 instructions of an SM quarter (gate/up 354 us): they are copied into
+// order once before (24 us). Measured no faster: one MMA warp, or two with three barriers each, one ring for rows and
+// weights, sum warps of 64 columns, waits that poll or sleep longer.
 #include <atomic>
 
 #include "experts.cuh"
@@ -56,7 +57,6 @@ struct TCfg {
   static constexpr int kRegsRows = 56, kRegsIssue = 40, kRegsDequant = 64, kRegsSum = 72;
   static_assert(!kDeal || kRegsRows + kRegsIssue + 2 * kRegsDequant + kSumGroups * kRegsSum <= 64 * kThreads / 128,
                 "the registers that the block was launched with");
-  static constexpr bool kGather = BN < kTileInOrder;  // gate/up: rows by their tokens, else already in order
   static constexpr int kXSub = BN * 128;  // one block of 64 k of BN rows
   static constexpr int kXBytes = CB * kXSub;
   static constexpr int kCodeBytes = CB * kTileBytes;
@@ -155,7 +155,6 @@ template <int DT, int BN, int CB, int SUB, bool GATED>
 __global__ void __launch_bounds__(TCfg<BN, CB, SUB>::kThreads, 1)
     experts_tmem_kernel(const __grid_constant__ CUtensorMap in_map, const __grid_constant__ Products p) {
   using C = TCfg<BN, CB, SUB>;
-  constexpr bool GATHER = GATED && C::kGather;
   constexpr int S = C::kXStages, W = C::kWStages;
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t go_bar[S], done_bar[S], wfull_bar[W], wfree_bar[W], free_bar[2][2], drain_bar[2];
@@ -167,8 +166,8 @@ __global__ void __launch_bounds__(TCfg<BN, CB, SUB>::kThreads, 1)
   volatile uint32_t *abort_flag = &abort_sh;
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
-      // the row warps, the chunk's dequant warps, and the sum warps of the accumulator's chunk before
-      mbar_init(smem_u32(&go_bar[s]), 4 + 4 + 4 * C::kSumGroups);
+      // the row warp, the chunk's dequant warps, and the sum warps of the accumulator's chunk before
+      mbar_init(smem_u32(&go_bar[s]), 1 + 4 + 4 * C::kSumGroups);
       mbar_init(smem_u32(&done_bar[s]), 1);
     }
     for (int s = 0; s < W; ++s) {
@@ -205,45 +204,22 @@ __global__ void __launch_bounds__(TCfg<BN, CB, SUB>::kThreads, 1)
   if (warp < 4) {
     // ----------------------------------------------------------------- rows
     regs_down<C::kDeal, C::kRegsRows>();
-    constexpr int kRows = BN / 4;  // of a warp
     Ring<S> at;
     uint32_t c = 0;
     bool ok = true;
     RowTile rt;
     int wt;
-    for (UnitWalk w(p, units); ok && w.take(&rt, &wt);) {
-      const int first = rt.row0 + warp * kRows;
-      const int rows = min(max(rt.rows - warp * kRows, 0), kRows);
-      // the tokens of the warp's rows, four to a copy (a copy's rows past the tile's are any row of it)
-      int32_t tok[kRows];
-      if (GATHER) {
-        const int32_t mine = rows > 0 ? p.plan.perm[first + min(lane, rows - 1)] / p.choices : 0;
-#pragma unroll
-        for (int i = 0; i < kRows; ++i) tok[i] = __shfl_sync(0xffffffffu, mine, i);
-      }
-      const uint32_t bytes = rows == 0 ? 0u : GATHER ? (rows + 3) / 4 * 512u : kRows * 128u;
+    for (UnitWalk w(p, units); warp == 0 && ok && w.take(&rt, &wt);) {
       for (int q = 0; q < chunks; ++q, ++c, at.step()) {
         if (c >= static_cast<uint32_t>(S)) ok = warp_wait(done0 + 8 * at.s, at.phase ^ 1, abort_flag, p.err, kLimit);
         if (!ok) break;
         if (elect_one()) {
-          const uint32_t to = smem_base + at.s * C::kXBytes + warp * kRows * 128;
           const uint32_t bar = go0 + 8 * at.s;
           const int nb = min(CB, p.KB - q * CB);
-          mbar_arrive_expect_tx(bar, bytes * nb);
+          mbar_arrive_expect_tx(bar, nb * C::kXSub);
 #pragma unroll
-          for (int b = 0; b < CB; ++b) {
-            if (b >= nb || rows == 0) break;
-            const int k = (q * CB + b) * kTK;
-            if (GATHER) {
-#pragma unroll
-              for (int i = 0; i < kRows / 4; ++i)
-                if (4 * i < rows)
-                  tma_gather4_2d(to + b * C::kXSub + i * 512, &in_map, k, tok[4 * i], tok[4 * i + 1], tok[4 * i + 2],
-                                 tok[4 * i + 3], bar);
-            } else {
-              tma_load_2d(to + b * C::kXSub, &in_map, k, first, bar);
-            }
-          }
+          for (int b = 0; b < CB; ++b)
+            if (b < nb) tma_load_2d(smem_base + at.s * C::kXBytes + b * C::kXSub, &in_map, (q * CB + b) * kTK, rt.row0, bar);
         }
         __syncwarp();
       }
@@ -513,7 +489,7 @@ cudaError_t launch_one(const Products &p, int num_sms, cudaStream_t stream) {
   const cudaError_t e = allow_smem(kern, bytes, &set);
   if (e != cudaSuccess) return e;
   CUtensorMap in_map;
-  if (!make_rows_map(&in_map, p.in, p.in_rows, p.K, GATED && TCfg<BN, CB, SUB>::kGather ? 1 : BN / 4, DT)) return cudaErrorInvalidValue;
+  if (!make_rows_map(&in_map, p.in, p.in_rows, p.K, BN, DT)) return cudaErrorInvalidValue;
   return launch_programmatic(kern, num_sms, TCfg<BN, CB, SUB>::kThreads, bytes, stream, in_map, p);
 }
 

@@ -239,16 +239,6 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap *map
       : "memory");
 }
 
-// As tma_load_2d for four rows of any index, one after another in shared memory; the map's box is one row high.
-__device__ __forceinline__ void tma_gather4_2d(uint32_t dst, const CUtensorMap *map, int32_t c0, int32_t r0, int32_t r1,
-                                               int32_t r2, int32_t r3, uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cta.global.tile::gather4.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5, "
-      "%6}], [%7];" ::"r"(dst),
-      "l"(map), "r"(c0), "r"(r0), "r"(r1), "r"(r2), "r"(r3), "r"(bar)
-      : "memory");
-}
-
 // 3-D tiled tensor copy global -> shared through a tensor map (TMA); c0 innermost (aligned as above).
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map, int32_t c0, int32_t c1, int32_t c2,
                                             uint32_t bar) {
