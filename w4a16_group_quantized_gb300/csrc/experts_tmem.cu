@@ -29,8 +29,8 @@
 // parity (S is at least 4, or 6 with two) are never overtaken.
 // Every wait is bounded (ptx.cuh).
 //
-// Measured (bf16, 64 experts of 2048 x 1024, 4096 rows of 8 choices): 281 us for gate/up and 161 for down, 0.98 and 0.85
-// PFLOP/s; issue slots bound it: some 700 warp instructions an SM quarter and chunk of 128 x 128 x 128 (dequant 270, sums
+// Measured (bf16, 64 experts of 2048 x 1024, 4096 rows of 8 choices): 279 us for gate/up and 160 for down, 0.98 and 0.86
+// PFLOP/s; the tensor pipe is 44% busy and the issue slots 77%: some 800 warp instructions an SM quarter and chunk of 128 x 128 x 128 (dequant 270, sums
 // 270) where the products take 512 cycles.
 // tcgen05 instructions are issued under elect.sync, which keeps their operands in uniform registers: by "lane 0" an
 // MMA took 125 cycles to issue, so 40. Gathering x's rows here, by 16-byte asynchronous copies of 128 threads, took 1200
