@@ -528,3 +528,31 @@ def test_rows_in_a_captured_graph():
     torch.cuda.synchronize()
     for a, b in zip(got, step()):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("g", [40, 64, 128])
+@pytest.mark.parametrize("T", [1, 2, 4])
+def test_experts_few_pairs_go_without_a_sort(T, g):
+    m = Experts(328, 264, 32, g, "bf16")
+    x = randn(T, T, 328, dtype="bf16")
+    ids, w = choices(T, T, 32, 2)
+    m.check(x, ids, w)
+    ids[0, 0] = -1
+    if T > 1:
+        ids[1] = 32
+    m.check(x, ids, w)
+
+
+@pytest.mark.parametrize("T,E,g", [(130, 3, 40), (20, 3, 8), (90, 4, 24), (300, 2, 72)])
+def test_experts_groups_that_end_anywhere(T, E, g):
+    """Groups that are no multiple of 32: the register-operand kernel at 16 and 32 rows a tile, several groups a block."""
+    m = Experts(264, 136, E, g, "f16")
+    m.check(randn(T, T, 264), *choices(T, T, E, 2))
+
+
+@pytest.mark.parametrize("g", [32, 64, 96, 128, 192])
+@pytest.mark.parametrize("T", [70, 400])
+def test_experts_many_rows_by_group_size(T, g):
+    """64 and 128 rows a tile, each way that groups cut a chunk, and sizes that end inside tiles, chunks and groups."""
+    m = Experts(456, 328, 4, g, "bf16")
+    m.check(randn(T, T, 456, dtype="bf16"), *choices(T, T, 4, 2, dropped=0.1))
