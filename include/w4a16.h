@@ -455,7 +455,10 @@ W4_API int w4_route(const void *logits_dev, int64_t T, int32_t experts, int64_t 
  *
  * Numerics: q - z enters the products exactly and a group's sum is scaled in
  * fp32; silu(gate) * up is rounded once to the type (the second product's
- * operand); sums are fp32, added in a fixed order, and y is rounded once.
+ * operand; for fp16 after division of a row whose largest value is past the
+ * type's range by a power of two, so that it cannot overflow), or, at one token
+ * and where T * k <= experts / 4, held in 16 bits of fraction; sums are fp32,
+ * added in a fixed order, and y is rounded once.
  * The workspace is at least w4a16_experts_workspace_bytes(...) bytes,
  * 256-byte aligned. Its first word is a device error word: after a wait inside
  * a kernel gave up (about a second) w4_last_device_error(workspace) reports

@@ -1,0 +1,79 @@
+"""Edges of w4_route, w4a16_experts and w4_lora_add on the GPU. Checks and bounds are test_gpu_rows.py's; what differs is derived here.
+
+ * h = silu(gate) * up of a row whose largest |h| is past fp16's range is held divided by a power of two no larger than
+   max |h| / 2^14, so the type's least step in it is 2^-25 max |h| / 2^14 instead of 2^-25.
+ * where the choices go without a sort, h is held to 2^-16 (two 8-bit fractions), so y's own rounding is all that is left: as a
+   2-norm u / sqrt(3 E[m^2]) = 0.39 u for fractions m spread over their logarithm, and some percent for those that are not.
+"""
+from __future__ import annotations
+
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from test_gpu_rows import U, Experts, choices, depth, f64, randn
+
+pytestmark = pytest.mark.gpu
+
+
+# ---------------------------------------------------------------------------------------------------------- experts
+
+def check_wide(m, x, ids, weights, rows=None, **kw):
+    """Experts.check for rows whose h may be past the type's range; `rows`: those to look at."""
+    y = m.run(x, ids, weights, **kw)
+    rows = range(x.shape[0]) if rows is None else rows
+    u = U[m.dtype]
+    x64, w64, idn = f64(x), f64(weights), ids.cpu().numpy()
+    top = 0.0
+    for t in rows:
+        want, tol = np.zeros(m.K), np.zeros(m.K)
+        for j, e in enumerate(idn[t]):
+            if e < 0 or e >= m.E:
+                continue
+            s, es = m.w1[e] @ x64[t], depth(m.K) * 62 * (m.s1[e] @ np.abs(x64[t]))
+            g, up, eg, eu = s[0::2], s[1::2], es[0::2], es[1::2]
+            silu = oracle.silu(g)
+            h = silu * up
+            top = max(top, np.abs(h).max())
+            eh = 1.1 * eg * (np.abs(up) + eu) + np.abs(silu) * eu
+            eh = eh + (u + 1e-5) * (np.abs(h) + eh) + 2.0 ** -25 * max(1.0, np.abs(h).max() * 2.0 ** -14)
+            eo = np.abs(m.w2[e]) @ eh + depth(m.I) * 62 * (m.s2[e] @ (np.abs(h) + eh))
+            o = m.w2[e] @ h
+            want += w64[t, j] * o
+            tol += abs(w64[t, j]) * (eo + 1e-6 * np.abs(o))
+        err = np.abs(f64(y[t]) - want)
+        assert np.isfinite(f64(y[t])).all(), t
+        bound = tol * (1 + u) + u * np.abs(want) + 2.0 ** -24
+        assert (err <= bound).all(), (t, (err / bound).max())
+    return top
+
+
+@pytest.mark.parametrize("T,E,g", [(1, 4, 128), (2, 16, 40), (6, 4, 64), (30, 4, 40), (70, 4, 40), (70, 4, 64), (70, 4, 32), (400, 4, 128),
+                                   (400, 4, 64)])
+def test_experts_h_past_fp16(T, E, g):
+    """silu(gate) * up past 65504 in some rows (y is in range): each kernel, and rows in range beside them."""
+    m = Experts(256, 136, E, g, "f16")
+    x = randn(T, T, 256)
+    x[::7] *= 400
+    ids, _ = choices(T, T, E, 2)
+    w = torch.full((T, 2), 2.0 ** -10, device="cuda")
+    assert check_wide(m, x, ids, w) > 2 * 65504
+    if T > 7:  # a row that is infinite stays infinite, or undefined, by itself
+        x[7, 5] = float("inf")
+        check_wide(m, x, ids, w, rows=[t for t in range(T) if t != 7])
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_experts_few_pairs_hold_h_in_more_bits(dtype):
+    m = Experts(1024, 136, 32, 128, dtype)
+    x = randn(9, 4, 1024, dtype=dtype)
+    ids, w = choices(9, 4, 32, 2)
+    y = f64(m.check(x, ids, w))
+    want = np.zeros(y.shape)
+    x64, w64 = f64(x), f64(w)
+    for t, row in enumerate(ids.tolist()):
+        for j, e in enumerate(row):
+            s = m.w1[e] @ x64[t]
+            want[t] += w64[t, j] * (m.w2[e] @ (oracle.silu(s[0::2]) * s[1::2]))
+    assert np.linalg.norm(y - want) <= 0.48 * U[dtype] * np.linalg.norm(want)

@@ -2,8 +2,12 @@
 // weights in 4-bit groups, w = (q - z) s.
 //
 // The pairs (token, choice) are sorted by expert (rows.cu) and cut into tiles of one expert; a first product makes
-// h = silu(gate) * up of each pair, rounded once to the 16-bit type (the second product's operand), a second one the
-// expert's output in 32 bits, and a last pass adds a token's outputs with their weights, in the order of its choices.
+// h = silu(gate) * up of each pair, rounded once to the 16-bit type (the second product's operand: 32 bits of it would take
+// two or three products instead of one), a second one the expert's output in 32 bits, and a last pass adds a token's
+// outputs with their weights, in the order of its choices. In fp16 a row of h whose largest value is past the type's range
+// is divided by a power of two before the second product (range_kernel).
+// Few pairs go without a sort, one row a product, which leaves columns of the products free: h then stands in two of them, as
+// its rounding to bf16 and what that left (16 bits and a 32-bit exponent, whatever the type: codes are exact in either).
 //
 // The products here run on register-operand tensor-core instructions, for few rows per expert: the weights of the
 // chosen experts are read once and that is the floor. Codes go through rings in shared memory that belong to one warp
@@ -77,6 +81,7 @@ __global__ void __launch_bounds__(32 * NW, NT == 1 && NW == 8 ? 2 : 1) experts_k
   using St = Stage<NT>;
   constexpr int D = St::kCount;
   constexpr bool ALL = DIRECT && !GATED;
+  constexpr int OT = ALL ? kDtypeBf16 : DT;  // the operands' type
   extern __shared__ __align__(128) uint8_t smem[];
   griddep_launch_dependents();
   griddep_wait();
@@ -89,6 +94,7 @@ __global__ void __launch_bounds__(32 * NW, NT == 1 && NW == 8 ? 2 : 1) experts_k
   const int tile = blockIdx.x / per_tile;
   const int n0 = ((blockIdx.x - tile * per_tile) * slabs_block + warp / kw) * kSlabRows;
   RowTile rt;
+  int cols;           // of `in` in the tile: its rows, or a row's two halves
   int id = -1;        // ALL: lane j's are choice j's
   float weight = 0.0f;
   if (DIRECT) {
@@ -103,6 +109,7 @@ __global__ void __launch_bounds__(32 * NW, NT == 1 && NW == 8 ? 2 : 1) experts_k
     rt = p.plan.tiles[tile];  // (read beside the count: the list has room for every block)
     if (tile >= *p.plan.ntiles) return;
   }
+  cols = ALL ? 2 : rt.rows;
 
   // the rows that the lane copies: lane / 8 and lane / 8 + 4 of each eight, piece lane % 8 of their 128 bytes
   const uint16_t *xr[2 * NT];
@@ -110,8 +117,8 @@ __global__ void __launch_bounds__(32 * NW, NT == 1 && NW == 8 ? 2 : 1) experts_k
   for (int n = 0; n < 2 * NT; ++n) {
     const int col = n * 4 + (lane >> 3), pos = rt.row0 + col;
     xr[n] = nullptr;
-    if (col < rt.rows) {
-      const int64_t row = ALL ? static_cast<int64_t>(pos) * p.choices
+    if (col < cols) {
+      const int64_t row = ALL ? static_cast<int64_t>(rt.row0) * p.choices * 2 + col
                           : DIRECT && GATED ? pos / p.choices
                           : GATED ? p.plan.perm[pos] / p.choices : pos;
       xr[n] = p.in + row * p.K + 8 * (lane & 7);
@@ -125,10 +132,10 @@ __global__ void __launch_bounds__(32 * NW, NT == 1 && NW == 8 ? 2 : 1) experts_k
   // where the lane's pieces of x go
   const uint32_t x_to = ring + St::kX + (lane >> 3) * 128 + ((lane & 7) ^ (lane >> 3)) * 16;
   const uint32_t x_to4 = ring + St::kX + ((lane >> 3) + 4) * 128 + ((lane & 7) ^ ((lane >> 3) + 4)) * 16;
-  if (rt.rows < 8 * NT)  // rows that the tile has not are zeros
+  if (cols < 8 * NT)  // rows that the tile has not are zeros
     for (int i = lane; i < D * 2 * NT * 64; i += 32) {
       const int at = i / 64, row = i % (64) / 8;
-      if (at % NT * 8 + row >= rt.rows)
+      if (at % NT * 8 + row >= cols)
         asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(ring + at / (2 * NT) * St::kBytes + St::kX +
                                                                       at % (2 * NT) * 1024 + i % 64 * 16),
                      "r"(0)
@@ -163,7 +170,7 @@ __global__ void __launch_bounds__(32 * NW, NT == 1 && NW == 8 ? 2 : 1) experts_k
           for (int n = 0; n < 2 * NT; ++n)
             if (xr[n])
               cp_async16_zfill((n & 1 ? x_to4 : x_to) + to + (u * NT + n / 2) * 1024,
-                               bytes ? xr[n] + (ALL ? static_cast<int64_t>(choice) * p.K : 0) + k : p.in, bytes);
+                               bytes ? xr[n] + (ALL ? static_cast<int64_t>(choice) * 2 * p.K : 0) + k : p.in, bytes);
           if (MODE == kBlock || (MODE == kTwo && u == 0)) {
             const uint8_t *m = expert + meta0 + static_cast<int64_t>(p.gdiv.div(k)) * kRecBytes;
             if (lane < 20)  // 32 scales and 32 zeros, 4 bytes a lane
@@ -183,7 +190,7 @@ __global__ void __launch_bounds__(32 * NW, NT == 1 && NW == 8 ? 2 : 1) experts_k
   };
   auto record_at = [&](uint32_t at) { return lds16(at + 2 * lane) | ((lds8(at + 64 + lane / 2) >> (4 * (lane & 1))) & 15) << 16; };
 
-  constexpr uint32_t kOne = DT == kDtypeBf16 ? 0x3F803F80u : 0x3C003C00u;
+  constexpr uint32_t kOne = OT == kDtypeBf16 ? 0x3F803F80u : 0x3C003C00u;
   float sum[2][NT][4] = {};  // rows g, g + 8 (and 16, 24): what is done
   float d0[NT][4], d1[NT][4], ones[NT][4];
   auto clear = [&] {
@@ -223,9 +230,9 @@ __global__ void __launch_bounds__(32 * NW, NT == 1 && NW == 8 ? 2 : 1) experts_k
       }
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        mma_16816<DT>(d0[n], a[0][2 * q], a[1][2 * q], a[0][2 * q + 1], a[1][2 * q + 1], b[2 * q], b[2 * q + 1]);
-        mma_16816<DT>(d1[n], a[2][2 * q], a[3][2 * q], a[2][2 * q + 1], a[3][2 * q + 1], b[2 * q], b[2 * q + 1]);
-        mma_16816<DT>(ones[n], kOne, kOne, kOne, kOne, b[2 * q], b[2 * q + 1]);
+        mma_16816<OT>(d0[n], a[0][2 * q], a[1][2 * q], a[0][2 * q + 1], a[1][2 * q + 1], b[2 * q], b[2 * q + 1]);
+        mma_16816<OT>(d1[n], a[2][2 * q], a[3][2 * q], a[2][2 * q + 1], a[3][2 * q + 1], b[2 * q], b[2 * q + 1]);
+        mma_16816<OT>(ones[n], kOne, kOne, kOne, kOne, b[2 * q], b[2 * q + 1]);
       }
     }
   };
@@ -254,8 +261,8 @@ __global__ void __launch_bounds__(32 * NW, NT == 1 && NW == 8 ? 2 : 1) experts_k
                      : "=r"(c0), "=r"(c1)
                      : "r"(at + u * 1024 + (t >> 1) * 512 + (8 * i + g) * 16 + 8 * (t & 1))
                      : "memory");
-        operands<DT>(c0, a[i]);
-        operands<DT>(c1, a[i] + 4);
+        operands<OT>(c0, a[i]);
+        operands<OT>(c1, a[i] + 4);
       }
       const uint32_t x_at = at + St::kX + u * NT * 1024;
       if (MODE == kAny) {
@@ -312,15 +319,24 @@ __global__ void __launch_bounds__(32 * NW, NT == 1 && NW == 8 ? 2 : 1) experts_k
         gate += red[w][col][2 * j];
         up += red[w][col][2 * j + 1];
       }
-      static_cast<uint16_t *>(p.out)[static_cast<int64_t>(rt.row0 + col) * (p.N / 2) + n0 / 2 + j] =
-          out_bits<DT>(silu_mul(gate, up));
+      const float h = silu_mul(gate, up);
+      const int64_t row = rt.row0 + col;
+      if (DIRECT) {  // (what an infinity leaves is nothing, not the NaN of its difference to itself)
+        uint16_t *out = static_cast<uint16_t *>(p.out) + row * p.N + n0 / 2 + j;
+        const uint16_t hi = out_bits<kDtypeBf16>(h);
+        const float left = value_f32<kDtypeBf16>(hi);
+        out[0] = hi;
+        out[p.N / 2] = out_bits<kDtypeBf16>(isinf(left) ? 0.0f : h - left);
+      } else {
+        store_h<DT>(p, h, row * (p.N / 2) + n0 / 2 + j, tile);
+      }
     }
   } else {
     for (int i = tid; i < rt.rows * 32; i += threads) {
       const int col = i / 32, r = i % 32;
       if (n0 + r >= p.N) continue;
       float v = 0.0f;
-      for (int w = w0; w < w0 + kw; ++w) v += red[w][col][r];
+      for (int w = w0; w < w0 + kw; ++w) v += ALL ? red[w][1][r] + red[w][0][r] : red[w][col][r];
       const int64_t at = static_cast<int64_t>(rt.row0 + col) * p.N + n0 + r;
       if (ALL)
         static_cast<uint16_t *>(p.out)[at] = out_bits<DT>(v);
@@ -344,11 +360,46 @@ __global__ void __launch_bounds__(256) order_kernel(const uint4 *__restrict__ x,
   for (int i = threadIdx.x & 31; i < pieces; i += 32) to[i] = __ldg(from + i);
 }
 
-// y[t] = sum over the token's choices of weight * output, in their order; a dropped choice adds nothing.
-template <int DT>
+// fp16: the rows of h in the tiles that gate/up has marked. A row with values past the type's range (infinities in h, whose 32-bit
+// values stand in `wide`) is written anew divided by 2^e, which brings its largest finite one below 2^15, and its factor is 2^e; every
+// other row's factor is 1. What a small value of such a row loses is below 2^-39 of its largest. A block a tile; without a marked
+// tile it writes the factors alone (a call of 16 rows 156.2 us with it, 154.8 without).
+__global__ void __launch_bounds__(256)
+    range_kernel(const RowTile *tiles, const int32_t *ntiles, uint16_t *h, const float *wide, int cols, float *factor) {
+  griddep_launch_dependents();
+  griddep_wait();
+  if (static_cast<int>(blockIdx.x) >= *ntiles) return;
+  const RowTile rt = tiles[blockIdx.x];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (!rt.flag) {
+    for (int r = threadIdx.x; r < rt.rows; r += 256) factor[rt.row0 + r] = 1.0f;
+    return;
+  }
+  for (int r = warp; r < rt.rows; r += 8) {
+    const int64_t at = static_cast<int64_t>(rt.row0 + r) * cols;
+    float top = 0.0f;
+    for (int j = lane; j < cols; j += 32)
+      if ((h[at + j] & 0x7FFFu) == 0x7C00u && !isinf(wide[at + j])) top = fmaxf(top, fabsf(wide[at + j]));
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+    const int e = top > 0.0f ? static_cast<int>(__float_as_uint(top) >> 23) - 127 - 14 : 0;  // 2^(e + 14) <= top < 2^(e + 15)
+    if (lane == 0) factor[rt.row0 + r] = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+    if (e == 0) continue;
+    const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+    for (int j = lane; j < cols; j += 32) {
+      const uint16_t bits = h[at + j];
+      const float v = (bits & 0x7FFFu) == 0x7C00u ? wide[at + j] : value_f32<kDtypeF16>(bits);
+      h[at + j] = out_bits<kDtypeF16>(v * down);
+    }
+  }
+}
+
+// y[t] = sum over the token's choices of weight * output, in their order; a dropped choice adds nothing. FACTOR: the outputs of
+// rows that range_kernel has divided are multiplied by their factors.
+template <int DT, bool FACTOR>
 __global__ void __launch_bounds__(256)
     combine_kernel(const float *__restrict__ part, const int32_t *__restrict__ inverse, const float *__restrict__ weights,
-                   int64_t T, int K, int choices, uint16_t *__restrict__ y) {
+                   const float *__restrict__ factor, int64_t T, int K, int choices, uint16_t *__restrict__ y) {
   griddep_launch_dependents();
   griddep_wait();
   const int per_row = K / 8;  // K is a multiple of 8
@@ -361,8 +412,13 @@ __global__ void __launch_bounds__(256)
     const int pos = inverse[t * choices + j];
     if (pos < 0) continue;
     const float w = weights[t * choices + j];
-    const float4 a = __ldg(reinterpret_cast<const float4 *>(part + static_cast<int64_t>(pos) * K + c));
-    const float4 b = __ldg(reinterpret_cast<const float4 *>(part + static_cast<int64_t>(pos) * K + c + 4));
+    float4 a = __ldg(reinterpret_cast<const float4 *>(part + static_cast<int64_t>(pos) * K + c));
+    float4 b = __ldg(reinterpret_cast<const float4 *>(part + static_cast<int64_t>(pos) * K + c + 4));
+    if (FACTOR) {
+      const float f = factor[pos];
+      a.x *= f, a.y *= f, a.z *= f, a.w *= f;
+      b.x *= f, b.y *= f, b.z *= f, b.w *= f;
+    }
     s[0] += w * a.x;
     s[1] += w * a.y;
     s[2] += w * a.z;
@@ -376,12 +432,14 @@ __global__ void __launch_bounds__(256)
                                                          out_bits2<DT>(s[4], s[5]), out_bits2<DT>(s[6], s[7]));
 }
 
-// The workspace: [error word][ntiles][outputs in 32 bits][h][perm][inverse][tiles].
+// The workspace: [error word][ntiles][outputs in 32 bits][h][perm][inverse][tiles]. Until the second product the outputs' place
+// holds what the first one needs: the rows in order (tensor memory) and, fp16, the values of h past the type's range. The second
+// product and the last pass need no perm: its place then holds the rows' factors (fp16).
 struct ExpertsPlan {
   bool direct;  // no sort: each pair by itself, and a token's choices added in the second product
   bool tmem;
   int tile, max_tiles;
-  size_t part, h, perm, inverse, tiles, bytes;
+  size_t part, wide, h, perm, inverse, tiles, bytes;
 };
 
 ExpertsPlan experts_plan(int64_t T, int64_t K, int64_t I, int experts, int k, int g) {
@@ -399,8 +457,11 @@ ExpertsPlan experts_plan(int64_t T, int64_t K, int64_t I, int experts, int k, in
   p.max_tiles = static_cast<int>(p.direct ? pairs : max_row_tiles(pairs, experts, p.tile));
   auto up = [](size_t v) { return (v + 255) / 256 * 256; };
   p.part = 256;
-  p.h = p.part + up(static_cast<size_t>(pairs) * K * 4);
-  p.perm = p.h + up(static_cast<size_t>(pairs) * I * 2);
+  p.wide = p.part + (p.tmem ? up(static_cast<size_t>(pairs) * K * 2) : 0);
+  const size_t outputs = p.direct ? 0 : up(static_cast<size_t>(pairs) * K * 4);
+  const size_t wide_end = p.direct ? 0 : p.wide - p.part + up(static_cast<size_t>(pairs) * I * 4);
+  p.h = p.part + (outputs > wide_end ? outputs : wide_end);
+  p.perm = p.h + up(static_cast<size_t>(pairs) * I * (p.direct ? 4 : 2));
   p.inverse = p.perm + up(static_cast<size_t>(pairs) * 4);
   p.tiles = p.inverse + up(static_cast<size_t>(pairs) * 4);
   p.bytes = p.tiles + up(static_cast<size_t>(p.max_tiles) * sizeof(RowTile));
@@ -462,6 +523,7 @@ cudaError_t launch_dt(const ExpertsArgs &a, uint8_t *ws, const ExpertsPlan &plan
     p.meta = cdiv(N, kTN) * p.KB * kTileBytes;
     p.expert_bytes = p.meta + cdiv(N, kTN) * p.G * kRecBytes;
     p.out = out;
+    p.wide = reinterpret_cast<float *>(ws + plan.wide);
     p.plan = rows;
     p.err = rows.err;
     p.slabs = static_cast<int>(cdiv(N, plan.tmem ? kTN : kSlabRows));
@@ -487,11 +549,19 @@ cudaError_t launch_dt(const ExpertsArgs &a, uint8_t *ws, const ExpertsPlan &plan
   if (e != cudaSuccess) return e;
   if (plan.direct)
     return launch_products<DT, false>(products(ws + plan.h, a.T * a.k, a.down, a.K, a.I, a.y), plan, a.T, num_sms, stream);
+  constexpr bool kRange = DT == kDtypeF16;
+  float *factor = reinterpret_cast<float *>(rows.perm);
+  if (kRange) {
+    e = launch_programmatic(range_kernel, plan.max_tiles, 256, 0, stream, static_cast<const RowTile *>(rows.tiles),
+                            static_cast<const int32_t *>(rows.ntiles), reinterpret_cast<uint16_t *>(ws + plan.h),
+                            reinterpret_cast<const float *>(ws + plan.wide), static_cast<int>(a.I), factor);
+    if (e != cudaSuccess) return e;
+  }
   e = launch_products<DT, false>(products(ws + plan.h, a.T * a.k, a.down, a.K, a.I, ws + plan.part), plan, a.T, num_sms, stream);
   if (e != cudaSuccess) return e;
-  return launch_programmatic(combine_kernel<DT>, static_cast<int>(cdiv(a.T * (a.K / 8), 256)), 256, 0, stream,
+  return launch_programmatic(combine_kernel<DT, kRange>, static_cast<int>(cdiv(a.T * (a.K / 8), 256)), 256, 0, stream,
                              reinterpret_cast<const float *>(ws + plan.part), static_cast<const int32_t *>(rows.inverse), a.weights,
-                             a.T, static_cast<int>(a.K), a.k, static_cast<uint16_t *>(a.y));
+                             static_cast<const float *>(factor), a.T, static_cast<int>(a.K), a.k, static_cast<uint16_t *>(a.y));
 }
 
 }  // namespace

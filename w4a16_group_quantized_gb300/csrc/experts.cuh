@@ -13,6 +13,7 @@ struct Products {
   int64_t expert_bytes;
   int64_t meta;          // offset of the group records in them
   void *out;             // gate/up: h [pairs, N / 2], 16 bits; down: [pairs, N], 32 bits
+  float *wide;           // fp16 gate/up after a sort: [pairs, N / 2], written only where h is past the type's range
   RowPlan plan;
   uint32_t *err;
   int64_t in_rows;
@@ -26,6 +27,18 @@ struct Products {
   int kw;                // warps that share a slab's K
   FastDiv gdiv;
 };
+
+// The h of sorted row pos, column j, of tile t: rounded to the type. Where that overflows, the 32-bit value goes to `wide` and the
+// tile is marked (range_kernel in experts.cu then scales the row).
+template <int DT>
+__device__ __forceinline__ void store_h(const Products &p, float h, int64_t at, int t) {
+  const uint16_t bits = out_bits<DT>(h);
+  static_cast<uint16_t *>(p.out)[at] = bits;
+  if (DT == kDtypeF16 && (bits & 0x7FFFu) == 0x7C00u) {
+    p.wide[at] = h;
+    p.plan.tiles[t].flag = 1;
+  }
+}
 
 // Whether the tensor-memory kernel takes groups of g: a block of 64 k then holds at most two, 32 k each.
 inline bool experts_tmem_takes(int g) { return g % 32 == 0; }

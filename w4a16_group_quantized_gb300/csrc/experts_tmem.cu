@@ -137,6 +137,8 @@ struct UnitWalk {
     if (u < units) next = p.plan.tiles[u / p.slabs];
     return true;
   }
+  // the index of the tile that was taken last
+  __device__ __forceinline__ int taken() const { return (u - step) / p.slabs; }
 };
 
 // A place in the ring of S stages: chunk c's, with the parity of its phase.
@@ -443,7 +445,6 @@ __global__ void __launch_bounds__(TCfg<BN, CB, SUB>::kThreads, 1)
         // rows n & ~1 (even lane: gate) and n | 1 (odd lane: up): the pair swaps values, the even lane makes the
         // first half of the columns, the odd lane the second
         const int odd = lane & 1;
-        uint16_t *out = static_cast<uint16_t *>(p.out) + n / 2;
         const int ld = p.N / 2;
 #pragma unroll
         for (int i = 0; i < kCols / 4; ++i) {
@@ -455,7 +456,7 @@ __global__ void __launch_bounds__(TCfg<BN, CB, SUB>::kThreads, 1)
             const float got = __shfl_xor_sync(0xffffffffu, odd ? f[j] : b[j], 1);
             const float gate = odd ? got : f[j], up = odd ? b[j] : got;
             const int col = 2 * i + j + odd * (kCols / 2);
-            if (n < p.N && col < cols) out[(pos0 + col) * ld] = out_bits<DT>(silu_mul(gate, up));
+            if (n < p.N && col < cols) store_h<DT>(p, silu_mul(gate, up), (pos0 + col) * ld + n / 2, w.taken());
           }
         }
       } else if (n < p.N) {

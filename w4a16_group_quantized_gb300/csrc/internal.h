@@ -156,7 +156,7 @@ struct RowTile {
   int32_t key;   // nkeys: rows without a key
   int32_t row0;  // first sorted position
   int32_t rows;
-  int32_t pad;
+  int32_t flag;  // 0; for the kernels after the sort
 };
 struct RowPlan {
   int32_t *perm;     // [count] the row at each sorted position
