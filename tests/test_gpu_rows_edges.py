@@ -12,7 +12,7 @@ import pytest
 import torch
 
 import oracle
-from test_gpu_rows import U, Experts, choices, depth, f64, randn
+from test_gpu_rows import U, Experts, check_route, choices, depth, f64, randn
 
 pytestmark = pytest.mark.gpu
 
@@ -77,3 +77,17 @@ def test_experts_few_pairs_hold_h_in_more_bits(dtype):
             s = m.w1[e] @ x64[t]
             want[t] += w64[t, j] * (m.w2[e] @ (oracle.silu(s[0::2]) * s[1::2]))
     assert np.linalg.norm(y - want) <= 0.48 * U[dtype] * np.linalg.norm(want)
+
+
+# ------------------------------------------------------------------------------------------------------------ route
+
+def test_route_scores_below_the_least_sum():
+    """Chosen scores that vanish in 32 bits are divided by their sum all the same."""
+    for at in (-80.0, -88.0, -95.0, -104.0, -300.0):
+        check_route(randn(7, 20, 64, dtype="f32", std=1.5) + at, 6, sigmoid=True, scale=2.5)
+    logits = randn(8, 20, 64, dtype="f32", std=1.5) - 150.0
+    logits[:, 5] = 3.0
+    b = randn(9, 64, dtype="f32", std=1.0)
+    b[5] = -50.0  # keeps the one expert with a score away
+    check_route(logits, 6, bias=b)
+    check_route(logits, 6, bias=b, renormalize=False)

@@ -3,9 +3,9 @@
 // For each row l of E logits: s_i = e^(l_i - max l) / sum e^(l - max l), or 1 / (1 + e^-l_i); c_i = s_i + b_i.
 // The row keeps its `top_groups` best groups of E / groups consecutive experts (a group is worth the sum of
 // its `group_top` best c) and chooses the k best c in them, the lowest index first among equals; its weights are
-// s at the chosen experts, divided by their sum if asked, times `scale`. Without a bias the chosen experts are
-// found by the logits themselves, which order the scores and do not round (32-bit scores of unlike logits may be
-// equal).
+// s at the chosen experts, divided by their sum if asked (also where they vanish in 32 bits), times `scale`.
+// Without a bias the chosen experts are found by the logits themselves, which order the scores and do not round
+// (32-bit scores of unlike logits may be equal).
 //
 // One warp per row: lane i holds PER consecutive experts as 32-bit keys whose unsigned order is that of the values, so
 // that each choice is a warp-wide integer reduction (the largest key) and a vote (the lowest lane that has it). Groups
@@ -214,7 +214,17 @@ __global__ void __launch_bounds__(32 * kRouteWarps)
     float all = w;
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) all += __shfl_xor_sync(kFull, all, d);
-    w = w / fmaxf(all, 1e-37f);
+    if (all < 1e-30f) {
+      // The chosen scores leave the range of 32 bits, but their quotients do not: below 1e-30 / 32 both kinds of score are
+      // e^l times what all experts share, so the weights are e^(l - m) over their sum, m the largest chosen logit.
+      const float c = lane < o.k ? masked(load_logit<DT>(logits, at + mine)) : -INFINITY;
+      const float m = value_of(__reduce_max_sync(kFull, key_of(c)));
+      w = exp_below(c, m);
+      all = w;
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) all += __shfl_xor_sync(kFull, all, d);
+    }
+    w = all > 0.0f ? w / all : 0.0f;  // no expert left: weights of 0
   }
   if (lane < o.k) {
     weights[row * o.k + lane] = w * o.scale;
