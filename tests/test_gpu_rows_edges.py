@@ -12,6 +12,7 @@ import pytest
 import torch
 
 import oracle
+import w4a16_group_quantized_gb300 as w4
 from test_gpu_rows import U, Experts, check_route, choices, depth, f64, randn
 
 pytestmark = pytest.mark.gpu
@@ -91,3 +92,70 @@ def test_route_scores_below_the_least_sum():
     b[5] = -50.0  # keeps the one expert with a score away
     check_route(logits, 6, bias=b)
     check_route(logits, 6, bias=b, renormalize=False)
+
+
+# ------------------------------------------------------------------------------------------------ streams and graphs
+
+def crowd(*sizes):
+    """New tensors of the current stream with every byte set: they take blocks that were freed too early."""
+    return [torch.full((s,), 0x7F, dtype=torch.uint8, device="cuda") for s in sizes for _ in range(4)]
+
+
+def test_workspace_grows_while_its_stream_is_busy():
+    """A short call and a long one on another stream, not waited for in between: the first one's buffer is still its own."""
+    m = Experts(256, 128, 8, 128, "bf16")
+    small, large = randn(1, 40, 256, dtype="bf16"), randn(2, 600, 256, dtype="bf16")
+    at = [choices(3, 40, 8, 2), choices(4, 600, 8, 2)]
+    A, B = randn(5, 3, 16, 256, dtype="bf16"), randn(6, 3, 320, 16, dtype="bf16")
+    adapter = [(torch.arange(T) % 4 - 1).to(torch.int32).cuda() for T in (40, 600)]
+
+    def calls(ws, stream):
+        out = []
+        for x, (ids, w), ad in zip((small, large), at, adapter):
+            out.append(w4.w4_lora_add(None, x, A, B, ad, workspace=ws, stream=stream))
+            out.append(m.run(x, ids, w, workspace=ws, stream=stream))
+            out += w4.w4_route(x[:, :64], 4, stream=stream)
+        return out
+
+    want = calls(w4.Workspace(), None)
+    ws, side = w4.Workspace(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    sizes = [256]
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)  # some 10 ms
+    got, grow = [], ws.get_scratch
+
+    def watch(nbytes, stream=None):
+        sizes.append(ws.scratch.numel())
+        return grow(nbytes, stream)
+
+    ws.get_scratch = watch
+    got = calls(ws, side)
+    assert len(sizes) > 2  # it has grown, more than once
+    junk = crowd(*sizes)
+    side.synchronize()
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+    del junk
+
+
+def test_workspace_grows_after_a_capture():
+    """A graph keeps the buffer that it was captured with."""
+    m = Experts(256, 128, 8, 128, "bf16")
+    x, (ids, w) = randn(1, 40, 256, dtype="bf16"), choices(3, 40, 8, 2)
+    ws = w4.Workspace()
+    want = m.run(x, ids, w, workspace=ws)
+    size = ws.scratch.numel()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = m.run(x, ids, w, workspace=ws)
+    m.run(randn(2, 600, 256, dtype="bf16"), *choices(4, 600, 8, 2), workspace=ws)
+    assert ws.scratch.numel() > size
+    torch.cuda.synchronize()
+    junk = crowd(size)
+    got.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
+    assert all((j == 0x7F).all() for j in junk)  # nothing that is another's was written

@@ -147,6 +147,17 @@ def _dev(t: torch.Tensor, name: str) -> ctypes.c_void_p:
     return ctypes.c_void_p(t.data_ptr())
 
 
+def _empty(shape, dtype, device, stream) -> torch.Tensor:
+    """What a call makes for its caller, in the memory of the stream that the call runs on: a block that another stream is not
+    done with would be written too early. The caller's stream may use it too."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream(device))
+    return t
+
+
 def _ngroups(K: int, g: int) -> int:
     return -(-K // g)
 
@@ -161,9 +172,9 @@ def w4_pack(W: torch.Tensor, g: int, stream=None, symmetric: bool = False):
         raise ValueError("W must be a 2-D fp16 or bf16 tensor")
     N, K = W.shape
     G = _ngroups(K, g) if g > 0 else 1
-    qw = torch.empty((N, -(-K // 8)), dtype=torch.int32, device=W.device)
-    scales = torch.empty((N, G), dtype=W.dtype, device=W.device)
-    zeros = torch.empty((N, -(-G // 8)), dtype=torch.int32, device=W.device)
+    qw = _empty((N, -(-K // 8)), torch.int32, W.device, stream)
+    scales = _empty((N, G), W.dtype, W.device, stream)
+    zeros = _empty((N, -(-G // 8)), torch.int32, W.device, stream)
     _check(load().w4_pack_ex(_dev(W, "W"), N, K, g, _DTYPES[W.dtype], int(bool(symmetric)), _dev(qw, "qw"),
                              _dev(scales, "scales"), _dev(zeros, "zeros"), _stream(stream)), "w4_pack")
     return qw, scales, zeros
@@ -180,7 +191,7 @@ def w4_repack(qw: torch.Tensor, scales: torch.Tensor, zeros: torch.Tensor, N: in
     if nbytes == 0:
         raise W4Error(1, "w4_repack")
     if out is None:
-        out = torch.empty(nbytes, dtype=torch.uint8, device=qw.device)
+        out = _empty(nbytes, torch.uint8, qw.device, stream)
     elif out.numel() * out.element_size() < nbytes:
         raise ValueError("out is too small")
     _check(load().w4_repack(_dev(qw, "qw"), _dev(scales, "scales"), _dev(zeros, "zeros"), N, K, g,
@@ -208,24 +219,41 @@ def w4a16_gemm_plan(M: int, N: int, K: int, g: int):
 
 
 class Workspace:
-    """A zero-filled device workspace that grows on demand (reuse it across calls on one stream). ``scratch`` is a second
-    buffer, for the calls that leave arbitrary bytes behind (w4a16_experts, w4_lora_add): the GEMMs' counters in the
-    first have to stay zero."""
+    """A zero-filled device workspace that grows on demand (reuse it across calls on one stream: a stream other than the one it
+    was made on waits for that one first, as for any tensor). ``scratch`` is a second buffer, for the calls that leave
+    arbitrary bytes behind (w4a16_experts, w4_lora_add): the GEMMs' counters in the first have to stay zero.
+
+    A buffer that was outgrown is kept: calls that are still running, or graphs that were captured, use it. Each buffer is
+    at least twice the one before, so all of them together are less than twice the last."""
 
     def __init__(self, device=None):
         self.device = torch.device(device or "cuda")
         self.buf = torch.zeros(256, dtype=torch.uint8, device=self.device)
         self.scratch = torch.zeros(256, dtype=torch.uint8, device=self.device)
+        self._outgrown = []
 
-    def get(self, nbytes: int) -> torch.Tensor:
+    def get(self, nbytes: int, stream=None) -> torch.Tensor:
+        """The first buffer, of ``nbytes`` at least, for a call on ``stream`` (None: the current one)."""
         if self.buf.numel() < nbytes:
-            self.buf = torch.zeros(max(nbytes, 2 * self.buf.numel()), dtype=torch.uint8, device=self.device)
+            self._outgrown.append(self.buf)
+            with torch.cuda.stream(stream):
+                self.buf = torch.zeros(max(nbytes, 2 * self.buf.numel()), dtype=torch.uint8, device=self.device)
         return self.buf
 
-    def get_scratch(self, nbytes: int) -> torch.Tensor:
+    def get_scratch(self, nbytes: int, stream=None) -> torch.Tensor:
+        """The second buffer, of ``nbytes`` at least, for a call on ``stream`` (None: the current one)."""
         if self.scratch.numel() < nbytes:
-            self.scratch = torch.empty(max(nbytes, 2 * self.scratch.numel()), dtype=torch.uint8, device=self.device)
+            self._outgrown.append(self.scratch)
+            with torch.cuda.stream(stream):
+                self.scratch = torch.empty(max(nbytes, 2 * self.scratch.numel()), dtype=torch.uint8, device=self.device)
         return self.scratch
+
+
+def _gemm_workspace(workspace, device, nbytes: int, stream) -> torch.Tensor:
+    if workspace is None:
+        with torch.cuda.stream(stream):
+            workspace = Workspace(device)
+    return workspace.get(nbytes, stream) if isinstance(workspace, Workspace) else workspace
 
 
 def _gemm_common(x, packed, N, K, g, y, workspace, block_n, ctas, schedule, stream):
@@ -233,15 +261,13 @@ def _gemm_common(x, packed, N, K, g, y, workspace, block_n, ctas, schedule, stre
         raise ValueError("x must be fp16 [M, K]")
     M = x.shape[0]
     if y is None:
-        y = torch.empty((M, N), dtype=torch.float16, device=x.device)
+        y = _empty((M, N), torch.float16, x.device, stream)
     elif y.dtype != torch.float16 or tuple(y.shape) != (M, N):
         raise ValueError("y must be fp16 [M, N]")
     need = w4a16_workspace_bytes_ex(M, N, K, g, block_n, ctas, schedule)
     if need == 0:
         raise W4Error(1, "w4a16_workspace_bytes")
-    if workspace is None:
-        workspace = Workspace(x.device)
-    ws = workspace.get(need) if isinstance(workspace, Workspace) else workspace
+    ws = _gemm_workspace(workspace, x.device, need, stream)
     nbytes = ws.numel() * ws.element_size()
     lib = load()
     if block_n == 0 and ctas == 0 and schedule == 0:
@@ -275,16 +301,14 @@ def w4a16_gemm_opts(x: torch.Tensor, packed: torch.Tensor, N: int, K: int, g: in
         raise ValueError("x must be fp16 or bf16 [M, K]")
     M = x.shape[0]
     if y is None:
-        y = torch.empty((M, N), dtype=x.dtype, device=x.device)
+        y = _empty((M, N), x.dtype, x.device, stream)
     elif y.dtype != x.dtype or tuple(y.shape) != (M, N):
         raise ValueError("y must be [M, N] of x's dtype")
     o = Options(kernel, block_n, ctas, schedule, cluster, flags, wait_limit_cycles, _DTYPES[x.dtype], 0)
     need = w4a16_workspace_bytes_opts(M, N, K, g, o)
     if need == 0:
         raise W4Error(1, "w4a16_workspace_bytes_opts")
-    if workspace is None:
-        workspace = Workspace(x.device)
-    ws = workspace.get(need) if isinstance(workspace, Workspace) else workspace
+    ws = _gemm_workspace(workspace, x.device, need, stream)
     nbytes = ws.numel() * ws.element_size()
     rc = load().w4a16_gemm_opts(_dev(x, "x"), _dev(packed, "packed"), M, N, K, g, _dev(y, "y"),
                                 _dev(ws, "workspace"), nbytes, ctypes.byref(o), _stream(stream))
@@ -309,7 +333,7 @@ def w4_last_device_error(workspace, stream=None) -> int:
 
 # ----------------------------------------------------------------------------- groups and epilogues
 
-def _problem_array(problems, M, dtype, device):
+def _problem_array(problems, M, dtype, device, stream=None):
     """(ctypes array of Problem, outputs per problem, tensors to keep alive)."""
     arr = (Problem * len(problems))()
     outs, keep = [], []
@@ -322,7 +346,7 @@ def _problem_array(problems, M, dtype, device):
             epi.kind = EPI_SILU_MUL
             y = pr.get("y")
             if y is None:
-                y = torch.empty((M, N // 2), dtype=dtype, device=device)
+                y = _empty((M, N // 2), dtype, device, stream)
             elif y.dtype != dtype or tuple(y.shape) != (M, N // 2):
                 raise ValueError(f"problem {i}: y must be [{M}, {N // 2}]")
             out = y
@@ -339,14 +363,14 @@ def _problem_array(problems, M, dtype, device):
                 if any(t.dtype != dtype or tuple(t.shape) != sh for t, sh in zip((q, k, v), shapes)):
                     raise ValueError(f"problem {i}: out must be q, k, v of shapes {shapes}")
             else:
-                q, k, v = (torch.empty(sh, dtype=dtype, device=device) for sh in shapes)
+                q, k, v = (_empty(sh, dtype, device, stream) for sh in shapes)
             epi.k_dev, epi.v_dev = k.data_ptr(), v.data_ptr()
             y, out = q, (q, k, v)
             keep += [k, v]
         else:
             y = pr.get("y")
             if y is None:
-                y = torch.empty((M, N), dtype=dtype, device=device)
+                y = _empty((M, N), dtype, device, stream)
             elif y.dtype != dtype or tuple(y.shape) != (M, N):
                 raise ValueError(f"problem {i}: y must be [{M}, {N}]")
             out = y
@@ -377,14 +401,12 @@ def w4a16_gemm_grouped(problems, g: int, *, kernel: int = 0, block_n: int = 0, c
     if x0.dtype not in _DTYPES:
         raise ValueError("x must be fp16 or bf16")
     M = x0.shape[0]
-    arr, outs, keep = _problem_array(problems, M, x0.dtype, x0.device)
+    arr, outs, keep = _problem_array(problems, M, x0.dtype, x0.device, stream)
     o = Options(kernel, block_n, ctas, schedule, cluster, flags, wait_limit_cycles, _DTYPES[x0.dtype], 0)
     need = int(load().w4a16_grouped_workspace_bytes(arr, len(problems), M, g, ctypes.byref(o)))
     if need == 0:
         raise W4Error(1, "w4a16_grouped_workspace_bytes")
-    if workspace is None:
-        workspace = Workspace(x0.device)
-    ws = workspace.get(need) if isinstance(workspace, Workspace) else workspace
+    ws = _gemm_workspace(workspace, x0.device, need, stream)
     nbytes = ws.numel() * ws.element_size()
     rc = load().w4a16_gemm_grouped(arr, len(problems), M, g, _dev(ws, "workspace"), nbytes, ctypes.byref(o),
                                    _stream(stream))
@@ -466,30 +488,23 @@ def _like(t: torch.Tensor, name: str, dtype, shape, device: int) -> int:
     return t.data_ptr()
 
 
-def _handle(stream, device: int, *made) -> int:
-    """The stream's handle. What a call made for itself (``made``) is kept until a stream given by the caller is done
-    with it."""
-    if stream is None:
-        return torch._C._cuda_getCurrentRawStream(device)
-    for t in made:
-        if t is not None:
-            t.record_stream(stream)
-    return stream.cuda_stream
+def _handle(stream, device: int) -> int:
+    return torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
 
 
-def _run_with(call, args, workspace, sized, device: int, stream, made, what: str):
+def _run_with(call, args, workspace, sized, device: int, stream, what: str):
     """call(args, workspace, its bytes, stream). A Workspace grows, and without one a buffer is made, by sized()."""
-    own = None
     if workspace is None:
-        ws = own = torch.empty(max(sized(), 1), dtype=torch.uint8, device=f"cuda:{device}")
+        with torch.cuda.stream(stream):
+            ws = torch.empty(max(sized(), 1), dtype=torch.uint8, device=f"cuda:{device}")
     else:
         ws = workspace.scratch if isinstance(workspace, Workspace) else workspace
         if ws.get_device() != device or not ws.is_contiguous():
             raise ValueError(f"workspace must be contiguous on cuda:{device}")
-    handle = _handle(stream, device, made, own)
+    handle = _handle(stream, device)
     rc = call(args, ws.data_ptr(), ws.nbytes, handle)
     if rc == 4 and isinstance(workspace, Workspace):
-        ws = workspace.get_scratch(sized())
+        ws = workspace.get_scratch(sized(), stream)
         rc = call(args, ws.data_ptr(), ws.nbytes, handle)
     if rc != 0:
         raise W4Error(rc, what)
@@ -511,21 +526,19 @@ def w4_route(logits: torch.Tensor, k: int, *, sigmoid: bool = False, bias: torch
     ld = _rows(logits, "logits")
     b = None if bias is None else _like(bias, "bias", torch.float32, (E,), device)
     shape = (T, max(k, 0))
-    made_w = made_i = None
     if weights is None:
-        weights = made_w = torch.empty(shape, dtype=torch.float32, device=logits.device)
+        weights = _empty(shape, torch.float32, logits.device, stream)
         w_at = weights.data_ptr()
     else:
         w_at = _like(weights, "weights", torch.float32, shape, device)
     if ids is None:
-        ids = made_i = torch.empty(shape, dtype=torch.int32, device=logits.device)
+        ids = _empty(shape, torch.int32, logits.device, stream)
         i_at = ids.data_ptr()
     else:
         i_at = _like(ids, "ids", torch.int32, shape, device)
     o = _ROUTE_OPTIONS.pack(k, sigmoid, groups, groups if top_groups is None else top_groups, group_top, renormalize, scale,
                             dt)
-    rc = (_lib or load()).w4_route(logits.data_ptr(), T, E, ld, b, o, w_at, i_at,
-                                   _handle(stream, device, made_w, made_i))
+    rc = (_lib or load()).w4_route(logits.data_ptr(), T, E, ld, b, o, w_at, i_at, _handle(stream, device))
     if rc != 0:
         raise W4Error(rc, "w4_route")
     return weights, ids
@@ -556,16 +569,16 @@ def w4a16_experts(x: torch.Tensor, gate_up: torch.Tensor, down: torch.Tensor, id
         raise W4Error(1, "w4a16_experts")
     if K % 8 or inter % 8:
         raise W4Error(2, "w4a16_experts")
-    made = None
-    if y is None:
-        y = made = torch.empty_like(x)
+    own = y is None
+    if own:
+        y = _empty(x.shape, x.dtype, x.device, stream)
     a = _EXPERTS_ARGS.pack(
         x.data_ptr(), _like(gate_up, "gate_up", torch.uint8, (E, gu_bytes), device),
         _like(down, "down", torch.uint8, (E, dn_bytes), device), _like(ids, "ids", torch.int32, (T, k), device),
         _like(weights, "weights", torch.float32, (T, k), device),
-        y.data_ptr() if made is not None else _like(y, "y", x.dtype, (T, K), device), T, K, inter, E, k, g, dt)
+        y.data_ptr() if own else _like(y, "y", x.dtype, (T, K), device), T, K, inter, E, k, g, dt)
     _run_with(lib.w4a16_experts, a, workspace, lambda: w4a16_experts_workspace_bytes(T, K, inter, E, k, g), device, stream,
-              made, "w4a16_experts")
+              "w4a16_experts")
     return y
 
 
@@ -591,9 +604,8 @@ def w4_lora_add(base: torch.Tensor | None, x: torch.Tensor, A: torch.Tensor, B: 
     N = B.shape[1]
     device = x.get_device()
     shape = (T, N)
-    made = None
     if y is None:
-        y = made = torch.empty(shape, dtype=dtype, device=x.device)
+        y = _empty(shape, dtype, x.device, stream)
     elif y.dtype is not dtype or y.shape != shape or y.get_device() != device:
         raise ValueError(f"y must be {dtype} [{T}, {N}] on cuda:{device}")
     if base is None:
@@ -609,5 +621,5 @@ def w4_lora_add(base: torch.Tensor | None, x: torch.Tensor, A: torch.Tensor, B: 
         0 if ranks is None else _like(ranks, "ranks", torch.int32, (R,), device),
         base_at, y.data_ptr(), T, K, N, _rows(x, "x"), ldbase, _rows(y, "y"), R, rank, dt, 0)
     _run_with((_lib or load()).w4_lora_add, a, workspace, lambda: w4_lora_workspace_bytes(T, K, N, R, rank), device, stream,
-              made, "w4_lora_add")
+              "w4_lora_add")
     return y
