@@ -159,3 +159,15 @@ def test_workspace_grows_after_a_capture():
     torch.cuda.synchronize()
     assert torch.equal(got, want)
     assert all((j == 0x7F).all() for j in junk)  # nothing that is another's was written
+
+
+def test_another_current_device_is_refused(monkeypatch):
+    m = Experts(64, 64, 3, 64, "f16")
+    x, (ids, w) = randn(1, 4, 64), choices(1, 4, 3, 2)
+    A, B, adapter = randn(2, 2, 8, 64), randn(3, 2, 32, 8), torch.zeros(4, dtype=torch.int32, device="cuda")
+    ws = w4.Workspace()
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 1)
+    for call in (lambda **kw: w4.w4_route(x, 2, **kw), lambda **kw: m.run(x, ids, w, **kw), lambda **kw: m.run(x, ids, w, workspace=ws, **kw),
+                 lambda **kw: w4.w4_lora_add(None, x, A, B, adapter, **kw)):
+        with pytest.raises(ValueError):
+            call()

@@ -61,3 +61,27 @@ def test_what_a_call_makes_is_made_on_its_stream(monkeypatch):
     assert t.shape == (2, 3) and made == ["side"] and recorded == ["current"]
     w4._empty((2, 3), torch.float16, "cpu", None)
     assert made == ["side", None] and recorded == ["current"]
+
+
+def test_tensors_and_streams_of_another_device_are_refused(monkeypatch):
+    """The library launches on the current device: handles of another one's streams or memory would run there."""
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda device: 7, raising=False)
+
+    class Stream:
+        def __init__(self, index):
+            self.device, self.cuda_stream = torch.device("cuda", index), 8 + index
+
+    assert w4._handle(None, 0) == 7 and w4._handle(Stream(0), 0) == 8
+    for stream, device in ((None, 1), (Stream(1), 1), (Stream(1), 0)):
+        with pytest.raises(ValueError):
+            w4._handle(stream, device)
+
+
+def test_a_workspace_stays_on_its_device(monkeypatch):
+    made = []
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 3)
+    monkeypatch.setattr(torch, "zeros", lambda *a, device=None, **kw: made.append(device))
+    assert w4.Workspace().device == w4.Workspace("cuda").device == torch.device("cuda", 3)
+    assert w4.Workspace("cuda:1").device == torch.device("cuda", 1)
+    assert {str(d) for d in made} == {"cuda:3", "cuda:1"}

@@ -227,7 +227,10 @@ class Workspace:
     at least twice the one before, so all of them together are less than twice the last."""
 
     def __init__(self, device=None):
-        self.device = torch.device(device or "cuda")
+        device = torch.device(device or "cuda")
+        if device.type == "cuda" and device.index is None:  # it grows there, whichever device is then the current one
+            device = torch.device("cuda", torch.cuda.current_device())
+        self.device = device
         self.buf = torch.zeros(256, dtype=torch.uint8, device=self.device)
         self.scratch = torch.zeros(256, dtype=torch.uint8, device=self.device)
         self._outgrown = []
@@ -489,11 +492,20 @@ def _like(t: torch.Tensor, name: str, dtype, shape, device: int) -> int:
 
 
 def _handle(stream, device: int) -> int:
-    return torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
+    """The stream's handle. The library launches on the current device, so the tensors and the stream have to be its own."""
+    current = torch._C._cuda_getDevice()
+    if device != current:
+        raise ValueError(f"the tensors are on cuda:{device}, the current device is cuda:{current}")
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device)
+    if stream.device.index != device:
+        raise ValueError(f"the tensors are on cuda:{device}, the stream is of {stream.device}")
+    return stream.cuda_stream
 
 
 def _run_with(call, args, workspace, sized, device: int, stream, what: str):
     """call(args, workspace, its bytes, stream). A Workspace grows, and without one a buffer is made, by sized()."""
+    handle = _handle(stream, device)
     if workspace is None:
         with torch.cuda.stream(stream):
             ws = torch.empty(max(sized(), 1), dtype=torch.uint8, device=f"cuda:{device}")
@@ -501,7 +513,6 @@ def _run_with(call, args, workspace, sized, device: int, stream, what: str):
         ws = workspace.scratch if isinstance(workspace, Workspace) else workspace
         if ws.get_device() != device or not ws.is_contiguous():
             raise ValueError(f"workspace must be contiguous on cuda:{device}")
-    handle = _handle(stream, device)
     rc = call(args, ws.data_ptr(), ws.nbytes, handle)
     if rc == 4 and isinstance(workspace, Workspace):
         ws = workspace.get_scratch(sized(), stream)
