@@ -509,7 +509,8 @@ W4_API size_t w4a16_experts_workspace_bytes(int64_t T, int64_t K, int64_t I, int
  * that hold about twice the type's bits (fp16: after division of the row by a
  * power of two, so that it cannot overflow); sums in fp32, y rounded once.
  * The workspace is at least w4_lora_workspace_bytes(...) bytes, 256-byte
- * aligned.
+ * aligned. Its first word is left as it is, so that w4a16_experts' error word
+ * outlasts a w4_lora_add on the same workspace.
  */
 typedef struct {
     const void *x_dev;

@@ -171,3 +171,28 @@ def test_another_current_device_is_refused(monkeypatch):
                  lambda **kw: w4.w4_lora_add(None, x, A, B, adapter, **kw)):
         with pytest.raises(ValueError):
             call()
+
+
+# ---------------------------------------------------------------------------------------------------- error words
+
+def test_a_timeout_of_the_experts_is_reported_by_the_workspace():
+    m = Experts(256, 128, 4, 128, "bf16")
+    x = randn(1, 64, 256, dtype="bf16")
+    ids, w = choices(1, 64, 4, 2)
+    lora = (None, x, randn(2, 3, 8, 256, dtype="bf16"), randn(3, 3, 64, 8, dtype="bf16"), torch.zeros(64, dtype=torch.int32, device="cuda"))
+    ws = w4.Workspace()
+    w4.w4_lora_add(*lora, workspace=ws)  # grows the scratch
+    assert w4.w4_last_device_error(ws) == 0
+    assert w4.w4_last_device_error(ws.scratch) == 0
+    m.run(x, ids, w, workspace=ws)
+    assert w4.w4_last_device_error(ws) == 0
+    ws.scratch[:4] = torch.tensor([1, 0, 0, 0], dtype=torch.uint8, device="cuda")  # as a wait that gave up leaves it
+    w4.w4_lora_add(*lora, workspace=ws)
+    assert w4.w4_last_device_error(ws) == 6
+    assert w4.w4_last_device_error(ws) == 0
+    ws.scratch[:4] = torch.tensor([1, 0, 0, 0], dtype=torch.uint8, device="cuda")
+    ws.get_scratch(4 * ws.scratch.numel())
+    assert w4.w4_last_device_error(ws) == 6
+    assert w4.w4_last_device_error(ws) == 0
+    m.run(x, ids, w, workspace=ws)
+    assert w4.w4_last_device_error(ws) == 0

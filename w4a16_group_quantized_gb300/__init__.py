@@ -246,9 +246,11 @@ class Workspace:
     def get_scratch(self, nbytes: int, stream=None) -> torch.Tensor:
         """The second buffer, of ``nbytes`` at least, for a call on ``stream`` (None: the current one)."""
         if self.scratch.numel() < nbytes:
-            self._outgrown.append(self.scratch)
+            old = self.scratch
+            self._outgrown.append(old)
             with torch.cuda.stream(stream):
-                self.scratch = torch.empty(max(nbytes, 2 * self.scratch.numel()), dtype=torch.uint8, device=self.device)
+                self.scratch = torch.empty(max(nbytes, 2 * old.numel()), dtype=torch.uint8, device=self.device)
+                self.scratch[:256] = old[:256]  # the error word
         return self.scratch
 
 
@@ -328,10 +330,11 @@ def w4a16_gemm_ex(x, packed, N, K, g, block_n: int = 0, ctas: int = 0, schedule:
 
 
 def w4_last_device_error(workspace, stream=None) -> int:
-    """Reads and clears the workspace's device error word (synchronises the stream). After
-    W4_ERR_TIMEOUT the workspace's tile counters are undefined too: zero it before reuse."""
-    ws = workspace.buf if isinstance(workspace, Workspace) else workspace
-    return int(load().w4_last_device_error(_dev(ws, "workspace"), _stream(stream)))
+    """Reads and clears the workspace's device error word, or a Workspace's two, of the GEMMs and of w4a16_experts (synchronises
+    the stream). After W4_ERR_TIMEOUT from a GEMM the workspace's tile counters are undefined too: zero it before reuse."""
+    buffers = (workspace.buf, workspace.scratch) if isinstance(workspace, Workspace) else (workspace,)
+    found = [int(load().w4_last_device_error(_dev(ws, "workspace"), _stream(stream))) for ws in buffers]
+    return next((rc for rc in found if rc), 0)
 
 
 # ----------------------------------------------------------------------------- groups and epilogues
@@ -565,7 +568,8 @@ def w4a16_experts(x: torch.Tensor, gate_up: torch.Tensor, down: torch.Tensor, id
 
     x [T, K] fp16 or bf16; gate_up uint8 [E, w4_repacked_bytes(2 * inter, K, g)], each expert's packed rows
     alternating gate, up (see interleave_gate_up); down uint8 [E, w4_repacked_bytes(K, inter, g)]; ids int32 and
-    weights fp32 [T, k] as w4_route gives them (an id outside [0, E) is a dropped choice)."""
+    weights fp32 [T, k] as w4_route gives them (an id outside [0, E) is a dropped choice). A wait that gave up inside a kernel
+    (y is then undefined) can be asked for with w4_last_device_error(workspace), so only where one is given."""
     dt = _DTYPES.get(x.dtype)
     if dt is None or x.dim() != 2 or not x.is_cuda or not x.is_contiguous():
         raise ValueError("x must be a contiguous fp16 or bf16 CUDA tensor [T, K]")

@@ -560,11 +560,11 @@ __global__ void __launch_bounds__(32 * kWarps, Expand<KB, false>::kBlocks)
   copies_wait<0>();
 }
 
-// The launch's shape, and the workspace's: [v][perm][tiles][ntiles].
+// The launch's shape, and the workspace's: [error block, left as it is, with ntiles in its second word][v][perm][tiles].
 struct LoraPlan {
   bool direct;
   int max_tiles, splits;
-  size_t perm, tiles, ntiles, bytes;
+  size_t v, perm, tiles, bytes;
 };
 
 LoraPlan lora_plan(int64_t T, int64_t N, int64_t K, int adapters, int rank, int num_sms) {
@@ -578,10 +578,10 @@ LoraPlan lora_plan(int64_t T, int64_t N, int64_t K, int adapters, int rank, int 
   const int64_t splits = want < turns ? want : turns;
   p.splits = static_cast<int>(splits < 1 ? 1 : splits < 8 ? splits : 8);
   auto up = [](size_t v) { return (v + 255) / 256 * 256; };
-  p.perm = up(static_cast<size_t>(T) * rank * 4);
+  p.v = 256;
+  p.perm = p.v + up(static_cast<size_t>(T) * rank * 4);
   p.tiles = p.perm + (p.direct ? 0 : up(static_cast<size_t>(T) * 4));
-  p.ntiles = p.tiles + (p.direct ? 0 : up(static_cast<size_t>(p.max_tiles) * sizeof(RowTile)));
-  p.bytes = p.ntiles + 256;
+  p.bytes = p.tiles + (p.direct ? 0 : up(static_cast<size_t>(p.max_tiles) * sizeof(RowTile)));
   return p;
 }
 
@@ -662,11 +662,11 @@ cudaError_t launch_lora(const LoraArgs &a, void *workspace, int num_sms, cudaStr
   if (!p.direct) {
     ts.plan.perm = reinterpret_cast<int32_t *>(ws + p.perm);
     ts.plan.tiles = reinterpret_cast<RowTile *>(ws + p.tiles);
-    ts.plan.ntiles = reinterpret_cast<int32_t *>(ws + p.ntiles);
+    ts.plan.ntiles = reinterpret_cast<int32_t *>(ws + 4);
     const cudaError_t e = launch_row_plan(a.adapter, a.T, a.adapters, kTileRows, true, ts.plan, stream);
     if (e != cudaSuccess) return e;
   }
-  float *v = reinterpret_cast<float *>(ws);
+  float *v = reinterpret_cast<float *>(ws + p.v);
   return a.dtype == kDtypeBf16 ? launch_dt<kDtypeBf16>(ts, a, p, v, num_sms, stream)
                                : launch_dt<kDtypeF16>(ts, a, p, v, num_sms, stream);
 }
