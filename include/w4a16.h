@@ -480,6 +480,13 @@ typedef struct {
     int32_t dtype;
 } w4a16_experts_args;
 W4_API int w4a16_experts(const w4a16_experts_args *args, void *workspace_dev, size_t workspace_bytes, void *stream);
+/*
+ * w4a16_experts with options (NULL: none). Of w4a16_options it takes wait_limit_cycles and, in tests only,
+ * W4_FLAG_TEST_TIMEOUT: on the tensor-memory kernel (many rows an expert), the one with waits, a barrier then expects an
+ * arrival more than will ever come. Its other fields have to be 0.
+ */
+W4_API int w4a16_experts_opts(const w4a16_experts_args *args, void *workspace_dev, size_t workspace_bytes,
+                              const w4a16_options *opts, void *stream);
 /* 0 for sizes that w4a16_experts refuses. */
 W4_API size_t w4a16_experts_workspace_bytes(int64_t T, int64_t K, int64_t I, int32_t experts, int32_t k, int32_t g);
 

@@ -196,3 +196,17 @@ def test_a_timeout_of_the_experts_is_reported_by_the_workspace():
     assert w4.w4_last_device_error(ws) == 0
     m.run(x, ids, w, workspace=ws)
     assert w4.w4_last_device_error(ws) == 0
+
+
+@pytest.mark.parametrize("T,g", [(64, 128), (400, 128), (64, 64), (400, 64), (64, 32)])
+def test_experts_wait_runs_out_then_next_call_is_right(T, g):
+    """A barrier that expects an arrival too many, with a short limit: the kernels come back, say so, and leave nothing behind."""
+    m = Experts(256, 136, 4, g, "bf16")
+    x, (ids, w) = randn(1, T, 256, dtype="bf16"), choices(1, T, 4, 2)
+    for ws in (w4.Workspace(), torch.zeros(w4.w4a16_experts_workspace_bytes(T, 256, 136, 4, 2, g), dtype=torch.uint8, device="cuda")):
+        m.run(x, ids, w, workspace=ws, flags=w4.FLAG_TEST_TIMEOUT, wait_limit_cycles=2_000_000)
+        torch.cuda.synchronize()
+        assert w4.w4_last_device_error(ws) == 6
+        m.check(x, ids, w, workspace=ws)
+        assert w4.w4_last_device_error(ws) == 0
+    m.check(x, ids, w, wait_limit_cycles=1 << 40)

@@ -1,4 +1,4 @@
-"""The binding's Workspace and what its calls make for themselves, without a GPU."""
+"""The binding's Workspace, what its calls make for themselves and what they refuse, without a GPU."""
 from __future__ import annotations
 
 import weakref
@@ -7,6 +7,7 @@ import pytest
 import torch
 
 import w4a16_group_quantized_gb300 as w4
+from w4a16_group_quantized_gb300 import build as w4build
 
 
 @pytest.mark.parametrize("name", ["get", "get_scratch"])
@@ -85,3 +86,19 @@ def test_a_workspace_stays_on_its_device(monkeypatch):
     assert w4.Workspace().device == w4.Workspace("cuda").device == torch.device("cuda", 3)
     assert w4.Workspace("cuda:1").device == torch.device("cuda", 1)
     assert {str(d) for d in made} == {"cuda:3", "cuda:1"}
+
+
+def test_experts_options_are_checked():
+    w4build.build()
+    lib = w4.load()
+    at = 0x10000  # an aligned address that no refused call reads
+    args = w4._EXPERTS_ARGS.pack(at, at, at, at, at, at, 0, 64, 64, 4, 2, 64, 1)  # no rows: nothing is enqueued
+
+    def status(**kw):
+        return lib.w4a16_experts_opts(args, at, 1 << 40, w4.ctypes.byref(w4.Options(**kw)), None)
+
+    assert lib.w4a16_experts_opts(args, at, 1 << 40, None, None) == 0
+    assert status() == status(flags=w4.FLAG_TEST_TIMEOUT, wait_limit_cycles=5) == 0
+    for kw in (dict(flags=w4.FLAG_WEIGHTS_STATIC), dict(flags=8), dict(kernel=1), dict(block_n=64), dict(ctas=1), dict(schedule=1),
+               dict(cluster=2), dict(dtype=1), dict(reserved=1)):
+        assert status(**kw) == 1, kw

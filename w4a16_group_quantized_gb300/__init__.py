@@ -112,6 +112,7 @@ def load() -> ctypes.CDLL:
             "w4a16_grouped_workspace_bytes": ([ctypes.POINTER(Problem), I32, I64, I32, ctypes.POINTER(Options)], SZ),
             "w4_route": ([P, I64, I32, I64, P, ctypes.c_char_p, P, P, P], ctypes.c_int),
             "w4a16_experts": ([ctypes.c_char_p, P, SZ, P], ctypes.c_int),
+            "w4a16_experts_opts": ([ctypes.c_char_p, P, SZ, ctypes.POINTER(Options), P], ctypes.c_int),
             "w4a16_experts_workspace_bytes": ([I64, I64, I64, I32, I32, I32], SZ),
             "w4_lora_add": ([ctypes.c_char_p, P, SZ, P], ctypes.c_int),
             "w4_lora_workspace_bytes": ([I64, I64, I64, I32, I32], SZ),
@@ -563,13 +564,16 @@ def w4a16_experts_workspace_bytes(T: int, K: int, I: int, experts: int, k: int, 
 
 
 def w4a16_experts(x: torch.Tensor, gate_up: torch.Tensor, down: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor,
-                  inter: int, g: int, *, y: torch.Tensor | None = None, workspace=None, stream=None) -> torch.Tensor:
+                  inter: int, g: int, *, y: torch.Tensor | None = None, workspace=None, stream=None, flags: int = 0,
+                  wait_limit_cycles: int = 0) -> torch.Tensor:
     """y [T, K] with y[t] = sum_j weights[t, j] * down_e (silu(gate_e x[t]) * up_e x[t]), e = ids[t, j].
 
     x [T, K] fp16 or bf16; gate_up uint8 [E, w4_repacked_bytes(2 * inter, K, g)], each expert's packed rows
     alternating gate, up (see interleave_gate_up); down uint8 [E, w4_repacked_bytes(K, inter, g)]; ids int32 and
     weights fp32 [T, k] as w4_route gives them (an id outside [0, E) is a dropped choice). A wait that gave up inside a kernel
-    (y is then undefined) can be asked for with w4_last_device_error(workspace), so only where one is given."""
+    (y is then undefined) can be asked for with w4_last_device_error(workspace), so only where one is given.
+    ``wait_limit_cycles``: after how many clock cycles a wait gives up (0: about 1.5 s); ``flags``: FLAG_TEST_TIMEOUT,
+    in tests."""
     dt = _DTYPES.get(x.dtype)
     if dt is None or x.dim() != 2 or not x.is_cuda or not x.is_contiguous():
         raise ValueError("x must be a contiguous fp16 or bf16 CUDA tensor [T, K]")
@@ -592,7 +596,13 @@ def w4a16_experts(x: torch.Tensor, gate_up: torch.Tensor, down: torch.Tensor, id
         _like(down, "down", torch.uint8, (E, dn_bytes), device), _like(ids, "ids", torch.int32, (T, k), device),
         _like(weights, "weights", torch.float32, (T, k), device),
         y.data_ptr() if own else _like(y, "y", x.dtype, (T, K), device), T, K, inter, E, k, g, dt)
-    _run_with(lib.w4a16_experts, a, workspace, lambda: w4a16_experts_workspace_bytes(T, K, inter, E, k, g), device, stream,
+    call = lib.w4a16_experts
+    if flags or wait_limit_cycles:
+        o = ctypes.byref(Options(flags=flags, wait_limit_cycles=wait_limit_cycles))
+
+        def call(args, ws, nbytes, handle):
+            return lib.w4a16_experts_opts(args, ws, nbytes, o, handle)
+    _run_with(call, a, workspace, lambda: w4a16_experts_workspace_bytes(T, K, inter, E, k, g), device, stream,
               "w4a16_experts")
     return y
 

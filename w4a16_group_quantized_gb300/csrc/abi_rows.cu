@@ -138,7 +138,15 @@ size_t w4a16_experts_workspace_bytes(int64_t T, int64_t K, int64_t I, int32_t ex
 }
 
 int w4a16_experts(const w4a16_experts_args *a, void *workspace_dev, size_t workspace_bytes, void *stream) {
+  return w4a16_experts_opts(a, workspace_dev, workspace_bytes, nullptr, stream);
+}
+
+int w4a16_experts_opts(const w4a16_experts_args *a, void *workspace_dev, size_t workspace_bytes, const w4a16_options *opts,
+                       void *stream) {
   if (!a) return W4_ERR_INVALID_ARG;
+  if (opts && (opts->kernel || opts->block_n || opts->ctas || opts->schedule || opts->cluster || opts->dtype || opts->reserved ||
+               (opts->flags & ~W4_FLAG_TEST_TIMEOUT)))
+    return W4_ERR_INVALID_ARG;
   const int rc = check_experts_sizes(a->T, a->K, a->I, a->experts, a->k, a->g);
   if (rc != W4_OK) return rc;
   if (!type16(a->dtype)) return W4_ERR_INVALID_ARG;
@@ -165,6 +173,8 @@ int w4a16_experts(const w4a16_experts_args *a, void *workspace_dev, size_t works
   e.k = a->k;
   e.g = a->g;
   e.dtype = a->dtype;
+  e.wait_limit = opts ? opts->wait_limit_cycles : 0;
+  e.test_timeout = opts && (opts->flags & W4_FLAG_TEST_TIMEOUT) != 0;
   return status_of(w4::launch_experts(e, workspace_dev, sms, static_cast<cudaStream_t>(stream)));
 }
 

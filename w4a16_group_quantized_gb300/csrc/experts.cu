@@ -533,6 +533,8 @@ cudaError_t launch_dt(const ExpertsArgs &a, uint8_t *ws, const ExpertsPlan &plan
     p.experts = a.experts;
     p.kw = 1;
     p.gdiv = make_fastdiv(static_cast<uint32_t>(a.g));
+    p.wait_limit = a.wait_limit ? a.wait_limit : kWaitLimitCycles;
+    p.test_extra = a.test_timeout ? 1 : 0;
     return p;
   };
   const void *in = a.x;

@@ -26,6 +26,9 @@ struct Products {
   int experts;
   int kw;                // warps that share a slab's K
   FastDiv gdiv;
+  // experts_tmem.cu
+  uint64_t wait_limit;   // cycles a wait may take before the kernel gives up
+  int test_extra;        // test only: arrivals that the first barrier expects and that never come
 };
 
 // The h of sorted row pos, column j, of tile t: rounded to the type. Where that overflows, the 32-bit value goes to `wide` and the

@@ -114,6 +114,12 @@ __device__ __forceinline__ void regs_up() {
   if constexpr (ON) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R));
 }
 
+// The limit of the waits, in shared memory: as a value it took registers from the roles (333 rows of 60 experts, 257 us: 261).
+struct SharedLimit {
+  const volatile uint64_t *at;
+  __device__ __forceinline__ operator uint64_t() const { return *at; }
+};
+
 // After a wait that gave up, the barriers say no more when the copies in flight have landed, which takes some
 // microseconds: ten milliseconds pass before the CTA leaves its shared memory.
 __device__ __forceinline__ void let_copies_land() {
@@ -162,6 +168,7 @@ __global__ void __launch_bounds__(TCfg<BN, CB, SUB>::kThreads, 1)
   __shared__ __align__(8) uint64_t go_bar[S], done_bar[S], wfull_bar[W], wfree_bar[W], free_bar[2][2], drain_bar[2];
   __shared__ float scales[C::kScaleSlots][SUB][kTN];
   __shared__ uint32_t tmem_sh, abort_sh;
+  __shared__ uint64_t limit_sh;
 
   const uint32_t smem_base = (smem_u32(smem_raw) + 1023u) & ~1023u;
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
@@ -169,7 +176,7 @@ __global__ void __launch_bounds__(TCfg<BN, CB, SUB>::kThreads, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
       // the row warp, the chunk's dequant warps, and the sum warps of the accumulator's chunk before
-      mbar_init(smem_u32(&go_bar[s]), 1 + 4 + 4 * C::kSumGroups);
+      mbar_init(smem_u32(&go_bar[s]), 1 + 4 + 4 * C::kSumGroups + (s == 0 ? p.test_extra : 0));
       mbar_init(smem_u32(&done_bar[s]), 1);
     }
     for (int s = 0; s < W; ++s) {
@@ -181,6 +188,7 @@ __global__ void __launch_bounds__(TCfg<BN, CB, SUB>::kThreads, 1)
       mbar_init(smem_u32(&drain_bar[e]), 1);
     }
     abort_sh = 0;
+    limit_sh = p.wait_limit;
     fence_mbar_init();
   }
   if (warp == 0 && elect_one()) prefetch_tensormap(&in_map);
@@ -197,7 +205,7 @@ __global__ void __launch_bounds__(TCfg<BN, CB, SUB>::kThreads, 1)
   griddep_wait();  // the plan and `in` come from the grids before this one
   const int units = *p.plan.ntiles * p.slabs;  // (the host has checked that this fits)
   const int chunks = (p.KB + CB - 1) / CB;  // of a unit
-  constexpr uint64_t kLimit = kWaitLimitCycles;
+  const SharedLimit limit{&limit_sh};
   const uint32_t go0 = smem_u32(&go_bar[0]), done0 = smem_u32(&done_bar[0]);
   const uint32_t wfull0 = smem_u32(&wfull_bar[0]), wfree0 = smem_u32(&wfree_bar[0]);
   const uint32_t w_base = smem_base + S * C::kXBytes;
@@ -213,7 +221,7 @@ __global__ void __launch_bounds__(TCfg<BN, CB, SUB>::kThreads, 1)
     int wt;
     for (UnitWalk w(p, units); warp == 0 && ok && w.take(&rt, &wt);) {
       for (int q = 0; q < chunks; ++q, ++c, at.step()) {
-        if (c >= static_cast<uint32_t>(S)) ok = warp_wait(done0 + 8 * at.s, at.phase ^ 1, abort_flag, p.err, kLimit);
+        if (c >= static_cast<uint32_t>(S)) ok = warp_wait(done0 + 8 * at.s, at.phase ^ 1, abort_flag, p.err, limit);
         if (!ok) break;
         if (elect_one()) {
           const uint32_t bar = go0 + 8 * at.s;
@@ -226,7 +234,6 @@ __global__ void __launch_bounds__(TCfg<BN, CB, SUB>::kThreads, 1)
         __syncwarp();
       }
     }
-    if (!ok) let_copies_land();
   } else if (warp < 8) {
     regs_down<C::kDeal, C::kRegsIssue>();
     if (warp < 6) {
@@ -245,7 +252,7 @@ __global__ void __launch_bounds__(TCfg<BN, CB, SUB>::kThreads, 1)
         for (; q < chunks; q += 2, ++n) {
           const uint32_t slot = 2 * e + (n & 1);
           const uint32_t d = C::kDBufs * e + n % C::kDBufs;
-          ok = warp_wait(go0 + 8 * at.s, at.phase, abort_flag, p.err, kLimit);
+          ok = warp_wait(go0 + 8 * at.s, at.phase, abort_flag, p.err, limit);
           if (!ok) break;
           tc_fence_after();
           if (elect_one()) {
@@ -292,7 +299,7 @@ __global__ void __launch_bounds__(TCfg<BN, CB, SUB>::kThreads, 1)
         const uint8_t *codes = expert + static_cast<int64_t>(wt) * p.KB * kTileBytes;
         const uint8_t *meta = expert + p.meta + static_cast<int64_t>(wt) * p.G * kRecBytes;
         for (int q = 0; q < chunks; ++q, ++c, at.step()) {
-          if (c >= static_cast<uint32_t>(W)) ok = warp_wait(wfree0 + 8 * at.s, at.phase ^ 1, abort_flag, p.err, kLimit);
+          if (c >= static_cast<uint32_t>(W)) ok = warp_wait(wfree0 + 8 * at.s, at.phase ^ 1, abort_flag, p.err, limit);
           if (!ok) break;
           if (elect_one()) {
             const uint32_t to = w_base + at.s * C::kWBytes;
@@ -312,7 +319,6 @@ __global__ void __launch_bounds__(TCfg<BN, CB, SUB>::kThreads, 1)
           __syncwarp();
         }
       }
-      if (!ok) let_copies_land();
     }
   } else if (warp < 16) {
     // ------------------------------------------------------------ dequant
@@ -335,9 +341,9 @@ __global__ void __launch_bounds__(TCfg<BN, CB, SUB>::kThreads, 1)
         ++i;
       }
       if (i >= mine) break;
-      if (!warp_wait(wfull0 + 8 * at.s, at.phase, abort_flag, p.err, kLimit)) break;
+      if (!warp_wait(wfull0 + 8 * at.s, at.phase, abort_flag, p.err, limit)) break;
       const uint32_t slot = 2 * e + (n & 1);
-      if (n >= 2 && !warp_wait(free0 + 8 * slot, (n / 2 - 1) & 1, abort_flag, p.err, kLimit)) break;
+      if (n >= 2 && !warp_wait(free0 + 8 * slot, (n / 2 - 1) & 1, abort_flag, p.err, limit)) break;
       const uint32_t codes = w_base + at.s * C::kWBytes + r * 16;
       const uint32_t rec = w_base + at.s * C::kWBytes + C::kCodeBytes;
       const int nb = min(CB, p.KB - q * CB);
@@ -406,7 +412,7 @@ __global__ void __launch_bounds__(TCfg<BN, CB, SUB>::kThreads, 1)
 #pragma unroll
       for (int i = 0; i < kCols / 2; ++i) acc[i] = 0ull;
       for (int q = 0; q < chunks; ++q, ++c, at.step()) {
-        ok = warp_wait(done0 + 8 * at.s, at.phase, abort_flag, p.err, kLimit);
+        ok = warp_wait(done0 + 8 * at.s, at.phase, abort_flag, p.err, limit);
         if (!ok) break;
         tc_fence_after();
         const uint32_t buf = C::kDBufs * (c & 1) + c / 2 % C::kDBufs;
@@ -476,7 +482,9 @@ __global__ void __launch_bounds__(TCfg<BN, CB, SUB>::kThreads, 1)
   tc_fence_before();
   __syncwarp();
   cta_sync_all();
+  if (*abort_flag) let_copies_land();  // (else every copy has been waited for)
   if (warp == 8) {
+    __syncwarp();
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }

@@ -309,8 +309,9 @@ __device__ __forceinline__ uint32_t out_bits2(float lo, float hi) {
 
 // A wait whose outcome is the same for all 32 lanes: the warp then either executes the
 // following .sync.aligned tcgen05 instructions together or leaves the loop together.
+template <typename Limit>
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile uint32_t *abort_flag,
-                                          uint32_t *err, uint64_t limit) {
+                                          uint32_t *err, Limit limit) {
   const bool ok = mbar_wait(bar, parity, abort_flag, err, limit);
   return __all_sync(0xffffffffu, ok);
 }

@@ -198,6 +198,8 @@ struct ExpertsArgs {
   void *y;
   int64_t T, K, I;
   int experts, k, g, dtype;
+  uint64_t wait_limit;  // cycles a wait may take; 0: the default
+  bool test_timeout;    // test only: a barrier expects an arrival more than will come
 };
 size_t experts_workspace_bytes(int64_t T, int64_t K, int64_t I, int experts, int k, int g);
 cudaError_t launch_experts(const ExpertsArgs &a, void *workspace, int num_sms, cudaStream_t stream);

@@ -82,14 +82,16 @@ __device__ __forceinline__ bool mbar_try_wait_sleep(uint32_t bar, uint32_t parit
 // global timer costs a few hundred nanoseconds, too much for a pipeline wait.
 constexpr uint32_t kSuspendNs = 20000;
 
+// `limit` is read only once a wait did not succeed at once: a uint64_t, or what converts to one.
+template <typename Limit>
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile uint32_t *abort_flag,
-                                          uint32_t *err_word, uint64_t limit) {
+                                          uint32_t *err_word, Limit limit) {
   if (mbar_try_wait(bar, parity)) return true;
   const uint64_t t0 = clock_cycles();
   for (;;) {
     if (mbar_try_wait_sleep(bar, parity, kSuspendNs)) return true;
     if (*abort_flag) return false;
-    if (clock_cycles() - t0 > limit) {
+    if (clock_cycles() - t0 > static_cast<uint64_t>(limit)) {
       *abort_flag = 1u;
       atomicOr(err_word, kDevErrTimeout);
       return false;
