@@ -13,7 +13,7 @@ import torch
 
 import oracle
 import w4a16_group_quantized_gb300 as w4
-from test_gpu_rows import U, Experts, check_route, choices, depth, f64, randn
+from test_gpu_rows import U, Experts, check_lora, check_route, choices, depth, f64, randn
 
 pytestmark = pytest.mark.gpu
 
@@ -78,6 +78,30 @@ def test_experts_few_pairs_hold_h_in_more_bits(dtype):
             s = m.w1[e] @ x64[t]
             want[t] += w64[t, j] * (m.w2[e] @ (oracle.silu(s[0::2]) * s[1::2]))
     assert np.linalg.norm(y - want) <= 0.48 * U[dtype] * np.linalg.norm(want)
+
+
+@pytest.mark.parametrize("T,E,k,dropped", [(1400, 5, 3, 0.2), (2100, 1024, 2, 0.0), (5000, 3, 1, 0.5)])
+def test_experts_many_pairs(T, E, k, dropped):
+    """Above 4096 pairs the sort runs in a cluster: skewed, dropped and out-of-range choices, and as many experts as there can be."""
+    m = Experts(64, 32, E, 32, "bf16")
+    ids, w = choices(T, T, E, k, dropped)
+    ids[: T // 2, 0] = E - 1  # a crowded expert, more than once a token
+    ids[T // 2:: 11] = torch.tensor([E, -2**31, 2**31 - 1, 0], dtype=torch.int32)[:k].cuda()
+    m.check(randn(T, T, 64, dtype="bf16"), ids, w)
+
+
+# ------------------------------------------------------------------------------------------------------------- lora
+
+@pytest.mark.parametrize("T,R", [(4097, 1024), (9000, 3), (8193, 1), (20000, 700)])
+def test_lora_many_rows(T, R):
+    """Above 4096 rows the sort runs in a cluster: a crowded adapter, adapters without rows, rows without an adapter."""
+    g = torch.Generator().manual_seed(T)
+    adapter = torch.randint(-1, R, (T,), generator=g)
+    adapter[torch.rand(T, generator=g) < 0.4] = R - 1
+    adapter[::97] = -2**31
+    adapter[5::101] = 2**31 - 1
+    adapter[T // 2: T // 2 + 200] = R // 2  # a run
+    check_lora(T, 64, 40, R, 8, "bf16", adapter=adapter)
 
 
 # ------------------------------------------------------------------------------------------------------------ route

@@ -141,7 +141,8 @@ __global__ void __launch_bounds__(kThreads)
     const int in = (i - tile_begin[lo]) * tile;
     plan.tiles[i] = RowTile{lo, first + in, min(tile, all[lo] - in), 0};
   }
-  if (C > 1) cluster_sync_all_relaxed(); else __syncthreads();  // counts of every block have been read
+  // counts of every block have been read, and begin by every thread of this one, which the loop below changes
+  if (C > 1) cluster_sync_all(); else __syncthreads();
   for (int64_t i0 = rank * part; i0 < i_end; i0 += kThreads) {
     const int64_t i = i0 + tid;
     int bucket = -1;
