@@ -348,16 +348,23 @@ __global__ void __launch_bounds__(32 * NW, NT == 1 && NW == 8 ? 2 : 1) experts_k
 
 // in[pos] = x[token of the pair at pos]: the rows of gate/up in the sort's order, a warp a row. The tensor-memory kernel
 // reads each of them once per 128 weight rows, a box of rows a copy.
-__global__ void __launch_bounds__(256) order_kernel(const uint4 *__restrict__ x, const int32_t *__restrict__ perm, int64_t pairs,
-                                                    int pieces, int choices, uint4 *__restrict__ in) {
+__global__ void __launch_bounds__(256) order_kernel(const uint4 *x, const int32_t *perm, int64_t pairs,
+                                                    int pieces, int choices, uint4 *in) {
   griddep_launch_dependents();
   griddep_wait();
   const int64_t pos = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
   if (pos >= pairs) return;
   const uint4 *from = x + static_cast<int64_t>(perm[pos] / choices) * pieces;
   uint4 *to = in + pos * pieces;
-#pragma unroll 4
-  for (int i = threadIdx.x & 31; i < pieces; i += 32) to[i] = __ldg(from + i);
+  for (int i = threadIdx.x & 31; i < pieces; i += 128) {
+    uint4 v[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (i + 32 * j < pieces) v[j] = from[i + 32 * j];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (i + 32 * j < pieces) to[i + 32 * j] = v[j];
+  }
 }
 
 // fp16: the rows of h in the tiles that gate/up has marked. A row with values past the type's range (infinities in h, whose 32-bit
@@ -398,8 +405,8 @@ __global__ void __launch_bounds__(256)
 // rows that range_kernel has divided are multiplied by their factors.
 template <int DT, bool FACTOR>
 __global__ void __launch_bounds__(256)
-    combine_kernel(const float *__restrict__ part, const int32_t *__restrict__ inverse, const float *__restrict__ weights,
-                   const float *__restrict__ factor, int64_t T, int K, int choices, uint16_t *__restrict__ y) {
+    combine_kernel(const float *part, const int32_t *inverse, const float *weights,
+                   const float *factor, int64_t T, int K, int choices, uint16_t *y) {
   griddep_launch_dependents();
   griddep_wait();
   const int per_row = K / 8;  // K is a multiple of 8
@@ -412,8 +419,8 @@ __global__ void __launch_bounds__(256)
     const int pos = inverse[t * choices + j];
     if (pos < 0) continue;
     const float w = weights[t * choices + j];
-    float4 a = __ldg(reinterpret_cast<const float4 *>(part + static_cast<int64_t>(pos) * K + c));
-    float4 b = __ldg(reinterpret_cast<const float4 *>(part + static_cast<int64_t>(pos) * K + c + 4));
+    float4 a = *reinterpret_cast<const float4 *>(part + static_cast<int64_t>(pos) * K + c);
+    float4 b = *reinterpret_cast<const float4 *>(part + static_cast<int64_t>(pos) * K + c + 4);
     if (FACTOR) {
       const float f = factor[pos];
       a.x *= f, a.y *= f, a.z *= f, a.w *= f;

@@ -65,13 +65,13 @@ __device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
   return v;
 }
 
-__device__ __forceinline__ uint4 ldg16(const uint16_t *p) { return __ldg(reinterpret_cast<const uint4 *>(p)); }
+__device__ __forceinline__ uint4 ldg16(const uint16_t *p) { return *reinterpret_cast<const uint4 *>(p); }
 
 // v[position][rank] = A[a] . x. A block holds a tile of 16 rows and NB * 8 ranks; its warps take 32 U of K in turn and add
 // their sums in shared memory, in a fixed order. Where tiles are few the blocks of a cluster split K and add theirs through
 // distributed shared memory, each a part of the tile, in the order of their ranks.
 template <int DT, int NB, int U>
-__global__ void __launch_bounds__(32 * kWarps, 2) lora_shrink_kernel(const Tiles ts, const LoraArgs a, float *__restrict__ v) {
+__global__ void __launch_bounds__(32 * kWarps, 2) lora_shrink_kernel(const Tiles ts, const LoraArgs a, float *v) {
   griddep_launch_dependents();
   griddep_wait();
   int key, row0, rows;
@@ -220,12 +220,12 @@ struct Expand {
 
 // The tile's v to shared memory; zero past the rows and past the adapter's rank, whatever stands there.
 template <int KB, int LD>
-__device__ __forceinline__ void load_v(float (*vs)[LD], const float *__restrict__ v, int row0, int rows, int rank, int rank_all) {
+__device__ __forceinline__ void load_v(float (*vs)[LD], const float *v, int row0, int rows, int rank, int rank_all) {
   for (int i = threadIdx.x; i < 16 * KB * 4; i += 32 * kWarps) {
     const int r = i / (KB * 4), k = i % (KB * 4) * 4;
     float4 p = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     if (r < rows && k < rank) {
-      p = __ldg(reinterpret_cast<const float4 *>(v + (static_cast<int64_t>(row0) + r) * rank_all + k));
+      p = *reinterpret_cast<const float4 *>(v + (static_cast<int64_t>(row0) + r) * rank_all + k);
       if (k + 1 >= rank) p.y = 0.0f;
       if (k + 2 >= rank) p.z = 0.0f;
       if (k + 3 >= rank) p.w = 0.0f;
@@ -300,7 +300,7 @@ __device__ __forceinline__ void product(float (&acc)[4], const uint32_t (&w)[E::
 // too few bytes were in flight: this kernel took 95 us for 8192 x 10240 at rank 32 instead of 74).
 template <int DT, int KB>
 __global__ void __launch_bounds__(32 * kWarps, Expand<KB, true>::kBlocks)
-    lora_expand_wide_kernel(const Tiles ts, const LoraArgs a, const float *__restrict__ v) {
+    lora_expand_wide_kernel(const Tiles ts, const LoraArgs a, const float *v) {
   using E = Expand<KB, true>;
   extern __shared__ __align__(16) uint8_t smem[];
   float(*vs)[E::kLd] = reinterpret_cast<float(*)[E::kLd]>(smem);
@@ -427,7 +427,7 @@ __global__ void __launch_bounds__(32 * kWarps, Expand<KB, true>::kBlocks)
 // of a pair. (1501 x 4099 at rank 24: 19 us; with every value's place worked out in the loop 35.)
 template <int DT, int KB>
 __global__ void __launch_bounds__(32 * kWarps, Expand<KB, false>::kBlocks)
-    lora_expand_kernel(const Tiles ts, const LoraArgs a, const float *__restrict__ v) {
+    lora_expand_kernel(const Tiles ts, const LoraArgs a, const float *v) {
   using E = Expand<KB, false>;
   extern __shared__ __align__(16) uint8_t smem[];
   float(*vs)[E::kLd] = reinterpret_cast<float(*)[E::kLd]>(smem);

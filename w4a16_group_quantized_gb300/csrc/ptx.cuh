@@ -191,6 +191,9 @@ __device__ __forceinline__ void cluster_sync_all_relaxed() {
 // Programmatic dependent launch: wait until the grids this launch depends on have completed and
 // their memory is visible (returns at once when the launch had no programmatic dependency), and
 // let the next grid in the stream start launching (its CTAs take SMs as this grid's CTAs exit).
+// What an earlier grid may have written is read by plain loads after the wait. Read-only loads (__ldg, const
+// __restrict__) are for data that does not change while the kernel is resident, which such data does; they are not
+// coherent with its writes and the compiler may move them above the wait.
 __device__ __forceinline__ void griddep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void griddep_launch_dependents() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");

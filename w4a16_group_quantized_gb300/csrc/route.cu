@@ -43,16 +43,16 @@ __device__ __forceinline__ void load_logits(const void *p, int64_t i, float (&l)
   if constexpr (kBytes >= 16) {
 #pragma unroll
     for (int j = 0; j < kBytes / 16; ++j) {
-      const uint4 v = __ldg(reinterpret_cast<const uint4 *>(at) + j);
+      const uint4 v = reinterpret_cast<const uint4 *>(at)[j];
       w[4 * j] = v.x, w[4 * j + 1] = v.y, w[4 * j + 2] = v.z, w[4 * j + 3] = v.w;
     }
   } else if constexpr (kBytes == 8) {
-    const uint2 v = __ldg(reinterpret_cast<const uint2 *>(at));
+    const uint2 v = *reinterpret_cast<const uint2 *>(at);
     w[0] = v.x, w[1] = v.y;
   } else if constexpr (kBytes == 4) {
-    w[0] = __ldg(reinterpret_cast<const uint32_t *>(at));
+    w[0] = *reinterpret_cast<const uint32_t *>(at);
   } else {
-    w[0] = __ldg(reinterpret_cast<const uint16_t *>(at));
+    w[0] = *reinterpret_cast<const uint16_t *>(at);
   }
 #pragma unroll
   for (int j = 0; j < PER; ++j)
@@ -83,8 +83,8 @@ __device__ __forceinline__ float exp_below(float l, float top) {
 
 template <int DT, int PER>
 __global__ void __launch_bounds__(32 * kRouteWarps)
-    route_kernel(const void *logits, int64_t T, int E, int64_t ld, const float *__restrict__ bias, RouteParams o,
-                 float *__restrict__ weights, int32_t *__restrict__ ids) {
+    route_kernel(const void *logits, int64_t T, int E, int64_t ld, const float *bias, RouteParams o,
+                 float *weights, int32_t *ids) {
   griddep_launch_dependents();
   const int lane = threadIdx.x & 31;
   const int64_t row = static_cast<int64_t>(blockIdx.x) * kRouteWarps + (threadIdx.x >> 5);
@@ -121,7 +121,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps)
   for (int i = 0; i < PER; ++i) {
     const int e = lane * PER + i;
     float c = l[i];
-    if (bias && e < E && c != -INFINITY) c = (o.sigmoid ? sigmoid(c) : exp_below(c, top) / sum) + __ldg(bias + e);
+    if (bias && e < E && c != -INFINITY) c = (o.sigmoid ? sigmoid(c) : exp_below(c, top) / sum) + bias[e];
     key[i] = e < E ? key_of(isnan(c) ? -INFINITY : c) : 0u;
   }
 

@@ -66,7 +66,7 @@ __device__ __forceinline__ int32_t ld_cluster_s32(uint32_t addr) {
 
 template <int C>
 __global__ void __launch_bounds__(kThreads)
-    row_plan_kernel(const int32_t *__restrict__ keys, int64_t count, int nkeys, int tile, int keyless, RowPlan plan) {
+    row_plan_kernel(const int32_t *keys, int64_t count, int nkeys, int tile, int keyless, RowPlan plan) {
   // counts: of this block's rows; all: of every block's; begin: the next free place of a bucket for this block
   __shared__ int32_t counts[kBuckets], all[kBuckets], begin[kBuckets], tile_begin[kBuckets];
   __shared__ int2 warp_sums[kThreads / 32];
