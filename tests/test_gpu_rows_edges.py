@@ -104,6 +104,20 @@ def test_lora_many_rows(T, R):
     check_lora(T, 64, 40, R, 8, "bf16", adapter=adapter)
 
 
+def test_lora_adapters_that_are_trained_are_refused():
+    """There is no gradient, so none is dropped without a word."""
+    x, A, B = randn(1, 4, 64), randn(2, 2, 8, 64), randn(3, 2, 32, 8)
+    adapter, scaling = torch.zeros(4, dtype=torch.int32, device="cuda"), torch.ones(2, device="cuda")
+    want = w4.w4_lora_add(None, x, A, B, adapter, scaling=scaling)
+    for t in (A, B, scaling):
+        t.requires_grad_()
+        with pytest.raises(ValueError):
+            w4.w4_lora_add(None, x, A, B, adapter, scaling=scaling)
+        with torch.no_grad():
+            assert torch.equal(w4.w4_lora_add(None, x, A, B, adapter, scaling=scaling), want)
+        t.requires_grad_(False)
+
+
 # ------------------------------------------------------------------------------------------------------------ route
 
 def test_route_scores_below_the_least_sum():

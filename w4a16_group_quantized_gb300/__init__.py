@@ -619,11 +619,14 @@ def w4_lora_add(base: torch.Tensor | None, x: torch.Tensor, A: torch.Tensor, B: 
 
     x [T, K], base [T, N] (or None for zeros) and y fp16 or bf16, rows contiguous, A [R, rank, K], B [R, N, rank] of
     the same type, adapter int32 [T], scaling fp32 [R] (None: 1), ranks int32 [R] (None: rank): an adapter's own
-    rank, past which A and B are not used. ``y`` may be ``base`` (in place)."""
+    rank, past which A and B are not used. ``y`` may be ``base`` (in place). There is no gradient: A, B or scaling that
+    require one are refused where gradients are recorded."""
     dtype = x.dtype
     dt = _DTYPES.get(dtype)
     if dt is None or x.dim() != 2 or not x.is_cuda or A.dim() != 3 or B.dim() != 3:
         raise ValueError("x must be a fp16 or bf16 CUDA tensor [T, K], A [R, rank, K] and B [R, N, rank]")
+    if (A.requires_grad or B.requires_grad or (scaling is not None and scaling.requires_grad)) and torch.is_grad_enabled():
+        raise ValueError("w4_lora_add has no gradient: call it under torch.no_grad(), or with A, B and scaling detached")
     T, K = x.shape
     R, rank, _ = A.shape
     N = B.shape[1]
