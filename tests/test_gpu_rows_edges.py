@@ -104,6 +104,37 @@ def test_lora_many_rows(T, R):
     check_lora(T, 64, 40, R, 8, "bf16", adapter=adapter)
 
 
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("T,rank", [(1, 128), (9, 72), (32, 128), (33, 72), (90, 128), (90, 104)])
+def test_lora_wide_rows_of_large_rank(T, rank, dtype):
+    check_lora(T, 264, 328, 4, rank, dtype)
+    check_lora(T, 264, 328, 3, rank, dtype, ranks=[rank, 65, 3], spoil=True, in_place=True)
+
+
+@pytest.mark.parametrize("T", [5, 70])
+@pytest.mark.parametrize("ldy,ldbase,y0,base0", [(132, 131, 0, 0), (131, 132, 0, 0), (132, 132, 0, 1), (132, 132, 1, 0), (133, 144, 2, 8),
+                                                 (144, 133, 8, 1)])
+def test_lora_rows_of_unlike_parity(T, ldy, ldbase, y0, base0):
+    """y's and base's rows on unlike sides of a 4-byte boundary, or one of the two 16-byte aligned: as from contiguous rows."""
+    N = 131
+    x, A, B = randn(1, T, 128, dtype="bf16"), randn(3, 3, 16, 128, dtype="bf16"), randn(4, 3, N, 16, dtype="bf16")
+    old = randn(2, T, N, dtype="bf16")
+    adapter = (torch.arange(T) % 4 - 1).to(torch.int32).cuda()
+    want = w4.w4_lora_add(old, x, A, B, adapter)
+
+    def rows(ld, at):
+        whole = torch.full((T * ld + 16,), 7.0, dtype=torch.bfloat16, device="cuda")
+        return whole, whole[at:].as_strided((T, N), (ld, 1))
+
+    _, base = rows(ldbase, base0)
+    base.copy_(old)
+    whole, y = rows(ldy, y0)
+    w4.w4_lora_add(base, x, A, B, adapter, y=y)
+    assert torch.equal(y, want)
+    y.fill_(7.0)
+    assert (whole == 7).all()  # nothing written beside the rows
+
+
 def test_lora_adapters_that_are_trained_are_refused():
     """There is no gradient, so none is dropped without a word."""
     x, A, B = randn(1, 4, 64), randn(2, 2, 8, 64), randn(3, 2, 32, 8)
@@ -119,6 +150,27 @@ def test_lora_adapters_that_are_trained_are_refused():
 
 
 # ------------------------------------------------------------------------------------------------------------ route
+
+@pytest.mark.parametrize("sigmoid", [True, False])
+@pytest.mark.parametrize("bias", [True, False])
+@pytest.mark.parametrize("E,groups,top_groups,k", [(64, 8, 3, 6), (60, 5, 2, 5), (24, 3, 2, 4), (256, 8, 4, 8), (96, 32, 5, 8)])
+@pytest.mark.parametrize("group_top", [1, 2])
+def test_route_masks_and_groups(E, groups, top_groups, k, group_top, bias, sigmoid):
+    logits = randn(E + k, 30, E, dtype="f32", std=1.5)
+    logits[torch.rand(30, E, generator=torch.Generator().manual_seed(k)).cuda() < 0.4] = -float("inf")
+    size = E // groups
+    logits[3, : 2 * size] = -float("inf")  # groups with nothing left
+    logits[4, size:] = -float("inf")  # one group with something left
+    logits[5] = -float("inf")
+    b = randn(3, E, dtype="f32", std=0.1) if bias else None
+    check_route(logits, k, sigmoid=sigmoid, bias=b, groups=groups, top_groups=top_groups, group_top=group_top)
+
+
+def test_route_many_rows():
+    check_route(randn(1, 2051, 60, dtype="f16", std=1.5), 6, renormalize=False)
+    check_route(randn(2, 2051, 256, dtype="bf16", std=1.5), 8, sigmoid=True, bias=randn(3, 256, dtype="f32", std=0.1), groups=8,
+                top_groups=4, group_top=2)
+
 
 def test_route_scores_below_the_least_sum():
     """Chosen scores that vanish in 32 bits are divided by their sum all the same."""
