@@ -3,13 +3,16 @@
 //
 // Two kernels, v = A x and y = base + scaling B v, with v in 32 bits between them. A row's 2 r (K + N) products go with
 // its 2 K + 4 N bytes of x, base and y, and an adapter's 2 r (K + N) bytes of weights with all its rows: at ranks up to
-// 64 every case is bound by memory, or, for a few rows, by the latency of its launches. The first kernel's operands go
+// 64 memory is the floor of every case. What bounds them is, for a few rows, the latency of the launches and of each block's
+// first loads, and for many that too few bytes are in flight (8192 rows: DRAM 41% busy in the first kernel, whose warps hold
+// one chunk of loads each and wait for it, 50% in the second). The first kernel's operands go
 // from global memory straight to the registers of the tensor-core products, 16 bytes a lane: a lane's k are consecutive
 // (mma.cuh). In the second, so are the four pairs of columns n that a lane holds of four products.
 //
 // Rows stand by adapter (rows.cu), in tiles of 16 (of 32 or 64, which read an adapter's weights less, 12 - 40% slower
 // at 64 to 1024 rows an adapter); up to kDirectRows rows go without a sort, one row to a tile (rows of one adapter then
-// read its weights again, from L2: 32 rows of 32 adapters 11.8 us against 15.0, 64 rows of 4 adapters 15.6 against 12.1).
+// read its weights again, from L2). Without and with the sort, us, 4096 -> 4096 at rank 16 and 4096 -> 12288 at rank 64: 32 rows
+// of one adapter 8.6 / 10.0 and 14.5 / 15.4, of 32 adapters 8.5 / 12.1 and 14.7 / 18.2; 64 rows of one 11.0 / 10.7 and 15.3 / 15.4.
 //
 // v stands in the second product as the sum of two 16-bit values, its rounding and what that left, which keeps about
 // twice the type's bits for one more product each (they are not what bounds the kernel). For fp16 a row of v is first
@@ -37,7 +40,6 @@ struct Tiles {
   RowPlan plan;
   const int32_t *adapter;  // direct: row i is tile i
   int direct;
-  int T;
 };
 
 // The block's tile: its adapter (-1: none) and rows; false past the last.
@@ -658,7 +660,6 @@ cudaError_t launch_lora(const LoraArgs &a, void *workspace, int num_sms, cudaStr
   Tiles ts = {};
   ts.adapter = a.adapter;
   ts.direct = p.direct;
-  ts.T = static_cast<int>(a.T);
   if (!p.direct) {
     ts.plan.perm = reinterpret_cast<int32_t *>(ws + p.perm);
     ts.plan.tiles = reinterpret_cast<RowTile *>(ws + p.tiles);
