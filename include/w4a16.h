@@ -543,6 +543,235 @@ W4_API int w4_lora_add(const w4_lora_args *args, void *workspace_dev, size_t wor
 /* 0 for sizes that w4_lora_add refuses. */
 W4_API size_t w4_lora_workspace_bytes(int64_t T, int64_t K, int64_t N, int32_t adapters, int32_t rank);
 
+/* ------------------------------------------------------------------------
+ * A decoder layer's attention, between the fused q/k/v projection and the
+ * output projection: norms and rotation of the heads, a paged cache of keys
+ * and values in 8 bits, attention of a few query rows over that cache, and
+ * causal attention over packed prompts. The pages have no counterpart; q, k
+ * and v are taken as W4_EPI_QKV_SPLIT writes them (heads one after another in
+ * a row), or as slices of wider rows.
+ *
+ * The cache: k_cache and v_cache hold `pages` pages of [heads, page, head_dim]
+ * e4m3 codes each (4 bits of exponent, 3 of fraction, no infinity; codes 0x7F
+ * and 0xFF are NaN), and a scale fp32 [pages, heads] for each of the two: a
+ * value is code * scale. Row i of the table int32 [batch, max_pages] lists the
+ * pages of sequence i: position p lies in page table[i][p / page], slot
+ * p % page. An entry outside [0, pages) is no page: nothing is written there,
+ * and positions in it are seen by no query.
+ *
+ * As above: no allocation, no synchronisation, capture into CUDA graphs,
+ * no rows is no error, results are the same run to run. Outputs must not
+ * overlap inputs, but for w4_qk_norm_rope's own.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * w4_qk_norm_rope -- norm and rotation of each head of queries and keys.
+ *
+ *   u = x                                     without weights
+ *   u = x / sqrt(mean(x^2) + eps) * weight    with (over the head)
+ *   a = positions[axis(i)][t] * freqs[i],  i < rot / 2
+ *   (y_i, y_j) = (u_i cos a - u_j sin a, u_j cos a + u_i sin a),
+ *   j = i + rot / 2, or the pair (2 i, 2 i + 1) (interleaved)
+ *   y = u past the first rot values of the head
+ *
+ * axis(i): the first section0 frequencies go by the first row of positions,
+ * the next section1 by the second, and so on (one axis: section0 = rot / 2).
+ * The angle's turn is formed exactly enough for any 32-bit position; sums and
+ * products in fp32, one rounding at the end.
+ *
+ * q_dev, k_dev  [T, heads, head_dim] of dtype (fp16 or bf16), rows ldq and ldk
+ *               values apart (multiples of 8), 16-byte aligned. k_dev may be
+ *               NULL with k_heads 0.
+ * q_out_dev, k_out_dev  alike, rows ldqo and ldko apart. May be the input
+ *               itself (with the same row distance).
+ * positions_dev int32 [axes, T], freqs_dev fp32 [rot / 2] (finite); NULL both
+ *               with rot 0: no rotation.
+ * q_weight_dev, k_weight_dev  [head_dim] of dtype, 16-byte aligned, or NULL.
+ * head_dim a multiple of 8, at most 256; rot a multiple of 16, at most
+ * head_dim; the sections are not negative and their sum is rot / 2; at least a
+ * rotation or a norm.
+ */
+typedef struct {
+    const void *q_dev;
+    const void *k_dev;
+    void *q_out_dev;
+    void *k_out_dev;
+    const int32_t *positions_dev;
+    const float *freqs_dev;
+    const void *q_weight_dev;
+    const void *k_weight_dev;
+    int64_t T;
+    int64_t ldq;
+    int64_t ldk;
+    int64_t ldqo;
+    int64_t ldko;
+    int32_t q_heads;
+    int32_t k_heads;
+    int32_t head_dim;
+    int32_t rot;
+    int32_t axes;        /* 1 to 4; 0 with rot 0 */
+    int32_t section0;
+    int32_t section1;
+    int32_t section2;
+    int32_t section3;
+    int32_t interleaved; /* 0 or 1 */
+    int32_t dtype;
+    float eps;           /* not negative */
+} w4_rope_args;
+W4_API int w4_qk_norm_rope(const w4_rope_args *args, void *stream);
+
+/*
+ * w4_kv_append -- new rows of keys and values into the paged cache.
+ *
+ * Row cu[i] + j of k and v (cu[i] <= its index < cu[i + 1]) goes to position
+ * lens[i] + j of sequence i. For each page and head that gets rows, with m the
+ * largest finite |value| among them:
+ *
+ *   need = the least 2^e with m <= 448 * 2^e, -100 <= e <= 120
+ *   s = max(old scale, need) where the page holds rows of the sequence already
+ *   (lens[i] lies inside it), else need
+ *   new rows: code = e4m3(x / s), rounded to nearest even; infinities and NaN
+ *   become NaN. Where s grew, the page's earlier rows: e4m3(code * (old / s)).
+ *
+ * With powers of two a page's rows lose nothing when its scale grows, but for
+ * what falls below the type's range. Rows outside [cu[0], cu[batch]) are not
+ * used, positions past the table's end are dropped, and the rest of the cache
+ * is left as it is. A page that gets rows belongs to one sequence only.
+ *
+ * k_dev, v_dev  [T, heads, head_dim] of dtype, rows ldk and ldv apart
+ *               (multiples of 8), 16-byte aligned.
+ * k_cache_dev, v_cache_dev  16-byte aligned; k_scale_dev, v_scale_dev fp32.
+ * table_dev     int32 [batch, max_pages]; cu_dev int32 [batch + 1], ascending;
+ *               lens_dev int32 [batch]: what the cache holds before the call.
+ * head_dim a multiple of 16, at most 128; page a multiple of 16, at most 256.
+ */
+typedef struct {
+    const void *k_dev;
+    const void *v_dev;
+    void *k_cache_dev;
+    void *v_cache_dev;
+    float *k_scale_dev;
+    float *v_scale_dev;
+    const int32_t *table_dev;
+    const int32_t *cu_dev;
+    const int32_t *lens_dev;
+    int64_t T;
+    int64_t ldk;
+    int64_t ldv;
+    int64_t pages;
+    int32_t batch;
+    int32_t max_pages;
+    int32_t heads;
+    int32_t head_dim;
+    int32_t page;
+    int32_t dtype;
+} w4_kv_append_args;
+W4_API int w4_kv_append(const w4_kv_append_args *args, void *stream);
+
+/*
+ * w4_kv_attention -- n query rows of each sequence over the paged cache.
+ *
+ *   out[i, j, h] = sum_p w_p v_p / sum_p w_p,  w_p = exp(scale * q[i, j, h] . k_p)
+ *
+ * over the positions p <= lens[i] - n + j of sequence i (p < max_pages * page),
+ * k and v of head h / (q_heads / k_heads): the queries are the sequence's last
+ * n positions. A query that sees no position gives zeros. What the cache holds
+ * at positions that a query does not see, NaN included, has no part in its
+ * output.
+ *
+ * Numerics: q (for bf16 rows times a power of two, which keeps every bit that
+ * matters), the codes and the weights w enter the products as fp16, sums and
+ * the softmax's maximum and sum are fp32, one rounding at the end. w is the one
+ * operand that is rounded: to 2^-11 of itself, or 2^-25 of the largest.
+ *
+ * q_dev, out_dev  [batch, n, q_heads, head_dim] of dtype, rows (i, j) ldq and
+ *               ldo values apart (multiples of 8), 16-byte aligned.
+ * lens_dev      int32 [batch], the new tokens included.
+ * q_heads a multiple of k_heads; head_dim a multiple of 16, at most 128; page a
+ * multiple of 16, at most 256; n at most 256; scale positive and finite.
+ * The workspace is at least w4_kv_attention_workspace_bytes(...) bytes,
+ * 256-byte aligned. Its first word is left as it is.
+ */
+typedef struct {
+    const void *q_dev;
+    const void *k_cache_dev;
+    const void *v_cache_dev;
+    const float *k_scale_dev;
+    const float *v_scale_dev;
+    const int32_t *table_dev;
+    const int32_t *lens_dev;
+    void *out_dev;
+    int64_t ldq;
+    int64_t ldo;
+    int64_t pages;
+    int32_t batch;
+    int32_t n;
+    int32_t max_pages;
+    int32_t q_heads;
+    int32_t k_heads;
+    int32_t head_dim;
+    int32_t page;
+    int32_t dtype;
+    float scale;
+} w4_kv_attention_args;
+W4_API int w4_kv_attention(const w4_kv_attention_args *args, void *workspace_dev, size_t workspace_bytes, void *stream);
+/* 0 for sizes that w4_kv_attention refuses. */
+W4_API size_t w4_kv_attention_workspace_bytes(int32_t batch, int32_t n, int32_t q_heads, int32_t k_heads, int32_t head_dim);
+
+/*
+ * w4_prompt_attention -- causal attention over packed prompts.
+ *
+ * Rows cu[i] .. cu[i + 1] - 1 are sequence i; row t of it sees the rows of its
+ * sequence up to itself:
+ *
+ *   out[t, h] = sum_p w_p v_p / sum_p w_p,  w_p = exp(scale * q[t, h] . k_p)
+ *
+ * k and v of head h / (q_heads / k_heads). Rows outside [cu[0], cu[batch]) are
+ * left as they are. What rows that a query does not see hold, NaN and
+ * infinities included, has no part in its output.
+ *
+ * Numerics: sums and the softmax's maximum and sum are fp32; the weights enter
+ * the second product in dtype; one rounding at the end.
+ *
+ * q_dev, out_dev  [T, q_heads, head_dim], k_dev, v_dev [T, k_heads, head_dim] of
+ *               dtype, rows ldq, ldo, ldk, ldv values apart (multiples of 8),
+ *               16-byte aligned.
+ * cu_dev        int32 [batch + 1], ascending, within [0, T].
+ * q_heads a multiple of k_heads; head_dim a multiple of 8, at most 128; scale
+ * positive and finite.
+ * The workspace is at least w4_prompt_attention_workspace_bytes(...) bytes,
+ * 256-byte aligned. Its first word is a device error word, which each call
+ * clears first, as w4a16_experts' is.
+ */
+typedef struct {
+    const void *q_dev;
+    const void *k_dev;
+    const void *v_dev;
+    const int32_t *cu_dev;
+    void *out_dev;
+    int64_t T;
+    int64_t ldq;
+    int64_t ldk;
+    int64_t ldv;
+    int64_t ldo;
+    int32_t batch;
+    int32_t q_heads;
+    int32_t k_heads;
+    int32_t head_dim;
+    int32_t dtype;
+    float scale;
+} w4_prompt_attention_args;
+W4_API int w4_prompt_attention(const w4_prompt_attention_args *args, void *workspace_dev, size_t workspace_bytes,
+                               void *stream);
+/*
+ * w4_prompt_attention with options (NULL: none). Of w4a16_options it takes wait_limit_cycles and, in tests only,
+ * W4_FLAG_TEST_TIMEOUT: a barrier then expects an arrival more than will ever come. Its other fields have to be 0.
+ */
+W4_API int w4_prompt_attention_opts(const w4_prompt_attention_args *args, void *workspace_dev, size_t workspace_bytes,
+                                    const w4a16_options *opts, void *stream);
+/* 0 for sizes that w4_prompt_attention refuses. */
+W4_API size_t w4_prompt_attention_workspace_bytes(int64_t T, int32_t batch, int32_t q_heads);
+
 #ifdef __cplusplus
 }
 #endif

@@ -31,7 +31,8 @@ __all__ = [
     "Epilogue", "Problem", "EPI_NONE", "EPI_SILU_MUL", "EPI_QKV_SPLIT", "w4a16_gemm_grouped",
     "w4a16_grouped_workspace_bytes", "w4a16_gemm_silu_mul", "w4a16_gemm_qkv", "interleave_gate_up",
     "qkv_head_group_rows", "w4_route", "w4a16_experts", "w4a16_experts_workspace_bytes", "w4_lora_add",
-    "w4_lora_workspace_bytes",
+    "w4_lora_workspace_bytes", "w4_qk_norm_rope", "w4_kv_append", "w4_kv_attention", "w4_kv_attention_workspace_bytes",
+    "w4_prompt_attention", "w4_prompt_attention_workspace_bytes",
 ]
 
 KERNEL_DECODE = 1
@@ -116,6 +117,13 @@ def load() -> ctypes.CDLL:
             "w4a16_experts_workspace_bytes": ([I64, I64, I64, I32, I32, I32], SZ),
             "w4_lora_add": ([ctypes.c_char_p, P, SZ, P], ctypes.c_int),
             "w4_lora_workspace_bytes": ([I64, I64, I64, I32, I32], SZ),
+            "w4_qk_norm_rope": ([ctypes.c_char_p, P], ctypes.c_int),
+            "w4_kv_append": ([ctypes.c_char_p, P], ctypes.c_int),
+            "w4_kv_attention": ([ctypes.c_char_p, P, SZ, P], ctypes.c_int),
+            "w4_kv_attention_workspace_bytes": ([I32, I32, I32, I32, I32], SZ),
+            "w4_prompt_attention": ([ctypes.c_char_p, P, SZ, P], ctypes.c_int),
+            "w4_prompt_attention_opts": ([ctypes.c_char_p, P, SZ, ctypes.POINTER(Options), P], ctypes.c_int),
+            "w4_prompt_attention_workspace_bytes": ([I64, I32, I32], SZ),
         }
         for name, (args, res) in sigs.items():
             fn = getattr(lib, name)
@@ -651,3 +659,217 @@ def w4_lora_add(base: torch.Tensor | None, x: torch.Tensor, A: torch.Tensor, B: 
     _run_with((_lib or load()).w4_lora_add, a, workspace, lambda: w4_lora_workspace_bytes(T, K, N, R, rank), device, stream,
               "w4_lora_add")
     return y
+
+
+# ----------------------------------------------------------------------------- a decoder layer's attention
+
+_ROPE_ARGS = struct.Struct("@8P5q11if")          # w4_rope_args
+_KV_APPEND_ARGS = struct.Struct("@9P4q6i")       # w4_kv_append_args
+_KV_ATTENTION_ARGS = struct.Struct("@8P3q8if")   # w4_kv_attention_args
+_PROMPT_ARGS = struct.Struct("@5P5q5if")         # w4_prompt_attention_args
+
+
+def _heads(t: torch.Tensor, name: str, dtype, shape, device: int):
+    """(address, values between rows) of a CUDA tensor [.., heads, head_dim] of this type and shape, whose rows hold their
+    heads one after another and lie evenly apart."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != device:
+        raise ValueError(f"{name} must be {dtype} {list(shape)} on cuda:{device}")
+    *lead, heads, dim = shape
+    width = heads * dim
+    if t.is_contiguous():
+        return t.data_ptr(), width
+    strides = t.stride()
+    if (dim > 1 and strides[-1] != 1) or (heads > 1 and strides[-2] != dim):
+        raise ValueError(f"the heads of {name} must follow one another in a row")
+    if len(lead) == 2 and lead[0] > 1 and lead[1] > 1 and strides[0] != lead[1] * strides[1]:
+        raise ValueError(f"the rows of {name} must lie evenly apart")
+    rows = [s for n, s in zip(lead, strides) if n > 1]
+    ld = rows[-1] if rows else width
+    if ld < width:
+        raise ValueError(f"the rows of {name} must not overlap")
+    return t.data_ptr(), ld
+
+
+def _no_gradient(what: str, *tensors):
+    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors):
+        raise ValueError(f"{what} has no gradient: call it under torch.no_grad(), or with its inputs detached")
+
+
+def w4_qk_norm_rope(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor | None, freqs: torch.Tensor | None, *,
+                    q_weight: torch.Tensor | None = None, k_weight: torch.Tensor | None = None, eps: float = 1e-6,
+                    sections=None, interleaved: bool = False, q_out: torch.Tensor | None = None,
+                    k_out: torch.Tensor | None = None, stream=None):
+    """Norm (with ``q_weight``, ``k_weight``: [head_dim]) and rotation by position of each head of q [T, heads, head_dim] and k
+    (or None), fp16 or bf16: (q, k) of the same shapes. Rows may lie further apart than they are long (slices of a fused
+    projection); ``q_out`` and ``k_out`` may be q and k (in place).
+
+    The first 2 * len(freqs) values of a head are turned by positions * freqs (int32 [T] and fp32): value i with i +
+    len(freqs), or neighbours (``interleaved``). With positions [axes, T] (up to 4: time, height, width) ``sections``
+    says how many of the frequencies, in order, go by each axis. freqs None: no rotation. There is no gradient."""
+    dt = _DTYPES.get(q.dtype)
+    if dt is None or q.dim() != 3 or not q.is_cuda:
+        raise ValueError("q must be a fp16 or bf16 CUDA tensor [T, heads, head_dim]")
+    _no_gradient("w4_qk_norm_rope", q, k, q_weight, k_weight)
+    dtype, device = q.dtype, q.get_device()
+    T, hq, dim = q.shape
+    q_at, ldq = _heads(q, "q", dtype, q.shape, device)
+    if q_out is None:
+        q_out = _empty((T, hq, dim), dtype, q.device, stream)
+        qo_at, ldqo = q_out.data_ptr(), hq * dim
+    else:
+        qo_at, ldqo = _heads(q_out, "q_out", dtype, q.shape, device)
+    if k is None:
+        if k_out is not None or k_weight is not None:
+            raise ValueError("k_out and k_weight go with k")
+        hk = k_at = ldk = ko_at = ldko = 0
+    else:
+        if k.dim() != 3:
+            raise ValueError("k must be [T, heads, head_dim]")
+        hk = k.shape[1]
+        k_at, ldk = _heads(k, "k", dtype, (T, hk, dim), device)
+        if k_out is None:
+            k_out = _empty((T, hk, dim), dtype, q.device, stream)
+            ko_at, ldko = k_out.data_ptr(), hk * dim
+        else:
+            ko_at, ldko = _heads(k_out, "k_out", dtype, (T, hk, dim), device)
+    part = [0, 0, 0, 0]
+    if freqs is None:
+        if positions is not None or sections is not None:
+            raise ValueError("positions and sections go with freqs")
+        half = axes = p_at = f_at = 0
+    else:
+        half = freqs.shape[0]
+        if positions is None or positions.dim() not in (1, 2):
+            raise ValueError("positions must be int32 [T] or [axes, T]")
+        axes = 1 if positions.dim() == 1 else positions.shape[0]
+        if sections is None:
+            if axes != 1:
+                raise ValueError("positions of several axes need sections")
+            part[0] = half
+        else:
+            if len(sections) != axes or axes > 4:
+                raise ValueError("sections must have an entry for each of up to 4 axes")
+            part[:axes] = sections
+        f_at = _like(freqs, "freqs", torch.float32, (half,), device)
+        p_at = _like(positions, "positions", torch.int32, positions.shape[:-1] + (T,), device)
+    a = _ROPE_ARGS.pack(q_at, k_at, qo_at, ko_at, p_at, f_at,
+                        0 if q_weight is None else _like(q_weight, "q_weight", dtype, (dim,), device),
+                        0 if k_weight is None else _like(k_weight, "k_weight", dtype, (dim,), device),
+                        T, ldq, ldk, ldqo, ldko, hq, hk, dim, 2 * half, axes, *part, interleaved, dt, eps)
+    rc = (_lib or load()).w4_qk_norm_rope(a, _handle(stream, device))
+    if rc != 0:
+        raise W4Error(rc, "w4_qk_norm_rope")
+    return q_out, k_out
+
+
+def _cache(k_cache, v_cache, k_scale, v_scale, table, batch: int, heads: int, dim: int, device: int):
+    """(addresses of the cache's two parts, their scales and the table; pages, page, max_pages)."""
+    if k_cache.dim() != 4 or table.dim() != 2:
+        raise ValueError("k_cache must be [pages, heads, page, head_dim] and table [batch, max_pages]")
+    pages, _, page, _ = k_cache.shape
+    shape = (pages, heads, page, dim)
+    f8 = torch.float8_e4m3fn
+    return ((_like(k_cache, "k_cache", f8, shape, device), _like(v_cache, "v_cache", f8, shape, device),
+             _like(k_scale, "k_scale", torch.float32, (pages, heads), device),
+             _like(v_scale, "v_scale", torch.float32, (pages, heads), device),
+             _like(table, "table", torch.int32, (batch, table.shape[1]), device)), pages, page, table.shape[1])
+
+
+def w4_kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, k_scale: torch.Tensor,
+                 v_scale: torch.Tensor, table: torch.Tensor, cu: torch.Tensor, lens: torch.Tensor, *, stream=None) -> None:
+    """Writes rows cu[i] .. cu[i + 1] - 1 of k and v (fp16 or bf16 [T, heads, head_dim]) to positions lens[i], lens[i] + 1, ... of
+    sequence i in the paged cache.
+
+    k_cache, v_cache float8_e4m3fn [pages, heads, page, head_dim], k_scale, v_scale fp32 [pages, heads]: a value is
+    code * scale. table int32 [batch, max_pages] lists each sequence's pages (-1: none; nothing is written there), cu int32
+    [batch + 1] ascends, lens int32 [batch] is what the cache holds before the call (the caller adds the new rows to it). A page that
+    gets rows must belong to one sequence only. See w4_kv_append in include/w4a16.h for the scales."""
+    dt = _DTYPES.get(k.dtype)
+    if dt is None or k.dim() != 3 or not k.is_cuda or lens.dim() != 1:
+        raise ValueError("k must be a fp16 or bf16 CUDA tensor [T, heads, head_dim] and lens [batch]")
+    _no_gradient("w4_kv_append", k, v)
+    T, heads, dim = k.shape
+    batch, device = lens.shape[0], k.get_device()
+    at, pages, page, max_pages = _cache(k_cache, v_cache, k_scale, v_scale, table, batch, heads, dim, device)
+    k_at, ldk = _heads(k, "k", k.dtype, k.shape, device)
+    v_at, ldv = _heads(v, "v", k.dtype, k.shape, device)
+    a = _KV_APPEND_ARGS.pack(k_at, v_at, *at, _like(cu, "cu", torch.int32, (batch + 1,), device),
+                             _like(lens, "lens", torch.int32, (batch,), device), T, ldk, ldv, pages, batch, max_pages, heads, dim,
+                             page, dt)
+    rc = (_lib or load()).w4_kv_append(a, _handle(stream, device))
+    if rc != 0:
+        raise W4Error(rc, "w4_kv_append")
+
+
+def w4_kv_attention_workspace_bytes(batch: int, n: int, q_heads: int, k_heads: int, head_dim: int) -> int:
+    return int(load().w4_kv_attention_workspace_bytes(batch, n, q_heads, k_heads, head_dim))
+
+
+def w4_kv_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor,
+                    table: torch.Tensor, lens: torch.Tensor, *, scale: float | None = None, out: torch.Tensor | None = None,
+                    workspace=None, stream=None) -> torch.Tensor:
+    """Attention of each sequence's last n positions over its part of the paged cache (w4_kv_append's): q fp16 or bf16
+    [batch, n, q_heads, head_dim] or, for n = 1, [batch, q_heads, head_dim]; the result has q's shape. lens int32 [batch] counts
+    the n positions in: query j sees positions up to lens[i] - n + j, and gives zeros where there is none. Query head h
+    reads key head h // (q_heads // k_heads). ``scale``: of the products (None: 1 / sqrt(head_dim)). There is no gradient."""
+    dt = _DTYPES.get(q.dtype)
+    if dt is None or q.dim() not in (3, 4) or not q.is_cuda:
+        raise ValueError("q must be a fp16 or bf16 CUDA tensor [batch, n, heads, head_dim] or [batch, heads, head_dim]")
+    _no_gradient("w4_kv_attention", q)
+    shape = q.shape
+    batch, n = shape[0], shape[1] if len(shape) == 4 else 1
+    hq, dim = shape[-2:]
+    hk, device = k_cache.shape[1] if k_cache.dim() == 4 else 0, q.get_device()
+    at, pages, page, max_pages = _cache(k_cache, v_cache, k_scale, v_scale, table, batch, hk, dim, device)
+    q_at, ldq = _heads(q, "q", q.dtype, shape, device)
+    if out is None:
+        out = _empty(shape, q.dtype, q.device, stream)
+        o_at, ldo = out.data_ptr(), hq * dim
+    else:
+        o_at, ldo = _heads(out, "out", q.dtype, shape, device)
+    a = _KV_ATTENTION_ARGS.pack(q_at, *at, _like(lens, "lens", torch.int32, (batch,), device), o_at, ldq, ldo, pages, batch, n,
+                                max_pages, hq, hk, dim, page, dt, dim ** -0.5 if scale is None else scale)
+    _run_with((_lib or load()).w4_kv_attention, a, workspace, lambda: w4_kv_attention_workspace_bytes(batch, n, hq, hk, dim),
+              device, stream, "w4_kv_attention")
+    return out
+
+
+def w4_prompt_attention_workspace_bytes(T: int, batch: int, q_heads: int) -> int:
+    return int(load().w4_prompt_attention_workspace_bytes(T, batch, q_heads))
+
+
+def w4_prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu: torch.Tensor, *, scale: float | None = None,
+                        out: torch.Tensor | None = None, workspace=None, stream=None, flags: int = 0,
+                        wait_limit_cycles: int = 0) -> torch.Tensor:
+    """Causal attention over packed prompts: rows cu[i] .. cu[i + 1] - 1 of q [T, q_heads, head_dim] and of k and v
+    [T, k_heads, head_dim], fp16 or bf16, are sequence i; a row sees its sequence up to itself, and query head h reads key head
+    h // (q_heads // k_heads). cu int32 [batch + 1] on the GPU, ascending. Rows outside of all sequences are left as they are in
+    ``out``. ``scale``: of the products (None: 1 / sqrt(head_dim)). There is no gradient. A wait that gave up inside the
+    kernel (out is then undefined) can be asked for with w4_last_device_error(workspace), so only where one is given;
+    ``wait_limit_cycles``: after how many clock cycles it gives up (0: about 1.5 s); ``flags``: FLAG_TEST_TIMEOUT, in tests."""
+    dt = _DTYPES.get(q.dtype)
+    if dt is None or q.dim() != 3 or k.dim() != 3 or not q.is_cuda or cu.dim() != 1 or cu.shape[0] < 1:
+        raise ValueError("q must be a fp16 or bf16 CUDA tensor [T, heads, head_dim], k alike and cu [batch + 1]")
+    _no_gradient("w4_prompt_attention", q, k, v)
+    T, hq, dim = q.shape
+    hk, batch, device = k.shape[1], cu.shape[0] - 1, q.get_device()
+    shape = (T, hk, dim)
+    q_at, ldq = _heads(q, "q", q.dtype, q.shape, device)
+    k_at, ldk = _heads(k, "k", q.dtype, shape, device)
+    v_at, ldv = _heads(v, "v", q.dtype, shape, device)
+    if out is None:
+        out = _empty(q.shape, q.dtype, q.device, stream)
+        o_at, ldo = out.data_ptr(), hq * dim
+    else:
+        o_at, ldo = _heads(out, "out", q.dtype, q.shape, device)
+    lib = _lib or load()
+    a = _PROMPT_ARGS.pack(q_at, k_at, v_at, _like(cu, "cu", torch.int32, (batch + 1,), device), o_at, T, ldq, ldk, ldv, ldo,
+                          batch, hq, hk, dim, dt, dim ** -0.5 if scale is None else scale)
+    call = lib.w4_prompt_attention
+    if flags or wait_limit_cycles:
+        o = ctypes.byref(Options(flags=flags, wait_limit_cycles=wait_limit_cycles))
+
+        def call(args, ws, nbytes, handle):
+            return lib.w4_prompt_attention_opts(args, ws, nbytes, o, handle)
+    _run_with(call, a, workspace, lambda: w4_prompt_attention_workspace_bytes(T, batch, hq), device, stream, "w4_prompt_attention")
+    return out

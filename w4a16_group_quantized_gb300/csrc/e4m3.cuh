@@ -1,0 +1,26 @@
+// Codes of 8 bits: e4m3 (4 bits of exponent, 3 of fraction, largest value 448, no infinity, 0x7F and 0xFF are NaN).
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include <cstdint>
+
+namespace w4 {
+namespace detail {
+
+// Two codes (the low one first) as two fp16 values, exactly.
+__device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t codes) {
+  uint32_t v;
+  asm("{\n\t.reg .b16 c;\n\tcvt.u16.u32 c, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, c;\n\t}" : "=r"(v) : "r"(codes));
+  return v;
+}
+
+// Two values rounded to codes, nearest even; |v| <= 448, or NaN.
+__device__ __forceinline__ uint32_t f32_e4m3x2(float lo, float hi) {
+  uint16_t c;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(c) : "f"(hi), "f"(lo));
+  return c;
+}
+
+}  // namespace detail
+}  // namespace w4

@@ -204,4 +204,65 @@ struct ExpertsArgs {
 size_t experts_workspace_bytes(int64_t T, int64_t K, int64_t I, int experts, int k, int g);
 cudaError_t launch_experts(const ExpertsArgs &a, void *workspace, int num_sms, cudaStream_t stream);
 
+// ------------------------------------------------------------------ a decoder layer's attention
+
+// w4_qk_norm_rope.
+struct RopeArgs {
+  const void *q, *k;
+  void *q_out, *k_out;
+  const int32_t *positions;  // [axes, T]
+  const float *freqs;
+  const void *q_weight, *k_weight;  // or null
+  int64_t T, ldq, ldk, ldqo, ldko;
+  int q_heads, k_heads, head_dim, rot;
+  int section_end[4];  // frequencies below section_end[a] (and not below the one before) go by axis a
+  bool interleaved;
+  int dtype;
+  float eps;
+};
+cudaError_t launch_rope(const RopeArgs &a, int num_sms, cudaStream_t stream);
+
+// The paged cache in 8 bits.
+constexpr int kKvMaxPage = 256;
+constexpr int kKvMaxDim = 128;
+
+// w4_kv_append.
+struct KvAppendArgs {
+  const void *k, *v;
+  void *k_cache, *v_cache;
+  float *k_scale, *v_scale;
+  const int32_t *table, *cu, *lens;
+  int64_t T, ldk, ldv, pages;
+  int batch, max_pages, heads, head_dim, page, dtype;
+};
+cudaError_t launch_kv_append(const KvAppendArgs &a, int num_sms, cudaStream_t stream);
+
+// w4_kv_attention.
+struct KvAttentionArgs {
+  const void *q, *k_cache, *v_cache;
+  const float *k_scale, *v_scale;
+  const int32_t *table, *lens;
+  void *out;
+  int64_t ldq, ldo, pages;
+  int batch, n, max_pages, q_heads, k_heads, head_dim, page, dtype;
+  float scale;
+};
+constexpr int kKvMaxQueries = 256;
+size_t kv_attention_workspace_bytes(int batch, int n, int q_heads, int k_heads, int head_dim, int num_sms);
+cudaError_t launch_kv_attention(const KvAttentionArgs &a, void *workspace, int num_sms, cudaStream_t stream);
+
+// w4_prompt_attention.
+struct PromptArgs {
+  const void *q, *k, *v;
+  const int32_t *cu;
+  void *out;
+  int64_t T, ldq, ldk, ldv, ldo;
+  int batch, q_heads, k_heads, head_dim, dtype;
+  float scale;
+  uint64_t wait_limit;  // cycles a wait may take; 0: the default
+  bool test_timeout;    // test only: a barrier expects an arrival more than will come
+};
+size_t prompt_attention_workspace_bytes(int64_t T, int batch, int q_heads);
+cudaError_t launch_prompt_attention(const PromptArgs &a, void *workspace, int num_sms, cudaStream_t stream);
+
 }  // namespace w4
