@@ -429,15 +429,21 @@ def test_kv_attention_queries_of_any_size(dtype, size):
 def check_prompt(q, k, v, lens, first=0, scale=None, **kw):
     got = w4.w4_prompt_attention(q, k, v, starts(lens, first), scale=scale, **kw)
     assert got.shape == q.shape and got.dtype == q.dtype
+    check_prompt_rows(got, q, k, v, lens, first, scale)
+    return got
+
+
+def check_prompt_rows(got, q, k, v, lens, first=0, scale=None, only=None):
+    """only: the rows to look at (by truth value)."""
     at = first
     for n in lens:
         rows = slice(at, at + n)
         seen = torch.ones(n, n, dtype=torch.bool, device="cuda").tril()
         o, tol = attend_want(q[rows], k[rows].double().transpose(0, 1), v[rows].double().transpose(0, 1), seen,
                              q.shape[-1] ** -0.5 if scale is None else scale, U[q.dtype])
-        within(got[rows], o, tol, n)
+        which = slice(None) if only is None else only[rows]
+        within(got[rows][which], o[which], tol[which], n)
         at += n
-    return got
 
 
 @pytest.mark.parametrize("dtype", ["f16", "bf16"])
@@ -484,7 +490,6 @@ def test_prompt_attention_what_is_not_seen(lens, bad):
         got = w4.w4_prompt_attention(q, k, v, starts(lens))
         clean = v.clone()
         clean[bad] = 0
-        want = w4.w4_prompt_attention(q, k, clean, starts(lens))
         end = next(e for e in starts(lens).tolist() if e > bad)
         sees = torch.zeros(T, 4, 64, dtype=torch.bool, device="cuda")
         sees[bad:end, 2:, 5] = True
@@ -492,7 +497,9 @@ def test_prompt_attention_what_is_not_seen(lens, bad):
         untouched = torch.ones(T, dtype=torch.bool, device="cuda")
         untouched[bad:end] = False
         assert torch.isfinite(got[~sees]).all()
-        within(got[untouched], want[untouched].double(), 4 * U[q.dtype] * want[untouched].double().abs() + 1e-3)
+        # the bound at the head for these rows too: the weights' rounding counts with sum w |v| / sum w (up to |v|'s largest, 4
+        # here), so that two ways of computing them may lie 2 u * 4 apart where |o| is small
+        check_prompt_rows(got, q, k, clean, lens, only=untouched)
         k[bad], v[bad] = value, value
         got = w4.w4_prompt_attention(q, k, v, starts(lens))
         assert not torch.isfinite(got[bad:end]).any() and torch.isfinite(got[untouched]).all()

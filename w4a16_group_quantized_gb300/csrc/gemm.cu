@@ -753,6 +753,21 @@ bool detail::make_rows_map(CUtensorMap *map, const void *rows, int64_t nrows, in
   return make_x_map(map, rows, nrows, cols, box_rows, 1, false, dtype);
 }
 
+// Rows of heads [nrows][heads][head_dim] of 16-bit values, rows ld values apart (ld and head_dim multiples of 8), 128-byte
+// swizzle, zero fill outside of the head too: one box is 64 values of one head of box_rows rows.
+bool detail::make_heads_map(CUtensorMap *map, const void *rows, int64_t nrows, int heads, int head_dim, int64_t ld, int box_rows,
+                            int dtype) {
+  EncodeTiledFn enc = encode_tiled_fn();
+  if (!enc) return false;
+  const CUtensorMapDataType dt = dtype == kDtypeBf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(head_dim), static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(nrows)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(head_dim) * 2, static_cast<cuuint64_t>(ld) * 2};
+  const cuuint32_t box[3] = {64, 1, static_cast<cuuint32_t>(box_rows)};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return enc(map, dt, 3, const_cast<void *>(rows), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 namespace {
 
 // The packed weights as two 3-D tensors of 32-bit words for the two-tile units (no swizzle, zero fill

@@ -455,6 +455,8 @@ cudaError_t allow_smem(Kernel kern, int bytes, std::atomic<uint64_t> *set) {
 
 // A tensor map of rows of 16-bit values in boxes of 64 columns x box_rows rows (gemm.cu).
 bool make_rows_map(CUtensorMap *map, const void *rows, int64_t nrows, int64_t cols, int box_rows, int dtype);
+// A tensor map of rows of heads in boxes of 64 values of one head x box_rows rows (gemm.cu).
+bool make_heads_map(CUtensorMap *map, const void *rows, int64_t nrows, int heads, int head_dim, int64_t ld, int box_rows, int dtype);
 
 // Launch with programmatic stream serialization: the launch may overlap the previous kernel's tail;
 // the kernels wait for it (griddepcontrol.wait) before touching global memory it may have written.

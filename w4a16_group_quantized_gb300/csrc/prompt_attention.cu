@@ -1,7 +1,26 @@
-// w4_prompt_attention: causal attention over packed prompts.
+// w4_prompt_attention: causal attention over packed prompts, on tcgen05.
 //
 // out[t, h] = sum_p w_p v_p / sum_p w_p, w_p = exp(scale * q . k_p) over the rows p <= t of t's sequence, with the running
-// maximum m and sum l of a softmax: s = q . k * scale * log2 e, w = 2^(s - m), O = O * 2^(m_old - m) + w v.
+// maximum m and sum l of a softmax: s = q . k * scale * log2 e, w = 2^(s - m), O = O * 2^(m_old - m) + w v. The maximum
+// need not be the newest for that: while no score is above it by more than 2^8 as a weight, O and l are left as they are and the
+// weights are simply larger than 1 (fp32 sums, and 16-bit weights keep their relative precision), so that O is
+// rescaled a few times in a row's life instead of at each step.
+//
+// A block takes 256 rows of one sequence and head as two tiles of 128, which share the keys and values that it copies, 128 rows a
+// step. Tensor memory holds for each tile the scores S (128 x 128 fp32, one row a lane), whose columns the 16-bit weights P
+// then take as the second product's A operand, and O (128 x head_dim fp32): all 512 columns. Roles (12 warps):
+//   2 x 4 softmax warps   a thread a row of its tile: S to registers, maximum, weights, P; at the end O / l to memory
+//   1 issue warp          S = Q K^T and O += P V of the two tiles in turn, so that one tile's softmax runs beside
+//                         the other's products
+//   1 copy warp           Q, then K and V of each step through a ring
+//   2 looking warps       see the tile's last V (the one with rows that its first queries do not see)
+// V is used as it stands, an MN-major operand.
+//
+// Rows that a query does not see have weight 0, but 0 * NaN is NaN. Rows behind the sequence's end are made 0 in shared
+// memory; where the tile's last 128 rows of V hold an infinity or NaN, the tile's rows are computed by themselves after all,
+// one warp a row.
+//
+// Every wait is bounded (ptx.cuh).
 #include <atomic>
 
 #include "gemm_common.cuh"
@@ -15,14 +34,30 @@ namespace {
 using namespace detail;
 
 constexpr uint32_t kAll = 0xffffffffu;
+constexpr int kTile = 128;         // query rows of a tile, and keys of a step
+constexpr int kPromptThreads = 384;
+constexpr float kSlack = 8.0f;     // how far a score may pass the maximum in use (log2 of the weight)
 
 struct PromptParams {
   const uint16_t *q, *k, *v;
   const int32_t *cu;
   uint16_t *out;
+  uint32_t *err;
   int64_t ldq, ldk, ldv, ldo;
   int T, batch, q_heads, r, head_dim;
   float scale;  // times log2 e
+  uint64_t wait_limit;
+  int test_extra;
+};
+
+// D: head_dim rounded up to 64 or 128.
+template <int D>
+struct PromptCfg {
+  static constexpr int kHalf = kTile * 128;           // 64 values of 128 rows
+  static constexpr int kTileBytes = kHalf * (D / 64);  // 128 rows of q, k or v
+  static constexpr int kStages = D == 128 ? 5 : 10;
+  static constexpr int kSmem = (2 + kStages) * kTileBytes + 1024;
+  static constexpr uint32_t kO = 2 * kTile;            // O's first column; O of the second tile D further
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -74,33 +109,453 @@ __device__ __noinline__ void one_row(const PromptParams &p, int begin, int row, 
     if (4 * lane + e < p.head_dim) out[4 * lane + e] = out_bits<DT>(o[e] / l);
 }
 
+template <int R>
+__device__ __forceinline__ void regs_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
+}
+template <int R>
+__device__ __forceinline__ void regs_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R));
+}
+constexpr int kRegsSoftmax = 208, kRegsOthers = 80;
+static_assert(2 * kRegsSoftmax + kRegsOthers <= 3 * 168, "the registers that the block was launched with (168 a thread)");
+
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+  return d;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float *lo, float *hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(*lo), "=f"(*hi) : "l"(v)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+// Two weights, the lower column's first.
 template <int DT>
-__global__ void __launch_bounds__(256) prompt_rows_kernel(const __grid_constant__ PromptParams p) {
+__device__ __forceinline__ uint32_t weights2(float lo, float hi) {
+  uint32_t d;
+  if (DT == kDtypeBf16)
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  else
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+
+// What a block works on.
+struct Work {
+  int begin, len;  // the sequence
+  int row0;        // the block's first row of it
+  int head;
+};
+
+// The block's part: sequences have ceil(len / 256) blocks a head, the last rows, which see most, first. One warp.
+__device__ __forceinline__ bool find_work(const PromptParams &p, Work *w) {
+  const int lane = threadIdx.x % 32;
+  auto count = [&](int b, int *begin, int *len) {
+    *begin = *len = 0;
+    if (b < p.batch) {
+      *begin = min(max(p.cu[b], 0), p.T);
+      *len = max(min(p.cu[b + 1], p.T) - *begin, 0);
+    }
+    return (*len + 2 * kTile - 1) / (2 * kTile);
+  };
+  int total = 0, begin, len;
+  for (int b0 = 0; b0 < p.batch; b0 += 32) total += static_cast<int>(__reduce_add_sync(kAll, count(b0 + lane, &begin, &len)));
+  int at = total - 1 - static_cast<int>(blockIdx.x) / p.q_heads;
+  w->head = blockIdx.x % p.q_heads;
+  if (at < 0) return false;
+  for (int b0 = 0; b0 < p.batch; b0 += 32) {
+    const int n = count(b0 + lane, &begin, &len);
+    int sum = n;  // up to this lane
+#pragma unroll
+    for (int i = 1; i < 32; i *= 2) {
+      const int x = __shfl_up_sync(kAll, sum, i);
+      if (lane >= i) sum += x;
+    }
+    const uint32_t past = __ballot_sync(kAll, sum > at);
+    if (past) {
+      const int from = __ffs(past) - 1;
+      w->begin = __shfl_sync(kAll, begin, from);
+      w->len = __shfl_sync(kAll, len, from);
+      w->row0 = (at - __shfl_sync(kAll, sum - n, from)) * 2 * kTile;
+      return true;
+    }
+    at -= __shfl_sync(kAll, sum, 31);
+  }
+  return false;
+}
+
+// After a wait that gave up, the copies in flight land within some microseconds: ten milliseconds pass before the block leaves
+// its shared memory.
+__device__ __forceinline__ void let_copies_land() {
+  const uint64_t t0 = clock_cycles();
+  while (clock_cycles() - t0 < 20ull * 1000 * 1000) __nanosleep(1000);
+}
+
+template <int DT, int D>
+__global__ void __launch_bounds__(kPromptThreads, 1)
+    prompt_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map,
+                            const __grid_constant__ CUtensorMap v_map, const __grid_constant__ PromptParams p) {
+  using C = PromptCfg<D>;
+  constexpr int S = C::kStages;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t q_bar[2], full_bar[S], free_bar[S], s_bar[2], p_bar[2], o_bar[2], last_bar[2], look_bar[2], drain_bar;
+  __shared__ uint32_t tmem_sh, abort_sh;
+  __shared__ uint32_t odd_sh[2];  // V of the tile's last step holds what is not finite
+  __shared__ Work work_sh;
+  __shared__ bool any_sh;
+  const uint32_t smem_base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  const int warp = __shfl_sync(kAll, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
+  volatile uint32_t *abort_flag = &abort_sh;
+
   griddep_launch_dependents();
   griddep_wait();
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * 8 + threadIdx.x / 32;
-  const int row = static_cast<int>(i / p.q_heads), h = static_cast<int>(i % p.q_heads);
-  if (row >= p.T) return;
-  for (int b = 0; b < p.batch; ++b) {
-    const int begin = max(p.cu[b], 0), end = min(p.cu[b + 1], p.T);
-    if (row >= begin && row < end) {
-      one_row<DT>(p, begin, row, h);
-      return;
+  if (blockIdx.x == 0 && threadIdx.x == 0) *p.err = 0;
+  if (warp == 0) {
+    Work w;
+    const bool any = find_work(p, &w);
+    if (lane == 0) {
+      work_sh = w;
+      any_sh = any;
     }
   }
+  if (threadIdx.x == 32) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&q_bar[i]), 1 + (i == 0 ? p.test_extra : 0));
+      mbar_init(smem_u32(&s_bar[i]), 1);
+      mbar_init(smem_u32(&p_bar[i]), 4);
+      mbar_init(smem_u32(&o_bar[i]), 1);
+      mbar_init(smem_u32(&last_bar[i]), 1);
+      mbar_init(smem_u32(&look_bar[i]), 1);
+      odd_sh[i] = 0;
+    }
+    for (int i = 0; i < S; ++i) {
+      mbar_init(smem_u32(&full_bar[i]), 1);
+      mbar_init(smem_u32(&free_bar[i]), 1);
+    }
+    mbar_init(smem_u32(&drain_bar), 1);
+    abort_sh = 0;
+    fence_mbar_init();
+  }
+  __syncthreads();
+  if (!any_sh) return;
+  if (warp == 8) {
+    tmem_alloc(smem_u32(&tmem_sh), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncwarp();
+  cta_sync_all();
+  tc_fence_after();
+  const uint32_t tmem = __shfl_sync(kAll, tmem_sh, 0);
+  const Work w = work_sh;
+  const bool two = w.len > w.row0 + kTile;  // the second tile has rows
+  const int n0 = w.row0 / kTile + 1;        // steps of the first tile; the second has one more
+  const int n = n0 + (two ? 1 : 0);
+  const uint32_t ring = smem_base + 2 * C::kTileBytes;
+  const uint32_t full0 = smem_u32(&full_bar[0]), free0 = smem_u32(&free_bar[0]);
+
+  if (warp < 8) {
+    // ------------------------------------------------------------ softmax
+    regs_up<kRegsSoftmax>();
+    const int tile = warp / 4;
+    const int r = warp % 4 * 32 + lane;  // the thread's row of the tile
+    const uint32_t lanes = static_cast<uint32_t>(warp % 4 * 32) << 16;
+    const uint32_t s_at = tmem + lanes + tile * kTile, o_at = tmem + lanes + C::kO + tile * D;
+    const uint32_t s_full = smem_u32(&s_bar[tile]), p_full = smem_u32(&p_bar[tile]);
+    const int steps = tile == 0 ? n0 : two ? n0 + 1 : 0;
+    const uint64_t scale2 = pack2(p.scale, p.scale);
+    float m = -INFINITY;
+    float l = 0.0f;
+    bool ok = true;
+    for (int i = 0; i < steps; ++i) {
+      ok = warp_wait(s_full, i & 1, abort_flag, p.err, p.wait_limit);
+      if (!ok) break;
+      tc_fence_after();
+      uint32_t s[4][32];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) tmem_ld_32x32b_x32(s_at + 32 * c, s[c]);
+      tmem_wait_ld();
+      if (i == steps - 1) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+          for (int j = 0; j < 32; ++j)
+            if (32 * c + j > r) s[c][j] = 0xFF800000u;  // -inf
+      }
+      float top[4];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        top[c] = __uint_as_float(s[c][0]);
+#pragma unroll
+        for (int j = 1; j < 32; ++j) top[c] = fmaxf(top[c], __uint_as_float(s[c][j]));
+      }
+      const float now = fmaxf(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])), m);
+      if (i == 0) {
+        m = now;
+      } else if (__any_sync(kAll, (now - m) * p.scale > kSlack)) {
+        // (the step before this one's S is complete, and with it O)
+        const float alpha = now == m ? 1.0f : ex2((m - now) * p.scale);
+        m = now;
+        l *= alpha;
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c) {
+          uint32_t o[16];
+          tmem_ld_32x32b_x16(o_at + 16 * c, o);
+          tmem_wait_ld();
+#pragma unroll
+          for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha);
+          tmem_st_32x32b_x16(o_at + 16 * c, o);
+        }
+      }
+      const float off = m == -INFINITY ? 0.0f : -m * p.scale;
+      const uint64_t off2 = pack2(off, off);
+      uint64_t sum[2] = {0ull, 0ull};
+#pragma unroll
+      for (int c = 0; c < 4; c += 2) {
+        uint32_t w2[32];
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+          const uint64_t e = fma2(pack2(__uint_as_float(s[c + j / 16][2 * (j % 16)]), __uint_as_float(s[c + j / 16][2 * (j % 16) + 1])),
+                                  scale2, off2);
+          float a, b;
+          unpack2(e, &a, &b);
+          a = ex2(a);
+          b = ex2(b);
+          sum[j & 1] = add2(sum[j & 1], pack2(a, b));
+          w2[j] = weights2<DT>(a, b);
+        }
+        tmem_st_32x32b_x32(s_at + 16 * c, w2);
+      }
+      float a, b;
+      unpack2(add2(sum[0], sum[1]), &a, &b);
+      l += a + b;
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(p_full);
+    }
+    if (ok && steps > 0) ok = warp_wait(smem_u32(&o_bar[tile]), 0, abort_flag, p.err, p.wait_limit);
+    if (ok && steps > 0) ok = warp_wait(smem_u32(&look_bar[tile]), 0, abort_flag, p.err, p.wait_limit);
+    if (ok && steps > 0) {
+      tc_fence_after();
+      const int row = w.row0 + tile * kTile + r;
+      const bool odd = *static_cast<volatile uint32_t *>(&odd_sh[tile]) != 0;
+      const float inv = 1.0f / l;
+      uint16_t *out = p.out + static_cast<int64_t>(w.begin + row) * p.ldo + static_cast<int64_t>(w.head) * p.head_dim;
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t o[32];
+        tmem_ld_32x32b_x32(o_at + 32 * c, o);
+        tmem_wait_ld();
+        if (row < w.len && !odd) {
+#pragma unroll
+          for (int j = 0; j < 32; j += 8) {
+            if (32 * c + j < p.head_dim) {
+              uint32_t x[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                x[e] = weights2<DT>(__uint_as_float(o[j + 2 * e]) * inv, __uint_as_float(o[j + 2 * e + 1]) * inv);
+              *reinterpret_cast<uint4 *>(out + 32 * c + j) = make_uint4(x[0], x[1], x[2], x[3]);
+            }
+          }
+        }
+      }
+      if (odd)
+        for (int i = 0; i < 32; ++i) {
+          const int rr = w.row0 + tile * kTile + warp % 4 * 32 + i;
+          if (rr < w.len) one_row<DT>(p, w.begin, w.begin + rr, w.head);
+        }
+    }
+  } else {
+    regs_down<kRegsOthers>();
+    if (warp == 8) {
+      // -------------------------------------------------------- products
+      const uint32_t qk = idesc_f16_f32(kTile, kTile, DT == kDtypeBf16);
+      const uint32_t pv = idesc_f16_f32(kTile, D, DT == kDtypeBf16, true);
+      auto scores = [&](int tile, uint32_t stage) {
+        const uint64_t a = sw128_kmajor_desc(smem_base + tile * C::kTileBytes), b = sw128_kmajor_desc(ring + stage * C::kTileBytes);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint64_t step = static_cast<uint64_t>(kk / 4 * (C::kHalf >> 4) + kk % 4 * 2);
+          mma_f16_ss(tmem + tile * kTile, a + step, b + step, qk, kk > 0);
+        }
+      };
+      auto values = [&](int tile, uint32_t stage, bool first) {
+        const uint64_t b = sw128_mnmajor_desc(ring + stage * C::kTileBytes, C::kHalf);
+#pragma unroll
+        for (int kk = 0; kk < kTile / 16; ++kk)
+          mma_f16_ts(tmem + C::kO + tile * D, tmem + tile * kTile + kk * 8, b + static_cast<uint64_t>(kk * (2048 >> 4)), pv,
+                     !first || kk > 0);
+      };
+      auto stage_of = [](int item) { return static_cast<uint32_t>(item % S); };
+      auto landed = [&](int item) {
+        return warp_wait(full0 + 8 * stage_of(item), (item / S) & 1, abort_flag, p.err, p.wait_limit);
+      };
+      bool ok = warp_wait(smem_u32(&q_bar[0]), 0, abort_flag, p.err, p.wait_limit) && landed(0);
+      if (ok) {
+        tc_fence_after();
+        if (elect_one()) {
+          scores(0, 0);
+          mma_commit(smem_u32(&s_bar[0]));
+        }
+        __syncwarp();
+      }
+      if (ok && two) {
+        ok = warp_wait(smem_u32(&q_bar[1]), 0, abort_flag, p.err, p.wait_limit);
+        if (ok) {
+          tc_fence_after();
+          if (elect_one()) {
+            scores(1, 0);
+            mma_commit(smem_u32(&s_bar[1]));
+          }
+          __syncwarp();
+        }
+      }
+      if (ok && elect_one()) mma_commit(free0);
+      __syncwarp();
+      for (int i = 0; ok && i < n; ++i) {
+        const uint32_t vs = stage_of(2 * i + 1), ks = stage_of(2 * i + 2);
+        // (the looking warps have waited for the last steps' V, and may have changed it)
+        ok = i < n0 - 1 ? landed(2 * i + 1) : warp_wait(smem_u32(&look_bar[i - (n0 - 1)]), 0, abort_flag, p.err, p.wait_limit);
+        if (ok && i + 1 < n) ok = landed(2 * i + 2);
+        if (!ok) break;
+#pragma unroll
+        for (int tile = 0; tile < 2; ++tile) {
+          const int steps = tile == 0 ? n0 : n;
+          if (tile == 1 && !two) break;
+          if (i >= steps) continue;
+          ok = warp_wait(smem_u32(&p_bar[tile]), i & 1, abort_flag, p.err, p.wait_limit);
+          if (!ok) break;
+          tc_fence_after();
+          if (elect_one()) {
+            values(tile, vs, i == 0);
+            if (i + 1 < steps) {
+              scores(tile, ks);
+              mma_commit(smem_u32(&s_bar[tile]));
+            } else {
+              mma_commit(smem_u32(&o_bar[tile]));
+            }
+          }
+          __syncwarp();
+        }
+        if (!ok) break;
+        if (elect_one()) {
+          mma_commit(free0 + 8 * vs);
+          if (i + 1 < n) mma_commit(free0 + 8 * ks);
+        }
+        __syncwarp();
+      }
+      const bool aborted = __any_sync(kAll, *abort_flag != 0);
+      if (aborted) {
+        if (elect_one()) mma_commit(smem_u32(&drain_bar));
+        __syncwarp();
+        drain_wait(smem_u32(&drain_bar), 0);
+      }
+    } else if (warp == 9) {
+      // ---------------------------------------------------------- copies
+      auto load = [&](const CUtensorMap *map, uint32_t to, int head, int row, uint32_t bar) {
+        mbar_arrive_expect_tx(bar, C::kTileBytes);
+#pragma unroll
+        for (int half = 0; half < D / 64; ++half) tma_load_3d(to + half * C::kHalf, map, 64 * half, head, row, bar);
+      };
+      const int kv_head = w.head / p.r;
+      bool ok = true;
+      if (elect_one()) load(&q_map, smem_base, w.head, w.begin + w.row0, smem_u32(&q_bar[0]));
+      __syncwarp();
+      for (int item = 0; item < 2 * n; ++item) {
+        const uint32_t stage = static_cast<uint32_t>(item % S);
+        if (item >= S) ok = warp_wait(free0 + 8 * stage, (item / S - 1) & 1, abort_flag, p.err, p.wait_limit);
+        if (!ok) break;
+        if (elect_one()) {
+          // the last steps' V signals barriers of its own, which have one phase: the looking warps do not follow the ring
+          const uint32_t bar = item % 2 && item / 2 >= n0 - 1 ? smem_u32(&last_bar[item / 2 - (n0 - 1)]) : full0 + 8 * stage;
+          load(item % 2 ? &v_map : &k_map, ring + stage * C::kTileBytes, kv_head, w.begin + item / 2 * kTile, bar);
+          if (item == 0 && two) load(&q_map, smem_base + C::kTileBytes, w.head, w.begin + w.row0 + kTile, smem_u32(&q_bar[1]));
+        }
+        __syncwarp();
+      }
+    } else {
+      // ------------------------------------- the last V of each tile (its place is not used again)
+      const int tile = warp - 10;
+      if (tile == 0 || two) {
+        const int step = n0 - 1 + tile;
+        const int item = 2 * step + 1;
+        const uint32_t stage = static_cast<uint32_t>(item % S);
+        if (warp_wait(smem_u32(&last_bar[tile]), 0, abort_flag, p.err, p.wait_limit)) {
+          const int live = min(w.len - step * kTile, kTile);  // rows of the sequence in it
+          const uint32_t at = ring + stage * C::kTileBytes;
+          bool odd = false;
+          constexpr uint32_t kInf = DT == kDtypeBf16 ? 0x7F80u : 0x7C00u;
+          for (int i = lane; i < C::kTileBytes / 16; i += 32) {
+            const int row = i / 8 % kTile;
+            if (row < live) {
+              const uint4 x = lds128(at + 16 * i);
+              const uint32_t v[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+              for (int e = 0; e < 4; ++e) odd |= (v[e] & kInf) == kInf || (v[e] >> 16 & kInf) == kInf;
+            } else {
+              asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(at + 16 * i), "r"(0u) : "memory");
+            }
+          }
+          odd = __any_sync(kAll, odd);
+          fence_proxy_async_shared();
+          __syncwarp();
+          if (lane == 0) {
+            odd_sh[tile] = odd;
+            mbar_arrive(smem_u32(&look_bar[tile]));
+          }
+        }
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncwarp();
+  cta_sync_all();
+  if (*abort_flag) let_copies_land();  // (else every copy has been waited for)
+  if (warp == 8) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int DT, int D>
+cudaError_t launch_tiles(const PromptArgs &a, const PromptParams &p, cudaStream_t stream) {
+  auto kern = prompt_attention_kernel<DT, D>;
+  using C = PromptCfg<D>;
+  static std::atomic<uint64_t> set{0};
+  const cudaError_t e = allow_smem(kern, C::kSmem, &set);
+  if (e != cudaSuccess) return e;
+  CUtensorMap q_map, k_map, v_map;
+  const int k_heads = a.k_heads;
+  if (!make_heads_map(&q_map, a.q, a.T, a.q_heads, a.head_dim, a.ldq, kTile, DT) ||
+      !make_heads_map(&k_map, a.k, a.T, k_heads, a.head_dim, a.ldk, kTile, DT) ||
+      !make_heads_map(&v_map, a.v, a.T, k_heads, a.head_dim, a.ldv, kTile, DT))
+    return cudaErrorInvalidValue;
+  const int64_t blocks = (a.T / (2 * kTile) + a.batch) * a.q_heads;
+  return launch_programmatic(kern, static_cast<int>(blocks), kPromptThreads, C::kSmem, stream, q_map, k_map, v_map, p);
 }
 
 }  // namespace
 
 size_t prompt_attention_workspace_bytes(int64_t, int, int) { return 256; }
 
-cudaError_t launch_prompt_attention(const PromptArgs &a, void *, int, cudaStream_t stream) {
+cudaError_t launch_prompt_attention(const PromptArgs &a, void *workspace, int, cudaStream_t stream) {
   PromptParams p;
   p.q = static_cast<const uint16_t *>(a.q);
   p.k = static_cast<const uint16_t *>(a.k);
   p.v = static_cast<const uint16_t *>(a.v);
   p.cu = a.cu;
   p.out = static_cast<uint16_t *>(a.out);
+  p.err = static_cast<uint32_t *>(workspace);
   p.ldq = a.ldq;
   p.ldk = a.ldk;
   p.ldv = a.ldv;
@@ -111,9 +566,11 @@ cudaError_t launch_prompt_attention(const PromptArgs &a, void *, int, cudaStream
   p.r = a.q_heads / a.k_heads;
   p.head_dim = a.head_dim;
   p.scale = a.scale * 1.4426950408889634f;
-  const int blocks = static_cast<int>(cdiv(a.T * a.q_heads, 8));
-  return a.dtype == kDtypeBf16 ? launch_programmatic(prompt_rows_kernel<kDtypeBf16>, blocks, 256, 0, stream, p)
-                               : launch_programmatic(prompt_rows_kernel<kDtypeF16>, blocks, 256, 0, stream, p);
+  p.wait_limit = a.wait_limit ? a.wait_limit : kWaitLimitCycles;
+  p.test_extra = a.test_timeout ? 1 : 0;
+  if (a.head_dim <= 64)
+    return a.dtype == kDtypeBf16 ? launch_tiles<kDtypeBf16, 64>(a, p, stream) : launch_tiles<kDtypeF16, 64>(a, p, stream);
+  return a.dtype == kDtypeBf16 ? launch_tiles<kDtypeBf16, 128>(a, p, stream) : launch_tiles<kDtypeF16, 128>(a, p, stream);
 }
 
 }  // namespace w4
