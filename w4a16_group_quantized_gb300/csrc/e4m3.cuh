@@ -15,6 +15,16 @@ __device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t codes) {
   return v;
 }
 
+// Four codes as two pairs of fp16 values.
+__device__ __forceinline__ void e4m3x4_f16x4(uint32_t codes, uint32_t *lo, uint32_t *hi) {
+  asm("{\n\t.reg .b16 l, h;\n\t"
+      "mov.b32 {l, h}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, l;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+      : "=r"(*lo), "=r"(*hi)
+      : "r"(codes));
+}
+
 // Two values rounded to codes, nearest even; |v| <= 448, or NaN.
 __device__ __forceinline__ uint32_t f32_e4m3x2(float lo, float hi) {
   uint16_t c;
