@@ -1,18 +1,23 @@
 // w4_kv_attention: a few query rows of each sequence over the paged cache of e4m3 codes.
 //
 // For a sequence and key head the n query rows of the r query heads that share it are n * r rows (row = j * r + head), taken 16
-// at a time (an item) as the M side of register-operand products (mma.sync m16n8k16, fp16 operands, fp32 sums): e4m3
-// codes are exact in fp16, and so are q's values (bf16 rows times a power of two that keeps them within fp16's range).
-// For a tile of 16 keys, which lies in one page: S = q . codes, s = S * (k scale * softmax scale * log2 e) + log2(v scale), a
-// row's running maximum m, w = 2^(s - m) in fp16, O += w . codes, l += (sum of w) / v scale: with the page's scale of the
-// values inside the weight no product needs a scale of its own. m may lag behind by 2^8 as a weight, so that O is
-// rescaled a few times in an item. A page whose scale is no positive number within 2^+-100 goes by a product of its own.
+// at a time (an item). For a tile of 16 keys, which lies in one page: S = q . codes, s = S * (k scale * softmax scale *
+// log2 e) + log2(v scale), a row's running maximum m, w = 2^(s - m) in fp16, O += w . codes, l += (sum of w) / v scale: with the
+// page's scale of the values inside the weight no product needs a scale of its own. m may lag behind by 2^8 as a weight, so
+// that O is rescaled a few times in an item. What of a scale of values is no positive number within 2^+-40 goes by a product
+// of its own.
+//
+// The products are register-operand ones (mma.sync m16n8k16, fp16 operands, fp32 sums): e4m3 codes are exact in fp16, and so
+// are q's values (bf16 rows times a power of two that keeps them within fp16's range). S has the rows on its M side and the
+// keys on its N side, so that its fragments are the second product's as they stand. With up to 8 rows (ROWS 8) that product is
+// turned round, values on the M side, rows on the N side: half the products, half the sums.
 //
 // The tiles of all items in order are dealt out evenly, a stretch to each of the device's warps, so that sequences of unlike
-// lengths load it evenly; a warp works alone and a lane copies to shared memory exactly the bytes that it will read
-// (cp.async, 16 bytes each, zeros past the sequence's end): no barriers. Which bytes follows from the fragments: of key 8 u +
-// lane / 4 the quarter of the head that its place in the quad has, in 16-byte pieces; of keys 2 t, 2 t + 1 and those plus 8
-// (t = lane % 4) an eighth of the head, whose codes of two neighbouring keys are put side by side by byte permutes.
+// lengths load it evenly (an item counts kItemCost tiles more for what it costs to begin); a warp works alone, with a ring of its
+// own in shared memory (cp.async, whole lines of 128 bytes, zeros past the sequence's end): no barriers. What a lane reads
+// follows from the fragments: of key 8 u + lane / 4 the quarter of the head that its place in the quad has, in 16-byte
+// pieces; of keys 2 t, 2 t + 1 and those plus 8 (t = lane % 4) an eighth of the head, whose codes of two neighbouring keys are
+// put side by side by byte permutes. The pieces of a line are exchanged so that these reads meet no bank twice.
 // Items cut between warps leave sums (O, m, l) in the workspace, one for a block whose warps are all within one item; a second
 // launch adds them in order.
 #include <atomic>
@@ -30,24 +35,40 @@ namespace {
 using namespace detail;
 
 constexpr uint32_t kAll = 0xffffffffu;
-constexpr int kKvWarps = 12;
+constexpr int kMostWarps = 16;    // of a block
+constexpr int kItemCost = 6;      // what beginning an item costs, in tiles
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kSlack = 8.0f;    // how far a score may pass the maximum in use (log2 of the weight)
 // Scales of values that go into the weights: 2^-40 to 2^40, so that a weight of one page beside another's stays a normal number
 // of 32 bits (it counts in the sum l, however small its part of O).
 constexpr float kScaleMin = 0x1p-40f, kScaleMax = 0x1p40f;
 
-// An item that begins in a warp's stretch and ends in another's: what the second launch adds.
-struct CutItem {
-  int32_t b, j;        // sequence and item of it
-  int32_t last;        // the warp that holds the item's end
-  int32_t reserved;
-  int64_t begin, end;  // the item's tiles in the order of all
-  int64_t total, workers;
+// How `units` are dealt out to warps: the first unit of each one's stretch is quotient * w + remainder * w / workers.
+struct Deal {
+  int64_t quotient;
+  uint32_t remainder, workers;  // workers <= 2^16
+  __device__ __forceinline__ int64_t start(uint32_t w) const {
+    w = min(w, workers);
+    return quotient * w + static_cast<uint32_t>(remainder * w) / workers;
+  }
+  // The warp in whose stretch a unit lies.
+  __device__ __forceinline__ int holder(int64_t unit) const {
+    int w = static_cast<int>(static_cast<double>(unit) / (static_cast<double>(quotient) + static_cast<double>(remainder) / workers));
+    while (w > 0 && start(w) > unit) --w;
+    while (start(w + 1) <= unit) ++w;
+    return w;
+  }
 };
 
-// The first tile of warp w's stretch.
-__device__ __forceinline__ int64_t stretch_of(int64_t w, int64_t workers, int64_t total) { return min(w, workers) * total / workers; }
+// An item that begins in a warp's stretch and ends in another's: what the second launch adds. Positions are in units: an item's are
+// kItemCost ones for its beginning and one for each tile.
+struct CutItem {
+  int32_t b, j;        // sequence and item of it
+  int32_t last;        // the warp that holds the item's last tile
+  int32_t warps;       // of a block that have stretches
+  int64_t begin, end;  // its tiles
+  Deal deal;
+};
 
 struct KvParams {
   const uint16_t *q;
@@ -55,20 +76,18 @@ struct KvParams {
   const float *k_scale, *v_scale;
   const int32_t *table, *lens;
   uint16_t *out;
-  int32_t *cut;    // [warps of the device]: whether cuts has an item
+  int32_t *workers;  // how many warps have a stretch
+  int32_t *cut;      // [workers]: whether cuts has an item
   CutItem *cuts;
   float *sums;     // [2 * warps]: O [rows][D], m [rows], l [rows], padded to 16 bytes, of a stretch's first and last item
   int64_t ldq, ldo, pages;
   int batch, n, max_pages, q_heads, k_heads, head_dim, page, r, row_tiles, rows, items;  // items of a sequence
   float scale;
-  FastDiv page_div, r_div;
+  FastDiv page_div, r_div, row_tiles_div;
 };
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_async8(uint32_t dst, const void *src, uint32_t bytes) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -88,29 +107,37 @@ __device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
 // Whether one of the four codes of a word is NaN (0x7F or 0xFF).
 __device__ __forceinline__ bool any_nan_code(uint32_t w) { return __vcmpeq4(w & 0x7F7F7F7Fu, 0x7F7F7F7Fu) != 0; }
 
-// D: head_dim rounded up to 64 or 128.
-template <int D>
+// D: head_dim rounded up to 64 or 128. ROWS: of an item, up to 8 or up to 16.
+template <int D, int ROWS>
 struct KvCfg {
+  static constexpr int kWarps = ROWS == 8 ? 12 : 8;
   static constexpr int kStages = 4;
   static constexpr int kPieces = D / 64;                 // 16-byte pieces of a key in a lane
   static constexpr int kVBytes = D / 8;                  // bytes of a value row in a lane
-  static constexpr int kTileBytesWarp = 32 * (32 * kPieces + 4 * kVBytes);
+  static constexpr int kPart = 16 * D;                   // bytes of a tile's keys, and of its values
+  static constexpr int kTileBytesWarp = 2 * kPart;
   static constexpr int kRing = kStages * kTileBytesWarp;
   static constexpr int kSumRow = D + 4;                  // floats of a row of a warp's sums in shared memory
-  static constexpr int kSumBytes = kKvWarps * 16 * kSumRow * 4;
-  static constexpr int kSmem = kKvWarps * kRing > kSumBytes ? kKvWarps * kRing : kSumBytes;
+  static constexpr int kSumBytes = kWarps * ROWS * kSumRow * 4;
+  static constexpr int kInfo = kWarps * 64 * 16;         // what the lookups found: two times 32 tiles a warp
+  static constexpr int kSmem = kInfo + (kWarps * kRing > kSumBytes ? kWarps * kRing : kSumBytes);
 };
 
-// What a row's sums are made of: value d of the item's row g (+ 8) is o[d % NT][2 i + e], d / NT = 2 t + e.
+// Where piece c of key (or value row) `key` of a tile lies in shared memory. Lines of 128 bytes, eight pieces each: a key, or two of 64
+// bytes. Eight lanes that read at once have, of keys, pieces t of keys g and g + 1, of values pieces g and g + 1 (or one
+// of them) of keys 2 t.
 template <int D>
-struct Sums {
-  float o[D / 8][4];
-  float m[2], l[2];
-};
+__device__ __forceinline__ int key_place(int key, int c) {
+  return D == 128 ? key * 128 + 16 * (c ^ (key & 1) << 2) : key * 64 + 16 * c;
+}
+template <int D>
+__device__ __forceinline__ int value_place(int key, int c) {
+  return D == 128 ? key * 128 + 16 * (c ^ (key >> 1 & 3) << 1) : (key >> 1) * 128 + 16 * (((key & 1) * 4 + c) ^ (key >> 1 & 3) << 1);
+}
 
 // The place of row i of item j of sequence b in q or out.
 __device__ __forceinline__ int64_t row_at(const KvParams &p, int b, int j, int i, int64_t ld) {
-  const int h = j / p.row_tiles, rho = (j - h * p.row_tiles) * 16 + i;
+  const int h = p.row_tiles_div.div(j), rho = (j - h * p.row_tiles) * 16 + i;
   const int token = p.r_div.div(rho);
   return (static_cast<int64_t>(b) * p.n + token) * ld + static_cast<int64_t>(h * p.r + rho - token * p.r) * p.head_dim;
 }
@@ -124,33 +151,76 @@ __device__ __forceinline__ uint4 eight_out(const float (&v)[8], float f) {
 // 0 for a row that saw nothing (sum 0; where it saw something the sum is positive or NaN).
 __device__ __forceinline__ float over_sum(float l) { return l == 0.0f ? 0.0f : 1.0f / l; }
 
-template <int DT, int D, bool WHOLE>
-__global__ void __launch_bounds__(32 * kKvWarps, 1) kv_attention_kernel(const __grid_constant__ KvParams p) {
-  using C = KvCfg<D>;
-  constexpr int NT = D / 8;  // n-tiles of the output
-  constexpr int S = C::kStages;
+// Which row the sums o[s][i] are of, and which value of it.
+template <int ROWS>
+__device__ __forceinline__ int row_of(int s, int i) {
+  return ROWS == 16 ? threadIdx.x % 32 / 4 + 8 * (s % 2) : threadIdx.x % 4 * 2 + i;
+}
+template <int D, int ROWS>
+__device__ __forceinline__ int value_of(int s, int i) {
+  return ROWS == 16 ? (threadIdx.x % 4 * 2 + i) * (D / 8) + s / 2 : threadIdx.x % 32 / 4 * (D / 8) + s;
+}
+
+// The second product of a tile, w the weights' fragments, added to o; or, SOME, f times it to the rows lo .. hi - 1 alone.
+template <int D, int ROWS, bool SOME>
+__device__ __forceinline__ void add_values(float (&o)[D / 8 * (ROWS / 8)][2], const uint32_t (&v)[4][D / 32],
+                                           const uint32_t (&w)[ROWS / 4], float f, int lo, int hi) {
+#pragma unroll
+  for (int x = 0; x < D / 32; ++x) {
+    uint32_t b0[4], b1[4];  // keys 2 t, 2 t + 1 and those plus 8, values 4 x .. 4 x + 3 of the lane's
+    e4m3x4_f16x4(__byte_perm(v[0][x], v[1][x], 0x5140), &b0[0], &b0[1]);
+    e4m3x4_f16x4(__byte_perm(v[0][x], v[1][x], 0x7362), &b0[2], &b0[3]);
+    e4m3x4_f16x4(__byte_perm(v[2][x], v[3][x], 0x5140), &b1[0], &b1[1]);
+    e4m3x4_f16x4(__byte_perm(v[2][x], v[3][x], 0x7362), &b1[2], &b1[3]);
+    // 16 rows: value 4 x + e of row g in set s, of row g + 8 in set s + 1, columns 2 t, 2 t + 1; 8 rows: value 4 x + e in set s, the
+    // next one in set s + 1, rows 2 t, 2 t + 1
+#pragma unroll
+    for (int e = 0; e < 4; e += ROWS == 16 ? 1 : 2) {
+      const int s = ROWS == 16 ? 2 * (4 * x + e) : 4 * x + e;
+      float d[4] = {};
+      if (!SOME) d[0] = o[s][0], d[1] = o[s][1], d[2] = o[s + 1][0], d[3] = o[s + 1][1];
+      if (ROWS == 16)
+        mma_16816<kDtypeF16>(d, w[0], w[ROWS / 4 - 2], w[1], w[ROWS / 4 - 1], b0[e], b1[e]);
+      else
+        mma_16816<kDtypeF16>(d, b0[e], b0[(e + 1) % 4], b1[e], b1[(e + 1) % 4], w[0], w[1]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int row = row_of<ROWS>(s + i / 2, i % 2);
+        if (!SOME)
+          o[s + i / 2][i % 2] = d[i];
+        else if (row >= lo && row < hi)
+          o[s + i / 2][i % 2] = fmaf(f, d[i], o[s + i / 2][i % 2]);
+      }
+    }
+  }
+}
+
+template <int DT, int D, int ROWS>
+__global__ void __launch_bounds__(32 * KvCfg<D, ROWS>::kWarps, 1) kv_attention_kernel(const __grid_constant__ KvParams p) {
+  using C = KvCfg<D, ROWS>;
+  constexpr int W = C::kWarps, S = C::kStages, RR = ROWS / 8;  // RR: rows of a lane in S
+  constexpr int NO = D / 8 * RR;  // sets of two sums: 16 rows: rows g, g + 8 x values; 8 rows: values x rows 2 t, 2 t + 1
   extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ int64_t upto[32 * kKvWarps];   // tiles of the sequences up to and with the thread's
-  // of a tile's page: k scale, log2 of the part of the v scale that goes into the weights, 1 / that part, and 0 for no page, 1
-  // for all of the scale in the weights, 2 else; the rest of it
-  __shared__ float4 stage_of[kKvWarps][S];
-  __shared__ float stage_rest[kKvWarps][S];
-  __shared__ bool together_sh;
-  __shared__ float row_m[kKvWarps][16], row_l[kKvWarps][16];
+  __shared__ int64_t upto[32 * W];  // units of the sequences up to and with the thread's
+  __shared__ float row_m[W][ROWS], row_l[W][ROWS];
   const int warp = __shfl_sync(kAll, threadIdx.x / 32, 0), lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
-  const uint32_t ring = smem_u32(smem) + warp * C::kRing;
+  // what the lookups found of a tile's page: k scale, log2 of the part of the v scale that goes into the weights, 1 / that part, the rest of it (1, or what
+  // the products are to be multiplied with)
+  float4 *info = reinterpret_cast<float4 *>(smem) + warp * 64;
+  const uint32_t ring = smem_u32(smem + C::kInfo) + warp * C::kRing;
   griddep_launch_dependents();
   griddep_wait();
 
   // ------------------------------------------------- the warp's stretch of the tiles
-  const int head_dim = WHOLE ? D : p.head_dim;
+  const int head_dim = p.head_dim;
+  const bool exact = head_dim == D;
   const int most = p.max_pages * p.page;
   auto tiles_of = [&](int b) { return max((min(p.lens[b], most) + 15) / 16, 1); };  // (a sequence without keys still has an output)
-  const int share = (p.batch + 32 * kKvWarps - 1) / (32 * kKvWarps);  // sequences a thread adds up
+  const int share = (p.batch + 32 * W - 1) / (32 * W);  // sequences a thread adds up
   int64_t sum = 0;
   for (int i = 0; i < share; ++i) {
     const int b = threadIdx.x * share + i;
-    if (b < p.batch) sum += static_cast<int64_t>(tiles_of(b)) * p.items;
+    if (b < p.batch) sum += static_cast<int64_t>(tiles_of(b) + kItemCost) * p.items;
   }
 #pragma unroll
   for (int i = 1; i < 32; i *= 2) {
@@ -164,141 +234,156 @@ __global__ void __launch_bounds__(32 * kKvWarps, 1) kv_attention_kernel(const __
   __syncthreads();
   upto[threadIdx.x] = sum + before;
   __syncthreads();
-  const int64_t total = upto[32 * kKvWarps - 1];
-  const int all_warps = kKvWarps * gridDim.x;
-  // fewer warps where the tiles are few: each takes two at least
-  const int64_t workers = min(static_cast<int64_t>(all_warps), max(total / 2, int64_t{1}));
-  const int me = blockIdx.x * kKvWarps + warp;
-  const int64_t from = stretch_of(me, workers, total), to = stretch_of(me + 1, workers, total);
-  const int count = static_cast<int>(to - from);
+  const int64_t total = upto[32 * W - 1];
+  // fewer warps where there is little to do
+  Deal deal;
+  deal.workers = static_cast<uint32_t>(min(static_cast<int64_t>(W * gridDim.x), max(total / 4, int64_t{1})));
+  deal.quotient = total / deal.workers;
+  deal.remainder = static_cast<uint32_t>(total - deal.quotient * deal.workers);
+  // (those that there are, in all blocks alike)
+  const int warps = static_cast<int>((deal.workers + gridDim.x - 1) / gridDim.x);
+  const int me = warp < warps ? blockIdx.x * warps + warp : gridDim.x * W;
+  if (blockIdx.x == 0 && threadIdx.x == 0) *p.workers = static_cast<int32_t>(deal.workers);
+  const int64_t from = deal.start(me), to = deal.start(me + 1);
   bool cut = false;
 
-  // the sequence, its item and the item's tile that `from` is
-  int b = 0, j = 0, tile = 0, tiles = 1;
-  {
-    int lo = 0, hi = 32 * kKvWarps - 1;
+  // the sequence and item that unit `at` lies in, and the unit within the item
+  auto find = [&](int64_t at, int *b, int *j, int *tiles) {
+    int lo = 0, hi = 32 * W - 1;
     while (lo < hi) {
       const int mid = (lo + hi) / 2;
-      if (upto[mid] > from)
+      if (upto[mid] > at)
         hi = mid;
       else
         lo = mid + 1;
     }
-    int64_t rest = from - (lo > 0 ? upto[lo - 1] : 0);
-    b = lo * share;
-    if (count > 0) {
-      for (;; ++b) {
-        tiles = tiles_of(b);
-        if (rest < static_cast<int64_t>(tiles) * p.items) break;
-        rest -= static_cast<int64_t>(tiles) * p.items;
-      }
-      j = static_cast<int>(rest / tiles);
-      tile = static_cast<int>(rest - static_cast<int64_t>(j) * tiles);
+    int64_t rest = at - (lo > 0 ? upto[lo - 1] : 0);
+    int64_t units;
+    for (*b = lo * share;; ++*b) {
+      *tiles = tiles_of(*b);
+      units = static_cast<int64_t>(*tiles + kItemCost) * p.items;
+      if (rest < units || *b + 1 >= p.batch) break;
+      rest -= units;
+    }
+    *j = static_cast<int>(rest / (*tiles + kItemCost));
+    return static_cast<int>(rest - static_cast<int64_t>(*j) * (*tiles + kItemCost));
+  };
+  // whether all the block's tiles are of one item: their sums are then added here
+  const int64_t block_from = deal.start(blockIdx.x * warps), block_to = deal.start((blockIdx.x + 1) * warps);
+  __shared__ int one_b, one_j, one_tiles;
+  __shared__ int64_t one_begin;
+  __shared__ bool one_sh;
+  if (threadIdx.x == 0) {
+    one_sh = false;
+    if (block_from < block_to) {
+      int ob, oj, otiles;
+      const int off = find(block_from, &ob, &oj, &otiles);
+      const int64_t begin = block_from - off + kItemCost;
+      one_sh = block_to > begin && block_to <= begin + otiles + kItemCost;
+      one_b = ob, one_j = oj, one_tiles = otiles, one_begin = begin;
     }
   }
-  // whether all the warps of the block are within one item (its first warp's): their sums are then added here
-  const int64_t block_from = stretch_of(static_cast<int64_t>(blockIdx.x) * kKvWarps, workers, total);
-  const int64_t block_to = stretch_of((static_cast<int64_t>(blockIdx.x) + 1) * kKvWarps, workers, total);
-  if (threadIdx.x == 0) together_sh = count > 0 && from - tile + tiles >= block_to;
   __syncthreads();
-  const bool together = together_sh;
+  const bool together = one_sh;
+
+  int b = 0, j = 0, tile = 0, tiles = 1;
+  int64_t at = to;  // the tile's unit
+  if (from < to) {
+    const int off = find(from, &b, &j, &tiles);
+    tile = max(off - kItemCost, 0);
+    at = from + max(kItemCost - off, 0);
+  }
 
   // ---------------------------------------------------------------- copies
-  // The tile that is copied next, and what the lookup found for 32 tiles of its item
-  int cb = b, cj = j, ct = tile, ctiles = tiles, found = 0, first = 0;
-  int at_page = -1;
-  float at_ks = 0.0f, at_vs = 0.0f;
-  const uint32_t lane_k = lane * 16, lane_v = 2 * C::kPieces * 512 + lane * C::kVBytes;
-  auto send = [&](int i) {
-    if (i < count) {
-      const int h = cj / p.row_tiles;
+  // The tile that is copied next, and what the lookups found for up to 32 tiles of its item (sent: tiles so far)
+  int cb = b, cj = j, ct = tile, ctiles = tiles, ckeys = 0, found = 0, first = 0, book = 0, next_book = 0;
+  int64_t cat = at;
+  uint32_t off_lo = 0, off_hi = 0;  // this lane's tile: offset in the cache, in 16 bytes; all ones: no page
+  int sent = 0;
+  uint32_t infos = 0;  // the places in `info` of the tiles on their way, 8 bits each (255: no page), the next one's lowest
+  // a lane copies piece lane_c of keys lane_key, lane_key + kCopyKeys, ...
+  constexpr int kCopyKeys = 512 / D;
+  const int lane_key = lane * 16 / D, lane_c = lane % (D / 16);
+  const int lane_off = lane_key * head_dim + lane_c * 16;
+  auto send = [&]() {
+    uint32_t place = 255;
+    __syncwarp();  // the place's last tile has been read
+    if (cat < to) {
       if (ct - first >= found) {  // look up the next 32 tiles of the item
+        if (ct == 0 || found == 0) ckeys = min(p.lens[cb], most);
         first = ct;
         found = min(32, ctiles - ct);
-        at_page = -1;
+        // (places go round: when it comes to a lookup, at most S tiles of the ones before are still to be worked on)
+        book = next_book;
+        next_book = (book + found) % 64;
+        int64_t off = -1;
         if (lane < found) {
-          const int pi = p.page_div.div((ct + lane) * 16);
-          int at = -1;
-          if (pi < p.max_pages) at = p.table[static_cast<int64_t>(cb) * p.max_pages + pi];
-          if (at >= 0 && at < p.pages) {
-            at_page = at;
-            at_ks = p.k_scale[static_cast<int64_t>(at) * p.k_heads + h];
-            at_vs = p.v_scale[static_cast<int64_t>(at) * p.k_heads + h];
+          const int key0 = (ct + lane) * 16;
+          const int pi = p.page_div.div(key0), h = p.row_tiles_div.div(cj);
+          int pg = -1;
+          if (pi < p.max_pages) pg = p.table[static_cast<int64_t>(cb) * p.max_pages + pi];
+          if (pg >= 0 && pg < p.pages) {
+            const int64_t ph = static_cast<int64_t>(pg) * p.k_heads + h;
+            const float ks = p.k_scale[ph], vs = p.v_scale[ph];
+            const float size = fabsf(vs);
+            const bool plain = size >= kScaleMin && size <= kScaleMax;
+            const float part = plain ? size : size > kScaleMax ? kScaleMax : kScaleMin;
+            info[(book + lane) % 64] = make_float4(ks, log2f(part), 1.0f / part, plain ? copysignf(1.0f, vs) : vs / part);
+            off = (ph * p.page + key0 - pi * p.page) * (head_dim / 16);
           }
         }
+        off_lo = static_cast<uint32_t>(off);
+        off_hi = static_cast<uint32_t>(off >> 32);
+        __syncwarp();
       }
-      const int page_at = __shfl_sync(kAll, at_page, ct - first);
-      if (lane == ct - first) {
-        const float size = fabsf(at_vs);
-        const bool plain = size >= kScaleMin && size <= kScaleMax;
-        const float part = plain ? size : size > kScaleMax ? kScaleMax : kScaleMin;
-        stage_of[warp][i % S] = make_float4(at_ks, log2f(part), 1.0f / part, at_page < 0 ? 0.0f : plain && at_vs > 0.0f ? 1.0f : 2.0f);
-        stage_rest[warp][i % S] = plain ? copysignf(1.0f, at_vs) : at_vs / part;
-      }
-      __syncwarp();
-      if (page_at >= 0) {
-        const int key0 = ct * 16;
-        const int slot0 = key0 - p.page_div.div(key0) * p.page;
-        const int64_t base = ((static_cast<int64_t>(page_at) * p.k_heads + h) * p.page + slot0) * head_dim;
-        const uint32_t to_k = ring + i % S * C::kTileBytesWarp + lane_k, to_v = ring + i % S * C::kTileBytesWarp + lane_v;
-        const uint8_t *k = p.k_cache + base + g * head_dim + t * 16, *v = p.v_cache + base + 2 * t * head_dim + g * C::kVBytes;
-        const int here = min(p.lens[cb], most) - key0;  // keys of the tile
-        if (WHOLE && here >= 16) {
+      const uint32_t lo = __shfl_sync(kAll, off_lo, ct - first), hi = __shfl_sync(kAll, off_hi, ct - first);
+      if (hi != 0xffffffffu) {
+        place = static_cast<uint32_t>(book + ct - first) % 64;
+        const int64_t base = static_cast<int64_t>((static_cast<uint64_t>(hi) << 32 | lo) * 16);
+        const uint32_t to = ring + sent % S * C::kTileBytesWarp;
+        const uint8_t *k = p.k_cache + base + lane_off, *v = p.v_cache + base + lane_off;
+        const int here = ckeys - ct * 16;  // keys of the tile
+        if (exact && here >= 16) {
 #pragma unroll
-          for (int u = 0; u < 2; ++u)
+          for (int i = 0; i < 16; i += kCopyKeys) cp_async16(to + key_place<D>(lane_key + i, lane_c), k + i * D);
 #pragma unroll
-            for (int c = 0; c < C::kPieces; ++c) cp_async16(to_k + (u * C::kPieces + c) * 512, k + 8 * u * D + 64 * c);
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const uint8_t *src = v + (c % 2 + c / 2 * 8) * D;
-            if (C::kVBytes == 16)
-              cp_async16(to_v + c * 512, src);
-            else
-              cp_async8(to_v + c * 256, src, 8);
-          }
+          for (int i = 0; i < 16; i += kCopyKeys) cp_async16(to + C::kPart + value_place<D>(lane_key + i, lane_c), v + i * D);
         } else {
 #pragma unroll
-          for (int u = 0; u < 2; ++u)
-#pragma unroll
-            for (int c = 0; c < C::kPieces; ++c) {
-              const bool there = 8 * u + g < here && (t + 4 * c) * 16 < head_dim;
-              cp_async16_zfill(to_k + (u * C::kPieces + c) * 512, there ? k + 8 * u * head_dim + 64 * c : p.k_cache, there ? 16u : 0u);
-            }
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const int key = c % 2 + c / 2 * 8;
-            const bool there = 2 * t + key < here && g * C::kVBytes < head_dim;
-            const uint8_t *src = there ? v + key * head_dim : p.v_cache;
-            if (C::kVBytes == 16)
-              cp_async16_zfill(to_v + c * 512, src, there ? 16u : 0u);
-            else
-              cp_async8(to_v + c * 256, src, there ? 8u : 0u);
+          for (int i = 0; i < 16; i += kCopyKeys) {
+            const bool there = lane_key + i < here && 16 * lane_c < head_dim;
+            cp_async16_zfill(to + key_place<D>(lane_key + i, lane_c), there ? k + i * head_dim : p.k_cache, there ? 16u : 0u);
+            cp_async16_zfill(to + C::kPart + value_place<D>(lane_key + i, lane_c), there ? v + i * head_dim : p.v_cache,
+                             there ? 16u : 0u);
           }
         }
       }
+      ++cat;
       if (++ct == ctiles) {  // the next item
         ct = first = found = 0;
+        cat += kItemCost;
         if (++cj == p.items) {
           cj = 0;
           if (++cb < p.batch) ctiles = tiles_of(cb);
         }
       }
     }
+    infos |= place << (8 * (S - 1));
+    ++sent;
     cp_commit();
   };
 
   // ------------------------------------------------------------ products
-  uint32_t q[D / 16][4];
-  Sums<D> a;
-  float mul[2];
-  int sees[2], least = 0, len = 0;
+  uint32_t q[D / 16][2 * RR];  // a step's pairs: (row g, pair 0), (row g, pair 1) and, of 16 rows, those of row g + 8
+  float o[NO][2], m[RR], l[RR], mul[RR];
+  int sees[RR], least = 0, len = 0;
   auto begin_item = [&]() {
-    const int h = j / p.row_tiles, rt = j - h * p.row_tiles;
+    const int rt = j - p.row_tiles_div.div(j) * p.row_tiles;
     len = max(p.lens[b], 0);
     const int keys = min(len, most);
     least = keys;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < RR; ++i) {
       const int rho = rt * 16 + g + 8 * i;
       const bool live = rho < p.n * p.r;
       const int token = p.r_div.div(rho);
@@ -344,47 +429,46 @@ __global__ void __launch_bounds__(32 * kKvWarps, 1) kv_attention_kernel(const __
           for (int x = 0; x < 4; ++x) {  // step 4 c + 2 e + x / 2, pair x % 2
             uint32_t bits = v[x];
             if (DT == kDtypeBf16) bits = half2_bits(value_f32<DT>(v[x] & 0xffffu) * up, value_f32<DT>(v[x] >> 16) * up);
-            q[4 * c + 2 * e + x / 2][x % 2 * 2 + i] = bits;
+            q[4 * c + 2 * e + x / 2][2 * i + x % 2] = bits;
           }
         }
-      a.m[i] = -INFINITY;
-      a.l[i] = 0.0f;
+      m[i] = -INFINITY;
+      l[i] = 0.0f;
     }
     least = static_cast<int>(__reduce_min_sync(kAll, least));
 #pragma unroll
-    for (int x = 0; x < NT; ++x)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) a.o[x][e] = 0.0f;
+    for (int x = 0; x < NO; ++x) o[x][0] = o[x][1] = 0.0f;
   };
-
-  a.m[0] = a.m[1] = -INFINITY;
-  a.l[0] = a.l[1] = 0.0f;
-#pragma unroll
-  for (int x = 0; x < NT; ++x)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) a.o[x][e] = 0.0f;
-  for (int i = 0; i < S - 1; ++i) send(i);
-  for (int i = 0; i < count; ++i) {
-    if (i == 0 || tile == 0) begin_item();
-    send(i + S - 1);  // (its place held tile i - 1, which is done)
+  begin_item();  // (also for a warp without tiles: sums of nothing)
+  for (int i = 0; i < S - 1; ++i) {
+    infos >>= 8;
+    send();
+  }
+  for (int i = 0; at < to; ++i) {
+    if (i > 0 && tile == 0) begin_item();
+    infos >>= 8;
+    send();  // (its place held tile i - 1, which is done)
     cp_wait<S - 1>();
-    const float4 st = stage_of[warp][i % S];
-    if (st.w != 0.0f) {
+    __syncwarp();  // (every lane has waited for what it copied)
+    const uint32_t mine = infos & 0xffu;
+    if (mine != 255u) {
+      const float4 st = info[mine];
       const int key0 = tile * 16;
-      const uint32_t kt = ring + i % S * C::kTileBytesWarp + lane_k, vt = ring + i % S * C::kTileBytesWarp + lane_v;
+      const uint32_t kt = ring + i % S * C::kTileBytesWarp, vt = kt + C::kPart;
       float s[2][4] = {};
 #pragma unroll
       for (int c = 0; c < C::kPieces; ++c) {
-        const uint4 k0 = lds128(kt + c * 512), k1 = lds128(kt + (C::kPieces + c) * 512);
+        const uint4 k0 = lds128(kt + key_place<D>(g, t + 4 * c)), k1 = lds128(kt + key_place<D>(g + 8, t + 4 * c));
         const uint32_t x[4] = {k0.x, k0.y, k0.z, k0.w}, y[4] = {k1.x, k1.y, k1.z, k1.w};
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
           uint32_t x0, x1, y0, y1;
           e4m3x4_f16x4(x[w], &x0, &x1);
           e4m3x4_f16x4(y[w], &y0, &y1);
-          const uint32_t(&f)[4] = q[4 * c + w];
-          mma_16816<kDtypeF16>(s[0], f[0], f[1], f[2], f[3], x0, x1);
-          mma_16816<kDtypeF16>(s[1], f[0], f[1], f[2], f[3], y0, y1);
+          const uint32_t(&f)[2 * RR] = q[4 * c + w];
+          const uint32_t f2 = RR == 2 ? f[2 * RR - 2] : 0u, f3 = RR == 2 ? f[2 * RR - 1] : 0u;
+          mma_16816<kDtypeF16>(s[0], f[0], f2, f[1], f3, x0, x1);
+          mma_16816<kDtypeF16>(s[1], f[0], f2, f[1], f3, y0, y1);
         }
       }
       // values: words of the four keys
@@ -392,58 +476,74 @@ __global__ void __launch_bounds__(32 * kKvWarps, 1) kv_attention_kernel(const __
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
         if constexpr (C::kVBytes == 16) {
-          const uint4 x = lds128(vt + c * 512);
+          const uint4 x = lds128(vt + value_place<D>(2 * t + c % 2 + c / 2 * 8, g));
           v[c][0] = x.x, v[c][1] = x.y, v[c][2] = x.z, v[c][3] = x.w;
         } else {
-          asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v[c][0]), "=r"(v[c][1]) : "r"(vt + c * 256) : "memory");
+          asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v[c][0]), "=r"(v[c][1]) : "r"(vt + value_place<D>(2 * t + c % 2 + c / 2 * 8, g / 2) + g % 2 * 8) : "memory");
         }
       }
       const bool border = key0 + 16 > least;  // some row does not see all of the tile
-      const bool own = st.w == 2.0f;          // not all of the values' scale is in the weights
-      float top[2];
+      float top[RR];
 #pragma unroll
-      for (int r2 = 0; r2 < 2; ++r2) {
+      for (int r2 = 0; r2 < RR; ++r2) {
         const float f = st.x * mul[r2];
 #pragma unroll
         for (int u = 0; u < 2; ++u)
 #pragma unroll
-          for (int e = 2 * r2; e < 2 * r2 + 2; ++e) {
-            s[u][e] = fmaf(s[u][e], f, st.y);
-            if (border && key0 + 8 * u + 2 * t + e % 2 >= sees[r2]) s[u][e] = -INFINITY;
-          }
-        top[r2] = fmaxf(fmaxf(s[0][2 * r2], s[0][2 * r2 + 1]), fmaxf(s[1][2 * r2], s[1][2 * r2 + 1]));
+          for (int e = 2 * r2; e < 2 * r2 + 2; ++e) s[u][e] = fmaf(s[u][e], f, st.y);
       }
+      if (border) {
+#pragma unroll
+        for (int r2 = 0; r2 < RR; ++r2)
+#pragma unroll
+          for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              if (key0 + 8 * u + 2 * t + e >= sees[r2]) s[u][2 * r2 + e] = -INFINITY;
+      }
+#pragma unroll
+      for (int r2 = 0; r2 < RR; ++r2)
+        top[r2] = fmaxf(fmaxf(s[0][2 * r2], s[0][2 * r2 + 1]), fmaxf(s[1][2 * r2], s[1][2 * r2 + 1]));
 #pragma unroll
       for (int x = 1; x < 4; x *= 2)
 #pragma unroll
-        for (int r2 = 0; r2 < 2; ++r2) top[r2] = fmaxf(top[r2], __shfl_xor_sync(kAll, top[r2], x));
+        for (int r2 = 0; r2 < RR; ++r2) top[r2] = fmaxf(top[r2], __shfl_xor_sync(kAll, top[r2], x));
       // (-inf + 8 is below any score: a row's first tile sets its maximum)
-      if (__any_sync(kAll, top[0] > a.m[0] + kSlack || top[1] > a.m[1] + kSlack)) {
+      if (__any_sync(kAll, top[0] > m[0] + kSlack || top[RR - 1] > m[RR - 1] + kSlack)) {
+        float alpha[RR];
 #pragma unroll
-        for (int r2 = 0; r2 < 2; ++r2) {
-          const float now = fmaxf(a.m[r2], top[r2]);
-          const float alpha = now == a.m[r2] ? 1.0f : ex2(a.m[r2] - now);
-          a.m[r2] = now;
-          a.l[r2] *= alpha;
+        for (int r2 = 0; r2 < RR; ++r2) {
+          const float now = fmaxf(m[r2], top[r2]);
+          alpha[r2] = now == m[r2] ? 1.0f : ex2(m[r2] - now);
+          m[r2] = now;
+          l[r2] *= alpha[r2];
+        }
+        if constexpr (ROWS == 16) {
 #pragma unroll
-          for (int x = 0; x < NT; ++x)
+          for (int x = 0; x < NO; ++x) o[x][0] *= alpha[x % 2], o[x][1] *= alpha[x % 2];
+        } else {
+          const float a0 = __shfl_sync(kAll, alpha[0], 8 * t), a1 = __shfl_sync(kAll, alpha[0], 8 * t + 4);
 #pragma unroll
-            for (int e = 2 * r2; e < 2 * r2 + 2; ++e) a.o[x][e] *= alpha;
+          for (int x = 0; x < NO; ++x) o[x][0] *= a0, o[x][1] *= a1;
         }
       }
 #pragma unroll
-      for (int r2 = 0; r2 < 2; ++r2) {
-        const float base = a.m[r2] == -INFINITY ? 0.0f : a.m[r2];  // (nothing seen yet: weights of 0)
+      for (int r2 = 0; r2 < RR; ++r2) {
+        const float base = m[r2] == -INFINITY ? 0.0f : m[r2];  // (nothing seen yet: weights of 0)
 #pragma unroll
         for (int u = 0; u < 2; ++u)
 #pragma unroll
           for (int e = 2 * r2; e < 2 * r2 + 2; ++e) s[u][e] = ex2(s[u][e] - base);
-        a.l[r2] = fmaf((s[0][2 * r2] + s[0][2 * r2 + 1]) + (s[1][2 * r2] + s[1][2 * r2 + 1]), st.z, a.l[r2]);
+        l[r2] = fmaf((s[0][2 * r2] + s[0][2 * r2 + 1]) + (s[1][2 * r2] + s[1][2 * r2 + 1]), st.z, l[r2]);
       }
-      const uint32_t w[4] = {half2_bits(s[0][0], s[0][1]), half2_bits(s[0][2], s[0][3]), half2_bits(s[1][0], s[1][1]),
-                             half2_bits(s[1][2], s[1][3])};
-      bool odd = own;
-      if (border && !own) {
+      uint32_t w[2 * RR];  // as q's: (row g, keys 2 t ..), (row g, those plus 8), row g + 8
+#pragma unroll
+      for (int r2 = 0; r2 < RR; ++r2) {
+        w[2 * r2] = half2_bits(s[0][2 * r2], s[0][2 * r2 + 1]);
+        w[2 * r2 + 1] = half2_bits(s[1][2 * r2], s[1][2 * r2 + 1]);
+      }
+      bool odd = st.w != 1.0f;
+      if (border && !odd) {
         // 0 * NaN is NaN: whether the tile, of which some rows do not see all, holds NaN
 #pragma unroll
         for (int c = 0; c < 4; ++c)
@@ -452,95 +552,81 @@ __global__ void __launch_bounds__(32 * kKvWarps, 1) kv_attention_kernel(const __
         odd = __any_sync(kAll, odd);
       }
       if (!odd) {
-#pragma unroll
-        for (int x = 0; x < C::kVBytes / 4; ++x) {
-          uint32_t b0[4], b1[4];
-          e4m3x4_f16x4(__byte_perm(v[0][x], v[1][x], 0x5140), &b0[0], &b0[1]);
-          e4m3x4_f16x4(__byte_perm(v[0][x], v[1][x], 0x7362), &b0[2], &b0[3]);
-          e4m3x4_f16x4(__byte_perm(v[2][x], v[3][x], 0x5140), &b1[0], &b1[1]);
-          e4m3x4_f16x4(__byte_perm(v[2][x], v[3][x], 0x7362), &b1[2], &b1[3]);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) mma_16816<kDtypeF16>(a.o[4 * x + e], w[0], w[1], w[2], w[3], b0[e], b1[e]);
-        }
+        add_values<D, ROWS, false>(o, v, w, 1.0f, 0, ROWS);
       } else {
         // each query's rows by themselves, with zeros in the place of what they do not see, and the rest of the scale on the
         // products
-        const float f = stage_rest[warp][i % S];
-        const int rt = j % p.row_tiles;
+        const int rt = j - p.row_tiles_div.div(j) * p.row_tiles;
 #pragma unroll 1
         for (int token = 0; token < p.n; ++token) {
           const int limit = min(max(len - p.n + token + 1, 0), most);
-          const bool on0 = p.r_div.div(rt * 16 + g) == token, on1 = p.r_div.div(rt * 16 + g + 8) == token;
-          if (limit <= key0 || !__any_sync(kAll, on0 || on1)) continue;
+          const int lo = token * p.r - rt * 16, hi = lo + p.r;  // the query's rows of the item
+          if (limit <= key0 || hi <= 0 || lo >= ROWS) continue;
+          uint32_t y[4][C::kVBytes / 4];
 #pragma unroll
-          for (int x = 0; x < C::kVBytes / 4; ++x) {
-            uint32_t y[4];
+          for (int c = 0; c < 4; ++c)
 #pragma unroll
-            for (int c = 0; c < 4; ++c) y[c] = key0 + 2 * t + c % 2 + c / 2 * 8 >= limit ? 0u : v[c][x];
-            uint32_t b0[4], b1[4];
-            e4m3x4_f16x4(__byte_perm(y[0], y[1], 0x5140), &b0[0], &b0[1]);
-            e4m3x4_f16x4(__byte_perm(y[0], y[1], 0x7362), &b0[2], &b0[3]);
-            e4m3x4_f16x4(__byte_perm(y[2], y[3], 0x5140), &b1[0], &b1[1]);
-            e4m3x4_f16x4(__byte_perm(y[2], y[3], 0x7362), &b1[2], &b1[3]);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              float d[4] = {};
-              mma_16816<kDtypeF16>(d, w[0], w[1], w[2], w[3], b0[e], b1[e]);
-              if (on0) a.o[4 * x + e][0] = fmaf(f, d[0], a.o[4 * x + e][0]), a.o[4 * x + e][1] = fmaf(f, d[1], a.o[4 * x + e][1]);
-              if (on1) a.o[4 * x + e][2] = fmaf(f, d[2], a.o[4 * x + e][2]), a.o[4 * x + e][3] = fmaf(f, d[3], a.o[4 * x + e][3]);
-            }
-          }
+            for (int x = 0; x < C::kVBytes / 4; ++x) y[c][x] = key0 + 2 * t + c % 2 + c / 2 * 8 >= limit ? 0u : v[c][x];
+          add_values<D, ROWS, true>(o, y, w, st.w, lo, hi);
         }
       }
     }
 
-    if (tile + 1 == tiles || i + 1 == count) {
+    if ((tile + 1 == tiles || at + 1 == to) && !together) {
       // ------------------------------------------- the item's end, or the stretch's
-      const int64_t item = from + i - tile;  // its first tile
+      const int64_t begin = at - tile, end = begin + tiles;
+      const bool here = begin >= from;  // the item begins in the stretch
+      const bool whole = here && end <= to;
 #pragma unroll
-      for (int r2 = 0; r2 < 2; ++r2) {
-        a.l[r2] += __shfl_xor_sync(kAll, a.l[r2], 1);
-        a.l[r2] += __shfl_xor_sync(kAll, a.l[r2], 2);
+      for (int r2 = 0; r2 < RR; ++r2) {
+        l[r2] += __shfl_xor_sync(kAll, l[r2], 1);
+        l[r2] += __shfl_xor_sync(kAll, l[r2], 2);
       }
-      const int rows = min(16, p.n * p.r - j % p.row_tiles * 16);
-      const bool whole = item >= from && item + tiles <= to;
-      if (together) break;
-      if (!whole && item >= from) {
+      const int rows = min(16, p.n * p.r - (j - p.row_tiles_div.div(j) * p.row_tiles) * 16);
+      if (here && !whole) {
         cut = true;
-        if (lane == 0)
-          p.cuts[me] = CutItem{b, j, static_cast<int32_t>(((item + tiles) * workers - 1) / total), 0, item, item + tiles, total, workers};
+        if (lane == 0) p.cuts[me] = CutItem{b, j, deal.holder(end - 1), warps, begin, end, deal};
+      }
+      float *sums = p.sums + (static_cast<int64_t>(2 * me) + (here ? 1 : 0)) * p.rows * (D + 4);
+      // a lane's sums of two rows: ROWS 16: rows g and g + 8 of two stretches of values, 8: rows 2 t and 2 t + 1 of one
+      float lr[2];
+      if constexpr (ROWS == 16) {
+        lr[0] = l[0], lr[1] = l[RR - 1];
+      } else {
+        lr[0] = __shfl_sync(kAll, l[0], 8 * t), lr[1] = __shfl_sync(kAll, l[0], 8 * t + 4);
       }
 #pragma unroll
       for (int r2 = 0; r2 < 2; ++r2) {
-        const int row = g + 8 * r2;
+        const int row = ROWS == 16 ? g + 8 * r2 : 2 * t + r2;
         if (row >= rows) continue;
-        if (whole) {
-          const float inv = over_sum(a.l[r2]);
-          uint16_t *out = p.out + row_at(p, b, j, row, p.ldo);
+        const float inv = over_sum(lr[r2]);
+        uint16_t *out = p.out + row_at(p, b, j, row, p.ldo);
 #pragma unroll
-          for (int e = 0; e < 2; ++e)
+        for (int e = 0; e < RR; ++e)
 #pragma unroll
-            for (int x = 0; x < NT; x += 8) {
-              const int d = (2 * t + e) * NT + x;
-              float v8[8];
+          for (int x = 0; x < D / 8; x += 8) {
+            float v8[8];
 #pragma unroll
-              for (int y = 0; y < 8; ++y) v8[y] = a.o[x + y][2 * r2 + e];
-              if (WHOLE || d < head_dim) *reinterpret_cast<uint4 *>(out + d) = eight_out<DT>(v8, inv);
+            for (int y = 0; y < 8; ++y) v8[y] = ROWS == 16 ? o[(2 * (x + y) + r2) % NO][e] : o[(x + y) % NO][r2];
+            const int d = ROWS == 16 ? (2 * t + e) * (D / 8) + x : g * (D / 8) + x;
+            if (whole) {
+              if (d < head_dim) *reinterpret_cast<uint4 *>(out + d) = eight_out<DT>(v8, inv);
+            } else {
+              *reinterpret_cast<float4 *>(sums + row * D + d) = make_float4(v8[0], v8[1], v8[2], v8[3]);
+              *reinterpret_cast<float4 *>(sums + row * D + d + 4) = make_float4(v8[4], v8[5], v8[6], v8[7]);
             }
-        } else {
-          float *sums = p.sums + (static_cast<int64_t>(2 * me) + (item >= from ? 1 : 0)) * p.rows * (D + 4);
+          }
+      }
+      if (!whole && t == 0) {
 #pragma unroll
-          for (int e = 0; e < 2; ++e)
-#pragma unroll
-            for (int x = 0; x < NT; x += 4)
-              *reinterpret_cast<float4 *>(sums + row * D + (2 * t + e) * NT + x) =
-                  make_float4(a.o[x][2 * r2 + e], a.o[x + 1][2 * r2 + e], a.o[x + 2][2 * r2 + e], a.o[x + 3][2 * r2 + e]);
-          if (t == 0) sums[p.rows * D + row] = a.m[r2], sums[p.rows * (D + 1) + row] = a.l[r2];
-        }
+        for (int r2 = 0; r2 < RR; ++r2)
+          if (g + 8 * r2 < rows) sums[p.rows * D + g + 8 * r2] = m[r2], sums[p.rows * (D + 1) + g + 8 * r2] = l[r2];
       }
     }
+    ++at;
     if (++tile == tiles) {
       tile = 0;
+      at += kItemCost;
       if (++j == p.items) {
         j = 0;
         if (++b < p.batch) tiles = tiles_of(b);
@@ -548,81 +634,71 @@ __global__ void __launch_bounds__(32 * kKvWarps, 1) kv_attention_kernel(const __
     }
   }
   if (!together) {
-    if (lane == 0) p.cut[me] = cut;
+    if (lane == 0 && from < to) p.cut[me] = cut;
     return;
   }
 
-  // ------------------------------------------- the block's warps are of one item
-  // (its first warp holds the item's place: b, j, tile and tiles as its stretch began)
-  __shared__ int b_sh, j_sh;
-  __shared__ int64_t begin_sh, end_sh;
-  if (threadIdx.x == 0) {
-    b_sh = b;
-    j_sh = j;
-    begin_sh = from + count - 1 - tile;  // (the loop was left at the stretch's last tile)
-    end_sh = begin_sh + tiles;
+  // ------------------------------------------- the block's tiles are of one item
+  const int64_t begin = one_begin, end = one_begin + one_tiles;
+  __syncthreads();  // the rings are idle (no copies are in flight: every tile sent was waited for)
+  float *sums = reinterpret_cast<float *>(smem + C::kInfo);
+#pragma unroll
+  for (int r2 = 0; r2 < RR; ++r2) {
+    l[r2] += __shfl_xor_sync(kAll, l[r2], 1);
+    l[r2] += __shfl_xor_sync(kAll, l[r2], 2);
+    if (t == 0) row_m[warp][g + 8 * r2] = m[r2], row_l[warp][g + 8 * r2] = l[r2];
   }
-  __syncthreads();  // the rings are idle
-  float *sums = reinterpret_cast<float *>(smem);
 #pragma unroll
-  for (int r2 = 0; r2 < 2; ++r2) {
-    float *to_row = sums + (warp * 16 + g + 8 * r2) * C::kSumRow;
+  for (int x = 0; x < NO; ++x)
 #pragma unroll
-    for (int e = 0; e < 2; ++e)
-#pragma unroll
-      for (int x = 0; x < NT; x += 4)
-        *reinterpret_cast<float4 *>(to_row + (2 * t + e) * NT + x) =
-            make_float4(a.o[x][2 * r2 + e], a.o[x + 1][2 * r2 + e], a.o[x + 2][2 * r2 + e], a.o[x + 3][2 * r2 + e]);
-    if (t == 0) row_m[warp][g + 8 * r2] = a.m[r2], row_l[warp][g + 8 * r2] = a.l[r2];
-  }
+    for (int i = 0; i < 2; ++i) sums[(warp * ROWS + row_of<ROWS>(x, i)) * C::kSumRow + value_of<D, ROWS>(x, i)] = o[x][i];
   __syncthreads();
-  const int64_t begin = begin_sh, end = end_sh;
-  const bool whole = begin >= block_from && end <= block_to;
-  if (lane == 0) {
-    p.cut[me] = !whole && begin >= block_from && warp == 0;
-    if (!whole && begin >= block_from && warp == 0)
-      p.cuts[me] = CutItem{b_sh, j_sh, static_cast<int32_t>((end * workers - 1) / total), 0, begin, end, total, workers};
+  const bool here = begin >= block_from, whole = here && end <= block_to;
+  if (lane == 0 && from < to) {
+    p.cut[me] = here && !whole && warp == 0;
+    if (here && !whole && warp == 0) p.cuts[me] = CutItem{one_b, one_j, deal.holder(end - 1), warps, begin, end, deal};
   }
-  const int rows = min(16, p.n * p.r - j_sh % p.row_tiles * 16);
-  float *slot = p.sums + (static_cast<int64_t>(2) * blockIdx.x * kKvWarps + (begin >= block_from ? 1 : 0)) * p.rows * (D + 4);
-  for (int i = threadIdx.x; i < rows * (D / 8); i += 32 * kKvWarps) {
-    const int row = i / (D / 8), d = i % (D / 8) * 8;
-    float top = -INFINITY, l = 0.0f, v8[8] = {};
+  const int rows = min(ROWS, p.n * p.r - (one_j - p.row_tiles_div.div(one_j) * p.row_tiles) * 16);
+  float *slot = p.sums + (static_cast<int64_t>(2) * blockIdx.x * warps + (here ? 1 : 0)) * p.rows * (D + 4);
+  for (int i = threadIdx.x; i < rows * (D / 4); i += 32 * W) {
+    const int row = i / (D / 4), d = i % (D / 4) * 4;
+    float high = -INFINITY, sum_l = 0.0f, x[4] = {};
 #pragma unroll
-    for (int w = 0; w < kKvWarps; ++w) top = fmaxf(top, row_m[w][row]);
+    for (int w = 0; w < W; ++w) high = fmaxf(high, row_m[w][row]);
 #pragma unroll 4
-    for (int w = 0; w < kKvWarps; ++w) {
-      const float f = row_m[w][row] == top ? 1.0f : ex2(row_m[w][row] - top);
-      l = fmaf(row_l[w][row], f, l);
-      const float *o = sums + (w * 16 + row) * C::kSumRow + d;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v8[e] = fmaf(o[e], f, v8[e]);
+    for (int w = 0; w < W; ++w) {
+      const float f = row_m[w][row] == high ? 1.0f : ex2(row_m[w][row] - high);
+      sum_l = fmaf(row_l[w][row], f, sum_l);
+      const float4 y = *reinterpret_cast<const float4 *>(sums + (w * ROWS + row) * C::kSumRow + d);
+      x[0] = fmaf(y.x, f, x[0]), x[1] = fmaf(y.y, f, x[1]), x[2] = fmaf(y.z, f, x[2]), x[3] = fmaf(y.w, f, x[3]);
     }
     if (whole) {
-      if (WHOLE || d < head_dim)
-        *reinterpret_cast<uint4 *>(p.out + row_at(p, b_sh, j_sh, row, p.ldo) + d) = eight_out<DT>(v8, over_sum(l));
+      const float inv = over_sum(sum_l);
+      if (d < head_dim)
+        *reinterpret_cast<uint2 *>(p.out + row_at(p, one_b, one_j, row, p.ldo) + d) =
+            make_uint2(out_bits2<DT>(x[0] * inv, x[1] * inv), out_bits2<DT>(x[2] * inv, x[3] * inv));
     } else {
-      *reinterpret_cast<float4 *>(slot + row * D + d) = make_float4(v8[0], v8[1], v8[2], v8[3]);
-      *reinterpret_cast<float4 *>(slot + row * D + d + 4) = make_float4(v8[4], v8[5], v8[6], v8[7]);
-      if (d == 0) slot[p.rows * D + row] = top, slot[p.rows * (D + 1) + row] = l;
+      *reinterpret_cast<float4 *>(slot + row * D + d) = make_float4(x[0], x[1], x[2], x[3]);
+      if (d == 0) slot[p.rows * D + row] = high, slot[p.rows * (D + 1) + row] = sum_l;
     }
   }
 }
 
 constexpr int kAddThreads = 256;
 
-// The items that are cut, their parts added in order. A block looks at warps [x * all / gridDim.x, (x + 1) * all / gridDim.x)
+// The items that are cut, their parts added in order. A block looks at warps [x * workers / gridDim.x, (x + 1) * workers / gridDim.x)
 // for items that begin there and adds p.add_rows rows of them; the groups of D / 4 threads take a row each or, with one row, the
 // parts in turn.
 template <int DT, int D>
-__global__ void __launch_bounds__(kAddThreads) kv_add_kernel(const __grid_constant__ KvParams p, int all_warps, int add_rows) {
+__global__ void __launch_bounds__(kAddThreads) kv_add_kernel(const __grid_constant__ KvParams p, int add_rows) {
   constexpr int kLane = D / 4, kGroups = kAddThreads / kLane;
   __shared__ float4 part_o[kGroups][kLane];
   __shared__ float part_m[kGroups], part_l[kGroups];
   griddep_launch_dependents();
   griddep_wait();
-  const int w0 = static_cast<int>(static_cast<int64_t>(blockIdx.x) * all_warps / gridDim.x);
-  const int w1 = static_cast<int>((static_cast<int64_t>(blockIdx.x) + 1) * all_warps / gridDim.x);
+  const int workers = *p.workers;
+  const int w0 = static_cast<int>(static_cast<int64_t>(blockIdx.x) * workers / gridDim.x);
+  const int w1 = static_cast<int>((static_cast<int64_t>(blockIdx.x) + 1) * workers / gridDim.x);
   const int group = threadIdx.x / kLane, x = threadIdx.x % kLane;
   const int row = blockIdx.y * add_rows + (add_rows > 1 ? group : 0);
   const int first = add_rows > 1 ? 0 : group, step = add_rows > 1 ? 1 : kGroups;
@@ -644,11 +720,10 @@ __global__ void __launch_bounds__(kAddThreads) kv_add_kernel(const __grid_consta
         if (row < rows && (add_rows == 1 || group < add_rows)) {
           for (int at = w + first; at <= it.last; at += step) {
             // a block within the item has one part, in its first warp's place
-            const int64_t block = at / kKvWarps;
-            const int64_t from = stretch_of(block * kKvWarps, it.workers, it.total);
-            const bool one = from >= it.begin && stretch_of((block + 1) * kKvWarps, it.workers, it.total) <= it.end;
-            if (one && at % kKvWarps != 0) continue;
-            const float *slot = p.sums + (static_cast<int64_t>(2 * at) + (stretch_of(at, it.workers, it.total) <= it.begin ? 1 : 0)) * p.rows * (D + 4);
+            const int block = at / it.warps * it.warps;
+            const bool one = it.deal.start(block) >= it.begin - kItemCost && it.deal.start(block + it.warps) <= it.end + kItemCost;
+            if (one && at != block) continue;
+            const float *slot = p.sums + (static_cast<int64_t>(2 * at) + (it.deal.start(at) <= it.begin ? 1 : 0)) * p.rows * (D + 4);
             const float pm = slot[p.rows * D + row], pl = slot[p.rows * (D + 1) + row];
             const float4 po = *reinterpret_cast<const float4 *>(slot + row * D + 4 * x);
             const float now = fmaxf(m, pm);
@@ -684,15 +759,16 @@ __global__ void __launch_bounds__(kAddThreads) kv_add_kernel(const __grid_consta
   }
 }
 
-template <int DT, int D, bool WHOLE>
+template <int DT, int D, int ROWS>
 cudaError_t launch_d(const KvParams &p, int num_sms, cudaStream_t stream) {
-  auto kern = kv_attention_kernel<DT, D, WHOLE>;
+  using C = KvCfg<D, ROWS>;
+  auto kern = kv_attention_kernel<DT, D, ROWS>;
   static std::atomic<uint64_t> set{0};
-  cudaError_t e = allow_smem(kern, KvCfg<D>::kSmem, &set);
+  cudaError_t e = allow_smem(kern, C::kSmem, &set);
   if (e != cudaSuccess) return e;
-  e = launch_programmatic(kern, num_sms, 32 * kKvWarps, KvCfg<D>::kSmem, stream, p);
+  e = launch_programmatic(kern, num_sms, 32 * C::kWarps, C::kSmem, stream, p);
   if (e != cudaSuccess) return e;
-  const int all = num_sms * kKvWarps;
+  const int all = num_sms * C::kWarps;
   const int64_t items = static_cast<int64_t>(p.batch) * p.items;
   const int add_rows = items >= num_sms ? (p.rows < 4 ? 4 : kAddThreads * 4 / D) : 1;
   cudaLaunchConfig_t cfg = {};
@@ -704,19 +780,20 @@ cudaError_t launch_d(const KvParams &p, int num_sms, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, kv_add_kernel<DT, D>, p, all, add_rows);
+  e = cudaLaunchKernelEx(&cfg, kv_add_kernel<DT, D>, p, add_rows);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-size_t slots_at(int num_sms) { return 256 + 256 * static_cast<size_t>(cdiv(num_sms * kKvWarps * (sizeof(CutItem) + sizeof(int32_t)), 256)); }
+size_t slots_at(int num_sms) { return 256 + 256 * static_cast<size_t>(cdiv(num_sms * kMostWarps * (sizeof(CutItem) + sizeof(int32_t)), 256)); }
 
 }  // namespace
 
-// The first block is left alone (its first word is another call's error word); then the cut items and their parts.
+// The first 256 bytes (whose first word, another call's error word, is left alone) hold the number of workers; then the cut items and their
+// parts.
 size_t kv_attention_workspace_bytes(int, int n, int q_heads, int k_heads, int head_dim, int num_sms) {
   const int64_t rows = static_cast<int64_t>(n) * (q_heads / k_heads);
   const size_t d = head_dim <= 64 ? 64 : 128;
-  return slots_at(num_sms) + static_cast<size_t>(2 * num_sms * kKvWarps) * (rows < 16 ? rows : 16) * (d + 4) * sizeof(float);
+  return slots_at(num_sms) + static_cast<size_t>(2 * num_sms * kMostWarps) * (rows < 16 ? rows : 16) * (d + 4) * sizeof(float);
 }
 
 cudaError_t launch_kv_attention(const KvAttentionArgs &a, void *workspace, int num_sms, cudaStream_t stream) {
@@ -730,8 +807,9 @@ cudaError_t launch_kv_attention(const KvAttentionArgs &a, void *workspace, int n
   p.lens = a.lens;
   p.out = static_cast<uint16_t *>(a.out);
   uint8_t *ws = static_cast<uint8_t *>(workspace);
+  p.workers = reinterpret_cast<int32_t *>(ws + 128);
   p.cuts = reinterpret_cast<CutItem *>(ws + 256);
-  p.cut = reinterpret_cast<int32_t *>(ws + 256 + static_cast<size_t>(num_sms) * kKvWarps * sizeof(CutItem));
+  p.cut = reinterpret_cast<int32_t *>(ws + 256 + static_cast<size_t>(num_sms) * kMostWarps * sizeof(CutItem));
   p.sums = reinterpret_cast<float *>(ws + slots_at(num_sms));
   p.ldq = a.ldq;
   p.ldo = a.ldo;
@@ -750,12 +828,11 @@ cudaError_t launch_kv_attention(const KvAttentionArgs &a, void *workspace, int n
   p.scale = a.scale;
   p.page_div = make_fastdiv(static_cast<uint32_t>(a.page));
   p.r_div = make_fastdiv(static_cast<uint32_t>(p.r));
+  p.row_tiles_div = make_fastdiv(static_cast<uint32_t>(p.row_tiles));
   auto go = [&](auto dt) {
     constexpr int DT = decltype(dt)::value;
-    if (a.head_dim == 128) return launch_d<DT, 128, true>(p, num_sms, stream);
-    if (a.head_dim > 64) return launch_d<DT, 128, false>(p, num_sms, stream);
-    if (a.head_dim == 64) return launch_d<DT, 64, true>(p, num_sms, stream);
-    return launch_d<DT, 64, false>(p, num_sms, stream);
+    if (p.rows <= 8) return a.head_dim > 64 ? launch_d<DT, 128, 8>(p, num_sms, stream) : launch_d<DT, 64, 8>(p, num_sms, stream);
+    return a.head_dim > 64 ? launch_d<DT, 128, 16>(p, num_sms, stream) : launch_d<DT, 64, 16>(p, num_sms, stream);
   };
   return a.dtype == kDtypeBf16 ? go(std::integral_constant<int, kDtypeBf16>{}) : go(std::integral_constant<int, kDtypeF16>{});
 }
