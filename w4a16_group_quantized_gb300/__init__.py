@@ -477,6 +477,9 @@ _EXPERTS_ARGS = struct.Struct("@6P3q4i")  # w4a16_experts_args
 _LORA_ARGS = struct.Struct("@8P6q4i")     # w4_lora_args
 
 
+_DEVICES = [torch.device("cuda", i) for i in range(64)]
+
+
 def _rows(t: torch.Tensor, name: str) -> int:
     """Values between the rows of a 2-D CUDA tensor, which are contiguous and do not overlap, but may lie further apart
     than they are long (a single row's stride says nothing)."""
@@ -519,8 +522,11 @@ def _run_with(call, args, workspace, sized, device: int, stream, what: str):
     """call(args, workspace, its bytes, stream). A Workspace grows, and without one a buffer is made, by sized()."""
     handle = _handle(stream, device)
     if workspace is None:
-        with torch.cuda.stream(stream):
-            ws = torch.empty(max(sized(), 1), dtype=torch.uint8, device=f"cuda:{device}")
+        if stream is None:
+            ws = torch.empty(max(sized(), 1), dtype=torch.uint8, device=_DEVICES[device])
+        else:
+            with torch.cuda.stream(stream):
+                ws = torch.empty(max(sized(), 1), dtype=torch.uint8, device=_DEVICES[device])
     else:
         ws = workspace.scratch if isinstance(workspace, Workspace) else workspace
         if ws.get_device() != device or not ws.is_contiguous():
@@ -669,29 +675,36 @@ _KV_ATTENTION_ARGS = struct.Struct("@8P3q8if")   # w4_kv_attention_args
 _PROMPT_ARGS = struct.Struct("@5P5q5if")         # w4_prompt_attention_args
 
 
+_F8, _F32, _I32 = torch.float8_e4m3fn, torch.float32, torch.int32
+
+
 def _heads(t: torch.Tensor, name: str, dtype, shape, device: int):
     """(address, values between rows) of a CUDA tensor [.., heads, head_dim] of this type and shape, whose rows hold their
     heads one after another and lie evenly apart."""
     if t.dtype is not dtype or t.shape != shape or t.get_device() != device:
         raise ValueError(f"{name} must be {dtype} {list(shape)} on cuda:{device}")
-    *lead, heads, dim = shape
+    heads, dim = shape[-2:]
     width = heads * dim
     if t.is_contiguous():
         return t.data_ptr(), width
     strides = t.stride()
     if (dim > 1 and strides[-1] != 1) or (heads > 1 and strides[-2] != dim):
         raise ValueError(f"the heads of {name} must follow one another in a row")
-    if len(lead) == 2 and lead[0] > 1 and lead[1] > 1 and strides[0] != lead[1] * strides[1]:
-        raise ValueError(f"the rows of {name} must lie evenly apart")
-    rows = [s for n, s in zip(lead, strides) if n > 1]
-    ld = rows[-1] if rows else width
+    if len(shape) == 3:
+        ld = strides[0] if shape[0] > 1 else width
+    else:
+        batch, n = shape[0], shape[1]
+        if batch > 1 and n > 1 and strides[0] != n * strides[1]:
+            raise ValueError(f"the rows of {name} must lie evenly apart")
+        ld = strides[1] if n > 1 else strides[0] if batch > 1 else width
     if ld < width:
         raise ValueError(f"the rows of {name} must not overlap")
     return t.data_ptr(), ld
 
 
-def _no_gradient(what: str, *tensors):
-    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors):
+def _no_gradient(what: str):
+    """For a call whose inputs require a gradient."""
+    if torch.is_grad_enabled():
         raise ValueError(f"{what} has no gradient: call it under torch.no_grad(), or with its inputs detached")
 
 
@@ -709,15 +722,17 @@ def w4_qk_norm_rope(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Te
     dt = _DTYPES.get(q.dtype)
     if dt is None or q.dim() != 3 or not q.is_cuda:
         raise ValueError("q must be a fp16 or bf16 CUDA tensor [T, heads, head_dim]")
-    _no_gradient("w4_qk_norm_rope", q, k, q_weight, k_weight)
-    dtype, device = q.dtype, q.get_device()
-    T, hq, dim = q.shape
-    q_at, ldq = _heads(q, "q", dtype, q.shape, device)
+    if (q.requires_grad or (k is not None and k.requires_grad) or (q_weight is not None and q_weight.requires_grad) or
+            (k_weight is not None and k_weight.requires_grad)):
+        _no_gradient("w4_qk_norm_rope")
+    dtype, device, shape = q.dtype, q.get_device(), q.shape
+    T, hq, dim = shape
+    q_at, ldq = _heads(q, "q", dtype, shape, device)
     if q_out is None:
-        q_out = _empty((T, hq, dim), dtype, q.device, stream)
+        q_out = _empty(shape, dtype, q.device, stream)
         qo_at, ldqo = q_out.data_ptr(), hq * dim
     else:
-        qo_at, ldqo = _heads(q_out, "q_out", dtype, q.shape, device)
+        qo_at, ldqo = _heads(q_out, "q_out", dtype, shape, device)
     if k is None:
         if k_out is not None or k_weight is not None:
             raise ValueError("k_out and k_weight go with k")
@@ -726,12 +741,13 @@ def w4_qk_norm_rope(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Te
         if k.dim() != 3:
             raise ValueError("k must be [T, heads, head_dim]")
         hk = k.shape[1]
-        k_at, ldk = _heads(k, "k", dtype, (T, hk, dim), device)
+        shape = (T, hk, dim)
+        k_at, ldk = _heads(k, "k", dtype, shape, device)
         if k_out is None:
-            k_out = _empty((T, hk, dim), dtype, q.device, stream)
+            k_out = _empty(shape, dtype, q.device, stream)
             ko_at, ldko = k_out.data_ptr(), hk * dim
         else:
-            ko_at, ldko = _heads(k_out, "k_out", dtype, (T, hk, dim), device)
+            ko_at, ldko = _heads(k_out, "k_out", dtype, shape, device)
     part = [0, 0, 0, 0]
     if freqs is None:
         if positions is not None or sections is not None:
@@ -743,15 +759,15 @@ def w4_qk_norm_rope(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Te
             raise ValueError("positions must be int32 [T] or [axes, T]")
         axes = 1 if positions.dim() == 1 else positions.shape[0]
         if sections is None:
-            if axes != 1:
-                raise ValueError("positions of several axes need sections")
+            if positions.dim() != 1:
+                raise ValueError("positions [axes, T] need sections")
             part[0] = half
         else:
-            if len(sections) != axes or axes > 4:
-                raise ValueError("sections must have an entry for each of up to 4 axes")
+            if positions.dim() != 2 or len(sections) != axes or axes > 4:
+                raise ValueError("positions must be [axes, T], and sections have an entry for each of up to 4 axes")
             part[:axes] = sections
-        f_at = _like(freqs, "freqs", torch.float32, (half,), device)
-        p_at = _like(positions, "positions", torch.int32, positions.shape[:-1] + (T,), device)
+        f_at = _like(freqs, "freqs", _F32, (half,), device)
+        p_at = _like(positions, "positions", _I32, (T,) if sections is None else (axes, T), device)
     a = _ROPE_ARGS.pack(q_at, k_at, qo_at, ko_at, p_at, f_at,
                         0 if q_weight is None else _like(q_weight, "q_weight", dtype, (dim,), device),
                         0 if k_weight is None else _like(k_weight, "k_weight", dtype, (dim,), device),
@@ -762,17 +778,25 @@ def w4_qk_norm_rope(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Te
     return q_out, k_out
 
 
-def _cache(k_cache, v_cache, k_scale, v_scale, table, batch: int, heads: int, dim: int, device: int):
-    """(addresses of the cache's two parts, their scales and the table; pages, page, max_pages)."""
-    if k_cache.dim() != 4 or table.dim() != 2:
+def _cache(k_cache, v_cache, k_scale, v_scale, table, batch: int, heads, dim: int, device: int):
+    """(pages, heads, page, max_pages) of a paged cache (heads None: as many as it has) that goes with a call's other tensors."""
+    shape = k_cache.shape
+    if len(shape) != 4 or table.dim() != 2:
         raise ValueError("k_cache must be [pages, heads, page, head_dim] and table [batch, max_pages]")
-    pages, _, page, _ = k_cache.shape
-    shape = (pages, heads, page, dim)
-    f8 = torch.float8_e4m3fn
-    return ((_like(k_cache, "k_cache", f8, shape, device), _like(v_cache, "v_cache", f8, shape, device),
-             _like(k_scale, "k_scale", torch.float32, (pages, heads), device),
-             _like(v_scale, "v_scale", torch.float32, (pages, heads), device),
-             _like(table, "table", torch.int32, (batch, table.shape[1]), device)), pages, page, table.shape[1])
+    pages, hk, page, d = shape
+    if (k_cache.dtype is not _F8 or v_cache.dtype is not _F8 or v_cache.shape != shape or d != dim or hk != (heads or hk) or
+            k_cache.get_device() != device or v_cache.get_device() != device):
+        raise ValueError(f"k_cache and v_cache must be {_F8} [pages, {heads or 'heads'}, page, {dim}] on cuda:{device}")
+    if (k_scale.dtype is not _F32 or v_scale.dtype is not _F32 or k_scale.shape != (pages, hk) or v_scale.shape != (pages, hk) or
+            k_scale.get_device() != device or v_scale.get_device() != device):
+        raise ValueError(f"k_scale and v_scale must be {_F32} [{pages}, {hk}] on cuda:{device}")
+    rows, max_pages = table.shape
+    if table.dtype is not _I32 or rows != batch or table.get_device() != device:
+        raise ValueError(f"table must be {_I32} [{batch}, max_pages] on cuda:{device}")
+    if not (k_cache.is_contiguous() and v_cache.is_contiguous() and k_scale.is_contiguous() and v_scale.is_contiguous() and
+            table.is_contiguous()):
+        raise ValueError("k_cache, v_cache, k_scale, v_scale and table must be contiguous")
+    return pages, hk, page, max_pages
 
 
 def w4_kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, k_scale: torch.Tensor,
@@ -787,15 +811,17 @@ def w4_kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cach
     dt = _DTYPES.get(k.dtype)
     if dt is None or k.dim() != 3 or not k.is_cuda or lens.dim() != 1:
         raise ValueError("k must be a fp16 or bf16 CUDA tensor [T, heads, head_dim] and lens [batch]")
-    _no_gradient("w4_kv_append", k, v)
-    T, heads, dim = k.shape
+    if k.requires_grad or v.requires_grad:
+        _no_gradient("w4_kv_append")
+    shape, dtype = k.shape, k.dtype
+    T, heads, dim = shape
     batch, device = lens.shape[0], k.get_device()
-    at, pages, page, max_pages = _cache(k_cache, v_cache, k_scale, v_scale, table, batch, heads, dim, device)
-    k_at, ldk = _heads(k, "k", k.dtype, k.shape, device)
-    v_at, ldv = _heads(v, "v", k.dtype, k.shape, device)
-    a = _KV_APPEND_ARGS.pack(k_at, v_at, *at, _like(cu, "cu", torch.int32, (batch + 1,), device),
-                             _like(lens, "lens", torch.int32, (batch,), device), T, ldk, ldv, pages, batch, max_pages, heads, dim,
-                             page, dt)
+    pages, _, page, max_pages = _cache(k_cache, v_cache, k_scale, v_scale, table, batch, heads, dim, device)
+    k_at, ldk = _heads(k, "k", dtype, shape, device)
+    v_at, ldv = _heads(v, "v", dtype, shape, device)
+    a = _KV_APPEND_ARGS.pack(k_at, v_at, k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+                             table.data_ptr(), _like(cu, "cu", _I32, (batch + 1,), device),
+                             _like(lens, "lens", _I32, (batch,), device), T, ldk, ldv, pages, batch, max_pages, heads, dim, page, dt)
     rc = (_lib or load()).w4_kv_append(a, _handle(stream, device))
     if rc != 0:
         raise W4Error(rc, "w4_kv_append")
@@ -812,23 +838,28 @@ def w4_kv_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     [batch, n, q_heads, head_dim] or, for n = 1, [batch, q_heads, head_dim]; the result has q's shape. lens int32 [batch] counts
     the n positions in: query j sees positions up to lens[i] - n + j, and gives zeros where there is none. Query head h
     reads key head h // (q_heads // k_heads). ``scale``: of the products (None: 1 / sqrt(head_dim)). There is no gradient."""
-    dt = _DTYPES.get(q.dtype)
-    if dt is None or q.dim() not in (3, 4) or not q.is_cuda:
+    dtype, shape = q.dtype, q.shape
+    dt, dims = _DTYPES.get(dtype), len(shape)
+    if dt is None or not 3 <= dims <= 4 or not q.is_cuda:
         raise ValueError("q must be a fp16 or bf16 CUDA tensor [batch, n, heads, head_dim] or [batch, heads, head_dim]")
-    _no_gradient("w4_kv_attention", q)
-    shape = q.shape
-    batch, n = shape[0], shape[1] if len(shape) == 4 else 1
-    hq, dim = shape[-2:]
-    hk, device = k_cache.shape[1] if k_cache.dim() == 4 else 0, q.get_device()
-    at, pages, page, max_pages = _cache(k_cache, v_cache, k_scale, v_scale, table, batch, hk, dim, device)
-    q_at, ldq = _heads(q, "q", q.dtype, shape, device)
+    if q.requires_grad:
+        _no_gradient("w4_kv_attention")
+    if dims == 3:
+        batch, hq, dim = shape
+        n = 1
+    else:
+        batch, n, hq, dim = shape
+    device = q.get_device()
+    pages, hk, page, max_pages = _cache(k_cache, v_cache, k_scale, v_scale, table, batch, None, dim, device)
+    q_at, ldq = _heads(q, "q", dtype, shape, device)
     if out is None:
-        out = _empty(shape, q.dtype, q.device, stream)
+        out = _empty(shape, dtype, q.device, stream)
         o_at, ldo = out.data_ptr(), hq * dim
     else:
-        o_at, ldo = _heads(out, "out", q.dtype, shape, device)
-    a = _KV_ATTENTION_ARGS.pack(q_at, *at, _like(lens, "lens", torch.int32, (batch,), device), o_at, ldq, ldo, pages, batch, n,
-                                max_pages, hq, hk, dim, page, dt, dim ** -0.5 if scale is None else scale)
+        o_at, ldo = _heads(out, "out", dtype, shape, device)
+    a = _KV_ATTENTION_ARGS.pack(q_at, k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), table.data_ptr(),
+                                _like(lens, "lens", _I32, (batch,), device), o_at, ldq, ldo, pages, batch, n, max_pages, hq, hk, dim,
+                                page, dt, dim ** -0.5 if scale is None else scale)
     _run_with((_lib or load()).w4_kv_attention, a, workspace, lambda: w4_kv_attention_workspace_bytes(batch, n, hq, hk, dim),
               device, stream, "w4_kv_attention")
     return out
@@ -847,24 +878,26 @@ def w4_prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu: t
     ``out``. ``scale``: of the products (None: 1 / sqrt(head_dim)). There is no gradient. A wait that gave up inside the
     kernel (out is then undefined) can be asked for with w4_last_device_error(workspace), so only where one is given;
     ``wait_limit_cycles``: after how many clock cycles it gives up (0: about 1.5 s); ``flags``: FLAG_TEST_TIMEOUT, in tests."""
-    dt = _DTYPES.get(q.dtype)
-    if dt is None or q.dim() != 3 or k.dim() != 3 or not q.is_cuda or cu.dim() != 1 or cu.shape[0] < 1:
+    dtype, shape = q.dtype, q.shape
+    dt = _DTYPES.get(dtype)
+    if dt is None or len(shape) != 3 or k.dim() != 3 or not q.is_cuda or cu.dim() != 1 or cu.shape[0] < 1:
         raise ValueError("q must be a fp16 or bf16 CUDA tensor [T, heads, head_dim], k alike and cu [batch + 1]")
-    _no_gradient("w4_prompt_attention", q, k, v)
-    T, hq, dim = q.shape
+    if q.requires_grad or k.requires_grad or v.requires_grad:
+        _no_gradient("w4_prompt_attention")
+    T, hq, dim = shape
     hk, batch, device = k.shape[1], cu.shape[0] - 1, q.get_device()
-    shape = (T, hk, dim)
-    q_at, ldq = _heads(q, "q", q.dtype, q.shape, device)
-    k_at, ldk = _heads(k, "k", q.dtype, shape, device)
-    v_at, ldv = _heads(v, "v", q.dtype, shape, device)
+    k_shape = (T, hk, dim)
+    q_at, ldq = _heads(q, "q", dtype, shape, device)
+    k_at, ldk = _heads(k, "k", dtype, k_shape, device)
+    v_at, ldv = _heads(v, "v", dtype, k_shape, device)
     if out is None:
-        out = _empty(q.shape, q.dtype, q.device, stream)
+        out = _empty(shape, dtype, q.device, stream)
         o_at, ldo = out.data_ptr(), hq * dim
     else:
-        o_at, ldo = _heads(out, "out", q.dtype, q.shape, device)
+        o_at, ldo = _heads(out, "out", dtype, shape, device)
     lib = _lib or load()
-    a = _PROMPT_ARGS.pack(q_at, k_at, v_at, _like(cu, "cu", torch.int32, (batch + 1,), device), o_at, T, ldq, ldk, ldv, ldo,
-                          batch, hq, hk, dim, dt, dim ** -0.5 if scale is None else scale)
+    a = _PROMPT_ARGS.pack(q_at, k_at, v_at, _like(cu, "cu", _I32, (batch + 1,), device), o_at, T, ldq, ldk, ldv, ldo, batch, hq, hk,
+                          dim, dt, dim ** -0.5 if scale is None else scale)
     call = lib.w4_prompt_attention
     if flags or wait_limit_cycles:
         o = ctypes.byref(Options(flags=flags, wait_limit_cycles=wait_limit_cycles))

@@ -6,10 +6,11 @@
 // bits any other scale keeps no more bits, and a page's rows survive a growing scale unchanged but for what
 // falls below the type's range.
 //
-// A block takes a stretch of rows of one head of k or v and does the runs that begin in it, so that no plan is needed: the
-// stretch is a page long for prompts and a row for a decode step. A run's values stay in registers between the search
-// for the maximum and the conversion. Bound by memory for prompts; by latency (cu, lens, table, old scale, one after
-// another) for a decode step.
+// A block takes a stretch of rows and does the runs that begin in it, so that no plan is needed: the stretch is a page long for
+// prompts and a row for a decode step. What it has to know of a run (cu, lens, table) is read once for a few heads of k and v,
+// and while one head's maximum is found and its values converted, which stay in registers between the two, the next
+// one's are on their way. Bound by memory for prompts; by latency (cu, lens, table, old scale, one after another) for a
+// decode step.
 #include "e4m3.cuh"
 #include "gemm_common.cuh"
 #include "internal.h"
@@ -32,6 +33,7 @@ struct AppendParams {
   int64_t T, ldk, ldv, pages;
   int batch, max_pages, heads, head_dim, page;
   int stretch;  // rows of a block
+  int tasks;    // heads of k and of v that a block takes: k of heads h, h + 1, .. and v of them in turn
   FastDiv page_div, piece_div;
 };
 
@@ -44,51 +46,162 @@ __device__ __forceinline__ int scale_exponent(float m) {
 
 __device__ __forceinline__ float power_of_two(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
 
-// x / s: a product where 1 / s is exact.
-__device__ __forceinline__ float over(float x, float s, float inv, bool exact) { return exact ? x * inv : __fdiv_rn(x, s); }
-
-// The code of a value; infinities become NaN (the conversion alone would make 448 of them).
 template <int DT>
-__device__ __forceinline__ float finite_or_nan(uint32_t bits) {
-  const float x = value_f32<DT>(bits);
-  constexpr uint32_t kInf = DT == kDtypeBf16 ? 0x7F80u : 0x7C00u;
-  return (bits & 0x7FFFu) >= kInf ? __uint_as_float(0x7FC00000u) : x;
+constexpr uint32_t kInf = DT == kDtypeBf16 ? 0x7F80u : 0x7C00u;
+
+// The larger sizes of two pairs of 16-bit values, as bits (which order them; infinities and NaN are above all others).
+__device__ __forceinline__ uint32_t most2(uint32_t m, uint32_t w) { return __vmaxu2(m, w & 0x7FFF7FFFu); }
+// Of those that are finite.
+template <int DT>
+__device__ __forceinline__ uint32_t most_finite2(uint32_t m, uint32_t w) {
+  const uint32_t lo = w & 0x7FFFu, hi = w >> 16 & 0x7FFFu;
+  return __vmaxu2(m, (lo < kInf<DT> ? lo : 0u) | (hi < kInf<DT> ? hi << 16 : 0u));
 }
 
+// Codes of four words' values / s, where 1 / s = inv is exact and all values are finite.
 template <int DT>
-__device__ __forceinline__ void most_of(uint32_t w, float *m) {
-  constexpr uint32_t kInf = DT == kDtypeBf16 ? 0x7F80u : 0x7C00u;
-  const uint32_t lo = w & 0x7FFFu, hi = w >> 16 & 0x7FFFu;
-  if (lo < kInf) *m = fmaxf(*m, value_f32<DT>(lo));
-  if (hi < kInf) *m = fmaxf(*m, value_f32<DT>(hi));
+__device__ __forceinline__ uint2 codes8(const uint4 &w, float inv) {
+  const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+  uint32_t c[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    float lo, hi;
+    if (DT == kDtypeBf16) {
+      lo = __uint_as_float(v[e] << 16), hi = __uint_as_float(v[e] & 0xffff0000u);
+    } else {
+      lo = value_f32<DT>(v[e] & 0xffffu), hi = value_f32<DT>(v[e] >> 16);
+    }
+    c[e] = f32_e4m3x2(lo * inv, hi * inv);
+  }
+  return make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
+}
+// Any values, any s: infinities become NaN (the conversion alone would make 448 of them).
+template <int DT>
+__device__ __noinline__ uint2 codes8_any(uint4 w, float s) {
+  const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+  uint32_t c[4];
+  for (int e = 0; e < 4; ++e) {
+    float f[2];
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t bits = v[e] >> (16 * i) & 0xffffu;
+      f[i] = (bits & 0x7FFFu) >= kInf<DT> ? __uint_as_float(0x7FC00000u) : __fdiv_rn(value_f32<DT>(bits), s);
+    }
+    c[e] = f32_e4m3x2(f[0], f[1]);
+  }
+  return make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
+}
+
+// A run: n rows of a sequence, from `row` on, into slots off .. of page `at`.
+struct Run {
+  int row, off, n, at;
+};
+
+template <int DT>
+__device__ __forceinline__ void append_run(const AppendParams &p, const Run &run, int first, int last, uint32_t *most_of_warp) {
+  const int pieces = p.head_dim / 8;  // 16-byte pieces of a row
+  const int count = run.n * pieces;
+  auto source = [&](int task, int i) {
+    const int r = p.piece_div.div(i), h = task / 2;
+    const int64_t ld = task % 2 ? p.ldv : p.ldk;
+    return reinterpret_cast<const uint4 *>((task % 2 ? p.v : p.k) + (run.row + r) * ld + h * p.head_dim + 8 * (i - r * pieces));
+  };
+  uint4 next[kHeldPieces];
+  auto load = [&](int task) {
+#pragma unroll
+    for (int j = 0; j < kHeldPieces; ++j) {
+      const int i = j * kAppendThreads + threadIdx.x;
+      next[j] = make_uint4(0, 0, 0, 0);
+      if (i < count) next[j] = *source(task, i);
+    }
+  };
+  load(first);
+  for (int task = first; task < last; ++task) {
+    uint4 keep[kHeldPieces];
+#pragma unroll
+    for (int j = 0; j < kHeldPieces; ++j) keep[j] = next[j];
+    const int64_t ph = static_cast<int64_t>(run.at) * p.heads + task / 2;
+    float *scale = (task % 2 ? p.v_scale : p.k_scale) + ph;
+    const float old = run.off > 0 ? *scale : 0.0f;
+    if (task + 1 < last) load(task + 1);
+    uint8_t *dst = (task % 2 ? p.v_cache : p.k_cache) + ph * p.page * p.head_dim;
+    // the largest size, and whether it is finite; where it is not, the largest finite one
+    uint32_t *most = most_of_warp + task % 2 * (kAppendThreads / 32);  // (a task's are read before those of the next but one are written)
+    auto largest = [&](auto two) {
+      uint32_t m2 = 0;
+#pragma unroll
+      for (int j = 0; j < kHeldPieces; ++j) m2 = two(two(two(two(m2, keep[j].x), keep[j].y), keep[j].z), keep[j].w);
+      for (int i = kHeldPieces * kAppendThreads + threadIdx.x; i < count; i += kAppendThreads) {
+        const uint4 w = *source(task, i);
+        m2 = two(two(two(two(m2, w.x), w.y), w.z), w.w);
+      }
+      m2 = __reduce_max_sync(0xffffffffu, max(m2 & 0xffffu, m2 >> 16));
+      if (threadIdx.x % 32 == 0) most[threadIdx.x / 32] = m2;
+      __syncthreads();  // (everyone has read the old scale, too)
+      return max(max(most[0], most[1]), max(most[2], most[3]));
+    };
+    uint32_t bits = largest([](uint32_t m, uint32_t w) { return most2(m, w); });
+    const bool finite = bits < kInf<DT>;
+    if (!finite) {
+      __syncthreads();
+      bits = largest([](uint32_t m, uint32_t w) { return most_finite2<DT>(m, w); });
+    }
+    const float need = power_of_two(scale_exponent(value_f32<DT>(bits)));
+    const bool grows = !(old >= need);
+    const float s = grows ? need : old;
+    const uint32_t sb = __float_as_uint(s);
+    const bool exact = finite && (sb & 0x7FFFFFu) == 0 && s >= 0x1p-126f && s <= 0x1p126f;
+    const float inv = 1.0f / s;
+    dst += run.off * p.head_dim;
+    // (pieces of 8 codes follow one another as pieces of 8 values do)
+#pragma unroll
+    for (int j = 0; j < kHeldPieces; ++j) {
+      const int i = j * kAppendThreads + threadIdx.x;
+      if (i < count) reinterpret_cast<uint2 *>(dst)[i] = exact ? codes8<DT>(keep[j], inv) : codes8_any<DT>(keep[j], s);
+    }
+    for (int i = kHeldPieces * kAppendThreads + threadIdx.x; i < count; i += kAppendThreads)
+      reinterpret_cast<uint2 *>(dst)[i] = exact ? codes8<DT>(*source(task, i), inv) : codes8_any<DT>(*source(task, i), s);
+    dst -= run.off * p.head_dim;
+    if (run.off > 0 && grows) {
+      const float f = __fdiv_rn(old, s);
+      for (int i = threadIdx.x; i < run.off * pieces; i += kAppendThreads) {
+        uint2 *to = reinterpret_cast<uint2 *>(dst) + i;
+        const uint2 w = *to;
+        const uint32_t v[2] = {w.x, w.y};
+        uint32_t c[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const uint32_t a = e4m3x2_f16x2(v[e] & 0xffffu), d = e4m3x2_f16x2(v[e] >> 16);
+          c[e] = f32_e4m3x2(value_f32<kDtypeF16>(a & 0xffffu) * f, value_f32<kDtypeF16>(a >> 16) * f) |
+                 f32_e4m3x2(value_f32<kDtypeF16>(d & 0xffffu) * f, value_f32<kDtypeF16>(d >> 16) * f) << 16;
+        }
+        *to = make_uint2(c[0], c[1]);
+      }
+    }
+    if (threadIdx.x == 0) *scale = s;
+  }
+  __syncthreads();  // the maxima have been read
 }
 
 template <int DT>
 __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const __grid_constant__ AppendParams p) {
-  __shared__ float most_of_warp[kAppendThreads / 32];
+  __shared__ uint32_t most_of_warp[2 * (kAppendThreads / 32)];
   griddep_launch_dependents();
   griddep_wait();
-  const int h = blockIdx.y;
-  const bool of_v = blockIdx.z != 0;
-  const uint16_t *x = (of_v ? p.v : p.k) + static_cast<int64_t>(h) * p.head_dim;
-  const int64_t ld = of_v ? p.ldv : p.ldk;
-  uint8_t *cache = of_v ? p.v_cache : p.k_cache;
-  float *scales = of_v ? p.v_scale : p.k_scale;
-  const int pieces = p.head_dim / 8;  // 16-byte pieces of a row
+  const int first = blockIdx.y * p.tasks, last = min(first + p.tasks, 2 * p.heads);
   const int T = static_cast<int>(p.T);
-
   int row = static_cast<int>(blockIdx.x) * p.stretch;
   const int stop = min(row + p.stretch, T);
-  // the last sequence that begins at or before the stretch
+  // the last sequence that begins at or before the stretch: each lane looks at one of 32 that cut what is left evenly
   int b = 0;
-  for (int lo = 0, hi = p.batch - 1; lo <= hi;) {
-    const int mid = (lo + hi) / 2;
-    if (p.cu[mid] <= row) {
-      b = mid;
-      lo = mid + 1;
-    } else {
-      hi = mid - 1;
-    }
+  for (int span = p.batch; span > 1;) {
+    const int cut = (span + 31) / 32;
+    const int at = b + static_cast<int>(threadIdx.x % 32) * cut;
+    const uint32_t before = __ballot_sync(0xffffffffu, at < b + span && p.cu[at] <= row);
+    const int top = before ? 31 - __clz(before) : 0;  // (cu ascends)
+    const int end = b + span;
+    b += top * cut;
+    span = min(cut, end - b);
+    if (cut == 1) break;
   }
   for (; b < p.batch && row < stop; ++b) {
     const int begin = max(p.cu[b], 0), end = min(p.cu[b + 1], T);
@@ -102,95 +215,14 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const __grid_
         break;
       }
       const int pi = p.page_div.div(static_cast<int>(pos));
-      const int off = static_cast<int>(pos) - pi * p.page;
-      const int left = p.page - off;
-      const int n = min(left, end - row);
-      if (off != 0 && row != begin) {  // inside a run of another block
-        row += n;
-        continue;
-      }
-      const int at = p.table[static_cast<int64_t>(b) * p.max_pages + pi];
-      if (at >= 0 && at < p.pages) {
-        const int64_t ph = static_cast<int64_t>(at) * p.heads + h;
-        uint8_t *dst = cache + ph * p.page * p.head_dim;
-        const int count = n * pieces;
-        uint4 keep[kHeldPieces];
-        float m = 0.0f;
-#pragma unroll
-        for (int j = 0; j < kHeldPieces; ++j) {
-          const int i = j * kAppendThreads + threadIdx.x;
-          keep[j] = make_uint4(0, 0, 0, 0);
-          if (i < count) {
-            const int r = p.piece_div.div(i);
-            keep[j] = *reinterpret_cast<const uint4 *>(x + static_cast<int64_t>(row + r) * ld + 8 * (i - r * pieces));
-          }
-        }
-#pragma unroll
-        for (int j = 0; j < kHeldPieces; ++j) {
-          most_of<DT>(keep[j].x, &m);
-          most_of<DT>(keep[j].y, &m);
-          most_of<DT>(keep[j].z, &m);
-          most_of<DT>(keep[j].w, &m);
-        }
-        for (int i = kHeldPieces * kAppendThreads + threadIdx.x; i < count; i += kAppendThreads) {
-          const int r = p.piece_div.div(i);
-          const uint4 w = *reinterpret_cast<const uint4 *>(x + static_cast<int64_t>(row + r) * ld + 8 * (i - r * pieces));
-          most_of<DT>(w.x, &m);
-          most_of<DT>(w.y, &m);
-          most_of<DT>(w.z, &m);
-          most_of<DT>(w.w, &m);
-        }
-        // (positive floats are ordered as their bits)
-        m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));
-        if (threadIdx.x % 32 == 0) most_of_warp[threadIdx.x / 32] = m;
-        const float old = off > 0 ? scales[ph] : 0.0f;
-        __syncthreads();
-        m = fmaxf(fmaxf(most_of_warp[0], most_of_warp[1]), fmaxf(most_of_warp[2], most_of_warp[3]));
-        const float need = power_of_two(scale_exponent(m));
-        const bool grows = !(old >= need);
-        const float s = grows ? need : old;
-        __syncthreads();  // everyone has read the old scale and the maxima
-        const uint32_t sb = __float_as_uint(s);
-        const bool exact = (sb & 0x7FFFFFu) == 0 && s >= 0x1p-126f && s <= 0x1p126f;
-        const float inv = 1.0f / s;
-        auto put = [&](int i, const uint4 &w) {
-          const uint32_t v[4] = {w.x, w.y, w.z, w.w};
-          uint32_t c[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            c[e] = f32_e4m3x2(over(finite_or_nan<DT>(v[e] & 0xffffu), s, inv, exact), over(finite_or_nan<DT>(v[e] >> 16), s, inv, exact));
-          const int r = p.piece_div.div(i);
-          *reinterpret_cast<uint2 *>(dst + static_cast<int64_t>(off + r) * p.head_dim + 8 * (i - r * pieces)) =
-              make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
-        };
-#pragma unroll
-        for (int j = 0; j < kHeldPieces; ++j) {
-          const int i = j * kAppendThreads + threadIdx.x;
-          if (i < count) put(i, keep[j]);
-        }
-        for (int i = kHeldPieces * kAppendThreads + threadIdx.x; i < count; i += kAppendThreads) {
-          const int r = p.piece_div.div(i);
-          put(i, *reinterpret_cast<const uint4 *>(x + static_cast<int64_t>(row + r) * ld + 8 * (i - r * pieces)));
-        }
-        if (off > 0 && grows) {
-          const float f = __fdiv_rn(old, s);
-          for (int i = threadIdx.x; i < off * p.head_dim / 8; i += kAppendThreads) {
-            uint2 *to = reinterpret_cast<uint2 *>(dst) + i;
-            const uint2 w = *to;
-            const uint32_t v[2] = {w.x, w.y};
-            uint32_t c[2];
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const uint32_t a = e4m3x2_f16x2(v[e] & 0xffffu), d = e4m3x2_f16x2(v[e] >> 16);
-              c[e] = f32_e4m3x2(value_f32<kDtypeF16>(a & 0xffffu) * f, value_f32<kDtypeF16>(a >> 16) * f) |
-                     f32_e4m3x2(value_f32<kDtypeF16>(d & 0xffffu) * f, value_f32<kDtypeF16>(d >> 16) * f) << 16;
-            }
-            *to = make_uint2(c[0], c[1]);
-          }
-        }
-        if (threadIdx.x == 0) scales[ph] = s;
-      }
-      row += n;
+      Run run;
+      run.row = row;
+      run.off = static_cast<int>(pos) - pi * p.page;
+      run.n = min(p.page - run.off, end - row);
+      row += run.n;
+      if (run.off != 0 && run.row != begin) continue;  // inside a run of another block
+      run.at = p.table[static_cast<int64_t>(b) * p.max_pages + pi];
+      if (run.at >= 0 && run.at < p.pages) append_run<DT>(p, run, first, last, most_of_warp);
     }
   }
 }
@@ -219,10 +251,13 @@ cudaError_t launch_kv_append(const KvAppendArgs &a, int num_sms, cudaStream_t st
   p.page = a.page;
   p.page_div = make_fastdiv(static_cast<uint32_t>(a.page));
   p.piece_div = make_fastdiv(static_cast<uint32_t>(a.head_dim / 8));
+  // a page's rows where there are enough of them to fill the device with blocks of a few heads each, else fewer
   p.stretch = 1;
   while (p.stretch < a.page && cdiv(a.T, p.stretch) * a.heads * 2 > 16 * num_sms) p.stretch *= 2;
+  p.tasks = 1;
+  while (p.tasks < 8 && cdiv(a.T, p.stretch) * cdiv(2 * a.heads, 2 * p.tasks) >= 8 * num_sms) p.tasks *= 2;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(cdiv(a.T, p.stretch)), static_cast<unsigned>(a.heads), 2);
+  cfg.gridDim = dim3(static_cast<unsigned>(cdiv(a.T, p.stretch)), static_cast<unsigned>(cdiv(2 * a.heads, p.tasks)));
   cfg.blockDim = dim3(kAppendThreads);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];

@@ -8,10 +8,16 @@
 // 1. A block forms freq / 2 pi modulo 1 once, in 64 bits, as a 64-bit fraction of a turn; the product with the
 // position in wrapping integer arithmetic is the turn, exact to position * 2^-64 and the fraction's own rounding.
 //
-// A lane holds 8 consecutive values (16 bytes) of a head, a power of two of lanes a head; the sum of squares and the pairs'
-// other halves (the same place of another lane, unless neighbours are paired) go by shuffles, so that a value is read and
-// written once and a call may run in place. Sines and cosines of a row are made once a block and shared by its heads.
-// Bound by memory for many rows, by latency for few.
+// A lane holds 8 values of a head, a power of two of lanes a head: four pairs' both halves (values 4 i .. 4 i + 3 and those
+// half the rotation further, or 8 neighbours where neighbours are paired), or 8 neighbours past the rotation. So a pair is
+// turned within a lane, and the sines and cosines that a lane needs are the same for all heads of a row: they stay in
+// registers. Only the sum of squares goes by shuffles. A value is read and written once, by the same lane, and a call may run in
+// place. Sines and cosines of a block's rows are made once and shared through shared memory, as are the weights in fp32.
+// Bound by memory for many rows, by latency for few. What keeps it from being bound by instructions is that all that differs
+// between calls but not within one (neighbours paired or not, norms or not) is a template's: chosen by the lane it was 307
+// instructions for 8 values, and 181 us for 16384 rows of 72 heads of 128.
+#include <type_traits>
+
 #include "gemm_common.cuh"
 #include "internal.h"
 #include "mma.cuh"
@@ -42,8 +48,8 @@ struct RopeParams {
 };
 
 template <int DT>
-__device__ __forceinline__ void unpack8(const uint4 &v, float (&f)[8]) {
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+__device__ __forceinline__ void unpack8(const uint2 &lo, const uint2 &hi, float (&f)[8]) {
+  const uint32_t w[4] = {lo.x, lo.y, hi.x, hi.y};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     f[2 * i] = value_f32<DT>(w[i] & 0xffffu);
@@ -51,94 +57,107 @@ __device__ __forceinline__ void unpack8(const uint4 &v, float (&f)[8]) {
   }
 }
 
-// LG: lanes a head.
-template <int DT, int LG>
+// LG: lanes a head. PAIRED: neighbours are paired.
+template <int DT, int LG, bool NORM, bool PAIRED>
 __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeParams p) {
-  extern __shared__ float2 turn[];  // [rows][half]: cosine, sine
+  extern __shared__ __align__(16) uint8_t smem[];
+  float *weights = reinterpret_cast<float *>(smem);                         // [q, k][LG][8] in the lanes' order
+  float *cosines = weights + (NORM ? 16 * LG : 0), *sines = cosines + p.rows * p.half;  // [rows][half] each
+  long long *fractions = reinterpret_cast<long long *>(sines + p.rows * p.half);        // [half], of a turn a position
   griddep_launch_dependents();
   griddep_wait();
   const int64_t row0 = static_cast<int64_t>(blockIdx.x / p.head_parts) * p.rows;
   const int part = blockIdx.x % p.head_parts;
   const int rows = static_cast<int>(min(static_cast<int64_t>(p.rows), p.T - row0));
-  // thread i % half's frequency, for the rows i / half, ...
-  for (int i = threadIdx.x; i < p.half * rows; i += kRopeThreads) {
-    const int f = i % p.half, r = i / p.half;
+  const int lane = threadIdx.x % LG;
+  const int group = threadIdx.x / LG;
+  // the lane's values: four from at0, four from at1
+  const bool inside = 8 * lane < p.head_dim, turned = 8 * lane < 2 * p.half;
+  const bool apart = turned && !PAIRED;
+  const int at0 = apart ? 4 * lane : 8 * lane, at1 = apart ? p.half + 4 * lane : 8 * lane + 4;
+  if (NORM && threadIdx.x < 2 * LG) {
+    const uint16_t *w = threadIdx.x < LG ? p.q_weight : p.k_weight;
+    uint2 lo = make_uint2(0, 0), hi = lo;
+    if (w && inside) lo = *reinterpret_cast<const uint2 *>(w + at0), hi = *reinterpret_cast<const uint2 *>(w + at1);
+    float f[8];
+    unpack8<DT>(lo, hi, f);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) weights[8 * threadIdx.x + e] = f[e];
+  }
+  for (int f = threadIdx.x; f < p.half; f += kRopeThreads) {
     const double turns = static_cast<double>(p.freqs[f]) * 0.15915494309189533577;  // 1 / 2 pi
-    const long long fraction = __double2ll_rn((turns - rint(turns)) * 18446744073709551616.0);
+    fractions[f] = __double2ll_rn((turns - rint(turns)) * 18446744073709551616.0);
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < p.half * rows; i += kRopeThreads) {
+    const int r = i / p.half, f = i - r * p.half;
     const int axis = (f >= p.section_end[0]) + (f >= p.section_end[1]) + (f >= p.section_end[2]);
-    const int32_t pos = p.positions[axis * p.T + row0 + r];
-    const long long at = static_cast<long long>(static_cast<unsigned long long>(fraction) * static_cast<unsigned long long>(static_cast<long long>(pos)));
-    float2 cs;
-    sincospif(__ll2float_rn(at) * 0x1p-63f, &cs.y, &cs.x);  // half turns
-    turn[i] = cs;
+    const long long pos = p.positions[axis * p.T + row0 + r];
+    const long long at = static_cast<long long>(static_cast<unsigned long long>(fractions[f]) * static_cast<unsigned long long>(pos));
+    sincospif(__ll2float_rn(at) * 0x1p-63f, &sines[i], &cosines[i]);  // half turns
   }
   __syncthreads();
 
-  const int lane = threadIdx.x % LG;
-  const int group = threadIdx.x / LG;
-  const bool inside = 8 * lane < p.head_dim;
   const float inv_dim = 1.0f / static_cast<float>(p.head_dim);
-  const int heads_here = p.head_step * p.head_parts;  // heads between a group's
-  // where this lane's values lie in the rotation: all of a lane's are on one side (half is a multiple of 8)
-  const bool turned = 8 * lane < 2 * p.half;
-  const bool upper = 8 * lane >= p.half;
-  const int other = upper ? lane - p.half / 8 : lane + p.half / 8;
+  const int step = p.head_step * p.head_parts;  // heads between a group's
+  const int first = part * p.head_step + group;
   for (int r = 0; r < rows; ++r) {
     const int64_t row = row0 + r;
-    for (int h = part * p.head_step + group; h - group < p.heads; h += heads_here) {
-      const bool live = inside && h < p.heads;
-      const bool of_q = h < p.q_heads;
-      const uint16_t *weight = of_q ? p.q_weight : p.k_weight;
-      const int hh = of_q ? h : h - p.q_heads;
-      uint4 raw = make_uint4(0, 0, 0, 0);
-      if (live) raw = *reinterpret_cast<const uint4 *>((of_q ? p.q + row * p.ldq : p.k + row * p.ldk) + hh * p.head_dim + 8 * lane);
+    const uint16_t *qx = p.q + row * p.ldq, *kx = p.k + row * p.ldk - p.q_heads * p.head_dim;
+    uint16_t *qy = p.q_out + row * p.ldqo, *ky = p.k_out + row * p.ldko - p.q_heads * p.head_dim;
+    float c[4], s[4];
+    if (turned) {
+      const float4 c4 = *reinterpret_cast<const float4 *>(cosines + r * p.half + 4 * lane);
+      const float4 s4 = *reinterpret_cast<const float4 *>(sines + r * p.half + 4 * lane);
+      c[0] = c4.x, c[1] = c4.y, c[2] = c4.z, c[3] = c4.w;
+      s[0] = s4.x, s[1] = s4.y, s[2] = s4.z, s[3] = s4.w;
+    }
+    auto load = [&](int h, uint2 *lo, uint2 *hi) {
+      *lo = *hi = make_uint2(0, 0);
+      if (inside && h < p.heads) {
+        const uint16_t *x = (h < p.q_heads ? qx : kx) + h * p.head_dim;
+        *lo = *reinterpret_cast<const uint2 *>(x + at0);
+        *hi = *reinterpret_cast<const uint2 *>(x + at1);
+      }
+    };
+    // the next head's while one is worked on (a lane writes only what it has read: in place too)
+    uint2 lo, hi, next_lo, next_hi;
+    load(first, &next_lo, &next_hi);
+    for (int h = first; h - group < p.heads; h += step) {
+      lo = next_lo, hi = next_hi;
+      load(h + step, &next_lo, &next_hi);
       float x[8];
-      unpack8<DT>(raw, x);
-      if (p.q_weight || p.k_weight) {  // (the same for the whole warp)
+      unpack8<DT>(lo, hi, x);
+      const bool of_q = h < p.q_heads;
+      if (NORM) {
         float sum = 0.0f;
 #pragma unroll
         for (int e = 0; e < 8; ++e) sum = fmaf(x[e], x[e], sum);
 #pragma unroll
-        for (int s = LG / 2; s > 0; s /= 2) sum += __shfl_xor_sync(kAll, sum, s, LG);
-        if (weight) {
-          float w[8];
-          uint4 wr = make_uint4(0, 0, 0, 0);
-          if (live) wr = *reinterpret_cast<const uint4 *>(weight + 8 * lane);
-          unpack8<DT>(wr, w);
+        for (int i = LG / 2; i > 0; i /= 2) sum += __shfl_xor_sync(kAll, sum, i, LG);
+        if (of_q ? p.q_weight != nullptr : p.k_weight != nullptr) {
           const float scale = rsqrtf(fmaf(sum, inv_dim, p.eps));
+          const float4 *w = reinterpret_cast<const float4 *>(weights + (of_q ? 0 : 8 * LG) + 8 * lane);
+          const float4 w0 = w[0], w1 = w[1];
+          const float f[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
 #pragma unroll
-          for (int e = 0; e < 8; ++e) x[e] = x[e] * scale * w[e];
+          for (int e = 0; e < 8; ++e) x[e] = x[e] * scale * f[e];
         }
       }
-      if (p.half) {
-        const float2 *cs = turn + r * p.half;
-        if (p.interleaved) {
-          if (turned) {
+      if (turned) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float2 c = cs[4 * lane + e];
-              const float a = x[2 * e], b = x[2 * e + 1];
-              x[2 * e] = a * c.x - b * c.y;
-              x[2 * e + 1] = fmaf(b, c.x, a * c.y);
-            }
-          }
-        } else {
-          float y[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) y[e] = __shfl_sync(kAll, x[e], other, LG);
-          if (turned) {
-            const float2 *mine = cs + 8 * (upper ? other : lane);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const float2 c = mine[e];
-              x[e] = upper ? fmaf(x[e], c.x, y[e] * c.y) : x[e] * c.x - y[e] * c.y;
-            }
-          }
+        for (int e = 0; e < 4; ++e) {
+          const int i = PAIRED ? 2 * e : e, j = PAIRED ? 2 * e + 1 : 4 + e;
+          const float a = x[i], b = x[j];
+          x[i] = a * c[e] - b * s[e];
+          x[j] = fmaf(b, c[e], a * s[e]);
         }
       }
-      if (live)
-        *reinterpret_cast<uint4 *>((of_q ? p.q_out + row * p.ldqo : p.k_out + row * p.ldko) + hh * p.head_dim + 8 * lane) =
-            make_uint4(out_bits2<DT>(x[0], x[1]), out_bits2<DT>(x[2], x[3]), out_bits2<DT>(x[4], x[5]), out_bits2<DT>(x[6], x[7]));
+      if (inside && h < p.heads) {
+        uint16_t *y = (of_q ? qy : ky) + h * p.head_dim;
+        *reinterpret_cast<uint2 *>(y + at0) = make_uint2(out_bits2<DT>(x[0], x[1]), out_bits2<DT>(x[2], x[3]));
+        *reinterpret_cast<uint2 *>(y + at1) = make_uint2(out_bits2<DT>(x[4], x[5]), out_bits2<DT>(x[6], x[7]));
+      }
     }
   }
 }
@@ -156,16 +175,22 @@ cudaError_t launch_dim(RopeParams p, int num_sms, cudaStream_t stream) {
   while (p.rows < 8 && p.T > static_cast<int64_t>(16) * num_sms * p.rows) p.rows *= 2;
   const int64_t blocks = cdiv(p.T, p.rows) * p.head_parts;
   if (blocks > 0x7FFFFFFF) return cudaErrorInvalidValue;
-  const int smem = p.rows * p.half * static_cast<int>(sizeof(float2));
+  const bool norm = p.q_weight || p.k_weight;
+  const int smem = (norm ? 16 * lg * static_cast<int>(sizeof(float)) : 0) + p.half * (p.rows * 2 * static_cast<int>(sizeof(float)) + static_cast<int>(sizeof(long long)));
   auto go = [&](auto kern) { return launch_programmatic(kern, static_cast<int>(blocks), kRopeThreads, smem, stream, p); };
-  switch (lg) {
-    case 1: return go(rope_kernel<DT, 1>);
-    case 2: return go(rope_kernel<DT, 2>);
-    case 4: return go(rope_kernel<DT, 4>);
-    case 8: return go(rope_kernel<DT, 8>);
-    case 16: return go(rope_kernel<DT, 16>);
-    default: return go(rope_kernel<DT, 32>);
-  }
+  auto pick = [&](auto n, auto paired) {
+    constexpr bool N = decltype(n)::value, P = decltype(paired)::value;
+    switch (lg) {
+      case 1: return go(rope_kernel<DT, 1, N, P>);
+      case 2: return go(rope_kernel<DT, 2, N, P>);
+      case 4: return go(rope_kernel<DT, 4, N, P>);
+      case 8: return go(rope_kernel<DT, 8, N, P>);
+      case 16: return go(rope_kernel<DT, 16, N, P>);
+      default: return go(rope_kernel<DT, 32, N, P>);
+    }
+  };
+  if (norm) return p.interleaved ? pick(std::true_type{}, std::true_type{}) : pick(std::true_type{}, std::false_type{});
+  return p.interleaved ? pick(std::false_type{}, std::true_type{}) : pick(std::false_type{}, std::false_type{});
 }
 
 }  // namespace
