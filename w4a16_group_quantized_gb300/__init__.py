@@ -683,6 +683,11 @@ def _heads(t: torch.Tensor, name: str, dtype, shape, device: int):
     heads one after another and lie evenly apart."""
     if t.dtype is not dtype or t.shape != shape or t.get_device() != device:
         raise ValueError(f"{name} must be {dtype} {list(shape)} on cuda:{device}")
+    return _heads_at(t, name, shape)
+
+
+def _heads_at(t: torch.Tensor, name: str, shape):
+    """_heads without its first checks, for the tensor that the others are checked against."""
     heads, dim = shape[-2:]
     width = heads * dim
     if t.is_contiguous():
@@ -719,15 +724,15 @@ def w4_qk_norm_rope(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Te
     The first 2 * len(freqs) values of a head are turned by positions * freqs (int32 [T] and fp32): value i with i +
     len(freqs), or neighbours (``interleaved``). With positions [axes, T] (up to 4: time, height, width) ``sections``
     says how many of the frequencies, in order, go by each axis. freqs None: no rotation. There is no gradient."""
-    dt = _DTYPES.get(q.dtype)
-    if dt is None or q.dim() != 3 or not q.is_cuda:
+    dtype, shape, device = q.dtype, q.shape, q.get_device()
+    dt = _DTYPES.get(dtype)
+    if dt is None or len(shape) != 3 or device < 0:
         raise ValueError("q must be a fp16 or bf16 CUDA tensor [T, heads, head_dim]")
     if (q.requires_grad or (k is not None and k.requires_grad) or (q_weight is not None and q_weight.requires_grad) or
             (k_weight is not None and k_weight.requires_grad)):
         _no_gradient("w4_qk_norm_rope")
-    dtype, device, shape = q.dtype, q.get_device(), q.shape
     T, hq, dim = shape
-    q_at, ldq = _heads(q, "q", dtype, shape, device)
+    q_at, ldq = _heads_at(q, "q", shape)
     if q_out is None:
         q_out = _empty(shape, dtype, q.device, stream)
         qo_at, ldqo = q_out.data_ptr(), hq * dim
@@ -738,36 +743,35 @@ def w4_qk_norm_rope(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Te
             raise ValueError("k_out and k_weight go with k")
         hk = k_at = ldk = ko_at = ldko = 0
     else:
-        if k.dim() != 3:
-            raise ValueError("k must be [T, heads, head_dim]")
-        hk = k.shape[1]
-        shape = (T, hk, dim)
-        k_at, ldk = _heads(k, "k", dtype, shape, device)
+        shape = k.shape
+        if len(shape) != 3 or shape[0] != T or shape[2] != dim or k.dtype is not dtype or k.get_device() != device:
+            raise ValueError(f"k must be {dtype} [{T}, heads, {dim}] on cuda:{device}")
+        hk = shape[1]
+        k_at, ldk = _heads_at(k, "k", shape)
         if k_out is None:
             k_out = _empty(shape, dtype, q.device, stream)
             ko_at, ldko = k_out.data_ptr(), hk * dim
         else:
             ko_at, ldko = _heads(k_out, "k_out", dtype, shape, device)
-    part = [0, 0, 0, 0]
+    part = 0, 0, 0, 0
     if freqs is None:
         if positions is not None or sections is not None:
             raise ValueError("positions and sections go with freqs")
         half = axes = p_at = f_at = 0
     else:
-        half = freqs.shape[0]
-        if positions is None or positions.dim() not in (1, 2):
-            raise ValueError("positions must be int32 [T] or [axes, T]")
-        axes = 1 if positions.dim() == 1 else positions.shape[0]
-        if sections is None:
-            if positions.dim() != 1:
-                raise ValueError("positions [axes, T] need sections")
-            part[0] = half
-        else:
-            if positions.dim() != 2 or len(sections) != axes or axes > 4:
-                raise ValueError("positions must be [axes, T], and sections have an entry for each of up to 4 axes")
-            part[:axes] = sections
+        half = freqs.numel()
         f_at = _like(freqs, "freqs", _F32, (half,), device)
-        p_at = _like(positions, "positions", _I32, (T,) if sections is None else (axes, T), device)
+        if positions is None:
+            raise ValueError("freqs go with positions")
+        if sections is None:
+            axes, part = 1, (half, 0, 0, 0)
+            p_at = _like(positions, "positions", _I32, (T,), device)
+        else:
+            axes = len(sections)
+            if not 1 <= axes <= 4:
+                raise ValueError("sections must have an entry for each of up to 4 axes")
+            part = (*sections, 0, 0, 0)[:4]
+            p_at = _like(positions, "positions", _I32, (axes, T), device)
     a = _ROPE_ARGS.pack(q_at, k_at, qo_at, ko_at, p_at, f_at,
                         0 if q_weight is None else _like(q_weight, "q_weight", dtype, (dim,), device),
                         0 if k_weight is None else _like(k_weight, "k_weight", dtype, (dim,), device),
@@ -808,16 +812,16 @@ def w4_kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cach
     code * scale. table int32 [batch, max_pages] lists each sequence's pages (-1: none; nothing is written there), cu int32
     [batch + 1] ascends, lens int32 [batch] is what the cache holds before the call (the caller adds the new rows to it). A page that
     gets rows must belong to one sequence only. See w4_kv_append in include/w4a16.h for the scales."""
-    dt = _DTYPES.get(k.dtype)
-    if dt is None or k.dim() != 3 or not k.is_cuda or lens.dim() != 1:
-        raise ValueError("k must be a fp16 or bf16 CUDA tensor [T, heads, head_dim] and lens [batch]")
+    dtype, shape, device = k.dtype, k.shape, k.get_device()
+    dt = _DTYPES.get(dtype)
+    if dt is None or len(shape) != 3 or device < 0:
+        raise ValueError("k must be a fp16 or bf16 CUDA tensor [T, heads, head_dim]")
     if k.requires_grad or v.requires_grad:
         _no_gradient("w4_kv_append")
-    shape, dtype = k.shape, k.dtype
     T, heads, dim = shape
-    batch, device = lens.shape[0], k.get_device()
+    batch = lens.numel()
     pages, _, page, max_pages = _cache(k_cache, v_cache, k_scale, v_scale, table, batch, heads, dim, device)
-    k_at, ldk = _heads(k, "k", dtype, shape, device)
+    k_at, ldk = _heads_at(k, "k", shape)
     v_at, ldv = _heads(v, "v", dtype, shape, device)
     a = _KV_APPEND_ARGS.pack(k_at, v_at, k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
                              table.data_ptr(), _like(cu, "cu", _I32, (batch + 1,), device),
@@ -838,9 +842,9 @@ def w4_kv_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     [batch, n, q_heads, head_dim] or, for n = 1, [batch, q_heads, head_dim]; the result has q's shape. lens int32 [batch] counts
     the n positions in: query j sees positions up to lens[i] - n + j, and gives zeros where there is none. Query head h
     reads key head h // (q_heads // k_heads). ``scale``: of the products (None: 1 / sqrt(head_dim)). There is no gradient."""
-    dtype, shape = q.dtype, q.shape
+    dtype, shape, device = q.dtype, q.shape, q.get_device()
     dt, dims = _DTYPES.get(dtype), len(shape)
-    if dt is None or not 3 <= dims <= 4 or not q.is_cuda:
+    if dt is None or not 3 <= dims <= 4 or device < 0:
         raise ValueError("q must be a fp16 or bf16 CUDA tensor [batch, n, heads, head_dim] or [batch, heads, head_dim]")
     if q.requires_grad:
         _no_gradient("w4_kv_attention")
@@ -849,9 +853,8 @@ def w4_kv_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
         n = 1
     else:
         batch, n, hq, dim = shape
-    device = q.get_device()
     pages, hk, page, max_pages = _cache(k_cache, v_cache, k_scale, v_scale, table, batch, None, dim, device)
-    q_at, ldq = _heads(q, "q", dtype, shape, device)
+    q_at, ldq = _heads_at(q, "q", shape)
     if out is None:
         out = _empty(shape, dtype, q.device, stream)
         o_at, ldo = out.data_ptr(), hq * dim
@@ -869,6 +872,9 @@ def w4_prompt_attention_workspace_bytes(T: int, batch: int, q_heads: int) -> int
     return int(load().w4_prompt_attention_workspace_bytes(T, batch, q_heads))
 
 
+_prompt_bytes = functools.lru_cache(maxsize=1024)(w4_prompt_attention_workspace_bytes)
+
+
 def w4_prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu: torch.Tensor, *, scale: float | None = None,
                         out: torch.Tensor | None = None, workspace=None, stream=None, flags: int = 0,
                         wait_limit_cycles: int = 0) -> torch.Tensor:
@@ -878,17 +884,19 @@ def w4_prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu: t
     ``out``. ``scale``: of the products (None: 1 / sqrt(head_dim)). There is no gradient. A wait that gave up inside the
     kernel (out is then undefined) can be asked for with w4_last_device_error(workspace), so only where one is given;
     ``wait_limit_cycles``: after how many clock cycles it gives up (0: about 1.5 s); ``flags``: FLAG_TEST_TIMEOUT, in tests."""
-    dtype, shape = q.dtype, q.shape
+    dtype, shape, device = q.dtype, q.shape, q.get_device()
     dt = _DTYPES.get(dtype)
-    if dt is None or len(shape) != 3 or k.dim() != 3 or not q.is_cuda or cu.dim() != 1 or cu.shape[0] < 1:
+    k_shape, batch = k.shape, cu.numel() - 1
+    if dt is None or len(shape) != 3 or len(k_shape) != 3 or device < 0 or batch < 0:
         raise ValueError("q must be a fp16 or bf16 CUDA tensor [T, heads, head_dim], k alike and cu [batch + 1]")
     if q.requires_grad or k.requires_grad or v.requires_grad:
         _no_gradient("w4_prompt_attention")
     T, hq, dim = shape
-    hk, batch, device = k.shape[1], cu.shape[0] - 1, q.get_device()
-    k_shape = (T, hk, dim)
-    q_at, ldq = _heads(q, "q", dtype, shape, device)
-    k_at, ldk = _heads(k, "k", dtype, k_shape, device)
+    hk = k_shape[1]
+    if k_shape[0] != T or k_shape[2] != dim or k.dtype is not dtype or k.get_device() != device:
+        raise ValueError(f"k must be {dtype} [{T}, heads, {dim}] on cuda:{device}")
+    q_at, ldq = _heads_at(q, "q", shape)
+    k_at, ldk = _heads_at(k, "k", k_shape)
     v_at, ldv = _heads(v, "v", dtype, k_shape, device)
     if out is None:
         out = _empty(shape, dtype, q.device, stream)
@@ -904,5 +912,5 @@ def w4_prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu: t
 
         def call(args, ws, nbytes, handle):
             return lib.w4_prompt_attention_opts(args, ws, nbytes, o, handle)
-    _run_with(call, a, workspace, lambda: w4_prompt_attention_workspace_bytes(T, batch, hq), device, stream, "w4_prompt_attention")
+    _run_with(call, a, workspace, lambda: _prompt_bytes(T, batch, hq), device, stream, "w4_prompt_attention")
     return out

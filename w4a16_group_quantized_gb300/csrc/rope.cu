@@ -10,12 +10,14 @@
 //
 // A lane holds 8 values of a head, a power of two of lanes a head: four pairs' both halves (values 4 i .. 4 i + 3 and those
 // half the rotation further, or 8 neighbours where neighbours are paired), or 8 neighbours past the rotation. So a pair is
-// turned within a lane, and the sines and cosines that a lane needs are the same for all heads of a row: they stay in
-// registers. Only the sum of squares goes by shuffles. A value is read and written once, by the same lane, and a call may run in
-// place. Sines and cosines of a block's rows are made once and shared through shared memory, as are the weights in fp32.
-// Bound by memory for many rows, by latency for few. What keeps it from being bound by instructions is that all that differs
-// between calls but not within one (neighbours paired or not, norms or not) is a template's: chosen by the lane it was 307
-// instructions for 8 values, and 181 us for 16384 rows of 72 heads of 128.
+// turned within a lane, and only the sum of squares goes by shuffles. A value is read and written once, by the same lane, and a
+// call may run in place. A block makes the sines and cosines of its rows once, in shared memory; then a lane stays with
+// a head for all of the block's rows, four rows' loads at a time: its weights stay in registers, and from row to row one
+// offset moves.
+// Bound by memory for many rows, by latency for few; for many rows it was bound by instructions until all that differs between
+// calls but not within one (neighbours paired or not, norms or not) became a template's, and the rows the inner loop (16384
+// rows of 72 heads of 128 with norms: 307 instructions for 8 values, 181 us; 181 and 125 us with heads inside; now 100 us).
+#include <algorithm>
 #include <type_traits>
 
 #include "gemm_common.cuh"
@@ -28,7 +30,8 @@ namespace {
 
 using namespace detail;
 
-constexpr int kRopeThreads = 256;
+constexpr int kRopeThreads = 128;
+constexpr int kBatch = 4;  // rows whose loads are on their way together
 constexpr uint32_t kAll = 0xffffffffu;
 
 struct RopeParams {
@@ -43,47 +46,65 @@ struct RopeParams {
   int interleaved;
   float eps;
   int rows;        // of a block
-  int head_step;   // heads of a block in a pass
+  int head_step;   // heads of a block in a turn
+  int q_turned;    // q's heads in whole turns
   int head_parts;  // blocks that share a row's heads
 };
 
+// Two fp32 values side by side.
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+  return d;
+}
+__device__ __forceinline__ float2 unpair(uint64_t v) {
+  float2 f;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
+  return f;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t sub2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+
 template <int DT>
-__device__ __forceinline__ void unpack8(const uint2 &lo, const uint2 &hi, float (&f)[8]) {
-  const uint32_t w[4] = {lo.x, lo.y, hi.x, hi.y};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f[2 * i] = value_f32<DT>(w[i] & 0xffffu);
-    f[2 * i + 1] = value_f32<DT>(w[i] >> 16);
-  }
+__device__ __forceinline__ uint64_t unpack2(uint32_t w) {
+  if (DT == kDtypeBf16) return pair(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+  return pair(value_f32<DT>(w & 0xffffu), value_f32<DT>(w >> 16));
+}
+template <int DT>
+__device__ __forceinline__ uint32_t pack2(uint64_t v) {
+  const float2 f = unpair(v);
+  uint32_t d;
+  if (DT == kDtypeBf16)
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(f.y), "f"(f.x));
+  else
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(f.y), "f"(f.x));
+  return d;
 }
 
 // LG: lanes a head. PAIRED: neighbours are paired.
 template <int DT, int LG, bool NORM, bool PAIRED>
 __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeParams p) {
   extern __shared__ __align__(16) uint8_t smem[];
-  float *weights = reinterpret_cast<float *>(smem);                         // [q, k][LG][8] in the lanes' order
-  float *cosines = weights + (NORM ? 16 * LG : 0), *sines = cosines + p.rows * p.half;  // [rows][half] each
+  float *cosines = reinterpret_cast<float *>(smem), *sines = cosines + p.rows * p.half;  // [rows][half] each
   long long *fractions = reinterpret_cast<long long *>(sines + p.rows * p.half);        // [half], of a turn a position
   griddep_launch_dependents();
   griddep_wait();
   const int64_t row0 = static_cast<int64_t>(blockIdx.x / p.head_parts) * p.rows;
   const int part = blockIdx.x % p.head_parts;
   const int rows = static_cast<int>(min(static_cast<int64_t>(p.rows), p.T - row0));
-  const int lane = threadIdx.x % LG;
-  const int group = threadIdx.x / LG;
-  // the lane's values: four from at0, four from at1
-  const bool inside = 8 * lane < p.head_dim, turned = 8 * lane < 2 * p.half;
-  const bool apart = turned && !PAIRED;
-  const int at0 = apart ? 4 * lane : 8 * lane, at1 = apart ? p.half + 4 * lane : 8 * lane + 4;
-  if (NORM && threadIdx.x < 2 * LG) {
-    const uint16_t *w = threadIdx.x < LG ? p.q_weight : p.k_weight;
-    uint2 lo = make_uint2(0, 0), hi = lo;
-    if (w && inside) lo = *reinterpret_cast<const uint2 *>(w + at0), hi = *reinterpret_cast<const uint2 *>(w + at1);
-    float f[8];
-    unpack8<DT>(lo, hi, f);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) weights[8 * threadIdx.x + e] = f[e];
-  }
   for (int f = threadIdx.x; f < p.half; f += kRopeThreads) {
     const double turns = static_cast<double>(p.freqs[f]) * 0.15915494309189533577;  // 1 / 2 pi
     fractions[f] = __double2ll_rn((turns - rint(turns)) * 18446744073709551616.0);
@@ -98,65 +119,80 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
   }
   __syncthreads();
 
+  const int lane = threadIdx.x % LG;
+  const int group = threadIdx.x / LG;
+  // the lane's values: four from at0, four from at1
+  const bool inside = 8 * lane < p.head_dim, turned = 8 * lane < 2 * p.half;
+  const bool apart = turned && !PAIRED;
+  const int at0 = apart ? 4 * lane : 8 * lane, at1 = apart ? p.half + 4 * lane : 8 * lane + 4;
   const float inv_dim = 1.0f / static_cast<float>(p.head_dim);
-  const int step = p.head_step * p.head_parts;  // heads between a group's
-  const int first = part * p.head_step + group;
-  for (int r = 0; r < rows; ++r) {
-    const int64_t row = row0 + r;
-    const uint16_t *qx = p.q + row * p.ldq, *kx = p.k + row * p.ldk - p.q_heads * p.head_dim;
-    uint16_t *qy = p.q_out + row * p.ldqo, *ky = p.k_out + row * p.ldko - p.q_heads * p.head_dim;
-    float c[4], s[4];
-    if (turned) {
-      const float4 c4 = *reinterpret_cast<const float4 *>(cosines + r * p.half + 4 * lane);
-      const float4 s4 = *reinterpret_cast<const float4 *>(sines + r * p.half + 4 * lane);
-      c[0] = c4.x, c[1] = c4.y, c[2] = c4.z, c[3] = c4.w;
-      s[0] = s4.x, s[1] = s4.y, s[2] = s4.z, s[3] = s4.w;
+  // q's heads, then k's, a head a group and turn
+  for (int base = part * p.head_step; base < p.q_turned + p.heads - p.q_heads; base += p.head_step * p.head_parts) {
+    const bool of_q = base < p.q_turned;  // (q's turns are whole ones: q_turned is a multiple of head_step)
+    const int h = of_q ? base + group : base - p.q_turned + group;
+    const bool live = inside && h < (of_q ? p.q_heads : p.heads - p.q_heads);
+    const int64_t ld = of_q ? p.ldq : p.ldk, ldo = of_q ? p.ldqo : p.ldko;
+    const char *x = reinterpret_cast<const char *>((of_q ? p.q : p.k) + row0 * ld);
+    char *y = reinterpret_cast<char *>((of_q ? p.q_out : p.k_out) + row0 * ldo);
+    const uint32_t hop = static_cast<uint32_t>(2 * ld), hop_out = static_cast<uint32_t>(2 * ldo);  // (a block's rows span less than 2^31 bytes)
+    uint32_t at = 2u * (h * p.head_dim + at0), at_out = at;
+    const uint32_t apart_by = 2u * (at1 - at0);
+    const uint16_t *weight = of_q ? p.q_weight : p.k_weight;
+    uint64_t w[4] = {};
+    if (NORM && weight && live) {
+      const uint2 lo = *reinterpret_cast<const uint2 *>(weight + at0), hi = *reinterpret_cast<const uint2 *>(weight + at1);
+      w[0] = unpack2<DT>(lo.x), w[1] = unpack2<DT>(lo.y), w[2] = unpack2<DT>(hi.x), w[3] = unpack2<DT>(hi.y);
     }
-    auto load = [&](int h, uint2 *lo, uint2 *hi) {
-      *lo = *hi = make_uint2(0, 0);
-      if (inside && h < p.heads) {
-        const uint16_t *x = (h < p.q_heads ? qx : kx) + h * p.head_dim;
-        *lo = *reinterpret_cast<const uint2 *>(x + at0);
-        *hi = *reinterpret_cast<const uint2 *>(x + at1);
+    const float *cs = cosines + 4 * lane, *sn = sines + 4 * lane;
+    for (int r = 0; r < rows; r += kBatch) {
+      uint2 lo[kBatch], hi[kBatch];
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        lo[i] = hi[i] = make_uint2(0, 0);
+        if (live && r + i < rows) {
+          lo[i] = *reinterpret_cast<const uint2 *>(x + at);
+          hi[i] = *reinterpret_cast<const uint2 *>(x + at + apart_by);
+        }
+        at += hop;
       }
-    };
-    // the next head's while one is worked on (a lane writes only what it has read: in place too)
-    uint2 lo, hi, next_lo, next_hi;
-    load(first, &next_lo, &next_hi);
-    for (int h = first; h - group < p.heads; h += step) {
-      lo = next_lo, hi = next_hi;
-      load(h + step, &next_lo, &next_hi);
-      float x[8];
-      unpack8<DT>(lo, hi, x);
-      const bool of_q = h < p.q_heads;
-      if (NORM) {
-        float sum = 0.0f;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) sum = fmaf(x[e], x[e], sum);
+      for (int i = 0; i < kBatch; ++i) {
+        if (r + i >= rows) break;
+        uint64_t v[4] = {unpack2<DT>(lo[i].x), unpack2<DT>(lo[i].y), unpack2<DT>(hi[i].x), unpack2<DT>(hi[i].y)};
+        if (NORM && weight) {
+          const float2 sums = unpair(fma2(v[3], v[3], fma2(v[2], v[2], fma2(v[1], v[1], mul2(v[0], v[0])))));
+          float sum = sums.x + sums.y;
 #pragma unroll
-        for (int i = LG / 2; i > 0; i /= 2) sum += __shfl_xor_sync(kAll, sum, i, LG);
-        if (of_q ? p.q_weight != nullptr : p.k_weight != nullptr) {
+          for (int e = LG / 2; e > 0; e /= 2) sum += __shfl_xor_sync(kAll, sum, e, LG);
           const float scale = rsqrtf(fmaf(sum, inv_dim, p.eps));
-          const float4 *w = reinterpret_cast<const float4 *>(weights + (of_q ? 0 : 8 * LG) + 8 * lane);
-          const float4 w0 = w[0], w1 = w[1];
-          const float f[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+          const uint64_t scale2 = pair(scale, scale);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) x[e] = x[e] * scale * f[e];
+          for (int e = 0; e < 4; ++e) v[e] = mul2(mul2(v[e], scale2), w[e]);
         }
-      }
-      if (turned) {
+        if (turned) {
+          const ulonglong2 c = *reinterpret_cast<const ulonglong2 *>(cs), s = *reinterpret_cast<const ulonglong2 *>(sn);
+          if (PAIRED) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int i = PAIRED ? 2 * e : e, j = PAIRED ? 2 * e + 1 : 4 + e;
-          const float a = x[i], b = x[j];
-          x[i] = a * c[e] - b * s[e];
-          x[j] = fmaf(b, c[e], a * s[e]);
+            for (int e = 0; e < 4; ++e) {
+              const float2 ab = unpair(v[e]), cc = unpair(e < 2 ? c.x : c.y), ss = unpair(e < 2 ? s.x : s.y);
+              const float ce = e % 2 ? cc.y : cc.x, se = e % 2 ? ss.y : ss.x;
+              v[e] = pair(ab.x * ce - ab.y * se, fmaf(ab.y, ce, ab.x * se));
+            }
+          } else {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const uint64_t a = v[e], b = v[2 + e], ce = e ? c.y : c.x, se = e ? s.y : s.x;
+              v[e] = sub2(mul2(a, ce), mul2(b, se));
+              v[2 + e] = fma2(b, ce, mul2(a, se));
+            }
+          }
         }
-      }
-      if (inside && h < p.heads) {
-        uint16_t *y = (of_q ? qy : ky) + h * p.head_dim;
-        *reinterpret_cast<uint2 *>(y + at0) = make_uint2(out_bits2<DT>(x[0], x[1]), out_bits2<DT>(x[2], x[3]));
-        *reinterpret_cast<uint2 *>(y + at1) = make_uint2(out_bits2<DT>(x[4], x[5]), out_bits2<DT>(x[6], x[7]));
+        cs += p.half, sn += p.half;
+        if (live) {
+          *reinterpret_cast<uint2 *>(y + at_out) = make_uint2(pack2<DT>(v[0]), pack2<DT>(v[1]));
+          *reinterpret_cast<uint2 *>(y + at_out + apart_by) = make_uint2(pack2<DT>(v[2]), pack2<DT>(v[3]));
+        }
+        at_out += hop_out;
       }
     }
   }
@@ -167,16 +203,18 @@ cudaError_t launch_dim(RopeParams p, int num_sms, cudaStream_t stream) {
   int lg = 1;
   while (8 * lg < p.head_dim) lg *= 2;
   p.head_step = kRopeThreads / lg;
-  const int passes = static_cast<int>(cdiv(p.heads, p.head_step));
-  // few rows: a row's heads go to blocks of their own; many: a block takes a few rows
+  const int q_turns = static_cast<int>(cdiv(p.q_heads, p.head_step)), turns = q_turns + static_cast<int>(cdiv(p.heads - p.q_heads, p.head_step));
+  p.q_turned = q_turns * p.head_step;
+  // few rows: a row's heads go to blocks of their own; many: a block takes a few rows (whose offsets fit 32 bits)
   p.head_parts = 1;
-  while (p.head_parts < passes && p.T * p.head_parts < 4 * num_sms) p.head_parts *= 2;
+  while (p.head_parts < turns && p.T * p.head_parts < 4 * num_sms) p.head_parts *= 2;
+  const int64_t widest = std::max(std::max(p.ldq, p.ldqo), std::max(p.ldk, p.ldko));
   p.rows = 1;
-  while (p.rows < 8 && p.T > static_cast<int64_t>(16) * num_sms * p.rows) p.rows *= 2;
+  while (p.rows < 8 && p.T > static_cast<int64_t>(16) * num_sms * p.rows && 4 * p.rows * widest < (int64_t{1} << 30)) p.rows *= 2;
   const int64_t blocks = cdiv(p.T, p.rows) * p.head_parts;
   if (blocks > 0x7FFFFFFF) return cudaErrorInvalidValue;
   const bool norm = p.q_weight || p.k_weight;
-  const int smem = (norm ? 16 * lg * static_cast<int>(sizeof(float)) : 0) + p.half * (p.rows * 2 * static_cast<int>(sizeof(float)) + static_cast<int>(sizeof(long long)));
+  const int smem = p.half * (p.rows * 2 * static_cast<int>(sizeof(float)) + static_cast<int>(sizeof(long long)));
   auto go = [&](auto kern) { return launch_programmatic(kern, static_cast<int>(blocks), kRopeThreads, smem, stream, p); };
   auto pick = [&](auto n, auto paired) {
     constexpr bool N = decltype(n)::value, P = decltype(paired)::value;
