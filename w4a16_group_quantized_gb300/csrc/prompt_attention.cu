@@ -10,10 +10,12 @@
 // step. Tensor memory holds for each tile the scores S (128 x 128 fp32, one row a lane), whose columns the 16-bit weights P
 // then take as the second product's A operand, and O (128 x head_dim fp32): all 512 columns. Roles (12 warps):
 //   2 x 4 softmax warps   a thread a row of its tile: S to registers, maximum, weights, P; at the end O / l to memory
-//   1 issue warp          S = Q K^T and O += P V of the two tiles in turn, so that one tile's softmax runs beside
-//                         the other's products
+//   2 issue warps         one a tile: O += P V, the first half of the keys as soon as their weights are there, then the next
+//                         S = Q K^T. One tile's softmax runs beside the other's products, and one warp's waits (some 130
+//                         cycles each, even when over) beside the other's: with one warp for both tiles a step took 2825
+//                         cycles, 550 of them its waits
 //   1 copy warp           Q, then K and V of each step through a ring
-//   2 looking warps       see the tile's last V (the one with rows that its first queries do not see)
+//   1 looking warp        sees the tiles' last V (the ones with rows that their first queries do not see)
 // V is used as it stands, an MN-major operand.
 //
 // Rows that a query does not see have weight 0, but 0 * NaN is NaN. Rows behind the sequence's end are made 0 in shared
@@ -117,6 +119,11 @@ template <int R>
 __device__ __forceinline__ void regs_up() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R));
 }
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
 constexpr int kRegsSoftmax = 208, kRegsOthers = 80;
 static_assert(2 * kRegsSoftmax + kRegsOthers <= 3 * 168, "the registers that the block was launched with (168 a thread)");
 
@@ -205,7 +212,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   using C = PromptCfg<D>;
   constexpr int S = C::kStages;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t q_bar[2], full_bar[S], free_bar[S], s_bar[2], p_bar[2], o_bar[2], last_bar[2], look_bar[2], drain_bar;
+  __shared__ __align__(8) uint64_t q_bar[2], full_bar[S], free_bar[S], s_bar[2], p_bar[2][2], o_bar[2], last_bar[2], look_bar[2], drain_bar[2];
   __shared__ uint32_t tmem_sh, abort_sh;
   __shared__ uint32_t odd_sh[2];  // V of the tile's last step holds what is not finite
   __shared__ Work work_sh;
@@ -229,22 +236,23 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&q_bar[i]), 1 + (i == 0 ? p.test_extra : 0));
       mbar_init(smem_u32(&s_bar[i]), 1);
-      mbar_init(smem_u32(&p_bar[i]), 4);
+      mbar_init(smem_u32(&p_bar[i][0]), 4);
+      mbar_init(smem_u32(&p_bar[i][1]), 4);
+      mbar_init(smem_u32(&drain_bar[i]), 1);
       mbar_init(smem_u32(&o_bar[i]), 1);
       mbar_init(smem_u32(&last_bar[i]), 1);
       mbar_init(smem_u32(&look_bar[i]), 1);
       odd_sh[i] = 0;
     }
-    for (int i = 0; i < S; ++i) {
-      mbar_init(smem_u32(&full_bar[i]), 1);
-      mbar_init(smem_u32(&free_bar[i]), 1);
-    }
-    mbar_init(smem_u32(&drain_bar), 1);
+    for (int i = 0; i < S; ++i) mbar_init(smem_u32(&full_bar[i]), 1);
     abort_sh = 0;
-    fence_mbar_init();
   }
   __syncthreads();
   if (!any_sh) return;
+  if (threadIdx.x == 32) {  // (the issue warps of the tiles that there are)
+    for (int i = 0; i < S; ++i) mbar_init(smem_u32(&free_bar[i]), work_sh.len > work_sh.row0 + kTile ? 2 : 1);
+    fence_mbar_init();
+  }
   if (warp == 8) {
     tmem_alloc(smem_u32(&tmem_sh), 512);
     tmem_relinquish();
@@ -268,7 +276,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     const int r = warp % 4 * 32 + lane;  // the thread's row of the tile
     const uint32_t lanes = static_cast<uint32_t>(warp % 4 * 32) << 16;
     const uint32_t s_at = tmem + lanes + tile * kTile, o_at = tmem + lanes + C::kO + tile * D;
-    const uint32_t s_full = smem_u32(&s_bar[tile]), p_full = smem_u32(&p_bar[tile]);
+    const uint32_t s_full = smem_u32(&s_bar[tile]), p_full = smem_u32(&p_bar[tile][0]);
     const int steps = tile == 0 ? n0 : two ? n0 + 1 : 0;
     const uint64_t scale2 = pack2(p.scale, p.scale);
     float m = -INFINITY;
@@ -294,9 +302,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       for (int c = 0; c < 4; ++c) {
         top[c] = __uint_as_float(s[c][0]);
 #pragma unroll
-        for (int j = 1; j < 32; ++j) top[c] = fmaxf(top[c], __uint_as_float(s[c][j]));
+        for (int j = 1; j + 1 < 32; j += 2) top[c] = max3(top[c], __uint_as_float(s[c][j]), __uint_as_float(s[c][j + 1]));
+        top[c] = fmaxf(top[c], __uint_as_float(s[c][31]));
       }
-      const float now = fmaxf(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])), m);
+      const float now = max3(max3(top[0], top[1], top[2]), top[3], m);
       if (i == 0) {
         m = now;
       } else if (__any_sync(kAll, (now - m) * p.scale > kSlack)) {
@@ -332,14 +341,14 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           w2[j] = weights2<DT>(a, b);
         }
         tmem_st_32x32b_x32(s_at + 16 * c, w2);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_full + 4 * c);  // (c 0, 2: the two barriers)
       }
       float a, b;
       unpack2(add2(sum[0], sum[1]), &a, &b);
       l += a + b;
-      tmem_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(p_full);
     }
     if (ok && steps > 0) ok = warp_wait(smem_u32(&o_bar[tile]), 0, abort_flag, p.err, p.wait_limit);
     if (ok && steps > 0) ok = warp_wait(smem_u32(&look_bar[tile]), 0, abort_flag, p.err, p.wait_limit);
@@ -375,90 +384,72 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     }
   } else {
     regs_down<kRegsOthers>();
-    if (warp == 8) {
+    if (warp < 10) {
       // -------------------------------------------------------- products
-      const uint32_t qk = idesc_f16_f32(kTile, kTile, DT == kDtypeBf16);
-      const uint32_t pv = idesc_f16_f32(kTile, D, DT == kDtypeBf16, true);
-      auto scores = [&](int tile, uint32_t stage) {
+      const int tile = warp - 8;
+      const int steps = tile == 0 ? n0 : two ? n : 0;
+      constexpr uint32_t qk = idesc_f16_f32(kTile, kTile, DT == kDtypeBf16), pv = idesc_f16_f32(kTile, D, DT == kDtypeBf16, true);
+      const uint32_t s_at = tmem + tile * kTile, o_at = tmem + C::kO + tile * D;
+      const uint32_t s_full = smem_u32(&s_bar[tile]), p_full = smem_u32(&p_bar[tile][0]);
+      auto scores = [&](uint32_t stage) {
         const uint64_t a = sw128_kmajor_desc(smem_base + tile * C::kTileBytes), b = sw128_kmajor_desc(ring + stage * C::kTileBytes);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           const uint64_t step = static_cast<uint64_t>(kk / 4 * (C::kHalf >> 4) + kk % 4 * 2);
-          mma_f16_ss(tmem + tile * kTile, a + step, b + step, qk, kk > 0);
+          mma_f16_ss(s_at, a + step, b + step, qk, kk > 0);
         }
+        mma_commit(s_full);
       };
-      auto values = [&](int tile, uint32_t stage, bool first) {
+      auto values = [&](uint32_t stage, int half, bool first) {
         const uint64_t b = sw128_mnmajor_desc(ring + stage * C::kTileBytes, C::kHalf);
 #pragma unroll
-        for (int kk = 0; kk < kTile / 16; ++kk)
-          mma_f16_ts(tmem + C::kO + tile * D, tmem + tile * kTile + kk * 8, b + static_cast<uint64_t>(kk * (2048 >> 4)), pv,
-                     !first || kk > 0);
+        for (int kk = half * 4; kk < half * 4 + 4; ++kk)
+          mma_f16_ts(o_at, s_at + kk * 8, b + static_cast<uint64_t>(kk * (2048 >> 4)), pv, !first || kk > 0);
       };
-      auto stage_of = [](int item) { return static_cast<uint32_t>(item % S); };
       auto landed = [&](int item) {
-        return warp_wait(full0 + 8 * stage_of(item), (item / S) & 1, abort_flag, p.err, p.wait_limit);
+        return warp_wait(full0 + 8 * static_cast<uint32_t>(item % S), (item / S) & 1, abort_flag, p.err, p.wait_limit);
       };
-      bool ok = warp_wait(smem_u32(&q_bar[0]), 0, abort_flag, p.err, p.wait_limit) && landed(0);
+      bool ok = steps > 0 && warp_wait(smem_u32(&q_bar[tile]), 0, abort_flag, p.err, p.wait_limit) && landed(0);
       if (ok) {
         tc_fence_after();
         if (elect_one()) {
-          scores(0, 0);
-          mma_commit(smem_u32(&s_bar[0]));
+          scores(0);
+          mma_commit(free0);
         }
         __syncwarp();
       }
-      if (ok && two) {
-        ok = warp_wait(smem_u32(&q_bar[1]), 0, abort_flag, p.err, p.wait_limit);
-        if (ok) {
-          tc_fence_after();
-          if (elect_one()) {
-            scores(1, 0);
-            mma_commit(smem_u32(&s_bar[1]));
-          }
-          __syncwarp();
-        }
-      }
-      if (ok && elect_one()) mma_commit(free0);
-      __syncwarp();
-      for (int i = 0; ok && i < n; ++i) {
-        const uint32_t vs = stage_of(2 * i + 1), ks = stage_of(2 * i + 2);
-        // (the looking warps have waited for the last steps' V, and may have changed it)
+      for (int i = 0; ok && i < steps; ++i) {
+        const uint32_t vs = static_cast<uint32_t>((2 * i + 1) % S), ks = static_cast<uint32_t>((2 * i + 2) % S);
+        // (the looking warp has waited for the last steps' V, and may have changed it)
         ok = i < n0 - 1 ? landed(2 * i + 1) : warp_wait(smem_u32(&look_bar[i - (n0 - 1)]), 0, abort_flag, p.err, p.wait_limit);
-        if (ok && i + 1 < n) ok = landed(2 * i + 2);
+        if (ok && i + 1 < steps) ok = landed(2 * i + 2);
+        if (ok) ok = warp_wait(p_full, i & 1, abort_flag, p.err, p.wait_limit);
         if (!ok) break;
-#pragma unroll
-        for (int tile = 0; tile < 2; ++tile) {
-          const int steps = tile == 0 ? n0 : n;
-          if (tile == 1 && !two) break;
-          if (i >= steps) continue;
-          ok = warp_wait(smem_u32(&p_bar[tile]), i & 1, abort_flag, p.err, p.wait_limit);
-          if (!ok) break;
-          tc_fence_after();
-          if (elect_one()) {
-            values(tile, vs, i == 0);
-            if (i + 1 < steps) {
-              scores(tile, ks);
-              mma_commit(smem_u32(&s_bar[tile]));
-            } else {
-              mma_commit(smem_u32(&o_bar[tile]));
-            }
-          }
-          __syncwarp();
-        }
+        tc_fence_after();
+        if (elect_one()) values(vs, 0, i == 0);
+        __syncwarp();
+        ok = warp_wait(p_full + 8, i & 1, abort_flag, p.err, p.wait_limit);
         if (!ok) break;
+        tc_fence_after();
         if (elect_one()) {
+          values(vs, 1, false);
           mma_commit(free0 + 8 * vs);
-          if (i + 1 < n) mma_commit(free0 + 8 * ks);
+          if (i + 1 < steps) {
+            scores(ks);
+            mma_commit(free0 + 8 * ks);
+          } else {
+            mma_commit(smem_u32(&o_bar[tile]));
+          }
         }
         __syncwarp();
       }
       const bool aborted = __any_sync(kAll, *abort_flag != 0);
       if (aborted) {
-        if (elect_one()) mma_commit(smem_u32(&drain_bar));
+        if (elect_one()) mma_commit(smem_u32(&drain_bar[tile]));
         __syncwarp();
-        drain_wait(smem_u32(&drain_bar), 0);
+        drain_wait(smem_u32(&drain_bar[tile]), 0);
       }
-    } else if (warp == 9) {
+    } else if (warp == 10) {
       // ---------------------------------------------------------- copies
       auto load = [&](const CUtensorMap *map, uint32_t to, int head, int row, uint32_t bar) {
         mbar_arrive_expect_tx(bar, C::kTileBytes);
@@ -483,34 +474,31 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       }
     } else {
       // ------------------------------------- the last V of each tile (its place is not used again)
-      const int tile = warp - 10;
-      if (tile == 0 || two) {
+      for (int tile = 0; tile < (two ? 2 : 1); ++tile) {
         const int step = n0 - 1 + tile;
-        const int item = 2 * step + 1;
-        const uint32_t stage = static_cast<uint32_t>(item % S);
-        if (warp_wait(smem_u32(&last_bar[tile]), 0, abort_flag, p.err, p.wait_limit)) {
-          const int live = min(w.len - step * kTile, kTile);  // rows of the sequence in it
-          const uint32_t at = ring + stage * C::kTileBytes;
-          bool odd = false;
-          constexpr uint32_t kInf = DT == kDtypeBf16 ? 0x7F80u : 0x7C00u;
-          for (int i = lane; i < C::kTileBytes / 16; i += 32) {
-            const int row = i / 8 % kTile;
-            if (row < live) {
-              const uint4 x = lds128(at + 16 * i);
-              const uint32_t v[4] = {x.x, x.y, x.z, x.w};
+        const uint32_t stage = static_cast<uint32_t>((2 * step + 1) % S);
+        if (!warp_wait(smem_u32(&last_bar[tile]), 0, abort_flag, p.err, p.wait_limit)) break;
+        const int live = min(w.len - step * kTile, kTile);  // rows of the sequence in it
+        const uint32_t at = ring + stage * C::kTileBytes;
+        bool odd = false;
+        constexpr uint32_t kInf = DT == kDtypeBf16 ? 0x7F80u : 0x7C00u;
+        for (int i = lane; i < C::kTileBytes / 16; i += 32) {
+          const int row = i / 8 % kTile;
+          if (row < live) {
+            const uint4 x = lds128(at + 16 * i);
+            const uint32_t v[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-              for (int e = 0; e < 4; ++e) odd |= (v[e] & kInf) == kInf || (v[e] >> 16 & kInf) == kInf;
-            } else {
-              asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(at + 16 * i), "r"(0u) : "memory");
-            }
+            for (int e = 0; e < 4; ++e) odd |= (v[e] & kInf) == kInf || (v[e] >> 16 & kInf) == kInf;
+          } else {
+            asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(at + 16 * i), "r"(0u) : "memory");
           }
-          odd = __any_sync(kAll, odd);
-          fence_proxy_async_shared();
-          __syncwarp();
-          if (lane == 0) {
-            odd_sh[tile] = odd;
-            mbar_arrive(smem_u32(&look_bar[tile]));
-          }
+        }
+        odd = __any_sync(kAll, odd);
+        fence_proxy_async_shared();
+        __syncwarp();
+        if (lane == 0) {
+          odd_sh[tile] = odd;
+          mbar_arrive(smem_u32(&look_bar[tile]));
         }
       }
     }
