@@ -297,18 +297,50 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           for (int j = 0; j < 32; ++j)
             if (32 * c + j > r) s[c][j] = 0xFF800000u;  // -inf
       }
-      float top[4];
+      // the first half's weights by the maximum in use, and the newest maximum beside them: for most steps the one in use stays
+      auto row_top = [&]() {
+        float top[4];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        top[c] = __uint_as_float(s[c][0]);
+        for (int c = 0; c < 4; ++c) {
+          top[c] = __uint_as_float(s[c][0]);
 #pragma unroll
-        for (int j = 1; j + 1 < 32; j += 2) top[c] = max3(top[c], __uint_as_float(s[c][j]), __uint_as_float(s[c][j + 1]));
-        top[c] = fmaxf(top[c], __uint_as_float(s[c][31]));
-      }
-      const float now = max3(max3(top[0], top[1], top[2]), top[3], m);
-      if (i == 0) {
-        m = now;
-      } else if (__any_sync(kAll, (now - m) * p.scale > kSlack)) {
+          for (int j = 1; j + 1 < 32; j += 2) top[c] = max3(top[c], __uint_as_float(s[c][j]), __uint_as_float(s[c][j + 1]));
+          top[c] = fmaxf(top[c], __uint_as_float(s[c][31]));
+        }
+        return max3(max3(top[0], top[1], top[2]), top[3], m);
+      };
+      uint64_t off2, sum[2];
+      uint32_t w2[32];
+      auto weights = [&](int c) {
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+          const uint64_t e = fma2(pack2(__uint_as_float(s[c + j / 16][2 * (j % 16)]), __uint_as_float(s[c + j / 16][2 * (j % 16) + 1])),
+                                  scale2, off2);
+          float a, b;
+          unpack2(e, &a, &b);
+          a = ex2(a);
+          b = ex2(b);
+          sum[j & 1] = add2(sum[j & 1], pack2(a, b));
+          w2[j] = weights2<DT>(a, b);
+        }
+      };
+      auto first_half = [&]() {
+        const float off = m == -INFINITY ? 0.0f : -m * p.scale;
+        off2 = pack2(off, off);
+        sum[0] = sum[1] = 0ull;
+        weights(0);
+      };
+      auto hand_over = [&](int c) {
+        tmem_st_32x32b_x32(s_at + 16 * c, w2);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_full + 4 * c);  // (c 0, 2: the two barriers)
+      };
+      if (i == 0) m = row_top();
+      first_half();
+      const float now = row_top();
+      if (__any_sync(kAll, (now - m) * p.scale > kSlack)) {
         // (the step before this one's S is complete, and with it O)
         const float alpha = now == m ? 1.0f : ex2((m - now) * p.scale);
         m = now;
@@ -322,30 +354,11 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha);
           tmem_st_32x32b_x16(o_at + 16 * c, o);
         }
+        first_half();
       }
-      const float off = m == -INFINITY ? 0.0f : -m * p.scale;
-      const uint64_t off2 = pack2(off, off);
-      uint64_t sum[2] = {0ull, 0ull};
-#pragma unroll
-      for (int c = 0; c < 4; c += 2) {
-        uint32_t w2[32];
-#pragma unroll
-        for (int j = 0; j < 32; ++j) {
-          const uint64_t e = fma2(pack2(__uint_as_float(s[c + j / 16][2 * (j % 16)]), __uint_as_float(s[c + j / 16][2 * (j % 16) + 1])),
-                                  scale2, off2);
-          float a, b;
-          unpack2(e, &a, &b);
-          a = ex2(a);
-          b = ex2(b);
-          sum[j & 1] = add2(sum[j & 1], pack2(a, b));
-          w2[j] = weights2<DT>(a, b);
-        }
-        tmem_st_32x32b_x32(s_at + 16 * c, w2);
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(p_full + 4 * c);  // (c 0, 2: the two barriers)
-      }
+      hand_over(0);
+      weights(2);
+      hand_over(2);
       float a, b;
       unpack2(add2(sum[0], sum[1]), &a, &b);
       l += a + b;
@@ -480,20 +493,20 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         if (!warp_wait(smem_u32(&last_bar[tile]), 0, abort_flag, p.err, p.wait_limit)) break;
         const int live = min(w.len - step * kTile, kTile);  // rows of the sequence in it
         const uint32_t at = ring + stage * C::kTileBytes;
-        bool odd = false;
-        constexpr uint32_t kInf = DT == kDtypeBf16 ? 0x7F80u : 0x7C00u;
-        for (int i = lane; i < C::kTileBytes / 16; i += 32) {
-          const int row = i / 8 % kTile;
-          if (row < live) {
-            const uint4 x = lds128(at + 16 * i);
-            const uint32_t v[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) odd |= (v[e] & kInf) == kInf || (v[e] >> 16 & kInf) == kInf;
-          } else {
-            asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(at + 16 * i), "r"(0u) : "memory");
+        // an exponent of all ones: one more carries into the sign's place
+        constexpr uint32_t kInf = DT == kDtypeBf16 ? 0x7F807F80u : 0x7C007C00u, kOne = DT == kDtypeBf16 ? 0x00800080u : 0x04000400u;
+        uint32_t carries = 0;
+        for (int h = 0; h < D / 64; ++h) {
+          const uint32_t end = at + h * C::kHalf + live * 128, stop = at + (h + 1) * C::kHalf;
+          uint32_t i = at + h * C::kHalf + 16 * lane;
+#pragma unroll 8
+          for (; i < end; i += 512) {
+            const uint4 x = lds128(i);
+            carries |= ((x.x & kInf) + kOne) | ((x.y & kInf) + kOne) | ((x.z & kInf) + kOne) | ((x.w & kInf) + kOne);
           }
+          for (; i < stop; i += 512) asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(i), "r"(0u) : "memory");
         }
-        odd = __any_sync(kAll, odd);
+        const bool odd = __any_sync(kAll, (carries & 0x80008000u) != 0);
         fence_proxy_async_shared();
         __syncwarp();
         if (lane == 0) {
