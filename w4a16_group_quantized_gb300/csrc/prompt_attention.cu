@@ -6,11 +6,13 @@
 // weights are simply larger than 1 (fp32 sums, and 16-bit weights keep their relative precision), so that O is
 // rescaled a few times in a row's life instead of at each step.
 //
-// A block takes 256 rows of one sequence and head as two tiles of 128, which share the keys and values that it copies, 128 rows a
-// step. Tensor memory holds for each tile the scores S (128 x 128 fp32, one row a lane), whose columns the 16-bit weights P
-// then take as the second product's A operand, and O (128 x head_dim fp32): all 512 columns. Roles (12 warps):
-//   2 x 4 softmax warps   a thread a row of its tile: S to registers, maximum, weights, P; at the end O / l to memory
-//   2 issue warps         one a tile: O += P V, the first half of the keys as soon as their weights are there, then the next
+// A block takes 128 or 256 rows of one sequence and head, as one tile or two, which share the keys and values that it copies,
+// 128 rows a step. Tensor memory holds for each tile the scores S (128 x 128 fp32, one row a lane), whose columns the 16-bit
+// weights P then take as the second product's A operand, and O (128 x head_dim fp32): 256 columns a tile. Blocks of one tile go
+// two to an SM, where one's beginning and end run beside the other's products; blocks of two read keys and values half as
+// often. Roles (8 or 12 warps):
+//   4 softmax warps a tile  a thread a row: S to registers, maximum, weights, P; at the end O / l to memory
+//   1 issue warp a tile   O += P V, the first half of the keys as soon as their weights are there, then the next
 //                         S = Q K^T. One tile's softmax runs beside the other's products, and one warp's waits (some 130
 //                         cycles each, even when over) beside the other's: with one warp for both tiles a step took 2825
 //                         cycles, 550 of them its waits
@@ -37,7 +39,6 @@ using namespace detail;
 
 constexpr uint32_t kAll = 0xffffffffu;
 constexpr int kTile = 128;         // query rows of a tile, and keys of a step
-constexpr int kPromptThreads = 384;
 constexpr float kSlack = 8.0f;     // how far a score may pass the maximum in use (log2 of the weight)
 
 struct PromptParams {
@@ -52,14 +53,19 @@ struct PromptParams {
   int test_extra;
 };
 
-// D: head_dim rounded up to 64 or 128.
-template <int D>
+// D: head_dim rounded up to 64 or 128. TILES: of a block; blocks of one go two to an SM.
+template <int D, int TILES>
 struct PromptCfg {
+  static constexpr int kThreads = (TILES + 1) * 128;
   static constexpr int kHalf = kTile * 128;           // 64 values of 128 rows
   static constexpr int kTileBytes = kHalf * (D / 64);  // 128 rows of q, k or v
-  static constexpr int kStages = D == 128 ? 5 : 10;
-  static constexpr int kSmem = (2 + kStages) * kTileBytes + 1024;
-  static constexpr uint32_t kO = 2 * kTile;            // O's first column; O of the second tile D further
+  static constexpr int kStages = TILES == 2 ? (D == 128 ? 5 : 10) : (D == 128 ? 2 : 5);
+  static constexpr int kSmem = (TILES + kStages) * kTileBytes + 1024;
+  static constexpr uint32_t kO = TILES * kTile;        // O's first column; O of the second tile D further
+  static constexpr uint32_t kColumns = TILES == 2 ? 512 : 256;
+  static_assert(kO + TILES * D <= kColumns, "tensor memory");
+  static constexpr int kRegsLaunch = TILES == 2 ? 168 : 128, kRegsSoftmax = 208, kRegsOthers = TILES == 2 ? 80 : 48;
+  static_assert(TILES * kRegsSoftmax + kRegsOthers <= (TILES + 1) * kRegsLaunch, "the registers that the block was launched with");
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -124,9 +130,6 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
 }
-constexpr int kRegsSoftmax = 208, kRegsOthers = 80;
-static_assert(2 * kRegsSoftmax + kRegsOthers <= 3 * 168, "the registers that the block was launched with (168 a thread)");
-
 __device__ __forceinline__ uint64_t pack2(float lo, float hi) {
   uint64_t d;
   asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
@@ -161,39 +164,53 @@ struct Work {
   int head;
 };
 
-// The block's part: sequences have ceil(len / 256) blocks a head, the last rows, which see most, first. One warp.
-__device__ __forceinline__ bool find_work(const PromptParams &p, Work *w) {
+// The block's part: sequences have a block a head for every `rows` rows. The blocks that see most come first, whatever their
+// sequence: block m of a sequence (rows m * rows ..) comes before block m - 1 of any. Up to and with block m there are
+// sum max(0, blocks - m) of them over the sequences, so that m is found by halving. One warp.
+__device__ __forceinline__ bool find_work(const PromptParams &p, int rows, Work *w) {
   const int lane = threadIdx.x % 32;
-  auto count = [&](int b, int *begin, int *len) {
-    *begin = *len = 0;
+  int begin, len;
+  auto count = [&](int b) {
+    begin = len = 0;
     if (b < p.batch) {
-      *begin = min(max(p.cu[b], 0), p.T);
-      *len = max(min(p.cu[b + 1], p.T) - *begin, 0);
+      begin = min(max(p.cu[b], 0), p.T);
+      len = max(min(p.cu[b + 1], p.T) - begin, 0);
     }
-    return (*len + 2 * kTile - 1) / (2 * kTile);
+    return (len + rows - 1) / rows;
   };
-  int total = 0, begin, len;
-  for (int b0 = 0; b0 < p.batch; b0 += 32) total += static_cast<int>(__reduce_add_sync(kAll, count(b0 + lane, &begin, &len)));
-  int at = total - 1 - static_cast<int>(blockIdx.x) / p.q_heads;
+  const int first = count(lane);
+  auto all_from = [&](int m) {  // blocks m and up of all sequences
+    int sum = max(first - m, 0);
+    for (int b = 32; b < p.batch; b += 32) sum += max(count(b + lane) - m, 0);
+    return static_cast<int>(__reduce_add_sync(kAll, sum));
+  };
+  int at = static_cast<int>(blockIdx.x) / p.q_heads;
   w->head = blockIdx.x % p.q_heads;
-  if (at < 0) return false;
-  for (int b0 = 0; b0 < p.batch; b0 += 32) {
-    const int n = count(b0 + lane, &begin, &len);
-    int sum = n;  // up to this lane
-#pragma unroll
-    for (int i = 1; i < 32; i *= 2) {
-      const int x = __shfl_up_sync(kAll, sum, i);
-      if (lane >= i) sum += x;
+  if (at >= all_from(0)) return false;
+  int most = first;
+  for (int b = 32; b < p.batch; b += 32) most = max(most, count(b + lane));
+  most = __reduce_max_sync(kAll, most);
+  int m = 0;  // the largest with all_from(m) > at
+  for (int lo = 1, hi = most - 1; lo <= hi;) {
+    const int mid = (lo + hi) / 2;
+    if (all_from(mid) > at) {
+      m = mid;
+      lo = mid + 1;
+    } else {
+      hi = mid - 1;
     }
-    const uint32_t past = __ballot_sync(kAll, sum > at);
-    if (past) {
-      const int from = __ffs(past) - 1;
+  }
+  at -= all_from(m + 1);
+  for (int b = 0; b < p.batch; b += 32) {
+    const uint32_t has = __ballot_sync(kAll, count(b + lane) > m);
+    if (at < __popc(has)) {
+      const int from = __fns(has, 0, at + 1);
       w->begin = __shfl_sync(kAll, begin, from);
       w->len = __shfl_sync(kAll, len, from);
-      w->row0 = (at - __shfl_sync(kAll, sum - n, from)) * 2 * kTile;
+      w->row0 = m * rows;
       return true;
     }
-    at -= __shfl_sync(kAll, sum, 31);
+    at -= __popc(has);
   }
   return false;
 }
@@ -205,14 +222,14 @@ __device__ __forceinline__ void let_copies_land() {
   while (clock_cycles() - t0 < 20ull * 1000 * 1000) __nanosleep(1000);
 }
 
-template <int DT, int D>
-__global__ void __launch_bounds__(kPromptThreads, 1)
+template <int DT, int D, int TILES>
+__global__ void __launch_bounds__(PromptCfg<D, TILES>::kThreads, 3 - TILES)
     prompt_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map,
                             const __grid_constant__ CUtensorMap v_map, const __grid_constant__ PromptParams p) {
-  using C = PromptCfg<D>;
-  constexpr int S = C::kStages;
+  using C = PromptCfg<D, TILES>;
+  constexpr int S = C::kStages, kIssue = 4 * TILES;  // the first warp that is not a softmax warp
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t q_bar[2], full_bar[S], free_bar[S], s_bar[2], p_bar[2][2], o_bar[2], last_bar[2], look_bar[2], drain_bar[2];
+  __shared__ __align__(8) uint64_t q_bar[2], full_bar[S], free_bar[TILES][S], s_bar[2], p_bar[2][2], o_bar[2], last_bar[2], look_bar[2], drain_bar[2];
   __shared__ uint32_t tmem_sh, abort_sh;
   __shared__ uint32_t odd_sh[2];  // V of the tile's last step holds what is not finite
   __shared__ Work work_sh;
@@ -226,7 +243,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   if (blockIdx.x == 0 && threadIdx.x == 0) *p.err = 0;
   if (warp == 0) {
     Work w;
-    const bool any = find_work(p, &w);
+    const bool any = find_work(p, TILES * kTile, &w);
     if (lane == 0) {
       work_sh = w;
       any_sh = any;
@@ -244,34 +261,41 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       mbar_init(smem_u32(&look_bar[i]), 1);
       odd_sh[i] = 0;
     }
-    for (int i = 0; i < S; ++i) mbar_init(smem_u32(&full_bar[i]), 1);
+    for (int i = 0; i < S; ++i) {
+      mbar_init(smem_u32(&full_bar[i]), 1);
+      for (int tile = 0; tile < TILES; ++tile) mbar_init(smem_u32(&free_bar[tile][i]), 1);
+    }
     abort_sh = 0;
-  }
-  __syncthreads();
-  if (!any_sh) return;
-  if (threadIdx.x == 32) {  // (the issue warps of the tiles that there are)
-    for (int i = 0; i < S; ++i) mbar_init(smem_u32(&free_bar[i]), work_sh.len > work_sh.row0 + kTile ? 2 : 1);
     fence_mbar_init();
   }
-  if (warp == 8) {
-    tmem_alloc(smem_u32(&tmem_sh), 512);
+  if (warp == kIssue) {
+    tmem_alloc(smem_u32(&tmem_sh), C::kColumns);
     tmem_relinquish();
+  }
+  if (warp == kIssue + 2 && elect_one()) {
+    prefetch_tensormap(&q_map);
+    prefetch_tensormap(&k_map);
+    prefetch_tensormap(&v_map);
   }
   tc_fence_before();
   __syncwarp();
   cta_sync_all();
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(kAll, tmem_sh, 0);
+  if (!any_sh) {  // (the grid is for as many blocks as there could be)
+    if (warp == kIssue) tmem_dealloc(tmem, C::kColumns);
+    return;
+  }
   const Work w = work_sh;
-  const bool two = w.len > w.row0 + kTile;  // the second tile has rows
+  const bool two = TILES == 2 && w.len > w.row0 + kTile;  // the second tile has rows
   const int n0 = w.row0 / kTile + 1;        // steps of the first tile; the second has one more
   const int n = n0 + (two ? 1 : 0);
-  const uint32_t ring = smem_base + 2 * C::kTileBytes;
-  const uint32_t full0 = smem_u32(&full_bar[0]), free0 = smem_u32(&free_bar[0]);
+  const uint32_t ring = smem_base + TILES * C::kTileBytes;
+  const uint32_t full0 = smem_u32(&full_bar[0]);
 
-  if (warp < 8) {
+  if (warp < kIssue) {
     // ------------------------------------------------------------ softmax
-    regs_up<kRegsSoftmax>();
+    regs_up<C::kRegsSoftmax>();
     const int tile = warp / 4;
     const int r = warp % 4 * 32 + lane;  // the thread's row of the tile
     const uint32_t lanes = static_cast<uint32_t>(warp % 4 * 32) << 16;
@@ -370,23 +394,34 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       const int row = w.row0 + tile * kTile + r;
       const bool odd = *static_cast<volatile uint32_t *>(&odd_sh[tile]) != 0;
       const float inv = 1.0f / l;
-      uint16_t *out = p.out + static_cast<int64_t>(w.begin + row) * p.ldo + static_cast<int64_t>(w.head) * p.head_dim;
+      // each warp's rows by way of the tile's place of Q, which is done with, so that they are stored as whole lines; the 16-byte
+      // pieces of a row are exchanged against bank conflicts
+      constexpr int kPieces = D / 8;
+      const uint32_t place = smem_base + tile * C::kTileBytes + warp % 4 * 32 * D * 2;
 #pragma unroll
       for (int c = 0; c < D / 32; ++c) {
         uint32_t o[32];
         tmem_ld_32x32b_x32(o_at + 32 * c, o);
         tmem_wait_ld();
-        if (row < w.len && !odd) {
 #pragma unroll
-          for (int j = 0; j < 32; j += 8) {
-            if (32 * c + j < p.head_dim) {
-              uint32_t x[4];
+        for (int j = 0; j < 4; ++j) {
+          uint32_t x[4];
 #pragma unroll
-              for (int e = 0; e < 4; ++e)
-                x[e] = weights2<DT>(__uint_as_float(o[j + 2 * e]) * inv, __uint_as_float(o[j + 2 * e + 1]) * inv);
-              *reinterpret_cast<uint4 *>(out + 32 * c + j) = make_uint4(x[0], x[1], x[2], x[3]);
-            }
-          }
+          for (int e = 0; e < 4; ++e)
+            x[e] = weights2<DT>(__uint_as_float(o[8 * j + 2 * e]) * inv, __uint_as_float(o[8 * j + 2 * e + 1]) * inv);
+          asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(place + lane * D * 2 + 16 * ((4 * c + j) ^ (lane % kPieces))),
+                       "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3])
+                       : "memory");
+        }
+      }
+      __syncwarp();
+      uint16_t *out = p.out + static_cast<int64_t>(w.begin + row - lane) * p.ldo + static_cast<int64_t>(w.head) * p.head_dim;
+      if (!odd) {
+#pragma unroll 4
+        for (int i = lane; i < 32 * kPieces; i += 32) {
+          const int rr = i / kPieces, c = i % kPieces;
+          if (row - lane + rr < w.len && 8 * c < p.head_dim)
+            *reinterpret_cast<uint4 *>(out + rr * p.ldo + 8 * c) = lds128(place + rr * D * 2 + 16 * (c ^ (rr % kPieces)));
         }
       }
       if (odd)
@@ -396,13 +431,14 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         }
     }
   } else {
-    regs_down<kRegsOthers>();
-    if (warp < 10) {
+    regs_down<C::kRegsOthers>();
+    if (warp < kIssue + TILES) {
       // -------------------------------------------------------- products
-      const int tile = warp - 8;
+      const int tile = warp - kIssue;
       const int steps = tile == 0 ? n0 : two ? n : 0;
       constexpr uint32_t qk = idesc_f16_f32(kTile, kTile, DT == kDtypeBf16), pv = idesc_f16_f32(kTile, D, DT == kDtypeBf16, true);
       const uint32_t s_at = tmem + tile * kTile, o_at = tmem + C::kO + tile * D;
+      const uint32_t free0 = smem_u32(&free_bar[tile][0]);
       const uint32_t s_full = smem_u32(&s_bar[tile]), p_full = smem_u32(&p_bar[tile][0]);
       auto scores = [&](uint32_t stage) {
         const uint64_t a = sw128_kmajor_desc(smem_base + tile * C::kTileBytes), b = sw128_kmajor_desc(ring + stage * C::kTileBytes);
@@ -462,7 +498,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         __syncwarp();
         drain_wait(smem_u32(&drain_bar[tile]), 0);
       }
-    } else if (warp == 10) {
+    } else if (warp == kIssue + 2) {
       // ---------------------------------------------------------- copies
       auto load = [&](const CUtensorMap *map, uint32_t to, int head, int row, uint32_t bar) {
         mbar_arrive_expect_tx(bar, C::kTileBytes);
@@ -475,7 +511,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       __syncwarp();
       for (int item = 0; item < 2 * n; ++item) {
         const uint32_t stage = static_cast<uint32_t>(item % S);
-        if (item >= S) ok = warp_wait(free0 + 8 * stage, (item / S - 1) & 1, abort_flag, p.err, p.wait_limit);
+        if (item >= S)
+          for (int tile = 0; tile < (two ? 2 : 1); ++tile)
+            ok = ok && warp_wait(smem_u32(&free_bar[tile][stage]), (item / S - 1) & 1, abort_flag, p.err, p.wait_limit);
         if (!ok) break;
         if (elect_one()) {
           // the last steps' V signals barriers of its own, which have one phase: the looking warps do not follow the ring
@@ -485,7 +523,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         }
         __syncwarp();
       }
-    } else {
+    } else if (warp == kIssue + 3) {
       // ------------------------------------- the last V of each tile (its place is not used again)
       for (int tile = 0; tile < (two ? 2 : 1); ++tile) {
         const int step = n0 - 1 + tile;
@@ -521,17 +559,17 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   __syncwarp();
   cta_sync_all();
   if (*abort_flag) let_copies_land();  // (else every copy has been waited for)
-  if (warp == 8) {
+  if (warp == kIssue) {
     __syncwarp();
     tc_fence_after();
-    tmem_dealloc(tmem, 512);
+    tmem_dealloc(tmem, C::kColumns);
   }
 }
 
-template <int DT, int D>
+template <int DT, int D, int TILES>
 cudaError_t launch_tiles(const PromptArgs &a, const PromptParams &p, cudaStream_t stream) {
-  auto kern = prompt_attention_kernel<DT, D>;
-  using C = PromptCfg<D>;
+  auto kern = prompt_attention_kernel<DT, D, TILES>;
+  using C = PromptCfg<D, TILES>;
   static std::atomic<uint64_t> set{0};
   const cudaError_t e = allow_smem(kern, C::kSmem, &set);
   if (e != cudaSuccess) return e;
@@ -541,15 +579,24 @@ cudaError_t launch_tiles(const PromptArgs &a, const PromptParams &p, cudaStream_
       !make_heads_map(&k_map, a.k, a.T, k_heads, a.head_dim, a.ldk, kTile, DT) ||
       !make_heads_map(&v_map, a.v, a.T, k_heads, a.head_dim, a.ldv, kTile, DT))
     return cudaErrorInvalidValue;
-  const int64_t blocks = (a.T / (2 * kTile) + a.batch) * a.q_heads;
-  return launch_programmatic(kern, static_cast<int>(blocks), kPromptThreads, C::kSmem, stream, q_map, k_map, v_map, p);
+  const int64_t blocks = (a.T / (TILES * kTile) + a.batch) * a.q_heads;
+  return launch_programmatic(kern, static_cast<int>(blocks), C::kThreads, C::kSmem, stream, q_map, k_map, v_map, p);
+}
+
+// One tile or two a block (bf16, us, one / two). Heads of 64: 8192 rows x 64 heads 513 / 561, nine prompts of up to 1900 rows x 24
+// heads 28 / 36, four of 256 x 32 8.5 / 7.8. Heads of 128: 8192 x 64 675 / 650, 4096 x 2 x 32 213 / 200, 2048 x 32 37.9 / 37.0,
+// 1000 x 8 14.4 / 18.1: two, where they are a block for each SM.
+template <int DT>
+cudaError_t launch_type(const PromptArgs &a, const PromptParams &p, int num_sms, cudaStream_t stream) {
+  if (a.head_dim <= 64) return launch_tiles<DT, 64, 1>(a, p, stream);
+  return cdiv(a.T, 2 * kTile) * a.q_heads < num_sms ? launch_tiles<DT, 128, 1>(a, p, stream) : launch_tiles<DT, 128, 2>(a, p, stream);
 }
 
 }  // namespace
 
 size_t prompt_attention_workspace_bytes(int64_t, int, int) { return 256; }
 
-cudaError_t launch_prompt_attention(const PromptArgs &a, void *workspace, int, cudaStream_t stream) {
+cudaError_t launch_prompt_attention(const PromptArgs &a, void *workspace, int num_sms, cudaStream_t stream) {
   PromptParams p;
   p.q = static_cast<const uint16_t *>(a.q);
   p.k = static_cast<const uint16_t *>(a.k);
@@ -569,9 +616,7 @@ cudaError_t launch_prompt_attention(const PromptArgs &a, void *workspace, int, c
   p.scale = a.scale * 1.4426950408889634f;
   p.wait_limit = a.wait_limit ? a.wait_limit : kWaitLimitCycles;
   p.test_extra = a.test_timeout ? 1 : 0;
-  if (a.head_dim <= 64)
-    return a.dtype == kDtypeBf16 ? launch_tiles<kDtypeBf16, 64>(a, p, stream) : launch_tiles<kDtypeF16, 64>(a, p, stream);
-  return a.dtype == kDtypeBf16 ? launch_tiles<kDtypeBf16, 128>(a, p, stream) : launch_tiles<kDtypeF16, 128>(a, p, stream);
+  return a.dtype == kDtypeBf16 ? launch_type<kDtypeBf16>(a, p, num_sms, stream) : launch_type<kDtypeF16>(a, p, num_sms, stream);
 }
 
 }  // namespace w4
