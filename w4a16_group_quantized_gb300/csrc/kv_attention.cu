@@ -37,6 +37,7 @@ using namespace detail;
 constexpr uint32_t kAll = 0xffffffffu;
 constexpr int kMostWarps = 16;    // of a block
 constexpr int kItemCost = 6;      // what beginning an item costs, in tiles
+constexpr int kSoloTiles = 16;    // tiles a warp, up to which items that are few go whole to a block each
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kSlack = 8.0f;    // how far a score may pass the maximum in use (log2 of the weight)
 // Scales of values that go into the weights: 2^-40 to 2^40, so that a weight of one page beside another's stays a normal number
@@ -216,83 +217,104 @@ __global__ void __launch_bounds__(32 * KvCfg<D, ROWS>::kWarps, 1) kv_attention_k
   const bool exact = head_dim == D;
   const int most = p.max_pages * p.page;
   auto tiles_of = [&](int b) { return max((min(p.lens[b], most) + 15) / 16, 1); };  // (a sequence without keys still has an output)
-  const int share = (p.batch + 32 * W - 1) / (32 * W);  // sequences a thread adds up
-  int64_t sum = 0;
-  for (int i = 0; i < share; ++i) {
-    const int b = threadIdx.x * share + i;
-    if (b < p.batch) sum += static_cast<int64_t>(tiles_of(b) + kItemCost) * p.items;
+  // The warp's stretch, its first tile (at: its unit) with the sequence and item, and whether all the block's tiles are of one
+  // item, whose sums are then added here
+  int64_t from, to, at, block_from, block_to, one_begin;
+  int b = 0, j = 0, tile = 0, tiles = 1, one_b, one_j, one_tiles, me = 0, warps = W;
+  bool together, solo = p.batch * p.items <= gridDim.x;
+  Deal deal = {};
+  if (solo) {
+    // few items: a block each, and nothing to add afterwards, unless the longest would take too long that way
+    int longest = 0;
+    for (int i = lane; i < p.batch; i += 32) longest = max(longest, tiles_of(i));
+    solo = __reduce_max_sync(kAll, longest) <= W * kSoloTiles;
   }
+  if (solo) {
+    if (blockIdx.x == 0 && threadIdx.x == 0) *p.workers = 0;
+    if (blockIdx.x >= p.batch * p.items) return;
+    one_b = b = blockIdx.x / p.items;
+    one_j = j = blockIdx.x - b * p.items;
+    one_tiles = tiles = tiles_of(b);
+    one_begin = block_from = 0;
+    block_to = tiles;
+    at = from = tile = static_cast<int>(static_cast<int64_t>(tiles) * warp / W);
+    to = static_cast<int64_t>(tiles) * (warp + 1) / W;
+    together = true;
+  } else {
+    const int share = (p.batch + 32 * W - 1) / (32 * W);  // sequences a thread adds up
+    int64_t sum = 0;
+    for (int i = 0; i < share; ++i) {
+      const int sb = threadIdx.x * share + i;
+      if (sb < p.batch) sum += static_cast<int64_t>(tiles_of(sb) + kItemCost) * p.items;
+    }
 #pragma unroll
-  for (int i = 1; i < 32; i *= 2) {
-    const int64_t x = __shfl_up_sync(kAll, sum, i);
-    if (lane >= i) sum += x;
-  }
-  upto[threadIdx.x] = sum;
-  __syncthreads();
-  int64_t before = 0;
-  for (int i = 0; i < warp; ++i) before += upto[32 * i + 31];
-  __syncthreads();
-  upto[threadIdx.x] = sum + before;
-  __syncthreads();
-  const int64_t total = upto[32 * W - 1];
-  // fewer warps where there is little to do
-  Deal deal;
-  deal.workers = static_cast<uint32_t>(min(static_cast<int64_t>(W * gridDim.x), max(total / 4, int64_t{1})));
-  deal.quotient = total / deal.workers;
-  deal.remainder = static_cast<uint32_t>(total - deal.quotient * deal.workers);
-  // (those that there are, in all blocks alike)
-  const int warps = static_cast<int>((deal.workers + gridDim.x - 1) / gridDim.x);
-  const int me = warp < warps ? blockIdx.x * warps + warp : gridDim.x * W;
-  if (blockIdx.x == 0 && threadIdx.x == 0) *p.workers = static_cast<int32_t>(deal.workers);
-  const int64_t from = deal.start(me), to = deal.start(me + 1);
-  bool cut = false;
+    for (int i = 1; i < 32; i *= 2) {
+      const int64_t x = __shfl_up_sync(kAll, sum, i);
+      if (lane >= i) sum += x;
+    }
+    upto[threadIdx.x] = sum;
+    __syncthreads();
+    int64_t before = 0;
+    for (int i = 0; i < warp; ++i) before += upto[32 * i + 31];
+    __syncthreads();
+    upto[threadIdx.x] = sum + before;
+    __syncthreads();
+    const int64_t total = upto[32 * W - 1];
+    // fewer warps where there is little to do
+    deal.workers = static_cast<uint32_t>(min(static_cast<int64_t>(W * gridDim.x), max(total / 4, int64_t{1})));
+    deal.quotient = total / deal.workers;
+    deal.remainder = static_cast<uint32_t>(total - deal.quotient * deal.workers);
+    // (those that there are, in all blocks alike)
+    warps = static_cast<int>((deal.workers + gridDim.x - 1) / gridDim.x);
+    me = warp < warps ? blockIdx.x * warps + warp : gridDim.x * W;
+    if (blockIdx.x == 0 && threadIdx.x == 0) *p.workers = static_cast<int32_t>(deal.workers);
+    from = deal.start(me), to = deal.start(me + 1);
+    block_from = deal.start(blockIdx.x * warps), block_to = deal.start((blockIdx.x + 1) * warps);
 
-  // the sequence and item that unit `at` lies in, and the unit within the item
-  auto find = [&](int64_t at, int *b, int *j, int *tiles) {
-    int lo = 0, hi = 32 * W - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi) / 2;
-      if (upto[mid] > at)
-        hi = mid;
-      else
-        lo = mid + 1;
-    }
-    int64_t rest = at - (lo > 0 ? upto[lo - 1] : 0);
-    int64_t units;
-    for (*b = lo * share;; ++*b) {
-      *tiles = tiles_of(*b);
-      units = static_cast<int64_t>(*tiles + kItemCost) * p.items;
-      if (rest < units || *b + 1 >= p.batch) break;
-      rest -= units;
-    }
-    *j = static_cast<int>(rest / (*tiles + kItemCost));
-    return static_cast<int>(rest - static_cast<int64_t>(*j) * (*tiles + kItemCost));
-  };
-  // whether all the block's tiles are of one item: their sums are then added here
-  const int64_t block_from = deal.start(blockIdx.x * warps), block_to = deal.start((blockIdx.x + 1) * warps);
-  __shared__ int one_b, one_j, one_tiles;
-  __shared__ int64_t one_begin;
-  __shared__ bool one_sh;
-  if (threadIdx.x == 0) {
-    one_sh = false;
+    // the sequence and item that a unit lies in, and the unit within the item
+    auto find = [&](int64_t unit, int *fb, int *fj, int *ftiles) {
+      int lo = 0, hi = 32 * W - 1;
+      while (lo < hi) {
+        const int mid = (lo + hi) / 2;
+        if (upto[mid] > unit)
+          hi = mid;
+        else
+          lo = mid + 1;
+      }
+      int64_t rest = unit - (lo > 0 ? upto[lo - 1] : 0);
+      for (*fb = lo * share;; ++*fb) {
+        *ftiles = tiles_of(*fb);
+        const int64_t units = static_cast<int64_t>(*ftiles + kItemCost) * p.items;
+        if (rest < units || *fb + 1 >= p.batch) break;
+        rest -= units;
+      }
+      *fj = static_cast<int>(rest / (*ftiles + kItemCost));
+      return static_cast<int>(rest - static_cast<int64_t>(*fj) * (*ftiles + kItemCost));
+    };
+    // (every warp finds the block's first item for itself: no more barriers)
+    together = false;
+    one_b = one_j = one_tiles = 0;
+    one_begin = 0;
     if (block_from < block_to) {
-      int ob, oj, otiles;
-      const int off = find(block_from, &ob, &oj, &otiles);
-      const int64_t begin = block_from - off + kItemCost;
-      one_sh = block_to > begin && block_to <= begin + otiles + kItemCost;
-      one_b = ob, one_j = oj, one_tiles = otiles, one_begin = begin;
+      const int off = find(block_from, &one_b, &one_j, &one_tiles);
+      one_begin = block_from - off + kItemCost;
+      together = block_to > one_begin && block_to <= one_begin + one_tiles + kItemCost;
+    }
+    at = to;
+    if (from < to) {
+      int off;
+      if (together) {
+        b = one_b, j = one_j, tiles = one_tiles;
+        off = static_cast<int>(from - one_begin) + kItemCost;
+      } else {
+        off = find(from, &b, &j, &tiles);
+      }
+      tile = max(off - kItemCost, 0);
+      at = from + max(kItemCost - off, 0);
+      if (tile >= tiles) tile = 0, at = to;  // (what is left of the block's stretch is the next item's beginning)
     }
   }
-  __syncthreads();
-  const bool together = one_sh;
-
-  int b = 0, j = 0, tile = 0, tiles = 1;
-  int64_t at = to;  // the tile's unit
-  if (from < to) {
-    const int off = find(from, &b, &j, &tiles);
-    tile = max(off - kItemCost, 0);
-    at = from + max(kItemCost - off, 0);
-  }
+  bool cut = false;
 
   // ---------------------------------------------------------------- copies
   // The tile that is copied next, and what the lookups found for up to 32 tiles of its item (sent: tiles so far)
@@ -305,6 +327,18 @@ __global__ void __launch_bounds__(32 * KvCfg<D, ROWS>::kWarps, 1) kv_attention_k
   constexpr int kCopyKeys = 512 / D;
   const int lane_key = lane * 16 / D, lane_c = lane % (D / 16);
   const int lane_off = lane_key * head_dim + lane_c * 16;
+  // what the scales of the last lookup become: done after its first copies have been sent
+  float found_ks = 0.0f, found_vs = 0.0f;
+  bool pending = false;
+  auto keep_scales = [&]() {
+    if (!pending) return;
+    pending = false;
+    const float size = fabsf(found_vs);
+    const bool plain = size >= kScaleMin && size <= kScaleMax;
+    const float part = plain ? size : size > kScaleMax ? kScaleMax : kScaleMin;
+    info[(book + lane) % 64] = make_float4(found_ks, log2f(part), 1.0f / part, plain ? copysignf(1.0f, found_vs) : found_vs / part);
+    __syncwarp();
+  };
   auto send = [&]() {
     uint32_t place = 255;
     __syncwarp();  // the place's last tile has been read
@@ -314,6 +348,7 @@ __global__ void __launch_bounds__(32 * KvCfg<D, ROWS>::kWarps, 1) kv_attention_k
         first = ct;
         found = min(32, ctiles - ct);
         // (places go round: when it comes to a lookup, at most S tiles of the ones before are still to be worked on)
+        keep_scales();
         book = next_book;
         next_book = (book + found) % 64;
         int64_t off = -1;
@@ -324,17 +359,13 @@ __global__ void __launch_bounds__(32 * KvCfg<D, ROWS>::kWarps, 1) kv_attention_k
           if (pi < p.max_pages) pg = p.table[static_cast<int64_t>(cb) * p.max_pages + pi];
           if (pg >= 0 && pg < p.pages) {
             const int64_t ph = static_cast<int64_t>(pg) * p.k_heads + h;
-            const float ks = p.k_scale[ph], vs = p.v_scale[ph];
-            const float size = fabsf(vs);
-            const bool plain = size >= kScaleMin && size <= kScaleMax;
-            const float part = plain ? size : size > kScaleMax ? kScaleMax : kScaleMin;
-            info[(book + lane) % 64] = make_float4(ks, log2f(part), 1.0f / part, plain ? copysignf(1.0f, vs) : vs / part);
+            found_ks = p.k_scale[ph], found_vs = p.v_scale[ph];
             off = (ph * p.page + key0 - pi * p.page) * (head_dim / 16);
           }
         }
+        pending = true;
         off_lo = static_cast<uint32_t>(off);
         off_hi = static_cast<uint32_t>(off >> 32);
-        __syncwarp();
       }
       const uint32_t lo = __shfl_sync(kAll, off_lo, ct - first), hi = __shfl_sync(kAll, off_hi, ct - first);
       if (hi != 0xffffffffu) {
@@ -439,15 +470,17 @@ __global__ void __launch_bounds__(32 * KvCfg<D, ROWS>::kWarps, 1) kv_attention_k
 #pragma unroll
     for (int x = 0; x < NO; ++x) o[x][0] = o[x][1] = 0.0f;
   };
-  begin_item();  // (also for a warp without tiles: sums of nothing)
   for (int i = 0; i < S - 1; ++i) {
     infos >>= 8;
     send();
   }
+  begin_item();  // (also for a warp without tiles: sums of nothing)
+  keep_scales();
   for (int i = 0; at < to; ++i) {
     if (i > 0 && tile == 0) begin_item();
     infos >>= 8;
     send();  // (its place held tile i - 1, which is done)
+    keep_scales();
     cp_wait<S - 1>();
     __syncwarp();  // (every lane has waited for what it copied)
     const uint32_t mine = infos & 0xffu;
@@ -654,7 +687,7 @@ __global__ void __launch_bounds__(32 * KvCfg<D, ROWS>::kWarps, 1) kv_attention_k
     for (int i = 0; i < 2; ++i) sums[(warp * ROWS + row_of<ROWS>(x, i)) * C::kSumRow + value_of<D, ROWS>(x, i)] = o[x][i];
   __syncthreads();
   const bool here = begin >= block_from, whole = here && end <= block_to;
-  if (lane == 0 && from < to) {
+  if (lane == 0 && from < to && !solo) {
     p.cut[me] = here && !whole && warp == 0;
     if (here && !whole && warp == 0) p.cuts[me] = CutItem{one_b, one_j, deal.holder(end - 1), warps, begin, end, deal};
   }
