@@ -44,6 +44,11 @@ constexpr float kSlack = 8.0f;    // how far a score may pass the maximum in use
 // of 32 bits (it counts in the sum l, however small its part of O).
 constexpr float kScaleMin = 0x1p-40f, kScaleMax = 0x1p40f;
 
+// n / d for n that mostly fits 32 bits.
+__device__ __forceinline__ int64_t quotient(int64_t n, uint32_t d) {
+  return n >> 32 == 0 ? static_cast<int64_t>(static_cast<uint32_t>(n) / d) : n / d;
+}
+
 // How `units` are dealt out to warps: the first unit of each one's stretch is quotient * w + remainder * w / workers.
 struct Deal {
   int64_t quotient;
@@ -241,28 +246,32 @@ __global__ void __launch_bounds__(32 * KvCfg<D, ROWS>::kWarps, 1) kv_attention_k
     to = static_cast<int64_t>(tiles) * (warp + 1) / W;
     together = true;
   } else {
-    const int share = (p.batch + 32 * W - 1) / (32 * W);  // sequences a thread adds up
+    // the units of the sequences up to and with each: for few, in each warp's lanes; else up to and with each thread's
+    const bool few = p.batch <= 32;
+    const int share = few ? 1 : (p.batch + 32 * W - 1) / (32 * W);  // sequences a thread adds up
+    const int sb0 = few ? lane : threadIdx.x * share;
+    const int lane_tiles = few && lane < p.batch ? tiles_of(lane) : 0;
     int64_t sum = 0;
-    for (int i = 0; i < share; ++i) {
-      const int sb = threadIdx.x * share + i;
-      if (sb < p.batch) sum += static_cast<int64_t>(tiles_of(sb) + kItemCost) * p.items;
-    }
+    for (int sb = sb0; sb < min(sb0 + share, p.batch); ++sb) sum += static_cast<int64_t>((few ? lane_tiles : tiles_of(sb)) + kItemCost) * p.items;
+    const int64_t mine = sum;
 #pragma unroll
     for (int i = 1; i < 32; i *= 2) {
       const int64_t x = __shfl_up_sync(kAll, sum, i);
       if (lane >= i) sum += x;
     }
-    upto[threadIdx.x] = sum;
-    __syncthreads();
-    int64_t before = 0;
-    for (int i = 0; i < warp; ++i) before += upto[32 * i + 31];
-    __syncthreads();
-    upto[threadIdx.x] = sum + before;
-    __syncthreads();
-    const int64_t total = upto[32 * W - 1];
+    if (!few) {
+      upto[threadIdx.x] = sum;
+      __syncthreads();
+      int64_t before = 0;
+      for (int i = 0; i < warp; ++i) before += upto[32 * i + 31];
+      __syncthreads();
+      upto[threadIdx.x] = sum + before;
+      __syncthreads();
+    }
+    const int64_t total = few ? __shfl_sync(kAll, sum, 31) : upto[32 * W - 1];
     // fewer warps where there is little to do
     deal.workers = static_cast<uint32_t>(min(static_cast<int64_t>(W * gridDim.x), max(total / 4, int64_t{1})));
-    deal.quotient = total / deal.workers;
+    deal.quotient = quotient(total, deal.workers);
     deal.remainder = static_cast<uint32_t>(total - deal.quotient * deal.workers);
     // (those that there are, in all blocks alike)
     warps = static_cast<int>((deal.workers + gridDim.x - 1) / gridDim.x);
@@ -273,22 +282,29 @@ __global__ void __launch_bounds__(32 * KvCfg<D, ROWS>::kWarps, 1) kv_attention_k
 
     // the sequence and item that a unit lies in, and the unit within the item
     auto find = [&](int64_t unit, int *fb, int *fj, int *ftiles) {
-      int lo = 0, hi = 32 * W - 1;
-      while (lo < hi) {
-        const int mid = (lo + hi) / 2;
-        if (upto[mid] > unit)
-          hi = mid;
-        else
-          lo = mid + 1;
+      int64_t rest;
+      if (few) {
+        *fb = __ffs(__ballot_sync(kAll, sum > unit)) - 1;
+        rest = unit - __shfl_sync(kAll, sum - mine, *fb);
+        *ftiles = __shfl_sync(kAll, lane_tiles, *fb);
+      } else {
+        int lo = 0, hi = 32 * W - 1;
+        while (lo < hi) {
+          const int mid = (lo + hi) / 2;
+          if (upto[mid] > unit)
+            hi = mid;
+          else
+            lo = mid + 1;
+        }
+        rest = unit - (lo > 0 ? upto[lo - 1] : 0);
+        for (*fb = lo * share;; ++*fb) {
+          *ftiles = tiles_of(*fb);
+          const int64_t units = static_cast<int64_t>(*ftiles + kItemCost) * p.items;
+          if (rest < units || *fb + 1 >= p.batch) break;
+          rest -= units;
+        }
       }
-      int64_t rest = unit - (lo > 0 ? upto[lo - 1] : 0);
-      for (*fb = lo * share;; ++*fb) {
-        *ftiles = tiles_of(*fb);
-        const int64_t units = static_cast<int64_t>(*ftiles + kItemCost) * p.items;
-        if (rest < units || *fb + 1 >= p.batch) break;
-        rest -= units;
-      }
-      *fj = static_cast<int>(rest / (*ftiles + kItemCost));
+      *fj = static_cast<int>(quotient(rest, static_cast<uint32_t>(*ftiles + kItemCost)));
       return static_cast<int>(rest - static_cast<int64_t>(*fj) * (*ftiles + kItemCost));
     };
     // (every warp finds the block's first item for itself: no more barriers)
@@ -720,75 +736,130 @@ __global__ void __launch_bounds__(32 * KvCfg<D, ROWS>::kWarps, 1) kv_attention_k
 constexpr int kAddThreads = 256;
 
 // The items that are cut, their parts added in order. A block looks at warps [x * workers / gridDim.x, (x + 1) * workers / gridDim.x)
-// for items that begin there and adds p.add_rows rows of them; the groups of D / 4 threads take a row each or, with one row, the
-// parts in turn.
-template <int DT, int D>
-__global__ void __launch_bounds__(kAddThreads) kv_add_kernel(const __grid_constant__ KvParams p, int add_rows) {
+// for items that begin there and adds ROWS rows of them: it lists the item's parts, finds what each row of each of them weighs,
+// and adds them up, a row by a group of D / 4 threads or, of one row, every kGroups-th part by each group.
+template <int DT, int D, int ROWS>
+__global__ void __launch_bounds__(kAddThreads) kv_add_kernel(const __grid_constant__ KvParams p) {
   constexpr int kLane = D / 4, kGroups = kAddThreads / kLane;
-  __shared__ float4 part_o[kGroups][kLane];
-  __shared__ float part_m[kGroups], part_l[kGroups];
+  static_assert(ROWS == 1 || ROWS == kGroups, "a group a row, or all groups one row");
+  __shared__ int32_t slots[kAddThreads];
+  __shared__ float factor[ROWS][kAddThreads];
+  __shared__ float row_m[ROWS], row_l[ROWS], row_f[ROWS];
+  __shared__ float4 part_o[ROWS == 1 ? kGroups : 1][kLane];
+  __shared__ int counts[kAddThreads / 32];
   griddep_launch_dependents();
   griddep_wait();
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int workers = *p.workers;
   const int w0 = static_cast<int>(static_cast<int64_t>(blockIdx.x) * workers / gridDim.x);
   const int w1 = static_cast<int>((static_cast<int64_t>(blockIdx.x) + 1) * workers / gridDim.x);
   const int group = threadIdx.x / kLane, x = threadIdx.x % kLane;
-  const int row = blockIdx.y * add_rows + (add_rows > 1 ? group : 0);
-  const int first = add_rows > 1 ? 0 : group, step = add_rows > 1 ? 1 : kGroups;
-  for (int base = w0; base < w1; base += kAddThreads) {
-    // (the whole block takes the same turns)
-    __shared__ uint32_t mask[kAddThreads / 32];
-    const int mine = base + threadIdx.x;
-    const uint32_t any = __ballot_sync(kAll, mine < w1 && p.cut[mine] != 0);
-    __syncthreads();
-    if (threadIdx.x % 32 == 0) mask[threadIdx.x / 32] = any;
-    __syncthreads();
-    for (int k = 0; k < kAddThreads / 32; ++k)
-      for (uint32_t bits = mask[k]; bits; bits &= bits - 1) {
-        const int w = base + 32 * k + __ffs(bits) - 1;
-        const CutItem it = p.cuts[w];
-        const int rows = min(16, p.n * p.r - it.j % p.row_tiles * 16);
-        float m = -INFINITY, l = 0.0f;
-        float4 o = make_float4(0, 0, 0, 0);
-        if (row < rows && (add_rows == 1 || group < add_rows)) {
-          for (int at = w + first; at <= it.last; at += step) {
-            // a block within the item has one part, in its first warp's place
-            const int block = at / it.warps * it.warps;
-            const bool one = it.deal.start(block) >= it.begin - kItemCost && it.deal.start(block + it.warps) <= it.end + kItemCost;
-            if (one && at != block) continue;
-            const float *slot = p.sums + (static_cast<int64_t>(2 * at) + (it.deal.start(at) <= it.begin ? 1 : 0)) * p.rows * (D + 4);
-            const float pm = slot[p.rows * D + row], pl = slot[p.rows * (D + 1) + row];
-            const float4 po = *reinterpret_cast<const float4 *>(slot + row * D + 4 * x);
-            const float now = fmaxf(m, pm);
-            const float f = m == now ? 1.0f : ex2(m - now), pf = pm == now ? 1.0f : ex2(pm - now);
-            m = now;
-            l = l * f + pl * pf;
-            o = make_float4(o.x * f + po.x * pf, o.y * f + po.y * pf, o.z * f + po.z * pf, o.w * f + po.w * pf);
-          }
+  const int row0 = blockIdx.y * ROWS;
+  __shared__ uint32_t cut_sh[kAddThreads / 32];
+  for (int w = w0, base0 = w0; base0 < w1; ++w) {
+    // the next warp that holds a cut item's beginning, by turns of the block's threads
+    if (w == base0) {
+      __syncthreads();
+      const uint32_t any = __ballot_sync(kAll, base0 + static_cast<int>(threadIdx.x) < w1 && p.cut[base0 + threadIdx.x] != 0);
+      if (lane == 0) cut_sh[warp] = any;
+      __syncthreads();
+    }
+    const int off = w - base0;
+    uint32_t bits = 0;
+    int word = off / 32;
+    if (off < kAddThreads) {
+      bits = cut_sh[word] & (0xffffffffu << (off % 32));
+      while (bits == 0 && ++word < kAddThreads / 32) bits = cut_sh[word];
+    }
+    if (bits == 0) {
+      base0 += kAddThreads;
+      w = base0 - 1;
+      continue;
+    }
+    w = base0 + 32 * word + __ffs(bits) - 1;
+    const CutItem it = p.cuts[w];
+    const int rows = min(min(16, p.n * p.r - (it.j - p.row_tiles_div.div(it.j) * p.row_tiles) * 16) - row0, ROWS);
+    if (rows <= 0) continue;
+    float4 o = make_float4(0, 0, 0, 0);
+    __syncthreads();  // (the item before is done with what is shared)
+    if (threadIdx.x < ROWS) row_m[threadIdx.x] = -INFINITY, row_l[threadIdx.x] = 0.0f;
+    for (int base = w; base <= it.last; base += kAddThreads) {
+      // the parts among the next warps: a block within the item has one, in its first warp's place
+      const int at = base + threadIdx.x;
+      bool part = at <= it.last;
+      int slot = 0;
+      if (part) {
+        const int block = at / it.warps * it.warps;
+        const bool one = it.deal.start(block) >= it.begin - kItemCost && it.deal.start(block + it.warps) <= it.end + kItemCost;
+        part = !one || at == block;
+        slot = 2 * at + (it.deal.start(at) <= it.begin ? 1 : 0);
+      }
+      const uint32_t mask = __ballot_sync(kAll, part);
+      if (lane == 0) counts[warp] = __popc(mask);
+      __syncthreads();
+      int before = 0, parts = 0;
+#pragma unroll
+      for (int i = 0; i < kAddThreads / 32; ++i) {
+        before += i < warp ? counts[i] : 0;
+        parts += counts[i];
+      }
+      if (part) slots[before + __popc(mask & ((1u << lane) - 1u))] = slot;
+      __syncthreads();
+      auto sums_of = [&](int i) { return p.sums + static_cast<int64_t>(slots[i]) * p.rows * (D + 4); };
+      // what each row of each part weighs against the largest so far, a row a warp
+      for (int row = warp; row < rows; row += kAddThreads / 32) {
+        const float old = row_m[row];
+        float high = old;
+        for (int i = lane; i < parts; i += 32) high = fmaxf(high, sums_of(i)[p.rows * D + row0 + row]);
+#pragma unroll
+        for (int i = 16; i > 0; i /= 2) high = fmaxf(high, __shfl_xor_sync(kAll, high, i));
+        float l = 0.0f;
+        for (int i = lane; i < parts; i += 32) {
+          const float *s = sums_of(i);
+          const float m = s[p.rows * D + row0 + row];
+          const float f = m == high ? 1.0f : ex2(m - high);
+          factor[row][i] = f;
+          l = fmaf(s[p.rows * (D + 1) + row0 + row], f, l);
         }
-        if (add_rows == 1) {
-          part_o[group][x] = o;
-          if (x == 0) part_m[group] = m, part_l[group] = l;
-          __syncthreads();
-          if (group == 0) {
-            for (int y = 1; y < kGroups; ++y) {
-              const float pm = part_m[y], pl = part_l[y];
-              const float4 po = part_o[y][x];
-              const float now = fmaxf(m, pm);
-              const float f = m == now ? 1.0f : ex2(m - now), pf = pm == now ? 1.0f : ex2(pm - now);
-              m = now;
-              l = l * f + pl * pf;
-              o = make_float4(o.x * f + po.x * pf, o.y * f + po.y * pf, o.z * f + po.z * pf, o.w * f + po.w * pf);
-            }
-          }
-          __syncthreads();
-        }
-        if (row < rows && (add_rows > 1 ? group < add_rows : group == 0) && 4 * x < p.head_dim) {
-          const float inv = over_sum(l);
-          *reinterpret_cast<uint2 *>(p.out + row_at(p, it.b, it.j, row, p.ldo) + 4 * x) =
-              make_uint2(out_bits2<DT>(o.x * inv, o.y * inv), out_bits2<DT>(o.z * inv, o.w * inv));
+#pragma unroll
+        for (int i = 16; i > 0; i /= 2) l += __shfl_xor_sync(kAll, l, i);
+        __syncwarp();
+        if (lane == 0) {
+          const float f = old == high ? 1.0f : ex2(old - high);
+          row_m[row] = high, row_f[row] = f, row_l[row] = fmaf(row_l[row], f, l);
         }
       }
+      __syncthreads();
+      const int r = ROWS == 1 ? 0 : group;
+      if (r < rows) {
+        const float f = row_f[r];
+        o = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
+#pragma unroll 4
+        for (int i = ROWS == 1 ? group : 0; i < parts; i += ROWS == 1 ? kGroups : 1) {
+          const float4 v = *reinterpret_cast<const float4 *>(sums_of(i) + (row0 + r) * D + 4 * x);
+          const float g = factor[r][i];
+          o = make_float4(fmaf(v.x, g, o.x), fmaf(v.y, g, o.y), fmaf(v.z, g, o.z), fmaf(v.w, g, o.w));
+        }
+      }
+      __syncthreads();  // (the lists are made anew)
+    }
+    if (ROWS == 1) {
+      part_o[group][x] = o;
+      __syncthreads();
+      if (group == 0) {
+#pragma unroll
+        for (int i = 1; i < kGroups; ++i) {
+          const float4 v = part_o[ROWS == 1 ? i : 0][x];
+          o = make_float4(o.x + v.x, o.y + v.y, o.z + v.z, o.w + v.w);
+        }
+      }
+    }
+    const int r = ROWS == 1 ? 0 : group;
+    if (r < rows && (ROWS > 1 || group == 0) && 4 * x < p.head_dim) {
+      const float inv = over_sum(row_l[r]);
+      *reinterpret_cast<uint2 *>(p.out + row_at(p, it.b, it.j, row0 + r, p.ldo) + 4 * x) =
+          make_uint2(out_bits2<DT>(o.x * inv, o.y * inv), out_bits2<DT>(o.z * inv, o.w * inv));
+    }
   }
 }
 
@@ -803,9 +874,11 @@ cudaError_t launch_d(const KvParams &p, int num_sms, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   const int all = num_sms * C::kWarps;
   const int64_t items = static_cast<int64_t>(p.batch) * p.items;
-  const int add_rows = items >= num_sms ? (p.rows < 4 ? 4 : kAddThreads * 4 / D) : 1;
+  // a block for each row of each item, or for a row a group where the items alone fill the device
+  constexpr int kGroups = kAddThreads * 4 / D;
+  const bool rows_apart = items < num_sms || p.rows == 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(items < all ? items : all), static_cast<unsigned>(cdiv(p.rows, add_rows)));
+  cfg.gridDim = dim3(static_cast<unsigned>(items < all ? items : all), static_cast<unsigned>(cdiv(p.rows, rows_apart ? 1 : kGroups)));
   cfg.blockDim = dim3(kAddThreads);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -813,7 +886,7 @@ cudaError_t launch_d(const KvParams &p, int num_sms, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, kv_add_kernel<DT, D>, p, add_rows);
+  e = rows_apart ? cudaLaunchKernelEx(&cfg, kv_add_kernel<DT, D, 1>, p) : cudaLaunchKernelEx(&cfg, kv_add_kernel<DT, D, kGroups>, p);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
