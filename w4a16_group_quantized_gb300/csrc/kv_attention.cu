@@ -37,7 +37,7 @@ using namespace detail;
 constexpr uint32_t kAll = 0xffffffffu;
 constexpr int kMostWarps = 16;    // of a block
 constexpr int kItemCost = 6;      // what beginning an item costs, in tiles
-constexpr int kSoloTiles = 16;    // tiles a warp, up to which items that are few go whole to a block each
+constexpr int kSoloTiles = 7;     // what adding parts takes, in tiles of a warp
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kSlack = 8.0f;    // how far a score may pass the maximum in use (log2 of the weight)
 // Scales of values that go into the weights: 2^-40 to 2^40, so that a weight of one page beside another's stays a normal number
@@ -229,10 +229,15 @@ __global__ void __launch_bounds__(32 * KvCfg<D, ROWS>::kWarps, 1) kv_attention_k
   bool together, solo = p.batch * p.items <= gridDim.x;
   Deal deal = {};
   if (solo) {
-    // few items: a block each, and nothing to add afterwards, unless the longest would take too long that way
-    int longest = 0;
-    for (int i = lane; i < p.batch; i += 32) longest = max(longest, tiles_of(i));
-    solo = __reduce_max_sync(kAll, longest) <= W * kSoloTiles;
+    // few items: a block each, and nothing to add afterwards, unless the longest takes longer that way (by more than the adding, as
+    // long as kSoloTiles tiles of a warp) than all of them dealt out evenly
+    int longest = 0, all = 0;
+    for (int i = lane; i < p.batch; i += 32) {
+      const int t16 = tiles_of(i);
+      longest = max(longest, t16);
+      all += t16 / 16;
+    }
+    solo = __reduce_max_sync(kAll, longest) <= W * kSoloTiles + static_cast<int64_t>(__reduce_add_sync(kAll, all)) * 16 * p.items / gridDim.x;
   }
   if (solo) {
     if (blockIdx.x == 0 && threadIdx.x == 0) *p.workers = 0;
