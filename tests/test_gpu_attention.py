@@ -505,6 +505,55 @@ def test_prompt_attention_what_is_not_seen(lens, bad):
         assert not torch.isfinite(got[bad:end]).any() and torch.isfinite(got[untouched]).all()
 
 
+def big(lens, hq, hk, dim, dtype="bf16"):
+    """q, k, v of prompts with rows and heads enough for blocks of two tiles."""
+    T = sum(lens)
+    return randn(1, T, hq, dim, dtype=dtype), randn(2, T, hk, dim, dtype=dtype), randn(3, T, hk, dim, dtype=dtype)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("lens,hq,hk,dim", [([1100, 1, 200, 257], 40, 8, 128), ([128, 129, 256, 255, 384, 385], 32, 4, 96), ([2049], 24, 24, 72),
+                                            ([640, 0, 511, 513], 36, 2, 128)])
+def test_prompt_attention_two_tiles(lens, hq, hk, dim, dtype):
+    check_prompt(*big(lens, hq, hk, dim, dtype), lens)
+
+
+@pytest.mark.parametrize("bad", [(130,), (383,), (384, 390), (1000, 1023), (1099,), (5, 700, 1090)])
+def test_prompt_attention_two_tiles_what_is_not_seen(bad):
+    """Values that are not finite in a block's last steps, of either tile, and in steps that all its rows see: a column is infinite from
+    the row of an infinity on, NaN from that of a second one of the other sign, and untouched before and elsewhere."""
+    lens = [1100, 300]
+    q, k, v = big(lens, 32, 4, 128)
+    clean = v.clone()
+    for i, row in enumerate(bad):
+        v[row, 2, 40] = -math.inf if i % 2 else math.inf
+        clean[row, 2, 40] = 0
+    got = w4.w4_prompt_attention(q, k, v, starts(lens))
+    column = got[:1100, 16:24, 40].float()
+    assert torch.isfinite(column[:bad[0]]).all()
+    if len(bad) > 1:
+        assert torch.isnan(column[bad[1]:]).all()
+    # (a weight may vanish in 32 bits, and 0 * infinity is NaN, but not within a step of its row)
+    assert (column[bad[0]] == math.inf).all() and not torch.isfinite(column[bad[0]:]).any()
+    untouched = torch.ones(1400, 32, 128, dtype=torch.bool, device="cuda")
+    untouched[bad[0]:1100, 16:24, 40] = False
+    assert torch.isfinite(got[untouched]).all()
+    check_prompt_rows(torch.where(untouched, got, w4.w4_prompt_attention(q, k, clean, starts(lens))), q, k, clean, lens)
+
+
+def test_prompt_attention_times_out():
+    """A barrier that expects an arrival too many: the wait gives up, the error word says so, and the next call clears it."""
+    ws = w4.Workspace()
+    q, k, v = (randn(i, 200, h, 64) for i, h in ((1, 4), (2, 2), (3, 2)))
+    w4.w4_prompt_attention(q, k, v, starts([200]), workspace=ws, flags=w4.FLAG_TEST_TIMEOUT, wait_limit_cycles=2_000_000)
+    assert w4.STATUS[w4.w4_last_device_error(ws)] == "W4_ERR_TIMEOUT"
+    for i in range(2):
+        q2, k2, v2 = big([600, 700], 32, 8, 128)
+        w4.w4_prompt_attention(q2, k2, v2, starts([600, 700]), workspace=ws, flags=w4.FLAG_TEST_TIMEOUT, wait_limit_cycles=2_000_000)
+    check_prompt(q, k, v, [200], workspace=ws)
+    assert w4.w4_last_device_error(ws) == 0
+
+
 @pytest.mark.parametrize("dtype", ["f16", "bf16"])
 def test_prompt_attention_scores_that_climb(dtype):
     """Each key tops all before it by far: the running maximum moves at every step."""

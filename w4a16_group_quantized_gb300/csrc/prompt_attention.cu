@@ -20,9 +20,9 @@
 //   1 looking warp        sees the tiles' last V (the ones with rows that their first queries do not see)
 // V is used as it stands, an MN-major operand.
 //
-// Rows that a query does not see have weight 0, but 0 * NaN is NaN. Rows behind the sequence's end are made 0 in shared
-// memory; where the tile's last 128 rows of V hold an infinity or NaN, the tile's rows are computed by themselves after all,
-// one warp a row.
+// Rows that a query does not see have weight 0, but 0 * NaN is NaN. The last 128 rows of V of a tile, of which its first queries do
+// not see all, go into the product with zeros in the place of rows behind the sequence's end and of values that are not
+// finite; those are added at the end, read from memory again, to the rows that do see them.
 //
 // Every wait is bounded (ptx.cuh).
 #include <atomic>
@@ -64,7 +64,8 @@ struct PromptCfg {
   static constexpr uint32_t kO = TILES * kTile;        // O's first column; O of the second tile D further
   static constexpr uint32_t kColumns = TILES == 2 ? 512 : 256;
   static_assert(kO + TILES * D <= kColumns, "tensor memory");
-  static constexpr int kRegsLaunch = TILES == 2 ? 168 : 128, kRegsSoftmax = 208, kRegsOthers = TILES == 2 ? 80 : 48;
+  static constexpr int kRegsLaunch = TILES == 2 ? 168 : 128, kRegsSoftmax = TILES == 2 ? 216 : 208,
+                       kRegsOthers = TILES == 2 ? 72 : 48;
   static_assert(TILES * kRegsSoftmax + kRegsOthers <= (TILES + 1) * kRegsLaunch, "the registers that the block was launched with");
 };
 
@@ -72,49 +73,6 @@ __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
-}
-
-// One row by one warp in fp32: 32 keys at a time, a key a lane for the products with q, four of the head's values a lane for
-// the sums.
-template <int DT>
-__device__ __noinline__ void one_row(const PromptParams &p, int begin, int row, int h) {
-  const int lane = threadIdx.x % 32;
-  const uint16_t *q = p.q + row * p.ldq + static_cast<int64_t>(h) * p.head_dim;
-  const uint16_t *k = p.k + static_cast<int64_t>(h / p.r) * p.head_dim;
-  const uint16_t *v = p.v + static_cast<int64_t>(h / p.r) * p.head_dim;
-  float m = -INFINITY, l = 0.0f, o[4] = {};
-  for (int key0 = begin; key0 <= row; key0 += 32) {
-    const int key = key0 + lane;
-    float s = -INFINITY;
-    if (key <= row) {
-      s = 0.0f;
-      for (int d = 0; d < p.head_dim; ++d) s = fmaf(value_f32<DT>(q[d]), value_f32<DT>(k[key * p.ldk + d]), s);
-      s *= p.scale;
-    }
-    float top = s;
-#pragma unroll
-    for (int i = 16; i > 0; i /= 2) top = fmaxf(top, __shfl_xor_sync(kAll, top, i));
-    const float now = fmaxf(m, top);
-    const float alpha = now == m ? 1.0f : ex2(m - now);
-    m = now;
-    const float w = key <= row ? ex2(s - now) : 0.0f;
-    l = l * alpha + w;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) o[e] *= alpha;
-    const int count = min(32, row - key0 + 1);
-    for (int j = 0; j < count; ++j) {
-      const float wj = __shfl_sync(kAll, w, j);
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (4 * lane + e < p.head_dim) o[e] = fmaf(wj, value_f32<DT>(v[(key0 + j) * p.ldv + 4 * lane + e]), o[e]);
-    }
-  }
-#pragma unroll
-  for (int i = 16; i > 0; i /= 2) l += __shfl_xor_sync(kAll, l, i);
-  uint16_t *out = p.out + row * p.ldo + static_cast<int64_t>(h) * p.head_dim;
-#pragma unroll
-  for (int e = 0; e < 4; ++e)
-    if (4 * lane + e < p.head_dim) out[4 * lane + e] = out_bits<DT>(o[e] / l);
 }
 
 template <int R>
@@ -125,6 +83,7 @@ template <int R>
 __device__ __forceinline__ void regs_up() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R));
 }
+
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
@@ -157,8 +116,29 @@ __device__ __forceinline__ uint32_t weights2(float lo, float hi) {
   return d;
 }
 
+// Adds what is not finite of 8 of V's values (at v) of the rows from `first` up to and with `row` to 8 values of a row of the output (a
+// weight is positive): infinities stay infinities, both signs or a NaN make NaN.
+template <int DT>
+__device__ __noinline__ uint4 add_odd(uint4 out, const uint16_t *v, int64_t ldv, int first, int row) {
+  constexpr uint32_t kInf = DT == kDtypeBf16 ? 0x7F80u : 0x7C00u;
+  float f[8];
+  const uint32_t w[4] = {out.x, out.y, out.z, out.w};
+#pragma unroll
+  for (int e = 0; e < 8; ++e) f[e] = value_f32<DT>(w[e / 2] >> (16 * (e % 2)) & 0xffffu);
+  for (int key = first; key <= row; ++key) {
+    const uint4 x = *reinterpret_cast<const uint4 *>(v + key * ldv);
+    const uint32_t y[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const uint32_t bits = y[e / 2] >> (16 * (e % 2)) & 0xffffu;
+      if ((bits & kInf) == kInf) f[e] += value_f32<DT>(bits);
+    }
+  }
+  return make_uint4(out_bits2<DT>(f[0], f[1]), out_bits2<DT>(f[2], f[3]), out_bits2<DT>(f[4], f[5]), out_bits2<DT>(f[6], f[7]));
+}
+
 // What a block works on.
-struct Work {
+struct __align__(16) Work {
   int begin, len;  // the sequence
   int row0;        // the block's first row of it
   int head;
@@ -229,7 +209,7 @@ __global__ void __launch_bounds__(PromptCfg<D, TILES>::kThreads, 3 - TILES)
   using C = PromptCfg<D, TILES>;
   constexpr int S = C::kStages, kIssue = 4 * TILES;  // the first warp that is not a softmax warp
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t q_bar[2], full_bar[S], free_bar[TILES][S], s_bar[2], p_bar[2][2], o_bar[2], last_bar[2], look_bar[2], drain_bar[2];
+  __shared__ __align__(8) uint64_t q_bar[2], full_bar[S], free_bar[TILES][S], s_bar[2], p_bar[2][2], o_bar[2], last_bar[2], look_bar[2], turn_bar[2], drain_bar[2];
   __shared__ uint32_t tmem_sh, abort_sh;
   __shared__ uint32_t odd_sh[2];  // V of the tile's last step holds what is not finite
   __shared__ Work work_sh;
@@ -259,6 +239,7 @@ __global__ void __launch_bounds__(PromptCfg<D, TILES>::kThreads, 3 - TILES)
       mbar_init(smem_u32(&o_bar[i]), 1);
       mbar_init(smem_u32(&last_bar[i]), 1);
       mbar_init(smem_u32(&look_bar[i]), 1);
+      mbar_init(smem_u32(&turn_bar[i]), 1);
       odd_sh[i] = 0;
     }
     for (int i = 0; i < S; ++i) {
@@ -348,12 +329,6 @@ __global__ void __launch_bounds__(PromptCfg<D, TILES>::kThreads, 3 - TILES)
           w2[j] = weights2<DT>(a, b);
         }
       };
-      auto first_half = [&]() {
-        const float off = m == -INFINITY ? 0.0f : -m * p.scale;
-        off2 = pack2(off, off);
-        sum[0] = sum[1] = 0ull;
-        weights(0);
-      };
       auto hand_over = [&](int c) {
         tmem_st_32x32b_x32(s_at + 16 * c, w2);
         tmem_wait_st();
@@ -361,24 +336,30 @@ __global__ void __launch_bounds__(PromptCfg<D, TILES>::kThreads, 3 - TILES)
         __syncwarp();
         if (lane == 0) mbar_arrive(p_full + 4 * c);  // (c 0, 2: the two barriers)
       };
-      if (i == 0) m = row_top();
-      first_half();
-      const float now = row_top();
-      if (__any_sync(kAll, (now - m) * p.scale > kSlack)) {
-        // (the step before this one's S is complete, and with it O)
-        const float alpha = now == m ? 1.0f : ex2((m - now) * p.scale);
-        m = now;
-        l *= alpha;
+      // (a loop, so that the code is there once: it fills much of the instruction cache)
+#pragma unroll 1
+      for (;;) {
+        const float off = m == -INFINITY ? 0.0f : -m * p.scale;
+        off2 = pack2(off, off);
+        sum[0] = sum[1] = 0ull;
+        weights(0);
+        const float now = row_top();
+        if (!__any_sync(kAll, (now - m) * p.scale > kSlack)) break;
+        if (i > 0) {
+          // (the step before this one's S is complete, and with it O)
+          const float alpha = now == m ? 1.0f : ex2((m - now) * p.scale);
+          l *= alpha;
+#pragma unroll 1
+          for (int c = 0; c < D / 16; ++c) {
+            uint32_t o[16];
+            tmem_ld_32x32b_x16(o_at + 16 * c, o);
+            tmem_wait_ld();
 #pragma unroll
-        for (int c = 0; c < D / 16; ++c) {
-          uint32_t o[16];
-          tmem_ld_32x32b_x16(o_at + 16 * c, o);
-          tmem_wait_ld();
-#pragma unroll
-          for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha);
-          tmem_st_32x32b_x16(o_at + 16 * c, o);
+            for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha);
+            tmem_st_32x32b_x16(o_at + 16 * c, o);
+          }
         }
-        first_half();
+        m = now;
       }
       hand_over(0);
       weights(2);
@@ -388,11 +369,19 @@ __global__ void __launch_bounds__(PromptCfg<D, TILES>::kThreads, 3 - TILES)
       l += a + b;
     }
     if (ok && steps > 0) ok = warp_wait(smem_u32(&o_bar[tile]), 0, abort_flag, p.err, p.wait_limit);
-    if (ok && steps > 0) ok = warp_wait(smem_u32(&look_bar[tile]), 0, abort_flag, p.err, p.wait_limit);
+    for (int i = 0; i <= tile; ++i)
+      if (ok && steps > 0) ok = warp_wait(smem_u32(&look_bar[i]), 0, abort_flag, p.err, p.wait_limit);
     if (ok && steps > 0) {
       tc_fence_after();
-      const int row = w.row0 + tile * kTile + r;
-      const bool odd = *static_cast<volatile uint32_t *>(&odd_sh[tile]) != 0;
+      // (the block's place is read again: in registers through the loop it cost the scores theirs)
+      Work e;
+      asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(e.begin), "=r"(e.len), "=r"(e.row0), "=r"(e.head)
+                   : "r"(smem_u32(&work_sh))
+                   : "memory");
+      const int row = e.row0 + tile * kTile + r;
+      // (the second tile's rows see all of the first one's last V)
+      const bool odd = (*static_cast<volatile uint32_t *>(&odd_sh[0]) | *static_cast<volatile uint32_t *>(&odd_sh[tile])) != 0;
       const float inv = 1.0f / l;
       // each warp's rows by way of the tile's place of Q, which is done with, so that they are stored as whole lines; the 16-byte
       // pieces of a row are exchanged against bank conflicts
@@ -415,20 +404,17 @@ __global__ void __launch_bounds__(PromptCfg<D, TILES>::kThreads, 3 - TILES)
         }
       }
       __syncwarp();
-      uint16_t *out = p.out + static_cast<int64_t>(w.begin + row - lane) * p.ldo + static_cast<int64_t>(w.head) * p.head_dim;
-      if (!odd) {
+      uint16_t *out = p.out + static_cast<int64_t>(e.begin + row - lane) * p.ldo + static_cast<int64_t>(e.head) * p.head_dim;
 #pragma unroll 4
-        for (int i = lane; i < 32 * kPieces; i += 32) {
-          const int rr = i / kPieces, c = i % kPieces;
-          if (row - lane + rr < w.len && 8 * c < p.head_dim)
-            *reinterpret_cast<uint4 *>(out + rr * p.ldo + 8 * c) = lds128(place + rr * D * 2 + 16 * (c ^ (rr % kPieces)));
+      for (int i = lane; i < 32 * kPieces; i += 32) {
+        const int rr = i / kPieces, c = i % kPieces;
+        if (row - lane + rr < e.len && 8 * c < p.head_dim) {
+          uint4 x = lds128(place + rr * D * 2 + 16 * (c ^ (rr % kPieces)));
+          if (odd)
+            x = add_odd<DT>(x, p.v + static_cast<int64_t>(e.head / p.r) * p.head_dim + 8 * c, p.ldv, e.begin + e.row0, e.begin + row - lane + rr);
+          *reinterpret_cast<uint4 *>(out + rr * p.ldo + 8 * c) = x;
         }
       }
-      if (odd)
-        for (int i = 0; i < 32; ++i) {
-          const int rr = w.row0 + tile * kTile + warp % 4 * 32 + i;
-          if (rr < w.len) one_row<DT>(p, w.begin, w.begin + rr, w.head);
-        }
     }
   } else {
     regs_down<C::kRegsOthers>();
@@ -472,6 +458,9 @@ __global__ void __launch_bounds__(PromptCfg<D, TILES>::kThreads, 3 - TILES)
         // (the looking warp has waited for the last steps' V, and may have changed it)
         ok = i < n0 - 1 ? landed(2 * i + 1) : warp_wait(smem_u32(&look_bar[i - (n0 - 1)]), 0, abort_flag, p.err, p.wait_limit);
         if (ok && i + 1 < steps) ok = landed(2 * i + 2);
+        // the tiles' products go in turns: run together they would take twice as long each and leave the tensor pipe idle together
+        if (ok && two && (tile == 0 ? i > 0 : i < n0))
+          ok = warp_wait(smem_u32(&turn_bar[tile]), (tile == 0 ? i - 1 : i) & 1, abort_flag, p.err, p.wait_limit);
         if (ok) ok = warp_wait(p_full, i & 1, abort_flag, p.err, p.wait_limit);
         if (!ok) break;
         tc_fence_after();
@@ -489,6 +478,7 @@ __global__ void __launch_bounds__(PromptCfg<D, TILES>::kThreads, 3 - TILES)
           } else {
             mma_commit(smem_u32(&o_bar[tile]));
           }
+          if (two) mbar_arrive(smem_u32(&turn_bar[1 - tile]));
         }
         __syncwarp();
       }
@@ -545,6 +535,20 @@ __global__ void __launch_bounds__(PromptCfg<D, TILES>::kThreads, 3 - TILES)
           for (; i < stop; i += 512) asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(i), "r"(0u) : "memory");
         }
         const bool odd = __any_sync(kAll, (carries & 0x80008000u) != 0);
+        if (odd) {
+          for (int h = 0; h < D / 64; ++h)
+#pragma unroll 1
+            for (uint32_t i = at + h * C::kHalf + 16 * lane; i < at + h * C::kHalf + live * 128; i += 512) {
+              const uint4 x = lds128(i);
+              auto finite = [&](uint32_t w) {
+                const uint32_t bad = ((w & kInf) + kOne) & 0x80008000u;
+                return w & ~((bad >> 15) * 0xffffu);
+              };
+              asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(i), "r"(finite(x.x)), "r"(finite(x.y)), "r"(finite(x.z)),
+                           "r"(finite(x.w))
+                           : "memory");
+            }
+        }
         fence_proxy_async_shared();
         __syncwarp();
         if (lane == 0) {
