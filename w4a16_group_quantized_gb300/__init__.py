@@ -683,16 +683,16 @@ def _heads(t: torch.Tensor, name: str, dtype, shape, device: int):
     heads one after another and lie evenly apart."""
     if t.dtype is not dtype or t.shape != shape or t.get_device() != device:
         raise ValueError(f"{name} must be {dtype} {list(shape)} on cuda:{device}")
-    return _heads_at(t, name, shape)
+    if t.is_contiguous():
+        return t.data_ptr(), shape[-2] * shape[-1]
+    return _apart(t, name)
 
 
-def _heads_at(t: torch.Tensor, name: str, shape):
-    """_heads without its first checks, for the tensor that the others are checked against."""
+def _apart(t: torch.Tensor, name: str):
+    """_heads of a tensor that is not contiguous, its type and shape apart."""
+    shape, strides = t.shape, t.stride()
     heads, dim = shape[-2:]
     width = heads * dim
-    if t.is_contiguous():
-        return t.data_ptr(), width
-    strides = t.stride()
     if (dim > 1 and strides[-1] != 1) or (heads > 1 and strides[-2] != dim):
         raise ValueError(f"the heads of {name} must follow one another in a row")
     if len(shape) == 3:
@@ -732,7 +732,7 @@ def w4_qk_norm_rope(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Te
             (k_weight is not None and k_weight.requires_grad)):
         _no_gradient("w4_qk_norm_rope")
     T, hq, dim = shape
-    q_at, ldq = _heads_at(q, "q", shape)
+    q_at, ldq = (q.data_ptr(), hq * dim) if q.is_contiguous() else _apart(q, "q")
     if q_out is None:
         q_out = _empty(shape, dtype, q.device, stream)
         qo_at, ldqo = q_out.data_ptr(), hq * dim
@@ -747,7 +747,7 @@ def w4_qk_norm_rope(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Te
         if len(shape) != 3 or shape[0] != T or shape[2] != dim or k.dtype is not dtype or k.get_device() != device:
             raise ValueError(f"k must be {dtype} [{T}, heads, {dim}] on cuda:{device}")
         hk = shape[1]
-        k_at, ldk = _heads_at(k, "k", shape)
+        k_at, ldk = (k.data_ptr(), hk * dim) if k.is_contiguous() else _apart(k, "k")
         if k_out is None:
             k_out = _empty(shape, dtype, q.device, stream)
             ko_at, ldko = k_out.data_ptr(), hk * dim
@@ -821,7 +821,7 @@ def w4_kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cach
     T, heads, dim = shape
     batch = lens.numel()
     pages, _, page, max_pages = _cache(k_cache, v_cache, k_scale, v_scale, table, batch, heads, dim, device)
-    k_at, ldk = _heads_at(k, "k", shape)
+    k_at, ldk = (k.data_ptr(), heads * dim) if k.is_contiguous() else _apart(k, "k")
     v_at, ldv = _heads(v, "v", dtype, shape, device)
     a = _KV_APPEND_ARGS.pack(k_at, v_at, k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
                              table.data_ptr(), _like(cu, "cu", _I32, (batch + 1,), device),
@@ -854,7 +854,7 @@ def w4_kv_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     else:
         batch, n, hq, dim = shape
     pages, hk, page, max_pages = _cache(k_cache, v_cache, k_scale, v_scale, table, batch, None, dim, device)
-    q_at, ldq = _heads_at(q, "q", shape)
+    q_at, ldq = (q.data_ptr(), hq * dim) if q.is_contiguous() else _apart(q, "q")
     if out is None:
         out = _empty(shape, dtype, q.device, stream)
         o_at, ldo = out.data_ptr(), hq * dim
@@ -895,8 +895,8 @@ def w4_prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu: t
     hk = k_shape[1]
     if k_shape[0] != T or k_shape[2] != dim or k.dtype is not dtype or k.get_device() != device:
         raise ValueError(f"k must be {dtype} [{T}, heads, {dim}] on cuda:{device}")
-    q_at, ldq = _heads_at(q, "q", shape)
-    k_at, ldk = _heads_at(k, "k", k_shape)
+    q_at, ldq = (q.data_ptr(), hq * dim) if q.is_contiguous() else _apart(q, "q")
+    k_at, ldk = (k.data_ptr(), hk * dim) if k.is_contiguous() else _apart(k, "k")
     v_at, ldv = _heads(v, "v", dtype, k_shape, device)
     if out is None:
         out = _empty(shape, dtype, q.device, stream)

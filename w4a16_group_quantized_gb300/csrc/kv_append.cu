@@ -11,6 +11,8 @@
 // and while one head's maximum is found and its values converted, which stay in registers between the two, the next
 // one's are on their way. Bound by memory for prompts; by latency (cu, lens, table, old scale, one after another) for a
 // decode step.
+#include <type_traits>
+
 #include "e4m3.cuh"
 #include "gemm_common.cuh"
 #include "internal.h"
@@ -23,7 +25,6 @@ namespace {
 using namespace detail;
 
 constexpr int kAppendThreads = 128;
-constexpr int kHeldPieces = 8;  // 16-byte pieces of a run that a thread keeps
 
 struct AppendParams {
   const uint16_t *k, *v;
@@ -96,7 +97,8 @@ struct Run {
   int row, off, n, at;
 };
 
-template <int DT>
+// HELD: 16-byte pieces of a run that a thread keeps (what is more is read twice).
+template <int DT, int HELD>
 __device__ __forceinline__ void append_run(const AppendParams &p, const Run &run, int first, int last, uint32_t *most_of_warp) {
   const int pieces = p.head_dim / 8;  // 16-byte pieces of a row
   const int count = run.n * pieces;
@@ -105,20 +107,21 @@ __device__ __forceinline__ void append_run(const AppendParams &p, const Run &run
     const int64_t ld = task % 2 ? p.ldv : p.ldk;
     return reinterpret_cast<const uint4 *>((task % 2 ? p.v : p.k) + (run.row + r) * ld + h * p.head_dim + 8 * (i - r * pieces));
   };
-  uint4 next[kHeldPieces];
+  uint4 next[HELD];
   auto load = [&](int task) {
 #pragma unroll
-    for (int j = 0; j < kHeldPieces; ++j) {
+    for (int j = 0; j < HELD; ++j) {
       const int i = j * kAppendThreads + threadIdx.x;
       next[j] = make_uint4(0, 0, 0, 0);
       if (i < count) next[j] = *source(task, i);
     }
   };
-  load(first);
+  load(first);  // (beside the table's entry)
+  if (run.at < 0 || run.at >= p.pages) return;
   for (int task = first; task < last; ++task) {
-    uint4 keep[kHeldPieces];
+    uint4 keep[HELD];
 #pragma unroll
-    for (int j = 0; j < kHeldPieces; ++j) keep[j] = next[j];
+    for (int j = 0; j < HELD; ++j) keep[j] = next[j];
     const int64_t ph = static_cast<int64_t>(run.at) * p.heads + task / 2;
     float *scale = (task % 2 ? p.v_scale : p.k_scale) + ph;
     const float old = run.off > 0 ? *scale : 0.0f;
@@ -129,8 +132,8 @@ __device__ __forceinline__ void append_run(const AppendParams &p, const Run &run
     auto largest = [&](auto two) {
       uint32_t m2 = 0;
 #pragma unroll
-      for (int j = 0; j < kHeldPieces; ++j) m2 = two(two(two(two(m2, keep[j].x), keep[j].y), keep[j].z), keep[j].w);
-      for (int i = kHeldPieces * kAppendThreads + threadIdx.x; i < count; i += kAppendThreads) {
+      for (int j = 0; j < HELD; ++j) m2 = two(two(two(two(m2, keep[j].x), keep[j].y), keep[j].z), keep[j].w);
+      for (int i = HELD * kAppendThreads + threadIdx.x; i < count; i += kAppendThreads) {
         const uint4 w = *source(task, i);
         m2 = two(two(two(two(m2, w.x), w.y), w.z), w.w);
       }
@@ -154,11 +157,11 @@ __device__ __forceinline__ void append_run(const AppendParams &p, const Run &run
     dst += run.off * p.head_dim;
     // (pieces of 8 codes follow one another as pieces of 8 values do)
 #pragma unroll
-    for (int j = 0; j < kHeldPieces; ++j) {
+    for (int j = 0; j < HELD; ++j) {
       const int i = j * kAppendThreads + threadIdx.x;
       if (i < count) reinterpret_cast<uint2 *>(dst)[i] = exact ? codes8<DT>(keep[j], inv) : codes8_any<DT>(keep[j], s);
     }
-    for (int i = kHeldPieces * kAppendThreads + threadIdx.x; i < count; i += kAppendThreads)
+    for (int i = HELD * kAppendThreads + threadIdx.x; i < count; i += kAppendThreads)
       reinterpret_cast<uint2 *>(dst)[i] = exact ? codes8<DT>(*source(task, i), inv) : codes8_any<DT>(*source(task, i), s);
     dst -= run.off * p.head_dim;
     if (run.off > 0 && grows) {
@@ -182,7 +185,7 @@ __device__ __forceinline__ void append_run(const AppendParams &p, const Run &run
   __syncthreads();  // the maxima have been read
 }
 
-template <int DT>
+template <int DT, int HELD>
 __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const __grid_constant__ AppendParams p) {
   __shared__ uint32_t most_of_warp[2 * (kAppendThreads / 32)];
   griddep_launch_dependents();
@@ -222,7 +225,7 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const __grid_
       row += run.n;
       if (run.off != 0 && run.row != begin) continue;  // inside a run of another block
       run.at = p.table[static_cast<int64_t>(b) * p.max_pages + pi];
-      if (run.at >= 0 && run.at < p.pages) append_run<DT>(p, run, first, last, most_of_warp);
+      append_run<DT, HELD>(p, run, first, last, most_of_warp);
     }
   }
 }
@@ -265,8 +268,14 @@ cudaError_t launch_kv_append(const KvAppendArgs &a, int num_sms, cudaStream_t st
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const cudaError_t e = a.dtype == kDtypeBf16 ? cudaLaunchKernelEx(&cfg, kv_append_kernel<kDtypeBf16>, p)
-                                              : cudaLaunchKernelEx(&cfg, kv_append_kernel<kDtypeF16>, p);
+  // short pages need few registers, and more blocks are resident (21 pieces of up to 700 rows of 6 heads of 48, pages of
+  // 16: 11.4 us with 8 pieces kept, 6.8 with 2; prompts into pages of 64 with heads of 128 need all 8 of them)
+  const bool few = a.page * (a.head_dim / 8) <= 2 * kAppendThreads;
+  auto go = [&](auto dt) {
+    constexpr int DT = decltype(dt)::value;
+    return few ? cudaLaunchKernelEx(&cfg, kv_append_kernel<DT, 2>, p) : cudaLaunchKernelEx(&cfg, kv_append_kernel<DT, 8>, p);
+  };
+  const cudaError_t e = a.dtype == kDtypeBf16 ? go(std::integral_constant<int, kDtypeBf16>{}) : go(std::integral_constant<int, kDtypeF16>{});
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
