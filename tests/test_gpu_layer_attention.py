@@ -62,3 +62,30 @@ def test_example_runs(layer):
     m = importlib.util.module_from_spec(spec)
     spec.loader.exec_module(m)
     assert len(m.main(["--tokens", "130", "--hidden", "256", "--inter", "128", "--experts", "8", "--k", "2", "--adapters", "3"])) == 5
+
+
+@pytest.mark.parametrize("m", [9, 16, 33, 64, 130])
+def test_a_gemm_right_behind_few_prompts(m):
+    """Tensor memory is taken by the prompts' blocks before the next grid may begin: a long call, a short one of few blocks behind it and
+    a GEMM behind that, all enqueued at once, with blocks of all three on one SM."""
+    w = w4.w4_repack(*w4.w4_pack(randn(2, 256, 256), 128), 256, 256, 128)
+    ws, ws2 = w4.Workspace(), w4.Workspace()
+    k, v = randn(3, 8192, 8, 64), randn(4, 8192, 8, 64)
+    cache = (*(torch.zeros(128, 8, 64, 64, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn) for _ in range(2)),
+             *(torch.zeros(128, 8, device="cuda") for _ in range(2)))
+    table, cu, zero = ints([list(range(128))]), ints([0, 8192]), ints([0])
+    q, few = randn(5, 300, 4, 64), starts([100, 200])
+    outs = []
+
+    def run():
+        w4.w4_kv_append(k, v, *cache, table, cu, zero)
+        y = w4.w4_prompt_attention(q, q, q, few, workspace=ws)
+        outs.append((y, w4.w4a16_gemm(y.flatten(1)[:m], w, 256, 256, 128, workspace=ws2)))
+
+    run()
+    torch.cuda.synchronize()
+    for _ in range(20):
+        run()
+    torch.cuda.synchronize()
+    assert w4.w4_last_device_error(ws) == 0
+    assert all(torch.equal(a, outs[0][0]) and torch.equal(b, outs[0][1]) for a, b in outs[1:])

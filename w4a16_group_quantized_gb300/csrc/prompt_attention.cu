@@ -218,17 +218,6 @@ __global__ void __launch_bounds__(PromptCfg<D, TILES>::kThreads, 3 - TILES)
   const int warp = __shfl_sync(kAll, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
   volatile uint32_t *abort_flag = &abort_sh;
 
-  griddep_launch_dependents();
-  griddep_wait();
-  if (blockIdx.x == 0 && threadIdx.x == 0) *p.err = 0;
-  if (warp == 0) {
-    Work w;
-    const bool any = find_work(p, TILES * kTile, &w);
-    if (lane == 0) {
-      work_sh = w;
-      any_sh = any;
-    }
-  }
   if (threadIdx.x == 32) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&q_bar[i]), 1 + (i == 0 ? p.test_extra : 0));
@@ -249,14 +238,27 @@ __global__ void __launch_bounds__(PromptCfg<D, TILES>::kThreads, 3 - TILES)
     abort_sh = 0;
     fence_mbar_init();
   }
+  // The next grid may begin only once every block has its tensor memory: a GEMM's blocks take theirs before they wait for this grid,
+  // and on a shared SM this block would wait for them and they for it.
   if (warp == kIssue) {
     tmem_alloc(smem_u32(&tmem_sh), C::kColumns);
     tmem_relinquish();
+    if (lane == 0) griddep_launch_dependents();
   }
   if (warp == kIssue + 2 && elect_one()) {
     prefetch_tensormap(&q_map);
     prefetch_tensormap(&k_map);
     prefetch_tensormap(&v_map);
+  }
+  griddep_wait();
+  if (blockIdx.x == 0 && threadIdx.x == 0) *p.err = 0;
+  if (warp == 0) {
+    Work w;
+    const bool any = find_work(p, TILES * kTile, &w);
+    if (lane == 0) {
+      work_sh = w;
+      any_sh = any;
+    }
   }
   tc_fence_before();
   __syncwarp();
