@@ -89,3 +89,25 @@ def test_a_gemm_right_behind_few_prompts(m):
     torch.cuda.synchronize()
     assert w4.w4_last_device_error(ws) == 0
     assert all(torch.equal(a, outs[0][0]) and torch.equal(b, outs[0][1]) for a, b in outs[1:])
+
+
+@pytest.mark.parametrize("dim, T", [(64, 300), (128, 300), (128, 1400)])
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+def test_a_prompt_alone_and_among_others(dim, T, dtype):
+    """A row of the prompts has the same bits whatever stands beside it: other prompts, later rows of its own, NaN and infinities there,
+    and scores that rise by far more than the slack with which a maximum may lag."""
+    q, k, v = ((randn(i, T, 40, dim) * s).to(dtype) for i, s in ((1, 4.0), (2, 3.0), (3, 1.0)))
+    k, v = k[:, :8], v[:, :8]
+    k *= torch.linspace(0.1, 3.0, T, device="cuda")[:, None, None].to(dtype)  # maxima that move often
+    cu = [0, 1, 60, 61, 190, T]
+    together = w4.w4_prompt_attention(q, k, v, ints(cu))
+    assert torch.isfinite(together).all()
+    for a, b in zip(cu, cu[1:]):
+        assert torch.equal(w4.w4_prompt_attention(q[a:b].contiguous(), k[a:b].contiguous(), v[a:b].contiguous(), ints([0, b - a])), together[a:b])
+    # later rows changed
+    at = cu[4] + 17
+    for bad in (float("nan"), float("inf"), 100.0):
+        q2, k2, v2 = q.clone(), k.clone(), v.clone()
+        for t in (q2, k2, v2):
+            t[at:] = bad
+        assert torch.equal(w4.w4_prompt_attention(q2, k2, v2, ints(cu))[:at], together[:at])

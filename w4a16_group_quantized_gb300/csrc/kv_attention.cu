@@ -567,7 +567,7 @@ __global__ void __launch_bounds__(32 * KvCfg<D, ROWS>::kWarps, 1) kv_attention_k
         float alpha[RR];
 #pragma unroll
         for (int r2 = 0; r2 < RR; ++r2) {
-          const float now = fmaxf(m[r2], top[r2]);
+          const float now = top[r2] > m[r2] + kSlack ? top[r2] : m[r2];  // (a row's own scores alone say when)
           alpha[r2] = now == m[r2] ? 1.0f : ex2(m[r2] - now);
           m[r2] = now;
           l[r2] *= alpha[r2];

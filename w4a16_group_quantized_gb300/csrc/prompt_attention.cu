@@ -345,8 +345,11 @@ __global__ void __launch_bounds__(PromptCfg<D, TILES>::kThreads, 3 - TILES)
         off2 = pack2(off, off);
         sum[0] = sum[1] = 0ull;
         weights(0);
-        const float now = row_top();
-        if (!__any_sync(kAll, (now - m) * p.scale > kSlack)) break;
+        const float top = row_top();
+        // (a row's own scores alone say when its maximum moves: what stands beside it does not change its roundings)
+        const bool passed = (top - m) * p.scale > kSlack;
+        if (!__any_sync(kAll, passed)) break;
+        const float now = passed ? top : m;
         if (i > 0) {
           // (the step before this one's S is complete, and with it O)
           const float alpha = now == m ? 1.0f : ex2((m - now) * p.scale);
