@@ -643,7 +643,8 @@ W4_API int w4_qk_norm_rope(const w4_rope_args *args, void *stream);
  * k_cache_dev, v_cache_dev  16-byte aligned; k_scale_dev, v_scale_dev fp32.
  * table_dev     int32 [batch, max_pages]; cu_dev int32 [batch + 1], ascending;
  *               lens_dev int32 [batch]: what the cache holds before the call.
- * head_dim a multiple of 16, at most 128; page a multiple of 16, at most 256.
+ * head_dim a multiple of 16, at most 128; page a multiple of 16, at most 256;
+ * at most 32767 heads, and max_pages * page below 2^31 - 1024.
  */
 typedef struct {
     const void *k_dev;
@@ -688,7 +689,10 @@ W4_API int w4_kv_append(const w4_kv_append_args *args, void *stream);
  *               ldo values apart (multiples of 8), 16-byte aligned.
  * lens_dev      int32 [batch], the new tokens included.
  * q_heads a multiple of k_heads; head_dim a multiple of 16, at most 128; page a
- * multiple of 16, at most 256; n at most 256; scale positive and finite.
+ * multiple of 16, at most 256; n at most 256; at most 32767 key heads; scale
+ * positive and finite; max_pages * page below 2^31 - 1024. With 16 query rows
+ * that share a key head as an item: at most 2^24 items, and at most 2^40 of
+ * items * max_pages * page / 16.
  * The workspace is at least w4_kv_attention_workspace_bytes(...) bytes,
  * 256-byte aligned. Its first word is left as it is.
  */
@@ -728,7 +732,8 @@ W4_API size_t w4_kv_attention_workspace_bytes(int32_t batch, int32_t n, int32_t 
  *
  * k and v of head h / (q_heads / k_heads). Rows outside [cu[0], cu[batch]) are
  * left as they are. What rows that a query does not see hold, NaN and
- * infinities included, has no part in its output.
+ * infinities included, has no part in its output: a prompt's rows have the
+ * same bits alone and among others.
  *
  * Numerics: sums and the softmax's maximum and sum are fp32; the weights enter
  * the second product in dtype; one rounding at the end.

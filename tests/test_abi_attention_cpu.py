@@ -70,6 +70,12 @@ def test_append_refusals(lib):
         assert append(lib, **kw) == MISALIGNED, kw
 
 
+def test_more_heads_than_a_grid_has_room_for(lib):
+    """Blocks are dealt by heads of k and of v along a grid's second axis, 65535 at most."""
+    for heads in (32768, 65535):
+        assert append(lib, heads=heads, ldk=64 * heads, ldv=64 * heads) == SHAPE
+
+
 def attend(lib, ws=PTR, ws_bytes=1 << 40, **kw):
     a = dict(q=PTR, kc=PTR, vc=PTR, ks=PTR, vs=PTR, table=PTR, lens=PTR, out=PTR, ldq=512, ldo=512, pages=9, batch=2, n=1, max_pages=3, hq=8,
              hk=2, dim=64, page=16, dtype=0, scale=0.125) | kw

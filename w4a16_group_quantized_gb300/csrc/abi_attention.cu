@@ -41,7 +41,7 @@ int check_rows(int64_t ld, int64_t heads, int64_t head_dim) {
 int check_cache(int64_t pages, int32_t batch, int32_t max_pages, int32_t heads, int32_t head_dim, int32_t page) {
   if (pages < 1 || batch < 0 || max_pages < 1 || heads < 1 || head_dim < 1 || page < 1) return W4_ERR_INVALID_ARG;
   if (head_dim % 16 != 0 || head_dim > w4::kKvMaxDim || page % 16 != 0 || page > w4::kKvMaxPage || pages > kMaxDim ||
-      heads > 65535 || static_cast<int64_t>(max_pages) * page > kMaxDim - 1024)
+      heads > 32767 || static_cast<int64_t>(max_pages) * page > kMaxDim - 1024)
     return W4_ERR_UNSUPPORTED_SHAPE;
   return W4_OK;
 }
