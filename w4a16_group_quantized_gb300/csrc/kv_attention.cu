@@ -70,7 +70,7 @@ struct Deal {
 // kItemCost ones for its beginning and one for each tile.
 struct CutItem {
   int32_t b, j;        // sequence and item of it
-  int32_t last;        // the warp that holds the item's last tile
+  int32_t first, last; // the warps that hold the item's first and last tile
   int32_t warps;       // of a block that have stretches
   int64_t begin, end;  // its tiles
   Deal deal;
@@ -83,11 +83,12 @@ struct KvParams {
   const int32_t *table, *lens;
   uint16_t *out;
   int32_t *workers;  // how many warps have a stretch
-  int32_t *cut;      // [workers]: whether cuts has an item
+  int32_t *cut;      // [workers], or [items] by_item: whether cuts has an item
   CutItem *cuts;
   float *sums;     // [2 * warps]: O [rows][D], m [rows], l [rows], padded to 16 bytes, of a stretch's first and last item
   int64_t ldq, ldo, pages;
   int batch, n, max_pages, q_heads, k_heads, head_dim, page, r, row_tiles, rows, items;  // items of a sequence
+  int by_item;     // few items: an entry of cut and cuts for each, else for each warp
   float scale;
   FastDiv page_div, r_div, row_tiles_div;
 };
@@ -637,9 +638,11 @@ __global__ void __launch_bounds__(32 * KvCfg<D, ROWS>::kWarps, 1) kv_attention_k
         l[r2] += __shfl_xor_sync(kAll, l[r2], 2);
       }
       const int rows = min(16, p.n * p.r - (j - p.row_tiles_div.div(j) * p.row_tiles) * 16);
-      if (here && !whole) {
-        cut = true;
-        if (lane == 0) p.cuts[me] = CutItem{b, j, deal.holder(end - 1), warps, begin, end, deal};
+      if (here) {
+        cut = !whole;
+        const int entry = p.by_item ? b * p.items + j : me;
+        if (cut && lane == 0) p.cuts[entry] = CutItem{b, j, me, deal.holder(end - 1), warps, begin, end, deal};
+        if (p.by_item && lane == 0) p.cut[entry] = cut;
       }
       float *sums = p.sums + (static_cast<int64_t>(2 * me) + (here ? 1 : 0)) * p.rows * (D + 4);
       // a lane's sums of two rows: ROWS 16: rows g and g + 8 of two stretches of values, 8: rows 2 t and 2 t + 1 of one
@@ -688,7 +691,7 @@ __global__ void __launch_bounds__(32 * KvCfg<D, ROWS>::kWarps, 1) kv_attention_k
     }
   }
   if (!together) {
-    if (lane == 0 && from < to) p.cut[me] = cut;
+    if (!p.by_item && lane == 0 && from < to) p.cut[me] = cut;
     return;
   }
 
@@ -709,8 +712,9 @@ __global__ void __launch_bounds__(32 * KvCfg<D, ROWS>::kWarps, 1) kv_attention_k
   __syncthreads();
   const bool here = begin >= block_from, whole = here && end <= block_to;
   if (lane == 0 && from < to && !solo) {
-    p.cut[me] = here && !whole && warp == 0;
-    if (here && !whole && warp == 0) p.cuts[me] = CutItem{one_b, one_j, deal.holder(end - 1), warps, begin, end, deal};
+    const int entry = p.by_item ? one_b * p.items + one_j : me;
+    if (p.by_item ? here && warp == 0 : true) p.cut[entry] = here && !whole && warp == 0;
+    if (here && !whole && warp == 0) p.cuts[entry] = CutItem{one_b, one_j, me, deal.holder(end - 1), warps, begin, end, deal};
   }
   const int rows = min(ROWS, p.n * p.r - (one_j - p.row_tiles_div.div(one_j) * p.row_tiles) * 16);
   float *slot = p.sums + (static_cast<int64_t>(2) * blockIdx.x * warps + (here ? 1 : 0)) * p.rows * (D + 4);
@@ -738,134 +742,116 @@ __global__ void __launch_bounds__(32 * KvCfg<D, ROWS>::kWarps, 1) kv_attention_k
   }
 }
 
-constexpr int kAddThreads = 256;
+constexpr int kAddWarps = 8;
 
-// The items that are cut, their parts added in order. A block looks at warps [x * workers / gridDim.x, (x + 1) * workers / gridDim.x)
-// for items that begin there and adds ROWS rows of them: it lists the item's parts, finds what each row of each of them weighs,
-// and adds them up, a row by a group of D / 4 threads or, of one row, every kGroups-th part by each group.
-template <int DT, int D, int ROWS>
-__global__ void __launch_bounds__(kAddThreads) kv_add_kernel(const __grid_constant__ KvParams p) {
-  constexpr int kLane = D / 4, kGroups = kAddThreads / kLane;
-  static_assert(ROWS == 1 || ROWS == kGroups, "a group a row, or all groups one row");
-  __shared__ int32_t slots[kAddThreads];
-  __shared__ float factor[ROWS][kAddThreads];
-  __shared__ float row_m[ROWS], row_l[ROWS], row_f[ROWS];
-  __shared__ float4 part_o[ROWS == 1 ? kGroups : 1][kLane];
-  __shared__ int counts[kAddThreads / 32];
+// The items that are cut, their parts added in order: a block for each entry of `cut`, a warp a row or, APART, a block a row, whose
+// warps have every eighth part each. Which parts there are follows from the dealing: an entry is all that is read first,
+// then the parts' maxima and sums with the first of their values.
+template <int DT, int D, bool APART>
+__global__ void __launch_bounds__(32 * kAddWarps) kv_add_kernel(const __grid_constant__ KvParams p) {
+  constexpr int N = D / 32;    // values of a lane
+  constexpr int kAhead = 8;    // parts whose values are fetched together
+  __shared__ float part_o[APART ? kAddWarps : 1][D], part_m[kAddWarps], part_l[kAddWarps];
   griddep_launch_dependents();
   griddep_wait();
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int workers = *p.workers;
-  const int w0 = static_cast<int>(static_cast<int64_t>(blockIdx.x) * workers / gridDim.x);
-  const int w1 = static_cast<int>((static_cast<int64_t>(blockIdx.x) + 1) * workers / gridDim.x);
-  const int group = threadIdx.x / kLane, x = threadIdx.x % kLane;
-  const int row0 = blockIdx.y * ROWS;
-  __shared__ uint32_t cut_sh[kAddThreads / 32];
-  for (int w = w0, base0 = w0; base0 < w1; ++w) {
-    // the next warp that holds a cut item's beginning, by turns of the block's threads
-    if (w == base0) {
-      __syncthreads();
-      const uint32_t any = __ballot_sync(kAll, base0 + static_cast<int>(threadIdx.x) < w1 && p.cut[base0 + threadIdx.x] != 0);
-      if (lane == 0) cut_sh[warp] = any;
-      __syncthreads();
-    }
-    const int off = w - base0;
-    uint32_t bits = 0;
-    int word = off / 32;
-    if (off < kAddThreads) {
-      bits = cut_sh[word] & (0xffffffffu << (off % 32));
-      while (bits == 0 && ++word < kAddThreads / 32) bits = cut_sh[word];
-    }
-    if (bits == 0) {
-      base0 += kAddThreads;
-      w = base0 - 1;
-      continue;
-    }
-    w = base0 + 32 * word + __ffs(bits) - 1;
-    const CutItem it = p.cuts[w];
-    const int rows = min(min(16, p.n * p.r - (it.j - p.row_tiles_div.div(it.j) * p.row_tiles) * 16) - row0, ROWS);
-    if (rows <= 0) continue;
-    float4 o = make_float4(0, 0, 0, 0);
-    __syncthreads();  // (the item before is done with what is shared)
-    if (threadIdx.x < ROWS) row_m[threadIdx.x] = -INFINITY, row_l[threadIdx.x] = 0.0f;
-    for (int base = w; base <= it.last; base += kAddThreads) {
-      // the parts among the next warps: a block within the item has one, in its first warp's place
-      const int at = base + threadIdx.x;
-      bool part = at <= it.last;
-      int slot = 0;
-      if (part) {
-        const int block = at / it.warps * it.warps;
-        const bool one = it.deal.start(block) >= it.begin - kItemCost && it.deal.start(block + it.warps) <= it.end + kItemCost;
-        part = !one || at == block;
-        slot = 2 * at + (it.deal.start(at) <= it.begin ? 1 : 0);
-      }
-      const uint32_t mask = __ballot_sync(kAll, part);
-      if (lane == 0) counts[warp] = __popc(mask);
-      __syncthreads();
-      int before = 0, parts = 0;
+  const int workers = *p.workers, cut = p.cut[blockIdx.x];
+  const CutItem it = p.cuts[blockIdx.x];
+  // (entries that this call has not written hold anything)
+  if (workers == 0 || (!p.by_item && static_cast<int>(blockIdx.x) >= workers) || !cut) return;
+  const int rows = min(16, p.n * p.r - (it.j - p.row_tiles_div.div(it.j) * p.row_tiles) * 16);
+  const int row = APART ? blockIdx.y : blockIdx.y * kAddWarps + warp;
+  if (row >= rows) return;
+  // the item's parts: those of its first block's warps, of its last block's, and of each block between them one; also one of a
+  // block that has tiles of no other item
+  const int block0 = it.first / it.warps, block1 = it.last / it.warps;
+  auto one = [&](int block) {
+    return it.deal.start(block * it.warps) >= it.begin - kItemCost && it.deal.start((block + 1) * it.warps) <= it.end + kItemCost;
+  };
+  const int end0 = min((block0 + 1) * it.warps - 1, it.last);
+  const int parts0 = one(block0) ? 1 : end0 - it.first + 1, between = max(block1 - block0 - 1, 0);
+  const int parts1 = block1 == block0 ? 0 : one(block1) ? 1 : it.last - block1 * it.warps + 1;
+  const int parts = parts0 + between + parts1;
+  // a part's sums
+  auto sums_of = [&](int i) {
+    const int at = i < parts0 ? it.first + i : i < parts0 + between ? (block0 + 1 + i - parts0) * it.warps : block1 * it.warps + i - parts0 - between;
+    return p.sums + (2 * static_cast<int64_t>(at) + (it.deal.start(at) <= it.begin ? 1 : 0)) * p.rows * (D + 4);
+  };
+  const int step = APART ? kAddWarps : 1, from = APART ? warp : 0;
+  float m = -INFINITY, l = 0.0f, o[N] = {};
+  for (int base = from; base < parts; base += 32 * step) {
+    const int here = min((parts - base + step - 1) / step, 32);  // parts of this turn, one a lane
+    const float *mine = sums_of(base + min(lane, here - 1) * step);
+    const uint64_t mine_at = reinterpret_cast<uint64_t>(mine + row * D);
+    float high = lane < here ? mine[p.rows * D + row] : -INFINITY;
+    const float l_part = lane < here ? mine[p.rows * (D + 1) + row] : 0.0f;
+    const float m_part = high;
+    float v[kAhead][N];
+    auto fetch = [&](int first) {
 #pragma unroll
-      for (int i = 0; i < kAddThreads / 32; ++i) {
-        before += i < warp ? counts[i] : 0;
-        parts += counts[i];
-      }
-      if (part) slots[before + __popc(mask & ((1u << lane) - 1u))] = slot;
-      __syncthreads();
-      auto sums_of = [&](int i) { return p.sums + static_cast<int64_t>(slots[i]) * p.rows * (D + 4); };
-      // what each row of each part weighs against the largest so far, a row a warp
-      for (int row = warp; row < rows; row += kAddThreads / 32) {
-        const float old = row_m[row];
-        float high = old;
-        for (int i = lane; i < parts; i += 32) high = fmaxf(high, sums_of(i)[p.rows * D + row0 + row]);
-#pragma unroll
-        for (int i = 16; i > 0; i /= 2) high = fmaxf(high, __shfl_xor_sync(kAll, high, i));
-        float l = 0.0f;
-        for (int i = lane; i < parts; i += 32) {
-          const float *s = sums_of(i);
-          const float m = s[p.rows * D + row0 + row];
-          const float f = m == high ? 1.0f : ex2(m - high);
-          factor[row][i] = f;
-          l = fmaf(s[p.rows * (D + 1) + row0 + row], f, l);
-        }
-#pragma unroll
-        for (int i = 16; i > 0; i /= 2) l += __shfl_xor_sync(kAll, l, i);
-        __syncwarp();
-        if (lane == 0) {
-          const float f = old == high ? 1.0f : ex2(old - high);
-          row_m[row] = high, row_f[row] = f, row_l[row] = fmaf(row_l[row], f, l);
+      for (int i = 0; i < kAhead; ++i) {
+        const float *from_part = reinterpret_cast<const float *>(__shfl_sync(kAll, mine_at, min(first + i, here - 1))) + N * lane;
+        if constexpr (N == 4) {
+          const float4 x = *reinterpret_cast<const float4 *>(from_part);
+          v[i][0] = x.x, v[i][1] = x.y, v[i][2] = x.z, v[i][3] = x.w;
+        } else {
+          const float2 x = *reinterpret_cast<const float2 *>(from_part);
+          v[i][0] = x.x, v[i][1] = x.y;
         }
       }
-      __syncthreads();
-      const int r = ROWS == 1 ? 0 : group;
-      if (r < rows) {
-        const float f = row_f[r];
-        o = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
-#pragma unroll 4
-        for (int i = ROWS == 1 ? group : 0; i < parts; i += ROWS == 1 ? kGroups : 1) {
-          const float4 v = *reinterpret_cast<const float4 *>(sums_of(i) + (row0 + r) * D + 4 * x);
-          const float g = factor[r][i];
-          o = make_float4(fmaf(v.x, g, o.x), fmaf(v.y, g, o.y), fmaf(v.z, g, o.z), fmaf(v.w, g, o.w));
-        }
-      }
-      __syncthreads();  // (the lists are made anew)
-    }
-    if (ROWS == 1) {
-      part_o[group][x] = o;
-      __syncthreads();
-      if (group == 0) {
+    };
+    fetch(0);
 #pragma unroll
-        for (int i = 1; i < kGroups; ++i) {
-          const float4 v = part_o[ROWS == 1 ? i : 0][x];
-          o = make_float4(o.x + v.x, o.y + v.y, o.z + v.z, o.w + v.w);
-        }
+    for (int i = 16; i > 0; i /= 2) high = fmaxf(high, __shfl_xor_sync(kAll, high, i));
+    high = fmaxf(high, m);
+    // (a maximum that is not above the one so far, -inf beside -inf among them, weighs 1 as it stands)
+    const float f = lane >= here ? 0.0f : m_part == high ? 1.0f : ex2(m_part - high);
+    const float f_old = m == high ? 1.0f : ex2(m - high);
+    float l_sum = lane < here ? l_part * f : 0.0f;
+#pragma unroll
+    for (int i = 16; i > 0; i /= 2) l_sum += __shfl_xor_sync(kAll, l_sum, i);
+    l = fmaf(l, f_old, l_sum);
+#pragma unroll
+    for (int x = 0; x < N; ++x) o[x] *= f_old;
+    m = high;
+    for (int first = 0; first < here; first += kAhead) {
+      if (first > 0) fetch(first);
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        const float g = __shfl_sync(kAll, f, min(first + i, 31));
+        if (first + i >= here) continue;
+#pragma unroll
+        for (int x = 0; x < N; ++x) o[x] = fmaf(v[i][x], g, o[x]);
       }
-    }
-    const int r = ROWS == 1 ? 0 : group;
-    if (r < rows && (ROWS > 1 || group == 0) && 4 * x < p.head_dim) {
-      const float inv = over_sum(row_l[r]);
-      *reinterpret_cast<uint2 *>(p.out + row_at(p, it.b, it.j, row0 + r, p.ldo) + 4 * x) =
-          make_uint2(out_bits2<DT>(o.x * inv, o.y * inv), out_bits2<DT>(o.z * inv, o.w * inv));
     }
   }
+  if (APART) {
+    if (lane == 0) part_m[warp] = m, part_l[warp] = l;
+#pragma unroll
+    for (int x = 0; x < N; ++x) part_o[APART ? warp : 0][N * lane + x] = o[x];
+    __syncthreads();
+    if (warp != 0) return;
+    float high = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kAddWarps; ++w) high = fmaxf(high, part_m[w]);
+    l = 0.0f;
+#pragma unroll
+    for (int x = 0; x < N; ++x) o[x] = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kAddWarps; ++w) {
+      const float f = part_m[w] == high ? 1.0f : ex2(part_m[w] - high);
+      l = fmaf(part_l[w], f, l);
+#pragma unroll
+      for (int x = 0; x < N; ++x) o[x] = fmaf(part_o[APART ? w : 0][N * lane + x], f, o[x]);
+    }
+  }
+  if (N * lane >= p.head_dim) return;
+  const float inv = over_sum(l);
+  uint16_t *out = p.out + row_at(p, it.b, it.j, row, p.ldo) + N * lane;
+  if constexpr (N == 4)
+    *reinterpret_cast<uint2 *>(out) = make_uint2(out_bits2<DT>(o[0] * inv, o[1] * inv), out_bits2<DT>(o[2] * inv, o[3] * inv));
+  else
+    *reinterpret_cast<uint32_t *>(out) = out_bits2<DT>(o[0] * inv, o[1] * inv);
 }
 
 template <int DT, int D, int ROWS>
@@ -877,21 +863,20 @@ cudaError_t launch_d(const KvParams &p, int num_sms, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   e = launch_programmatic(kern, num_sms, 32 * C::kWarps, C::kSmem, stream, p);
   if (e != cudaSuccess) return e;
-  const int all = num_sms * C::kWarps;
-  const int64_t items = static_cast<int64_t>(p.batch) * p.items;
-  // a block for each row of each item, or for a row a group where the items alone fill the device
-  constexpr int kGroups = kAddThreads * 4 / D;
-  const bool rows_apart = items < num_sms || p.rows == 1;
+  // an entry an item, or one a warp where there are more items than blocks; a row's parts to a block's warps where they may be many, or
+  // where a row is all there is
+  const bool apart = p.by_item || p.rows == 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(items < all ? items : all), static_cast<unsigned>(cdiv(p.rows, rows_apart ? 1 : kGroups)));
-  cfg.blockDim = dim3(kAddThreads);
+  cfg.gridDim = dim3(static_cast<unsigned>(p.by_item ? p.batch * p.items : num_sms * C::kWarps),
+                     static_cast<unsigned>(apart ? p.rows : cdiv(p.rows, kAddWarps)));
+  cfg.blockDim = dim3(32 * kAddWarps);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = rows_apart ? cudaLaunchKernelEx(&cfg, kv_add_kernel<DT, D, 1>, p) : cudaLaunchKernelEx(&cfg, kv_add_kernel<DT, D, kGroups>, p);
+  e = apart ? cudaLaunchKernelEx(&cfg, kv_add_kernel<DT, D, true>, p) : cudaLaunchKernelEx(&cfg, kv_add_kernel<DT, D, false>, p);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
@@ -936,6 +921,7 @@ cudaError_t launch_kv_attention(const KvAttentionArgs &a, void *workspace, int n
   p.row_tiles = static_cast<int>(cdiv(static_cast<int64_t>(a.n) * p.r, 16));
   p.rows = a.n * p.r < 16 ? a.n * p.r : 16;
   p.items = p.row_tiles * a.k_heads;
+  p.by_item = static_cast<int64_t>(p.batch) * p.items <= num_sms;
   p.scale = a.scale;
   p.page_div = make_fastdiv(static_cast<uint32_t>(a.page));
   p.r_div = make_fastdiv(static_cast<uint32_t>(p.r));
