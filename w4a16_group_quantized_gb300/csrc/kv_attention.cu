@@ -36,7 +36,7 @@ using namespace detail;
 
 constexpr uint32_t kAll = 0xffffffffu;
 constexpr int kMostWarps = 16;    // of a block
-constexpr int kItemCost = 6;      // what beginning an item costs, in tiles
+constexpr int kItemCost = 4;      // what beginning an item costs, in tiles
 constexpr int kSoloTiles = 7;     // what adding parts takes, in tiles of a warp
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kSlack = 8.0f;    // how far a score may pass the maximum in use (log2 of the weight)
@@ -59,7 +59,8 @@ struct Deal {
   }
   // The warp in whose stretch a unit lies.
   __device__ __forceinline__ int holder(int64_t unit) const {
-    int w = static_cast<int>(static_cast<double>(unit) / (static_cast<double>(quotient) + static_cast<double>(remainder) / workers));
+    // (32 bits are right to a warp or two; 64 would go through a pipe that takes tens of cycles for an instruction)
+    int w = static_cast<int>(static_cast<float>(unit) / (static_cast<float>(quotient) + static_cast<float>(remainder) / static_cast<float>(workers)));
     while (w > 0 && start(w) > unit) --w;
     while (start(w + 1) <= unit) ++w;
     return w;
@@ -232,13 +233,14 @@ __global__ void __launch_bounds__(32 * KvCfg<D, ROWS>::kWarps, 1) kv_attention_k
   if (solo) {
     // few items: a block each, and nothing to add afterwards, unless the longest takes longer that way (by more than the adding, as
     // long as kSoloTiles tiles of a warp) than all of them dealt out evenly
-    int longest = 0, all = 0;
+    int longest = 0, all = 0;  // in tiles, and in 16 of them
     for (int i = lane; i < p.batch; i += 32) {
       const int t16 = tiles_of(i);
       longest = max(longest, t16);
       all += t16 / 16;
     }
-    solo = __reduce_max_sync(kAll, longest) <= W * kSoloTiles + static_cast<int64_t>(__reduce_add_sync(kAll, all)) * 16 * p.items / gridDim.x;
+    solo = static_cast<int64_t>(__reduce_max_sync(kAll, longest) - W * kSoloTiles) * gridDim.x <=
+           static_cast<int64_t>(__reduce_add_sync(kAll, all)) * (16 * p.items);
   }
   if (solo) {
     if (blockIdx.x == 0 && threadIdx.x == 0) *p.workers = 0;
@@ -248,8 +250,8 @@ __global__ void __launch_bounds__(32 * KvCfg<D, ROWS>::kWarps, 1) kv_attention_k
     one_tiles = tiles = tiles_of(b);
     one_begin = block_from = 0;
     block_to = tiles;
-    at = from = tile = static_cast<int>(static_cast<int64_t>(tiles) * warp / W);
-    to = static_cast<int64_t>(tiles) * (warp + 1) / W;
+    at = from = tile = tiles / W * warp + tiles % W * warp / W;
+    to = tiles / W * (warp + 1) + tiles % W * (warp + 1) / W;
     together = true;
   } else {
     // the units of the sequences up to and with each: for few, in each warp's lanes; else up to and with each thread's
@@ -276,7 +278,7 @@ __global__ void __launch_bounds__(32 * KvCfg<D, ROWS>::kWarps, 1) kv_attention_k
     }
     const int64_t total = few ? __shfl_sync(kAll, sum, 31) : upto[32 * W - 1];
     // fewer warps where there is little to do
-    deal.workers = static_cast<uint32_t>(min(static_cast<int64_t>(W * gridDim.x), max(total / 4, int64_t{1})));
+    deal.workers = static_cast<uint32_t>(min(static_cast<int64_t>(W * gridDim.x), max(total / 2, int64_t{1})));
     deal.quotient = quotient(total, deal.workers);
     deal.remainder = static_cast<uint32_t>(total - deal.quotient * deal.workers);
     // (those that there are, in all blocks alike)
