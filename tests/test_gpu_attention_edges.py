@@ -238,3 +238,32 @@ def test_refusals_of_the_binding():
         with pytest.raises(w4.W4Error) as e:
             call()
         assert e.value.status == status
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+def test_rope_of_any_frequency_and_position(dtype):
+    """Values (1, 0) turned: the cosine and sine of position * freq, the product exact in Python's integers. The turn is off by
+    |position| (freq + 1) 2^-64 at most, 2^-33 (freq + 1) of a turn; the sine of it in 32 bits by some 2^-22; one rounding."""
+    from fractions import Fraction
+    import math
+    freqs = torch.tensor([1.0, -1.0, 0.75, 1e-6, 2.0 ** -40, 100.5, -3e4, 2.0 ** -149], dtype=torch.float32, device="cuda")
+    positions = [0, 1, -1, 12345678, 2 ** 31 - 1, -2 ** 31]
+    q = torch.zeros(len(positions), 1, 16, dtype=dtype, device="cuda")
+    q[:, :, :8] = 1.0
+    out, _ = w4.w4_qk_norm_rope(q, None, torch.tensor(positions, dtype=torch.int32, device="cuda"), freqs)
+    # 2 pi to 160 bits by Machin's formula
+    bits = 200
+    def arctan_inverse(n):
+        total, term, k = 0, (1 << bits) // n, 1
+        while term:
+            total, term, k = total + (term // k if k % 4 == 1 else -(term // k)), term // (n * n), k + 2
+        return total
+    tau = Fraction(8 * (4 * arctan_inverse(5) - arctan_inverse(239)), 1 << bits)
+    for i, pos in enumerate(positions):
+        for j, f in enumerate(freqs.tolist()):
+            angle = Fraction(f) * pos
+            turn = angle / tau
+            a = float((turn - round(turn)) * tau)
+            slop = 2 * math.pi * 2.0 ** -33 * (abs(f) + 1) + 2.0 ** -21
+            for got, want in ((out[i, 0, j].item(), math.cos(a)), (out[i, 0, 8 + j].item(), math.sin(a))):
+                assert abs(got - want) <= torch.finfo(dtype).eps / 2 * abs(want) + slop, (pos, f)

@@ -5,8 +5,8 @@
 // (y_i, y_j) = (u_i cos a - u_j sin a, u_j cos a + u_i sin a) with the angle a = position * freq_i.
 //
 // A position may be far (a = 10^6 and more), and 32 bits would lose the angle: what matters is position * freq / 2 pi modulo
-// 1. A block forms freq / 2 pi modulo 1 once, in 64 bits, as a 64-bit fraction of a turn; the product with the
-// position in wrapping integer arithmetic is the turn, exact to position * 2^-64 and the fraction's own rounding.
+// 1. A block forms freq / 2 pi modulo 1 once, as a 64-bit fraction of a turn; the product with the position in wrapping
+// integer arithmetic is the turn, exact to position * 2^-64 and the fraction's own rounding.
 //
 // A lane holds 8 values of a head, a power of two of lanes a head: four pairs' both halves (values 4 i .. 4 i + 3 and those
 // half the rotation further, or 8 neighbours where neighbours are paired), or 8 neighbours past the rotation. So a pair is
@@ -94,28 +94,52 @@ __device__ __forceinline__ uint32_t pack2(uint64_t v) {
   return d;
 }
 
+// freq / 2 pi modulo 1 in units of 2^-64: freq is m * 2^(e - 150) with integers m and e, and m * (2^64 / 2 pi) a product of 24 by 62
+// bits. Off by freq * 2^-64 and the last unit. (64-bit floating point would do, but each of its instructions takes
+// some 40 cycles here.)
+__device__ __forceinline__ uint64_t fraction_of_turn(float freq) {
+  constexpr uint64_t kInvTwoPi = 0x28BE60DB9391054Aull;  // 2^64 / 2 pi
+  const uint32_t bits = __float_as_uint(freq), e = bits >> 23 & 255u;
+  const uint64_t m = (bits & 0x7FFFFFu) | (e ? 0x800000u : 0u);
+  const int down = 150 - static_cast<int>(e ? e : 1u);  // the product's places below 2^-64
+  const uint64_t lo = m * kInvTwoPi, hi = __umul64hi(m, kInvTwoPi);
+  uint64_t f = 0;
+  if (down <= 0)
+    f = down > -64 ? lo << -down : 0;
+  else if (down < 64)
+    f = lo >> down | hi << (64 - down);
+  else if (down < 128)
+    f = hi >> (down - 64);
+  return bits >> 31 ? 0 - f : f;
+}
+
 // LG: lanes a head. PAIRED: neighbours are paired.
 template <int DT, int LG, bool NORM, bool PAIRED>
 __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeParams p) {
   extern __shared__ __align__(16) uint8_t smem[];
   float *cosines = reinterpret_cast<float *>(smem), *sines = cosines + p.rows * p.half;  // [rows][half] each
-  long long *fractions = reinterpret_cast<long long *>(sines + p.rows * p.half);        // [half], of a turn a position
+  uint64_t *fractions = reinterpret_cast<uint64_t *>(sines + p.rows * p.half);          // [half], of a turn a position
   griddep_launch_dependents();
   griddep_wait();
   const int64_t row0 = static_cast<int64_t>(blockIdx.x / p.head_parts) * p.rows;
   const int part = blockIdx.x % p.head_parts;
   const int rows = static_cast<int>(min(static_cast<int64_t>(p.rows), p.T - row0));
-  for (int f = threadIdx.x; f < p.half; f += kRopeThreads) {
-    const double turns = static_cast<double>(p.freqs[f]) * 0.15915494309189533577;  // 1 / 2 pi
-    fractions[f] = __double2ll_rn((turns - rint(turns)) * 18446744073709551616.0);
-  }
+  auto position = [&](int i, int *f) {
+    const int r = i / p.half;
+    *f = i - r * p.half;
+    const int axis = (*f >= p.section_end[0]) + (*f >= p.section_end[1]) + (*f >= p.section_end[2]);
+    return p.positions[axis * p.T + row0 + r];
+  };
+  int f, pos = 0;
+  if (static_cast<int>(threadIdx.x) < p.half * rows) pos = position(threadIdx.x, &f);  // (beside the frequencies)
+  for (int i = threadIdx.x; i < p.half; i += kRopeThreads) fractions[i] = fraction_of_turn(p.freqs[i]);
   __syncthreads();
   for (int i = threadIdx.x; i < p.half * rows; i += kRopeThreads) {
-    const int r = i / p.half, f = i - r * p.half;
-    const int axis = (f >= p.section_end[0]) + (f >= p.section_end[1]) + (f >= p.section_end[2]);
-    const long long pos = p.positions[axis * p.T + row0 + r];
-    const long long at = static_cast<long long>(static_cast<unsigned long long>(fractions[f]) * static_cast<unsigned long long>(pos));
-    sincospif(__ll2float_rn(at) * 0x1p-63f, &sines[i], &cosines[i]);  // half turns
+    if (i >= kRopeThreads) pos = position(i, &f);
+    const uint64_t at = fractions[f] * static_cast<uint64_t>(static_cast<int64_t>(pos));
+    // as half turns; the two halves by themselves, as a conversion of 64 bits would go through the slow pipe
+    const float half_turns = fmaf(static_cast<float>(static_cast<int32_t>(at >> 32)), 0x1p-31f, static_cast<float>(static_cast<uint32_t>(at)) * 0x1p-63f);
+    sincospif(half_turns, &sines[i], &cosines[i]);
   }
   __syncthreads();
 
@@ -214,7 +238,7 @@ cudaError_t launch_dim(RopeParams p, int num_sms, cudaStream_t stream) {
   const int64_t blocks = cdiv(p.T, p.rows) * p.head_parts;
   if (blocks > 0x7FFFFFFF) return cudaErrorInvalidValue;
   const bool norm = p.q_weight || p.k_weight;
-  const int smem = p.half * (p.rows * 2 * static_cast<int>(sizeof(float)) + static_cast<int>(sizeof(long long)));
+  const int smem = p.half * (p.rows * 2 * static_cast<int>(sizeof(float)) + static_cast<int>(sizeof(uint64_t)));
   auto go = [&](auto kern) { return launch_programmatic(kern, static_cast<int>(blocks), kRopeThreads, smem, stream, p); };
   auto pick = [&](auto n, auto paired) {
     constexpr bool N = decltype(n)::value, P = decltype(paired)::value;
