@@ -691,8 +691,8 @@ W4_API int w4_kv_append(const w4_kv_append_args *args, void *stream);
  * q_heads a multiple of k_heads; head_dim a multiple of 16, at most 128; page a
  * multiple of 16, at most 256; n at most 256; at most 32767 key heads; scale
  * positive and finite; max_pages * page below 2^31 - 1024. With 16 query rows
- * that share a key head as an item: at most 2^24 items, and at most 2^40 of
- * items * max_pages * page / 16.
+ * that share a key head as an item: at most 2^24 items, and at most 2^30 of
+ * items * (max_pages * page / 16 + 16).
  * The workspace is at least w4_kv_attention_workspace_bytes(...) bytes,
  * 256-byte aligned. Its first word is left as it is.
  */

@@ -97,6 +97,12 @@ def test_attention_refusals(lib):
     assert attend(lib, ws_bytes=16) == SMALL
 
 
+def test_more_tiles_than_are_counted(lib):
+    """16 keys of 16 query rows are a tile, counted in 32 bits."""
+    assert attend(lib, batch=1 << 14, max_pages=1 << 16) == SHAPE
+    assert attend(lib, batch=1 << 14, max_pages=1 << 14, ws_bytes=0) == SMALL  # (sizes that are taken)
+
+
 def prompt(lib, ws=PTR, ws_bytes=1 << 40, **kw):
     a = dict(q=PTR, k=PTR, v=PTR, cu=PTR, out=PTR, T=4, ldq=512, ldk=128, ldv=128, ldo=512, batch=2, hq=8, hk=2, dim=64, dtype=0,
              scale=0.125) | kw

@@ -165,9 +165,9 @@ int w4_kv_attention(const w4_kv_attention_args *a, void *workspace_dev, size_t w
   if (rc == W4_OK) rc = check_rows(a->ldq, a->q_heads, a->head_dim);
   if (rc == W4_OK) rc = check_rows(a->ldo, a->q_heads, a->head_dim);
   if (rc != W4_OK) return rc;
-  // a warp's share of the tiles (16 keys of 16 query rows) is counted in 32 bits
+  // tiles (16 keys of 16 query rows) and what beginning an item costs are counted in 32 bits
   const int64_t items = static_cast<int64_t>(a->batch) * a->k_heads * w4::cdiv(static_cast<int64_t>(a->n) * (a->q_heads / a->k_heads), 16);
-  if (items * w4::cdiv(static_cast<int64_t>(a->max_pages) * a->page, 16) > (int64_t{1} << 40)) return W4_ERR_UNSUPPORTED_SHAPE;
+  if (items * (w4::cdiv(static_cast<int64_t>(a->max_pages) * a->page, 16) + 16) > (int64_t{1} << 30)) return W4_ERR_UNSUPPORTED_SHAPE;
   if (a->batch == 0) return W4_OK;
   if (!a->q_dev || !a->k_cache_dev || !a->v_cache_dev || !a->k_scale_dev || !a->v_scale_dev || !a->table_dev || !a->lens_dev ||
       !a->out_dev || !workspace_dev)

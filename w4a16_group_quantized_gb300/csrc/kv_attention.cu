@@ -44,22 +44,16 @@ constexpr float kSlack = 8.0f;    // how far a score may pass the maximum in use
 // of 32 bits (it counts in the sum l, however small its part of O).
 constexpr float kScaleMin = 0x1p-40f, kScaleMax = 0x1p40f;
 
-// n / d for n that mostly fits 32 bits.
-__device__ __forceinline__ int64_t quotient(int64_t n, uint32_t d) {
-  return n >> 32 == 0 ? static_cast<int64_t>(static_cast<uint32_t>(n) / d) : n / d;
-}
-
 // How `units` are dealt out to warps: the first unit of each one's stretch is quotient * w + remainder * w / workers.
 struct Deal {
-  int64_t quotient;
-  uint32_t remainder, workers;  // workers <= 2^16
-  __device__ __forceinline__ int64_t start(uint32_t w) const {
+  uint32_t quotient, remainder, workers;  // workers <= 2^12
+  __device__ __forceinline__ int start(uint32_t w) const {
     w = min(w, workers);
-    return quotient * w + static_cast<uint32_t>(remainder * w) / workers;
+    return static_cast<int>(quotient * w + remainder * w / workers);
   }
   // The warp in whose stretch a unit lies.
-  __device__ __forceinline__ int holder(int64_t unit) const {
-    // (32 bits are right to a warp or two; 64 would go through a pipe that takes tens of cycles for an instruction)
+  __device__ __forceinline__ int holder(int unit) const {
+    // (right to a warp or two)
     int w = static_cast<int>(static_cast<float>(unit) / (static_cast<float>(quotient) + static_cast<float>(remainder) / static_cast<float>(workers)));
     while (w > 0 && start(w) > unit) --w;
     while (start(w + 1) <= unit) ++w;
@@ -68,12 +62,13 @@ struct Deal {
 };
 
 // An item that begins in a warp's stretch and ends in another's: what the second launch adds. Positions are in units: an item's are
-// kItemCost ones for its beginning and one for each tile.
+// kItemCost ones for its beginning and one for each tile (2^30 in all at most: 64-bit divisions and conversions would cost a call
+// some 2 us, by a pipe of some 40 cycles an instruction).
 struct CutItem {
   int32_t b, j;        // sequence and item of it
   int32_t first, last; // the warps that hold the item's first and last tile
   int32_t warps;       // of a block that have stretches
-  int64_t begin, end;  // its tiles
+  int32_t begin, end;  // its tiles
   Deal deal;
 };
 
@@ -209,7 +204,7 @@ __global__ void __launch_bounds__(32 * KvCfg<D, ROWS>::kWarps, 1) kv_attention_k
   constexpr int W = C::kWarps, S = C::kStages, RR = ROWS / 8;  // RR: rows of a lane in S
   constexpr int NO = D / 8 * RR;  // sets of two sums: 16 rows: rows g, g + 8 x values; 8 rows: values x rows 2 t, 2 t + 1
   extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ int64_t upto[32 * W];  // units of the sequences up to and with the thread's
+  __shared__ int upto[32 * W];  // units of a warp's sequences up to and with the thread's
   __shared__ float row_m[W][ROWS], row_l[W][ROWS];
   const int warp = __shfl_sync(kAll, threadIdx.x / 32, 0), lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
   // what the lookups found of a tile's page: k scale, log2 of the part of the v scale that goes into the weights, 1 / that part, the rest of it (1, or what
@@ -226,7 +221,7 @@ __global__ void __launch_bounds__(32 * KvCfg<D, ROWS>::kWarps, 1) kv_attention_k
   auto tiles_of = [&](int b) { return max((min(p.lens[b], most) + 15) / 16, 1); };  // (a sequence without keys still has an output)
   // The warp's stretch, its first tile (at: its unit) with the sequence and item, and whether all the block's tiles are of one
   // item, whose sums are then added here
-  int64_t from, to, at, block_from, block_to, one_begin;
+  int from, to, at, block_from, block_to, one_begin;
   int b = 0, j = 0, tile = 0, tiles = 1, one_b, one_j, one_tiles, me = 0, warps = W;
   bool together, solo = p.batch * p.items <= gridDim.x;
   Deal deal = {};
@@ -254,33 +249,35 @@ __global__ void __launch_bounds__(32 * KvCfg<D, ROWS>::kWarps, 1) kv_attention_k
     to = tiles / W * (warp + 1) + tiles % W * (warp + 1) / W;
     together = true;
   } else {
-    // the units of the sequences up to and with each: for few, in each warp's lanes; else up to and with each thread's
+    // the units of the sequences up to and with each: for few, in each warp's lanes; else by warps, and within each by threads
     const bool few = p.batch <= 32;
     const int share = few ? 1 : (p.batch + 32 * W - 1) / (32 * W);  // sequences a thread adds up
     const int sb0 = few ? lane : threadIdx.x * share;
     const int lane_tiles = few && lane < p.batch ? tiles_of(lane) : 0;
-    int64_t sum = 0;
-    for (int sb = sb0; sb < min(sb0 + share, p.batch); ++sb) sum += static_cast<int64_t>((few ? lane_tiles : tiles_of(sb)) + kItemCost) * p.items;
-    const int64_t mine = sum;
+    int sum = 0;
+    for (int sb = sb0; sb < min(sb0 + share, p.batch); ++sb) sum += ((few ? lane_tiles : tiles_of(sb)) + kItemCost) * p.items;
+    const int mine = sum;
 #pragma unroll
     for (int i = 1; i < 32; i *= 2) {
-      const int64_t x = __shfl_up_sync(kAll, sum, i);
+      const int x = __shfl_up_sync(kAll, sum, i);
       if (lane >= i) sum += x;
     }
+    int warp_sum = 0, warp_mine = 0;  // of the warps up to and with the lane's, and of that one
     if (!few) {
       upto[threadIdx.x] = sum;
       __syncthreads();
-      int64_t before = 0;
-      for (int i = 0; i < warp; ++i) before += upto[32 * i + 31];
-      __syncthreads();
-      upto[threadIdx.x] = sum + before;
-      __syncthreads();
+      warp_sum = warp_mine = lane < W ? upto[32 * lane + 31] : 0;
+#pragma unroll
+      for (int i = 1; i < 16; i *= 2) {
+        const int x = __shfl_up_sync(kAll, warp_sum, i);
+        if (lane >= i) warp_sum += x;
+      }
     }
-    const int64_t total = few ? __shfl_sync(kAll, sum, 31) : upto[32 * W - 1];
+    const int total = __shfl_sync(kAll, few ? sum : warp_sum, few ? 31 : W - 1);
     // fewer warps where there is little to do
-    deal.workers = static_cast<uint32_t>(min(static_cast<int64_t>(W * gridDim.x), max(total / 2, int64_t{1})));
-    deal.quotient = quotient(total, deal.workers);
-    deal.remainder = static_cast<uint32_t>(total - deal.quotient * deal.workers);
+    deal.workers = min(W * gridDim.x, static_cast<uint32_t>(max(total / 2, 1)));
+    deal.quotient = total / deal.workers;
+    deal.remainder = total - deal.quotient * deal.workers;
     // (those that there are, in all blocks alike)
     warps = static_cast<int>((deal.workers + gridDim.x - 1) / gridDim.x);
     me = warp < warps ? blockIdx.x * warps + warp : gridDim.x * W;
@@ -289,31 +286,29 @@ __global__ void __launch_bounds__(32 * KvCfg<D, ROWS>::kWarps, 1) kv_attention_k
     block_from = deal.start(blockIdx.x * warps), block_to = deal.start((blockIdx.x + 1) * warps);
 
     // the sequence and item that a unit lies in, and the unit within the item
-    auto find = [&](int64_t unit, int *fb, int *fj, int *ftiles) {
-      int64_t rest;
+    auto find = [&](int unit, int *fb, int *fj, int *ftiles) {
+      int rest;
       if (few) {
         *fb = __ffs(__ballot_sync(kAll, sum > unit)) - 1;
         rest = unit - __shfl_sync(kAll, sum - mine, *fb);
         *ftiles = __shfl_sync(kAll, lane_tiles, *fb);
       } else {
-        int lo = 0, hi = 32 * W - 1;
-        while (lo < hi) {
-          const int mid = (lo + hi) / 2;
-          if (upto[mid] > unit)
-            hi = mid;
-          else
-            lo = mid + 1;
-        }
-        rest = unit - (lo > 0 ? upto[lo - 1] : 0);
+        const int of = __ffs(__ballot_sync(kAll, lane < W && warp_sum > unit)) - 1;
+        rest = unit - __shfl_sync(kAll, warp_sum - warp_mine, of);
+        const int within = upto[32 * of + lane];
+        const int at = __ffs(__ballot_sync(kAll, within > rest)) - 1;
+        const int before = __shfl_sync(kAll, within, max(at - 1, 0));
+        rest -= at > 0 ? before : 0;
+        const int lo = 32 * of + at;
         for (*fb = lo * share;; ++*fb) {
           *ftiles = tiles_of(*fb);
-          const int64_t units = static_cast<int64_t>(*ftiles + kItemCost) * p.items;
+          const int units = (*ftiles + kItemCost) * p.items;
           if (rest < units || *fb + 1 >= p.batch) break;
           rest -= units;
         }
       }
-      *fj = static_cast<int>(quotient(rest, static_cast<uint32_t>(*ftiles + kItemCost)));
-      return static_cast<int>(rest - static_cast<int64_t>(*fj) * (*ftiles + kItemCost));
+      *fj = static_cast<uint32_t>(rest) / static_cast<uint32_t>(*ftiles + kItemCost);
+      return rest - *fj * (*ftiles + kItemCost);
     };
     // (every warp finds the block's first item for itself: no more barriers)
     together = false;
@@ -329,7 +324,7 @@ __global__ void __launch_bounds__(32 * KvCfg<D, ROWS>::kWarps, 1) kv_attention_k
       int off;
       if (together) {
         b = one_b, j = one_j, tiles = one_tiles;
-        off = static_cast<int>(from - one_begin) + kItemCost;
+        off = from - one_begin + kItemCost;
       } else {
         off = find(from, &b, &j, &tiles);
       }
@@ -343,7 +338,7 @@ __global__ void __launch_bounds__(32 * KvCfg<D, ROWS>::kWarps, 1) kv_attention_k
   // ---------------------------------------------------------------- copies
   // The tile that is copied next, and what the lookups found for up to 32 tiles of its item (sent: tiles so far)
   int cb = b, cj = j, ct = tile, ctiles = tiles, ckeys = 0, found = 0, first = 0, book = 0, next_book = 0;
-  int64_t cat = at;
+  int cat = at;
   uint32_t off_lo = 0, off_hi = 0;  // this lane's tile: offset in the cache, in 16 bytes; all ones: no page
   int sent = 0;
   uint32_t infos = 0;  // the places in `info` of the tiles on their way, 8 bits each (255: no page), the next one's lowest
@@ -631,7 +626,7 @@ __global__ void __launch_bounds__(32 * KvCfg<D, ROWS>::kWarps, 1) kv_attention_k
 
     if ((tile + 1 == tiles || at + 1 == to) && !together) {
       // ------------------------------------------- the item's end, or the stretch's
-      const int64_t begin = at - tile, end = begin + tiles;
+      const int begin = at - tile, end = begin + tiles;
       const bool here = begin >= from;  // the item begins in the stretch
       const bool whole = here && end <= to;
 #pragma unroll
@@ -698,7 +693,7 @@ __global__ void __launch_bounds__(32 * KvCfg<D, ROWS>::kWarps, 1) kv_attention_k
   }
 
   // ------------------------------------------- the block's tiles are of one item
-  const int64_t begin = one_begin, end = one_begin + one_tiles;
+  const int begin = one_begin, end = one_begin + one_tiles;
   __syncthreads();  // the rings are idle (no copies are in flight: every tile sent was waited for)
   float *sums = reinterpret_cast<float *>(smem + C::kInfo);
 #pragma unroll
@@ -750,9 +745,9 @@ constexpr int kAddWarps = 8;
 // warps have every eighth part each. Which parts there are follows from the dealing: an entry is all that is read first,
 // then the parts' maxima and sums with the first of their values.
 template <int DT, int D, bool APART>
-__global__ void __launch_bounds__(32 * kAddWarps) kv_add_kernel(const __grid_constant__ KvParams p) {
+__global__ void __launch_bounds__(32 * kAddWarps, APART ? 3 : 5) kv_add_kernel(const __grid_constant__ KvParams p) {
   constexpr int N = D / 32;    // values of a lane
-  constexpr int kAhead = 8;    // parts whose values are fetched together
+  constexpr int kAhead = APART ? 8 : 4;  // parts whose values are fetched together
   __shared__ float part_o[APART ? kAddWarps : 1][D], part_m[kAddWarps], part_l[kAddWarps];
   griddep_launch_dependents();
   griddep_wait();
@@ -865,6 +860,8 @@ cudaError_t launch_d(const KvParams &p, int num_sms, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   e = launch_programmatic(kern, num_sms, 32 * C::kWarps, C::kSmem, stream, p);
   if (e != cudaSuccess) return e;
+  // (a cache whose sequences have no more tiles than this never cuts an item)
+  if (p.by_item && cdiv(static_cast<int64_t>(p.max_pages) * p.page, 16) <= C::kWarps * kSoloTiles) return cudaSuccess;
   // an entry an item, or one a warp where there are more items than blocks; a row's parts to a block's warps where they may be many, or
   // where a row is all there is
   const bool apart = p.by_item || p.rows == 1;
