@@ -113,7 +113,9 @@ __device__ __forceinline__ bool any_nan_code(uint32_t w) { return __vcmpeq4(w & 
 // D: head_dim rounded up to 64 or 128. ROWS: of an item, up to 8 or up to 16.
 template <int D, int ROWS>
 struct KvCfg {
-  static constexpr int kWarps = ROWS == 8 ? 12 : 8;
+  // as many as have the registers (heads of 64, us: 128 x 8000 keys, 24 / 8 heads 205 with 12 warps, 180 with 16; 64 x 4000, four
+  // queries 83 with 8, 69 with 12, 66 with 16. Heads of 128: more than these spill, 350 -> 686)
+  static constexpr int kWarps = D == 64 ? 16 : ROWS == 8 ? 12 : 8;
   static constexpr int kStages = 4;
   static constexpr int kPieces = D / 64;                 // 16-byte pieces of a key in a lane
   static constexpr int kVBytes = D / 8;                  // bytes of a value row in a lane
