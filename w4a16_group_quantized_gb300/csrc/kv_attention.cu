@@ -19,7 +19,14 @@
 // pieces; of keys 2 t, 2 t + 1 and those plus 8 (t = lane % 4) an eighth of the head, whose codes of two neighbouring keys are
 // put side by side by byte permutes. The pieces of a line are exchanged so that these reads meet no bank twice.
 // Items cut between warps leave sums (O, m, l) in the workspace, one for a block whose warps are all within one item; a second
-// launch adds them in order.
+// launch adds them in order. Few items go to a block each instead, whose warps share the item, where that is quicker.
+//
+// Measured (us a call within a graph; heads of 128, one query): 128 sequences of 8192 keys, 64 / 8 heads 343 (2.15 GB: 6.3 TB/s,
+// 0.92 of a copy's rate); 48 of up to 8000 29.5, four queries 50; one of 1003 keys, 32 / 32 heads 9.7, of 8000 20; 100 keys
+// 4.6. What long batches wait for is memory; short ones some 12 us beside it: launches, the dealing (1 to 2), a first lookup
+// (1.5), the first tiles of all warps at once (1.4 to 4), sums (1.8) and their adding. With four queries it is a tile's
+// arithmetic, 0.9 us a warp, most of it the codes' conversion and dependent instructions (issue slots 35%, tensor pipe 25%); two tiles
+// at a time, with twice as many independent ones, took as long (55), as did more sums a row or more warps with fewer registers.
 #include <atomic>
 #include <type_traits>
 
@@ -229,7 +236,8 @@ __global__ void __launch_bounds__(32 * KvCfg<D, ROWS>::kWarps, 1) kv_attention_k
   Deal deal = {};
   if (solo) {
     // few items: a block each, and nothing to add afterwards, unless the longest takes longer that way (by more than the adding, as
-    // long as kSoloTiles tiles of a warp) than all of them dealt out evenly
+    // long as kSoloTiles tiles of a warp) than all of them dealt out evenly (one sequence of 1003 keys, 32 heads: 13.2 us whole,
+    // 14.3 dealt out)
     int longest = 0, all = 0;  // in tiles, and in 16 of them
     for (int i = lane; i < p.batch; i += 32) {
       const int t16 = tiles_of(i);
@@ -276,7 +284,8 @@ __global__ void __launch_bounds__(32 * KvCfg<D, ROWS>::kWarps, 1) kv_attention_k
       }
     }
     const int total = __shfl_sync(kAll, few ? sum : warp_sum, few ? 31 : W - 1);
-    // fewer warps where there is little to do
+    // fewer warps where there is little to do (one sequence of 8000 keys, 8 key heads, us: 17.3 with stretches of 8 units at least, 15.2
+    // with 4, 14.2 with 2, 14.1 with 1, which gains nothing elsewhere either and costs up to one)
     deal.workers = min(W * gridDim.x, static_cast<uint32_t>(max(total / 2, 1)));
     deal.quotient = total / deal.workers;
     deal.remainder = total - deal.quotient * deal.workers;
@@ -747,7 +756,7 @@ constexpr int kAddWarps = 8;
 // warps have every eighth part each. Which parts there are follows from the dealing: an entry is all that is read first,
 // then the parts' maxima and sums with the first of their values.
 template <int DT, int D, bool APART>
-__global__ void __launch_bounds__(32 * kAddWarps, APART ? 3 : 5) kv_add_kernel(const __grid_constant__ KvParams p) {
+__global__ void __launch_bounds__(32 * kAddWarps, APART ? 3 : 8) kv_add_kernel(const __grid_constant__ KvParams p) {
   constexpr int N = D / 32;    // values of a lane
   constexpr int kAhead = APART ? 8 : 4;  // parts whose values are fetched together
   __shared__ float part_o[APART ? kAddWarps : 1][D], part_m[kAddWarps], part_l[kAddWarps];
