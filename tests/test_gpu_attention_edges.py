@@ -267,3 +267,23 @@ def test_rope_of_any_frequency_and_position(dtype):
             slop = 2 * math.pi * 2.0 ** -33 * (abs(f) + 1) + 2.0 ** -21
             for got, want in ((out[i, 0, j].item(), math.cos(a)), (out[i, 0, 8 + j].item(), math.sin(a))):
                 assert abs(got - want) <= torch.finfo(dtype).eps / 2 * abs(want) + slop, (pos, f)
+
+
+@pytest.mark.parametrize("lens,n,hq,hk,dim,page,width", [
+    ([5000], 1, 1, 1, 128, 64, None), ([5000], 3, 8, 1, 64, 16, 400), ([4000, 10, 900], 1, 8, 8, 128, 64, 64), ([600], 1, 32, 32, 128, 64, None),
+    ([600], 1, 32, 32, 128, 64, 200), ([1344, 1345], 1, 4, 4, 128, 16, None), ([1345] * 5, 1, 30, 30, 64, 64, None), ([2500, 1] * 20, 1, 4, 4, 128, 64, None),
+    ([17 * i % 700 for i in range(33)], 2, 16, 8, 128, 16, None), ([31 * i % 900 for i in range(129)], 1, 8, 4, 64, 32, 64),
+    ([7 * i % 90 for i in range(600)], 1, 2, 1, 128, 16, None), ([3000] * 19, 4, 32, 8, 128, 64, None), ([300] * 70, 1, 12, 12, 48, 16, None)])
+@pytest.mark.parametrize("fill", [0xFF, 0x3C])
+def test_kv_attention_deals_in_a_used_workspace(lens, n, hq, hk, dim, page, width, fill):
+    """All ways to deal the items out, in a workspace that holds anything: few items whole or cut, many, and the same bits again and
+    with a table that is wider than it has to be."""
+    c = Cache(lens, hk, dim, page, seed=len(lens), max_pages=width)
+    q = randn(7, len(lens), n, hq, dim, dtype="bf16")
+    ws = torch.full((w4.w4_kv_attention_workspace_bytes(len(lens), n, hq, hk, dim),), fill, dtype=torch.uint8, device="cuda")
+    a = check_kv(c, q, lens, workspace=ws)
+    assert ws[:4].tolist() == [fill] * 4  # (the first word is another call's)
+    assert torch.equal(a, w4.w4_kv_attention(q, *c.args(), ints(lens), workspace=ws))
+    wider = torch.full((len(lens), c.table.shape[1] + 300), -1, dtype=torch.int32, device="cuda")
+    wider[:, : c.table.shape[1]] = c.table
+    assert torch.equal(a, w4.w4_kv_attention(q, *c.args()[:4], wider, ints(lens), workspace=ws))
