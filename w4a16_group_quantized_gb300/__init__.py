@@ -707,6 +707,13 @@ def _apart(t: torch.Tensor, name: str):
     return t.data_ptr(), ld
 
 
+def _empty_heads(t: torch.Tensor, stream) -> torch.Tensor:
+    """_empty of a tensor's type and shape (empty_like takes a third less time, but keeps strides)."""
+    if stream is None and t.is_contiguous():
+        return torch.empty_like(t)
+    return _empty(t.shape, t.dtype, t.device, stream)
+
+
 def _no_gradient(what: str):
     """For a call whose inputs require a gradient."""
     if torch.is_grad_enabled():
@@ -734,7 +741,7 @@ def w4_qk_norm_rope(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Te
     T, hq, dim = shape
     q_at, ldq = (q.data_ptr(), hq * dim) if q.is_contiguous() else _apart(q, "q")
     if q_out is None:
-        q_out = _empty(shape, dtype, q.device, stream)
+        q_out = _empty_heads(q, stream)
         qo_at, ldqo = q_out.data_ptr(), hq * dim
     else:
         qo_at, ldqo = _heads(q_out, "q_out", dtype, shape, device)
@@ -749,7 +756,7 @@ def w4_qk_norm_rope(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Te
         hk = shape[1]
         k_at, ldk = (k.data_ptr(), hk * dim) if k.is_contiguous() else _apart(k, "k")
         if k_out is None:
-            k_out = _empty(shape, dtype, q.device, stream)
+            k_out = _empty_heads(k, stream)
             ko_at, ldko = k_out.data_ptr(), hk * dim
         else:
             ko_at, ldko = _heads(k_out, "k_out", dtype, shape, device)
@@ -856,7 +863,7 @@ def w4_kv_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     pages, hk, page, max_pages = _cache(k_cache, v_cache, k_scale, v_scale, table, batch, None, dim, device)
     q_at, ldq = (q.data_ptr(), hq * dim) if q.is_contiguous() else _apart(q, "q")
     if out is None:
-        out = _empty(shape, dtype, q.device, stream)
+        out = _empty_heads(q, stream)
         o_at, ldo = out.data_ptr(), hq * dim
     else:
         o_at, ldo = _heads(out, "out", dtype, shape, device)
@@ -899,7 +906,7 @@ def w4_prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu: t
     k_at, ldk = (k.data_ptr(), hk * dim) if k.is_contiguous() else _apart(k, "k")
     v_at, ldv = _heads(v, "v", dtype, k_shape, device)
     if out is None:
-        out = _empty(shape, dtype, q.device, stream)
+        out = _empty_heads(q, stream)
         o_at, ldo = out.data_ptr(), hq * dim
     else:
         o_at, ldo = _heads(out, "out", dtype, shape, device)
