@@ -287,3 +287,26 @@ def test_kv_attention_deals_in_a_used_workspace(lens, n, hq, hk, dim, page, widt
     wider = torch.full((len(lens), c.table.shape[1] + 300), -1, dtype=torch.int32, device="cuda")
     wider[:, : c.table.shape[1]] = c.table
     assert torch.equal(a, w4.w4_kv_attention(q, *c.args()[:4], wider, ints(lens), workspace=ws))
+
+
+@pytest.mark.parametrize("lens,hq,hk,dim", [([130] * 40 + [1, 64, 65, 127, 128, 129, 700], 40, 8, 64), ([2100, 64, 63, 5] * 3, 40, 8, 48), ([60] * 130, 32, 32, 64)])
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_prompts_in_steps_of_64_keys(lens, hq, hk, dim, dtype):
+    """Many blocks of heads of up to 64, with rows behind a prompt's end, NaN and infinities among the last values."""
+    q, k, v = (randn(i, sum(lens), h, dim, dtype=dtype) for i, h in ((1, hq), (2, hk), (3, hk)))
+    check_prompt(q, k, v, lens)
+    a = w4.w4_prompt_attention(q, k, v, starts(lens))
+    # what the last row of each prompt holds is seen by that row alone
+    last = (starts(lens)[1:] - 1).long()
+    k2, v2 = k.clone(), v.clone()
+    k2[last], v2[last] = float("inf"), float("nan")
+    b = w4.w4_prompt_attention(q, k2, v2, starts(lens))
+    others = torch.ones(sum(lens), dtype=torch.bool, device="cuda")
+    others[last] = False
+    assert torch.equal(a[others], b[others]) and not torch.isfinite(b[last]).any()
+    # infinite values: the sum of what is finite has no part in it, other columns are as they were
+    v2 = v.clone()
+    v2[last, :, 3] = float("-inf")
+    b = w4.w4_prompt_attention(q, k, v2, starts(lens))
+    assert torch.equal(a[others], b[others]) and (b[last][:, :, 3] == float("-inf")).all()
+    assert torch.equal(torch.cat([a[..., :3], a[..., 4:]], -1), torch.cat([b[..., :3], b[..., 4:]], -1))

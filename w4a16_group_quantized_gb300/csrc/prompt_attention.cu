@@ -10,23 +10,23 @@
 // 128 rows a step. Tensor memory holds for each tile the scores S (128 x 128 fp32, one row a lane), whose columns the 16-bit
 // weights P then take as the second product's A operand, and O (128 x head_dim fp32): 256 columns a tile. Blocks of one tile go
 // two to an SM, where one's beginning and end run beside the other's products; blocks of two read keys and values half as
-// often. Roles (8 or 12 warps):
+// often. With heads of 64 and many blocks a step is 64 keys, and with 128 columns a tile four blocks go to an SM. Roles (8 or 12 warps):
 //   4 softmax warps a tile  a thread a row: S to registers, maximum, weights, P; at the end O / l to memory
 //   1 issue warp a tile   O += P V, the first half of the keys as soon as their weights are there, then the next
 //                         S = Q K^T. One tile's softmax runs beside the other's products, and one warp's waits (some 130
 //                         cycles each, even when over) beside the other's: with one warp for both tiles a step took 2825
 //                         cycles, 550 of them its waits
 //   1 copy warp           Q, then K and V of each step through a ring
-//   1 looking warp        sees the tiles' last V (the ones with rows that their first queries do not see)
+//   1 looking warp        sees the V of the block's own rows (which their first queries do not all see)
 // V is used as it stands, an MN-major operand.
 //
-// Rows that a query does not see have weight 0, but 0 * NaN is NaN. The last 128 rows of V of a tile, of which its first queries do
+// Rows that a query does not see have weight 0, but 0 * NaN is NaN. The rows of V that are the block's own, of which its first queries do
 // not see all, go into the product with zeros in the place of rows behind the sequence's end and of values that are not
 // finite; those are added at the end, read from memory again, to the rows that do see them.
 //
 // Measured (bf16): 8192 rows, 64 / 8 heads of 128: 613 us in a burst, 1.79 PFLOP/s, 0.94 of the rate of large products in a burst, 680
 // in longer runs, where the clock falls (0.95 of that rate there); the tensor pipe is busy 80% of the time. Heads of 64 are
-// bound by the exponentials instead: as many of them for half of the products (8192 rows 513 us, 1.07 PFLOP/s). A prompt of
+// bound by the softmax instead: as many exponentials for half of the products (8192 rows 488 us, 1.13 PFLOP/s). A prompt of
 // 37 rows: 5.7 to 6.5 us.
 //
 // Every wait is bounded (ptx.cuh).
@@ -58,19 +58,20 @@ struct PromptParams {
   int test_extra;
 };
 
-// D: head_dim rounded up to 64 or 128. TILES: of a block; blocks of one go two to an SM.
-template <int D, int TILES>
+// D: head_dim rounded up to 64 or 128. TILES: of a block. KEYS: of a step. BLOCKS: to an SM.
+template <int D, int TILES, int KEYS, int BLOCKS>
 struct PromptCfg {
   static constexpr int kThreads = (TILES + 1) * 128;
-  static constexpr int kHalf = kTile * 128;           // 64 values of 128 rows
-  static constexpr int kTileBytes = kHalf * (D / 64);  // 128 rows of q, k or v
-  static constexpr int kStages = TILES == 2 ? (D == 128 ? 5 : 10) : (D == 128 ? 2 : 5);
-  static constexpr int kSmem = (TILES + kStages) * kTileBytes + 1024;
-  static constexpr uint32_t kO = TILES * kTile;        // O's first column; O of the second tile D further
-  static constexpr uint32_t kColumns = TILES == 2 ? 512 : 256;
-  static_assert(kO + TILES * D <= kColumns, "tensor memory");
-  static constexpr int kRegsLaunch = TILES == 2 ? 168 : 128, kRegsSoftmax = TILES == 2 ? 216 : 208,
-                       kRegsOthers = TILES == 2 ? 72 : 48;
+  static constexpr int kQHalf = kTile * 128, kKvHalf = KEYS * 128;  // 64 values of a tile's rows, of a step's
+  static constexpr int kQBytes = kQHalf * (D / 64), kKvBytes = kKvHalf * (D / 64);
+  static constexpr int kStages = TILES == 2 || D == 64 && KEYS == 128 ? 5 : D == 64 ? 4 : 2;
+  static constexpr int kSmem = TILES * kQBytes + kStages * kKvBytes + 1024;
+  static constexpr uint32_t kO = TILES * KEYS;         // O's first column; O of the second tile D further
+  static constexpr uint32_t kColumns = 512 / BLOCKS >= 256 ? 512 / BLOCKS : 128;
+  static_assert(kO + TILES * D <= kColumns && kColumns * BLOCKS <= 512, "tensor memory");
+  static constexpr int kRegsLaunch = TILES == 2 ? 168 : BLOCKS == 2 ? 128 : BLOCKS == 3 ? 80 : 64;
+  static constexpr int kRegsSoftmax = TILES == 2 ? 216 : BLOCKS == 2 ? 208 : BLOCKS == 3 ? 120 : 96;
+  static constexpr int kRegsOthers = TILES == 2 ? 72 : BLOCKS == 2 ? 48 : BLOCKS == 3 ? 40 : 32;
   static_assert(TILES * kRegsSoftmax + kRegsOthers <= (TILES + 1) * kRegsLaunch, "the registers that the block was launched with");
 };
 
@@ -207,11 +208,11 @@ __device__ __forceinline__ void let_copies_land() {
   while (clock_cycles() - t0 < 20ull * 1000 * 1000) __nanosleep(1000);
 }
 
-template <int DT, int D, int TILES>
-__global__ void __launch_bounds__(PromptCfg<D, TILES>::kThreads, 3 - TILES)
+template <int DT, int D, int TILES, int KEYS, int BLOCKS>
+__global__ void __launch_bounds__(PromptCfg<D, TILES, KEYS, BLOCKS>::kThreads, BLOCKS)
     prompt_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map,
                             const __grid_constant__ CUtensorMap v_map, const __grid_constant__ PromptParams p) {
-  using C = PromptCfg<D, TILES>;
+  using C = PromptCfg<D, TILES, KEYS, BLOCKS>;
   constexpr int S = C::kStages, kIssue = 4 * TILES;  // the first warp that is not a softmax warp
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t q_bar[2], full_bar[S], free_bar[TILES][S], s_bar[2], p_bar[2][2], o_bar[2], last_bar[2], look_bar[2], turn_bar[2], drain_bar[2];
@@ -276,9 +277,11 @@ __global__ void __launch_bounds__(PromptCfg<D, TILES>::kThreads, 3 - TILES)
   }
   const Work w = work_sh;
   const bool two = TILES == 2 && w.len > w.row0 + kTile;  // the second tile has rows
-  const int n0 = w.row0 / kTile + 1;        // steps of the first tile; the second has one more
+  // steps: before the block's own rows, of the first tile, of the block
+  const int looked = w.row0 / KEYS;
+  const int n0 = looked + (KEYS == kTile ? 1 : min((w.len - w.row0 + KEYS - 1) / KEYS, kTile / KEYS));
   const int n = n0 + (two ? 1 : 0);
-  const uint32_t ring = smem_base + TILES * C::kTileBytes;
+  const uint32_t ring = smem_base + TILES * C::kQBytes;
   const uint32_t full0 = smem_u32(&full_bar[0]);
 
   if (warp < kIssue) {
@@ -287,9 +290,10 @@ __global__ void __launch_bounds__(PromptCfg<D, TILES>::kThreads, 3 - TILES)
     const int tile = warp / 4;
     const int r = warp % 4 * 32 + lane;  // the thread's row of the tile
     const uint32_t lanes = static_cast<uint32_t>(warp % 4 * 32) << 16;
-    const uint32_t s_at = tmem + lanes + tile * kTile, o_at = tmem + lanes + C::kO + tile * D;
+    const uint32_t s_at = tmem + lanes + tile * KEYS, o_at = tmem + lanes + C::kO + tile * D;
     const uint32_t s_full = smem_u32(&s_bar[tile]), p_full = smem_u32(&p_bar[tile][0]);
     const int steps = tile == 0 ? n0 : two ? n0 + 1 : 0;
+    const int own = KEYS == kTile ? steps - 1 : looked;  // the first step with keys that not all rows of the tile see
     const uint64_t scale2 = pack2(p.scale, p.scale);
     float m = -INFINITY;
     float l = 0.0f;
@@ -298,36 +302,39 @@ __global__ void __launch_bounds__(PromptCfg<D, TILES>::kThreads, 3 - TILES)
       ok = warp_wait(s_full, i & 1, abort_flag, p.err, p.wait_limit);
       if (!ok) break;
       tc_fence_after();
-      uint32_t s[4][32];
+      constexpr int N32 = KEYS / 32;
+      uint32_t s[N32][32];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) tmem_ld_32x32b_x32(s_at + 32 * c, s[c]);
+      for (int c = 0; c < N32; ++c) tmem_ld_32x32b_x32(s_at + 32 * c, s[c]);
       tmem_wait_ld();
-      if (i == steps - 1) {
+      if (i >= own) {
+        const int last = KEYS == kTile ? r : r - (i - own) * KEYS;
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
+        for (int c = 0; c < N32; ++c)
 #pragma unroll
           for (int j = 0; j < 32; ++j)
-            if (32 * c + j > r) s[c][j] = 0xFF800000u;  // -inf
+            if (32 * c + j > last) s[c][j] = 0xFF800000u;  // -inf
       }
       // the first half's weights by the maximum in use, and the newest maximum beside them: for most steps the one in use stays
       auto row_top = [&]() {
-        float top[4];
+        float top[N32];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
+        for (int c = 0; c < N32; ++c) {
           top[c] = __uint_as_float(s[c][0]);
 #pragma unroll
           for (int j = 1; j + 1 < 32; j += 2) top[c] = max3(top[c], __uint_as_float(s[c][j]), __uint_as_float(s[c][j + 1]));
           top[c] = fmaxf(top[c], __uint_as_float(s[c][31]));
         }
-        return max3(max3(top[0], top[1], top[2]), top[3], m);
+        if constexpr (N32 == 2) return max3(top[0], top[1], m);
+        else return max3(max3(top[0], top[1], top[N32 - 2]), top[N32 - 1], m);
       };
       uint64_t off2, sum[2];
-      uint32_t w2[32];
-      auto weights = [&](int c) {
+      uint32_t w2[KEYS / 4];
+      auto weights = [&](int half) {
 #pragma unroll
-        for (int j = 0; j < 32; ++j) {
-          const uint64_t e = fma2(pack2(__uint_as_float(s[c + j / 16][2 * (j % 16)]), __uint_as_float(s[c + j / 16][2 * (j % 16) + 1])),
-                                  scale2, off2);
+        for (int j = 0; j < KEYS / 4; ++j) {
+          const int c = half * (N32 / 2) + j / 16;
+          const uint64_t e = fma2(pack2(__uint_as_float(s[c][2 * (j % 16)]), __uint_as_float(s[c][2 * (j % 16) + 1])), scale2, off2);
           float a, b;
           unpack2(e, &a, &b);
           a = ex2(a);
@@ -336,12 +343,15 @@ __global__ void __launch_bounds__(PromptCfg<D, TILES>::kThreads, 3 - TILES)
           w2[j] = weights2<DT>(a, b);
         }
       };
-      auto hand_over = [&](int c) {
-        tmem_st_32x32b_x32(s_at + 16 * c, w2);
+      auto hand_over = [&](int half) {
+        if constexpr (KEYS == 128)
+          tmem_st_32x32b_x32(s_at + 32 * half, w2);
+        else
+          tmem_st_32x32b_x16(s_at + 16 * half, w2);
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(p_full + 4 * c);  // (c 0, 2: the two barriers)
+        if (lane == 0) mbar_arrive(p_full + 8 * half);
       };
       // (a loop, so that the code is there once: it fills much of the instruction cache)
 #pragma unroll 1
@@ -372,14 +382,14 @@ __global__ void __launch_bounds__(PromptCfg<D, TILES>::kThreads, 3 - TILES)
         m = now;
       }
       hand_over(0);
-      weights(2);
-      hand_over(2);
+      weights(1);
+      hand_over(1);
       float a, b;
       unpack2(add2(sum[0], sum[1]), &a, &b);
       l += a + b;
     }
     if (ok && steps > 0) ok = warp_wait(smem_u32(&o_bar[tile]), 0, abort_flag, p.err, p.wait_limit);
-    for (int i = 0; i <= tile; ++i)
+    for (int i = 0; i < (KEYS == kTile ? tile + 1 : steps - looked); ++i)
       if (ok && steps > 0) ok = warp_wait(smem_u32(&look_bar[i]), 0, abort_flag, p.err, p.wait_limit);
     if (ok && steps > 0) {
       tc_fence_after();
@@ -391,12 +401,12 @@ __global__ void __launch_bounds__(PromptCfg<D, TILES>::kThreads, 3 - TILES)
                    : "memory");
       const int row = e.row0 + tile * kTile + r;
       // (the second tile's rows see all of the first one's last V)
-      const bool odd = (*static_cast<volatile uint32_t *>(&odd_sh[0]) | *static_cast<volatile uint32_t *>(&odd_sh[tile])) != 0;
+      const bool odd = (*static_cast<volatile uint32_t *>(&odd_sh[0]) | *static_cast<volatile uint32_t *>(&odd_sh[KEYS == kTile ? tile : steps - looked - 1])) != 0;
       const float inv = 1.0f / l;
       // each warp's rows by way of the tile's place of Q, which is done with, so that they are stored as whole lines; the 16-byte
       // pieces of a row are exchanged against bank conflicts
       constexpr int kPieces = D / 8;
-      const uint32_t place = smem_base + tile * C::kTileBytes + warp % 4 * 32 * D * 2;
+      const uint32_t place = smem_base + tile * C::kQBytes + warp % 4 * 32 * D * 2;
 #pragma unroll
       for (int c = 0; c < D / 32; ++c) {
         uint32_t o[32];
@@ -432,23 +442,22 @@ __global__ void __launch_bounds__(PromptCfg<D, TILES>::kThreads, 3 - TILES)
       // -------------------------------------------------------- products
       const int tile = warp - kIssue;
       const int steps = tile == 0 ? n0 : two ? n : 0;
-      constexpr uint32_t qk = idesc_f16_f32(kTile, kTile, DT == kDtypeBf16), pv = idesc_f16_f32(kTile, D, DT == kDtypeBf16, true);
-      const uint32_t s_at = tmem + tile * kTile, o_at = tmem + C::kO + tile * D;
+      constexpr uint32_t qk = idesc_f16_f32(kTile, KEYS, DT == kDtypeBf16), pv = idesc_f16_f32(kTile, D, DT == kDtypeBf16, true);
+      const uint32_t s_at = tmem + tile * KEYS, o_at = tmem + C::kO + tile * D;
       const uint32_t free0 = smem_u32(&free_bar[tile][0]);
       const uint32_t s_full = smem_u32(&s_bar[tile]), p_full = smem_u32(&p_bar[tile][0]);
       auto scores = [&](uint32_t stage) {
-        const uint64_t a = sw128_kmajor_desc(smem_base + tile * C::kTileBytes), b = sw128_kmajor_desc(ring + stage * C::kTileBytes);
+        const uint64_t a = sw128_kmajor_desc(smem_base + tile * C::kQBytes), b = sw128_kmajor_desc(ring + stage * C::kKvBytes);
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint64_t step = static_cast<uint64_t>(kk / 4 * (C::kHalf >> 4) + kk % 4 * 2);
-          mma_f16_ss(s_at, a + step, b + step, qk, kk > 0);
-        }
+        for (int kk = 0; kk < D / 16; ++kk)
+          mma_f16_ss(s_at, a + static_cast<uint64_t>(kk / 4 * (C::kQHalf >> 4) + kk % 4 * 2),
+                     b + static_cast<uint64_t>(kk / 4 * (C::kKvHalf >> 4) + kk % 4 * 2), qk, kk > 0);
         mma_commit(s_full);
       };
       auto values = [&](uint32_t stage, int half, bool first) {
-        const uint64_t b = sw128_mnmajor_desc(ring + stage * C::kTileBytes, C::kHalf);
+        const uint64_t b = sw128_mnmajor_desc(ring + stage * C::kKvBytes, C::kKvHalf);
 #pragma unroll
-        for (int kk = half * 4; kk < half * 4 + 4; ++kk)
+        for (int kk = half * (KEYS / 32); kk < (half + 1) * (KEYS / 32); ++kk)
           mma_f16_ts(o_at, s_at + kk * 8, b + static_cast<uint64_t>(kk * (2048 >> 4)), pv, !first || kk > 0);
       };
       auto landed = [&](int item) {
@@ -466,7 +475,7 @@ __global__ void __launch_bounds__(PromptCfg<D, TILES>::kThreads, 3 - TILES)
       for (int i = 0; ok && i < steps; ++i) {
         const uint32_t vs = static_cast<uint32_t>((2 * i + 1) % S), ks = static_cast<uint32_t>((2 * i + 2) % S);
         // (the looking warp has waited for the last steps' V, and may have changed it)
-        ok = i < n0 - 1 ? landed(2 * i + 1) : warp_wait(smem_u32(&look_bar[i - (n0 - 1)]), 0, abort_flag, p.err, p.wait_limit);
+        ok = i < looked ? landed(2 * i + 1) : warp_wait(smem_u32(&look_bar[i - looked]), 0, abort_flag, p.err, p.wait_limit);
         if (ok && i + 1 < steps) ok = landed(2 * i + 2);
         // the tiles' products go in turns: run together they would take twice as long each and leave the tensor pipe idle together
         if (ok && two && (tile == 0 ? i > 0 : i < n0))
@@ -500,14 +509,14 @@ __global__ void __launch_bounds__(PromptCfg<D, TILES>::kThreads, 3 - TILES)
       }
     } else if (warp == kIssue + 2) {
       // ---------------------------------------------------------- copies
-      auto load = [&](const CUtensorMap *map, uint32_t to, int head, int row, uint32_t bar) {
-        mbar_arrive_expect_tx(bar, C::kTileBytes);
+      auto load = [&](const CUtensorMap *map, uint32_t to, int half_bytes, int head, int row, uint32_t bar) {
+        mbar_arrive_expect_tx(bar, half_bytes * (D / 64));
 #pragma unroll
-        for (int half = 0; half < D / 64; ++half) tma_load_3d(to + half * C::kHalf, map, 64 * half, head, row, bar);
+        for (int half = 0; half < D / 64; ++half) tma_load_3d(to + half * half_bytes, map, 64 * half, head, row, bar);
       };
       const int kv_head = w.head / p.r;
       bool ok = true;
-      if (elect_one()) load(&q_map, smem_base, w.head, w.begin + w.row0, smem_u32(&q_bar[0]));
+      if (elect_one()) load(&q_map, smem_base, C::kQHalf, w.head, w.begin + w.row0, smem_u32(&q_bar[0]));
       __syncwarp();
       for (int item = 0; item < 2 * n; ++item) {
         const uint32_t stage = static_cast<uint32_t>(item % S);
@@ -517,26 +526,26 @@ __global__ void __launch_bounds__(PromptCfg<D, TILES>::kThreads, 3 - TILES)
         if (!ok) break;
         if (elect_one()) {
           // the last steps' V signals barriers of its own, which have one phase: the looking warps do not follow the ring
-          const uint32_t bar = item % 2 && item / 2 >= n0 - 1 ? smem_u32(&last_bar[item / 2 - (n0 - 1)]) : full0 + 8 * stage;
-          load(item % 2 ? &v_map : &k_map, ring + stage * C::kTileBytes, kv_head, w.begin + item / 2 * kTile, bar);
-          if (item == 0 && two) load(&q_map, smem_base + C::kTileBytes, w.head, w.begin + w.row0 + kTile, smem_u32(&q_bar[1]));
+          const uint32_t bar = item % 2 && item / 2 >= looked ? smem_u32(&last_bar[item / 2 - looked]) : full0 + 8 * stage;
+          load(item % 2 ? &v_map : &k_map, ring + stage * C::kKvBytes, C::kKvHalf, kv_head, w.begin + item / 2 * KEYS, bar);
+          if (item == 0 && two) load(&q_map, smem_base + C::kQBytes, C::kQHalf, w.head, w.begin + w.row0 + kTile, smem_u32(&q_bar[1]));
         }
         __syncwarp();
       }
     } else if (warp == kIssue + 3) {
-      // ------------------------------------- the last V of each tile (its place is not used again)
-      for (int tile = 0; tile < (two ? 2 : 1); ++tile) {
-        const int step = n0 - 1 + tile;
+      // ------------------------- V of the steps with the block's own rows (its places are not used again)
+      for (int tile = 0; tile < n - looked; ++tile) {
+        const int step = looked + tile;
         const uint32_t stage = static_cast<uint32_t>((2 * step + 1) % S);
         if (!warp_wait(smem_u32(&last_bar[tile]), 0, abort_flag, p.err, p.wait_limit)) break;
-        const int live = min(w.len - step * kTile, kTile);  // rows of the sequence in it
-        const uint32_t at = ring + stage * C::kTileBytes;
+        const int live = min(w.len - step * KEYS, KEYS);  // rows of the sequence in it
+        const uint32_t at = ring + stage * C::kKvBytes;
         // an exponent of all ones: one more carries into the sign's place
         constexpr uint32_t kInf = DT == kDtypeBf16 ? 0x7F807F80u : 0x7C007C00u, kOne = DT == kDtypeBf16 ? 0x00800080u : 0x04000400u;
         uint32_t carries = 0;
         for (int h = 0; h < D / 64; ++h) {
-          const uint32_t end = at + h * C::kHalf + live * 128, stop = at + (h + 1) * C::kHalf;
-          uint32_t i = at + h * C::kHalf + 16 * lane;
+          const uint32_t end = at + h * C::kKvHalf + live * 128, stop = at + (h + 1) * C::kKvHalf;
+          uint32_t i = at + h * C::kKvHalf + 16 * lane;
 #pragma unroll 8
           for (; i < end; i += 512) {
             const uint4 x = lds128(i);
@@ -548,7 +557,7 @@ __global__ void __launch_bounds__(PromptCfg<D, TILES>::kThreads, 3 - TILES)
         if (odd) {
           for (int h = 0; h < D / 64; ++h)
 #pragma unroll 1
-            for (uint32_t i = at + h * C::kHalf + 16 * lane; i < at + h * C::kHalf + live * 128; i += 512) {
+            for (uint32_t i = at + h * C::kKvHalf + 16 * lane; i < at + h * C::kKvHalf + live * 128; i += 512) {
               const uint4 x = lds128(i);
               auto finite = [&](uint32_t w) {
                 const uint32_t bad = ((w & kInf) + kOne) & 0x80008000u;
@@ -580,18 +589,18 @@ __global__ void __launch_bounds__(PromptCfg<D, TILES>::kThreads, 3 - TILES)
   }
 }
 
-template <int DT, int D, int TILES>
+template <int DT, int D, int TILES, int KEYS, int BLOCKS>
 cudaError_t launch_tiles(const PromptArgs &a, const PromptParams &p, cudaStream_t stream) {
-  auto kern = prompt_attention_kernel<DT, D, TILES>;
-  using C = PromptCfg<D, TILES>;
+  auto kern = prompt_attention_kernel<DT, D, TILES, KEYS, BLOCKS>;
+  using C = PromptCfg<D, TILES, KEYS, BLOCKS>;
   static std::atomic<uint64_t> set{0};
   const cudaError_t e = allow_smem(kern, C::kSmem, &set);
   if (e != cudaSuccess) return e;
   CUtensorMap q_map, k_map, v_map;
   const int k_heads = a.k_heads;
   if (!make_heads_map(&q_map, a.q, a.T, a.q_heads, a.head_dim, a.ldq, kTile, DT) ||
-      !make_heads_map(&k_map, a.k, a.T, k_heads, a.head_dim, a.ldk, kTile, DT) ||
-      !make_heads_map(&v_map, a.v, a.T, k_heads, a.head_dim, a.ldv, kTile, DT))
+      !make_heads_map(&k_map, a.k, a.T, k_heads, a.head_dim, a.ldk, KEYS, DT) ||
+      !make_heads_map(&v_map, a.v, a.T, k_heads, a.head_dim, a.ldv, KEYS, DT))
     return cudaErrorInvalidValue;
   const int64_t blocks = (a.T / (TILES * kTile) + a.batch) * a.q_heads;
   return launch_programmatic(kern, static_cast<int>(blocks), C::kThreads, C::kSmem, stream, q_map, k_map, v_map, p);
@@ -600,10 +609,17 @@ cudaError_t launch_tiles(const PromptArgs &a, const PromptParams &p, cudaStream_
 // One tile or two a block (bf16, us, one / two). Heads of 64: 8192 rows x 64 heads 513 / 561, nine prompts of up to 1900 rows x 24
 // heads 28 / 36, four of 256 x 32 8.5 / 7.8. Heads of 128: 8192 x 64 675 / 650, 4096 x 2 x 32 213 / 200, 2048 x 32 37.9 / 37.0,
 // 1000 x 8 14.4 / 18.1: two, where they are a block for each SM.
+// Heads of 64, steps of 128 keys and two blocks an SM / of 64 and four: a step of 64 takes nearly as long as one of 128, but more of them
+// run beside each other, which pays where there are many blocks for each place: 256 x 64 x 32 heads 106 / 76, 512 x 32 x 32 105 / 83, forty of
+// up to 3000 x 32 163 / 137, 8192 x 64 520 / 488, 4096 x 64 154 / 143, 1000 x 8 x 16 39 / 33; nine of up to 1900 x 24 30 / 34,
+// 2048 x 32 27 / 39, 1000 x 8 11.6 / 14.8. Taken from 12 tiles an SM on.
 template <int DT>
 cudaError_t launch_type(const PromptArgs &a, const PromptParams &p, int num_sms, cudaStream_t stream) {
-  if (a.head_dim <= 64) return launch_tiles<DT, 64, 1>(a, p, stream);
-  return cdiv(a.T, 2 * kTile) * a.q_heads < num_sms ? launch_tiles<DT, 128, 1>(a, p, stream) : launch_tiles<DT, 128, 2>(a, p, stream);
+  if (a.head_dim <= 64)
+    return cdiv(a.T, kTile) * a.q_heads < 12 * num_sms ? launch_tiles<DT, 64, 1, 128, 2>(a, p, stream)
+                                                       : launch_tiles<DT, 64, 1, 64, 4>(a, p, stream);
+  return cdiv(a.T, 2 * kTile) * a.q_heads < num_sms ? launch_tiles<DT, 128, 1, 128, 2>(a, p, stream)
+                                                    : launch_tiles<DT, 128, 2, 128, 1>(a, p, stream);
 }
 
 }  // namespace
