@@ -608,7 +608,8 @@ cudaError_t launch_tiles(const PromptArgs &a, const PromptParams &p, cudaStream_
 
 // One tile or two a block (bf16, us, one / two). Heads of 64: 8192 rows x 64 heads 513 / 561, nine prompts of up to 1900 rows x 24
 // heads 28 / 36, four of 256 x 32 8.5 / 7.8. Heads of 128: 8192 x 64 675 / 650, 4096 x 2 x 32 213 / 200, 2048 x 32 37.9 / 37.0,
-// 1000 x 8 14.4 / 18.1: two, where they are a block for each SM.
+// 1000 x 8 14.4 / 18.1: two, where they are a block for each SM and prompts are long enough for whole ones (64 x 128 x 32 heads 113 / 202,
+// 128 x 64 66 / 108, 256 x 64 138 / 147, up to 500 x 64 83 / 120, 300 x 40 136 / 163; 512 x 32 148 / 145, 1000 x 16 188 / 177).
 // Heads of 64, steps of 128 keys and two blocks an SM / of 64 and four: a step of 64 takes nearly as long as one of 128, but more of them
 // run beside each other, which pays where there are many blocks for each place: 256 x 64 x 32 heads 106 / 76, 512 x 32 x 32 105 / 83, forty of
 // up to 3000 x 32 163 / 137, 8192 x 64 520 / 488, 4096 x 64 154 / 143, 1000 x 8 x 16 39 / 33; nine of up to 1900 x 24 30 / 34,
@@ -618,7 +619,8 @@ cudaError_t launch_type(const PromptArgs &a, const PromptParams &p, int num_sms,
   if (a.head_dim <= 64)
     return cdiv(a.T, kTile) * a.q_heads < 12 * num_sms ? launch_tiles<DT, 64, 1, 128, 2>(a, p, stream)
                                                        : launch_tiles<DT, 64, 1, 64, 4>(a, p, stream);
-  return cdiv(a.T, 2 * kTile) * a.q_heads < num_sms ? launch_tiles<DT, 128, 1, 128, 2>(a, p, stream)
+  const bool few = cdiv(a.T, 2 * kTile) * a.q_heads < num_sms, brief = a.T < 4 * kTile * static_cast<int64_t>(a.batch);
+  return few || brief ? launch_tiles<DT, 128, 1, 128, 2>(a, p, stream)
                                                     : launch_tiles<DT, 128, 2, 128, 1>(a, p, stream);
 }
 
