@@ -188,9 +188,10 @@ __device__ __forceinline__ bool find_work(const PromptParams &p, int rows, Work 
   }
   at -= all_from(m + 1);
   for (int b = 0; b < p.batch; b += 32) {
-    const uint32_t has = __ballot_sync(kAll, count(b + lane) > m);
+    const bool mine = count(b + lane) > m;
+    const uint32_t has = __ballot_sync(kAll, mine);
     if (at < __popc(has)) {
-      const int from = __fns(has, 0, at + 1);
+      const int from = __ffs(__ballot_sync(kAll, mine && __popc(has & ((1u << lane) - 1u)) == at)) - 1;  // the at-th that has one
       w->begin = __shfl_sync(kAll, begin, from);
       w->len = __shfl_sync(kAll, len, from);
       w->row0 = m * rows;
