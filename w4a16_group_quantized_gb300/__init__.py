@@ -230,7 +230,7 @@ def w4a16_gemm_plan(M: int, N: int, K: int, g: int):
 class Workspace:
     """A zero-filled device workspace that grows on demand (reuse it across calls on one stream: a stream other than the one it
     was made on waits for that one first, as for any tensor). ``scratch`` is a second buffer, for the calls that leave
-    arbitrary bytes behind (w4a16_experts, w4_lora_add): the GEMMs' counters in the first have to stay zero.
+    arbitrary bytes behind (w4a16_experts, w4_lora_add, the attention calls): the GEMMs' counters in the first have to stay zero.
 
     A buffer that was outgrown is kept: calls that are still running, or graphs that were captured, use it. Each buffer is
     at least twice the one before, so all of them together are less than twice the last."""
