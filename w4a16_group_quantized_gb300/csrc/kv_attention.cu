@@ -44,7 +44,7 @@ using namespace detail;
 constexpr uint32_t kAll = 0xffffffffu;
 constexpr int kMostWarps = 16;    // of a block
 constexpr int kItemCost = 4;      // what beginning an item costs, in tiles
-constexpr int kSoloTiles = 7;     // what adding parts takes, in tiles of a warp
+constexpr int kSoloTiles = 6;     // what adding parts takes, in tiles of a warp
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kSlack = 8.0f;    // how far a score may pass the maximum in use (log2 of the weight)
 // Scales of values that go into the weights: 2^-40 to 2^40, so that a weight of one page beside another's stays a normal number
@@ -235,17 +235,17 @@ __global__ void __launch_bounds__(32 * KvCfg<D, ROWS>::kWarps, 1) kv_attention_k
   bool together, solo = p.batch * p.items <= gridDim.x;
   Deal deal = {};
   if (solo) {
-    // few items: a block each, and nothing to add afterwards, unless the longest takes longer that way (by more than the adding, as
-    // long as kSoloTiles tiles of a warp) than all of them dealt out evenly (one sequence of 1003 keys, 32 heads: 13.2 us whole,
-    // 14.3 dealt out)
+    // few items: a block each, and nothing to add afterwards, unless the longest takes longer that way, by more than the adding (as
+    // long as kSoloTiles tiles of a warp), than 1.2 times all of them dealt out evenly (us, whole / dealt out: one sequence of
+    // 1003 keys, 32 heads 9.8 / 10.3, of 1500 12.5 / 11.0; 8 of 2000, 8 key heads 17.3 / 19.0; 16 of 1003 12.8 / 14.8)
     int longest = 0, all = 0;  // in tiles, and in 16 of them
     for (int i = lane; i < p.batch; i += 32) {
       const int t16 = tiles_of(i);
       longest = max(longest, t16);
       all += t16 / 16;
     }
-    solo = static_cast<int64_t>(__reduce_max_sync(kAll, longest) - W * kSoloTiles) * gridDim.x <=
-           static_cast<int64_t>(__reduce_add_sync(kAll, all)) * (16 * p.items);
+    solo = static_cast<int64_t>(__reduce_max_sync(kAll, longest) - W * kSoloTiles) * (5 * gridDim.x) <=
+           static_cast<int64_t>(__reduce_add_sync(kAll, all)) * (6 * 16 * p.items);
   }
   if (solo) {
     if (blockIdx.x == 0 && threadIdx.x == 0) *p.workers = 0;
