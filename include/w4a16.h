@@ -683,7 +683,9 @@ W4_API int w4_kv_append(const w4_kv_append_args *args, void *stream);
  * Numerics: q (for bf16 rows times a power of two, which keeps every bit that
  * matters), the codes and the weights w enter the products as fp16, sums and
  * the softmax's maximum and sum are fp32, one rounding at the end. w is the one
- * operand that is rounded: to 2^-11 of itself, or 2^-25 of the largest.
+ * operand that is rounded: to 2^-11 of itself, or 2^-25 of the largest, however
+ * unlike the pages' scales of values are (what a page adds may be lost where its
+ * scale is below 2^-100 of another one's of the sequence and head).
  *
  * q_dev, out_dev  [batch, n, q_heads, head_dim] of dtype, rows (i, j) ldq and
  *               ldo values apart (multiples of 8), 16-byte aligned.

@@ -2,10 +2,14 @@
 //
 // For a sequence and key head the n query rows of the r query heads that share it are n * r rows (row = j * r + head), taken 16
 // at a time (an item). For a tile of 16 keys, which lies in one page: S = q . codes, s = S * (k scale * softmax scale *
-// log2 e) + log2(v scale), a row's running maximum m, w = 2^(s - m) in fp16, O += w . codes, l += (sum of w) / v scale: with the
-// page's scale of the values inside the weight no product needs a scale of its own. m may lag behind by 2^8 as a weight, so
-// that O is rescaled a few times in an item. What of a scale of values is no positive number within 2^+-40 goes by a product
-// of its own.
+// log2 e) + log2(v scale / unit), a row's running maximum m, w = 2^(s - m) in fp16, O += w . codes, l += (sum of w) / (v scale /
+// unit): with the page's scale of the values inside the weight no product needs a scale of its own. m may lag behind by 2^5 as a
+// weight, so that O is rescaled a few times in an item.
+// O is in units of `unit`, a warp's own: the scale of the first page or of a later one that is more than 2^5 times the one in
+// use (O is rescaled then). Scales from 2^-5 to 2^5 units go into the weights, which are kept 2^10 times larger than
+// 2^(s - m): 2^15 at most, and what fp16's smallest step loses, 2^-25, is 2^-35 of the maximum in use, 2^-25 of a row's largest
+// exp(score) at least, whichever pages' scales stand beside each other. Smaller scales and those that are not positive and finite go
+// by a product of their own, in fp32.
 //
 // The products are register-operand ones (mma.sync m16n8k16, fp16 operands, fp32 sums): e4m3 codes are exact in fp16, and so
 // are q's values (bf16 rows times a power of two that keeps them within fp16's range). S has the rows on its M side and the
@@ -46,10 +50,11 @@ constexpr int kMostWarps = 16;    // of a block
 constexpr int kItemCost = 4;      // what beginning an item costs, in tiles
 constexpr int kSoloTiles = 6;     // what adding parts takes, in tiles of a warp
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kSlack = 8.0f;    // how far a score may pass the maximum in use (log2 of the weight)
-// Scales of values that go into the weights: 2^-40 to 2^40, so that a weight of one page beside another's stays a normal number
-// of 32 bits (it counts in the sum l, however small its part of O).
-constexpr float kScaleMin = 0x1p-40f, kScaleMax = 0x1p40f;
+// log2 of how far a score may pass the maximum in use, of the scales that go into the weights (either way from the unit), and of
+// what the weights are raised by: kSlack + kRaise within fp16's range, and 2 kFold <= kRaise, so that a raised weight of
+// 2^-kFold units under a maximum of 2^kFold loses no more to fp16's smallest step than an unraised one under its own.
+constexpr float kSlack = 5.0f, kFold = 5.0f, kRaise = 10.0f;
+constexpr float kLeastUnit = -126.0f;  // log2
 
 // How `units` are dealt out to warps: the first unit of each one's stretch is quotient * w + remainder * w / workers.
 struct Deal {
@@ -88,7 +93,7 @@ struct KvParams {
   int32_t *workers;  // how many warps have a stretch
   int32_t *cut;      // [workers], or [items] by_item: whether cuts has an item
   CutItem *cuts;
-  float *sums;     // [2 * warps]: O [rows][D], m [rows], l [rows], padded to 16 bytes, of a stretch's first and last item
+  float *sums;     // [2 * warps]: O / l [rows][D], m [rows], l [rows], padded to 16 bytes, of a stretch's first and last item
   int64_t ldq, ldo, pages;
   int batch, n, max_pages, q_heads, k_heads, head_dim, page, r, row_tiles, rows, items;  // items of a sequence
   int by_item;     // few items: an entry of cut and cuts for each, else for each warp
@@ -155,9 +160,8 @@ __device__ __forceinline__ int64_t row_at(const KvParams &p, int b, int j, int i
 }
 
 template <int DT>
-__device__ __forceinline__ uint4 eight_out(const float (&v)[8], float f) {
-  return make_uint4(out_bits2<DT>(v[0] * f, v[1] * f), out_bits2<DT>(v[2] * f, v[3] * f), out_bits2<DT>(v[4] * f, v[5] * f),
-                    out_bits2<DT>(v[6] * f, v[7] * f));
+__device__ __forceinline__ uint4 eight_out(const float (&v)[8]) {
+  return make_uint4(out_bits2<DT>(v[0], v[1]), out_bits2<DT>(v[2], v[3]), out_bits2<DT>(v[4], v[5]), out_bits2<DT>(v[6], v[7]));
 }
 
 // 0 for a row that saw nothing (sum 0; where it saw something the sum is positive or NaN).
@@ -216,8 +220,8 @@ __global__ void __launch_bounds__(32 * KvCfg<D, ROWS>::kWarps, 1) kv_attention_k
   __shared__ int upto[32 * W];  // units of a warp's sequences up to and with the thread's
   __shared__ float row_m[W][ROWS], row_l[W][ROWS];
   const int warp = __shfl_sync(kAll, threadIdx.x / 32, 0), lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
-  // what the lookups found of a tile's page: k scale, log2 of the part of the v scale that goes into the weights, 1 / that part, the rest of it (1, or what
-  // the products are to be multiplied with)
+  // what the lookups found of a tile's page: k scale, log2 of the v scale's size (NaN where it is not finite), its sign (itself where it is not
+  // finite)
   float4 *info = reinterpret_cast<float4 *>(smem) + warp * 64;
   const uint32_t ring = smem_u32(smem + C::kInfo) + warp * C::kRing;
   griddep_launch_dependents();
@@ -364,9 +368,8 @@ __global__ void __launch_bounds__(32 * KvCfg<D, ROWS>::kWarps, 1) kv_attention_k
     if (!pending) return;
     pending = false;
     const float size = fabsf(found_vs);
-    const bool plain = size >= kScaleMin && size <= kScaleMax;
-    const float part = plain ? size : size > kScaleMax ? kScaleMax : kScaleMin;
-    info[(book + lane) % 64] = make_float4(found_ks, log2f(part), 1.0f / part, plain ? copysignf(1.0f, found_vs) : found_vs / part);
+    const bool finite = size < INFINITY;
+    info[(book + lane) % 64] = make_float4(found_ks, finite ? log2f(size) : NAN, finite ? copysignf(1.0f, found_vs) : found_vs, 0.0f);
     __syncwarp();
   };
   auto send = [&]() {
@@ -436,7 +439,7 @@ __global__ void __launch_bounds__(32 * KvCfg<D, ROWS>::kWarps, 1) kv_attention_k
 
   // ------------------------------------------------------------ products
   uint32_t q[D / 16][2 * RR];  // a step's pairs: (row g, pair 0), (row g, pair 1) and, of 16 rows, those of row g + 8
-  float o[NO][2], m[RR], l[RR], mul[RR];
+  float o[NO][2], m[RR], l[RR], mul[RR], unit = kLeastUnit;  // (m: the maximum in use less kRaise; unit: log2 of it)
   int sees[RR], least = 0, len = 0;
   auto begin_item = [&]() {
     const int rt = j - p.row_tiles_div.div(j) * p.row_tiles;
@@ -497,6 +500,7 @@ __global__ void __launch_bounds__(32 * KvCfg<D, ROWS>::kWarps, 1) kv_attention_k
       l[i] = 0.0f;
     }
     least = static_cast<int>(__reduce_min_sync(kAll, least));
+    unit = kLeastUnit;
 #pragma unroll
     for (int x = 0; x < NO; ++x) o[x][0] = o[x][1] = 0.0f;
   };
@@ -546,6 +550,11 @@ __global__ void __launch_bounds__(32 * KvCfg<D, ROWS>::kWarps, 1) kv_attention_k
         }
       }
       const bool border = key0 + 16 > least;  // some row does not see all of the tile
+      // the page's scale in units: inside the weights, or what the products are multiplied with
+      const float apart = st.y - unit, size = ex2(-fabsf(apart));
+      const float move = apart > kFold ? size : 1.0f, rest = apart < -kFold ? st.z * size : st.z;
+      const float scale = fabsf(apart) <= kFold ? apart : 0.0f;
+      if (apart > kFold) unit = st.y;
       float top[RR];
 #pragma unroll
       for (int r2 = 0; r2 < RR; ++r2) {
@@ -553,7 +562,7 @@ __global__ void __launch_bounds__(32 * KvCfg<D, ROWS>::kWarps, 1) kv_attention_k
 #pragma unroll
         for (int u = 0; u < 2; ++u)
 #pragma unroll
-          for (int e = 2 * r2; e < 2 * r2 + 2; ++e) s[u][e] = fmaf(s[u][e], f, st.y);
+          for (int e = 2 * r2; e < 2 * r2 + 2; ++e) s[u][e] = fmaf(s[u][e], f, scale);
       }
       if (border) {
 #pragma unroll
@@ -571,15 +580,16 @@ __global__ void __launch_bounds__(32 * KvCfg<D, ROWS>::kWarps, 1) kv_attention_k
       for (int x = 1; x < 4; x *= 2)
 #pragma unroll
         for (int r2 = 0; r2 < RR; ++r2) top[r2] = fmaxf(top[r2], __shfl_xor_sync(kAll, top[r2], x));
-      // (-inf + 8 is below any score: a row's first tile sets its maximum)
-      if (__any_sync(kAll, top[0] > m[0] + kSlack || top[RR - 1] > m[RR - 1] + kSlack)) {
+      // (-inf + 15 is below any score: a row's first tile sets its maximum)
+      if (__any_sync(kAll, top[0] > m[0] + (kSlack + kRaise) || top[RR - 1] > m[RR - 1] + (kSlack + kRaise) || move != 1.0f)) {
         float alpha[RR];
 #pragma unroll
         for (int r2 = 0; r2 < RR; ++r2) {
-          const float now = top[r2] > m[r2] + kSlack ? top[r2] : m[r2];  // (a row's own scores alone say when)
+          const float now = top[r2] > m[r2] + (kSlack + kRaise) ? top[r2] - kRaise : m[r2];  // (a row's own scores alone say when)
           alpha[r2] = now == m[r2] ? 1.0f : ex2(m[r2] - now);
           m[r2] = now;
           l[r2] *= alpha[r2];
+          alpha[r2] *= move;
         }
         if constexpr (ROWS == 16) {
 #pragma unroll
@@ -590,6 +600,7 @@ __global__ void __launch_bounds__(32 * KvCfg<D, ROWS>::kWarps, 1) kv_attention_k
           for (int x = 0; x < NO; ++x) o[x][0] *= a0, o[x][1] *= a1;
         }
       }
+      const float per_unit = ex2(-scale);
 #pragma unroll
       for (int r2 = 0; r2 < RR; ++r2) {
         const float base = m[r2] == -INFINITY ? 0.0f : m[r2];  // (nothing seen yet: weights of 0)
@@ -597,7 +608,7 @@ __global__ void __launch_bounds__(32 * KvCfg<D, ROWS>::kWarps, 1) kv_attention_k
         for (int u = 0; u < 2; ++u)
 #pragma unroll
           for (int e = 2 * r2; e < 2 * r2 + 2; ++e) s[u][e] = ex2(s[u][e] - base);
-        l[r2] = fmaf((s[0][2 * r2] + s[0][2 * r2 + 1]) + (s[1][2 * r2] + s[1][2 * r2 + 1]), st.z, l[r2]);
+        l[r2] = fmaf((s[0][2 * r2] + s[0][2 * r2 + 1]) + (s[1][2 * r2] + s[1][2 * r2 + 1]), per_unit, l[r2]);
       }
       uint32_t w[2 * RR];  // as q's: (row g, keys 2 t ..), (row g, those plus 8), row g + 8
 #pragma unroll
@@ -605,7 +616,7 @@ __global__ void __launch_bounds__(32 * KvCfg<D, ROWS>::kWarps, 1) kv_attention_k
         w[2 * r2] = half2_bits(s[0][2 * r2], s[0][2 * r2 + 1]);
         w[2 * r2 + 1] = half2_bits(s[1][2 * r2], s[1][2 * r2 + 1]);
       }
-      bool odd = st.w != 1.0f;
+      bool odd = rest != 1.0f;
       if (border && !odd) {
         // 0 * NaN is NaN: whether the tile, of which some rows do not see all, holds NaN
 #pragma unroll
@@ -617,20 +628,20 @@ __global__ void __launch_bounds__(32 * KvCfg<D, ROWS>::kWarps, 1) kv_attention_k
       if (!odd) {
         add_values<D, ROWS, false>(o, v, w, 1.0f, 0, ROWS);
       } else {
-        // each query's rows by themselves, with zeros in the place of what they do not see, and the rest of the scale on the
-        // products
+        // the rest of the scale on the products, and where some rows do not see all, each query's rows by themselves, with zeros
+        // in the place of what they do not see
         const int rt = j - p.row_tiles_div.div(j) * p.row_tiles;
 #pragma unroll 1
-        for (int token = 0; token < p.n; ++token) {
-          const int limit = min(max(len - p.n + token + 1, 0), most);
-          const int lo = token * p.r - rt * 16, hi = lo + p.r;  // the query's rows of the item
+        for (int token = 0; token < (border ? p.n : 1); ++token) {
+          const int limit = border ? min(max(len - p.n + token + 1, 0), most) : key0 + 16;
+          const int lo = border ? token * p.r - rt * 16 : 0, hi = border ? lo + p.r : ROWS;  // the query's rows of the item
           if (limit <= key0 || hi <= 0 || lo >= ROWS) continue;
           uint32_t y[4][C::kVBytes / 4];
 #pragma unroll
           for (int c = 0; c < 4; ++c)
 #pragma unroll
             for (int x = 0; x < C::kVBytes / 4; ++x) y[c][x] = key0 + 2 * t + c % 2 + c / 2 * 8 >= limit ? 0u : v[c][x];
-          add_values<D, ROWS, true>(o, y, w, st.w, lo, hi);
+          add_values<D, ROWS, true>(o, y, w, rest, lo, hi);
         }
       }
     }
@@ -664,7 +675,7 @@ __global__ void __launch_bounds__(32 * KvCfg<D, ROWS>::kWarps, 1) kv_attention_k
       for (int r2 = 0; r2 < 2; ++r2) {
         const int row = ROWS == 16 ? g + 8 * r2 : 2 * t + r2;
         if (row >= rows) continue;
-        const float inv = over_sum(lr[r2]);
+        const float inv = over_sum(lr[r2]), one_unit = ex2(unit);
         uint16_t *out = p.out + row_at(p, b, j, row, p.ldo);
 #pragma unroll
         for (int e = 0; e < RR; ++e)
@@ -672,10 +683,10 @@ __global__ void __launch_bounds__(32 * KvCfg<D, ROWS>::kWarps, 1) kv_attention_k
           for (int x = 0; x < D / 8; x += 8) {
             float v8[8];
 #pragma unroll
-            for (int y = 0; y < 8; ++y) v8[y] = ROWS == 16 ? o[(2 * (x + y) + r2) % NO][e] : o[(x + y) % NO][r2];
+            for (int y = 0; y < 8; ++y) v8[y] = (ROWS == 16 ? o[(2 * (x + y) + r2) % NO][e] : o[(x + y) % NO][r2]) * inv * one_unit;
             const int d = ROWS == 16 ? (2 * t + e) * (D / 8) + x : g * (D / 8) + x;
             if (whole) {
-              if (d < head_dim) *reinterpret_cast<uint4 *>(out + d) = eight_out<DT>(v8, inv);
+              if (d < head_dim) *reinterpret_cast<uint4 *>(out + d) = eight_out<DT>(v8);
             } else {
               *reinterpret_cast<float4 *>(sums + row * D + d) = make_float4(v8[0], v8[1], v8[2], v8[3]);
               *reinterpret_cast<float4 *>(sums + row * D + d + 4) = make_float4(v8[4], v8[5], v8[6], v8[7]);
@@ -713,10 +724,16 @@ __global__ void __launch_bounds__(32 * KvCfg<D, ROWS>::kWarps, 1) kv_attention_k
     l[r2] += __shfl_xor_sync(kAll, l[r2], 2);
     if (t == 0) row_m[warp][g + 8 * r2] = m[r2], row_l[warp][g + 8 * r2] = l[r2];
   }
+  // (as O / l, so that parts of unlike units can be added)
+  float inv[2];
+  inv[0] = over_sum(ROWS == 16 ? l[0] : __shfl_sync(kAll, l[0], 8 * t));
+  inv[1] = over_sum(ROWS == 16 ? l[RR - 1] : __shfl_sync(kAll, l[0], 8 * t + 4));
+  const float one_unit = ex2(unit);
 #pragma unroll
   for (int x = 0; x < NO; ++x)
 #pragma unroll
-    for (int i = 0; i < 2; ++i) sums[(warp * ROWS + row_of<ROWS>(x, i)) * C::kSumRow + value_of<D, ROWS>(x, i)] = o[x][i];
+    for (int i = 0; i < 2; ++i)
+      sums[(warp * ROWS + row_of<ROWS>(x, i)) * C::kSumRow + value_of<D, ROWS>(x, i)] = o[x][i] * inv[ROWS == 16 ? x % 2 : i] * one_unit;
   __syncthreads();
   const bool here = begin >= block_from, whole = here && end <= block_to;
   if (lane == 0 && from < to && !solo) {
@@ -728,21 +745,25 @@ __global__ void __launch_bounds__(32 * KvCfg<D, ROWS>::kWarps, 1) kv_attention_k
   float *slot = p.sums + (static_cast<int64_t>(2) * blockIdx.x * warps + (here ? 1 : 0)) * p.rows * (D + 4);
   for (int i = threadIdx.x; i < rows * (D / 4); i += 32 * W) {
     const int row = i / (D / 4), d = i % (D / 4) * 4;
-    float high = -INFINITY, sum_l = 0.0f, x[4] = {};
+    float high = -INFINITY, sum_l = 0.0f, part_l[W], x[4] = {};
 #pragma unroll
     for (int w = 0; w < W; ++w) high = fmaxf(high, row_m[w][row]);
-#pragma unroll 4
+#pragma unroll
     for (int w = 0; w < W; ++w) {
-      const float f = row_m[w][row] == high ? 1.0f : ex2(row_m[w][row] - high);
-      sum_l = fmaf(row_l[w][row], f, sum_l);
+      part_l[w] = row_l[w][row] * (row_m[w][row] == high ? 1.0f : ex2(row_m[w][row] - high));
+      sum_l += part_l[w];
+    }
+    const float over = over_sum(sum_l);
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      const float f = part_l[w] * over;
       const float4 y = *reinterpret_cast<const float4 *>(sums + (w * ROWS + row) * C::kSumRow + d);
       x[0] = fmaf(y.x, f, x[0]), x[1] = fmaf(y.y, f, x[1]), x[2] = fmaf(y.z, f, x[2]), x[3] = fmaf(y.w, f, x[3]);
     }
     if (whole) {
-      const float inv = over_sum(sum_l);
       if (d < head_dim)
         *reinterpret_cast<uint2 *>(p.out + row_at(p, one_b, one_j, row, p.ldo) + d) =
-            make_uint2(out_bits2<DT>(x[0] * inv, x[1] * inv), out_bits2<DT>(x[2] * inv, x[3] * inv));
+            make_uint2(out_bits2<DT>(x[0], x[1]), out_bits2<DT>(x[2], x[3]));
     } else {
       *reinterpret_cast<float4 *>(slot + row * D + d) = make_float4(x[0], x[1], x[2], x[3]);
       if (d == 0) slot[p.rows * D + row] = high, slot[p.rows * (D + 1) + row] = sum_l;
@@ -813,12 +834,14 @@ __global__ void __launch_bounds__(32 * kAddWarps, APART ? 3 : 8) kv_add_kernel(c
     for (int i = 16; i > 0; i /= 2) high = fmaxf(high, __shfl_xor_sync(kAll, high, i));
     high = fmaxf(high, m);
     // (a maximum that is not above the one so far, -inf beside -inf among them, weighs 1 as it stands)
-    const float f = lane >= here ? 0.0f : m_part == high ? 1.0f : ex2(m_part - high);
-    const float f_old = m == high ? 1.0f : ex2(m - high);
-    float l_sum = lane < here ? l_part * f : 0.0f;
+    const float l_here = lane >= here ? 0.0f : m_part == high ? l_part : l_part * ex2(m_part - high);
+    const float l_old = m == high ? l : l * ex2(m - high);
+    float l_sum = l_here;
 #pragma unroll
     for (int i = 16; i > 0; i /= 2) l_sum += __shfl_xor_sync(kAll, l_sum, i);
-    l = fmaf(l, f_old, l_sum);
+    l = l_old + l_sum;
+    // the parts are O / l of theirs: each weighs its share of the sum
+    const float over = over_sum(l), f = l_here * over, f_old = l_old * over;
 #pragma unroll
     for (int x = 0; x < N; ++x) o[x] *= f_old;
     m = high;
@@ -843,23 +866,26 @@ __global__ void __launch_bounds__(32 * kAddWarps, APART ? 3 : 8) kv_add_kernel(c
 #pragma unroll
     for (int w = 0; w < kAddWarps; ++w) high = fmaxf(high, part_m[w]);
     l = 0.0f;
+    float f[kAddWarps];
+#pragma unroll
+    for (int w = 0; w < kAddWarps; ++w) {
+      f[w] = part_m[w] == high ? part_l[w] : part_l[w] * ex2(part_m[w] - high);
+      l += f[w];
+    }
+    const float over = over_sum(l);
 #pragma unroll
     for (int x = 0; x < N; ++x) o[x] = 0.0f;
 #pragma unroll
-    for (int w = 0; w < kAddWarps; ++w) {
-      const float f = part_m[w] == high ? 1.0f : ex2(part_m[w] - high);
-      l = fmaf(part_l[w], f, l);
+    for (int w = 0; w < kAddWarps; ++w)
 #pragma unroll
-      for (int x = 0; x < N; ++x) o[x] = fmaf(part_o[APART ? w : 0][N * lane + x], f, o[x]);
-    }
+      for (int x = 0; x < N; ++x) o[x] = fmaf(part_o[APART ? w : 0][N * lane + x], f[w] * over, o[x]);
   }
   if (N * lane >= p.head_dim) return;
-  const float inv = over_sum(l);
   uint16_t *out = p.out + row_at(p, it.b, it.j, row, p.ldo) + N * lane;
   if constexpr (N == 4)
-    *reinterpret_cast<uint2 *>(out) = make_uint2(out_bits2<DT>(o[0] * inv, o[1] * inv), out_bits2<DT>(o[2] * inv, o[3] * inv));
+    *reinterpret_cast<uint2 *>(out) = make_uint2(out_bits2<DT>(o[0], o[1]), out_bits2<DT>(o[2], o[3]));
   else
-    *reinterpret_cast<uint32_t *>(out) = out_bits2<DT>(o[0] * inv, o[1] * inv);
+    *reinterpret_cast<uint32_t *>(out) = out_bits2<DT>(o[0], o[1]);
 }
 
 template <int DT, int D, int ROWS>
