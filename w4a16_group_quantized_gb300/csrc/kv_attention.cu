@@ -164,8 +164,13 @@ __device__ __forceinline__ uint4 eight_out(const float (&v)[8]) {
   return make_uint4(out_bits2<DT>(v[0], v[1]), out_bits2<DT>(v[2], v[3]), out_bits2<DT>(v[4], v[5]), out_bits2<DT>(v[6], v[7]));
 }
 
-// 0 for a row that saw nothing (sum 0; where it saw something the sum is positive or NaN).
+// The least maximum of a row that has seen a key: all its scores may be -inf, which is not the same as seeing nothing.
+constexpr float kLeastMax = -3.402823466e38f;
+
+// 1 / l of a part, 0 where it has no weight.
 __device__ __forceinline__ float over_sum(float l) { return l == 0.0f ? 0.0f : 1.0f / l; }
+// Of all of a row: 0 where it saw nothing, NaN where all that it saw scores -inf.
+__device__ __forceinline__ float over_sum(float l, float m) { return l != 0.0f ? 1.0f / l : m == -INFINITY ? 0.0f : NAN; }
 
 // Which row the sums o[s][i] are of, and which value of it.
 template <int ROWS>
@@ -609,6 +614,7 @@ __global__ void __launch_bounds__(32 * KvCfg<D, ROWS>::kWarps, 1) kv_attention_k
 #pragma unroll
           for (int e = 2 * r2; e < 2 * r2 + 2; ++e) s[u][e] = ex2(s[u][e] - base);
         l[r2] = fmaf((s[0][2 * r2] + s[0][2 * r2 + 1]) + (s[1][2 * r2] + s[1][2 * r2 + 1]), per_unit, l[r2]);
+        if (key0 < sees[r2]) m[r2] = fmaxf(m[r2], kLeastMax);
       }
       uint32_t w[2 * RR];  // as q's: (row g, keys 2 t ..), (row g, those plus 8), row g + 8
 #pragma unroll
@@ -665,17 +671,19 @@ __global__ void __launch_bounds__(32 * KvCfg<D, ROWS>::kWarps, 1) kv_attention_k
       }
       float *sums = p.sums + (static_cast<int64_t>(2 * me) + (here ? 1 : 0)) * p.rows * (D + 4);
       // a lane's sums of two rows: ROWS 16: rows g and g + 8 of two stretches of values, 8: rows 2 t and 2 t + 1 of one
-      float lr[2];
+      float lr[2], mr[2];
       if constexpr (ROWS == 16) {
         lr[0] = l[0], lr[1] = l[RR - 1];
+        mr[0] = m[0], mr[1] = m[RR - 1];
       } else {
         lr[0] = __shfl_sync(kAll, l[0], 8 * t), lr[1] = __shfl_sync(kAll, l[0], 8 * t + 4);
+        mr[0] = __shfl_sync(kAll, m[0], 8 * t), mr[1] = __shfl_sync(kAll, m[0], 8 * t + 4);
       }
 #pragma unroll
       for (int r2 = 0; r2 < 2; ++r2) {
         const int row = ROWS == 16 ? g + 8 * r2 : 2 * t + r2;
         if (row >= rows) continue;
-        const float inv = over_sum(lr[r2]), one_unit = ex2(unit);
+        const float inv = whole ? over_sum(lr[r2], mr[r2]) : over_sum(lr[r2]), one_unit = ex2(unit);
         uint16_t *out = p.out + row_at(p, b, j, row, p.ldo);
 #pragma unroll
         for (int e = 0; e < RR; ++e)
@@ -753,7 +761,7 @@ __global__ void __launch_bounds__(32 * KvCfg<D, ROWS>::kWarps, 1) kv_attention_k
       part_l[w] = row_l[w][row] * (row_m[w][row] == high ? 1.0f : ex2(row_m[w][row] - high));
       sum_l += part_l[w];
     }
-    const float over = over_sum(sum_l);
+    const float over = whole ? over_sum(sum_l, high) : over_sum(sum_l);
 #pragma unroll
     for (int w = 0; w < W; ++w) {
       const float f = part_l[w] * over;
@@ -865,6 +873,7 @@ __global__ void __launch_bounds__(32 * kAddWarps, APART ? 3 : 8) kv_add_kernel(c
     float high = -INFINITY;
 #pragma unroll
     for (int w = 0; w < kAddWarps; ++w) high = fmaxf(high, part_m[w]);
+    m = high;
     l = 0.0f;
     float f[kAddWarps];
 #pragma unroll
@@ -881,6 +890,10 @@ __global__ void __launch_bounds__(32 * kAddWarps, APART ? 3 : 8) kv_add_kernel(c
       for (int x = 0; x < N; ++x) o[x] = fmaf(part_o[APART ? w : 0][N * lane + x], f[w] * over, o[x]);
   }
   if (N * lane >= p.head_dim) return;
+  if (l == 0.0f && m > -INFINITY) {  // (as over_sum of all of a row)
+#pragma unroll
+    for (int x = 0; x < N; ++x) o[x] = NAN;
+  }
   uint16_t *out = p.out + row_at(p, it.b, it.j, row, p.ldo) + N * lane;
   if constexpr (N == 4)
     *reinterpret_cast<uint2 *>(out) = make_uint2(out_bits2<DT>(o[0], o[1]), out_bits2<DT>(o[2], o[3]));
