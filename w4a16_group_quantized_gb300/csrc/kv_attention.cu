@@ -5,11 +5,11 @@
 // log2 e) + log2(v scale / unit), a row's running maximum m, w = 2^(s - m) in fp16, O += w . codes, l += (sum of w) / (v scale /
 // unit): with the page's scale of the values inside the weight no product needs a scale of its own. m may lag behind by 2^5 as a
 // weight, so that O is rescaled a few times in an item.
-// O is in units of `unit`, a warp's own: the scale of the first page or of a later one that is more than 2^5 times the one in
-// use (O is rescaled then). Scales from 2^-5 to 2^5 units go into the weights, which are kept 2^10 times larger than
-// 2^(s - m): 2^15 at most, and what fp16's smallest step loses, 2^-25, is 2^-35 of the maximum in use, 2^-25 of a row's largest
-// exp(score) at least, whichever pages' scales stand beside each other. Smaller scales and those that are not positive and finite go
-// by a product of their own, in fp32.
+// O is in units of `unit`, a warp's own: the power of two below the largest scale that its lookups, of 32 tiles each, have found
+// in the item so far (O is rescaled where it grows). Scales from 2^-8 units up go into the weights, smaller ones and those that
+// are not positive and finite go by a product of their own, in fp32. The weights are kept 2^10 times larger than 2^(s - m): 2^15
+// at most; m is at most 2 above a row's largest exp(score) and a page's scale 2^8 below it, so that fp16's smallest step
+// loses at most 2^-26 of that exp(score), whichever pages' scales stand beside each other.
 //
 // The products are register-operand ones (mma.sync m16n8k16, fp16 operands, fp32 sums): e4m3 codes are exact in fp16, and so
 // are q's values (bf16 rows times a power of two that keeps them within fp16's range). S has the rows on its M side and the
@@ -50,10 +50,9 @@ constexpr int kMostWarps = 16;    // of a block
 constexpr int kItemCost = 4;      // what beginning an item costs, in tiles
 constexpr int kSoloTiles = 6;     // what adding parts takes, in tiles of a warp
 constexpr float kLog2e = 1.4426950408889634f;
-// log2 of how far a score may pass the maximum in use, of the scales that go into the weights (either way from the unit), and of
-// what the weights are raised by: kSlack + kRaise within fp16's range, and 2 kFold <= kRaise, so that a raised weight of
-// 2^-kFold units under a maximum of 2^kFold loses no more to fp16's smallest step than an unraised one under its own.
-constexpr float kSlack = 5.0f, kFold = 5.0f, kRaise = 10.0f;
+// log2 of how far a score may pass the maximum in use, of the least scale in units that goes into the weights, and of what the
+// weights are raised by.
+constexpr float kSlack = 5.0f, kFold = -8.0f, kRaise = 10.0f;
 constexpr float kLeastUnit = -126.0f;  // log2
 
 // How `units` are dealt out to warps: the first unit of each one's stretch is quotient * w + remainder * w / workers.
@@ -167,10 +166,17 @@ __device__ __forceinline__ uint4 eight_out(const float (&v)[8]) {
 // The least maximum of a row that has seen a key: all its scores may be -inf, which is not the same as seeing nothing.
 constexpr float kLeastMax = -3.402823466e38f;
 
-// 1 / l of a part, 0 where it has no weight.
-__device__ __forceinline__ float over_sum(float l) { return l == 0.0f ? 0.0f : 1.0f / l; }
-// Of all of a row: 0 where it saw nothing, NaN where all that it saw scores -inf.
+// 1 / l of all of a row: 0 where it saw nothing, NaN where all that it saw scores -inf.
 __device__ __forceinline__ float over_sum(float l, float m) { return l != 0.0f ? 1.0f / l : m == -INFINITY ? 0.0f : NAN; }
+
+// Parts of a row are kept as O / l, in fp32 whatever their units, with l times 2^-20: sums of O / l times that stay far from fp32's ends. 1 / l of
+// a part, to a unit or two; 0 where it has no weight.
+constexpr float kPartSum = 0x1p-20f;
+__device__ __forceinline__ float over_part(float l) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(l));
+  return l == 0.0f ? 0.0f : y;
+}
 
 // Which row the sums o[s][i] are of, and which value of it.
 template <int ROWS>
@@ -225,8 +231,8 @@ __global__ void __launch_bounds__(32 * KvCfg<D, ROWS>::kWarps, 1) kv_attention_k
   __shared__ int upto[32 * W];  // units of a warp's sequences up to and with the thread's
   __shared__ float row_m[W][ROWS], row_l[W][ROWS];
   const int warp = __shfl_sync(kAll, threadIdx.x / 32, 0), lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
-  // what the lookups found of a tile's page: k scale, log2 of the v scale's size (NaN where it is not finite), its sign (itself where it is not
-  // finite)
+  // what the lookups found of a tile's page: k scale, log2 of the v scale in units as far as it goes into the weights, log2 of the unit, and the rest
+  // of the scale (1, or what the products are to be multiplied with)
   float4 *info = reinterpret_cast<float4 *>(smem) + warp * 64;
   const uint32_t ring = smem_u32(smem + C::kInfo) + warp * C::kRing;
   griddep_launch_dependents();
@@ -369,12 +375,18 @@ __global__ void __launch_bounds__(32 * KvCfg<D, ROWS>::kWarps, 1) kv_attention_k
   // what the scales of the last lookup become: done after its first copies have been sent
   float found_ks = 0.0f, found_vs = 0.0f;
   bool pending = false;
+  float unit_found = kLeastUnit;  // of the item so far
   auto keep_scales = [&]() {
     if (!pending) return;
     pending = false;
     const float size = fabsf(found_vs);
     const bool finite = size < INFINITY;
-    info[(book + lane) % 64] = make_float4(found_ks, finite ? log2f(size) : NAN, finite ? copysignf(1.0f, found_vs) : found_vs, 0.0f);
+    const int exponent = static_cast<int>(__reduce_max_sync(kAll, finite ? __float_as_uint(size) >> 23 : 0u));
+    unit_found = fmaxf(unit_found, static_cast<float>(exponent - 127));
+    const float in_units = log2f(size) - unit_found;
+    const bool inside = in_units >= kFold && finite;
+    const float rest = inside ? copysignf(1.0f, found_vs) : finite ? copysignf(ex2(in_units), found_vs) : found_vs;
+    info[(book + lane) % 64] = make_float4(found_ks, inside ? in_units : 0.0f, unit_found, rest);
     __syncwarp();
   };
   auto send = [&]() {
@@ -382,14 +394,15 @@ __global__ void __launch_bounds__(32 * KvCfg<D, ROWS>::kWarps, 1) kv_attention_k
     __syncwarp();  // the place's last tile has been read
     if (cat < to) {
       if (ct - first >= found) {  // look up the next 32 tiles of the item
-        if (ct == 0 || found == 0) ckeys = min(p.lens[cb], most);
+        keep_scales();
+        if (ct == 0 || found == 0) ckeys = min(p.lens[cb], most), unit_found = kLeastUnit;
         first = ct;
         found = min(32, ctiles - ct);
         // (places go round: when it comes to a lookup, at most S tiles of the ones before are still to be worked on)
-        keep_scales();
         book = next_book;
         next_book = (book + found) % 64;
         int64_t off = -1;
+        found_vs = 0.0f;
         if (lane < found) {
           const int key0 = (ct + lane) * 16;
           const int pi = p.page_div.div(key0), h = p.row_tiles_div.div(cj);
@@ -555,11 +568,6 @@ __global__ void __launch_bounds__(32 * KvCfg<D, ROWS>::kWarps, 1) kv_attention_k
         }
       }
       const bool border = key0 + 16 > least;  // some row does not see all of the tile
-      // the page's scale in units: inside the weights, or what the products are multiplied with
-      const float apart = st.y - unit, size = ex2(-fabsf(apart));
-      const float move = apart > kFold ? size : 1.0f, rest = apart < -kFold ? st.z * size : st.z;
-      const float scale = fabsf(apart) <= kFold ? apart : 0.0f;
-      if (apart > kFold) unit = st.y;
       float top[RR];
 #pragma unroll
       for (int r2 = 0; r2 < RR; ++r2) {
@@ -567,7 +575,7 @@ __global__ void __launch_bounds__(32 * KvCfg<D, ROWS>::kWarps, 1) kv_attention_k
 #pragma unroll
         for (int u = 0; u < 2; ++u)
 #pragma unroll
-          for (int e = 2 * r2; e < 2 * r2 + 2; ++e) s[u][e] = fmaf(s[u][e], f, scale);
+          for (int e = 2 * r2; e < 2 * r2 + 2; ++e) s[u][e] = fmaf(s[u][e], f, st.y);
       }
       if (border) {
 #pragma unroll
@@ -586,7 +594,9 @@ __global__ void __launch_bounds__(32 * KvCfg<D, ROWS>::kWarps, 1) kv_attention_k
 #pragma unroll
         for (int r2 = 0; r2 < RR; ++r2) top[r2] = fmaxf(top[r2], __shfl_xor_sync(kAll, top[r2], x));
       // (-inf + 15 is below any score: a row's first tile sets its maximum)
-      if (__any_sync(kAll, top[0] > m[0] + (kSlack + kRaise) || top[RR - 1] > m[RR - 1] + (kSlack + kRaise) || move != 1.0f)) {
+      if (__any_sync(kAll, top[0] > m[0] + (kSlack + kRaise) || top[RR - 1] > m[RR - 1] + (kSlack + kRaise) || st.z != unit)) {
+        const float move = ex2(unit - st.z);
+        unit = st.z;
         float alpha[RR];
 #pragma unroll
         for (int r2 = 0; r2 < RR; ++r2) {
@@ -605,7 +615,7 @@ __global__ void __launch_bounds__(32 * KvCfg<D, ROWS>::kWarps, 1) kv_attention_k
           for (int x = 0; x < NO; ++x) o[x][0] *= a0, o[x][1] *= a1;
         }
       }
-      const float per_unit = ex2(-scale);
+      const float per_unit = ex2(-st.y);
 #pragma unroll
       for (int r2 = 0; r2 < RR; ++r2) {
         const float base = m[r2] == -INFINITY ? 0.0f : m[r2];  // (nothing seen yet: weights of 0)
@@ -622,7 +632,7 @@ __global__ void __launch_bounds__(32 * KvCfg<D, ROWS>::kWarps, 1) kv_attention_k
         w[2 * r2] = half2_bits(s[0][2 * r2], s[0][2 * r2 + 1]);
         w[2 * r2 + 1] = half2_bits(s[1][2 * r2], s[1][2 * r2 + 1]);
       }
-      bool odd = rest != 1.0f;
+      bool odd = st.w != 1.0f;
       if (border && !odd) {
         // 0 * NaN is NaN: whether the tile, of which some rows do not see all, holds NaN
 #pragma unroll
@@ -647,7 +657,7 @@ __global__ void __launch_bounds__(32 * KvCfg<D, ROWS>::kWarps, 1) kv_attention_k
           for (int c = 0; c < 4; ++c)
 #pragma unroll
             for (int x = 0; x < C::kVBytes / 4; ++x) y[c][x] = key0 + 2 * t + c % 2 + c / 2 * 8 >= limit ? 0u : v[c][x];
-          add_values<D, ROWS, true>(o, y, w, rest, lo, hi);
+          add_values<D, ROWS, true>(o, y, w, st.w, lo, hi);
         }
       }
     }
@@ -683,7 +693,7 @@ __global__ void __launch_bounds__(32 * KvCfg<D, ROWS>::kWarps, 1) kv_attention_k
       for (int r2 = 0; r2 < 2; ++r2) {
         const int row = ROWS == 16 ? g + 8 * r2 : 2 * t + r2;
         if (row >= rows) continue;
-        const float inv = whole ? over_sum(lr[r2], mr[r2]) : over_sum(lr[r2]), one_unit = ex2(unit);
+        const float inv = whole ? over_sum(lr[r2], mr[r2]) : over_part(lr[r2]), one_unit = ex2(unit);
         uint16_t *out = p.out + row_at(p, b, j, row, p.ldo);
 #pragma unroll
         for (int e = 0; e < RR; ++e)
@@ -704,7 +714,7 @@ __global__ void __launch_bounds__(32 * KvCfg<D, ROWS>::kWarps, 1) kv_attention_k
       if (!whole && t == 0) {
 #pragma unroll
         for (int r2 = 0; r2 < RR; ++r2)
-          if (g + 8 * r2 < rows) sums[p.rows * D + g + 8 * r2] = m[r2], sums[p.rows * (D + 1) + g + 8 * r2] = l[r2];
+          if (g + 8 * r2 < rows) sums[p.rows * D + g + 8 * r2] = m[r2], sums[p.rows * (D + 1) + g + 8 * r2] = l[r2] * kPartSum;
       }
     }
     ++at;
@@ -730,12 +740,12 @@ __global__ void __launch_bounds__(32 * KvCfg<D, ROWS>::kWarps, 1) kv_attention_k
   for (int r2 = 0; r2 < RR; ++r2) {
     l[r2] += __shfl_xor_sync(kAll, l[r2], 1);
     l[r2] += __shfl_xor_sync(kAll, l[r2], 2);
-    if (t == 0) row_m[warp][g + 8 * r2] = m[r2], row_l[warp][g + 8 * r2] = l[r2];
+    if (t == 0) row_m[warp][g + 8 * r2] = m[r2], row_l[warp][g + 8 * r2] = l[r2] * kPartSum;
   }
   // (as O / l, so that parts of unlike units can be added)
   float inv[2];
-  inv[0] = over_sum(ROWS == 16 ? l[0] : __shfl_sync(kAll, l[0], 8 * t));
-  inv[1] = over_sum(ROWS == 16 ? l[RR - 1] : __shfl_sync(kAll, l[0], 8 * t + 4));
+  inv[0] = over_part(ROWS == 16 ? l[0] : __shfl_sync(kAll, l[0], 8 * t));
+  inv[1] = over_part(ROWS == 16 ? l[RR - 1] : __shfl_sync(kAll, l[0], 8 * t + 4));
   const float one_unit = ex2(unit);
 #pragma unroll
   for (int x = 0; x < NO; ++x)
@@ -753,21 +763,19 @@ __global__ void __launch_bounds__(32 * KvCfg<D, ROWS>::kWarps, 1) kv_attention_k
   float *slot = p.sums + (static_cast<int64_t>(2) * blockIdx.x * warps + (here ? 1 : 0)) * p.rows * (D + 4);
   for (int i = threadIdx.x; i < rows * (D / 4); i += 32 * W) {
     const int row = i / (D / 4), d = i % (D / 4) * 4;
-    float high = -INFINITY, sum_l = 0.0f, part_l[W], x[4] = {};
+    float high = -INFINITY, sum_l = 0.0f, x[4] = {};
 #pragma unroll
     for (int w = 0; w < W; ++w) high = fmaxf(high, row_m[w][row]);
-#pragma unroll
+#pragma unroll 4
     for (int w = 0; w < W; ++w) {
-      part_l[w] = row_l[w][row] * (row_m[w][row] == high ? 1.0f : ex2(row_m[w][row] - high));
-      sum_l += part_l[w];
-    }
-    const float over = whole ? over_sum(sum_l, high) : over_sum(sum_l);
-#pragma unroll
-    for (int w = 0; w < W; ++w) {
-      const float f = part_l[w] * over;
+      const float f = row_m[w][row] == high ? row_l[w][row] : row_l[w][row] * ex2(row_m[w][row] - high);
+      sum_l += f;
       const float4 y = *reinterpret_cast<const float4 *>(sums + (w * ROWS + row) * C::kSumRow + d);
       x[0] = fmaf(y.x, f, x[0]), x[1] = fmaf(y.y, f, x[1]), x[2] = fmaf(y.z, f, x[2]), x[3] = fmaf(y.w, f, x[3]);
     }
+    const float over = whole ? over_sum(sum_l, high) : over_part(sum_l);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[e] *= over;
     if (whole) {
       if (d < head_dim)
         *reinterpret_cast<uint2 *>(p.out + row_at(p, one_b, one_j, row, p.ldo) + d) =
@@ -842,14 +850,12 @@ __global__ void __launch_bounds__(32 * kAddWarps, APART ? 3 : 8) kv_add_kernel(c
     for (int i = 16; i > 0; i /= 2) high = fmaxf(high, __shfl_xor_sync(kAll, high, i));
     high = fmaxf(high, m);
     // (a maximum that is not above the one so far, -inf beside -inf among them, weighs 1 as it stands)
-    const float l_here = lane >= here ? 0.0f : m_part == high ? l_part : l_part * ex2(m_part - high);
-    const float l_old = m == high ? l : l * ex2(m - high);
-    float l_sum = l_here;
+    const float f = lane >= here ? 0.0f : m_part == high ? l_part : l_part * ex2(m_part - high);
+    const float f_old = m == high ? 1.0f : ex2(m - high);
+    float l_sum = f;
 #pragma unroll
     for (int i = 16; i > 0; i /= 2) l_sum += __shfl_xor_sync(kAll, l_sum, i);
-    l = l_old + l_sum;
-    // the parts are O / l of theirs: each weighs its share of the sum
-    const float over = over_sum(l), f = l_here * over, f_old = l_old * over;
+    l = fmaf(l, f_old, l_sum);
 #pragma unroll
     for (int x = 0; x < N; ++x) o[x] *= f_old;
     m = high;
@@ -875,30 +881,23 @@ __global__ void __launch_bounds__(32 * kAddWarps, APART ? 3 : 8) kv_add_kernel(c
     for (int w = 0; w < kAddWarps; ++w) high = fmaxf(high, part_m[w]);
     m = high;
     l = 0.0f;
-    float f[kAddWarps];
-#pragma unroll
-    for (int w = 0; w < kAddWarps; ++w) {
-      f[w] = part_m[w] == high ? part_l[w] : part_l[w] * ex2(part_m[w] - high);
-      l += f[w];
-    }
-    const float over = over_sum(l);
 #pragma unroll
     for (int x = 0; x < N; ++x) o[x] = 0.0f;
 #pragma unroll
-    for (int w = 0; w < kAddWarps; ++w)
+    for (int w = 0; w < kAddWarps; ++w) {
+      const float f = part_m[w] == high ? 1.0f : ex2(part_m[w] - high);
+      l = fmaf(part_l[w], f, l);
 #pragma unroll
-      for (int x = 0; x < N; ++x) o[x] = fmaf(part_o[APART ? w : 0][N * lane + x], f[w] * over, o[x]);
+      for (int x = 0; x < N; ++x) o[x] = fmaf(part_o[APART ? w : 0][N * lane + x], f, o[x]);
+    }
   }
   if (N * lane >= p.head_dim) return;
-  if (l == 0.0f && m > -INFINITY) {  // (as over_sum of all of a row)
-#pragma unroll
-    for (int x = 0; x < N; ++x) o[x] = NAN;
-  }
+  const float inv = over_sum(l, m);
   uint16_t *out = p.out + row_at(p, it.b, it.j, row, p.ldo) + N * lane;
   if constexpr (N == 4)
-    *reinterpret_cast<uint2 *>(out) = make_uint2(out_bits2<DT>(o[0], o[1]), out_bits2<DT>(o[2], o[3]));
+    *reinterpret_cast<uint2 *>(out) = make_uint2(out_bits2<DT>(o[0] * inv, o[1] * inv), out_bits2<DT>(o[2] * inv, o[3] * inv));
   else
-    *reinterpret_cast<uint32_t *>(out) = out_bits2<DT>(o[0], o[1]);
+    *reinterpret_cast<uint32_t *>(out) = out_bits2<DT>(o[0] * inv, o[1] * inv);
 }
 
 template <int DT, int D, int ROWS>
