@@ -686,6 +686,7 @@ W4_API int w4_kv_append(const w4_kv_append_args *args, void *stream);
  * operand that is rounded: to 2^-11 of itself, or 2^-25 of the largest, however
  * unlike the pages' scales of values are (what a page adds may be lost where its
  * scale is below 2^-100 of another one's of the sequence and head).
+ * The sum that divides is that of the rounded weights.
  *
  * q_dev, out_dev  [batch, n, q_heads, head_dim] of dtype, rows (i, j) ldq and
  *               ldo values apart (multiples of 8), 16-byte aligned.

@@ -3,8 +3,9 @@
 // For a sequence and key head the n query rows of the r query heads that share it are n * r rows (row = j * r + head), taken 16
 // at a time (an item). For a tile of 16 keys, which lies in one page: S = q . codes, s = S * (k scale * softmax scale *
 // log2 e) + log2(v scale / unit), a row's running maximum m, w = 2^(s - m) in fp16, O += w . codes, l += (sum of w) / (v scale /
-// unit): with the page's scale of the values inside the weight no product needs a scale of its own. m may lag behind by 2^5 as a
-// weight, so that O is rescaled a few times in an item.
+// unit): with the page's scale of the values inside the weight no product needs a scale of its own. The sum is that of the
+// weights as they were rounded, by a product with ones, so that an output is an average of values. m may lag behind by 2^5 as
+// a weight, so that O is rescaled a few times in an item.
 // O is in units of `unit`, a warp's own: the power of two below the largest scale that its lookups, of 32 tiles each, have found
 // in the item so far (O is rescaled where it grows). Scales from 2^-8 units up go into the weights, smaller ones and those that
 // are not positive and finite go by a product of their own, in fp32. The weights are kept 2^10 times larger than 2^(s - m): 2^15
@@ -457,7 +458,7 @@ __global__ void __launch_bounds__(32 * KvCfg<D, ROWS>::kWarps, 1) kv_attention_k
 
   // ------------------------------------------------------------ products
   uint32_t q[D / 16][2 * RR];  // a step's pairs: (row g, pair 0), (row g, pair 1) and, of 16 rows, those of row g + 8
-  float o[NO][2], m[RR], l[RR], mul[RR], unit = kLeastUnit;  // (m: the maximum in use less kRaise; unit: log2 of it)
+  float o[NO][2], m[RR], l[2], mul[RR], unit = kLeastUnit;  // (l: of the rows of o; m: the maximum in use less kRaise; unit: log2 of it)
   int sees[RR], least = 0, len = 0;
   auto begin_item = [&]() {
     const int rt = j - p.row_tiles_div.div(j) * p.row_tiles;
@@ -515,10 +516,10 @@ __global__ void __launch_bounds__(32 * KvCfg<D, ROWS>::kWarps, 1) kv_attention_k
           }
         }
       m[i] = -INFINITY;
-      l[i] = 0.0f;
     }
     least = static_cast<int>(__reduce_min_sync(kAll, least));
     unit = kLeastUnit;
+    l[0] = l[1] = 0.0f;
 #pragma unroll
     for (int x = 0; x < NO; ++x) o[x][0] = o[x][1] = 0.0f;
   };
@@ -603,19 +604,14 @@ __global__ void __launch_bounds__(32 * KvCfg<D, ROWS>::kWarps, 1) kv_attention_k
           const float now = top[r2] > m[r2] + (kSlack + kRaise) ? top[r2] - kRaise : m[r2];  // (a row's own scores alone say when)
           alpha[r2] = now == m[r2] ? 1.0f : ex2(m[r2] - now);
           m[r2] = now;
-          l[r2] *= alpha[r2];
-          alpha[r2] *= move;
         }
-        if constexpr (ROWS == 16) {
+        const float a0 = ROWS == 16 ? alpha[0] : __shfl_sync(kAll, alpha[0], 8 * t);
+        const float a1 = ROWS == 16 ? alpha[RR - 1] : __shfl_sync(kAll, alpha[0], 8 * t + 4);
+        l[0] *= a0, l[1] *= a1;
+        const float o0 = a0 * move, o1 = a1 * move;
 #pragma unroll
-          for (int x = 0; x < NO; ++x) o[x][0] *= alpha[x % 2], o[x][1] *= alpha[x % 2];
-        } else {
-          const float a0 = __shfl_sync(kAll, alpha[0], 8 * t), a1 = __shfl_sync(kAll, alpha[0], 8 * t + 4);
-#pragma unroll
-          for (int x = 0; x < NO; ++x) o[x][0] *= a0, o[x][1] *= a1;
-        }
+        for (int x = 0; x < NO; ++x) o[x][0] *= ROWS == 16 && x % 2 ? o1 : o0, o[x][1] *= ROWS == 16 && x % 2 == 0 ? o0 : o1;
       }
-      const float per_unit = ex2(-st.y);
 #pragma unroll
       for (int r2 = 0; r2 < RR; ++r2) {
         const float base = m[r2] == -INFINITY ? 0.0f : m[r2];  // (nothing seen yet: weights of 0)
@@ -623,7 +619,6 @@ __global__ void __launch_bounds__(32 * KvCfg<D, ROWS>::kWarps, 1) kv_attention_k
         for (int u = 0; u < 2; ++u)
 #pragma unroll
           for (int e = 2 * r2; e < 2 * r2 + 2; ++e) s[u][e] = ex2(s[u][e] - base);
-        l[r2] = fmaf((s[0][2 * r2] + s[0][2 * r2 + 1]) + (s[1][2 * r2] + s[1][2 * r2 + 1]), per_unit, l[r2]);
         if (key0 < sees[r2]) m[r2] = fmaxf(m[r2], kLeastMax);
       }
       uint32_t w[2 * RR];  // as q's: (row g, keys 2 t ..), (row g, those plus 8), row g + 8
@@ -631,6 +626,18 @@ __global__ void __launch_bounds__(32 * KvCfg<D, ROWS>::kWarps, 1) kv_attention_k
       for (int r2 = 0; r2 < RR; ++r2) {
         w[2 * r2] = half2_bits(s[0][2 * r2], s[0][2 * r2 + 1]);
         w[2 * r2 + 1] = half2_bits(s[1][2 * r2], s[1][2 * r2 + 1]);
+      }
+      {
+        // l: the sum of the weights as they were rounded, by a product with ones
+        constexpr uint32_t kOnes = 0x3C003C00u;
+        const float per_unit = ex2(-st.y);
+        float d[4] = {};
+        if (ROWS == 16)
+          mma_16816<kDtypeF16>(d, w[0], w[ROWS / 4 - 2], w[1], w[ROWS / 4 - 1], kOnes, kOnes);
+        else
+          mma_16816<kDtypeF16>(d, kOnes, kOnes, kOnes, kOnes, w[0], w[1]);
+        l[0] = fmaf(d[0], per_unit, l[0]);
+        l[1] = fmaf(d[ROWS == 16 ? 2 : 1], per_unit, l[1]);
       }
       bool odd = st.w != 1.0f;
       if (border && !odd) {
@@ -667,11 +674,6 @@ __global__ void __launch_bounds__(32 * KvCfg<D, ROWS>::kWarps, 1) kv_attention_k
       const int begin = at - tile, end = begin + tiles;
       const bool here = begin >= from;  // the item begins in the stretch
       const bool whole = here && end <= to;
-#pragma unroll
-      for (int r2 = 0; r2 < RR; ++r2) {
-        l[r2] += __shfl_xor_sync(kAll, l[r2], 1);
-        l[r2] += __shfl_xor_sync(kAll, l[r2], 2);
-      }
       const int rows = min(16, p.n * p.r - (j - p.row_tiles_div.div(j) * p.row_tiles) * 16);
       if (here) {
         cut = !whole;
@@ -681,19 +683,14 @@ __global__ void __launch_bounds__(32 * KvCfg<D, ROWS>::kWarps, 1) kv_attention_k
       }
       float *sums = p.sums + (static_cast<int64_t>(2 * me) + (here ? 1 : 0)) * p.rows * (D + 4);
       // a lane's sums of two rows: ROWS 16: rows g and g + 8 of two stretches of values, 8: rows 2 t and 2 t + 1 of one
-      float lr[2], mr[2];
-      if constexpr (ROWS == 16) {
-        lr[0] = l[0], lr[1] = l[RR - 1];
-        mr[0] = m[0], mr[1] = m[RR - 1];
-      } else {
-        lr[0] = __shfl_sync(kAll, l[0], 8 * t), lr[1] = __shfl_sync(kAll, l[0], 8 * t + 4);
-        mr[0] = __shfl_sync(kAll, m[0], 8 * t), mr[1] = __shfl_sync(kAll, m[0], 8 * t + 4);
-      }
+      float mr[2];
+      mr[0] = ROWS == 16 ? m[0] : __shfl_sync(kAll, m[0], 8 * t);
+      mr[1] = ROWS == 16 ? m[RR - 1] : __shfl_sync(kAll, m[0], 8 * t + 4);
 #pragma unroll
       for (int r2 = 0; r2 < 2; ++r2) {
         const int row = ROWS == 16 ? g + 8 * r2 : 2 * t + r2;
         if (row >= rows) continue;
-        const float inv = whole ? over_sum(lr[r2], mr[r2]) : over_part(lr[r2]), one_unit = ex2(unit);
+        const float inv = whole ? over_sum(l[r2], mr[r2]) : over_part(l[r2]), one_unit = ex2(unit);
         uint16_t *out = p.out + row_at(p, b, j, row, p.ldo);
 #pragma unroll
         for (int e = 0; e < RR; ++e)
@@ -710,11 +707,7 @@ __global__ void __launch_bounds__(32 * KvCfg<D, ROWS>::kWarps, 1) kv_attention_k
               *reinterpret_cast<float4 *>(sums + row * D + d + 4) = make_float4(v8[4], v8[5], v8[6], v8[7]);
             }
           }
-      }
-      if (!whole && t == 0) {
-#pragma unroll
-        for (int r2 = 0; r2 < RR; ++r2)
-          if (g + 8 * r2 < rows) sums[p.rows * D + g + 8 * r2] = m[r2], sums[p.rows * (D + 1) + g + 8 * r2] = l[r2] * kPartSum;
+        if (!whole && (ROWS == 16 ? t : g) == 0) sums[p.rows * D + row] = mr[r2], sums[p.rows * (D + 1) + row] = l[r2] * kPartSum;
       }
     }
     ++at;
@@ -737,15 +730,13 @@ __global__ void __launch_bounds__(32 * KvCfg<D, ROWS>::kWarps, 1) kv_attention_k
   __syncthreads();  // the rings are idle (no copies are in flight: every tile sent was waited for)
   float *sums = reinterpret_cast<float *>(smem + C::kInfo);
 #pragma unroll
-  for (int r2 = 0; r2 < RR; ++r2) {
-    l[r2] += __shfl_xor_sync(kAll, l[r2], 1);
-    l[r2] += __shfl_xor_sync(kAll, l[r2], 2);
-    if (t == 0) row_m[warp][g + 8 * r2] = m[r2], row_l[warp][g + 8 * r2] = l[r2] * kPartSum;
-  }
+  for (int r2 = 0; r2 < RR; ++r2)
+    if (t == 0) row_m[warp][g + 8 * r2] = m[r2];
+#pragma unroll
+  for (int r2 = 0; r2 < 2; ++r2)
+    if ((ROWS == 16 ? t : g) == 0) row_l[warp][ROWS == 16 ? g + 8 * r2 : 2 * t + r2] = l[r2] * kPartSum;
   // (as O / l, so that parts of unlike units can be added)
-  float inv[2];
-  inv[0] = over_part(ROWS == 16 ? l[0] : __shfl_sync(kAll, l[0], 8 * t));
-  inv[1] = over_part(ROWS == 16 ? l[RR - 1] : __shfl_sync(kAll, l[0], 8 * t + 4));
+  const float inv[2] = {over_part(l[0]), over_part(l[1])};
   const float one_unit = ex2(unit);
 #pragma unroll
   for (int x = 0; x < NO; ++x)
