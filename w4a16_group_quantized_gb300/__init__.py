@@ -890,7 +890,8 @@ def w4_prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu: t
     h // (q_heads // k_heads). cu int32 [batch + 1] on the GPU, ascending. Rows outside of all sequences are left as they are in
     ``out``. ``scale``: of the products (None: 1 / sqrt(head_dim)). There is no gradient. A wait that gave up inside the
     kernel (out is then undefined) can be asked for with w4_last_device_error(workspace), so only where one is given;
-    ``wait_limit_cycles``: after how many clock cycles it gives up (0: about 1.5 s); ``flags``: FLAG_TEST_TIMEOUT, in tests."""
+    ``wait_limit_cycles``: after how many clock cycles it gives up (0: about 1.5 s), for a step of 64 or 128 keys however many a
+    prompt has; ``flags``: FLAG_TEST_TIMEOUT, in tests."""
     dtype, shape, device = q.dtype, q.shape, q.get_device()
     dt = _DTYPES.get(dtype)
     k_shape, batch = k.shape, cu.numel() - 1

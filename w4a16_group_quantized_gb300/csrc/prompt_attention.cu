@@ -535,10 +535,12 @@ __global__ void __launch_bounds__(PromptCfg<D, TILES, KEYS, BLOCKS>::kThreads, B
       }
     } else if (warp == kIssue + 3) {
       // ------------------------- V of the steps with the block's own rows (its places are not used again)
+      // (this wait lasts all the block's steps, each of which has the limit; a warp that gives up within one ends it)
+      const uint64_t limit = __umul64hi(p.wait_limit, n) ? ~0ull : p.wait_limit * n;
       for (int tile = 0; tile < n - looked; ++tile) {
         const int step = looked + tile;
         const uint32_t stage = static_cast<uint32_t>((2 * step + 1) % S);
-        if (!warp_wait(smem_u32(&last_bar[tile]), 0, abort_flag, p.err, p.wait_limit)) break;
+        if (!warp_wait(smem_u32(&last_bar[tile]), 0, abort_flag, p.err, limit)) break;
         const int live = min(w.len - step * KEYS, KEYS);  // rows of the sequence in it
         const uint32_t at = ring + stage * C::kKvBytes;
         // an exponent of all ones: one more carries into the sign's place
