@@ -736,7 +736,8 @@ def w4_qk_norm_rope(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Te
     if dt is None or len(shape) != 3 or device < 0:
         raise ValueError("q must be a fp16 or bf16 CUDA tensor [T, heads, head_dim]")
     if (q.requires_grad or (k is not None and k.requires_grad) or (q_weight is not None and q_weight.requires_grad) or
-            (k_weight is not None and k_weight.requires_grad)):
+            (k_weight is not None and k_weight.requires_grad) or (freqs is not None and freqs.requires_grad) or
+            (q_out is not None and q_out.requires_grad) or (k_out is not None and k_out.requires_grad)):
         _no_gradient("w4_qk_norm_rope")
     T, hq, dim = shape
     q_at, ldq = (q.data_ptr(), hq * dim) if q.is_contiguous() else _apart(q, "q")
@@ -789,9 +790,11 @@ def w4_qk_norm_rope(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Te
     return q_out, k_out
 
 
-def _cache(k_cache, v_cache, k_scale, v_scale, table, batch: int, heads, dim: int, device: int):
+def _cache(k_cache, v_cache, k_scale, v_scale, table, batch: int, heads, dim: int, device: int, what: str):
     """(pages, heads, page, max_pages) of a paged cache (heads None: as many as it has) that goes with a call's other tensors."""
     shape = k_cache.shape
+    if k_cache.requires_grad or v_cache.requires_grad or k_scale.requires_grad or v_scale.requires_grad:
+        _no_gradient(what)
     if len(shape) != 4 or table.dim() != 2:
         raise ValueError("k_cache must be [pages, heads, page, head_dim] and table [batch, max_pages]")
     pages, hk, page, d = shape
@@ -827,7 +830,7 @@ def w4_kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cach
         _no_gradient("w4_kv_append")
     T, heads, dim = shape
     batch = lens.numel()
-    pages, _, page, max_pages = _cache(k_cache, v_cache, k_scale, v_scale, table, batch, heads, dim, device)
+    pages, _, page, max_pages = _cache(k_cache, v_cache, k_scale, v_scale, table, batch, heads, dim, device, "w4_kv_append")
     k_at, ldk = (k.data_ptr(), heads * dim) if k.is_contiguous() else _apart(k, "k")
     v_at, ldv = _heads(v, "v", dtype, shape, device)
     a = _KV_APPEND_ARGS.pack(k_at, v_at, k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
@@ -853,14 +856,14 @@ def w4_kv_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     dt, dims = _DTYPES.get(dtype), len(shape)
     if dt is None or not 3 <= dims <= 4 or device < 0:
         raise ValueError("q must be a fp16 or bf16 CUDA tensor [batch, n, heads, head_dim] or [batch, heads, head_dim]")
-    if q.requires_grad:
+    if q.requires_grad or (out is not None and out.requires_grad):
         _no_gradient("w4_kv_attention")
     if dims == 3:
         batch, hq, dim = shape
         n = 1
     else:
         batch, n, hq, dim = shape
-    pages, hk, page, max_pages = _cache(k_cache, v_cache, k_scale, v_scale, table, batch, None, dim, device)
+    pages, hk, page, max_pages = _cache(k_cache, v_cache, k_scale, v_scale, table, batch, None, dim, device, "w4_kv_attention")
     q_at, ldq = (q.data_ptr(), hq * dim) if q.is_contiguous() else _apart(q, "q")
     if out is None:
         out = _empty_heads(q, stream)
@@ -897,7 +900,7 @@ def w4_prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu: t
     k_shape, batch = k.shape, cu.numel() - 1
     if dt is None or len(shape) != 3 or len(k_shape) != 3 or device < 0 or batch < 0:
         raise ValueError("q must be a fp16 or bf16 CUDA tensor [T, heads, head_dim], k alike and cu [batch + 1]")
-    if q.requires_grad or k.requires_grad or v.requires_grad:
+    if q.requires_grad or k.requires_grad or v.requires_grad or (out is not None and out.requires_grad):
         _no_gradient("w4_prompt_attention")
     T, hq, dim = shape
     hk = k_shape[1]
