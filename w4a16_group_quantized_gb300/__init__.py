@@ -872,7 +872,7 @@ def w4_kv_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
         o_at, ldo = _heads(out, "out", dtype, shape, device)
     a = _KV_ATTENTION_ARGS.pack(q_at, k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), table.data_ptr(),
                                 _like(lens, "lens", _I32, (batch,), device), o_at, ldq, ldo, pages, batch, n, max_pages, hq, hk, dim,
-                                page, dt, dim ** -0.5 if scale is None else scale)
+                                page, dt, (dim or 1) ** -0.5 if scale is None else scale)
     _run_with((_lib or load()).w4_kv_attention, a, workspace, lambda: w4_kv_attention_workspace_bytes(batch, n, hq, hk, dim),
               device, stream, "w4_kv_attention")
     return out
@@ -916,7 +916,7 @@ def w4_prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu: t
         o_at, ldo = _heads(out, "out", dtype, shape, device)
     lib = _lib or load()
     a = _PROMPT_ARGS.pack(q_at, k_at, v_at, _like(cu, "cu", _I32, (batch + 1,), device), o_at, T, ldq, ldk, ldv, ldo, batch, hq, hk,
-                          dim, dt, dim ** -0.5 if scale is None else scale)
+                          dim, dt, (dim or 1) ** -0.5 if scale is None else scale)
     call = lib.w4_prompt_attention
     if flags or wait_limit_cycles:
         o = ctypes.byref(Options(flags=flags, wait_limit_cycles=wait_limit_cycles))
