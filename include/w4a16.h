@@ -737,7 +737,7 @@ W4_API size_t w4_kv_attention_workspace_bytes(int32_t batch, int32_t n, int32_t 
  * left as they are. What rows that a query does not see hold, NaN and
  * infinities included, has no part in its output. With head_dim above 64 a
  * prompt's rows have the same bits alone and among others (up to 64 the steps
- * over the keys, and with them the roundings, go by T and q_heads).
+ * over the keys, and with them the roundings, go by T, batch and q_heads).
  *
  * Numerics: sums and the softmax's maximum and sum are fp32; the weights enter
  * the second product in dtype; one rounding at the end.

@@ -614,14 +614,17 @@ cudaError_t launch_tiles(const PromptArgs &a, const PromptParams &p, cudaStream_
 // 1000 x 8 14.4 / 18.1: two, where they are a block for each SM and prompts are long enough for whole ones (64 x 128 x 32 heads 113 / 202,
 // 128 x 64 66 / 108, 256 x 64 138 / 147, up to 500 x 64 83 / 120, 300 x 40 136 / 163; 512 x 32 148 / 145, 1000 x 16 188 / 177).
 // Heads of 64, steps of 128 keys and two blocks an SM / of 64 and four: a step of 64 takes nearly as long as one of 128, but more of them
-// run beside each other, which pays where there are many blocks for each place: 256 x 64 x 32 heads 106 / 76, 512 x 32 x 32 105 / 83, forty of
-// up to 3000 x 32 163 / 137, 8192 x 64 520 / 488, 4096 x 64 154 / 143, 1000 x 8 x 16 39 / 33; nine of up to 1900 x 24 30 / 34,
-// 2048 x 32 27 / 39, 1000 x 8 11.6 / 14.8. Taken from 12 tiles an SM on.
+// run beside each other, which pays where there are many blocks for each place. With the tiles an SM: 16 x 256 x 16 heads (3.4)
+// 13.1 / 11.9, 8 x 1000 x 8 (3.3) 18.9 / 23.2, 2048 x 32 (3.4) 25.8 / 38.2, 4096 x 24 (5.1) 60.5 / 72.4, 2048 x 48 (5.1) 39.2 / 40.5, 8 x 1000 x
+// 12 (5.0) 28.1 / 24.5, x 16 (6.6) 37.1 / 31.2, 16 x 256 x 32 (6.7) 26.7 / 19.6, 4096 x 32 (6.7) 76.4 / 74.6, 8192 x 16 (6.7) 127 / 138, x 24 (10.1)
+// 188 / 191, twenty of up to 1000 x 16 (8.1) 42.1 / 34.1, 4096 x 64 (13.5) 146 / 139, nine of up to 1900 x 32 (16.4) 102 / 86, 8192 x 64 (27) 520 /
+// 488. Taken from 6 tiles an SM on, where prompts are longer than 4096 rows on average from 12 on.
 template <int DT>
 cudaError_t launch_type(const PromptArgs &a, const PromptParams &p, int num_sms, cudaStream_t stream) {
+  const bool lengthy = a.T > 4096 * static_cast<int64_t>(a.batch);
   if (a.head_dim <= 64)
-    return cdiv(a.T, kTile) * a.q_heads < 12 * num_sms ? launch_tiles<DT, 64, 1, 128, 2>(a, p, stream)
-                                                       : launch_tiles<DT, 64, 1, 64, 4>(a, p, stream);
+    return cdiv(a.T, kTile) * a.q_heads < (lengthy ? 12 : 6) * num_sms ? launch_tiles<DT, 64, 1, 128, 2>(a, p, stream)
+                                                                         : launch_tiles<DT, 64, 1, 64, 4>(a, p, stream);
   const bool few = cdiv(a.T, 2 * kTile) * a.q_heads < num_sms, brief = a.T < 4 * kTile * static_cast<int64_t>(a.batch);
   return few || brief ? launch_tiles<DT, 128, 1, 128, 2>(a, p, stream)
                                                     : launch_tiles<DT, 128, 2, 128, 1>(a, p, stream);
