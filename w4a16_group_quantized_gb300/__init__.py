@@ -882,9 +882,6 @@ def w4_prompt_attention_workspace_bytes(T: int, batch: int, q_heads: int) -> int
     return int(load().w4_prompt_attention_workspace_bytes(T, batch, q_heads))
 
 
-_prompt_bytes = functools.lru_cache(maxsize=1024)(w4_prompt_attention_workspace_bytes)
-
-
 def w4_prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu: torch.Tensor, *, scale: float | None = None,
                         out: torch.Tensor | None = None, workspace=None, stream=None, flags: int = 0,
                         wait_limit_cycles: int = 0) -> torch.Tensor:
@@ -923,5 +920,5 @@ def w4_prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu: t
 
         def call(args, ws, nbytes, handle):
             return lib.w4_prompt_attention_opts(args, ws, nbytes, o, handle)
-    _run_with(call, a, workspace, lambda: _prompt_bytes(T, batch, hq), device, stream, "w4_prompt_attention")
+    _run_with(call, a, workspace, lambda: lib.w4_prompt_attention_workspace_bytes(T, batch, hq), device, stream, "w4_prompt_attention")
     return out

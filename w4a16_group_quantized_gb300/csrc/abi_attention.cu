@@ -154,7 +154,7 @@ int w4_kv_append(const w4_kv_append_args *a, void *stream) {
 
 size_t w4_kv_attention_workspace_bytes(int32_t batch, int32_t n, int32_t q_heads, int32_t k_heads, int32_t head_dim) {
   if (check_kv_attention_sizes(batch, n, q_heads, k_heads, head_dim) != W4_OK) return 0;
-  return w4::kv_attention_workspace_bytes(batch > 0 ? batch : 1, n, q_heads, k_heads, head_dim, num_sms_current_device());
+  return w4::kv_attention_workspace_bytes(n, q_heads, k_heads, head_dim, num_sms_current_device());
 }
 
 int w4_kv_attention(const w4_kv_attention_args *a, void *workspace_dev, size_t workspace_bytes, void *stream) {
@@ -177,7 +177,7 @@ int w4_kv_attention(const w4_kv_attention_args *a, void *workspace_dev, size_t w
       !aligned(workspace_dev, 256))
     return W4_ERR_MISALIGNED;
   const int sms = num_sms_current_device();
-  if (workspace_bytes < w4::kv_attention_workspace_bytes(a->batch, a->n, a->q_heads, a->k_heads, a->head_dim, sms))
+  if (workspace_bytes < w4::kv_attention_workspace_bytes(a->n, a->q_heads, a->k_heads, a->head_dim, sms))
     return W4_ERR_WORKSPACE_TOO_SMALL;
   w4::KvAttentionArgs k;
   k.q = a->q_dev;
@@ -215,7 +215,7 @@ int check_prompt_sizes(int64_t T, int32_t batch, int32_t q_heads) {
 
 size_t w4_prompt_attention_workspace_bytes(int64_t T, int32_t batch, int32_t q_heads) {
   if (check_prompt_sizes(T, batch, q_heads) != W4_OK) return 0;
-  return w4::prompt_attention_workspace_bytes(T, batch, q_heads);
+  return w4::kPromptWorkspaceBytes;
 }
 
 int w4_prompt_attention(const w4_prompt_attention_args *a, void *workspace_dev, size_t workspace_bytes, void *stream) {
@@ -243,7 +243,7 @@ int w4_prompt_attention_opts(const w4_prompt_attention_args *a, void *workspace_
   if (!aligned(a->q_dev, 16) || !aligned(a->k_dev, 16) || !aligned(a->v_dev, 16) || !aligned(a->out_dev, 16) ||
       !aligned(a->cu_dev, 4) || !aligned(workspace_dev, 256))
     return W4_ERR_MISALIGNED;
-  if (workspace_bytes < w4::prompt_attention_workspace_bytes(a->T, a->batch, a->q_heads)) return W4_ERR_WORKSPACE_TOO_SMALL;
+  if (workspace_bytes < w4::kPromptWorkspaceBytes) return W4_ERR_WORKSPACE_TOO_SMALL;
   w4::PromptArgs p;
   p.q = a->q_dev;
   p.k = a->k_dev;

@@ -248,7 +248,7 @@ struct KvAttentionArgs {
   float scale;
 };
 constexpr int kKvMaxQueries = 256;
-size_t kv_attention_workspace_bytes(int batch, int n, int q_heads, int k_heads, int head_dim, int num_sms);
+size_t kv_attention_workspace_bytes(int n, int q_heads, int k_heads, int head_dim, int num_sms);
 cudaError_t launch_kv_attention(const KvAttentionArgs &a, void *workspace, int num_sms, cudaStream_t stream);
 
 // w4_prompt_attention.
@@ -262,7 +262,7 @@ struct PromptArgs {
   uint64_t wait_limit;  // cycles a wait may take; 0: the default
   bool test_timeout;    // test only: a barrier expects an arrival more than will come
 };
-size_t prompt_attention_workspace_bytes(int64_t T, int batch, int q_heads);
+constexpr size_t kPromptWorkspaceBytes = 256;  // the error word
 cudaError_t launch_prompt_attention(const PromptArgs &a, void *workspace, int num_sms, cudaStream_t stream);
 
 }  // namespace w4

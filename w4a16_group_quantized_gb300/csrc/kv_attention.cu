@@ -95,7 +95,7 @@ struct KvParams {
   CutItem *cuts;
   float *sums;     // [2 * warps]: O / l [rows][D], m [rows], l [rows], padded to 16 bytes, of a stretch's first and last item
   int64_t ldq, ldo, pages;
-  int batch, n, max_pages, q_heads, k_heads, head_dim, page, r, row_tiles, rows, items;  // items of a sequence
+  int batch, n, max_pages, k_heads, head_dim, page, r, row_tiles, rows, items;  // items of a sequence
   int by_item;     // few items: an entry of cut and cuts for each, else for each warp
   float scale;
   FastDiv page_div, r_div, row_tiles_div;
@@ -925,7 +925,7 @@ size_t slots_at(int num_sms) { return 256 + 256 * static_cast<size_t>(cdiv(num_s
 
 // The first 256 bytes (whose first word, another call's error word, is left alone) hold the number of workers; then the cut items and their
 // parts.
-size_t kv_attention_workspace_bytes(int, int n, int q_heads, int k_heads, int head_dim, int num_sms) {
+size_t kv_attention_workspace_bytes(int n, int q_heads, int k_heads, int head_dim, int num_sms) {
   const int64_t rows = static_cast<int64_t>(n) * (q_heads / k_heads);
   const size_t d = head_dim <= 64 ? 64 : 128;
   return slots_at(num_sms) + static_cast<size_t>(2 * num_sms * kMostWarps) * (rows < 16 ? rows : 16) * (d + 4) * sizeof(float);
@@ -952,7 +952,6 @@ cudaError_t launch_kv_attention(const KvAttentionArgs &a, void *workspace, int n
   p.batch = a.batch;
   p.n = a.n;
   p.max_pages = a.max_pages;
-  p.q_heads = a.q_heads;
   p.k_heads = a.k_heads;
   p.head_dim = a.head_dim;
   p.page = a.page;

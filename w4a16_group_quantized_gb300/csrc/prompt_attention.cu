@@ -69,9 +69,9 @@ struct PromptCfg {
   static constexpr uint32_t kO = TILES * KEYS;         // O's first column; O of the second tile D further
   static constexpr uint32_t kColumns = 512 / BLOCKS >= 256 ? 512 / BLOCKS : 128;
   static_assert(kO + TILES * D <= kColumns && kColumns * BLOCKS <= 512, "tensor memory");
-  static constexpr int kRegsLaunch = TILES == 2 ? 168 : BLOCKS == 2 ? 128 : BLOCKS == 3 ? 80 : 64;
-  static constexpr int kRegsSoftmax = TILES == 2 ? 216 : BLOCKS == 2 ? 208 : BLOCKS == 3 ? 120 : 96;
-  static constexpr int kRegsOthers = TILES == 2 ? 72 : BLOCKS == 2 ? 48 : BLOCKS == 3 ? 40 : 32;
+  static constexpr int kRegsLaunch = TILES == 2 ? 168 : BLOCKS == 2 ? 128 : 64;
+  static constexpr int kRegsSoftmax = TILES == 2 ? 216 : BLOCKS == 2 ? 208 : 96;
+  static constexpr int kRegsOthers = TILES == 2 ? 72 : BLOCKS == 2 ? 48 : 32;
   static_assert(TILES * kRegsSoftmax + kRegsOthers <= (TILES + 1) * kRegsLaunch, "the registers that the block was launched with");
 };
 
@@ -631,8 +631,6 @@ cudaError_t launch_type(const PromptArgs &a, const PromptParams &p, int num_sms,
 }
 
 }  // namespace
-
-size_t prompt_attention_workspace_bytes(int64_t, int, int) { return 256; }
 
 cudaError_t launch_prompt_attention(const PromptArgs &a, void *workspace, int num_sms, cudaStream_t stream) {
   PromptParams p;
