@@ -47,7 +47,6 @@ namespace {
 using namespace detail;
 
 constexpr uint32_t kAll = 0xffffffffu;
-constexpr int kMostWarps = 16;    // of a block
 constexpr int kItemCost = 4;      // what beginning an item costs, in tiles
 constexpr int kSoloTiles = 6;     // what adding parts takes, in tiles of a warp
 constexpr float kLog2e = 1.4426950408889634f;
@@ -122,12 +121,15 @@ __device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
 // Whether one of the four codes of a word is NaN (0x7F or 0xFF).
 __device__ __forceinline__ bool any_nan_code(uint32_t w) { return __vcmpeq4(w & 0x7F7F7F7Fu, 0x7F7F7F7Fu) != 0; }
 
+// Warps of a block, with heads of up to d values and up to `rows` rows an item: as many as have the registers, but for a few words at
+// most (heads of 64, us: 128 x 8000 keys, 24 / 8 heads 205 with 12 warps, 180 with 16; 64 x 4000, four queries 83 with 8, 69 with 12, 66 with
+// 16. Heads of 128: 16 spill a tile's operands, 350 -> 686; 12 for 16 rows take as long as 8).
+constexpr int warps_of(int d, int rows) { return d <= 64 ? 16 : rows <= 8 ? 12 : 8; }
+
 // D: head_dim rounded up to 64 or 128. ROWS: of an item, up to 8 or up to 16.
 template <int D, int ROWS>
 struct KvCfg {
-  // as many as have the registers (heads of 64, us: 128 x 8000 keys, 24 / 8 heads 205 with 12 warps, 180 with 16; 64 x 4000, four
-  // queries 83 with 8, 69 with 12, 66 with 16. Heads of 128: more than these spill, 350 -> 686)
-  static constexpr int kWarps = D == 64 ? 16 : ROWS == 8 ? 12 : 8;
+  static constexpr int kWarps = warps_of(D, ROWS);
   static constexpr int kStages = 4;
   static constexpr int kPieces = D / 64;                 // 16-byte pieces of a key in a lane
   static constexpr int kVBytes = D / 8;                  // bytes of a value row in a lane
@@ -919,16 +921,18 @@ cudaError_t launch_d(const KvParams &p, int num_sms, cudaStream_t stream) {
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-size_t slots_at(int num_sms) { return 256 + 256 * static_cast<size_t>(cdiv(num_sms * kMostWarps * (sizeof(CutItem) + sizeof(int32_t)), 256)); }
+// Where the parts begin, for so many warps in all.
+size_t slots_at(int warps) { return 256 + 256 * static_cast<size_t>(cdiv(warps * (sizeof(CutItem) + sizeof(int32_t)), 256)); }
 
 }  // namespace
 
 // The first 256 bytes (whose first word, another call's error word, is left alone) hold the number of workers; then the cut items and their
 // parts.
 size_t kv_attention_workspace_bytes(int n, int q_heads, int k_heads, int head_dim, int num_sms) {
-  const int64_t rows = static_cast<int64_t>(n) * (q_heads / k_heads);
+  const int64_t all = static_cast<int64_t>(n) * (q_heads / k_heads);
+  const int rows = all < 16 ? static_cast<int>(all) : 16, warps = num_sms * warps_of(head_dim, rows);
   const size_t d = head_dim <= 64 ? 64 : 128;
-  return slots_at(num_sms) + static_cast<size_t>(2 * num_sms * kMostWarps) * (rows < 16 ? rows : 16) * (d + 4) * sizeof(float);
+  return slots_at(warps) + static_cast<size_t>(2 * warps) * rows * (d + 4) * sizeof(float);
 }
 
 cudaError_t launch_kv_attention(const KvAttentionArgs &a, void *workspace, int num_sms, cudaStream_t stream) {
@@ -944,8 +948,6 @@ cudaError_t launch_kv_attention(const KvAttentionArgs &a, void *workspace, int n
   uint8_t *ws = static_cast<uint8_t *>(workspace);
   p.workers = reinterpret_cast<int32_t *>(ws + 128);
   p.cuts = reinterpret_cast<CutItem *>(ws + 256);
-  p.cut = reinterpret_cast<int32_t *>(ws + 256 + static_cast<size_t>(num_sms) * kMostWarps * sizeof(CutItem));
-  p.sums = reinterpret_cast<float *>(ws + slots_at(num_sms));
   p.ldq = a.ldq;
   p.ldo = a.ldo;
   p.pages = a.pages;
@@ -958,6 +960,9 @@ cudaError_t launch_kv_attention(const KvAttentionArgs &a, void *workspace, int n
   p.r = a.q_heads / a.k_heads;
   p.row_tiles = static_cast<int>(cdiv(static_cast<int64_t>(a.n) * p.r, 16));
   p.rows = a.n * p.r < 16 ? a.n * p.r : 16;
+  const int warps = num_sms * warps_of(a.head_dim, p.rows);
+  p.cut = reinterpret_cast<int32_t *>(ws + 256 + static_cast<size_t>(warps) * sizeof(CutItem));
+  p.sums = reinterpret_cast<float *>(ws + slots_at(warps));
   p.items = p.row_tiles * a.k_heads;
   p.by_item = static_cast<int64_t>(p.batch) * p.items <= num_sms;
   p.scale = a.scale;
