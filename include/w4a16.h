@@ -576,8 +576,12 @@ W4_API size_t w4_lora_workspace_bytes(int64_t T, int64_t K, int64_t N, int32_t a
  *
  * axis(i): the first section0 frequencies go by the first row of positions,
  * the next section1 by the second, and so on (one axis: section0 = rot / 2).
- * The angle's turn is formed exactly enough for any 32-bit position; sums and
- * products in fp32, one rounding at the end.
+ * The angle's turn is formed in integers for any 32-bit position: it is off by
+ * |position| (|freq| + 1) 2^-64 of a turn, which is below 2^-32 where |freq| is
+ * at most 1 (2^-13 for one of 2^20 at the farthest position). Its sine and
+ * cosine, sums and products in fp32, one rounding at the end: a head whose
+ * squares leave fp32's range (values past 2^59, or below 2^-63 with an eps as
+ * small) is not normed.
  *
  * q_dev, k_dev  [T, heads, head_dim] of dtype (fp16 or bf16), rows ldq and ldk
  *               values apart (multiples of 8), 16-byte aligned. k_dev may be
@@ -589,7 +593,8 @@ W4_API size_t w4_lora_workspace_bytes(int64_t T, int64_t K, int64_t N, int32_t a
  * q_weight_dev, k_weight_dev  [head_dim] of dtype, 16-byte aligned, or NULL.
  * head_dim a multiple of 8, at most 256; rot a multiple of 16, at most
  * head_dim; the sections are not negative and their sum is rot / 2; at least a
- * rotation or a norm.
+ * rotation or a norm; at most 65535 heads of each; T, and the rows' distances
+ * here and below, less than 2^31.
  */
 typedef struct {
     const void *q_dev;
@@ -644,7 +649,8 @@ W4_API int w4_qk_norm_rope(const w4_rope_args *args, void *stream);
  * table_dev     int32 [batch, max_pages]; cu_dev int32 [batch + 1], ascending;
  *               lens_dev int32 [batch]: what the cache holds before the call.
  * head_dim a multiple of 16, at most 128; page a multiple of 16, at most 256;
- * at most 32767 heads, and max_pages * page below 2^31 - 1024.
+ * at most 32767 heads; T and max_pages * page below 2^31 - 1024, pages below
+ * 2^31.
  */
 typedef struct {
     const void *k_dev;
@@ -692,8 +698,9 @@ W4_API int w4_kv_append(const w4_kv_append_args *args, void *stream);
  *               ldo values apart (multiples of 8), 16-byte aligned.
  * lens_dev      int32 [batch], the new tokens included.
  * q_heads a multiple of k_heads; head_dim a multiple of 16, at most 128; page a
- * multiple of 16, at most 256; n at most 256; at most 32767 key heads; scale
- * positive and finite; max_pages * page below 2^31 - 1024. With 16 query rows
+ * multiple of 16, at most 256; n at most 256; at most 32767 key heads and 65535
+ * query heads; scale positive and finite; max_pages * page below 2^31 - 1024,
+ * pages below 2^31. With 16 query rows
  * that share a key head as an item: at most 2^24 items, and at most 2^30 of
  * items * (max_pages * page / 16 + 16).
  * The workspace is at least w4_kv_attention_workspace_bytes(...) bytes,
@@ -740,17 +747,21 @@ W4_API size_t w4_kv_attention_workspace_bytes(int32_t batch, int32_t n, int32_t 
  * over the keys, and with them the roundings, go by T, batch and q_heads).
  *
  * Numerics: sums and the softmax's maximum and sum are fp32; the weights enter
- * the second product in dtype; one rounding at the end.
+ * the second product in dtype (fp16: rounded to 2^-11 of themselves, or 2^-25 of
+ * the largest; the sum that divides is that of the unrounded ones); one rounding
+ * at the end.
  *
  * q_dev, out_dev  [T, q_heads, head_dim], k_dev, v_dev [T, k_heads, head_dim] of
  *               dtype, rows ldq, ldo, ldk, ldv values apart (multiples of 8),
  *               16-byte aligned.
  * cu_dev        int32 [batch + 1], ascending, within [0, T].
- * q_heads a multiple of k_heads; head_dim a multiple of 8, at most 128; scale
- * positive and finite.
+ * q_heads a multiple of k_heads, at most 65535; head_dim a multiple of 8, at most
+ * 128; scale positive and finite; T at most 2^30, and (T / 128 + batch) * q_heads,
+ * T / 128 rounded up, below 2^31.
  * The workspace is at least w4_prompt_attention_workspace_bytes(...) bytes,
  * 256-byte aligned. Its first word is a device error word, which each call
- * clears first, as w4a16_experts' is.
+ * clears first, as w4a16_experts' is; a call without rows or sequences launches
+ * nothing and leaves it as it is.
  */
 typedef struct {
     const void *q_dev;

@@ -3,8 +3,10 @@
 // out[t, h] = sum_p w_p v_p / sum_p w_p, w_p = exp(scale * q . k_p) over the rows p <= t of t's sequence, with the running
 // maximum m and sum l of a softmax: s = q . k * scale * log2 e, w = 2^(s - m), O = O * 2^(m_old - m) + w v. The maximum
 // need not be the newest for that: while no score is above it by more than 2^8 as a weight, O and l are left as they are and the
-// weights are simply larger than 1 (fp32 sums, and 16-bit weights keep their relative precision), so that O is
-// rescaled a few times in a row's life instead of at each step.
+// weights are simply larger than 1 (in fp32 sums; as 16 bits they are rounded to the type's half step of themselves, in fp16 to
+// 2^-25 of the maximum in use where that is more), so that O is rescaled a few times in a row's life instead of at
+// each step. The sum that divides is that of the unrounded weights: rounded ones would have to be taken apart again, in the
+// softmax's warps, which are what heads of 64 wait for.
 //
 // A block takes 128 or 256 rows of one sequence and head, as one tile or two, which share the keys and values that it copies,
 // 128 rows a step. Tensor memory holds for each tile the scores S (128 x 128 fp32, one row a lane), whose columns the 16-bit
