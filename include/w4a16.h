@@ -641,7 +641,8 @@ W4_API int w4_qk_norm_rope(const w4_rope_args *args, void *stream);
  * With powers of two a page's rows lose nothing when its scale grows, but for
  * what falls below the type's range. Rows outside [cu[0], cu[batch]) are not
  * used, positions past the table's end are dropped, and the rest of the cache
- * is left as it is. A page that gets rows belongs to one sequence only.
+ * is left as it is. A page that gets rows belongs to one sequence only, and stands
+ * once in its row of the table.
  *
  * k_dev, v_dev  [T, heads, head_dim] of dtype, rows ldk and ldv apart
  *               (multiples of 8), 16-byte aligned.

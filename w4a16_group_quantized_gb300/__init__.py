@@ -821,7 +821,7 @@ def w4_kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cach
     k_cache, v_cache float8_e4m3fn [pages, heads, page, head_dim], k_scale, v_scale fp32 [pages, heads]: a value is
     code * scale. table int32 [batch, max_pages] lists each sequence's pages (-1: none; nothing is written there), cu int32
     [batch + 1] ascends, lens int32 [batch] is what the cache holds before the call (the caller adds the new rows to it). A page that
-    gets rows must belong to one sequence only. See w4_kv_append in include/w4a16.h for the scales."""
+    gets rows must belong to one sequence only, and stand once in its row of the table. See w4_kv_append in include/w4a16.h for the scales."""
     dtype, shape, device = k.dtype, k.shape, k.get_device()
     dt = _DTYPES.get(dtype)
     if dt is None or len(shape) != 3 or device < 0:

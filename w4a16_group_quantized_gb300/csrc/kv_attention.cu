@@ -23,14 +23,14 @@
 // follows from the fragments: of key 8 u + lane / 4 the quarter of the head that its place in the quad has, in 16-byte
 // pieces; of keys 2 t, 2 t + 1 and those plus 8 (t = lane % 4) an eighth of the head, whose codes of two neighbouring keys are
 // put side by side by byte permutes. The pieces of a line are exchanged so that these reads meet no bank twice.
-// Items cut between warps leave sums (O, m, l) in the workspace, one for a block whose warps are all within one item; a second
+// Items cut between warps leave parts (O / l, m, l) in the workspace, one for a block whose warps are all within one item; a second
 // launch adds them in order. Few items go to a block each instead, whose warps share the item, where that is quicker.
 //
-// Measured (us a call within a graph; heads of 128, one query): 128 sequences of 8192 keys, 64 / 8 heads 343 (2.15 GB: 6.3 TB/s,
-// 0.92 of a copy's rate); 48 of up to 8000 29.5, four queries 50; one of 1003 keys, 32 / 32 heads 9.7, of 8000 20; 100 keys
-// 4.6. What long batches wait for is memory; short ones some 12 us beside it: launches, the dealing (1 to 2), a first lookup
+// Measured (us a call within a graph; heads of 128, one query): 128 sequences of 8192 keys, 64 / 8 heads 337 (2.15 GB: 6.4 TB/s,
+// 0.94 of a copy's rate); 48 of up to 8000 29.9, four queries 50; one of 1003 keys, 32 / 32 heads 10.0, of 8000 20.6; 100 keys
+// 4.5. What long batches wait for is memory; short ones some 12 us beside it: launches, the dealing (1 to 2), a first lookup
 // (1.5), the first tiles of all warps at once (1.4 to 4), sums (1.8) and their adding. With four queries it is a tile's
-// arithmetic, 0.9 us a warp, most of it the codes' conversion and dependent instructions (issue slots 35%, tensor pipe 25%); two tiles
+// arithmetic, 0.9 us a warp, most of it the codes' conversion and dependent instructions (issue slots 36%, tensor pipe 26%); two tiles
 // at a time, with twice as many independent ones, took as long (55), as did more sums a row or more warps with fewer registers.
 #include <atomic>
 #include <type_traits>

@@ -20,7 +20,7 @@
 //                         cycles, 550 of them its waits
 //   1 copy warp           Q, then K and V of each step through a ring
 //   1 looking warp        sees the V of the block's own rows (which their first queries do not all see)
-// V is used as it stands, an MN-major operand.
+// V is used as it stands, an MN-major operand. (Blocks that go four to an SM have 64 registers a thread, and spill some 40 bytes.)
 //
 // Rows that a query does not see have weight 0, but 0 * NaN is NaN. The rows of V that are the block's own, of which its first queries do
 // not see all, go into the product with zeros in the place of rows behind the sequence's end and of values that are not
