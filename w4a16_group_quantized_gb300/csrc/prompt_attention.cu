@@ -5,8 +5,9 @@
 // need not be the newest for that: while no score is above it by more than 2^8 as a weight, O and l are left as they are and the
 // weights are simply larger than 1 (in fp32 sums; as 16 bits they are rounded to the type's half step of themselves, in fp16 to
 // 2^-25 of the maximum in use where that is more), so that O is rescaled a few times in a row's life instead of at
-// each step. The sum that divides is that of the unrounded weights: rounded ones would have to be taken apart again, in the
-// softmax's warps, which are what heads of 64 wait for.
+// each step. The sum that divides is that of the unrounded weights: taking the rounded ones apart again for it made 8192 rows of 64
+// heads of 128 660 us instead of 602, of 64 525 instead of 484, for an error of 1.16 to 1.22 times that of 32-bit weights instead of
+// 1.27 to 1.30.
 //
 // A block takes 128 or 256 rows of one sequence and head, as one tile or two, which share the keys and values that it copies,
 // 128 rows a step. Tensor memory holds for each tile the scores S (128 x 128 fp32, one row a lane), whose columns the 16-bit
