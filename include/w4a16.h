@@ -705,7 +705,8 @@ W4_API int w4_kv_append(const w4_kv_append_args *args, void *stream);
  * that share a key head as an item: at most 2^24 items, and at most 2^30 of
  * items * (max_pages * page / 16 + 16).
  * The workspace is at least w4_kv_attention_workspace_bytes(...) bytes,
- * 256-byte aligned. Its first word is left as it is.
+ * 256-byte aligned; what is enough for n is enough for fewer. Its first word is
+ * left as it is.
  */
 typedef struct {
     const void *q_dev;

@@ -27,3 +27,14 @@ def test_nothing_is_written_behind_the_workspace(lens, n, hq, hk, dim):
     with pytest.raises(w4.W4Error) as e:
         w4.w4_kv_attention(q, *c.args(), ints(lens), workspace=ws[:need - 1])
     assert e.value.status == 4
+
+
+@pytest.mark.parametrize("hq,hk", [(1, 1), (8, 4), (6, 2), (32, 2), (20, 1)])
+@pytest.mark.parametrize("dim", [48, 128])
+def test_a_workspace_for_many_queries_is_enough_for_fewer(hq, hk, dim):
+    sizes = [w4.w4_kv_attention_workspace_bytes(3, n, hq, hk, dim) for n in range(1, 40)]
+    assert sizes == sorted(sizes)
+    c = Cache([900, 3, 4000], hk, dim, 32)
+    ws = torch.empty(sizes[8], dtype=torch.uint8, device="cuda")
+    for n in range(1, 10):
+        check_kv(c, randn(n, 3, n, hq, dim), [900, 3, 4000], workspace=ws)

@@ -927,12 +927,16 @@ size_t slots_at(int warps) { return 256 + 256 * static_cast<size_t>(cdiv(warps *
 }  // namespace
 
 // The first 256 bytes (whose first word, another call's error word, is left alone) hold the number of workers; then the cut items and their
-// parts.
+// parts. What is enough for n queries is for fewer: 8 rows, which have more warps, take more than 9.
 size_t kv_attention_workspace_bytes(int n, int q_heads, int k_heads, int head_dim, int num_sms) {
   const int64_t all = static_cast<int64_t>(n) * (q_heads / k_heads);
-  const int rows = all < 16 ? static_cast<int>(all) : 16, warps = num_sms * warps_of(head_dim, rows);
   const size_t d = head_dim <= 64 ? 64 : 128;
-  return slots_at(warps) + static_cast<size_t>(2 * warps) * rows * (d + 4) * sizeof(float);
+  auto of = [&](int rows) {
+    const int warps = num_sms * warps_of(head_dim, rows);
+    return slots_at(warps) + static_cast<size_t>(2 * warps) * rows * (d + 4) * sizeof(float);
+  };
+  const size_t own = of(all < 16 ? static_cast<int>(all) : 16), fewer = of(all < 8 ? static_cast<int>(all) : 8);
+  return own > fewer ? own : fewer;
 }
 
 cudaError_t launch_kv_attention(const KvAttentionArgs &a, void *workspace, int num_sms, cudaStream_t stream) {
